@@ -1,8 +1,9 @@
 """Builds the CUDA library ``libflp.so`` in-tree with nvcc for sm_103a.
 
-The library is one translation unit (``csrc/flp.cu``) that holds the C ABI of
-``include/flp.h`` and the kernels.  Rebuilt when any source is newer than the
-shared object.
+The library is one translation unit (``csrc_step/libflp.cu``: the fused head in
+``csrc/`` and the training-step operators in ``csrc_step/``) that holds the C
+ABI of ``include/flp.h`` and the kernels.  Rebuilt when any source is newer
+than the shared object.
 """
 from __future__ import annotations
 
@@ -18,7 +19,8 @@ ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
 def sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(PKG, "csrc", "*"))) + [os.path.join(ROOT, "include", "flp.h")]
+    return (sorted(glob.glob(os.path.join(PKG, "csrc", "*")) + glob.glob(os.path.join(PKG, "csrc_step", "*")))
+            + [os.path.join(ROOT, "include", "flp.h")])
 
 
 def nvcc_path() -> str:
@@ -31,7 +33,7 @@ def nvcc_path() -> str:
 def command(out: str, extra: list[str] | None = None) -> list[str]:
     return [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
             "-shared", "-I" + os.path.join(ROOT, "include"), "-o", out,
-            os.path.join(PKG, "csrc", "flp.cu")] + (extra or [])
+            os.path.join(PKG, "csrc_step", "libflp.cu")] + (extra or [])
 
 
 def stale() -> bool:

@@ -1,0 +1,609 @@
+// step_abi.cuh - host side of the training-step operators declared in
+// include/flp.h: argument checks, kernel choice by size and alignment, and
+// launches.
+#pragma once
+#include "balance.cuh"
+#include "checkpoint.cuh"
+#include "norm.cuh"
+#include "wgrad.cuh"
+
+namespace {
+
+using namespace flp;
+
+constexpr int64_t kMaxRows = INT32_MAX;
+
+// One launch; with `after_kernel` it follows another kernel of the same call
+// and may be scheduled while that one finishes (it waits in griddep_wait).
+template <typename... KArgs, typename... Args>
+flp_status launch_step(void (*kernel)(KArgs...), int64_t grid, int threads, size_t smem, cudaStream_t s,
+                       const char* what, bool after_kernel, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_kernel ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    return e == cudaSuccess ? FLP_OK : cuda_fail(e, what);
+}
+
+// The device is an sm_103 one (no attributes are needed by these kernels).
+flp_status step_device(DevInfo** d) {
+    const flp_status st = device_info(d, nullptr);
+    if (st != FLP_OK) return st;
+    if ((*d)->major != 10 || (*d)->minor != 3)
+        return fail(FLP_ERR_UNSUPPORTED, "kernels are built for sm_103a (GB300) only");
+    return FLP_OK;
+}
+
+inline bool is_dtype(int t) { return t == FLP_F32 || t == FLP_BF16; }
+inline int64_t elem(int t) { return t == FLP_F32 ? 4 : 2; }
+inline int64_t ck_cols(int64_t H) { return cdiv(H, CK_BLOCK) * CK_BLOCK; }
+
+// Whether rows at this base and pitch (in elements) are 16-byte aligned.
+inline bool rows16(const void* p, int64_t ld, int dtype) { return aligned16(p) && (ld * elem(dtype)) % 16 == 0; }
+
+// ------------------------------------------------------------------ layer norm
+
+// Calls f(threads per row, vectors per thread) as compile-time constants for
+// rows of `vecs` vectors.  Up to 1024 (16-byte vectors) or 256 elements a warp
+// takes a row, so the row sums need no block barrier; above, as many threads
+// as leave 2 to 4 vectors each, which keeps the row in registers and enough
+// loads in flight.
+template <int V, typename F>
+flp_status norm_shape(int64_t vecs, F&& f) {
+#define FLP_SHAPE(TPR, NV) \
+    if (vecs <= (TPR) * (NV)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{});
+    if constexpr (V > 1) {
+        FLP_SHAPE(32, 1)
+        FLP_SHAPE(32, 2)
+        FLP_SHAPE(32, 4)
+        FLP_SHAPE(128, 2)
+        FLP_SHAPE(256, 2)
+        FLP_SHAPE(256, 3)
+        FLP_SHAPE(512, 2)
+        FLP_SHAPE(512, 4)
+        FLP_SHAPE(1024, 4)
+    } else {
+        FLP_SHAPE(32, 8)
+        FLP_SHAPE(128, 8)
+        FLP_SHAPE(256, 16)
+        FLP_SHAPE(1024, 16)
+    }
+#undef FLP_SHAPE
+    return fail(FLP_ERR_UNSUPPORTED, "layer norm rows hold at most 16384 elements");
+}
+
+flp_status norm_checks(int64_t M, int64_t H, int dtype, int param_dtype, const void* weight, const void* bias) {
+    if (M < 0 || H < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0 and H >= 1 required");
+    if (!is_dtype(dtype) || !is_dtype(param_dtype)) return fail(FLP_ERR_INVALID_ARG, "dtypes are FLP_F32 or FLP_BF16");
+    if (M > kMaxRows) return fail(FLP_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
+    if (H > NORM_MAX_H) return fail(FLP_ERR_UNSUPPORTED, "layer norm rows hold at most 16384 elements");
+    if ((weight && reinterpret_cast<uintptr_t>(weight) % elem(param_dtype)) ||
+        (bias && reinterpret_cast<uintptr_t>(bias) % elem(param_dtype)))
+        return fail(FLP_ERR_INVALID_ARG, "weight and bias must be aligned to their elements");
+    return FLP_OK;
+}
+
+flp_status ck_checks(const void* q, const void* scale) {
+    if (!q || !scale) return fail(FLP_ERR_INVALID_ARG, "a checkpoint needs both q and scale");
+    if (!aligned16(q)) return fail(FLP_ERR_INVALID_ARG, "checkpoint q must be 16-byte aligned");
+    return FLP_OK;
+}
+
+flp_status row_checks(const void* p, int64_t ld, int64_t H, int dtype, const char* what) {
+    if (!p) return fail(FLP_ERR_INVALID_ARG, what);
+    if (ld < H || reinterpret_cast<uintptr_t>(p) % elem(dtype))
+        return fail(FLP_ERR_INVALID_ARG, "row pitch below the width, or a pointer not aligned to its elements");
+    return FLP_OK;
+}
+
+// Blocks of the norm backward: each writes 2 H partial sums, so no more than
+// fill the device.
+int64_t norm_bwd_blocks(int64_t M, int64_t rows_per_block, int sm_count, int64_t blocks_per_sm) {
+    return std::max<int64_t>(1, std::min(cdiv(M, rows_per_block), sm_count * blocks_per_sm));
+}
+
+constexpr int64_t kNormBwdBlocksPerSm = 8;  // the most any shape uses: what the workspace query allows for
+
+// -------------------------------------------------------------- weight gradient
+
+struct WgradPlan {
+    int64_t Kp;          // padded columns of X^
+    int64_t Np;          // pitch of the aligned copy of dY (0: read in place)
+    int tn, tk, whole, rest, splits, units;
+    size_t off_x, off_y, off_part, bytes;
+};
+
+// Whole rounds of tiles go straight to dW; the rest are split.  A split run
+// costs its 64-row blocks plus writing and joining its partial tile (about
+// the time of 6 blocks: 512 KiB written and read back).
+WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t K, int dw_dtype, int pairs) {
+    WgradPlan w{};
+    pairs = std::max(1, pairs);
+    w.Kp = ck_cols(K);
+    w.Np = rows16(dY, lddy, FLP_BF16) ? 0 : cdiv(N, 8) * 8;
+    w.tn = static_cast<int>(cdiv(N, PM));
+    w.tk = static_cast<int>(cdiv(K, 2 * BN));
+    const int64_t tiles = static_cast<int64_t>(w.tn) * w.tk;
+    const int64_t KB = std::max<int64_t>(1, cdiv(M, BK));
+    const bool direct = (K * elem(dw_dtype)) % 16 == 0;  // a TMA store's row pitch
+    w.whole = direct ? static_cast<int>(tiles / pairs * pairs) : 0;
+    int64_t rest = tiles - w.whole;
+    w.splits = 1;
+    if (rest > 0) {
+        double best = 1e300;
+        const int64_t most = std::min<int64_t>(KB, std::max<int64_t>(1, 4 * pairs / std::max<int64_t>(1, rest)));
+        for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
+            const double joined = s > 1 || !direct ? 6.0 : 0.0;
+            const double cost = static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(KB, s)) + joined);
+            if (cost < best - 1e-9) {
+                best = cost;
+                w.splits = static_cast<int>(s);
+            }
+        }
+        if (w.splits == 1 && direct) {
+            w.whole = static_cast<int>(tiles);
+            rest = 0;
+        }
+    }
+    w.rest = static_cast<int>(rest);
+    w.units = w.whole + w.rest * w.splits;
+    w.off_x = kHeaderBytes;
+    w.off_y = w.off_x + align_up(static_cast<size_t>(std::max<int64_t>(M, 1)) * w.Kp * 2, 1024);
+    w.off_part = w.off_y + align_up(static_cast<size_t>(M) * w.Np * 2, 1024);
+    w.bytes = w.off_part + static_cast<size_t>(w.rest) * w.splits * PM * 2 * BN * 4;
+    return w;
+}
+
+flp_status wgrad_checks(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t K, int dw_dtype) {
+    if (M < 0 || N < 1 || K < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0, N >= 1 and K >= 1 required");
+    if (M > kMaxRows - 256 || N > kMaxRows - 1024 || K > kMaxRows - 1024 ||
+        cdiv(N, PM) * cdiv(K, 2 * BN) > (1 << 24))
+        return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
+    if (!is_dtype(dw_dtype)) return fail(FLP_ERR_INVALID_ARG, "dW_dtype is FLP_F32 or FLP_BF16");
+    if (M > 0 && lddy < N) return fail(FLP_ERR_INVALID_ARG, "row pitch of dY below N");
+    if (reinterpret_cast<uintptr_t>(dY) % 2) return fail(FLP_ERR_INVALID_ARG, "dY must be aligned to its elements");
+    return FLP_OK;
+}
+
+// The contraction's shared memory, once per device.
+flp_status wgrad_attrs() {
+    static bool done[kMaxDevices] = {};
+    int dev = 0;
+    FLP_CUDA(cudaGetDevice(&dev));  // in range: check_device has run
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!done[dev]) {
+        FLP_CUDA(cudaFuncSetAttribute(flp_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        done[dev] = true;
+    }
+    return FLP_OK;
+}
+
+template <int V, typename T>
+CkParams ck_params(void* x, int64_t ldx, const void* q, const void* scale, int64_t M, int64_t H) {
+    CkParams p{};
+    p.x = x;
+    p.ldx = ldx;
+    p.q = static_cast<uint8_t*>(const_cast<void*>(q));
+    p.scale = static_cast<uint8_t*>(const_cast<void*>(scale));
+    p.M = M;
+    p.H = static_cast<int>(H);
+    p.Hp = static_cast<int>(ck_cols(H));
+    p.per_row = static_cast<unsigned>(p.Hp / V);
+    p.total = M * p.per_row;
+    return p;
+}
+
+template <typename T, int V>
+flp_status ck_launch(bool pack, void* x, int64_t ldx, const void* q, const void* scale, int64_t M, int64_t H,
+                     cudaStream_t s) {
+    const CkParams p = ck_params<V, T>(x, ldx, q, scale, M, H);
+    const int64_t grid = cdiv(p.total, CK_THREADS * CK_PER_THREAD);
+    if (grid > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
+    return pack ? launch_step(flp_ck_pack_kernel<T, V>, grid, CK_THREADS, 0, s, "flp_ck_pack_kernel launch", false, p)
+                : launch_step(flp_ck_unpack_kernel<T, V>, grid, CK_THREADS, 0, s, "flp_ck_unpack_kernel launch", false, p);
+}
+
+flp_status ck_run(bool pack, const void* x, int64_t ldx, int dtype, const void* q, const void* scale, int64_t M,
+                  int64_t H, cudaStream_t s) {
+    if (M < 0 || H < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0 and H >= 1 required");
+    if (!is_dtype(dtype)) return fail(FLP_ERR_INVALID_ARG, "dtype is FLP_F32 or FLP_BF16");
+    if (H > INT32_MAX - CK_BLOCK) return fail(FLP_ERR_UNSUPPORTED, "rows of more than 2^31 elements");
+    if (M == 0) return FLP_OK;
+    flp_status st = ck_checks(q, scale);
+    if (st == FLP_OK) st = row_checks(x, ldx, H, dtype, "X must be non-null");
+    DevInfo* d;
+    if (st == FLP_OK) st = step_device(&d);
+    if (st == FLP_OK) st = check_on_current_device(x, "X");
+    if (st != FLP_OK) return st;
+    void* xx = const_cast<void*>(x);
+    if (dtype == FLP_BF16)
+        return rows16(x, ldx, dtype) && H % 8 == 0 ? ck_launch<bf16, 8>(pack, xx, ldx, q, scale, M, H, s)
+                                                   : ck_launch<bf16, 1>(pack, xx, ldx, q, scale, M, H, s);
+    return rows16(x, ldx, dtype) && H % 4 == 0 ? ck_launch<float, 4>(pack, xx, ldx, q, scale, M, H, s)
+                                               : ck_launch<float, 1>(pack, xx, ldx, q, scale, M, H, s);
+}
+
+// ----------------------------------------------------------------- balance loss
+
+// Calls f(lanes per row, experts per lane) for E experts.
+template <typename F>
+flp_status balance_shape(int64_t E, F&& f) {
+#define FLP_SHAPE(L, NE) \
+    if (E <= (L) * (NE)) return f(std::integral_constant<int, L>{}, std::integral_constant<int, NE>{});
+    FLP_SHAPE(8, 1)
+    FLP_SHAPE(16, 1)
+    FLP_SHAPE(32, 1)
+    FLP_SHAPE(32, 2)
+    FLP_SHAPE(32, 4)
+    FLP_SHAPE(32, 8)
+    FLP_SHAPE(32, 16)
+    FLP_SHAPE(32, 32)
+#undef FLP_SHAPE
+    return fail(FLP_ERR_UNSUPPORTED, "at most 1024 experts");
+}
+
+constexpr int64_t kBalanceBlocksPerSm = 4;
+
+struct BalancePlan {
+    int64_t blocks;
+    size_t off_stat, off_p, off_c, off_n, off_load, bytes;
+};
+
+BalancePlan plan_balance(int64_t T, int64_t E, int sm_count) {
+    BalancePlan b{};
+    const int64_t lanes = E <= 8 ? 8 : E <= 16 ? 16 : 32;
+    const int64_t rows = BAL_THREADS / lanes;
+    b.blocks = std::min(cdiv(T, rows), sm_count * kBalanceBlocksPerSm);
+    b.off_stat = 0;
+    b.off_p = align_up(static_cast<size_t>(T) * 8, 256);
+    b.off_c = b.off_p + align_up(static_cast<size_t>(b.blocks) * E * 4, 256);
+    b.off_n = b.off_c + align_up(static_cast<size_t>(b.blocks) * E * 4, 256);
+    b.off_load = b.off_n + align_up(static_cast<size_t>(b.blocks) * 4, 256);
+    b.bytes = b.off_load + align_up(static_cast<size_t>(E + 1) * 4, 256);
+    return b;
+}
+
+flp_status balance_checks(int64_t T, int64_t E, int64_t top_k) {
+    if (T < 0 || E < 1) return fail(FLP_ERR_INVALID_ARG, "T >= 0 and E >= 1 required");
+    if (top_k < 1 || top_k > E) return fail(FLP_ERR_INVALID_ARG, "1 <= top_k <= E required");
+    if (E > BAL_MAX_E) return fail(FLP_ERR_UNSUPPORTED, "at most 1024 experts");
+    if (T > kMaxRows) return fail(FLP_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
+    return FLP_OK;
+}
+
+}  // namespace
+
+// =================================================================== C ABI
+
+extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, const void* weight, const void* bias,
+                                     int param_dtype, int64_t M, int64_t H, float eps, void* Y, int64_t ldy,
+                                     float* mean, float* rstd, void* q, void* scale, void* stream) {
+    flp_status st = norm_checks(M, H, dtype, param_dtype, weight, bias);
+    if (st != FLP_OK) return st;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(FLP_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (M == 0) return FLP_OK;
+    st = row_checks(X, ldx, H, dtype, "X must be non-null");
+    if (st == FLP_OK) st = row_checks(Y, ldy, H, dtype, "Y must be non-null");
+    if (st == FLP_OK && (q || scale)) st = ck_checks(q, scale);
+    DevInfo* d;
+    if (st == FLP_OK) st = step_device(&d);
+    if (st == FLP_OK) st = check_on_current_device(X, "X");
+    if (st != FLP_OK) return st;
+    NormFwdParams p{};
+    p.x = X;
+    p.ldx = ldx;
+    p.w = weight;
+    p.b = bias;
+    p.param_f32 = param_dtype == FLP_F32;
+    p.M = M;
+    p.H = static_cast<int>(H);
+    p.inv_h = static_cast<float>(1.0 / static_cast<double>(H));
+    p.eps = eps;
+    p.y = Y;
+    p.ldy = ldy;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.q = static_cast<uint8_t*>(q);
+    p.scale = static_cast<uint8_t*>(scale);
+    p.Hp = static_cast<int>(ck_cols(H));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto run = [&](auto t, auto v, auto ck) -> flp_status {
+        using T = decltype(t);
+        constexpr int V = decltype(v)::value;
+        constexpr bool CK = decltype(ck)::value;
+        return norm_shape<V>(cdiv(CK ? p.Hp : p.H, V), [&](auto tpr, auto nv) {
+            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+            constexpr int RPB = norm_rows_per_block<TPR>();
+            return launch_step(flp_norm_fwd_kernel<T, V, TPR, NV, CK>, cdiv(M, RPB), TPR * RPB, 0, s,
+                               "flp_norm_fwd_kernel launch", false, p);
+        });
+    };
+    auto typed = [&](auto t) -> flp_status {
+        using T = decltype(t);
+        constexpr int V = wide_v<T>();
+        const bool wide = H % V == 0 && rows16(X, ldx, dtype) && rows16(Y, ldy, dtype) && aligned16(weight) && aligned16(bias);
+        if (wide)
+            return q ? run(t, std::integral_constant<int, V>{}, std::true_type{})
+                     : run(t, std::integral_constant<int, V>{}, std::false_type{});
+        return q ? run(t, std::integral_constant<int, 1>{}, std::true_type{})
+                 : run(t, std::integral_constant<int, 1>{}, std::false_type{});
+    };
+    return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
+}
+
+extern "C" flp_status flp_layer_norm_workspace(int64_t M, int64_t H, size_t* bytes) {
+    if (!bytes) return fail(FLP_ERR_INVALID_ARG, "bytes must be non-null");
+    flp_status st = norm_checks(M, H, FLP_F32, FLP_F32, nullptr, nullptr);
+    if (st != FLP_OK) return st;
+    DevInfo* d;
+    st = step_device(&d);
+    if (st != FLP_OK) return st;
+    *bytes = static_cast<size_t>(norm_bwd_blocks(M, 1, d->sm_count, kNormBwdBlocksPerSm)) * 2 * H * 4;
+    return FLP_OK;
+}
+
+extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* q,
+                                              const void* scale, int dtype, const void* weight, int param_dtype,
+                                              const float* mean, const float* rstd, int64_t M, int64_t H, void* dX,
+                                              int64_t lddx, float* dweight, float* dbias, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+    flp_status st = norm_checks(M, H, dtype, param_dtype, weight, nullptr);
+    if (st != FLP_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    DevInfo* d;
+    if (M > 0) {
+        if ((X != nullptr) == (q != nullptr)) return fail(FLP_ERR_INVALID_ARG, "exactly one of X and its checkpoint");
+        if (!mean || !rstd) return fail(FLP_ERR_INVALID_ARG, "mean and rstd must be non-null");
+        st = row_checks(dY, lddy, H, dtype, "dY must be non-null");
+        if (st == FLP_OK) st = row_checks(dX, lddx, H, dtype, "dX must be non-null");
+        if (st == FLP_OK && X) st = row_checks(X, ldx, H, dtype, "X must be non-null");
+        if (st == FLP_OK && q) st = ck_checks(q, scale);
+    }
+    if (st == FLP_OK) st = step_device(&d);
+    if (st == FLP_OK && M > 0) st = check_on_current_device(dY, "dY");
+    if (st != FLP_OK) return st;
+    const bool sums = dweight || dbias;
+    int64_t blocks = 0;
+    if (M > 0) {
+        if (!workspace || !aligned16(workspace))
+            return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace null or misaligned");
+        NormBwdParams p{};
+        p.dy = dY;
+        p.lddy = lddy;
+        p.x = X;
+        p.ldx = ldx;
+        p.q = static_cast<const uint8_t*>(q);
+        p.scale = static_cast<const uint8_t*>(scale);
+        p.Hp = static_cast<int>(ck_cols(H));
+        p.w = weight;
+        p.param_f32 = param_dtype == FLP_F32;
+        p.mean = mean;
+        p.rstd = rstd;
+        p.M = M;
+        p.H = static_cast<int>(H);
+        p.inv_h = static_cast<float>(1.0 / static_cast<double>(H));
+        p.dx = dX;
+        p.lddx = lddx;
+        p.part = static_cast<float*>(workspace);
+        auto run = [&](auto t, auto v, auto ck) -> flp_status {
+            using T = decltype(t);
+            constexpr int V = decltype(v)::value;
+            constexpr bool CK = decltype(ck)::value;
+            return norm_shape<V>(cdiv(p.H, V), [&](auto tpr, auto nv) {
+                constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+                constexpr int RPB = norm_rows_per_block<TPR>();
+                constexpr int threads = TPR * RPB;
+                blocks = norm_bwd_blocks(M, RPB, d->sm_count, std::max(1, std::min<int>(kNormBwdBlocksPerSm, 512 / threads)));
+                if (workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
+                    return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
+                return launch_step(flp_norm_bwd_kernel<T, V, TPR, NV, CK>, blocks, threads, 0, s,
+                                   "flp_norm_bwd_kernel launch", false, p);
+            });
+        };
+        auto typed = [&](auto t) -> flp_status {
+            using T = decltype(t);
+            constexpr int V = wide_v<T>();
+            const bool wide = H % V == 0 && rows16(dY, lddy, dtype) && rows16(dX, lddx, dtype) && aligned16(weight) &&
+                              (!X || rows16(X, ldx, dtype));
+            if (wide)
+                return q ? run(t, std::integral_constant<int, V>{}, std::true_type{})
+                         : run(t, std::integral_constant<int, V>{}, std::false_type{});
+            return q ? run(t, std::integral_constant<int, 1>{}, std::true_type{})
+                     : run(t, std::integral_constant<int, 1>{}, std::false_type{});
+        };
+        st = dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
+        if (st != FLP_OK) return st;
+    }
+    if (!sums) return FLP_OK;
+    NormJoinParams j{};
+    j.part = static_cast<const float*>(workspace);
+    j.P = static_cast<int>(blocks);
+    j.H = static_cast<int>(H);
+    j.dw = dweight;
+    j.db = dbias;
+    return launch_step(flp_norm_join_kernel, cdiv(2 * H, 32), 1024, 0, s, "flp_norm_join_kernel launch", M > 0, j);
+}
+
+extern "C" flp_status flp_checkpoint_pack(const void* X, int64_t ldx, int dtype, int64_t M, int64_t H, void* q,
+                                          void* scale, void* stream) {
+    return ck_run(true, X, ldx, dtype, q, scale, M, H, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" flp_status flp_checkpoint_unpack(const void* q, const void* scale, int64_t M, int64_t H, void* X,
+                                            int64_t ldx, int dtype, void* stream) {
+    return ck_run(false, X, ldx, dtype, q, scale, M, H, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" flp_status flp_checkpoint_weight_grad_workspace(const void* dY, int64_t lddy, int64_t M, int64_t N,
+                                                           int64_t K, int dW_dtype, size_t* bytes) {
+    if (!bytes) return fail(FLP_ERR_INVALID_ARG, "bytes must be non-null");
+    flp_status st = wgrad_checks(dY, lddy, M, N, K, dW_dtype);
+    if (st != FLP_OK) return st;
+    DevInfo* d;
+    st = check_device(&d);
+    if (st != FLP_OK) return st;
+    *bytes = plan_wgrad(dY, lddy, M, N, K, dW_dtype, d->pairs).bytes;
+    return FLP_OK;
+}
+
+extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, const void* q, const void* scale,
+                                                 int64_t M, int64_t N, int64_t K, void* dW, int dW_dtype,
+                                                 int accumulate_dW, void* workspace, size_t workspace_bytes,
+                                                 void* stream) {
+    flp_status st = wgrad_checks(dY, lddy, M, N, K, dW_dtype);
+    if (st != FLP_OK) return st;
+    if (!dW || !aligned16(dW)) return fail(FLP_ERR_INVALID_ARG, "dW must be non-null and 16-byte aligned");
+    if (accumulate_dW && dW_dtype != FLP_F32)
+        return fail(FLP_ERR_UNSUPPORTED, "only an fp32 dW accumulates (a bf16 one would be rounded at every call)");
+    if (M > 0 && !dY) return fail(FLP_ERR_INVALID_ARG, "dY must be non-null");
+    if (M > 0 && (st = ck_checks(q, scale)) != FLP_OK) return st;
+    DevInfo* d;
+    st = check_device(&d);
+    if (st != FLP_OK) return st;
+    if ((st = check_on_current_device(dW, "dW")) != FLP_OK) return st;
+    if ((st = wgrad_attrs()) != FLP_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const WgradPlan w = plan_wgrad(dY, lddy, M, N, K, dW_dtype, d->pairs);
+    if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace))
+        return fail(FLP_ERR_WORKSPACE, "weight gradient workspace null, misaligned or too small");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    FLP_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));  // the error word
+    if (M == 0) {
+        if (!accumulate_dW) FLP_CUDA(cudaMemsetAsync(dW, 0, static_cast<size_t>(N) * K * elem(dW_dtype), s));
+        return FLP_OK;
+    }
+    if ((st = check_on_current_device(dY, "dY")) != FLP_OK) return st;
+    // the pads of the checkpoint's last blocks are unpacked with the rest (they hold zeros)
+    if ((st = ck_launch<bf16, 8>(false, ws + w.off_x, w.Kp, q, scale, M, w.Kp, s)) != FLP_OK) return st;
+    const void* y = dY;
+    int64_t ldy = lddy;
+    if (w.Np) {
+        y = ws + w.off_y;
+        ldy = w.Np;
+        st = launch_step(flp_wgrad_align_kernel, M, 256, 0, s, "flp_wgrad_align_kernel launch", false,
+                         static_cast<const bf16*>(dY), static_cast<long long>(lddy), static_cast<int>(N),
+                         reinterpret_cast<bf16*>(ws + w.off_y), static_cast<long long>(w.Np));
+        if (st != FLP_OK) return st;
+    }
+    const int64_t es = elem(dW_dtype);
+    const bool b16 = dW_dtype == FLP_BF16;
+    CUtensorMap my, mx, mw, mp;
+    if ((st = tmap_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, ldy * 2, 64, 64)) != FLP_OK) return st;
+    if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ws + w.off_x, w.Kp, M, w.Kp * 2, 64, 64)) != FLP_OK)
+        return st;
+    const size_t part_rows = std::max<size_t>(1, static_cast<size_t>(w.rest) * w.splits) * PM;
+    // without split tiles (or without whole ones) one of the two output maps is
+    // not used: it repeats the other
+    if (w.rest &&
+        (st = tmap_2d(&mp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + w.off_part, 2 * BN, part_rows, 2 * BN * 4, 16, BM,
+                      CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
+        return st;
+    if (w.whole &&
+        (st = tmap_2d(&mw, b16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dW, K, N, K * es,
+                      b16 ? 32 : 16, BM, CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
+        return st;
+    if (!w.rest) mp = mw;
+    if (!w.whole) mw = mp;
+    WgradParams p{};
+    p.tn = w.tn;
+    p.tk = w.tk;
+    p.group = std::min(w.tn, 8);
+    p.whole = w.whole;
+    p.splits = w.splits;
+    p.units = w.units;
+    p.KB = static_cast<int>(cdiv(M, BK));
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.add = accumulate_dW ? 1 : 0;
+    p.bf16_out = b16 ? 1 : 0;
+    p.err = reinterpret_cast<int*>(ws);
+    p.wait_limit_ns = kWaitLimitNs;
+    const int grid = 2 * static_cast<int>(std::min<int64_t>(w.units, d->pairs));
+    st = launch_pairs_n(flp_wgrad_kernel, grid, WIDE_THREADS, s, "flp_wgrad_kernel launch", true, my, mx, mw, mp, p);
+    if (st != FLP_OK || !w.rest) return st;
+    WgradJoinParams j{};
+    j.part = reinterpret_cast<const float*>(ws + w.off_part);
+    j.g = p;
+    j.dw = dW;
+    j.add = p.add;
+    j.err = p.err;
+    return launch_step(flp_wgrad_join_kernel, static_cast<int64_t>(w.rest) * (PM / WJ_ROWS), WJ_THREADS, 0, s,
+                       "flp_wgrad_join_kernel launch", true, j);
+}
+
+extern "C" flp_status flp_balance_loss_workspace(int64_t T, int64_t E, size_t* bytes) {
+    if (!bytes) return fail(FLP_ERR_INVALID_ARG, "bytes must be non-null");
+    flp_status st = balance_checks(T, E, 1);
+    if (st != FLP_OK) return st;
+    DevInfo* d;
+    st = step_device(&d);
+    if (st != FLP_OK) return st;
+    *bytes = plan_balance(T, E, d->sm_count).bytes;
+    return FLP_OK;
+}
+
+extern "C" flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype, const uint8_t* mask,
+                                       const int64_t* experts, int64_t T, int64_t E, int64_t top_k, float coef,
+                                       float* loss, void* grad, int64_t* counts, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    flp_status st = balance_checks(T, E, top_k);
+    if (st != FLP_OK) return st;
+    if (!is_dtype(dtype)) return fail(FLP_ERR_INVALID_ARG, "dtype is FLP_F32 or FLP_BF16");
+    if (!loss || !counts) return fail(FLP_ERR_INVALID_ARG, "loss and counts must be non-null");
+    if (!std::isfinite(coef)) return fail(FLP_ERR_INVALID_ARG, "coef must be finite");
+    if (T > 0 && (st = row_checks(logits, ld, E, dtype, "logits must be non-null")) != FLP_OK) return st;
+    if (reinterpret_cast<uintptr_t>(grad) % elem(dtype))
+        return fail(FLP_ERR_INVALID_ARG, "grad must be aligned to its elements");
+    DevInfo* d;
+    st = step_device(&d);
+    if (st != FLP_OK) return st;
+    if (T > 0 && (st = check_on_current_device(logits, "logits")) != FLP_OK) return st;
+    const BalancePlan b = plan_balance(T, E, d->sm_count);
+    if (!workspace || workspace_bytes < b.bytes || !aligned16(workspace))
+        return fail(FLP_ERR_WORKSPACE, "balance loss workspace null, misaligned or too small");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    BalParams p{};
+    p.z = logits;
+    p.ld = ld;
+    p.mask = mask;
+    p.experts = reinterpret_cast<const long long*>(experts);
+    p.T = T;
+    p.E = static_cast<int>(E);
+    p.k = static_cast<int>(top_k);
+    p.coef = coef;
+    p.grad = grad;
+    p.loss = loss;
+    p.counts = reinterpret_cast<long long*>(counts);
+    p.stat = reinterpret_cast<float2*>(ws + b.off_stat);
+    p.part_p = reinterpret_cast<float*>(ws + b.off_p);
+    p.part_c = reinterpret_cast<int*>(ws + b.off_c);
+    p.part_n = reinterpret_cast<int*>(ws + b.off_n);
+    p.load = reinterpret_cast<float*>(ws + b.off_load);
+    p.blocks = static_cast<int>(b.blocks);
+    const size_t smem = (2 * static_cast<size_t>(E) + 1) * 4;
+    auto typed = [&](auto t) -> flp_status {
+        using T_ = decltype(t);
+        return balance_shape(E, [&](auto l, auto ne) -> flp_status {
+            constexpr int L = decltype(l)::value, NE = decltype(ne)::value;
+            if (T > 0) {
+                const flp_status r = launch_step(flp_balance_rows_kernel<T_, L, NE>, b.blocks, BAL_THREADS, smem, s,
+                                                 "flp_balance_rows_kernel launch", false, p);
+                if (r != FLP_OK) return r;
+            }
+            const flp_status r = launch_step(flp_balance_join_kernel, 1, BAL_JOIN_THREADS, 0, s,
+                                             "flp_balance_join_kernel launch", T > 0, p);
+            if (r != FLP_OK || !grad || T == 0) return r;
+            return launch_step(flp_balance_grad_kernel<T_, L, NE>, b.blocks, BAL_THREADS, 0, s,
+                               "flp_balance_grad_kernel launch", true, p);
+        });
+    };
+    return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
+}

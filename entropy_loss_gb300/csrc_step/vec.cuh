@@ -1,0 +1,264 @@
+// vec.cuh - what the training-step kernels share: typed vector access, warp
+// and row reductions, and the 8-bit checkpoint's block arithmetic.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+
+namespace flp {
+
+using bf16 = __nv_bfloat16;
+
+// Elements per access: 16 bytes where rows are 16-byte aligned and hold a
+// whole number of such vectors, else one element.
+template <typename T>
+__host__ __device__ constexpr int wide_v() { return 16 / static_cast<int>(sizeof(T)); }
+
+// V elements as loaded, and their values in fp32.
+template <typename T, int V>
+struct Raw;
+template <>
+struct Raw<bf16, 8> {
+    uint4 u;
+    __device__ __forceinline__ void load(const bf16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load_kept(const bf16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void to(float (&v)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Raw<float, 4> {
+    float4 u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldcs(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void load_kept(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void to(float (&v)[4]) const {
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    }
+};
+template <>
+struct Raw<bf16, 1> {
+    unsigned short u;
+    __device__ __forceinline__ void load(const bf16* p) { u = __ldcs(reinterpret_cast<const unsigned short*>(p)); }
+    __device__ __forceinline__ void load_kept(const bf16* p) { u = __ldg(reinterpret_cast<const unsigned short*>(p)); }
+    __device__ __forceinline__ void zero() { u = 0; }
+    __device__ __forceinline__ void to(float (&v)[1]) const { v[0] = __uint_as_float(static_cast<uint32_t>(u) << 16); }
+};
+template <>
+struct Raw<float, 1> {
+    float u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldcs(p); }
+    __device__ __forceinline__ void load_kept(const float* p) { u = __ldg(p); }
+    __device__ __forceinline__ void zero() { u = 0.f; }
+    __device__ __forceinline__ void to(float (&v)[1]) const { v[0] = u; }
+};
+
+// Stores V values at p, rounded once to T (nearest, ties to even).
+template <int V>
+__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[V]) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    else
+        *p = __float2bfloat16_rn(v[0]);
+}
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
+    if constexpr (V == 4)
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *p = v[0];
+}
+
+// Parameters (norm weight and bias): V values of either type, kept in cache.
+template <int V>
+__device__ __forceinline__ void load_param(const void* base, bool f32, int col, float (&v)[V]) {
+    if (f32) {
+        const float* p = static_cast<const float*>(base) + col;
+        if constexpr (V % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
+                v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+            }
+        } else {
+            v[0] = __ldg(p);
+        }
+    } else {
+        const unsigned short* p = static_cast<const unsigned short*>(base) + col;
+        uint32_t w[(V + 1) / 2];
+        if constexpr (V == 8) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else if constexpr (V == 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = u.x, w[1] = u.y;
+        } else {
+            w[0] = __ldg(p);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sums of N values over the TPR threads of a row (a warp, or the whole block);
+// every thread gets them, in the same order.  `red` holds 32 * N floats that
+// no thread of the block still reads (alternate two of them between calls).
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
+    if constexpr (TPR > 32) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) red[n * 32 + warp] = v[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float s = 0.f;
+            if constexpr (TPR <= 256) {
+#pragma unroll
+                for (int w = 0; w < TPR / 32; ++w) s += red[n * 32 + w];
+            } else {
+                s = warp_sum(lane < TPR / 32 ? red[n * 32 + lane] : 0.f);
+            }
+            v[n] = s;
+        }
+    }
+}
+
+// ------------------------------------------------------------ 8-bit blocks
+//
+// A block is 32 consecutive columns of a row.  With a = max |x| over it and
+// E = floor(log2 a), its step is 2^max(E - 6, -126) and
+//     q = clamp(rint(x / step), -127, 127),   value = q * step.
+// The step's biased exponent is the block's scale byte (1..249); |x| / step is
+// below 128, so only values that round to 128 are clamped (by at most one
+// step).  A block that holds a NaN or an infinity gets the byte 255 and reads
+// back as NaN.  Dividing by a power of two is exact, and 7 bits of magnitude
+// times a power of two are exact in bf16, so the values are the same however
+// they are computed.
+
+constexpr int CK_BLOCK = 32;
+constexpr uint32_t CK_NAN = 255;
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The scale byte of a block from the largest |x| bits in it (NaN > inf > finite).
+__device__ __forceinline__ uint32_t ck_byte(uint32_t top) {
+    return top >= 0x7f800000u ? CK_NAN : static_cast<uint32_t>(max(1, static_cast<int>(top >> 23) - 6));
+}
+
+// 1 / step and step of a scale byte.
+__device__ __forceinline__ float ck_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+__device__ __forceinline__ float ck_step(uint32_t byte) {
+    return byte == CK_NAN ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
+}
+
+// rint(x * inverse) in [-127, 127] as the low byte of the result: adding
+// 1.5 * 2^23 rounds to an integer (ties to even) that sits in the low mantissa
+// bits as two's complement; the product is exact, so the fma rounds once.
+__device__ __forceinline__ uint32_t ck_round(float x, float inverse) {
+    const float magic = 12582912.f;
+    return __float_as_uint(fminf(fmaxf(__fmaf_rn(x, inverse, magic), magic - 127.f), magic + 127.f));
+}
+
+// The low bytes of four words in one.
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Four values of a q word times the step: byte b + 128 placed in the mantissa
+// of 2^23 gives 2^23 + 128 + q, from which q comes out exactly.
+__device__ __forceinline__ void ck_values4(uint32_t q, float step, float* v) {
+    const uint32_t u = q ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 + i)) - 8388736.f) * step;
+}
+
+// Quantises one vector of a row: lanes that are consecutive in `lane` order
+// hold consecutive vectors, so CK_BLOCK / V of them share a block.  `w` gets
+// the V bytes (one word for V <= 4); returns the block's scale byte.  Every
+// lane of the warp takes part.
+template <int V>
+__device__ __forceinline__ uint32_t ck_quantise(const float (&v)[V], uint32_t (&w)[V > 4 ? 2 : 1]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = max(top, abs_bits(v[i]));
+#pragma unroll
+    for (int o = 1; o < CK_BLOCK / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t byte = ck_byte(top);
+    const float inv = byte == CK_NAN ? 0.f : ck_inverse(byte);
+    uint32_t r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[i] = ck_round(v[i], inv);
+    if constexpr (V == 1) {
+        w[0] = r[0] & 0xffu;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) w[i] = pack_bytes(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    }
+    if (byte == CK_NAN) {
+#pragma unroll
+        for (int i = 0; i < (V > 4 ? 2 : 1); ++i) w[i] = 0;
+    }
+    return byte;
+}
+
+template <int V>
+__device__ __forceinline__ void ck_store(uint8_t* q, const uint32_t (&w)[V > 4 ? 2 : 1]) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint32_t*>(q) = w[0];
+    else
+        *q = static_cast<uint8_t>(w[0]);
+}
+
+// V bytes of a checkpoint row and their block's scale byte.
+template <int V>
+struct RawCk {
+    uint32_t w[V > 4 ? 2 : 1];
+    uint32_t byte;
+    __device__ __forceinline__ void load(const uint8_t* q, const uint8_t* scale, int col) {
+        if constexpr (V == 8) {
+            const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q + col));
+            w[0] = u.x, w[1] = u.y;
+        } else if constexpr (V == 4) {
+            w[0] = __ldcs(reinterpret_cast<const uint32_t*>(q + col));
+        } else {
+            w[0] = __ldcs(q + col);
+        }
+        byte = __ldcs(scale + col / CK_BLOCK);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (V > 4 ? 2 : 1); ++i) w[i] = 0;
+        byte = 1;
+    }
+    __device__ __forceinline__ void to(float (&v)[V]) const {
+        const float step = ck_step(byte);
+        if constexpr (V == 1) {
+            v[0] = (__uint_as_float(0x4b000000u | (w[0] ^ 0x80u)) - 8388736.f) * step;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) ck_values4(w[i], step, v + 4 * i);
+        }
+    }
+};
+
+}  // namespace flp

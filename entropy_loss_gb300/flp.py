@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -29,7 +30,10 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_set_phase_events", "flp_status_string", "flp_last_error_message",
            "flp_forward_noalloc", "flp_selftest_wait_timeout", "flp_loss", "flp_backward_ex",
            "flp_backward_plan", "flp_backward_schedule", "flp_selftest_dependency_timeout",
-           "flp_selftest_dz_wait_timeout", "flp_policy_loss")
+           "flp_selftest_dz_wait_timeout", "flp_policy_loss", "flp_layer_norm", "flp_layer_norm_workspace",
+           "flp_layer_norm_backward", "flp_checkpoint_pack", "flp_checkpoint_unpack",
+           "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad",
+           "flp_balance_loss_workspace", "flp_balance_loss")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
 FLP_LOSS_NLL_SUM = 3
@@ -106,6 +110,20 @@ def load(path: str = LIB_PATH):
     lib.flp_policy_loss.argtypes = [p, p, i64, i64, p, i64, p, p, p, ctypes.c_float, ctypes.c_float,
                                     ctypes.c_float, i32, i32, ctypes.c_double, p, p, p, p]
     lib.flp_policy_loss.restype = i32
+    f32, size = ctypes.c_float, ctypes.POINTER(ctypes.c_size_t)
+    for name, args in (
+            ("flp_layer_norm", [p, i64, i32, p, p, i32, i64, i64, f32, p, i64, p, p, p, p, p]),
+            ("flp_layer_norm_workspace", [i64, i64, size]),
+            ("flp_layer_norm_backward", [p, i64, p, i64, p, p, i32, p, i32, p, p, i64, i64, p, i64, p, p, p,
+                                         ctypes.c_size_t, p]),
+            ("flp_checkpoint_pack", [p, i64, i32, i64, i64, p, p, p]),
+            ("flp_checkpoint_unpack", [p, p, i64, i64, p, i64, i32, p]),
+            ("flp_checkpoint_weight_grad_workspace", [p, i64, i64, i64, i64, i32, size]),
+            ("flp_checkpoint_weight_grad", [p, i64, p, p, i64, i64, i64, p, i32, i32, p, ctypes.c_size_t, p]),
+            ("flp_balance_loss_workspace", [i64, i64, size]),
+            ("flp_balance_loss", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, p, p, ctypes.c_size_t, p])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, i32
     lib.flp_get_error.argtypes = [p, p]
     lib.flp_set_phase_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i32]
     lib.flp_set_phase_events.restype = i32
@@ -404,6 +422,254 @@ def policy_loss(logprob, y, old_logprob, advantage, *, seq_offsets=None, ignore_
                                   _ptr(out), _stream(stream)),
            "flp_policy_loss")
     return out, grad, per
+
+
+# ---------------------------------------------------------------- training-step operators
+#
+# The norm in front of the head, 8-bit checkpoints of activations with their
+# use in the backward pass, and the router balance loss (include/flp.h has the
+# formulas).  Row matrices may have any row pitch (a view of a wider tensor);
+# their last dimension is contiguous.
+
+CHECKPOINT_BLOCK = 32  # columns that share a step
+_DTYPE = {torch.float32: FLP_F32, torch.bfloat16: FLP_BF16}
+
+
+class Checkpoint8(NamedTuple):
+    """An 8-bit checkpoint of a [rows, cols] activation: q int8 [rows, padded
+    cols], scale uint8 [rows, padded cols / 32], and the type it reads back as."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+    dtype: torch.dtype
+
+    @property
+    def shape(self):
+        return (self.q.shape[0], self.cols)
+
+
+def _dtype(t, name):
+    try:
+        return _DTYPE[t.dtype]
+    except KeyError:
+        raise ValueError(f"{name}: expected bf16 or fp32, got {t.dtype}") from None
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """(address, row pitch) of a CUDA matrix whose rows are contiguous."""
+    if t.dim() != 2 or not t.is_cuda or (shape is not None and t.shape != shape) or (
+            dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{name}: expected a CUDA matrix{'' if shape is None else f' of shape {tuple(shape)}'}"
+                         f"{'' if dtype is None else f' of {dtype}'}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    pitch, unit = t.stride()
+    rows, cols = t.shape
+    if (unit != 1 and cols > 1) or (pitch < cols and rows > 1):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
+    return t.data_ptr(), pitch if rows > 1 else cols
+
+
+def _check_checkpoint(c, name):
+    rows, padded = c.q.shape
+    if (c.q.dtype is not torch.int8 or c.scale.dtype is not torch.uint8 or not c.q.is_cuda or not c.scale.is_cuda
+            or padded != -(-c.cols // CHECKPOINT_BLOCK) * CHECKPOINT_BLOCK
+            or c.scale.shape != (rows, padded // CHECKPOINT_BLOCK)
+            or not c.q.is_contiguous() or not c.scale.is_contiguous()):
+        raise ValueError(f"{name}: not an 8-bit checkpoint: q {c.q.dtype} {tuple(c.q.shape)}, scale {c.scale.dtype} "
+                         f"{tuple(c.scale.shape)}, {c.cols} columns")
+
+
+def _new_checkpoint(rows, cols, dtype, device):
+    blocks = -(-cols // CHECKPOINT_BLOCK)
+    return Checkpoint8(torch.empty(rows, blocks * CHECKPOINT_BLOCK, dtype=torch.int8, device=device),
+                       torch.empty(rows, blocks, dtype=torch.uint8, device=device), cols, dtype)
+
+
+def _norm_param(t, cols, dtype, name):
+    """Address of a norm parameter: [cols], the activations' type or fp32."""
+    if t is None:
+        return None
+    if t.dtype not in (dtype, torch.float32) or t.shape != (cols,) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous CUDA {dtype} or fp32 of shape ({cols},), "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _query(fn, what, *args):
+    n = ctypes.c_size_t(0)
+    _check(fn(*args, ctypes.byref(n)), what)
+    return n.value
+
+
+def _scratch(workspace, fn, what, *args):
+    """(address, bytes, owner) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(max(16, _query(fn, what, *args)), dtype=torch.uint8, device="cuda")
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor")
+    return workspace.data_ptr(), _nbytes(workspace), workspace
+
+
+def _on_stream(stream, fn, *args, **kw):
+    """fn on `stream`, which its new tensors and workspace then belong to."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _raw_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, checkpoint: bool = False, out=None, stream=None):
+    """Layer norm of each row of x [M, H] (bf16 or fp32; weight and bias in x's
+    type or both fp32): (y, mean, rstd), and with `checkpoint` also the
+    Checkpoint8 of x, written from the same read."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm, x, weight, bias, eps=eps, checkpoint=checkpoint, out=out)
+    xp, ldx = _rows(x, "x")
+    M, H = x.shape
+    dt, dev = x.dtype, x.device
+    code = _dtype(x, "x")
+    wp, bp = _norm_param(weight, H, dt, "weight"), _norm_param(bias, H, dt, "bias")
+    param = weight if weight is not None else bias
+    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
+        raise ValueError(f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
+    if out is None:
+        out = torch.empty(M, H, dtype=dt, device=dev)
+    yp, ldy = _rows(out, "out", x.shape, dt)
+    mean, rstd = torch.empty(2, M, dtype=torch.float32, device=dev).unbind(0)
+    kept = _new_checkpoint(M, H, dt, dev) if checkpoint else None
+    status = load().flp_layer_norm(xp, ldx, code, wp, bp, code if param is None else _DTYPE[param.dtype], M, H, eps,
+                                   yp, ldy, mean.data_ptr(), rstd.data_ptr(),
+                                   kept.q.data_ptr() if checkpoint else None,
+                                   kept.scale.data_ptr() if checkpoint else None, _raw_stream())
+    if status:
+        _check(status, "flp_layer_norm")
+    return (out, mean, rstd, kept) if checkpoint else (out, mean, rstd)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, workspace=None, stream=None):
+    """(dx, dweight, dbias) of layer_norm; x is the activation (dy's type) or
+    its Checkpoint8, mean and rstd the forward's.  dx has dy's type, dweight
+    and dbias are fp32.  Without a weight its gradient is the one of all ones."""
+    if stream is not None:
+        return _on_stream(stream, layer_norm_backward, dy, x, weight, mean, rstd, dx=dx, workspace=workspace)
+    dyp, lddy = _rows(dy, "dy")
+    M, H = dy.shape
+    dt, dev = dy.dtype, dy.device
+    code = _dtype(dy, "dy")
+    xp = ldx = qp = sp = None
+    if isinstance(x, Checkpoint8):
+        _check_checkpoint(x, "x")
+        if x.shape != (M, H):
+            raise ValueError(f"x: checkpoint of shape {x.shape}, expected {(M, H)}")
+        qp, sp, ldx = x.q.data_ptr(), x.scale.data_ptr(), 0
+    else:
+        xp, ldx = _rows(x, "x", dy.shape, dt)
+    wp = _norm_param(weight, H, dt, "weight")
+    _need(mean, torch.float32, (M,), "mean")
+    _need(rstd, torch.float32, (M,), "rstd")
+    if dx is None:
+        dx = torch.empty(M, H, dtype=dt, device=dev)
+    dxp, lddx = _rows(dx, "dx", dy.shape, dt)
+    dweight, dbias = torch.empty(2, H, dtype=torch.float32, device=dev).unbind(0)
+    lib = load()
+    ws, ws_bytes, _keep = _scratch(workspace, lib.flp_layer_norm_workspace, "flp_layer_norm_workspace", M, H)
+    status = lib.flp_layer_norm_backward(dyp, lddy, xp, ldx, qp, sp, code, wp,
+                                         code if weight is None else _DTYPE[weight.dtype], mean.data_ptr(),
+                                         rstd.data_ptr(), M, H, dxp, lddx, dweight.data_ptr(), dbias.data_ptr(),
+                                         ws, ws_bytes, _raw_stream())
+    if status:
+        _check(status, "flp_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+def checkpoint_pack(x, *, stream=None) -> Checkpoint8:
+    """The 8-bit checkpoint of x [M, H] (bf16 or fp32): 33/32 bytes an element."""
+    if stream is not None:
+        return _on_stream(stream, checkpoint_pack, x)
+    xp, ldx = _rows(x, "x")
+    code = _dtype(x, "x")
+    kept = _new_checkpoint(x.shape[0], x.shape[1], x.dtype, x.device)
+    status = load().flp_checkpoint_pack(xp, ldx, code, x.shape[0], x.shape[1], kept.q.data_ptr(),
+                                        kept.scale.data_ptr(), _raw_stream())
+    if status:
+        _check(status, "flp_checkpoint_pack")
+    return kept
+
+
+def checkpoint_unpack(kept: Checkpoint8, *, dtype=None, out=None, stream=None):
+    """The values a checkpoint stands for, in its own type or the given one."""
+    if stream is not None:
+        return _on_stream(stream, checkpoint_unpack, kept, dtype=dtype, out=out)
+    _check_checkpoint(kept, "checkpoint")
+    if out is None:
+        out = torch.empty(kept.shape, dtype=dtype or kept.dtype, device=kept.q.device)
+    elif dtype is not None and out.dtype is not dtype:
+        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+    xp, ldx = _rows(out, "out", kept.shape)
+    status = load().flp_checkpoint_unpack(kept.q.data_ptr(), kept.scale.data_ptr(), kept.q.shape[0], kept.cols, xp,
+                                          ldx, _dtype(out, "out"), _raw_stream())
+    if status:
+        _check(status, "flp_checkpoint_unpack")
+    return out
+
+
+def checkpoint_weight_grad(dY, kept: Checkpoint8, *, dW=None, dw_dtype=torch.float32, accumulate: bool = False,
+                           workspace=None, stream=None):
+    """dW [N, K] = dY^T x of a linear layer whose input x [M, K] was kept as a
+    checkpoint; dY bf16 [M, N].  With `accumulate` it is added to dW (fp32)."""
+    if stream is not None:
+        return _on_stream(stream, checkpoint_weight_grad, dY, kept, dW=dW, dw_dtype=dw_dtype, accumulate=accumulate,
+                          workspace=workspace)
+    _check_checkpoint(kept, "checkpoint")
+    yp, ldy = _rows(dY, "dY", dtype=torch.bfloat16)
+    M, N = dY.shape
+    K = kept.cols
+    if kept.q.shape[0] != M:
+        raise ValueError(f"dY has {M} rows, the checkpoint {kept.q.shape[0]}")
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dW to add to")
+        dW = torch.empty(N, K, dtype=dw_dtype, device=dY.device)
+    _need(dW, (torch.bfloat16, torch.float32), (N, K), "dW")
+    code = _DTYPE[dW.dtype]
+    lib = load()
+    ws, ws_bytes, _keep = _scratch(workspace, lib.flp_checkpoint_weight_grad_workspace,
+                                   "flp_checkpoint_weight_grad_workspace", yp, ldy, M, N, K, code)
+    status = lib.flp_checkpoint_weight_grad(yp, ldy, kept.q.data_ptr(), kept.scale.data_ptr(), M, N, K, dW.data_ptr(),
+                                            code, int(accumulate), ws, ws_bytes, _raw_stream())
+    if status:
+        _check(status, "flp_checkpoint_weight_grad")
+    return dW
+
+
+def balance_loss(logits, top_k: int, *, experts=None, mask=None, coef: float = 1.0, grad: bool = True, workspace=None,
+                 stream=None):
+    """Balance loss of router logits [T, E]: (loss [1], its gradient by the
+    logits or None, counts int64 [E]).  mask: bool [T], the tokens that count;
+    experts: int64 [T, top_k], the router's own choice (default: the top_k
+    largest logits, ties to the lowest index)."""
+    if stream is not None:
+        return _on_stream(stream, balance_loss, logits, top_k, experts=experts, mask=mask, coef=coef, grad=grad,
+                          workspace=workspace)
+    zp, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    code = _dtype(logits, "logits")
+    dev = logits.device
+    _need_opt(mask, torch.bool, (T,), "mask")
+    _need_opt(experts, torch.int64, (T, top_k), "experts")
+    loss_out = torch.empty(1, dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int64, device=dev)
+    g = torch.empty(T, E, dtype=logits.dtype, device=dev) if grad else None
+    lib = load()
+    ws, ws_bytes, _keep = _scratch(workspace, lib.flp_balance_loss_workspace, "flp_balance_loss_workspace", T, E)
+    status = lib.flp_balance_loss(zp, ld, code, None if mask is None else mask.data_ptr(),
+                                  None if experts is None else experts.data_ptr(), T, E, top_k, coef,
+                                  loss_out.data_ptr(), None if g is None else g.data_ptr(), counts.data_ptr(), ws,
+                                  ws_bytes, _raw_stream())
+    if status:
+        _check(status, "flp_balance_loss")
+    return loss_out, g, counts
 
 
 def get_error(workspace, stream=None) -> int:

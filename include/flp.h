@@ -408,6 +408,108 @@ flp_status flp_selftest_dependency_timeout(void* workspace, size_t workspace_byt
 flp_status flp_selftest_dz_wait_timeout(void* workspace, size_t workspace_bytes, int stall_after,
                                         int64_t wait_limit_ns, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Training-step operators beside the head: the norm that makes its hidden
+ * states, 8-bit checkpoints of activations and their use in the backward
+ * pass, and the balance loss of a mixture-of-experts router.  They follow the
+ * conventions above (asynchronous on `stream`, caller-owned memory,
+ * deterministic, argument errors returned before any launch) except that rows
+ * may have a pitch (ld*, in elements, at least the width) and any width and
+ * alignment: 16-byte vectors are used where base, pitch and width allow, else
+ * single elements.
+ */
+
+/*
+ * Layer norm over the last dimension of X [M, H] (bf16 or fp32, dtype):
+ *   mean = sum_j x_j / H, rstd = (sum_j (x_j - mean)^2 / H + eps)^(-1/2),
+ *   y_j  = (x_j - mean) rstd weight_j + bias_j          (fp32, rounded once)
+ * Y has X's type.  weight and bias ([H], param_dtype) may be NULL (1 and 0),
+ * mean and rstd (fp32 [M]) may be NULL (not written).  With q and scale
+ * non-NULL the call also writes the 8-bit checkpoint of X (flp_checkpoint_pack)
+ * from the same read.  Y may be X itself.  H <= 16384, else
+ * FLP_ERR_UNSUPPORTED.
+ */
+flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, const void* weight, const void* bias,
+                          int param_dtype, int64_t M, int64_t H, float eps, void* Y, int64_t ldy,
+                          float* mean, float* rstd, void* q, void* scale, void* stream);
+
+/* Workspace bytes of flp_layer_norm_backward on the current device. */
+flp_status flp_layer_norm_workspace(int64_t M, int64_t H, size_t* bytes);
+
+/*
+ * Layer norm backward, with xh = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - sum(g) / H - xh sum(g xh) / H)    (the type of dY)
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy   (fp32 [H])
+ * The activations come as X (the type of dY) or as their checkpoint q, scale
+ * (exactly one of the two); mean and rstd are the forward's.  dweight and
+ * dbias may be NULL.  M == 0 writes zeros to them.  dX may be dY itself.
+ */
+flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* q,
+                                   const void* scale, int dtype, const void* weight, int param_dtype,
+                                   const float* mean, const float* rstd, int64_t M, int64_t H, void* dX,
+                                   int64_t lddx, float* dweight, float* dbias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit checkpoint of X [M, H].  Blocks are 32 consecutive columns of a row
+ * (the last block of a row may be short).  With a the block's largest |x| and
+ * E = floor(log2 a), its step is 2^max(E - 6, -126) and each element is kept as
+ *   q = clamp(rint(x / step), -127, 127),        read back as q * step.
+ *   q     : int8  [M, Hp], Hp = H rounded up to a multiple of 32, 16-byte
+ *           aligned, zero in the columns past H
+ *   scale : uint8 [M, Hp / 32], log2(step) + 127 (1..249)
+ * The error is at most half a step (one step for fp32 values within half a
+ * step of 2^(E+1), which are clamped).  A block with a NaN or an infinity gets
+ * the byte 255 and reads back as NaN throughout, so that an overflow is not
+ * lost.  Read back as bf16 or fp32 the values are exact.
+ */
+flp_status flp_checkpoint_pack(const void* X, int64_t ldx, int dtype, int64_t M, int64_t H, void* q,
+                               void* scale, void* stream);
+flp_status flp_checkpoint_unpack(const void* q, const void* scale, int64_t M, int64_t H, void* X,
+                                 int64_t ldx, int dtype, void* stream);
+
+/*
+ * Weight gradient of a linear layer y = x W^T whose input x [M, K] was kept as
+ * a checkpoint:  dW [N, K] (+)= dY^T x^,  dY bf16 [M, N], x^ the checkpoint's
+ * values (exact in bf16), fp32 accumulation on the tensor cores.  dW is fp32
+ * (added to when accumulate_dW != 0) or bf16 (overwritten; accumulating into
+ * it is FLP_ERR_UNSUPPORTED), contiguous, 16-byte aligned.  M == 0 writes
+ * zeros (or adds nothing).  The workspace's first word is the error word of
+ * flp_get_error (FLP_ERR_TIMEOUT).  The workspace query takes dY for its
+ * alignment only.
+ */
+flp_status flp_checkpoint_weight_grad_workspace(const void* dY, int64_t lddy, int64_t M, int64_t N,
+                                                int64_t K, int dW_dtype, size_t* bytes);
+flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, const void* q, const void* scale,
+                                      int64_t M, int64_t N, int64_t K, void* dW, int dW_dtype,
+                                      int accumulate_dW, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Balance loss of a mixture-of-experts router over T tokens and E experts
+ * (1 <= E <= 1024), the per-expert counts and the gradient by the logits:
+ *   live row : mask[t] != 0 (mask NULL: every row) and some logit above -inf;
+ *              N live rows, p_t = softmax(logits_t) on them
+ *   chosen   : the top_k largest logits of a live row (equal logits: the lowest
+ *              index first; -inf is never chosen, a row that holds a NaN or
+ *              +inf chooses none), or experts[t, 0..top_k) when experts is
+ *              non-NULL (values outside [0, E) are dropped slots)
+ *   c_e      = times expert e is chosen, C = sum_e c_e
+ *   loss     = coef E sum_e (c_e / C) (sum_t p_te / N)   (coef when the load is
+ *              even; 0 when N or C is 0)
+ *   grad_te  = coef E / (N C) p_te (c_e - sum_f c_f p_tf), 0 on other rows
+ * The counts are constants of the gradient.  logits: bf16 or fp32 [T, E] at
+ * pitch ld; mask: bytes [T]; experts: int64 [T, top_k]; loss: one fp32; grad:
+ * the logits' type, contiguous [T, E], or NULL; counts: int64 [E].  A NaN or
+ * +inf in a live row makes the loss and that row's gradient NaN; what masked
+ * rows hold is not looked at.
+ */
+flp_status flp_balance_loss_workspace(int64_t T, int64_t E, size_t* bytes);
+flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype, const uint8_t* mask,
+                            const int64_t* experts, int64_t T, int64_t E, int64_t top_k, float coef,
+                            float* loss, void* grad, int64_t* counts, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* flp_status_string(flp_status status);
 
