@@ -246,6 +246,276 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) flp_norm_bwd_kernel(con
     }
 }
 
+// ---------------------------------------------------------------- streaming rows
+//
+// Rows of 16-byte vectors.  A group of threads (a warp for short rows, else the
+// block) takes rows group by group through the matrix and holds each in
+// registers, NV vectors a thread; S rows ahead are on their way through shared
+// memory.  The parameters stay in registers from the first row to the last.
+// Arithmetic runs on packed pairs, which halves the instructions that bound
+// these kernels once enough bytes are in flight.
+
+template <typename T, int NV, int S, bool CK, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 512) flp_norm_fwd_stream_kernel(const NormFwdParams p) {
+    constexpr int P = Pairs<T>::N, V = 2 * P;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][32];
+    const int group = WARP ? 32 : blockDim.x;
+    const int groups = WARP ? blockDim.x / 32 : 1;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const long long first = static_cast<long long>(blockIdx.x) * groups + (WARP ? threadIdx.x >> 5 : 0);
+    const long long step = static_cast<long long>(gridDim.x) * groups;
+    const uint32_t slot = smem_addr(ring) + threadIdx.x * 16;
+    const uint32_t pitch = blockDim.x * 16;  // from one vector of this thread to its next
+
+    auto fetch = [&](long long row, int stage) {
+        if (row < p.M) {
+            const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (t + k * group) * V;
+                if (col < p.H) cp_async<16>(slot + (stage * NV + k) * pitch, x + col);
+            }
+        }
+        cp_async_commit();
+    };
+    {
+        long long row = first;
+#pragma unroll
+        for (int s = 0; s < S; ++s, row += step) fetch(row, s);
+    }
+    uint64_t w[NV][P], b[NV][P];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int col = (t + k * group) * V;
+        param_pairs<V>(p.w, p.param_f32, col, col < p.H, 1.f, w[k]);
+        param_pairs<V>(p.b, p.param_f32, col, col < p.H, 0.f, b[k]);
+    }
+    int stage = 0;
+    for (long long row = first; row < p.M; row += step) {
+        cp_async_wait<S - 1>();
+        uint4 raw[NV];
+        uint64_t v[NV][P];
+        uint64_t acc = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            raw[k] = (t + k * group) * V < p.H ? ld_shared_16(slot + (stage * NV + k) * pitch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                v[k][i] = Pairs<T>::get(raw[k], i);
+                acc = f2_add(acc, v[k][i]);
+            }
+        }
+        float s[1] = {f2_sum(acc)};
+        group_sum_n<WARP>(s, red[0]);
+        // the sum has taken every value of this stage: its slots are free
+        fetch(row + S * step, stage);
+        if (++stage == S) stage = 0;
+        const float mean = s[0] * p.inv_h;
+        const uint64_t minus = f2_splat(-mean);
+        acc = 0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int col = (t + k * group) * V;
+            if constexpr (CK) {
+                uint32_t q[P / 2];
+                const uint32_t byte = ck_quantise_pairs<T>(raw[k], v[k], q);
+                if (col < p.Hp) {
+                    ck_store_words(p.q + row * p.Hp + col, q);
+                    if ((col % CK_BLOCK) == 0)
+                        p.scale[row * (p.Hp / CK_BLOCK) + col / CK_BLOCK] = static_cast<uint8_t>(byte);
+                }
+            }
+            if (col < p.H) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    v[k][i] = f2_add(v[k][i], minus);
+                    acc = f2_fma(v[k][i], v[k][i], acc);
+                }
+            }
+        }
+        float c[1] = {f2_sum(acc)};
+        group_sum_n<WARP>(c, red[1]);
+        const float rstd = rsqrtf(fmaf(c[0], p.inv_h, p.eps));
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        const uint64_t r2 = f2_splat(rstd);
+        T* y = static_cast<T*>(p.y) + row * p.ldy;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int col = (t + k * group) * V;
+            if (col < p.H) {
+                uint64_t o[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i) o[i] = f2_fma(f2_mul(v[k][i], r2), w[k][i], b[k][i]);
+                Pairs<T>::store(y + col, o);
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
+template <typename T, int NV, int S, bool CK, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : 512) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
+    constexpr int P = Pairs<T>::N, V = 2 * P;
+    constexpr int XB = CK ? V : 16;  // bytes of a vector of x in the ring
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][2][32];
+    const int group = WARP ? 32 : blockDim.x;
+    const int groups = WARP ? blockDim.x / 32 : 1;
+    const int sub = WARP ? threadIdx.x >> 5 : 0;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const long long first = static_cast<long long>(blockIdx.x) * groups + sub;
+    const long long step = static_cast<long long>(gridDim.x) * groups;
+    const uint32_t slot_y = smem_addr(ring) + threadIdx.x * 16;
+    const uint32_t pitch_y = blockDim.x * 16;
+    const uint32_t slot_x = smem_addr(ring) + S * NV * pitch_y + threadIdx.x * XB;
+    const uint32_t pitch_x = blockDim.x * XB;
+
+    auto fetch = [&](long long row, int stage) {
+        if (row < p.M) {
+            const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int col = (t + k * group) * V;
+                if (col < p.H) {
+                    cp_async<16>(slot_y + (stage * NV + k) * pitch_y, dy + col);
+                    if constexpr (CK)
+                        cp_async<XB>(slot_x + (stage * NV + k) * pitch_x, p.q + row * p.Hp + col);
+                    else
+                        cp_async<16>(slot_x + (stage * NV + k) * pitch_x, static_cast<const T*>(p.x) + row * p.ldx + col);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    // what a row needs beside its vectors, one row ahead in registers
+    float mean = 0.f, rstd = 0.f;
+    uint32_t byte[NV] = {};
+    auto fetch_few = [&](long long row) {
+        if (row < p.M) {
+            mean = __ldg(p.mean + row);
+            rstd = __ldg(p.rstd + row);
+            if constexpr (CK) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const int col = (t + k * group) * V;
+                    if (col < p.H) byte[k] = __ldg(p.scale + row * (p.Hp / CK_BLOCK) + col / CK_BLOCK);
+                }
+            }
+        }
+    };
+    {
+        long long row = first;
+#pragma unroll
+        for (int s = 0; s < S; ++s, row += step) fetch(row, s);
+    }
+    fetch_few(first);
+    uint64_t w[NV][P], dw[NV][P] = {}, db[NV][P] = {};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int col = (t + k * group) * V;
+        param_pairs<V>(p.w, p.param_f32, col, col < p.H, 1.f, w[k]);
+    }
+    int stage = 0, buf = 0;
+    for (long long row = first; row < p.M; row += step) {
+        cp_async_wait<S - 1>();
+        uint4 ry[NV];
+        uint64_t xh[NV][P];
+        uint64_t s0 = 0, s1 = 0;
+        const uint64_t minus = f2_splat(-mean), r2 = f2_splat(rstd);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const bool in = (t + k * group) * V < p.H;
+            ry[k] = in ? ld_shared_16(slot_y + (stage * NV + k) * pitch_y) : make_uint4(0, 0, 0, 0);
+            if (in) {
+                if constexpr (CK) {
+                    uint32_t q[V / 4];
+                    if constexpr (V == 8) {
+                        const uint2 u = ld_shared_8(slot_x + (stage * NV + k) * pitch_x);
+                        q[0] = u.x, q[1] = u.y;
+                    } else {
+                        q[0] = ld_shared_4(slot_x + (stage * NV + k) * pitch_x);
+                    }
+                    ck_pairs<V>(q, ck_step(byte[k]), xh[k]);
+                } else {
+                    const uint4 rx = ld_shared_16(slot_x + (stage * NV + k) * pitch_x);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) xh[k][i] = Pairs<T>::get(rx, i);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) xh[k][i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const uint64_t d = Pairs<T>::get(ry[k], i);
+                xh[k][i] = f2_mul(f2_add(xh[k][i], minus), r2);
+                dw[k][i] = f2_fma(d, xh[k][i], dw[k][i]);
+                db[k][i] = f2_add(db[k][i], d);
+                const uint64_t g = f2_mul(d, w[k][i]);
+                s0 = f2_add(s0, g);
+                s1 = f2_fma(g, xh[k][i], s1);
+            }
+        }
+        const float r = rstd;
+        fetch_few(row + step);
+        float s[2] = {f2_sum(s0), f2_sum(s1)};
+        group_sum_n<WARP>(s, &red[buf][0][0]);
+        buf ^= 1;
+        // the sums have taken every value of this stage: its slots are free
+        fetch(row + S * step, stage);
+        if (++stage == S) stage = 0;
+        const uint64_t m1 = f2_splat(-s[0] * p.inv_h), m2 = f2_splat(-s[1] * p.inv_h), rr = f2_splat(r);
+        T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int col = (t + k * group) * V;
+            if (col < p.H) {
+                uint64_t o[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    o[i] = f2_mul(rr, f2_fma(xh[k][i], m2, f2_fma(Pairs<T>::get(ry[k], i), w[k][i], m1)));
+                Pairs<T>::store(dx + col, o);
+            }
+        }
+    }
+    cp_async_wait<0>();
+    griddep_launch_dependents();
+    // this block's sums; with a row per warp, the warps join first (the ring is free)
+    float* join = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float* out = p.part + (static_cast<long long>(blockIdx.x) * 2 + which) * p.H;
+        if constexpr (WARP) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int col = (t + k * group) * V;
+            if (col < p.H) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float2 a;
+                    f2_unpack(which ? db[k][i] : dw[k][i], a.x, a.y);
+                    if constexpr (WARP)
+                        *reinterpret_cast<float2*>(join + sub * (NV * 32 * V) + col + 2 * i) = a;
+                    else
+                        *reinterpret_cast<float2*>(out + col + 2 * i) = a;
+                }
+            }
+        }
+        if constexpr (WARP) {
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+                float a = 0.f;
+                for (int u = 0; u < groups; ++u) a += join[u * (NV * 32 * V) + c];
+                out[c] = a;
+            }
+        }
+    }
+}
+
 struct NormJoinParams {
     const float* part;  // [P][2][H]
     int P, H;

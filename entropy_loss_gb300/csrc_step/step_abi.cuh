@@ -2,6 +2,9 @@
 // include/flp.h: argument checks, kernel choice by size and alignment, and
 // launches.
 #pragma once
+#include <map>
+#include <tuple>
+
 #include "balance.cuh"
 #include "checkpoint.cuh"
 #include "norm.cuh"
@@ -50,33 +53,61 @@ inline bool rows16(const void* p, int64_t ld, int dtype) { return aligned16(p) &
 
 // ------------------------------------------------------------------ layer norm
 
-// Calls f(threads per row, vectors per thread) as compile-time constants for
-// rows of `vecs` vectors.  Up to 1024 (16-byte vectors) or 256 elements a warp
-// takes a row, so the row sums need no block barrier; above, as many threads
-// as leave 2 to 4 vectors each, which keeps the row in registers and enough
-// loads in flight.
-template <int V, typename F>
-flp_status norm_shape(int64_t vecs, F&& f) {
-#define FLP_SHAPE(TPR, NV) \
-    if (vecs <= (TPR) * (NV)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{});
-    if constexpr (V > 1) {
-        FLP_SHAPE(32, 1)
-        FLP_SHAPE(32, 2)
-        FLP_SHAPE(32, 4)
-        FLP_SHAPE(128, 2)
-        FLP_SHAPE(256, 2)
-        FLP_SHAPE(256, 3)
-        FLP_SHAPE(512, 2)
-        FLP_SHAPE(512, 4)
-        FLP_SHAPE(1024, 4)
-    } else {
-        FLP_SHAPE(32, 8)
-        FLP_SHAPE(128, 8)
-        FLP_SHAPE(256, 16)
-        FLP_SHAPE(1024, 16)
+// Resident blocks per SM of a kernel with dynamic shared memory (its limit
+// raised where needed), asked once per kernel, block size and device.
+flp_status resident_blocks(const void* kernel, int threads, size_t smem, int* per_sm) {
+    static std::map<std::tuple<const void*, int, int>, int> known;
+    int dev = 0;
+    FLP_CUDA(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lk(g_mu);
+    const auto key = std::make_tuple(kernel, threads, dev);
+    const auto at = known.find(key);
+    if (at != known.end()) {
+        *per_sm = at->second;
+        return FLP_OK;
     }
+    FLP_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+    int n = 0;
+    FLP_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
+    if (n < 1) return fail(FLP_ERR_UNSUPPORTED, "a block of the kernel does not fit an SM");
+    known[key] = n;
+    *per_sm = n;
+    return FLP_OK;
+}
+
+// Single-element access (rows that are not 16-byte aligned or not whole
+// vectors): calls f(threads per row, elements per thread).
+template <typename F>
+flp_status norm_shape(int64_t cols, F&& f) {
+#define FLP_SHAPE(TPR, NV) \
+    if (cols <= (TPR) * (NV)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{});
+    FLP_SHAPE(32, 8)
+    FLP_SHAPE(128, 8)
+    FLP_SHAPE(256, 16)
+    FLP_SHAPE(1024, 16)
 #undef FLP_SHAPE
     return fail(FLP_ERR_UNSUPPORTED, "layer norm rows hold at most 16384 elements");
+}
+
+// Streaming rows: calls f(vectors per thread, stages, row per warp, threads of
+// a block).  16 elements a thread keep a row, its parameters and the column
+// sums in registers; rows of up to 512 elements go to one warp, which needs no
+// block barrier; rows above 8192 take more elements a thread.  The stages put
+// 64 KiB or so per SM in flight in every shape.
+template <typename T, typename F>
+flp_status norm_stream_shape(int64_t cols, F&& f) {
+    constexpr int V = wide_v<T>(), N2 = 16 / V;  // N2 vectors of V = 16 elements
+    const int64_t vecs = cdiv(cols, V);
+    const std::integral_constant<int, 4> s4{};
+    const std::integral_constant<int, 2> s2{};
+    if (vecs <= 32) return f(std::integral_constant<int, 1>{}, s4, std::true_type{}, 256);
+    if (vecs <= 64) return f(std::integral_constant<int, 2>{}, s4, std::true_type{}, 256);
+    if constexpr (V == 4)
+        if (vecs <= 128) return f(std::integral_constant<int, 4>{}, s2, std::true_type{}, 256);
+    if (cols <= 8192)
+        return f(std::integral_constant<int, N2>{}, std::integral_constant<int, V == 8 ? 4 : 2>{}, std::false_type{},
+                 static_cast<int>(cdiv(vecs, 32 * N2) * 32));
+    return f(std::integral_constant<int, 2 * N2>{}, s2, std::false_type{}, static_cast<int>(cdiv(vecs, 64 * N2) * 32));
 }
 
 flp_status norm_checks(int64_t M, int64_t H, int dtype, int param_dtype, const void* weight, const void* bias) {
@@ -192,10 +223,10 @@ CkParams ck_params(void* x, int64_t ldx, const void* q, const void* scale, int64
     p.ldx = ldx;
     p.q = static_cast<uint8_t*>(const_cast<void*>(q));
     p.scale = static_cast<uint8_t*>(const_cast<void*>(scale));
-    p.M = M;
     p.H = static_cast<int>(H);
     p.Hp = static_cast<int>(ck_cols(H));
     p.per_row = static_cast<unsigned>(p.Hp / V);
+    p.inverse = ~0ull / p.per_row + 1;
     p.total = M * p.per_row;
     return p;
 }
@@ -205,7 +236,8 @@ flp_status ck_launch(bool pack, void* x, int64_t ldx, const void* q, const void*
                      cudaStream_t s) {
     const CkParams p = ck_params<V, T>(x, ldx, q, scale, M, H);
     const int64_t grid = cdiv(p.total, CK_THREADS * CK_PER_THREAD);
-    if (grid > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
+    // the row of a vector comes exactly from one multiplication while vectors x vectors per row < 2^64
+    if (grid > INT32_MAX || static_cast<double>(p.total + (1 << 20)) * p.per_row > 1.8e19) return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
     return pack ? launch_step(flp_ck_pack_kernel<T, V>, grid, CK_THREADS, 0, s, "flp_ck_pack_kernel launch", false, p)
                 : launch_step(flp_ck_unpack_kernel<T, V>, grid, CK_THREADS, 0, s, "flp_ck_unpack_kernel launch", false, p);
 }
@@ -314,27 +346,33 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
     p.scale = static_cast<uint8_t*>(scale);
     p.Hp = static_cast<int>(ck_cols(H));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto run = [&](auto t, auto v, auto ck) -> flp_status {
+    const bool wide = rows16(X, ldx, dtype) && rows16(Y, ldy, dtype) && aligned16(weight) && aligned16(bias) &&
+                      (H * elem(dtype)) % 16 == 0;
+    auto run = [&](auto t, auto ck) -> flp_status {
         using T = decltype(t);
-        constexpr int V = decltype(v)::value;
         constexpr bool CK = decltype(ck)::value;
-        return norm_shape<V>(cdiv(CK ? p.Hp : p.H, V), [&](auto tpr, auto nv) {
+        const int64_t cols = CK ? p.Hp : p.H;
+        if (wide)
+            return norm_stream_shape<T>(cols, [&](auto nv, auto stages, auto warp, int threads) -> flp_status {
+                constexpr int NV = decltype(nv)::value, S = decltype(stages)::value;
+                constexpr bool WARP = decltype(warp)::value;
+                auto* kernel = flp_norm_fwd_stream_kernel<T, NV, S, CK, WARP>;
+                const size_t smem = static_cast<size_t>(S) * NV * threads * 16;
+                int per_sm = 0;
+                const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+                if (r != FLP_OK) return r;
+                const int64_t rows = WARP ? threads / 32 : 1;
+                return launch_step(kernel, std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count),
+                                   threads, smem, s, "flp_norm_fwd_stream_kernel launch", false, p);
+            });
+        return norm_shape(cols, [&](auto tpr, auto nv) {
             constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
             constexpr int RPB = norm_rows_per_block<TPR>();
-            return launch_step(flp_norm_fwd_kernel<T, V, TPR, NV, CK>, cdiv(M, RPB), TPR * RPB, 0, s,
+            return launch_step(flp_norm_fwd_kernel<T, 1, TPR, NV, CK>, cdiv(M, RPB), TPR * RPB, 0, s,
                                "flp_norm_fwd_kernel launch", false, p);
         });
     };
-    auto typed = [&](auto t) -> flp_status {
-        using T = decltype(t);
-        constexpr int V = wide_v<T>();
-        const bool wide = H % V == 0 && rows16(X, ldx, dtype) && rows16(Y, ldy, dtype) && aligned16(weight) && aligned16(bias);
-        if (wide)
-            return q ? run(t, std::integral_constant<int, V>{}, std::true_type{})
-                     : run(t, std::integral_constant<int, V>{}, std::false_type{});
-        return q ? run(t, std::integral_constant<int, 1>{}, std::true_type{})
-                 : run(t, std::integral_constant<int, 1>{}, std::false_type{});
-    };
+    auto typed = [&](auto t) { return q ? run(t, std::true_type{}) : run(t, std::false_type{}); };
     return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
 }
 
@@ -392,32 +430,45 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
         p.dx = dX;
         p.lddx = lddx;
         p.part = static_cast<float*>(workspace);
-        auto run = [&](auto t, auto v, auto ck) -> flp_status {
+        // two stages of an fp32 row above 8192 elements, dY and X, do not fit
+        // shared memory: such rows go element by element
+        const bool wide = rows16(dY, lddy, dtype) && rows16(dX, lddx, dtype) && aligned16(weight) &&
+                          (!X || rows16(X, ldx, dtype)) && (H * elem(dtype)) % 16 == 0 &&
+                          (dtype == FLP_BF16 || H <= 8192);
+        auto fits = [&]() {
+            return workspace_bytes >= static_cast<size_t>(blocks) * 2 * H * 4
+                       ? FLP_OK
+                       : fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
+        };
+        auto run = [&](auto t, auto ck) -> flp_status {
             using T = decltype(t);
-            constexpr int V = decltype(v)::value;
             constexpr bool CK = decltype(ck)::value;
-            return norm_shape<V>(cdiv(p.H, V), [&](auto tpr, auto nv) {
+            if (wide)
+                return norm_stream_shape<T>(p.H, [&](auto nv, auto stages, auto warp, int threads) -> flp_status {
+                    constexpr int NV = decltype(nv)::value, S = decltype(stages)::value;
+                    constexpr bool WARP = decltype(warp)::value;
+                    auto* kernel = flp_norm_bwd_stream_kernel<T, NV, S, CK, WARP>;
+                    const size_t smem = static_cast<size_t>(S) * NV * threads * (16 + (CK ? wide_v<T>() : 16));
+                    int per_sm = 0;
+                    flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+                    if (r != FLP_OK) return r;
+                    blocks = norm_bwd_blocks(M, WARP ? threads / 32 : 1, d->sm_count,
+                                             std::min<int64_t>(kNormBwdBlocksPerSm, per_sm));
+                    if ((r = fits()) != FLP_OK) return r;
+                    return launch_step(kernel, blocks, threads, smem, s, "flp_norm_bwd_stream_kernel launch", false, p);
+                });
+            return norm_shape(p.H, [&](auto tpr, auto nv) -> flp_status {
                 constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
                 constexpr int RPB = norm_rows_per_block<TPR>();
                 constexpr int threads = TPR * RPB;
                 blocks = norm_bwd_blocks(M, RPB, d->sm_count, std::max(1, std::min<int>(kNormBwdBlocksPerSm, 512 / threads)));
-                if (workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
-                    return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
-                return launch_step(flp_norm_bwd_kernel<T, V, TPR, NV, CK>, blocks, threads, 0, s,
+                const flp_status r = fits();
+                if (r != FLP_OK) return r;
+                return launch_step(flp_norm_bwd_kernel<T, 1, TPR, NV, CK>, blocks, threads, 0, s,
                                    "flp_norm_bwd_kernel launch", false, p);
             });
         };
-        auto typed = [&](auto t) -> flp_status {
-            using T = decltype(t);
-            constexpr int V = wide_v<T>();
-            const bool wide = H % V == 0 && rows16(dY, lddy, dtype) && rows16(dX, lddx, dtype) && aligned16(weight) &&
-                              (!X || rows16(X, ldx, dtype));
-            if (wide)
-                return q ? run(t, std::integral_constant<int, V>{}, std::true_type{})
-                         : run(t, std::integral_constant<int, V>{}, std::false_type{});
-            return q ? run(t, std::integral_constant<int, 1>{}, std::true_type{})
-                     : run(t, std::integral_constant<int, 1>{}, std::false_type{});
-        };
+        auto typed = [&](auto t) { return q ? run(t, std::true_type{}) : run(t, std::false_type{}); };
         st = dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
         if (st != FLP_OK) return st;
     }

@@ -22,6 +22,7 @@ struct Raw<bf16, 8> {
     __device__ __forceinline__ void load(const bf16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void load_kept(const bf16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ uint4 bits() const { return u; }
     __device__ __forceinline__ void to(float (&v)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -37,6 +38,9 @@ struct Raw<float, 4> {
     __device__ __forceinline__ void load(const float* p) { u = __ldcs(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void load_kept(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ uint4 bits() const {
+        return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z), __float_as_uint(u.w));
+    }
     __device__ __forceinline__ void to(float (&v)[4]) const {
         v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
     }
@@ -106,6 +110,98 @@ __device__ __forceinline__ void load_param(const void* base, bool f32, int col, 
     }
 }
 
+// ------------------------------------------- vectors on their way through smem
+//
+// A thread copies ahead the vectors that it will itself read, each into its own
+// 16 bytes (or 8) of shared memory, so a completed cp.async group is all the
+// synchronisation there is, and the bytes in flight are not limited by registers.
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t a) {
+    uint4 u;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(a) : "memory");
+    return u;
+}
+__device__ __forceinline__ uint2 ld_shared_8(uint32_t a) {
+    uint2 u;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(a) : "memory");
+    return u;
+}
+__device__ __forceinline__ uint32_t ld_shared_4(uint32_t a) {
+    uint32_t u;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(a) : "memory");
+    return u;
+}
+
+// A 16-byte vector as packed fp32 pairs (two lanes per instruction).
+template <typename T>
+struct Pairs;
+template <>
+struct Pairs<bf16> {
+    static constexpr int N = 4;  // pairs of a vector
+    __device__ __forceinline__ static uint64_t get(const uint4& u, int i) {
+        const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+        return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ static void store(bf16* p, const uint64_t (&v)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            f2_unpack(v[i], lo, hi);
+            w[i] = pack_bf16x2(lo, hi);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Pairs<float> {
+    static constexpr int N = 2;
+    __device__ __forceinline__ static uint64_t get(const uint4& u, int i) {
+        return i == 0 ? f2_pack(__uint_as_float(u.x), __uint_as_float(u.y))
+                      : f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+    __device__ __forceinline__ static void store(float* p, const uint64_t (&v)[2]) {
+        float4 u;
+        f2_unpack(v[0], u.x, u.y);
+        f2_unpack(v[1], u.z, u.w);
+        *reinterpret_cast<float4*>(p) = u;
+    }
+};
+
+__device__ __forceinline__ uint64_t f2_splat(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
+}
+
+// V parameter values from `col` on as pairs (1 or 0 where there are none).
+template <int V>
+__device__ __forceinline__ void param_pairs(const void* base, bool f32, int col, bool in, float none, uint64_t (&v)[V / 2]) {
+    float w[V];
+    if (base && in) {
+        load_param<V>(base, f32, col, w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = none;
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = f2_pack(w[2 * i], w[2 * i + 1]);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -137,6 +233,24 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
             }
             v[n] = s;
         }
+    }
+}
+
+// The same over a warp (kWarp) or over the whole block, whose size is known at
+// run time.
+template <bool kWarp, int N>
+__device__ __forceinline__ void group_sum_n(float (&v)[N], float* red) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
+    if constexpr (!kWarp) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        if (lane == 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) red[n * 32 + warp] = v[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = warp_sum(lane < warps ? red[n * 32 + lane] : 0.f);
     }
 }
 
@@ -217,6 +331,66 @@ __device__ __forceinline__ uint32_t ck_quantise(const float (&v)[V], uint32_t (&
         for (int i = 0; i < (V > 4 ? 2 : 1); ++i) w[i] = 0;
     }
     return byte;
+}
+
+// The same for a 16-byte vector as loaded (`raw`) and as pairs.  Only a block
+// whose largest value lies within half a step of 128 steps can round to 128, so
+// the clamp runs for those blocks alone (about one in 130 of normal values).
+template <typename T>
+__device__ __forceinline__ uint32_t ck_quantise_pairs(const uint4& raw, const uint64_t (&v)[Pairs<T>::N],
+                                                      uint32_t (&w)[Pairs<T>::N / 2]) {
+    constexpr int V = 2 * Pairs<T>::N;
+    uint32_t top;
+    if constexpr (V == 8) {
+        // bf16 magnitudes compare as 16-bit integers, two per instruction
+        constexpr uint32_t mag = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(raw.x & mag, raw.y & mag), __vmaxu2(raw.z & mag, raw.w & mag));
+        top = max(m << 16, m & 0xffff0000u);
+    } else {
+        top = max(max(raw.x & 0x7fffffffu, raw.y & 0x7fffffffu), max(raw.z & 0x7fffffffu, raw.w & 0x7fffffffu));
+    }
+#pragma unroll
+    for (int o = 1; o < CK_BLOCK / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t byte = ck_byte(top);
+    const float magic = 12582912.f;
+    const uint64_t inv = f2_splat(ck_inverse(byte == CK_NAN ? 1u : byte)), add = f2_splat(magic);
+    float r[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f2_unpack(f2_fma(v[i], inv, add), r[2 * i], r[2 * i + 1]);
+    if ((top & 0x7f0000u) == 0x7f0000u) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[i] = fminf(fmaxf(r[i], magic - 127.f), magic + 127.f);
+    }
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+        w[i] = pack_bytes(__float_as_uint(r[4 * i]), __float_as_uint(r[4 * i + 1]), __float_as_uint(r[4 * i + 2]),
+                          __float_as_uint(r[4 * i + 3]));
+        if (byte == CK_NAN) w[i] = 0;
+    }
+    return byte;
+}
+
+__device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[2]) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[1]) {
+    *reinterpret_cast<uint32_t*>(q) = w[0];
+}
+
+// Values of a vector's bytes as pairs.
+template <int V>
+__device__ __forceinline__ void ck_pairs(const uint32_t* w, float step, uint64_t (&v)[V / 2]) {
+    const uint64_t off = f2_splat(-8388736.f), s = f2_splat(step);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+        const uint32_t u = w[i] ^ 0x80808080u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            v[2 * i + j] = f2_mul(f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 + 2 * j)),
+                                                 __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7541 + 2 * j))),
+                                         off),
+                                  s);
+    }
 }
 
 template <int V>

@@ -8,6 +8,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -449,62 +450,69 @@ class Checkpoint8(NamedTuple):
 
 
 def _dtype(t, name):
-    try:
-        return _DTYPE[t.dtype]
-    except KeyError:
-        raise ValueError(f"{name}: expected bf16 or fp32, got {t.dtype}") from None
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bf16 or fp32, got {t.dtype}")
+    return code
 
 
 def _rows(t, name, shape=None, dtype=None):
     """(address, row pitch) of a CUDA matrix whose rows are contiguous."""
-    if t.dim() != 2 or not t.is_cuda or (shape is not None and t.shape != shape) or (
+    size = t.shape
+    if len(size) != 2 or not t.is_cuda or (shape is not None and size != shape) or (
             dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name}: expected a CUDA matrix{'' if shape is None else f' of shape {tuple(shape)}'}"
-                         f"{'' if dtype is None else f' of {dtype}'}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                         f"{'' if dtype is None else f' of {dtype}'}, got {t.dtype} {tuple(size)} on {t.device}")
     pitch, unit = t.stride()
-    rows, cols = t.shape
+    rows, cols = size
     if (unit != 1 and cols > 1) or (pitch < cols and rows > 1):
         raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
     return t.data_ptr(), pitch if rows > 1 else cols
 
 
 def _check_checkpoint(c, name):
-    rows, padded = c.q.shape
-    if (c.q.dtype is not torch.int8 or c.scale.dtype is not torch.uint8 or not c.q.is_cuda or not c.scale.is_cuda
-            or padded != -(-c.cols // CHECKPOINT_BLOCK) * CHECKPOINT_BLOCK
-            or c.scale.shape != (rows, padded // CHECKPOINT_BLOCK)
-            or not c.q.is_contiguous() or not c.scale.is_contiguous()):
-        raise ValueError(f"{name}: not an 8-bit checkpoint: q {c.q.dtype} {tuple(c.q.shape)}, scale {c.scale.dtype} "
-                         f"{tuple(c.scale.shape)}, {c.cols} columns")
+    q, scale = c.q, c.scale
+    rows, padded = q.shape
+    blocks = -(-c.cols // CHECKPOINT_BLOCK)
+    if (q.dtype is not torch.int8 or scale.dtype is not torch.uint8 or not q.is_cuda or not scale.is_cuda
+            or padded != blocks * CHECKPOINT_BLOCK or scale.shape != (rows, blocks)
+            or not q.is_contiguous() or not scale.is_contiguous()):
+        raise ValueError(f"{name}: not an 8-bit checkpoint: q {q.dtype} {tuple(q.shape)}, scale {scale.dtype} "
+                         f"{tuple(scale.shape)}, {c.cols} columns")
 
 
 def _new_checkpoint(rows, cols, dtype, device):
     blocks = -(-cols // CHECKPOINT_BLOCK)
-    return Checkpoint8(torch.empty(rows, blocks * CHECKPOINT_BLOCK, dtype=torch.int8, device=device),
-                       torch.empty(rows, blocks, dtype=torch.uint8, device=device), cols, dtype)
+    return Checkpoint8(torch.empty((rows, blocks * CHECKPOINT_BLOCK), dtype=torch.int8, device=device),
+                       torch.empty((rows, blocks), dtype=torch.uint8, device=device), cols, dtype)
 
 
 def _norm_param(t, cols, dtype, name):
-    """Address of a norm parameter: [cols], the activations' type or fp32."""
+    """(address, dtype code) of a norm parameter: [cols], the activations' type or fp32."""
     if t is None:
-        return None
-    if t.dtype not in (dtype, torch.float32) or t.shape != (cols,) or not t.is_cuda or not t.is_contiguous():
+        return None, None
+    d = t.dtype
+    if (d is not dtype and d is not torch.float32) or t.shape != (cols,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous CUDA {dtype} or fp32 of shape ({cols},), "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    return t.data_ptr(), _DTYPE[d]
 
 
-def _query(fn, what, *args):
+# Workspace sizes by device and problem: a pure function of both, remembered
+# because asking costs as much as a small launch.
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(fn: str, device: int, *args) -> int:
     n = ctypes.c_size_t(0)
-    _check(fn(*args, ctypes.byref(n)), what)
-    return n.value
+    _check(getattr(load(), fn)(*args, ctypes.byref(n)), fn)
+    return max(16, n.value)
 
 
-def _scratch(workspace, fn, what, *args):
-    """(address, bytes, owner) of the caller's workspace, or of a new one."""
+def _scratch(workspace, device, need):
+    """(address, bytes, owner) of the caller's workspace, or of a new one of `need` bytes."""
     if workspace is None:
-        workspace = torch.empty(max(16, _query(fn, what, *args)), dtype=torch.uint8, device="cuda")
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace.data_ptr(), need, workspace
+    if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA tensor")
     return workspace.data_ptr(), _nbytes(workspace), workspace
 
@@ -515,8 +523,9 @@ def _on_stream(stream, fn, *args, **kw):
         return fn(*args, **kw)
 
 
-def _raw_stream():
-    return torch.cuda.current_stream().cuda_stream
+# The current stream's handle, without the Stream object around it (which costs
+# as much as a small launch).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, checkpoint: bool = False, out=None, stream=None):
@@ -526,22 +535,27 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, checkpoint: bool
     if stream is not None:
         return _on_stream(stream, layer_norm, x, weight, bias, eps=eps, checkpoint=checkpoint, out=out)
     xp, ldx = _rows(x, "x")
-    M, H = x.shape
+    M, H = shape = x.shape
     dt, dev = x.dtype, x.device
     code = _dtype(x, "x")
-    wp, bp = _norm_param(weight, H, dt, "weight"), _norm_param(bias, H, dt, "bias")
-    param = weight if weight is not None else bias
-    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
+    wp, wt = _norm_param(weight, H, dt, "weight")
+    bp, bt = _norm_param(bias, H, dt, "bias")
+    if wt != bt and wt is not None and bt is not None:
         raise ValueError(f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
     if out is None:
-        out = torch.empty(M, H, dtype=dt, device=dev)
-    yp, ldy = _rows(out, "out", x.shape, dt)
-    mean, rstd = torch.empty(2, M, dtype=torch.float32, device=dev).unbind(0)
-    kept = _new_checkpoint(M, H, dt, dev) if checkpoint else None
-    status = load().flp_layer_norm(xp, ldx, code, wp, bp, code if param is None else _DTYPE[param.dtype], M, H, eps,
-                                   yp, ldy, mean.data_ptr(), rstd.data_ptr(),
-                                   kept.q.data_ptr() if checkpoint else None,
-                                   kept.scale.data_ptr() if checkpoint else None, _raw_stream())
+        out = torch.empty(shape, dtype=dt, device=dev)
+        yp, ldy = out.data_ptr(), H
+    else:
+        yp, ldy = _rows(out, "out", shape, dt)
+    mean = torch.empty(M, dtype=torch.float32, device=dev)
+    rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    qp = sp = None
+    if checkpoint:
+        kept = _new_checkpoint(M, H, dt, dev)
+        qp, sp = kept.q.data_ptr(), kept.scale.data_ptr()
+    param = wt if wt is not None else bt if bt is not None else code
+    status = load().flp_layer_norm(xp, ldx, code, wp, bp, param, M, H, eps, yp, ldy, mean.data_ptr(),
+                                   rstd.data_ptr(), qp, sp, _raw_stream(dev.index))
     if status:
         _check(status, "flp_layer_norm")
     return (out, mean, rstd, kept) if checkpoint else (out, mean, rstd)
@@ -554,30 +568,35 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, workspace=None, s
     if stream is not None:
         return _on_stream(stream, layer_norm_backward, dy, x, weight, mean, rstd, dx=dx, workspace=workspace)
     dyp, lddy = _rows(dy, "dy")
-    M, H = dy.shape
+    M, H = shape = dy.shape
     dt, dev = dy.dtype, dy.device
     code = _dtype(dy, "dy")
-    xp = ldx = qp = sp = None
+    xp = qp = sp = None
+    ldx = 0
     if isinstance(x, Checkpoint8):
         _check_checkpoint(x, "x")
-        if x.shape != (M, H):
+        if x.cols != H or x.q.shape[0] != M:
             raise ValueError(f"x: checkpoint of shape {x.shape}, expected {(M, H)}")
-        qp, sp, ldx = x.q.data_ptr(), x.scale.data_ptr(), 0
+        qp, sp = x.q.data_ptr(), x.scale.data_ptr()
     else:
-        xp, ldx = _rows(x, "x", dy.shape, dt)
-    wp = _norm_param(weight, H, dt, "weight")
-    _need(mean, torch.float32, (M,), "mean")
-    _need(rstd, torch.float32, (M,), "rstd")
+        xp, ldx = _rows(x, "x", shape, dt)
+    wp, wt = _norm_param(weight, H, dt, "weight")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype is not torch.float32 or t.shape != (M,) or not t.is_cuda or not t.is_contiguous():
+            _need(t, torch.float32, (M,), name)
     if dx is None:
-        dx = torch.empty(M, H, dtype=dt, device=dev)
-    dxp, lddx = _rows(dx, "dx", dy.shape, dt)
-    dweight, dbias = torch.empty(2, H, dtype=torch.float32, device=dev).unbind(0)
-    lib = load()
-    ws, ws_bytes, _keep = _scratch(workspace, lib.flp_layer_norm_workspace, "flp_layer_norm_workspace", M, H)
-    status = lib.flp_layer_norm_backward(dyp, lddy, xp, ldx, qp, sp, code, wp,
-                                         code if weight is None else _DTYPE[weight.dtype], mean.data_ptr(),
-                                         rstd.data_ptr(), M, H, dxp, lddx, dweight.data_ptr(), dbias.data_ptr(),
-                                         ws, ws_bytes, _raw_stream())
+        dx = torch.empty(shape, dtype=dt, device=dev)
+        dxp, lddx = dx.data_ptr(), H
+    else:
+        dxp, lddx = _rows(dx, "dx", shape, dt)
+    dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    dbias = torch.empty(H, dtype=torch.float32, device=dev)
+    device = dev.index
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+                                   _workspace_bytes("flp_layer_norm_workspace", device, M, H))
+    status = load().flp_layer_norm_backward(dyp, lddy, xp, ldx, qp, sp, code, wp, code if wt is None else wt,
+                                            mean.data_ptr(), rstd.data_ptr(), M, H, dxp, lddx, dweight.data_ptr(),
+                                            dbias.data_ptr(), ws, ws_bytes, _raw_stream(device))
     if status:
         _check(status, "flp_layer_norm_backward")
     return dx, dweight, dbias
@@ -588,10 +607,11 @@ def checkpoint_pack(x, *, stream=None) -> Checkpoint8:
     if stream is not None:
         return _on_stream(stream, checkpoint_pack, x)
     xp, ldx = _rows(x, "x")
-    code = _dtype(x, "x")
-    kept = _new_checkpoint(x.shape[0], x.shape[1], x.dtype, x.device)
-    status = load().flp_checkpoint_pack(xp, ldx, code, x.shape[0], x.shape[1], kept.q.data_ptr(),
-                                        kept.scale.data_ptr(), _raw_stream())
+    M, H = x.shape
+    code, dev = _dtype(x, "x"), x.device
+    kept = _new_checkpoint(M, H, x.dtype, dev)
+    status = load().flp_checkpoint_pack(xp, ldx, code, M, H, kept.q.data_ptr(), kept.scale.data_ptr(),
+                                        _raw_stream(dev.index))
     if status:
         _check(status, "flp_checkpoint_pack")
     return kept
@@ -602,13 +622,17 @@ def checkpoint_unpack(kept: Checkpoint8, *, dtype=None, out=None, stream=None):
     if stream is not None:
         return _on_stream(stream, checkpoint_unpack, kept, dtype=dtype, out=out)
     _check_checkpoint(kept, "checkpoint")
+    q, H = kept.q, kept.cols
+    M, dev = q.shape[0], q.device
     if out is None:
-        out = torch.empty(kept.shape, dtype=dtype or kept.dtype, device=kept.q.device)
-    elif dtype is not None and out.dtype is not dtype:
-        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
-    xp, ldx = _rows(out, "out", kept.shape)
-    status = load().flp_checkpoint_unpack(kept.q.data_ptr(), kept.scale.data_ptr(), kept.q.shape[0], kept.cols, xp,
-                                          ldx, _dtype(out, "out"), _raw_stream())
+        out = torch.empty((M, H), dtype=dtype or kept.dtype, device=dev)
+        xp, ldx = out.data_ptr(), H
+    else:
+        if dtype is not None and out.dtype is not dtype:
+            raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+        xp, ldx = _rows(out, "out", (M, H))
+    status = load().flp_checkpoint_unpack(q.data_ptr(), kept.scale.data_ptr(), M, H, xp, ldx, _dtype(out, "out"),
+                                          _raw_stream(dev.index))
     if status:
         _check(status, "flp_checkpoint_unpack")
     return out
@@ -624,20 +648,22 @@ def checkpoint_weight_grad(dY, kept: Checkpoint8, *, dW=None, dw_dtype=torch.flo
     _check_checkpoint(kept, "checkpoint")
     yp, ldy = _rows(dY, "dY", dtype=torch.bfloat16)
     M, N = dY.shape
-    K = kept.cols
+    K, dev = kept.cols, dY.device
     if kept.q.shape[0] != M:
         raise ValueError(f"dY has {M} rows, the checkpoint {kept.q.shape[0]}")
     if dW is None:
         if accumulate:
             raise ValueError("accumulate needs the dW to add to")
-        dW = torch.empty(N, K, dtype=dw_dtype, device=dY.device)
+        dW = torch.empty((N, K), dtype=dw_dtype, device=dev)
     _need(dW, (torch.bfloat16, torch.float32), (N, K), "dW")
     code = _DTYPE[dW.dtype]
-    lib = load()
-    ws, ws_bytes, _keep = _scratch(workspace, lib.flp_checkpoint_weight_grad_workspace,
-                                   "flp_checkpoint_weight_grad_workspace", yp, ldy, M, N, K, code)
-    status = lib.flp_checkpoint_weight_grad(yp, ldy, kept.q.data_ptr(), kept.scale.data_ptr(), M, N, K, dW.data_ptr(),
-                                            code, int(accumulate), ws, ws_bytes, _raw_stream())
+    device = dev.index
+    # of the address only its alignment matters
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+                                   _workspace_bytes("flp_checkpoint_weight_grad_workspace", device, yp % 16, ldy, M, N,
+                                                    K, code))
+    status = load().flp_checkpoint_weight_grad(yp, ldy, kept.q.data_ptr(), kept.scale.data_ptr(), M, N, K,
+                                               dW.data_ptr(), code, accumulate, ws, ws_bytes, _raw_stream(device))
     if status:
         _check(status, "flp_checkpoint_weight_grad")
     return dW
@@ -653,20 +679,22 @@ def balance_loss(logits, top_k: int, *, experts=None, mask=None, coef: float = 1
         return _on_stream(stream, balance_loss, logits, top_k, experts=experts, mask=mask, coef=coef, grad=grad,
                           workspace=workspace)
     zp, ld = _rows(logits, "logits")
-    T, E = logits.shape
-    code = _dtype(logits, "logits")
-    dev = logits.device
-    _need_opt(mask, torch.bool, (T,), "mask")
-    _need_opt(experts, torch.int64, (T, top_k), "experts")
+    T, E = shape = logits.shape
+    code, dev = _dtype(logits, "logits"), logits.device
+    if mask is not None:
+        _need(mask, torch.bool, (T,), "mask")
+    if experts is not None:
+        _need(experts, torch.int64, (T, top_k), "experts")
     loss_out = torch.empty(1, dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int64, device=dev)
-    g = torch.empty(T, E, dtype=logits.dtype, device=dev) if grad else None
-    lib = load()
-    ws, ws_bytes, _keep = _scratch(workspace, lib.flp_balance_loss_workspace, "flp_balance_loss_workspace", T, E)
-    status = lib.flp_balance_loss(zp, ld, code, None if mask is None else mask.data_ptr(),
-                                  None if experts is None else experts.data_ptr(), T, E, top_k, coef,
-                                  loss_out.data_ptr(), None if g is None else g.data_ptr(), counts.data_ptr(), ws,
-                                  ws_bytes, _raw_stream())
+    g = torch.empty(shape, dtype=logits.dtype, device=dev) if grad else None
+    device = dev.index
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+                                   _workspace_bytes("flp_balance_loss_workspace", device, T, E))
+    status = load().flp_balance_loss(zp, ld, code, None if mask is None else mask.data_ptr(),
+                                     None if experts is None else experts.data_ptr(), T, E, top_k, coef,
+                                     loss_out.data_ptr(), None if g is None else g.data_ptr(), counts.data_ptr(), ws,
+                                     ws_bytes, _raw_stream(device))
     if status:
         _check(status, "flp_balance_loss")
     return loss_out, g, counts

@@ -180,12 +180,11 @@ def test_weight_gradient_against_differences(flp):
 def test_weight_gradient_stays_inside_its_buffers(flp):
     M, N, K = 130, 266, 520
     dy, kept = make(flp, M, N, K)
-    lib = flp.load()
     for dtype in (torch.float32, torch.bfloat16):
         raw = torch.full((N * K * dtype.itemsize + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
         dw = raw[4096:4096 + N * K * dtype.itemsize].view(dtype).view(N, K)
-        need = flp._query(lib.flp_checkpoint_weight_grad_workspace, "q", dy.data_ptr(), dy.stride(0), M, N, K,
-                          flp._DTYPE[dtype])
+        need = flp._workspace_bytes("flp_checkpoint_weight_grad_workspace", 0, dy.data_ptr(), dy.stride(0), M, N, K,
+                                    flp._DTYPE[dtype])
         ws = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
         flp.checkpoint_weight_grad(dy, kept, dW=dw, workspace=ws[4096:4096 + need])
         check_wgrad(flp, dy, kept, dw)

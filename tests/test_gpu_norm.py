@@ -222,7 +222,7 @@ def test_own_stream(flp):
 
 def test_graph_replay(flp):
     x = torch.randn(300, 4096, device="cuda").to(torch.bfloat16)
-    ws = torch.empty(flp._query(flp.load().flp_layer_norm_workspace, "q", 300, 4096), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(flp._workspace_bytes("flp_layer_norm_workspace", 0, 300, 4096), dtype=torch.uint8, device="cuda")
     step = lambda: (lambda r: (r, flp.layer_norm_backward(r[0], r[3], None, r[1], r[2], workspace=ws)))(
         flp.layer_norm(x, checkpoint=True))
     step()
