@@ -11,17 +11,24 @@
 // (a_e is centred: subtracting a constant changes nothing because sum p = 1,
 // and keeps the difference free of cancellation when the load is near even.)
 //
-// Three launches: statistics of the rows (softmax, choice) with each block's
-// sums per expert, the join of the blocks' sums into counts, loss and a_e, and
-// the gradient, which reads the logits again (from L2 when they fit).
+// Three launches: the rows' statistics (softmax, choice) with each block's sums
+// per expert; the join of the blocks' sums; and the gradient, whose blocks turn
+// the counts into the loads a_e and which reads the logits again (from L2 when
+// they fit).  Few rows take one launch instead: a cluster of blocks joins its
+// sums through distributed shared memory between the two passes.
+//
+// A row belongs to L lanes of a warp, lane l holding vectors l, l + L, ... of V
+// experts: the sums per expert then stay in the same registers from row to row.
+// The next row's logits are loaded before this row's are worked on.
 #pragma once
 #include "vec.cuh"
 
 namespace flp {
 
 constexpr int BAL_MAX_E = 1024;
-constexpr int BAL_THREADS = 256;
-constexpr int BAL_JOIN_THREADS = 1024;
+constexpr int BAL_THREADS = 512;
+constexpr int BAL_CLUSTER = 8;  // blocks of the one-launch form
+constexpr int BAL_CLUSTER_TRIPS = 4;  // trips of its row loop up to which it is the faster one
 
 struct BalParams {
     const void* z;
@@ -34,33 +41,28 @@ struct BalParams {
     void* grad;  // [T, E] in the logits' type; NULL: not wanted
     float* loss;
     long long* counts;  // [E]
-    float2* stat;       // [T]: row maximum and 1 / sum of exponentials (0: not live)
+    float2* stat;       // [T]
     float* part_p;      // [blocks][E]
     int* part_c;        // [blocks][E]
     int* part_n;        // [blocks]
-    float* load;        // [E]: a_e; [E]: coef / N
+    double* tot_p;      // [E]
+    long long* tot_c;   // [E]
+    long long* tot_n;   // [1]
     int blocks;
 };
 
 // An integer that orders floats: larger float, larger key (NaN excluded; the
-// two zeros are equal); 0 is below every float's key.
+// two zeros are equal).  -inf has the key below BAL_LOWEST.
+constexpr uint32_t BAL_LOWEST = 0x00800000u;
 __device__ __forceinline__ uint32_t order_key(float z) {
     const uint32_t b = __float_as_uint(z + 0.f);  // -0 -> +0
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    return b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
 
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+
 template <int L>
 __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
     if constexpr (L == 32) {
@@ -72,251 +74,510 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
     }
 }
 template <int L>
-__device__ __forceinline__ uint32_t group_umin(uint32_t v) {
-    if constexpr (L == 32) {
-        return __reduce_min_sync(0xffffffffu, v);
-    } else {
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-        for (int o = L / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
-        return v;
+    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Expert i of lane l.
+template <int L, int V>
+__device__ __forceinline__ int expert(int l, int i) {
+    return i / V * (L * V) + l * V + i % V;
+}
+
+// A lane's logits as loaded (V per access), and in fp32.
+template <typename T, int V>
+struct Logits;
+template <>
+struct Logits<float, 1> {
+    float u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldg(p); }
+    __device__ __forceinline__ void to(float* v) const { v[0] = u; }
+};
+template <>
+struct Logits<float, 2> {
+    float2 u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float2*>(p)); }
+    __device__ __forceinline__ void to(float* v) const { v[0] = u.x, v[1] = u.y; }
+};
+template <>
+struct Logits<float, 4> {
+    float4 u;
+    __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void to(float* v) const { v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w; }
+};
+template <>
+struct Logits<bf16, 1> {
+    unsigned short u;
+    __device__ __forceinline__ void load(const bf16* p) { u = __ldg(reinterpret_cast<const unsigned short*>(p)); }
+    __device__ __forceinline__ void to(float* v) const { v[0] = __uint_as_float(static_cast<uint32_t>(u) << 16); }
+};
+template <>
+struct Logits<bf16, 2> {
+    uint32_t u;
+    __device__ __forceinline__ void load(const bf16* p) { u = __ldg(reinterpret_cast<const uint32_t*>(p)); }
+    __device__ __forceinline__ void to(float* v) const {
+        v[0] = __uint_as_float(u << 16), v[1] = __uint_as_float(u & 0xffff0000u);
+    }
+};
+template <>
+struct Logits<bf16, 4> {
+    uint2 u;
+    __device__ __forceinline__ void load(const bf16* p) { u = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void to(float* v) const {
+        v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void store_grad(float* p, const float* v) {
+    if constexpr (V == 4)
+        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    else if constexpr (V == 2)
+        __stcs(reinterpret_cast<float2*>(p), make_float2(v[0], v[1]));
+    else
+        __stcs(p, v[0]);
+}
+template <int V>
+__device__ __forceinline__ void store_grad(bf16* p, const float* v) {
+    if constexpr (V == 4)
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+    else if constexpr (V == 2)
+        __stcs(reinterpret_cast<uint32_t*>(p), pack_bf16x2(v[0], v[1]));
+    else
+        *p = __float2bfloat16_rn(v[0]);
+}
+
+// Adds 1 to cnt[i] for the row's k largest keys, ties to the lowest expert.
+// One expert per lane, L lanes: a lane's rank is the number of lanes before it.
+template <int L>
+__device__ __forceinline__ void choose_by_rank(uint32_t key, int l, int k, int& cnt) {
+    int before = 0;
+#pragma unroll
+    for (int o = 1; o < L; ++o) {
+        const int from = (l + o) % L;
+        const uint32_t other = __shfl_sync(0xffffffffu, key, from, L);
+        before += (other > key || (other == key && from < l)) ? 1 : 0;
+    }
+    cnt += (key >= BAL_LOWEST && before < k) ? 1 : 0;
+}
+
+// The same for a warp with NE experts per lane.  The k-th largest of the lanes'
+// maxima bounds the k-th largest key from below: keys above the bound are
+// candidates, and the smallest are dropped until k are left (about one for 256
+// experts and k = 8).  Above 16 the experts are taken one at a time, which drops
+// nothing when many of the largest share a lane.
+template <int NE, int V>
+__device__ __forceinline__ void choose(const uint32_t (&key)[NE], uint32_t top, int l, int k, int (&cnt)[NE]) {
+    constexpr uint32_t ALL = 0xffffffffu;
+    uint32_t bound = BAL_LOWEST;
+    int left = k;   // experts still to take among the keys equal to `tie`
+    uint32_t tie = 0;
+    if (k <= 16) {
+        for (int j = 0; j < k; ++j) {
+            bound = __reduce_max_sync(ALL, top);
+            if (top == bound) top = 0;
+        }
+        bound = max(bound, BAL_LOWEST);
+        auto count = [&]() {  // keys at or above the bound
+            int mine = 0;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) mine += key[i] >= bound ? 1 : 0;
+            return __reduce_add_sync(ALL, mine);
+        };
+        int total = count();
+        left = 0;
+        while (total > k) {
+            uint32_t low = ALL;
+#pragma unroll
+            for (int i = 0; i < NE; ++i) low = min(low, key[i] >= bound ? key[i] : ALL);
+            low = __reduce_min_sync(ALL, low);
+            bound = low + 1;
+            total = count();
+            if (total < k) {  // only some of the smallest fit
+                tie = low;
+                left = k - total;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NE; ++i) cnt[i] += key[i] >= bound ? 1 : 0;
+    }
+    if (left == 0) return;
+    // one at a time: the largest key that is left (the tie above, or any for large k)
+    uint32_t rest[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) rest[i] = tie == 0 ? key[i] : key[i] == tie ? tie : 0u;
+    for (int j = 0; j < left; ++j) {
+        uint32_t m = rest[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) m = max(m, rest[i]);
+        m = __reduce_max_sync(ALL, m);
+        if (m < BAL_LOWEST) break;
+        uint32_t at = ALL;
+#pragma unroll
+        for (int i = NE - 1; i >= 0; --i)
+            if (rest[i] == m) at = static_cast<uint32_t>(expert<32, V>(l, i));
+        at = __reduce_min_sync(ALL, at);
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (static_cast<uint32_t>(expert<32, V>(l, i)) == at) {
+                ++cnt[i];
+                rest[i] = 0;
+            }
     }
 }
-template <int L>
-__device__ __forceinline__ bool group_any(bool b) {
-    return group_umax<L>(b ? 1u : 0u) != 0u;
+
+// This block's sums per expert in shared memory: [4][E] fp32 probabilities (the
+// first row ends up with the sums), [E] counts, one count of live rows.
+constexpr int BAL_SHARES = 4;
+struct BalSums {
+    float* p;
+    int* c;
+    int* n;
+};
+inline size_t bal_smem(int64_t E) { return ((BAL_SHARES + 1) * static_cast<size_t>(E) + 1) * 4; }
+__device__ __forceinline__ BalSums bal_sums(uint32_t* dyn, int E) {
+    BalSums s;
+    s.p = reinterpret_cast<float*>(dyn);
+    s.c = reinterpret_cast<int*>(dyn + BAL_SHARES * E);
+    s.n = s.c + E;
+    return s;
 }
 
-__device__ __forceinline__ float load_logit(const bf16* p) {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16);
-}
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
+// The lane's logits of a row; -inf where there is no expert.
+template <typename T, int L, int NE, int V>
+struct RowLogits {
+    Logits<T, V> u[NE / V];
+    __device__ __forceinline__ void load(const BalParams& p, long long row, int l) {
+        const T* z = static_cast<const T*>(p.z) + row * p.ld;
+#pragma unroll
+        for (int i = 0; i < NE; i += V)
+            if (row < p.T && expert<L, V>(l, i) < p.E) u[i / V].load(z + expert<L, V>(l, i));
+    }
+    __device__ __forceinline__ void to(const BalParams& p, int l, bool wanted, float (&v)[NE]) const {
+#pragma unroll
+        for (int i = 0; i < NE; i += V) {
+            if (wanted && expert<L, V>(l, i) < p.E) {
+                u[i / V].to(v + i);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i + j] = -INFINITY;
+            }
+        }
+    }
+};
 
-// L lanes per row; lane l holds experts l, l + L, ..., NE of them.
-template <typename T, int L, int NE>
-__global__ void __launch_bounds__(BAL_THREADS) flp_balance_rows_kernel(const BalParams p) {
-    extern __shared__ uint32_t dyn[];  // [E] float sums, [E] counts, one live count
-    float* bp = reinterpret_cast<float*>(dyn);
-    int* bc = reinterpret_cast<int*>(dyn + p.E);
-    int* bn = bc + p.E;
-    for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) bc[e] = 0;
-    if (threadIdx.x == 0) *bn = 0;
-    __syncthreads();
+// The first pass over rows `block`, `block + blocks`, ... (times the rows a
+// block holds).  Ends with a block barrier behind the sums.
+// `stat` gets each row's maximum and 1 / sum of exponentials (0: not live), by
+// row, or (kLocal) by the block's own count of rows.
+template <typename T, int L, int NE, int V, bool kLocal>
+__device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& sums, float2* stat, int block, int blocks) {
     constexpr int RPB = BAL_THREADS / L;
+    for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) sums.c[e] = 0;
+    if (threadIdx.x == 0) *sums.n = 0;
+    __syncthreads();
     const int l = threadIdx.x % L, sub = threadIdx.x / L;
     float psum[NE] = {};
     int cnt[NE] = {};
     int live_rows = 0;
-    const long long stride = static_cast<long long>(gridDim.x) * RPB;
+    const long long stride = static_cast<long long>(blocks) * RPB;
     // every lane of a warp makes the same trips: the row groups of a warp move together
-    const long long first = static_cast<long long>(blockIdx.x) * RPB;
-    for (long long base = first; base < p.T; base += stride) {
+    long long base = static_cast<long long>(block) * RPB;
+    RowLogits<T, L, NE, V> next;
+    next.load(p, base + sub, l);
+    bool kept_next = base + sub < p.T && (!p.mask || p.mask[base + sub]);
+    for (int own = sub; base < p.T; base += stride, own += RPB) {
         const long long row = base + sub;
-        const bool in = row < p.T;
-        const T* z = static_cast<const T*>(p.z) + row * p.ld;
+        const bool kept = kept_next;
         float v[NE];
-        float m = -INFINITY;
+        next.to(p, l, kept, v);
+        next.load(p, row + stride, l);
+        kept_next = row + stride < p.T && (!p.mask || p.mask[row + stride]);
         bool odd = false;  // NaN or +inf
-        const bool kept = in && (!p.mask || p.mask[row]);
+        uint32_t key[NE], top = 0;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = l + i * L;
-            v[i] = kept && e < p.E ? load_logit(z + e) : -INFINITY;
             odd |= !(v[i] < INFINITY);
-            m = fmaxf(m, v[i]);
+            key[i] = order_key(v[i]);
+            top = max(top, key[i]);
         }
-        odd = group_any<L>(odd);
-        m = group_max<L>(m);
-        const bool live = odd || m > -INFINITY;
+        if constexpr (L == 32) {
+            odd = __any_sync(0xffffffffu, odd);
+        } else {
+            const uint32_t votes = __ballot_sync(0xffffffffu, odd) >> ((threadIdx.x & 31) / L * L);
+            odd = (votes & ((1u << L) - 1u)) != 0u;
+        }
+        const uint32_t most = group_umax<L>(top);
+        const bool live = odd || most >= BAL_LOWEST;
+        // a row without any logit gets maximum 0: all its exponentials are 0
+        const float m = live ? key_value(most) : 0.f;
         float s = 0.f;
         float ex[NE];
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            ex[i] = live ? expf(v[i] - m) : 0.f;
+            // the difference is formed first: its error grows with its own size alone
+            ex[i] = ex2_approx((v[i] - m) * LOG2E);
             s += ex[i];
         }
         s = group_sum<L>(s);
-        const float inv = odd ? __uint_as_float(0x7fc00000u) : live ? 1.f / s : 0.f;
-        if (live) {
+        const float inv = odd ? __uint_as_float(0x7fc00000u) : live ? rcp_approx(s) : 0.f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) psum[i] = fmaf(ex[i], inv, psum[i]);
-        }
-        if (l == 0 && in) {
-            p.stat[row] = make_float2(m, inv);
+        for (int i = 0; i < NE; ++i) psum[i] = fmaf(ex[i], inv, psum[i]);
+        if (l == 0 && row < p.T) {
+            stat[kLocal ? own : row] = make_float2(m, inv);
             live_rows += live;
         }
         if (p.experts) {
             if (live)
                 for (int j = l; j < p.k; j += L) {
                     const long long e = p.experts[row * p.k + j];
-                    if (e >= 0 && e < p.E) atomicAdd(&bc[e], 1);  // integers: any order gives the same sum
+                    if (e >= 0 && e < p.E) atomicAdd(&sums.c[e], 1);  // integers: any order gives the same sum
                 }
+        } else if constexpr (L < 32) {
+            choose_by_rank<L>(odd ? 0u : key[0], l, p.k, cnt[0]);
         } else {
-            uint32_t key[NE];
-#pragma unroll
-            for (int i = 0; i < NE; ++i) key[i] = !odd && v[i] > -INFINITY ? order_key(v[i]) : 0u;
-            for (int j = 0; j < p.k; ++j) {
-                uint32_t top = key[0];
-#pragma unroll
-                for (int i = 1; i < NE; ++i) top = max(top, key[i]);
-                top = group_umax<L>(top);
-                uint32_t at = 0xffffffffu;  // the lowest expert that holds it
-#pragma unroll
-                for (int i = NE - 1; i >= 0; --i)
-                    if (key[i] == top) at = static_cast<uint32_t>(l + i * L);
-                at = group_umin<L>(at);
-                if (top == 0u) at = 0xffffffffu;  // nothing left to choose
-#pragma unroll
-                for (int i = 0; i < NE; ++i)
-                    if (static_cast<uint32_t>(l + i * L) == at) {
-                        ++cnt[i];
-                        key[i] = 0u;
-                    }
-            }
+            if (live && !odd) choose<NE, V>(key, top, l, p.k, cnt);  // the same in the whole warp
         }
     }
-    griddep_launch_dependents();
-    // this block's sums: counts in any order, the fp32 sums row group by row group
+    // counts in any order, the fp32 sums in a fixed one: lanes of a warp that
+    // hold the same experts, then the warps
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-        const int e = l + i * L;
-        if (e < p.E && cnt[i]) atomicAdd(&bc[e], cnt[i]);
+        const int e = expert<L, V>(l, i);
+        if (e < p.E && cnt[i]) atomicAdd(&sums.c[e], cnt[i]);
     }
-    if (l == 0 && live_rows) atomicAdd(bn, live_rows);
-    // lanes of a warp that hold the same experts first
+    if (l == 0 && live_rows) atomicAdd(sums.n, live_rows);
 #pragma unroll
     for (int i = 0; i < NE; ++i)
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) psum[i] += __shfl_xor_sync(0xffffffffu, psum[i], o);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int w = 0; w < BAL_THREADS / 32; ++w) {
-        if (warp == w && lane < L) {
+#pragma unroll
+    for (int w = 0; w < BAL_THREADS / 32; w += BAL_SHARES) {
+        if (warp >= w && warp < w + BAL_SHARES && lane < L) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
-                const int e = l + i * L;
-                if (e < p.E) bp[e] = (w ? bp[e] : 0.f) + psum[i];
+                const int e = expert<L, V>(l, i);
+                float* at = sums.p + (warp - w) * p.E + e;
+                if (e < p.E) *at = (w ? *at : 0.f) + psum[i];
             }
         }
         __syncthreads();
     }
     for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) {
-        p.part_p[static_cast<long long>(blockIdx.x) * p.E + e] = bp[e];
-        p.part_c[static_cast<long long>(blockIdx.x) * p.E + e] = bc[e];
-    }
-    if (threadIdx.x == 0) p.part_n[blockIdx.x] = *bn;
-}
-
-// One block: counts, loss and the centred loads from the blocks' sums, in 64
-// bits and a fixed order.
-__global__ void __launch_bounds__(BAL_JOIN_THREADS) flp_balance_join_kernel(const BalParams p) {
-    __shared__ double dsum[32], tot_p[BAL_MAX_E];
-    __shared__ long long isum[32], tot_c[BAL_MAX_E];
-    __shared__ double sh_d;
-    __shared__ long long sh_i[2];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_wait();
-    // a warp takes 32 experts at a time and, when there are few experts, a
-    // share of the blocks
-    const int groups = (p.E + 31) / 32;
-    for (int e = threadIdx.x; e < p.E; e += BAL_JOIN_THREADS) tot_p[e] = 0., tot_c[e] = 0;
-    __shared__ double wp[32][32];
-    __shared__ long long wc[32][32];
-    const int ways = max(1, 32 / groups);  // warps per group of experts
-    for (int g0 = 0; g0 < groups; g0 += 32 / ways) {
-        const int g = g0 + warp / ways, way = warp % ways;
-        double a = 0.;
-        long long c = 0;
-        const int e = g * 32 + lane;
-        const bool on = warp / ways < 32 / ways && g < groups && e < p.E;
-        if (on)
-            for (int b = way; b < p.blocks; b += ways) {
-                a += p.part_p[static_cast<long long>(b) * p.E + e];
-                c += p.part_c[static_cast<long long>(b) * p.E + e];
-            }
-        wp[warp][lane] = a;
-        wc[warp][lane] = c;
-        __syncthreads();
-        if (on && way == 0) {
-            for (int w = 1; w < ways; ++w) a += wp[warp + w][lane], c += wc[warp + w][lane];
-            tot_p[e] = a;
-            tot_c[e] = c;
-        }
-        __syncthreads();
-    }
-    // N and C
-    long long n = 0, c = 0;
-    for (int b = threadIdx.x; b < p.blocks; b += BAL_JOIN_THREADS) n += p.part_n[b];
-    for (int e = threadIdx.x; e < p.E; e += BAL_JOIN_THREADS) c += tot_c[e];
-    for (int which = 0; which < 2; ++which) {
-        long long x = which ? c : n;
+        float t = sums.p[e];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) isum[warp] = x;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            long long y = 0;
-            for (int w = 0; w < 32; ++w) y += isum[w];
-            sh_i[which] = y;
-        }
-        __syncthreads();
+        for (int w = 1; w < BAL_SHARES; ++w) t += sums.p[w * p.E + e];
+        sums.p[e] = t;
     }
-    const long long N = sh_i[0], C = sh_i[1];
-    const bool any = N > 0 && C > 0;
-    // loss = coef (1 + sum_e a_e p_e / N)
-    double part = 0.;
-    for (int e = threadIdx.x; e < p.E; e += BAL_JOIN_THREADS) {
-        const double a = any ? (static_cast<double>(p.E) * static_cast<double>(tot_c[e]) - static_cast<double>(C)) /
-                                   static_cast<double>(C)
-                             : 0.;
-        p.load[e] = static_cast<float>(a);
-        p.counts[e] = tot_c[e];
-        part += a * tot_p[e];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) dsum[warp] = part;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        sh_d = 0.;
-        for (int w = 0; w < 32; ++w) sh_d += dsum[w];
-        *p.loss = any ? static_cast<float>(p.coef * (1. + sh_d / static_cast<double>(N))) : 0.f;
-        p.load[p.E] = any ? static_cast<float>(p.coef / static_cast<double>(N)) : 0.f;
-    }
-    griddep_launch_dependents();
 }
 
-template <typename T, int L, int NE>
-__global__ void __launch_bounds__(BAL_THREADS) flp_balance_grad_kernel(const BalParams p) {
+// The centred load a_e = (E c - C) / C: the numerator is exact in 64-bit integers.
+__device__ __forceinline__ float bal_load(int E, long long c, long long C) {
+    return static_cast<float>(E * c - C) / static_cast<float>(C);
+}
+
+// hi + lo += x with the rounding of the sum kept in lo (a 64-bit sum's accuracy
+// without 64-bit arithmetic, of which the chip has very little).
+__device__ __forceinline__ void sum_exactly(float& hi, float& lo, float x) {
+    const float s = hi + x;
+    const float t = s - hi;
+    lo += (hi - (s - t)) + (x - t);
+    hi = s;
+}
+
+// Sum over the block of 64-bit values, the same in every thread; `red` holds one per warp.
+template <typename V>
+__device__ __forceinline__ V bal_block_sum(V x, V* red) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    V y = red[0];
+    for (int w = 1; w < BAL_THREADS / 32; ++w) y += red[w];
+    return y;
+}
+
+// From the totals (tot_c(e), tot_p(e), N): this lane's loads and the factor of
+// the gradient; `first` (one block) also writes counts and loss.
+template <int L, int NE, int V, typename FC, typename FP>
+__device__ __forceinline__ float balance_loads(const BalParams& p, bool first, long long N, FC&& tot_c, FP&& tot_p,
+                                               float (&a)[NE]) {
+    __shared__ long long red_i[BAL_THREADS / 32];
+    __shared__ double red_d[BAL_THREADS / 32];
+    long long c = 0;
+    for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) c += tot_c(e);
+    const long long C = bal_block_sum(c, red_i);
+    const bool any = N > 0 && C > 0;
+    const int l = threadIdx.x % L;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        const int e = expert<L, V>(l, i);
+        a[i] = any && e < p.E ? bal_load(p.E, tot_c(e), C) : 0.f;
+    }
+    if (first) {
+        // loss = coef (1 + sum_e a_e p_e / N)
+        double part = 0.;
+        for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) {
+            p.counts[e] = tot_c(e);
+            part += static_cast<double>(p.E * tot_c(e) - C) * tot_p(e);
+        }
+        part = bal_block_sum(part, red_d);
+        if (threadIdx.x == 0)
+            *p.loss = any ? static_cast<float>(p.coef * (1. + part / (static_cast<double>(N) * static_cast<double>(C)))) : 0.f;
+    }
+    return any ? static_cast<float>(p.coef / static_cast<double>(N)) : 0.f;
+}
+
+// The second pass.
+template <typename T, int L, int NE, int V, bool kLocal>
+__device__ __forceinline__ void balance_grad(const BalParams& p, const float2* stat, const float (&a)[NE], float scale,
+                                             int block, int blocks) {
     constexpr int RPB = BAL_THREADS / L;
     const int l = threadIdx.x % L, sub = threadIdx.x / L;
-    griddep_wait();
-    float a[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) a[i] = l + i * L < p.E ? p.load[l + i * L] : 0.f;
-    const float scale = p.load[p.E];
-    const long long stride = static_cast<long long>(gridDim.x) * RPB;
-    for (long long base = static_cast<long long>(blockIdx.x) * RPB; base < p.T; base += stride) {
+    const long long stride = static_cast<long long>(blocks) * RPB;
+    long long base = static_cast<long long>(block) * RPB;
+    RowLogits<T, L, NE, V> next;
+    next.load(p, base + sub, l);
+    float2 st_next = base + sub < p.T ? stat[kLocal ? sub : base + sub] : make_float2(0.f, 0.f);
+    for (int own = sub; base < p.T; base += stride, own += RPB) {
         const long long row = base + sub;
-        const bool in = row < p.T;
-        const float2 st = in ? p.stat[row] : make_float2(0.f, 0.f);
-        const bool live = !(st.y == 0.f);  // NaN counts
-        const T* z = static_cast<const T*>(p.z) + row * p.ld;
+        const float2 st = st_next;
         float pr[NE];
+        // a row that is not live (1 / sum = 0) has exponentials of 0 whatever it holds
+        next.to(p, l, !(st.y == 0.f), pr);
+        next.load(p, row + stride, l);
+        if (row + stride < p.T) st_next = stat[kLocal ? own + RPB : row + stride];
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const int e = l + i * L;
-            pr[i] = live && e < p.E ? expf(load_logit(z + e) - st.x) * st.y : 0.f;
+            pr[i] = ex2_approx((pr[i] - st.x) * LOG2E) * st.y;
             dot = fmaf(pr[i], a[i], dot);
         }
         dot = group_sum<L>(dot);
         T* g = static_cast<T*>(p.grad) + row * p.E;
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = l + i * L;
-            const float o[1] = {live ? pr[i] * (a[i] - dot) * scale : 0.f};
-            if (in && e < p.E) store_vec<1>(g + e, o);
+        for (int i = 0; i < NE; ++i) pr[i] *= (a[i] - dot) * scale;
+#pragma unroll
+        for (int i = 0; i < NE; i += V)
+            if (row < p.T && expert<L, V>(l, i) < p.E) store_grad<V>(g + expert<L, V>(l, i), pr + i);
+    }
+}
+
+template <typename T, int L, int NE, int V>
+__global__ void __launch_bounds__(BAL_THREADS) flp_balance_rows_kernel(const BalParams p) {
+    extern __shared__ uint32_t dyn[];
+    const BalSums sums = bal_sums(dyn, p.E);
+    balance_rows<T, L, NE, V, false>(p, sums, p.stat, blockIdx.x, gridDim.x);
+    griddep_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) {
+        p.part_p[static_cast<long long>(blockIdx.x) * p.E + e] = sums.p[e];
+        p.part_c[static_cast<long long>(blockIdx.x) * p.E + e] = sums.c[e];
+    }
+    if (threadIdx.x == 0) p.part_n[blockIdx.x] = *sums.n;
+}
+
+// The blocks' sums per expert in a fixed order: 32 experts per block, a warp per
+// share of the partials.
+__global__ void __launch_bounds__(1024) flp_balance_join_kernel(const BalParams p) {
+    __shared__ float wp[2][32][33];
+    __shared__ int wc[32][33];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * 32 + lane;
+    griddep_wait();
+    griddep_launch_dependents();
+    float hi = 0.f, lo = 0.f;
+    int c = 0;  // at most T < 2^31 for one expert
+    if (e < p.E) {
+#pragma unroll 4
+        for (int b = warp; b < p.blocks; b += 32) {
+            sum_exactly(hi, lo, p.part_p[static_cast<long long>(b) * p.E + e]);
+            c += p.part_c[static_cast<long long>(b) * p.E + e];
         }
     }
+    wp[0][warp][lane] = hi;
+    wp[1][warp][lane] = lo;
+    wc[warp][lane] = c;
+    __syncthreads();
+    hi = wp[0][lane][warp];
+    lo = wp[1][lane][warp];
+    c = wc[lane][warp];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, hi, o);
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        sum_exactly(hi, lo, other);
+        c += __shfl_xor_sync(0xffffffffu, c, o);
+    }
+    const int f = blockIdx.x * 32 + warp;
+    if (lane == 0 && f < p.E) {
+        p.tot_p[f] = static_cast<double>(hi) + static_cast<double>(lo);
+        p.tot_c[f] = c;
+    }
+    if (blockIdx.x == 0 && warp == 0) {
+        int n = 0;
+        for (int b = lane; b < p.blocks; b += 32) n += p.part_n[b];
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) *p.tot_n = n;
+    }
+}
+
+// Loss, counts and (unless there is none to write) the gradient.
+template <typename T, int L, int NE, int V>
+__global__ void __launch_bounds__(BAL_THREADS) flp_balance_grad_kernel(const BalParams p) {
+    griddep_wait();
+    float a[NE];
+    const float scale = balance_loads<L, NE, V>(
+        p, blockIdx.x == 0, *p.tot_n, [&](int e) { return p.tot_c[e]; }, [&](int e) { return p.tot_p[e]; }, a);
+    if (p.grad) balance_grad<T, L, NE, V, false>(p, p.stat, a, scale, blockIdx.x, gridDim.x);
+}
+
+// Both passes in one launch of one cluster.
+template <typename T, int L, int NE, int V>
+__global__ void __launch_bounds__(BAL_THREADS) __cluster_dims__(BAL_CLUSTER, 1, 1)
+    flp_balance_cluster_kernel(const BalParams p) {
+    extern __shared__ uint32_t dyn[];
+    __shared__ double tot_p[BAL_MAX_E];
+    __shared__ int tot_c[BAL_MAX_E];
+    __shared__ float2 stat[BAL_CLUSTER_TRIPS * BAL_THREADS / L];
+    const int rank = static_cast<int>(cluster_ctarank());
+    const BalSums sums = bal_sums(dyn, p.E);
+    balance_rows<T, L, NE, V, true>(p, sums, stat, rank, BAL_CLUSTER);
+    cluster_sync();
+    auto peer = [](const void* at, int r) {
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_addr(at), r)) : "memory");
+        return v;
+    };
+    for (int e = threadIdx.x; e < p.E; e += BAL_THREADS) {
+        float hi = 0.f, lo = 0.f;
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < BAL_CLUSTER; ++r) {
+            sum_exactly(hi, lo, __uint_as_float(peer(sums.p + e, r)));
+            c += static_cast<int>(peer(sums.c + e, r));
+        }
+        tot_p[e] = static_cast<double>(hi) + static_cast<double>(lo);
+        tot_c[e] = c;
+    }
+    long long n = 0;
+    for (int r = 0; r < BAL_CLUSTER; ++r) n += static_cast<int>(peer(sums.n, r));
+    cluster_sync();  // the peers' sums have been read: blocks may go their own ways
+    float a[NE];
+    const float scale = balance_loads<L, NE, V>(
+        p, rank == 0, n, [&](int e) -> long long { return tot_c[e]; }, [&](int e) { return tot_p[e]; }, a);
+    if (p.grad) balance_grad<T, L, NE, V, true>(p, stat, a, scale, rank, BAL_CLUSTER);
 }
 
 }  // namespace flp

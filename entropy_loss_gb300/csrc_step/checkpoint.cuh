@@ -14,6 +14,7 @@ struct CkParams {
     unsigned per_row;            // vectors of a padded row
     unsigned long long inverse;  // 2^64 / per_row, rounded up: row = hi(vector * inverse)
     long long total;             // vectors in all
+    int* clear;                  // a word that unpack zeroes (NULL: none)
 };
 
 constexpr int CK_THREADS = 256;
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_unpack_kernel(const CkParam
     long long row[CK_PER_THREAD];
     int col[CK_PER_THREAD];
     griddep_launch_dependents();  // the weight gradient's contraction may set up meanwhile
+    if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0;
 #pragma unroll
     for (int k = 0; k < CK_PER_THREAD; ++k) {
         const long long j = first + k * CK_THREADS;

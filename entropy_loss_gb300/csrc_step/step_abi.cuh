@@ -151,9 +151,10 @@ struct WgradPlan {
     size_t off_x, off_y, off_part, bytes;
 };
 
-// Whole rounds of tiles go straight to dW; the rest are split.  A split run
-// costs its 64-row blocks plus writing and joining its partial tile (about
-// the time of 6 blocks: 512 KiB written and read back).
+// Whole rounds of tiles go straight to dW; the rest are split into the number
+// of runs that costs least, in the time of a 64-row block of a tile (0.54 us):
+// the blocks of a run, and for joining 5 (a launch) and a quarter per partial
+// tile (512 KiB written and read back).
 WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t K, int dw_dtype, int pairs) {
     WgradPlan w{};
     pairs = std::max(1, pairs);
@@ -171,8 +172,8 @@ WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t
         double best = 1e300;
         const int64_t most = std::min<int64_t>(KB, std::max<int64_t>(1, 4 * pairs / std::max<int64_t>(1, rest)));
         for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
-            const double joined = s > 1 || !direct ? 6.0 : 0.0;
-            const double cost = static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(KB, s)) + joined);
+            const double joined = s > 1 || !direct ? 5.0 + 0.25 * static_cast<double>(rest * s) : 0.0;
+            const double cost = static_cast<double>(cdiv(rest * s, pairs) * cdiv(KB, s)) + joined;
             if (cost < best - 1e-9) {
                 best = cost;
                 w.splits = static_cast<int>(s);
@@ -233,8 +234,9 @@ CkParams ck_params(void* x, int64_t ldx, const void* q, const void* scale, int64
 
 template <typename T, int V>
 flp_status ck_launch(bool pack, void* x, int64_t ldx, const void* q, const void* scale, int64_t M, int64_t H,
-                     cudaStream_t s) {
-    const CkParams p = ck_params<V, T>(x, ldx, q, scale, M, H);
+                     cudaStream_t s, int* clear = nullptr) {
+    CkParams p = ck_params<V, T>(x, ldx, q, scale, M, H);
+    p.clear = clear;
     const int64_t grid = cdiv(p.total, CK_THREADS * CK_PER_THREAD);
     // the row of a vector comes exactly from one multiplication while vectors x vectors per row < 2^64
     if (grid > INT32_MAX || static_cast<double>(p.total + (1 << 20)) * p.per_row > 1.8e19) return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
@@ -264,41 +266,59 @@ flp_status ck_run(bool pack, const void* x, int64_t ldx, int dtype, const void* 
 
 // ----------------------------------------------------------------- balance loss
 
-// Calls f(lanes per row, experts per lane) for E experts.
+// Calls f(lanes per row, experts per lane, experts per access) for E experts;
+// `vec`: rows are aligned to four elements and hold a multiple of four.
 template <typename F>
-flp_status balance_shape(int64_t E, F&& f) {
-#define FLP_SHAPE(L, NE) \
-    if (E <= (L) * (NE)) return f(std::integral_constant<int, L>{}, std::integral_constant<int, NE>{});
-    FLP_SHAPE(8, 1)
-    FLP_SHAPE(16, 1)
-    FLP_SHAPE(32, 1)
-    FLP_SHAPE(32, 2)
-    FLP_SHAPE(32, 4)
-    FLP_SHAPE(32, 8)
-    FLP_SHAPE(32, 16)
-    FLP_SHAPE(32, 32)
+flp_status balance_shape(int64_t E, bool vec, F&& f) {
+#define FLP_SHAPE(L, NE, V)    \
+    if (E <= (L) * (NE))       \
+        return f(std::integral_constant<int, L>{}, std::integral_constant<int, NE>{}, std::integral_constant<int, V>{});
+    FLP_SHAPE(8, 1, 1)
+    FLP_SHAPE(16, 1, 1)
+    FLP_SHAPE(32, 1, 1)
+    if (vec) {
+        FLP_SHAPE(32, 2, 2)
+        FLP_SHAPE(32, 4, 4)
+        FLP_SHAPE(32, 8, 4)
+    } else {
+        FLP_SHAPE(32, 2, 1)
+        FLP_SHAPE(32, 4, 1)
+        FLP_SHAPE(32, 8, 1)
+    }
+    FLP_SHAPE(32, 16, 1)
+    FLP_SHAPE(32, 32, 1)
 #undef FLP_SHAPE
     return fail(FLP_ERR_UNSUPPORTED, "at most 1024 experts");
 }
 
-constexpr int64_t kBalanceBlocksPerSm = 4;
+constexpr int64_t kBalanceBlocksPerSm = 2;
 
 struct BalancePlan {
     int64_t blocks;
-    size_t off_stat, off_p, off_c, off_n, off_load, bytes;
+    bool cluster;  // one launch of one cluster
+    size_t off_p, off_c, off_n, off_tp, off_tc, off_tn, bytes;
 };
 
 BalancePlan plan_balance(int64_t T, int64_t E, int sm_count) {
     BalancePlan b{};
     const int64_t lanes = E <= 8 ? 8 : E <= 16 ? 16 : 32;
     const int64_t rows = BAL_THREADS / lanes;
-    b.blocks = std::min(cdiv(T, rows), sm_count * kBalanceBlocksPerSm);
-    b.off_stat = 0;
-    b.off_p = align_up(static_cast<size_t>(T) * 8, 256);
-    b.off_c = b.off_p + align_up(static_cast<size_t>(b.blocks) * E * 4, 256);
-    b.off_n = b.off_c + align_up(static_cast<size_t>(b.blocks) * E * 4, 256);
-    b.off_load = b.off_n + align_up(static_cast<size_t>(b.blocks) * 4, 256);
-    b.bytes = b.off_load + align_up(static_cast<size_t>(E + 1) * 4, 256);
+    b.cluster = cdiv(T, rows) <= BAL_CLUSTER * BAL_CLUSTER_TRIPS;
+    b.blocks = std::max<int64_t>(1, std::min(cdiv(T, rows), sm_count * kBalanceBlocksPerSm));
+    if (b.cluster) return b;  // no workspace: everything is in shared memory
+    size_t at = align_up(static_cast<size_t>(T) * 8, 256);  // the rows' statistics first
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += align_up(n, 256);
+        return here;
+    };
+    b.off_p = take(static_cast<size_t>(b.blocks) * E * 4);
+    b.off_c = take(static_cast<size_t>(b.blocks) * E * 4);
+    b.off_n = take(static_cast<size_t>(b.blocks) * 4);
+    b.off_tp = take(static_cast<size_t>(E) * 8);
+    b.off_tc = take(static_cast<size_t>(E) * 8);
+    b.off_tn = take(8);
+    b.bytes = at;
     return b;
 }
 
@@ -525,14 +545,16 @@ extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, c
     if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace))
         return fail(FLP_ERR_WORKSPACE, "weight gradient workspace null, misaligned or too small");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    FLP_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));  // the error word
     if (M == 0) {
+        FLP_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), s));  // the error word
         if (!accumulate_dW) FLP_CUDA(cudaMemsetAsync(dW, 0, static_cast<size_t>(N) * K * elem(dW_dtype), s));
         return FLP_OK;
     }
     if ((st = check_on_current_device(dY, "dY")) != FLP_OK) return st;
-    // the pads of the checkpoint's last blocks are unpacked with the rest (they hold zeros)
-    if ((st = ck_launch<bf16, 8>(false, ws + w.off_x, w.Kp, q, scale, M, w.Kp, s)) != FLP_OK) return st;
+    // the pads of the checkpoint's last blocks are unpacked with the rest (they
+    // hold zeros); the same kernel clears the error word
+    st = ck_launch<bf16, 8>(false, ws + w.off_x, w.Kp, q, scale, M, w.Kp, s, reinterpret_cast<int*>(ws));
+    if (st != FLP_OK) return st;
     const void* y = dY;
     int64_t ldy = lddy;
     if (w.Np) {
@@ -570,6 +592,8 @@ extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, c
     p.splits = w.splits;
     p.units = w.units;
     p.KB = static_cast<int>(cdiv(M, BK));
+    // equal runs of at most WGRAD_RUN blocks
+    p.run = static_cast<int>(cdiv(p.KB, cdiv(p.KB, WGRAD_RUN)));
     p.N = static_cast<int>(N);
     p.K = static_cast<int>(K);
     p.add = accumulate_dW ? 1 : 0;
@@ -617,7 +641,7 @@ extern "C" flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype
     if (st != FLP_OK) return st;
     if (T > 0 && (st = check_on_current_device(logits, "logits")) != FLP_OK) return st;
     const BalancePlan b = plan_balance(T, E, d->sm_count);
-    if (!workspace || workspace_bytes < b.bytes || !aligned16(workspace))
+    if (b.bytes > 0 && (!workspace || workspace_bytes < b.bytes || !aligned16(workspace)))
         return fail(FLP_ERR_WORKSPACE, "balance loss workspace null, misaligned or too small");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -633,27 +657,33 @@ extern "C" flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype
     p.grad = grad;
     p.loss = loss;
     p.counts = reinterpret_cast<long long*>(counts);
-    p.stat = reinterpret_cast<float2*>(ws + b.off_stat);
+    p.stat = reinterpret_cast<float2*>(ws);
     p.part_p = reinterpret_cast<float*>(ws + b.off_p);
     p.part_c = reinterpret_cast<int*>(ws + b.off_c);
     p.part_n = reinterpret_cast<int*>(ws + b.off_n);
-    p.load = reinterpret_cast<float*>(ws + b.off_load);
+    p.tot_p = reinterpret_cast<double*>(ws + b.off_tp);
+    p.tot_c = reinterpret_cast<long long*>(ws + b.off_tc);
+    p.tot_n = reinterpret_cast<long long*>(ws + b.off_tn);
     p.blocks = static_cast<int>(b.blocks);
-    const size_t smem = (2 * static_cast<size_t>(E) + 1) * 4;
+    const size_t smem = bal_smem(E);
     auto typed = [&](auto t) -> flp_status {
         using T_ = decltype(t);
-        return balance_shape(E, [&](auto l, auto ne) -> flp_status {
-            constexpr int L = decltype(l)::value, NE = decltype(ne)::value;
-            if (T > 0) {
-                const flp_status r = launch_step(flp_balance_rows_kernel<T_, L, NE>, b.blocks, BAL_THREADS, smem, s,
-                                                 "flp_balance_rows_kernel launch", false, p);
-                if (r != FLP_OK) return r;
-            }
-            const flp_status r = launch_step(flp_balance_join_kernel, 1, BAL_JOIN_THREADS, 0, s,
-                                             "flp_balance_join_kernel launch", T > 0, p);
-            if (r != FLP_OK || !grad || T == 0) return r;
-            return launch_step(flp_balance_grad_kernel<T_, L, NE>, b.blocks, BAL_THREADS, 0, s,
-                               "flp_balance_grad_kernel launch", true, p);
+        const size_t four = 4 * static_cast<size_t>(elem(dtype));
+        const bool vec = E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % four == 0 &&
+                         reinterpret_cast<uintptr_t>(grad) % four == 0;
+        return balance_shape(E, vec, [&](auto l, auto ne, auto v) -> flp_status {
+            constexpr int L = decltype(l)::value, NE = decltype(ne)::value, V = decltype(v)::value;
+            if (b.cluster)
+                return launch_step(flp_balance_cluster_kernel<T_, L, NE, V>, BAL_CLUSTER, BAL_THREADS, smem, s,
+                                   "flp_balance_cluster_kernel launch", false, p);
+            flp_status r = launch_step(flp_balance_rows_kernel<T_, L, NE, V>, b.blocks, BAL_THREADS, smem, s,
+                                       "flp_balance_rows_kernel launch", false, p);
+            if (r == FLP_OK)
+                r = launch_step(flp_balance_join_kernel, cdiv(E, 32), 1024, 0, s, "flp_balance_join_kernel launch", true, p);
+            if (r == FLP_OK)
+                r = launch_step(flp_balance_grad_kernel<T_, L, NE, V>, grad ? b.blocks : 1, BAL_THREADS, 0, s,
+                                "flp_balance_grad_kernel launch", true, p);
+            return r;
         });
     };
     return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});

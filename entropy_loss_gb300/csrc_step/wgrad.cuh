@@ -28,6 +28,7 @@ struct WgradParams {
     int splits;    // runs of each other tile
     int units;
     int KB;        // 64-row blocks of dY and X^
+    int run;       // 64-row blocks that one accumulation takes (fp32 results)
     int N, K;
     int add;       // whole tiles add into dW
     int bf16_out;  // dW in bf16 (else fp32)
@@ -40,7 +41,17 @@ struct WgradUnit {
     int kb0, kb1;  // 64-row blocks
     int part;      // partial tile index, -1: written to dW
     int halves;    // 256-column halves that hold columns of dW
+    int run;       // blocks accumulated before the accumulators are drained
 };
+
+// The tensor cores round an accumulator toward zero at every step, so the error
+// of a long sum grows with its length: 3.0e-6 of the result over 8192 rows of
+// normal values, 1.9e-5 over 32768, against 4.8e-7 over 2048.  An fp32 result is
+// therefore summed in runs of at most 2048 rows, whose sums are added in memory,
+// rounded to nearest.  Each further run drains the accumulators once more, about
+// 6 us a tile: 8192 x 8192 x 5120 takes 455 us, in one run 377 us.  A bf16
+// result's own rounding (1.7e-3) leaves nothing of that: one run.
+constexpr int WGRAD_RUN = 32;
 
 __device__ __forceinline__ WgradUnit wgrad_unit(const WgradParams& p, int u) {
     WgradUnit t;
@@ -62,6 +73,7 @@ __device__ __forceinline__ WgradUnit wgrad_unit(const WgradParams& p, int u) {
     t.k0 = r / rows * (2 * BN);
     t.n0 = (g * p.group + r % rows) * PM;
     t.halves = t.k0 + BN < p.K ? 2 : 1;
+    t.run = t.part < 0 && p.bf16_out ? t.kb1 - t.kb0 : p.run;
     return t;
 }
 
@@ -161,54 +173,56 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             };
             for (int u = pair; u < p.units && ok; u += npairs) {
                 const WgradUnit t = wgrad_unit(p, u);
-                const int KB = t.kb1 - t.kb0;
-                ok = wait_tempty(0);
-                if (t.halves == 1) {
-                    for (int kb = 0; kb < KB && ok; ++kb) {
-                        ok = wait_full(gk + kb);
+                for (int kb0 = t.kb0; kb0 < t.kb1 && ok; kb0 += t.run) {
+                    const int KB = min(t.run, t.kb1 - kb0);
+                    ok = wait_tempty(0);
+                    if (t.halves == 1) {
+                        for (int kb = 0; kb < KB && ok; ++kb) {
+                            ok = wait_full(gk + kb);
+                            if (!ok) break;
+                            issue(gk + kb, 0, kb == 0);
+                            release(gk + kb);
+                        }
+                        if (ok) publish(0);
+                    } else {
+                        // halves staggered at both ends of the tile: half 0 completes
+                        // (and is drained) under the last half-1 MMAs, and fills while
+                        // the previous tile's half 1 is still drained
+                        const int head = min(WIDE_EDGE, KB);
+                        const int tail0 = max(head, KB - WIDE_EDGE);
+                        for (int kb = 0; kb < head && ok; ++kb) {
+                            ok = wait_full(gk + kb);
+                            if (ok) issue(gk + kb, 0, kb == 0);
+                        }
                         if (!ok) break;
-                        issue(gk + kb, 0, kb == 0);
-                        release(gk + kb);
-                    }
-                    if (ok) publish(0);
-                } else {
-                    // halves staggered at both ends of the tile: half 0 completes
-                    // (and is drained) under the last half-1 MMAs, and fills while
-                    // the previous tile's half 1 is still drained
-                    const int head = min(WIDE_EDGE, KB);
-                    const int tail0 = max(head, KB - WIDE_EDGE);
-                    for (int kb = 0; kb < head && ok; ++kb) {
-                        ok = wait_full(gk + kb);
-                        if (ok) issue(gk + kb, 0, kb == 0);
-                    }
-                    if (!ok) break;
-                    if (head == KB) publish(0);
-                    ok = wait_tempty(1);
-                    if (!ok) break;
-                    for (int kb = 0; kb < head; ++kb) {
-                        issue(gk + kb, 1, kb == 0);
-                        release(gk + kb);
-                    }
-                    for (int kb = head; kb < tail0 && ok; ++kb) {
-                        ok = wait_full(gk + kb);
+                        if (head == KB) publish(0);
+                        ok = wait_tempty(1);
                         if (!ok) break;
-                        issue(gk + kb, 0, false);
-                        issue(gk + kb, 1, false);
-                        release(gk + kb);
+                        for (int kb = 0; kb < head; ++kb) {
+                            issue(gk + kb, 1, kb == 0);
+                            release(gk + kb);
+                        }
+                        for (int kb = head; kb < tail0 && ok; ++kb) {
+                            ok = wait_full(gk + kb);
+                            if (!ok) break;
+                            issue(gk + kb, 0, false);
+                            issue(gk + kb, 1, false);
+                            release(gk + kb);
+                        }
+                        for (int kb = tail0; kb < KB && ok; ++kb) {
+                            ok = wait_full(gk + kb);
+                            if (ok) issue(gk + kb, 0, false);
+                        }
+                        if (!ok) break;
+                        if (head < KB) publish(0);
+                        for (int kb = tail0; kb < KB; ++kb) {
+                            issue(gk + kb, 1, false);
+                            release(gk + kb);
+                        }
+                        publish(1);
                     }
-                    for (int kb = tail0; kb < KB && ok; ++kb) {
-                        ok = wait_full(gk + kb);
-                        if (ok) issue(gk + kb, 0, false);
-                    }
-                    if (!ok) break;
-                    if (head < KB) publish(0);
-                    for (int kb = tail0; kb < KB; ++kb) {
-                        issue(gk + kb, 1, false);
-                        release(gk + kb);
-                    }
-                    publish(1);
+                    gk += static_cast<uint32_t>(KB);
                 }
-                gk += static_cast<uint32_t>(KB);
             }
             if (!ok) raise_abort(sm, p.err);
             umma_commit_pair_mc(sm.drain, 0x1);  // every MMA issued so far has completed
@@ -225,48 +239,53 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const uint32_t tempty = mapa_shared(smem_addr(&sm.tempty[g]), 0);
         const uint32_t bar_box = 1 + 2 * g, bar_vote = 2 + 2 * g;
         uint8_t* box0 = sm.base + SMEM_STG + g * (2 * NBOX_BYTES);
+        StoreRing ring;
         uint32_t phase = 0;
         bool ok = true;
-        StoreRing ring;
         for (int u = pair; u < p.units; u += npairs) {
             const WgradUnit t = wgrad_unit(p, u);
             if (g >= t.halves) continue;
-            const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
-            // every thread of the group takes the same branch (the box barriers need all of them)
-            if (!named_bar_all(bar_vote, EPI_THREADS, ready)) {
-                ok = false;
-                break;
-            }
-            phase ^= 1u;
-            tc_fence_after();
             const bool partial = t.part >= 0;
             const CUtensorMap* out = partial ? &tmPart : &tmDw;
             const int x0 = (partial ? 0 : t.k0) + g * BN;
             const int y0 = (partial ? t.part * PM : t.n0) + rofs;
             const bool bf16_out = !partial && p.bf16_out;
-            const bool add = !partial && p.add;
             const int cols = min(BN, p.K - t.k0 - g * BN);  // columns of dW in this half
-#pragma unroll 1
-            for (int b = 0; b < BN / 32; ++b) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tbase + b * 32, v);
-                tmem_wait_ld();
-                if (b == BN / 32 - 1) {
-                    tc_fence_before();
-                    mbar_arrive_cluster(tempty);
+            for (int kb0 = t.kb0; kb0 < t.kb1 && ok; kb0 += t.run) {
+                const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
+                // every thread of the group takes the same branch (the box barriers need all of them)
+                if (!named_bar_all(bar_vote, EPI_THREADS, ready)) {
+                    ok = false;
+                    break;
                 }
-                if (b * 32 >= cols) continue;  // the whole box lies past dW's last column
-                if (bf16_out) {
-                    uint32_t w[16];
+                phase ^= 1u;
+                tc_fence_after();
+                // a later run adds to what this thread's earlier bulk stores wrote
+                const bool add = kb0 > t.kb0 || (!partial && p.add);
+                if (kb0 > t.kb0 && et == 0) bulk_wait_group<0>();
+#pragma unroll 1
+                for (int b = 0; b < BN / 32; ++b) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tbase + b * 32, v);
+                    tmem_wait_ld();
+                    if (b == BN / 32 - 1) {
+                        tc_fence_before();
+                        mbar_arrive_cluster(tempty);
+                    }
+                    if (b * 32 >= cols) continue;  // the whole box lies past dW's last column
+                    if (bf16_out) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                    narrow_box_store(ring, box0, bar_box, et, r, w, out, x0 + b * 32, y0, false);
-                } else {
-                    narrow_box_store(ring, box0, bar_box, et, r, v, out, x0 + b * 32, y0, add);
-                    narrow_box_store(ring, box0, bar_box, et, r, v + 16, out, x0 + b * 32 + 16, y0, add);
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        narrow_box_store(ring, box0, bar_box, et, r, w, out, x0 + b * 32, y0, false);
+                    } else {
+                        narrow_box_store(ring, box0, bar_box, et, r, v, out, x0 + b * 32, y0, add);
+                        narrow_box_store(ring, box0, bar_box, et, r, v + 16, out, x0 + b * 32 + 16, y0, add);
+                    }
                 }
             }
+            if (!ok) break;
         }
         if (!ok) raise_abort(sm, p.err);
         if (et == 0) bulk_wait_group<0>();
@@ -284,11 +303,11 @@ struct WgradJoinParams {
 };
 
 // Sums the partial tiles' splits in order and writes their part of dW (adding
-// to what is there, in fp32, when asked).  One block per 8 rows of a tile.
+// to what is there, in fp32, when asked).  One block per 2 rows of a tile.
 // After a timeout of the contraction the sums are NaN, so that no incomplete
 // value passes for a result.
 constexpr int WJ_THREADS = 256;
-constexpr int WJ_ROWS = 8;
+constexpr int WJ_ROWS = 2;
 
 __global__ void __launch_bounds__(WJ_THREADS) flp_wgrad_join_kernel(const WgradJoinParams p) {
     const int tile = blockIdx.x / (PM / WJ_ROWS);
@@ -299,15 +318,16 @@ __global__ void __launch_bounds__(WJ_THREADS) flp_wgrad_join_kernel(const WgradJ
     const float* base = p.part + static_cast<long long>(tile) * p.g.splits * (PM * 2 * BN);
     // dW rows are 16-byte (fp32) or 8-byte (bf16) aligned four columns at a time
     const bool vec = p.g.K % 4 == 0;
-#pragma unroll
-    for (int i = 0; i < WJ_ROWS * 2 * BN / 4 / WJ_THREADS; ++i) {
-        const int at = i * WJ_THREADS + threadIdx.x;
-        const int r = r0 + at / (2 * BN / 4), c = at % (2 * BN / 4) * 4;
+    static_assert(WJ_ROWS * 2 * BN / 4 == WJ_THREADS, "four columns a thread");
+    {
+        const int r = r0 + threadIdx.x / (2 * BN / 4), c = threadIdx.x % (2 * BN / 4) * 4;
         const int n = t.n0 + r, k = t.k0 + c;
-        if (n >= p.g.N || k >= p.g.K) continue;
+        if (n >= p.g.N || k >= p.g.K) return;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* at = base + static_cast<long long>(r) * (2 * BN) + c;
+#pragma unroll 8
         for (int j = 0; j < p.g.splits; ++j) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(base + (static_cast<long long>(j) * PM + r) * (2 * BN) + c));
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(at + static_cast<long long>(j) * (PM * 2 * BN)));
             s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
         }
         float v[4] = {s.x, s.y, s.z, s.w};

@@ -504,12 +504,14 @@ def _norm_param(t, cols, dtype, name):
 def _workspace_bytes(fn: str, device: int, *args) -> int:
     n = ctypes.c_size_t(0)
     _check(getattr(load(), fn)(*args, ctypes.byref(n)), fn)
-    return max(16, n.value)
+    return n.value
 
 
 def _scratch(workspace, device, need):
-    """(address, bytes, owner) of the caller's workspace, or of a new one of `need` bytes."""
+    """(address, bytes, owner) of the caller's workspace, or of a new one of `need` bytes (none for 0)."""
     if workspace is None:
+        if need == 0:
+            return None, 0, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         return workspace.data_ptr(), need, workspace
     if not workspace.is_cuda or not workspace.is_contiguous():

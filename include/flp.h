@@ -502,7 +502,7 @@ flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, const void* 
  * pitch ld; mask: bytes [T]; experts: int64 [T, top_k]; loss: one fp32; grad:
  * the logits' type, contiguous [T, E], or NULL; counts: int64 [E].  A NaN or
  * +inf in a live row makes the loss and that row's gradient NaN; what masked
- * rows hold is not looked at.
+ * rows hold is not looked at.  Few rows need no workspace (the query says 0).
  */
 flp_status flp_balance_loss_workspace(int64_t T, int64_t E, size_t* bytes);
 flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype, const uint8_t* mask,

@@ -195,5 +195,6 @@ def test_refusals(flp):
     with pytest.raises(ValueError):
         flp.balance_loss(z, 2, experts=torch.zeros(8, 2, dtype=torch.int32, device="cuda"))
     with pytest.raises(flp.FlpError) as e:
-        flp.balance_loss(z, 2, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        flp.balance_loss(torch.randn(5000, 16, device="cuda"), 2,
+                         workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == flp.FLP_ERR_WORKSPACE
