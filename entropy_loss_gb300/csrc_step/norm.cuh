@@ -255,199 +255,233 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) flp_norm_bwd_kernel(con
 // Arithmetic runs on packed pairs, which halves the instructions that bound
 // these kernels once enough bytes are in flight.
 
-template <typename T, int NV, int S, bool CK, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512) flp_norm_fwd_stream_kernel(const NormFwdParams p) {
+template <typename T, int NV, int S, bool CK, bool WARP, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const NormFwdParams p) {
     constexpr int P = Pairs<T>::N, V = 2 * P;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][16];
     const int group = WARP ? 32 : blockDim.x;
     const int groups = WARP ? blockDim.x / 32 : 1;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const long long first = static_cast<long long>(blockIdx.x) * groups + (WARP ? threadIdx.x >> 5 : 0);
     const long long step = static_cast<long long>(gridDim.x) * groups;
-    const uint32_t slot = smem_addr(ring) + threadIdx.x * 16;
     const uint32_t pitch = blockDim.x * 16;  // from one vector of this thread to its next
-
-    auto fetch = [&](long long row, int stage) {
-        if (row < p.M) {
-            const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16, ring_end = slot0 + S * NV * pitch;
+    const int apart = group * V;             // columns between this thread's vectors
+    bool in[NV];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = (t + k * group) * V;
-                if (col < p.H) cp_async<16>(slot + (stage * NV + k) * pitch, x + col);
-            }
+    for (int k = 0; k < NV; ++k) in[k] = t * V + k * apart < p.H;
+    if (!WARP && threadIdx.x < 32) (&red[0][0])[threadIdx.x] = 0.f;
+
+    const T* ahead = static_cast<const T*>(p.x) + first * p.ldx + t * V;  // of the next row to fetch
+    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = rows_left;
+    auto fetch = [&](uint32_t slot) {
+        if (to_fetch > 0) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) cp_async<16>(slot + k * pitch, ahead + k * apart, in[k]);
         }
+        --to_fetch;
+        ahead += step * p.ldx;
         cp_async_commit();
     };
-    {
-        long long row = first;
+    // columns past the row read as zeros, which nothing overwrites
 #pragma unroll
-        for (int s = 0; s < S; ++s, row += step) fetch(row, s);
-    }
+    for (int k = 0; k < S * NV; ++k)
+        if (!in[k % NV]) st_shared_zero_16(slot0 + k * pitch);
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(slot0 + s * NV * pitch);
     uint64_t w[NV][P], b[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int col = (t + k * group) * V;
-        param_pairs<V>(p.w, p.param_f32, col, col < p.H, 1.f, w[k]);
-        param_pairs<V>(p.b, p.param_f32, col, col < p.H, 0.f, b[k]);
+        param_pairs<V>(p.w, p.param_f32, t * V + k * apart, in[k], 1.f, w[k]);
+        param_pairs<V>(p.b, p.param_f32, t * V + k * apart, in[k], 0.f, b[k]);
     }
-    int stage = 0;
-    for (long long row = first; row < p.M; row += step) {
+    T* y = static_cast<T*>(p.y) + first * p.ldy + t * V;
+    float* mean_at = p.mean ? p.mean + first : nullptr;
+    float* rstd_at = p.rstd ? p.rstd + first : nullptr;
+    const unsigned blocks = static_cast<unsigned>(p.Hp) / CK_BLOCK;
+    uint8_t* q = CK ? p.q + first * p.Hp + t * V : nullptr;
+    uint8_t* scale = CK ? p.scale + first * blocks + static_cast<unsigned>(t * V) / CK_BLOCK : nullptr;
+    const bool leads = (t * V) % CK_BLOCK == 0;  // and so for all of this thread's vectors
+    uint32_t slot = slot0;
+    if constexpr (!WARP) __syncthreads();
+    for (; rows_left > 0; --rows_left) {
         cp_async_wait<S - 1>();
         uint4 raw[NV];
         uint64_t v[NV][P];
         uint64_t acc = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            raw[k] = (t + k * group) * V < p.H ? ld_shared_16(slot + (stage * NV + k) * pitch) : make_uint4(0, 0, 0, 0);
+            raw[k] = ld_shared_16(slot + k * pitch);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 v[k][i] = Pairs<T>::get(raw[k], i);
                 acc = f2_add(acc, v[k][i]);
             }
         }
-        float s[1] = {f2_sum(acc)};
-        group_sum_n<WARP>(s, red[0]);
+        float mean = f2_sum(acc);
+        group_sum<WARP>(mean, red[0]);
         // the sum has taken every value of this stage: its slots are free
-        fetch(row + S * step, stage);
-        if (++stage == S) stage = 0;
-        const float mean = s[0] * p.inv_h;
+        fetch(slot);
+        slot += NV * pitch;
+        if (slot == ring_end) slot = slot0;
+        mean *= p.inv_h;
         const uint64_t minus = f2_splat(-mean);
         acc = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * group) * V;
             if constexpr (CK) {
-                uint32_t q[P / 2];
-                const uint32_t byte = ck_quantise_pairs<T>(raw[k], v[k], q);
-                if (col < p.Hp) {
-                    ck_store_words(p.q + row * p.Hp + col, q);
-                    if ((col % CK_BLOCK) == 0)
-                        p.scale[row * (p.Hp / CK_BLOCK) + col / CK_BLOCK] = static_cast<uint8_t>(byte);
-                }
+                uint32_t w8[P / 2];
+                const uint32_t byte = ck_quantise_pairs<T>(raw[k], v[k], w8);
+                const bool on = t * V + k * apart < p.Hp;
+                ck_store_words(q + k * apart, w8, on);
+                st_global_1(scale + static_cast<unsigned>(k * apart) / CK_BLOCK, byte, on && leads);
             }
-            if (col < p.H) {
+            const uint64_t off = in[k] ? minus : 0;  // zeros past the row stay zeros
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    v[k][i] = f2_add(v[k][i], minus);
-                    acc = f2_fma(v[k][i], v[k][i], acc);
-                }
+            for (int i = 0; i < P; ++i) {
+                v[k][i] = f2_add(v[k][i], off);
+                acc = f2_fma(v[k][i], v[k][i], acc);
             }
         }
-        float c[1] = {f2_sum(acc)};
-        group_sum_n<WARP>(c, red[1]);
-        const float rstd = rsqrtf(fmaf(c[0], p.inv_h, p.eps));
+        float rstd = f2_sum(acc);
+        group_sum<WARP>(rstd, red[1]);
+        rstd = rsqrtf(fmaf(rstd, p.inv_h, p.eps));
         if (t == 0) {
-            if (p.mean) p.mean[row] = mean;
-            if (p.rstd) p.rstd[row] = rstd;
+            if (mean_at) *mean_at = mean;
+            if (rstd_at) *rstd_at = rstd;
         }
+        if (mean_at) mean_at += step;
+        if (rstd_at) rstd_at += step;
         const uint64_t r2 = f2_splat(rstd);
-        T* y = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * group) * V;
-            if (col < p.H) {
-                uint64_t o[P];
+            uint64_t o[P];
 #pragma unroll
-                for (int i = 0; i < P; ++i) o[i] = f2_fma(f2_mul(v[k][i], r2), w[k][i], b[k][i]);
-                Pairs<T>::store(y + col, o);
-            }
+            for (int i = 0; i < P; ++i) o[i] = f2_fma(f2_mul(v[k][i], r2), w[k][i], b[k][i]);
+            Pairs<T>::store(y + k * apart, o, in[k]);
+        }
+        y += step * p.ldy;
+        if constexpr (CK) {
+            q += step * p.Hp;
+            scale += step * blocks;
         }
     }
     cp_async_wait<0>();
 }
 
-template <typename T, int NV, int S, bool CK, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
+template <typename T, int NV, int S, bool CK, bool WARP, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
     constexpr int P = Pairs<T>::N, V = 2 * P;
     constexpr int XB = CK ? V : 16;  // bytes of a vector of x in the ring
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float red[2][2][32];
+    __shared__ __align__(16) float red[2][32];
     const int group = WARP ? 32 : blockDim.x;
     const int groups = WARP ? blockDim.x / 32 : 1;
     const int sub = WARP ? threadIdx.x >> 5 : 0;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const long long first = static_cast<long long>(blockIdx.x) * groups + sub;
     const long long step = static_cast<long long>(gridDim.x) * groups;
-    const uint32_t slot_y = smem_addr(ring) + threadIdx.x * 16;
-    const uint32_t pitch_y = blockDim.x * 16;
-    const uint32_t slot_x = smem_addr(ring) + S * NV * pitch_y + threadIdx.x * XB;
-    const uint32_t pitch_x = blockDim.x * XB;
+    const uint32_t pitch_y = blockDim.x * 16, pitch_x = blockDim.x * XB;
+    const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16, ring_end = slot0 + S * NV * pitch_y;
+    const uint32_t slot_x0 = smem_addr(ring) + S * NV * pitch_y + threadIdx.x * XB;
+    const int apart = group * V;
+    bool in[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) in[k] = t * V + k * apart < p.H;
+    if (!WARP && threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
 
-    auto fetch = [&](long long row, int stage) {
-        if (row < p.M) {
-            const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+    // of the next row to fetch
+    const T* ahead_y = static_cast<const T*>(p.dy) + first * p.lddy + t * V;
+    const T* ahead_x = CK ? nullptr : static_cast<const T*>(p.x) + first * p.ldx + t * V;
+    const uint8_t* ahead_q = CK ? p.q + first * p.Hp + t * V : nullptr;
+    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = rows_left;
+    auto fetch = [&](uint32_t slot, uint32_t slot_x) {
+        if (to_fetch > 0) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = (t + k * group) * V;
-                if (col < p.H) {
-                    cp_async<16>(slot_y + (stage * NV + k) * pitch_y, dy + col);
-                    if constexpr (CK)
-                        cp_async<XB>(slot_x + (stage * NV + k) * pitch_x, p.q + row * p.Hp + col);
-                    else
-                        cp_async<16>(slot_x + (stage * NV + k) * pitch_x, static_cast<const T*>(p.x) + row * p.ldx + col);
-                }
+                cp_async<16>(slot + k * pitch_y, ahead_y + k * apart, in[k]);
+                if constexpr (CK)
+                    cp_async<XB>(slot_x + k * pitch_x, ahead_q + k * apart, in[k]);
+                else
+                    cp_async<16>(slot_x + k * pitch_x, ahead_x + k * apart, in[k]);
             }
         }
+        --to_fetch;
+        ahead_y += step * p.lddy;
+        if constexpr (CK)
+            ahead_q += step * p.Hp;
+        else
+            ahead_x += step * p.ldx;
         cp_async_commit();
     };
-    // what a row needs beside its vectors, one row ahead in registers
-    float mean = 0.f, rstd = 0.f;
-    uint32_t byte[NV] = {};
-    auto fetch_few = [&](long long row) {
-        if (row < p.M) {
-            mean = __ldg(p.mean + row);
-            rstd = __ldg(p.rstd + row);
+    // what a row needs beside its vectors, two rows ahead in registers (a miss takes
+    // longer than a row)
+    struct Few {
+        float mean, rstd;
+        uint32_t byte[CK ? NV : 1];
+    };
+    const float* mean_at = p.mean + first;
+    const float* rstd_at = p.rstd + first;
+    const unsigned blocks = static_cast<unsigned>(p.Hp) / CK_BLOCK;
+    const uint8_t* scale = CK ? p.scale + first * blocks + static_cast<unsigned>(t * V) / CK_BLOCK : nullptr;
+    auto fetch_few = [&](Few& f, bool there) {
+        if (there) {
+            f.mean = __ldg(mean_at);
+            f.rstd = __ldg(rstd_at);
             if constexpr (CK) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int col = (t + k * group) * V;
-                    if (col < p.H) byte[k] = __ldg(p.scale + row * (p.Hp / CK_BLOCK) + col / CK_BLOCK);
-                }
+                for (int k = 0; k < NV; ++k)
+                    if (in[k]) f.byte[k] = __ldg(scale + static_cast<unsigned>(k * apart) / CK_BLOCK);
             }
         }
+        mean_at += step;
+        rstd_at += step;
+        if constexpr (CK) scale += step * blocks;
     };
-    {
-        long long row = first;
+    // columns past the row read as zeros, which nothing overwrites (a checkpoint's
+    // bytes are multiplied by a step of 0 there)
 #pragma unroll
-        for (int s = 0; s < S; ++s, row += step) fetch(row, s);
+    for (int k = 0; k < S * NV; ++k) {
+        if (!in[k % NV]) {
+            st_shared_zero_16(slot0 + k * pitch_y);
+            if constexpr (!CK) st_shared_zero_16(slot_x0 + k * pitch_x);
+        }
     }
-    fetch_few(first);
+#pragma unroll
+    for (int s = 0; s < S; ++s) fetch(slot0 + s * NV * pitch_y, slot_x0 + s * NV * pitch_x);
+    Few even{}, odd{};
+    fetch_few(even, rows_left > 0);
+    fetch_few(odd, rows_left > 1);
     uint64_t w[NV][P], dw[NV][P] = {}, db[NV][P] = {};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int col = (t + k * group) * V;
-        param_pairs<V>(p.w, p.param_f32, col, col < p.H, 1.f, w[k]);
-    }
-    int stage = 0, buf = 0;
-    for (long long row = first; row < p.M; row += step) {
+    for (int k = 0; k < NV; ++k) param_pairs<V>(p.w, p.param_f32, t * V + k * apart, in[k], 1.f, w[k]);
+    T* dx = static_cast<T*>(p.dx) + first * p.lddx + t * V;
+    uint32_t slot = slot0, slot_x = slot_x0;
+    int buf = 0;
+    if constexpr (!WARP) __syncthreads();
+    auto one_row = [&](Few& few) {
         cp_async_wait<S - 1>();
         uint4 ry[NV];
         uint64_t xh[NV][P];
         uint64_t s0 = 0, s1 = 0;
-        const uint64_t minus = f2_splat(-mean), r2 = f2_splat(rstd);
+        const uint64_t minus = f2_splat(-few.mean), r2 = f2_splat(few.rstd);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const bool in = (t + k * group) * V < p.H;
-            ry[k] = in ? ld_shared_16(slot_y + (stage * NV + k) * pitch_y) : make_uint4(0, 0, 0, 0);
-            if (in) {
-                if constexpr (CK) {
-                    uint32_t q[V / 4];
-                    if constexpr (V == 8) {
-                        const uint2 u = ld_shared_8(slot_x + (stage * NV + k) * pitch_x);
-                        q[0] = u.x, q[1] = u.y;
-                    } else {
-                        q[0] = ld_shared_4(slot_x + (stage * NV + k) * pitch_x);
-                    }
-                    ck_pairs<V>(q, ck_step(byte[k]), xh[k]);
+            ry[k] = ld_shared_16(slot + k * pitch_y);
+            if constexpr (CK) {
+                uint32_t q[V / 4];
+                if constexpr (V == 8) {
+                    const uint2 u = ld_shared_8(slot_x + k * pitch_x);
+                    q[0] = u.x, q[1] = u.y;
                 } else {
-                    const uint4 rx = ld_shared_16(slot_x + (stage * NV + k) * pitch_x);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) xh[k][i] = Pairs<T>::get(rx, i);
+                    q[0] = ld_shared_4(slot_x + k * pitch_x);
                 }
+                ck_pairs<V>(q, ck_step(few.byte[k]), xh[k]);
             } else {
+                const uint4 rx = ld_shared_16(slot_x + k * pitch_x);
 #pragma unroll
-                for (int i = 0; i < P; ++i) xh[k][i] = 0;
+                for (int i = 0; i < P; ++i) xh[k][i] = Pairs<T>::get(rx, i);
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -460,27 +494,30 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) flp_norm_bwd_stream_kernel(c
                 s1 = f2_fma(g, xh[k][i], s1);
             }
         }
-        const float r = rstd;
-        fetch_few(row + step);
-        float s[2] = {f2_sum(s0), f2_sum(s1)};
-        group_sum_n<WARP>(s, &red[buf][0][0]);
+        fetch_few(few, rows_left > 2);
+        float m1 = f2_sum(s0), m2 = f2_sum(s1);
+        group_sum2<WARP>(m1, m2, red[buf]);
         buf ^= 1;
         // the sums have taken every value of this stage: its slots are free
-        fetch(row + S * step, stage);
-        if (++stage == S) stage = 0;
-        const uint64_t m1 = f2_splat(-s[0] * p.inv_h), m2 = f2_splat(-s[1] * p.inv_h), rr = f2_splat(r);
-        T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+        fetch(slot, slot_x);
+        slot += NV * pitch_y;
+        slot_x += NV * pitch_x;
+        if (slot == ring_end) slot = slot0, slot_x = slot_x0;
+        const uint64_t n1 = f2_splat(-m1 * p.inv_h), n2 = f2_splat(-m2 * p.inv_h);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * group) * V;
-            if (col < p.H) {
-                uint64_t o[P];
+            uint64_t o[P];
 #pragma unroll
-                for (int i = 0; i < P; ++i)
-                    o[i] = f2_mul(rr, f2_fma(xh[k][i], m2, f2_fma(Pairs<T>::get(ry[k], i), w[k][i], m1)));
-                Pairs<T>::store(dx + col, o);
-            }
+            for (int i = 0; i < P; ++i)
+                o[i] = f2_mul(r2, f2_fma(xh[k][i], n2, f2_fma(Pairs<T>::get(ry[k], i), w[k][i], n1)));
+            Pairs<T>::store(dx + k * apart, o, in[k]);
         }
+        dx += step * p.lddx;
+        --rows_left;
+    };
+    while (rows_left > 0) {
+        one_row(even);
+        if (rows_left > 0) one_row(odd);
     }
     cp_async_wait<0>();
     griddep_launch_dependents();

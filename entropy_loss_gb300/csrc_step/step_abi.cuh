@@ -89,25 +89,37 @@ flp_status norm_shape(int64_t cols, F&& f) {
     return fail(FLP_ERR_UNSUPPORTED, "layer norm rows hold at most 16384 elements");
 }
 
-// Streaming rows: calls f(vectors per thread, stages, row per warp, threads of
-// a block).  16 elements a thread keep a row, its parameters and the column
-// sums in registers; rows of up to 512 elements go to one warp, which needs no
-// block barrier; rows above 8192 take more elements a thread.  The stages put
-// 64 KiB or so per SM in flight in every shape.
-template <typename T, typename F>
+#ifndef FWD_MINB
+#define FWD_MINB 3
+#endif
+#ifndef BWD_MINB
+#define BWD_MINB 2
+#endif
+// Streaming rows: calls f(shape, threads of a block).  16 elements a thread
+// keep a row, its parameters and the column sums in registers; rows of up to
+// 512 elements go to one warp, which needs no block barrier; rows above 8192
+// take more elements a thread.  The stages put 64 KiB or so per SM in flight in
+// every shape, and the blocks per SM that a size must fit bound the registers.
+template <int NV_, int S_, bool WARP_, int MAXT_, int MINB_>
+struct StreamShape {
+    static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;
+    static constexpr bool WARP = WARP_;
+};
+
+template <typename T, int MINB256, typename F>
 flp_status norm_stream_shape(int64_t cols, F&& f) {
     constexpr int V = wide_v<T>(), N2 = 16 / V;  // N2 vectors of V = 16 elements
+    constexpr int S = V == 8 ? 4 : 2;
     const int64_t vecs = cdiv(cols, V);
-    const std::integral_constant<int, 4> s4{};
-    const std::integral_constant<int, 2> s2{};
-    if (vecs <= 32) return f(std::integral_constant<int, 1>{}, s4, std::true_type{}, 256);
-    if (vecs <= 64) return f(std::integral_constant<int, 2>{}, s4, std::true_type{}, 256);
+    if (vecs <= 32) return f(StreamShape<1, 4, true, 256, 1>{}, 256);
+    if (vecs <= 64) return f(StreamShape<2, 4, true, 256, 1>{}, 256);
     if constexpr (V == 4)
-        if (vecs <= 128) return f(std::integral_constant<int, 4>{}, s2, std::true_type{}, 256);
-    if (cols <= 8192)
-        return f(std::integral_constant<int, N2>{}, std::integral_constant<int, V == 8 ? 4 : 2>{}, std::false_type{},
-                 static_cast<int>(cdiv(vecs, 32 * N2) * 32));
-    return f(std::integral_constant<int, 2 * N2>{}, s2, std::false_type{}, static_cast<int>(cdiv(vecs, 64 * N2) * 32));
+        if (vecs <= 128) return f(StreamShape<4, 2, true, 256, 1>{}, 256);
+    const int threads = static_cast<int>(cdiv(vecs, 32 * N2) * 32);
+    if (threads <= 256) return f(StreamShape<N2, S, false, 256, MINB256>{}, threads);
+    if (threads <= 320) return f(StreamShape<N2, S, false, 320, 2>{}, threads);
+    if (threads <= 512) return f(StreamShape<N2, S, false, 512, 1>{}, threads);
+    return f(StreamShape<2 * N2, 2, false, 512, 1>{}, static_cast<int>(cdiv(vecs, 64 * N2) * 32));
 }
 
 flp_status norm_checks(int64_t M, int64_t H, int dtype, int param_dtype, const void* weight, const void* bias) {
@@ -373,10 +385,11 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
         constexpr bool CK = decltype(ck)::value;
         const int64_t cols = CK ? p.Hp : p.H;
         if (wide)
-            return norm_stream_shape<T>(cols, [&](auto nv, auto stages, auto warp, int threads) -> flp_status {
-                constexpr int NV = decltype(nv)::value, S = decltype(stages)::value;
-                constexpr bool WARP = decltype(warp)::value;
-                auto* kernel = flp_norm_fwd_stream_kernel<T, NV, S, CK, WARP>;
+            return norm_stream_shape<T, FWD_MINB>(cols, [&](auto shape, int threads) -> flp_status {
+                using X = decltype(shape);
+                constexpr int NV = X::NV, S = X::S;
+                constexpr bool WARP = X::WARP;
+                auto* kernel = flp_norm_fwd_stream_kernel<T, NV, S, CK, WARP, X::MAXT, X::MINB>;
                 const size_t smem = static_cast<size_t>(S) * NV * threads * 16;
                 int per_sm = 0;
                 const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
@@ -464,10 +477,11 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
             using T = decltype(t);
             constexpr bool CK = decltype(ck)::value;
             if (wide)
-                return norm_stream_shape<T>(p.H, [&](auto nv, auto stages, auto warp, int threads) -> flp_status {
-                    constexpr int NV = decltype(nv)::value, S = decltype(stages)::value;
-                    constexpr bool WARP = decltype(warp)::value;
-                    auto* kernel = flp_norm_bwd_stream_kernel<T, NV, S, CK, WARP>;
+                return norm_stream_shape<T, BWD_MINB>(p.H, [&](auto shape, int threads) -> flp_status {
+                    using X = decltype(shape);
+                    constexpr int NV = X::NV, S = X::S;
+                    constexpr bool WARP = X::WARP;
+                    auto* kernel = flp_norm_bwd_stream_kernel<T, NV, S, CK, WARP, X::MAXT, X::MINB>;
                     const size_t smem = static_cast<size_t>(S) * NV * threads * (16 + (CK ? wide_v<T>() : 16));
                     int per_sm = 0;
                     flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);

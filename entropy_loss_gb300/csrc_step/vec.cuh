@@ -116,13 +116,40 @@ __device__ __forceinline__ void load_param(const void* base, bool f32, int col, 
 // 16 bytes (or 8) of shared memory, so a completed cp.async group is all the
 // synchronisation there is, and the bytes in flight are not limited by registers.
 
+// Accesses with a predicate of their own instead of a branch around them.
 template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on) {
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+                     "l"(src), "r"(static_cast<int>(on))
+                     : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], %2;\n\t}" ::"r"(dst),
+            "l"(src), "n"(BYTES), "r"(static_cast<int>(on))
+            : "memory");
 }
+__device__ __forceinline__ void st_global_16(void* p, uint4 u, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
+                 "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w), "r"(static_cast<int>(on))
+                 : "memory");
+}
+__device__ __forceinline__ void st_global_8(void* p, uint32_t x, uint32_t y, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.global.v2.b32 [%0], {%1, %2};\n\t}" ::"l"(p), "r"(x), "r"(y),
+                 "r"(static_cast<int>(on))
+                 : "memory");
+}
+__device__ __forceinline__ void st_global_4(void* p, uint32_t x, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(p), "r"(x),
+                 "r"(static_cast<int>(on))
+                 : "memory");
+}
+__device__ __forceinline__ void st_global_1(void* p, uint32_t x, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.u8 [%0], %1;\n\t}" ::"l"(p), "r"(x),
+                 "r"(static_cast<int>(on))
+                 : "memory");
+}
+__device__ __forceinline__ void st_shared_zero_16(uint32_t a) { st_shared_v4(a, 0, 0, 0, 0); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -155,7 +182,7 @@ struct Pairs<bf16> {
         const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
         return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    __device__ __forceinline__ static void store(bf16* p, const uint64_t (&v)[4]) {
+    __device__ __forceinline__ static void store(bf16* p, const uint64_t (&v)[4], bool on = true) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -163,7 +190,7 @@ struct Pairs<bf16> {
             f2_unpack(v[i], lo, hi);
             w[i] = pack_bf16x2(lo, hi);
         }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        st_global_16(p, make_uint4(w[0], w[1], w[2], w[3]), on);
     }
 };
 template <>
@@ -173,11 +200,11 @@ struct Pairs<float> {
         return i == 0 ? f2_pack(__uint_as_float(u.x), __uint_as_float(u.y))
                       : f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
     }
-    __device__ __forceinline__ static void store(float* p, const uint64_t (&v)[2]) {
+    __device__ __forceinline__ static void store(float* p, const uint64_t (&v)[2], bool on = true) {
         float4 u;
         f2_unpack(v[0], u.x, u.y);
         f2_unpack(v[1], u.z, u.w);
-        *reinterpret_cast<float4*>(p) = u;
+        st_global_16(p, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z), __float_as_uint(u.w)), on);
     }
 };
 
@@ -236,21 +263,48 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
     }
 }
 
-// The same over a warp (kWarp) or over the whole block, whose size is known at
-// run time.
-template <bool kWarp, int N>
-__device__ __forceinline__ void group_sum_n(float (&v)[N], float* red) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
+// Sums of one or two values over a warp (kWarp) or over the whole block of up to
+// 16 warps, known at run time; every thread gets them.  `red` holds 16 * N
+// floats, zero beyond the block's warps, that no thread still reads (alternate
+// two of them between calls).  Two values halve the shuffles: after the first
+// exchange the lower lanes sum one of them and the upper lanes the other.  The
+// warps' sums are read back four at a time by every thread, which takes less
+// time than another five shuffles.
+__device__ __forceinline__ float sum_red(const float* red, int warps) {
+    uint64_t a = 0;
+#pragma unroll 2
+    for (int w = 0; w < warps; w += 4) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(red + w);
+        a = f2_add(a, f2_add(u.x, u.y));
+    }
+    return f2_sum(a);
+}
+
+template <bool kWarp>
+__device__ __forceinline__ void group_sum(float& v, float* red) {
+    v = warp_sum(v);
     if constexpr (!kWarp) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) red[n * 32 + warp] = v[n];
-        }
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
+        v = sum_red(red, blockDim.x >> 5);
+    }
+}
+
+template <bool kWarp>
+__device__ __forceinline__ void group_sum2(float& v0, float& v1, float* red) {
+    const int lane = threadIdx.x & 31;
+    const bool upper = lane & 16;
+    float r = (upper ? v1 : v0) + __shfl_xor_sync(0xffffffffu, upper ? v0 : v1, 16);
 #pragma unroll
-        for (int n = 0; n < N; ++n) v[n] = warp_sum(lane < warps ? red[n * 32 + lane] : 0.f);
+    for (int o = 8; o; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if constexpr (kWarp) {
+        v0 = __shfl_sync(0xffffffffu, r, 0);
+        v1 = __shfl_sync(0xffffffffu, r, 16);
+    } else {
+        if ((lane & 15) == 0) red[lane + (threadIdx.x >> 5)] = r;
+        __syncthreads();
+        v0 = sum_red(red, blockDim.x >> 5);
+        v1 = sum_red(red + 16, blockDim.x >> 5);
     }
 }
 
@@ -333,6 +387,12 @@ __device__ __forceinline__ uint32_t ck_quantise(const float (&v)[V], uint32_t (&
     return byte;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+}
+
 // The same for a 16-byte vector as loaded (`raw`) and as pairs.  Only a block
 // whose largest value lies within half a step of 128 steps can round to 128, so
 // the clamp runs for those blocks alone (about one in 130 of normal values).
@@ -344,38 +404,34 @@ __device__ __forceinline__ uint32_t ck_quantise_pairs(const uint4& raw, const ui
     if constexpr (V == 8) {
         // bf16 magnitudes compare as 16-bit integers, two per instruction
         constexpr uint32_t mag = 0x7fff7fffu;
-        const uint32_t m = __vmaxu2(__vmaxu2(raw.x & mag, raw.y & mag), __vmaxu2(raw.z & mag, raw.w & mag));
+        const uint32_t m = max_u16x2(max_u16x2(raw.x & mag, raw.y & mag), max_u16x2(raw.z & mag, raw.w & mag));
         top = max(m << 16, m & 0xffff0000u);
     } else {
         top = max(max(raw.x & 0x7fffffffu, raw.y & 0x7fffffffu), max(raw.z & 0x7fffffffu, raw.w & 0x7fffffffu));
     }
 #pragma unroll
     for (int o = 1; o < CK_BLOCK / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t byte = ck_byte(top);
+    uint32_t byte = static_cast<uint32_t>(max(1, static_cast<int>(top >> 23) - 6));
     const float magic = 12582912.f;
-    const uint64_t inv = f2_splat(ck_inverse(byte == CK_NAN ? 1u : byte)), add = f2_splat(magic);
+    const uint64_t inv = f2_splat(ck_inverse(byte)), add = f2_splat(magic);
     float r[V];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) f2_unpack(f2_fma(v[i], inv, add), r[2 * i], r[2 * i + 1]);
-    if ((top & 0x7f0000u) == 0x7f0000u) {
+    const bool bad = top >= 0x7f800000u;
+    if ((top & 0x7f0000u) == 0x7f0000u || bad) {
+        if (bad) byte = CK_NAN;
 #pragma unroll
-        for (int i = 0; i < V; ++i) r[i] = fminf(fmaxf(r[i], magic - 127.f), magic + 127.f);
+        for (int i = 0; i < V; ++i) r[i] = bad ? 0.f : fminf(fmaxf(r[i], magic - 127.f), magic + 127.f);
     }
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
+    for (int i = 0; i < V / 4; ++i)
         w[i] = pack_bytes(__float_as_uint(r[4 * i]), __float_as_uint(r[4 * i + 1]), __float_as_uint(r[4 * i + 2]),
                           __float_as_uint(r[4 * i + 3]));
-        if (byte == CK_NAN) w[i] = 0;
-    }
     return byte;
 }
 
-__device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[2]) {
-    *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-}
-__device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[1]) {
-    *reinterpret_cast<uint32_t*>(q) = w[0];
-}
+__device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[2], bool on) { st_global_8(q, w[0], w[1], on); }
+__device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[1], bool on) { st_global_4(q, w[0], on); }
 
 // Values of a vector's bytes as pairs.
 template <int V>
