@@ -31,7 +31,7 @@ def nvcc_path() -> str:
 
 
 def command(out: str, extra: list[str] | None = None) -> list[str]:
-    return [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
+    return [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "--split-compile=0", "-Xcompiler", "-fPIC",
             "-shared", "-I" + os.path.join(ROOT, "include"), "-o", out,
             os.path.join(PKG, "csrc_step", "libflp.cu")] + (extra or [])
 

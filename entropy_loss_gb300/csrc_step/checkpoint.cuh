@@ -10,10 +10,10 @@ struct CkParams {
     long long ldx;
     uint8_t* q;      // [M, Hp]
     uint8_t* scale;  // [M, Hp / 32]
+    long long M;
     int H, Hp;
-    unsigned per_row;            // vectors of a padded row
+    unsigned per_row;            // vectors of a padded row (loose rows: a multiple of a warp's 32)
     unsigned long long inverse;  // 2^64 / per_row, rounded up: row = hi(vector * inverse)
-    long long total;             // vectors in all
     int* clear;                  // a word that unpack zeroes (NULL: none)
 };
 
@@ -28,75 +28,122 @@ __device__ __forceinline__ long long ck_place(const CkParams& p, long long j, in
     return row;
 }
 
-// V elements per access: 16 bytes (V > 1), or one where rows are not 16-byte
-// aligned or not whole vectors.
-template <typename T, int V>
-__global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams p) {
-    const long long first = static_cast<long long>(blockIdx.x) * (CK_THREADS * CK_PER_THREAD) + threadIdx.x;
-    Raw<T, V> r[CK_PER_THREAD];
+// A thread's vectors.  Loose rows: a warp's 32 vectors are consecutive in one row
+// (lanes past the row's end idle), so that they can move as words.
+template <typename T, bool LOOSE>
+struct CkPlaces {
+    static constexpr int V = wide_v<T>();
     long long row[CK_PER_THREAD];
     int col[CK_PER_THREAD];
+    int valid[CK_PER_THREAD];  // elements of the row from there on; at most 0: nothing of x
+    bool on[CK_PER_THREAD];    // the checkpoint has the vector
+    __device__ __forceinline__ explicit CkPlaces(const CkParams& p) {
+#pragma unroll
+        for (int k = 0; k < CK_PER_THREAD; ++k) {
+            const long long j = static_cast<long long>(blockIdx.x) * (CK_THREADS * CK_PER_THREAD) + k * CK_THREADS + threadIdx.x;
+            row[k] = ck_place<V>(p, j, col[k]);
+            on[k] = row[k] < p.M && col[k] < p.Hp;
+            valid[k] = row[k] < p.M ? p.H - col[k] : -32 * V;
+        }
+    }
+};
+
+template <typename T, bool LOOSE>
+__global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams p) {
+    constexpr int P = Pairs<T>::N, N = LOOSE ? WarpWords<T>::N : 4;
+    __shared__ __align__(16) uint8_t words[LOOSE ? Stage<T, true>::bytes(CK_THREADS) : 16];
+    const CkPlaces<T, LOOSE> at(p);
+    const T* src[CK_PER_THREAD];
+    uint32_t r[CK_PER_THREAD][N];
 #pragma unroll
     for (int k = 0; k < CK_PER_THREAD; ++k) {
-        const long long j = first + k * CK_THREADS;
-        row[k] = ck_place<V>(p, j, col[k]);
-        if (j < p.total && col[k] < p.H)
-            r[k].load(static_cast<const T*>(p.x) + row[k] * p.ldx + col[k]);
-        else
-            r[k].zero();
+        src[k] = static_cast<const T*>(p.x) + at.row[k] * p.ldx + at.col[k];
+        if constexpr (LOOSE) {
+            const Extent all = extent_of<T>(p.x, p.M, p.ldx, p.H);
+            if (at.row[k] > 0 && at.row[k] < p.M - 1 && WarpWords<T>::full(at.valid[k])) {
+                const char* a = WarpWords<T>::lane_word(src[k]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[k][i] = __ldcs(reinterpret_cast<const uint32_t*>(a + 128 * i));
+                if (N == 5) {
+                    r[k][N - 1] = 0;
+                    if ((threadIdx.x & 31) == 0 && (reinterpret_cast<uintptr_t>(src[k]) & 2))
+                        r[k][N - 1] = __ldcs(reinterpret_cast<const uint32_t*>(a + 512));
+                }
+            } else {
+                const WarpWords<T> w(src[k], at.valid[k]);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const char* a = w.word(i);
+                    r[k][i] = 0;
+                    if (w.has(i)) {
+                        if (sizeof(T) == 4 || (a >= all.lo && a + 4 <= all.hi))
+                            r[k][i] = __ldcs(reinterpret_cast<const uint32_t*>(a));
+                        else
+                            r[k][i] = outer_word(a, all);
+                    }
+                }
+            }
+        } else {
+            const uint4 u = at.valid[k] > 0 ? __ldcs(reinterpret_cast<const uint4*>(src[k])) : make_uint4(0, 0, 0, 0);
+            r[k][0] = u.x, r[k][1] = u.y, r[k][2] = u.z, r[k][3] = u.w;
+        }
     }
 #pragma unroll
     for (int k = 0; k < CK_PER_THREAD; ++k) {
-        uint32_t byte;
-        uint32_t w[V > 4 ? 2 : 1];
-        if constexpr (V > 1) {
-            uint64_t v[V / 2];
+        uint4 u = make_uint4(r[k][0], r[k][1], r[k][2], r[k][3]);
+        if constexpr (LOOSE) {
+            const uint32_t base = smem_addr(words) + threadIdx.x / 32 * WARP_WORDS_BYTES, lane = threadIdx.x & 31;
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) v[i] = Pairs<T>::get(r[k].bits(), i);
-            byte = ck_quantise_pairs<T>(r[k].bits(), v, w);
-        } else {
-            float v[V];
-            r[k].to(v);
-            byte = ck_quantise<V>(v, w);
+            for (int i = 0; i < N; ++i)
+                if (i < 4 || lane == 0)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (lane + 32 * i) * 4), "r"(r[k][i]) : "memory");
+            __syncwarp();
+            u = vec_of_words<T>(base, at.valid[k], sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(src[k]) & 2));
+            __syncwarp();
         }
-        if (first + k * CK_THREADS < p.total) {
-            ck_store<V>(p.q + row[k] * p.Hp + col[k], w);
-            if (col[k] % CK_BLOCK == 0) p.scale[row[k] * (p.Hp / CK_BLOCK) + col[k] / CK_BLOCK] = static_cast<uint8_t>(byte);
-        }
+        uint32_t w[P / 2];
+        uint64_t v[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = Pairs<T>::get(u, i);
+        const uint32_t byte = ck_quantise_pairs<T>(u, v, w);
+        ck_store_words(p.q + at.row[k] * p.Hp + at.col[k], w, at.on[k]);
+        st_global_1(p.scale + at.row[k] * (static_cast<unsigned>(p.Hp) / CK_BLOCK) + static_cast<unsigned>(at.col[k]) / CK_BLOCK,
+                    byte, at.on[k] && at.col[k] % CK_BLOCK == 0);
     }
 }
 
-template <typename T, int V>
+template <typename T, bool LOOSE>
 __global__ void __launch_bounds__(CK_THREADS) flp_ck_unpack_kernel(const CkParams p) {
-    const long long first = static_cast<long long>(blockIdx.x) * (CK_THREADS * CK_PER_THREAD) + threadIdx.x;
-    RawCk<V> r[CK_PER_THREAD];
-    long long row[CK_PER_THREAD];
-    int col[CK_PER_THREAD];
+    constexpr int P = Pairs<T>::N, V = 2 * P;
+    __shared__ __align__(16) uint8_t words[LOOSE ? Stage<T, true>::bytes(CK_THREADS) : 16];
+    const uint32_t stage = smem_addr(words) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
+    const CkPlaces<T, LOOSE> at(p);
+    uint32_t w[CK_PER_THREAD][P / 2];
+    uint32_t byte[CK_PER_THREAD];
     griddep_launch_dependents();  // the weight gradient's contraction may set up meanwhile
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0;
 #pragma unroll
     for (int k = 0; k < CK_PER_THREAD; ++k) {
-        const long long j = first + k * CK_THREADS;
-        row[k] = ck_place<V>(p, j, col[k]);
-        if (j < p.total)
-            r[k].load(p.q + row[k] * p.Hp, p.scale + row[k] * (p.Hp / CK_BLOCK), col[k]);
-        else
-            r[k].zero();
+        byte[k] = 0;
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) w[k][i] = 0;
+        if (at.on[k]) {
+            const uint8_t* q = p.q + at.row[k] * p.Hp + at.col[k];
+            if constexpr (V == 8) {
+                const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
+                w[k][0] = u.x, w[k][1] = u.y;
+            } else {
+                w[k][0] = __ldcs(reinterpret_cast<const uint32_t*>(q));
+            }
+            byte[k] = __ldcs(p.scale + at.row[k] * (static_cast<unsigned>(p.Hp) / CK_BLOCK) +
+                             static_cast<unsigned>(at.col[k]) / CK_BLOCK);
+        }
     }
 #pragma unroll
     for (int k = 0; k < CK_PER_THREAD; ++k) {
-        if (first + k * CK_THREADS < p.total && col[k] < p.H) {
-            T* x = static_cast<T*>(p.x) + row[k] * p.ldx + col[k];
-            if constexpr (V > 1) {
-                uint64_t v[V / 2];
-                ck_pairs<V>(r[k].w, ck_step(r[k].byte), v);
-                Pairs<T>::store(x, v);
-            } else {
-                float v[V];
-                r[k].to(v);
-                store_vec<V>(x, v);
-            }
-        }
+        uint64_t v[P];
+        ck_pairs<V>(w[k], ck_step(byte[k]), v);
+        store_row_vec<T, LOOSE>(static_cast<T*>(p.x) + at.row[k] * p.ldx + at.col[k], Pairs<T>::put(v), at.valid[k], stage);
     }
 }
 

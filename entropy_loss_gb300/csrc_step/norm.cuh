@@ -33,82 +33,6 @@ struct NormFwdParams {
     int Hp;
 };
 
-template <int TPR>
-__host__ __device__ constexpr int norm_rows_per_block() { return TPR >= 128 ? 1 : 128 / TPR; }
-
-// One row per TPR threads, held in registers (NV vectors of V elements each).
-template <typename T, int V, int TPR, int NV, bool CK>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) flp_norm_fwd_kernel(const NormFwdParams p) {
-    constexpr int RPB = norm_rows_per_block<TPR>();
-    __shared__ float red[2][32];
-    const long long row = static_cast<long long>(blockIdx.x) * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
-    const int t = RPB > 1 ? threadIdx.x % TPR : threadIdx.x;
-    if (row >= p.M) return;  // a whole warp
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    float v[NV][V];
-    float s[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int col = (t + k * TPR) * V;
-        Raw<T, V> r;
-        if (col < p.H)
-            r.load(x + col);
-        else
-            r.zero();
-        r.to(v[k]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[0] += v[k][i];
-    }
-    row_sum<TPR>(s, red[0]);
-    const float mean = s[0] * p.inv_h;
-    float c[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        if ((t + k * TPR) * V < p.H) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = v[k][i] - mean;
-                c[0] = fmaf(d, d, c[0]);
-            }
-        }
-    }
-    row_sum<TPR>(c, red[1]);
-    const float rstd = rsqrtf(fmaf(c[0], p.inv_h, p.eps));
-    if (t == 0) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    T* y = static_cast<T*>(p.y) + row * p.ldy;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int col = (t + k * TPR) * V;
-        if constexpr (CK) {
-            uint32_t w[V > 4 ? 2 : 1];
-            const uint32_t byte = ck_quantise<V>(v[k], w);
-            if (col < p.Hp) {
-                ck_store<V>(p.q + row * p.Hp + col, w);
-                if ((col % CK_BLOCK) == 0) p.scale[row * (p.Hp / CK_BLOCK) + col / CK_BLOCK] = static_cast<uint8_t>(byte);
-            }
-        }
-        if (col < p.H) {
-            float w[V], b[V], o[V];
-            if (p.w)
-                load_param<V>(p.w, p.param_f32, col, w);
-            else
-#pragma unroll
-                for (int i = 0; i < V; ++i) w[i] = 1.f;
-            if (p.b)
-                load_param<V>(p.b, p.param_f32, col, b);
-            else
-#pragma unroll
-                for (int i = 0; i < V; ++i) b[i] = 0.f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaf((v[k][i] - mean) * rstd, w[i], b[i]);
-            store_vec<V>(y + col, o);
-        }
-    }
-}
-
 struct NormBwdParams {
     const void* dy;
     long long lddy;
@@ -129,172 +53,61 @@ struct NormBwdParams {
     float* part;  // [gridDim.x][2][H] fp32 partial sums of dw and db
 };
 
-// Each block takes rows blockIdx.x, blockIdx.x + gridDim.x, ... (times the rows
-// a block holds) and keeps its columns' share of dw and db in registers; the
-// next row's vectors are loaded before the current row's sums are known.
-template <typename T, int V, int TPR, int NV, bool CK>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) flp_norm_bwd_kernel(const NormBwdParams p) {
-    constexpr int RPB = norm_rows_per_block<TPR>();
-    __shared__ float red[2][2][32];
-    __shared__ float join[RPB > 1 ? RPB * TPR * NV * V : 1];
-    const int sub = RPB > 1 ? threadIdx.x / TPR : 0;
-    const int t = RPB > 1 ? threadIdx.x % TPR : threadIdx.x;
-    const long long step = static_cast<long long>(gridDim.x) * RPB;
-    float dw[NV][V] = {}, db[NV][V] = {};
-    Raw<T, V> rdy[NV], rx[NV];
-    RawCk<V> rq[NV];
-    float mean = 0.f, rstd = 0.f;
-
-    auto fetch = [&](long long row) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * TPR) * V;
-            if (row < p.M && col < p.H) {
-                rdy[k].load(static_cast<const T*>(p.dy) + row * p.lddy + col);
-                if constexpr (CK)
-                    rq[k].load(p.q + row * p.Hp, p.scale + row * (p.Hp / CK_BLOCK), col);
-                else
-                    rx[k].load(static_cast<const T*>(p.x) + row * p.ldx + col);
-            } else {
-                rdy[k].zero();
-                if constexpr (CK)
-                    rq[k].zero();
-                else
-                    rx[k].zero();
-            }
-        }
-        if (row < p.M) {
-            mean = __ldg(p.mean + row);
-            rstd = __ldg(p.rstd + row);
-        }
-    };
-
-    long long row = static_cast<long long>(blockIdx.x) * RPB + sub;
-    fetch(row);
-    int buf = 0;
-    for (; row < p.M; row += step) {
-        float g[NV][V], xh[NV][V];
-        const float r = rstd;
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * TPR) * V;
-            float d[V], w[V];
-            rdy[k].to(d);
-            if constexpr (CK)
-                rq[k].to(xh[k]);
-            else
-                rx[k].to(xh[k]);
-            if (p.w && col < p.H)
-                load_param<V>(p.w, p.param_f32, col, w);
-            else
-#pragma unroll
-                for (int i = 0; i < V; ++i) w[i] = 1.f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                xh[k][i] = (xh[k][i] - mean) * r;
-                dw[k][i] = fmaf(d[i], xh[k][i], dw[k][i]);
-                db[k][i] += d[i];
-                g[k][i] = d[i] * w[i];
-                s[0] += g[k][i];
-                s[1] = fmaf(g[k][i], xh[k][i], s[1]);
-            }
-        }
-        fetch(row + step);
-        row_sum<TPR>(s, &red[buf][0][0]);
-        buf ^= 1;
-        const float m1 = s[0] * p.inv_h, m2 = s[1] * p.inv_h;
-        T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * TPR) * V;
-            if (col < p.H) {
-                float o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = r * (g[k][i] - fmaf(xh[k][i], m2, m1));
-                store_vec<V>(dx + col, o);
-            }
-        }
-    }
-    griddep_launch_dependents();
-    // this block's sums; with several rows per block, the row groups join first
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        float* out = p.part + (static_cast<long long>(blockIdx.x) * 2 + which) * p.H;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * TPR) * V;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float a = which ? db[k][i] : dw[k][i];
-                if constexpr (RPB > 1)
-                    join[sub * (TPR * NV * V) + col + i] = a;
-                else if (col + i < p.H)
-                    out[col + i] = a;
-            }
-        }
-        if constexpr (RPB > 1) {
-            __syncthreads();
-            for (int c = threadIdx.x; c < p.H; c += RPB * TPR) {
-                float a = 0.f;
-#pragma unroll
-                for (int u = 0; u < RPB; ++u) a += join[u * (TPR * NV * V) + c];
-                out[c] = a;
-            }
-            __syncthreads();
-        }
-    }
-}
-
 // ---------------------------------------------------------------- streaming rows
 //
-// Rows of 16-byte vectors.  A group of threads (a warp for short rows, else the
-// block) takes rows group by group through the matrix and holds each in
-// registers, NV vectors a thread; S rows ahead are on their way through shared
-// memory.  The parameters stay in registers from the first row to the last.
-// Arithmetic runs on packed pairs, which halves the instructions that bound
-// these kernels once enough bytes are in flight.
+// A group of threads (a warp for short rows, else the block) takes rows group by
+// group through the matrix and holds each in registers, NV vectors a thread; S
+// rows ahead are on their way through shared memory.  The parameters stay in
+// registers from the first row to the last.  Arithmetic runs on packed pairs,
+// which halves the instructions that bound these kernels once enough bytes are
+// in flight.
 
-template <typename T, int NV, int S, bool CK, bool WARP, int MAXT, int MINB>
+template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const NormFwdParams p) {
+    using X = Stage<T, LOOSE>;
     constexpr int P = Pairs<T>::N, V = 2 * P;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float red[2][16];
+    __shared__ __align__(16) uint8_t out_stage[LOOSE ? Stage<T, true>::bytes(MAXT) : 16];
     const int group = WARP ? 32 : blockDim.x;
     const int groups = WARP ? blockDim.x / 32 : 1;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const long long first = static_cast<long long>(blockIdx.x) * groups + (WARP ? threadIdx.x >> 5 : 0);
     const long long step = static_cast<long long>(gridDim.x) * groups;
-    const uint32_t pitch = blockDim.x * 16;  // from one vector of this thread to its next
-    const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16, ring_end = slot0 + S * NV * pitch;
+    const uint32_t pitch = X::bytes(blockDim.x);  // from one vector to the next
+    const uint32_t slot0 = X::mine(smem_addr(ring)), ring_end = slot0 + S * NV * pitch;
     const int apart = group * V;             // columns between this thread's vectors
-    bool in[NV];
+    int valid[NV];                           // elements of the row from this thread's vectors on
 #pragma unroll
-    for (int k = 0; k < NV; ++k) in[k] = t * V + k * apart < p.H;
+    for (int k = 0; k < NV; ++k) valid[k] = p.H - t * V - k * apart;
     if (!WARP && threadIdx.x < 32) (&red[0][0])[threadIdx.x] = 0.f;
+    const uint32_t stage = smem_addr(out_stage) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
+    const Extent all = extent_of<T>(p.x, p.M, p.ldx, p.H);
 
     const T* ahead = static_cast<const T*>(p.x) + first * p.ldx + t * V;  // of the next row to fetch
-    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = rows_left;
+    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = first;
+    // bf16 rows that start at an odd element (LOOSE), this one and whether it alternates
+    bool odd = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead) & 2);
+    const bool alternates = X::SHIFT && ((step * p.ldx) & 1);
     auto fetch = [&](uint32_t slot) {
-        if (to_fetch > 0) {
+        if (to_fetch < p.M) {
+            const bool edge = to_fetch == 0 || to_fetch == p.M - 1;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) cp_async<16>(slot + k * pitch, ahead + k * apart, in[k]);
+            for (int k = 0; k < NV; ++k) X::fetch(slot + k * pitch, ahead + k * apart, valid[k], edge, all);
         }
-        --to_fetch;
+        to_fetch += step;
         ahead += step * p.ldx;
         cp_async_commit();
     };
-    // columns past the row read as zeros, which nothing overwrites
 #pragma unroll
-    for (int k = 0; k < S * NV; ++k)
-        if (!in[k % NV]) st_shared_zero_16(slot0 + k * pitch);
+    for (int k = 0; k < S * NV; ++k) X::clear(slot0 + k * pitch, valid[k % NV]);
 #pragma unroll
     for (int s = 0; s < S; ++s) fetch(slot0 + s * NV * pitch);
     uint64_t w[NV][P], b[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        param_pairs<V>(p.w, p.param_f32, t * V + k * apart, in[k], 1.f, w[k]);
-        param_pairs<V>(p.b, p.param_f32, t * V + k * apart, in[k], 0.f, b[k]);
+        param_pairs<V, LOOSE>(p.w, p.param_f32, t * V + k * apart, p.H, 1.f, w[k]);
+        param_pairs<V, LOOSE>(p.b, p.param_f32, t * V + k * apart, p.H, 0.f, b[k]);
     }
     T* y = static_cast<T*>(p.y) + first * p.ldy + t * V;
     float* mean_at = p.mean ? p.mean + first : nullptr;
@@ -307,12 +120,13 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
     if constexpr (!WARP) __syncthreads();
     for (; rows_left > 0; --rows_left) {
         cp_async_wait<S - 1>();
+        X::arrived();
         uint4 raw[NV];
         uint64_t v[NV][P];
         uint64_t acc = 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            raw[k] = ld_shared_16(slot + k * pitch);
+            raw[k] = X::read(slot + k * pitch, valid[k], odd);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 v[k][i] = Pairs<T>::get(raw[k], i);
@@ -337,10 +151,13 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
                 ck_store_words(q + k * apart, w8, on);
                 st_global_1(scale + static_cast<unsigned>(k * apart) / CK_BLOCK, byte, on && leads);
             }
-            const uint64_t off = in[k] ? minus : 0;  // zeros past the row stay zeros
+            // zeros past the row stay zeros
+            const uint64_t off = valid[k] > 0 ? minus : 0;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                v[k][i] = f2_add(v[k][i], off);
+                uint64_t o = off;
+                if constexpr (LOOSE) o = 2 * i + 1 < valid[k] ? off : 2 * i < valid[k] ? f2_pack(-mean, 0.f) : 0;
+                v[k][i] = f2_add(v[k][i], o);
                 acc = f2_fma(v[k][i], v[k][i], acc);
             }
         }
@@ -359,9 +176,10 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
             uint64_t o[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) o[i] = f2_fma(f2_mul(v[k][i], r2), w[k][i], b[k][i]);
-            Pairs<T>::store(y + k * apart, o, in[k]);
+            store_row_vec<T, LOOSE>(y + k * apart, Pairs<T>::put(o), valid[k], stage);
         }
         y += step * p.ldy;
+        odd ^= alternates;
         if constexpr (CK) {
             q += step * p.Hp;
             scale += step * blocks;
@@ -370,44 +188,53 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
     cp_async_wait<0>();
 }
 
-template <typename T, int NV, int S, bool CK, bool WARP, int MAXT, int MINB>
+template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
+    using X = Stage<T, LOOSE>;
     constexpr int P = Pairs<T>::N, V = 2 * P;
-    constexpr int XB = CK ? V : 16;  // bytes of a vector of x in the ring
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ __align__(16) float red[2][32];
+    __shared__ __align__(16) uint8_t out_stage[LOOSE ? Stage<T, true>::bytes(MAXT) : 16];
     const int group = WARP ? 32 : blockDim.x;
     const int groups = WARP ? blockDim.x / 32 : 1;
     const int sub = WARP ? threadIdx.x >> 5 : 0;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const long long first = static_cast<long long>(blockIdx.x) * groups + sub;
     const long long step = static_cast<long long>(gridDim.x) * groups;
-    const uint32_t pitch_y = blockDim.x * 16, pitch_x = blockDim.x * XB;
-    const uint32_t slot0 = smem_addr(ring) + threadIdx.x * 16, ring_end = slot0 + S * NV * pitch_y;
-    const uint32_t slot_x0 = smem_addr(ring) + S * NV * pitch_y + threadIdx.x * XB;
+    const uint32_t pitch_y = X::bytes(blockDim.x), pitch_x = CK ? blockDim.x * V : pitch_y;
+    const uint32_t ring_x = smem_addr(ring) + S * NV * pitch_y;
+    const uint32_t slot0 = X::mine(smem_addr(ring)), ring_end = slot0 + S * NV * pitch_y;
+    const uint32_t slot_x0 = CK ? ring_x + threadIdx.x * V : X::mine(ring_x);
     const int apart = group * V;
-    bool in[NV];
+    int valid[NV];  // elements of the row from this thread's vectors on
 #pragma unroll
-    for (int k = 0; k < NV; ++k) in[k] = t * V + k * apart < p.H;
+    for (int k = 0; k < NV; ++k) valid[k] = p.H - t * V - k * apart;
     if (!WARP && threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
+    const uint32_t stage = smem_addr(out_stage) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
+    const Extent all_y = extent_of<T>(p.dy, p.M, p.lddy, p.H), all_x = extent_of<T>(p.x, p.M, p.ldx, p.H);
 
     // of the next row to fetch
     const T* ahead_y = static_cast<const T*>(p.dy) + first * p.lddy + t * V;
     const T* ahead_x = CK ? nullptr : static_cast<const T*>(p.x) + first * p.ldx + t * V;
     const uint8_t* ahead_q = CK ? p.q + first * p.Hp + t * V : nullptr;
-    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = rows_left;
+    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = first;
+    // bf16 rows that start at an odd element (LOOSE), these ones and whether they alternate
+    bool odd_y = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_y) & 2);
+    bool odd_x = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_x) & 2);
+    const bool alternates_y = X::SHIFT && ((step * p.lddy) & 1), alternates_x = X::SHIFT && ((step * p.ldx) & 1);
     auto fetch = [&](uint32_t slot, uint32_t slot_x) {
-        if (to_fetch > 0) {
+        if (to_fetch < p.M) {
+            const bool edge = to_fetch == 0 || to_fetch == p.M - 1;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                cp_async<16>(slot + k * pitch_y, ahead_y + k * apart, in[k]);
+                X::fetch(slot + k * pitch_y, ahead_y + k * apart, valid[k], edge, all_y);
                 if constexpr (CK)
-                    cp_async<XB>(slot_x + k * pitch_x, ahead_q + k * apart, in[k]);
+                    cp_async<V>(slot_x + k * pitch_x, ahead_q + k * apart, valid[k] > 0);
                 else
-                    cp_async<16>(slot_x + k * pitch_x, ahead_x + k * apart, in[k]);
+                    X::fetch(slot_x + k * pitch_x, ahead_x + k * apart, valid[k], edge, all_x);
             }
         }
-        --to_fetch;
+        to_fetch += step;
         ahead_y += step * p.lddy;
         if constexpr (CK)
             ahead_q += step * p.Hp;
@@ -432,43 +259,43 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
             if constexpr (CK) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
-                    if (in[k]) f.byte[k] = __ldg(scale + static_cast<unsigned>(k * apart) / CK_BLOCK);
+                    if (valid[k] > 0) f.byte[k] = __ldg(scale + static_cast<unsigned>(k * apart) / CK_BLOCK);
             }
         }
         mean_at += step;
         rstd_at += step;
         if constexpr (CK) scale += step * blocks;
     };
-    // columns past the row read as zeros, which nothing overwrites (a checkpoint's
-    // bytes are multiplied by a step of 0 there)
+    // columns past the row read as zeros: dY's (so that nothing of what is beside
+    // the row enters a sum), and x's so that no NaN comes of it (a checkpoint's bytes
+    // are multiplied by a step of 0 there, or are its own padding)
 #pragma unroll
     for (int k = 0; k < S * NV; ++k) {
-        if (!in[k % NV]) {
-            st_shared_zero_16(slot0 + k * pitch_y);
-            if constexpr (!CK) st_shared_zero_16(slot_x0 + k * pitch_x);
-        }
+        X::clear(slot0 + k * pitch_y, valid[k % NV]);
+        if constexpr (!CK) X::clear(slot_x0 + k * pitch_x, valid[k % NV]);
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) fetch(slot0 + s * NV * pitch_y, slot_x0 + s * NV * pitch_x);
-    Few even{}, odd{};
+    Few even{}, other{};
     fetch_few(even, rows_left > 0);
-    fetch_few(odd, rows_left > 1);
+    fetch_few(other, rows_left > 1);
     uint64_t w[NV][P], dw[NV][P] = {}, db[NV][P] = {};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) param_pairs<V>(p.w, p.param_f32, t * V + k * apart, in[k], 1.f, w[k]);
+    for (int k = 0; k < NV; ++k) param_pairs<V, LOOSE>(p.w, p.param_f32, t * V + k * apart, p.H, 1.f, w[k]);
     T* dx = static_cast<T*>(p.dx) + first * p.lddx + t * V;
     uint32_t slot = slot0, slot_x = slot_x0;
     int buf = 0;
     if constexpr (!WARP) __syncthreads();
     auto one_row = [&](Few& few) {
         cp_async_wait<S - 1>();
+        X::arrived();
         uint4 ry[NV];
         uint64_t xh[NV][P];
         uint64_t s0 = 0, s1 = 0;
         const uint64_t minus = f2_splat(-few.mean), r2 = f2_splat(few.rstd);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            ry[k] = ld_shared_16(slot + k * pitch_y);
+            ry[k] = X::read(slot + k * pitch_y, valid[k], odd_y);
             if constexpr (CK) {
                 uint32_t q[V / 4];
                 if constexpr (V == 8) {
@@ -479,7 +306,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                 }
                 ck_pairs<V>(q, ck_step(few.byte[k]), xh[k]);
             } else {
-                const uint4 rx = ld_shared_16(slot_x + k * pitch_x);
+                const uint4 rx = X::read(slot_x + k * pitch_x, valid[k], odd_x);
 #pragma unroll
                 for (int i = 0; i < P; ++i) xh[k][i] = Pairs<T>::get(rx, i);
             }
@@ -510,14 +337,16 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 o[i] = f2_mul(r2, f2_fma(xh[k][i], n2, f2_fma(Pairs<T>::get(ry[k], i), w[k][i], n1)));
-            Pairs<T>::store(dx + k * apart, o, in[k]);
+            store_row_vec<T, LOOSE>(dx + k * apart, Pairs<T>::put(o), valid[k], stage);
         }
         dx += step * p.lddx;
+        odd_y ^= alternates_y;
+        odd_x ^= alternates_x;
         --rows_left;
     };
     while (rows_left > 0) {
         one_row(even);
-        if (rows_left > 0) one_row(odd);
+        if (rows_left > 0) one_row(other);
     }
     cp_async_wait<0>();
     griddep_launch_dependents();
@@ -529,16 +358,17 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
         if constexpr (WARP) __syncthreads();
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int col = (t + k * group) * V;
-            if (col < p.H) {
+            const int col = t * V + k * apart;
+            float* at = WARP ? join + sub * (NV * 32 * V) + col : out + col;
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    float2 a;
-                    f2_unpack(which ? db[k][i] : dw[k][i], a.x, a.y);
-                    if constexpr (WARP)
-                        *reinterpret_cast<float2*>(join + sub * (NV * 32 * V) + col + 2 * i) = a;
-                    else
-                        *reinterpret_cast<float2*>(out + col + 2 * i) = a;
+            for (int i = 0; i < P; ++i) {
+                float2 a;
+                f2_unpack(which ? db[k][i] : dw[k][i], a.x, a.y);
+                if (!LOOSE || WARP) {
+                    if (WARP || valid[k] > 0) *reinterpret_cast<float2*>(at + 2 * i) = a;
+                } else {
+                    if (2 * i < valid[k]) at[2 * i] = a.x;
+                    if (2 * i + 1 < valid[k]) at[2 * i + 1] = a.y;
                 }
             }
         }

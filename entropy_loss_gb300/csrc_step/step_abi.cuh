@@ -75,38 +75,20 @@ flp_status resident_blocks(const void* kernel, int threads, size_t smem, int* pe
     return FLP_OK;
 }
 
-// Single-element access (rows that are not 16-byte aligned or not whole
-// vectors): calls f(threads per row, elements per thread).
-template <typename F>
-flp_status norm_shape(int64_t cols, F&& f) {
-#define FLP_SHAPE(TPR, NV) \
-    if (cols <= (TPR) * (NV)) return f(std::integral_constant<int, TPR>{}, std::integral_constant<int, NV>{});
-    FLP_SHAPE(32, 8)
-    FLP_SHAPE(128, 8)
-    FLP_SHAPE(256, 16)
-    FLP_SHAPE(1024, 16)
-#undef FLP_SHAPE
-    return fail(FLP_ERR_UNSUPPORTED, "layer norm rows hold at most 16384 elements");
-}
-
-#ifndef FWD_MINB
-#define FWD_MINB 3
-#endif
-#ifndef BWD_MINB
-#define BWD_MINB 2
-#endif
 // Streaming rows: calls f(shape, threads of a block).  16 elements a thread
 // keep a row, its parameters and the column sums in registers; rows of up to
 // 512 elements go to one warp, which needs no block barrier; rows above 8192
 // take more elements a thread.  The stages put 64 KiB or so per SM in flight in
-// every shape, and the blocks per SM that a size must fit bound the registers.
+// every shape.  MINB blocks of up to 256 threads must fit an SM, which bounds the
+// registers: 3 for the forward (32768 x 4096 bf16 with a checkpoint: 111 us, with
+// 2 blocks 124), 2 where more would spill (the backward; loose rows).
 template <int NV_, int S_, bool WARP_, int MAXT_, int MINB_>
 struct StreamShape {
     static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;
     static constexpr bool WARP = WARP_;
 };
 
-template <typename T, int MINB256, typename F>
+template <typename T, int MINB, typename F>
 flp_status norm_stream_shape(int64_t cols, F&& f) {
     constexpr int V = wide_v<T>(), N2 = 16 / V;  // N2 vectors of V = 16 elements
     constexpr int S = V == 8 ? 4 : 2;
@@ -116,7 +98,7 @@ flp_status norm_stream_shape(int64_t cols, F&& f) {
     if constexpr (V == 4)
         if (vecs <= 128) return f(StreamShape<4, 2, true, 256, 1>{}, 256);
     const int threads = static_cast<int>(cdiv(vecs, 32 * N2) * 32);
-    if (threads <= 256) return f(StreamShape<N2, S, false, 256, MINB256>{}, threads);
+    if (threads <= 256) return f(StreamShape<N2, S, false, 256, MINB>{}, threads);
     if (threads <= 320) return f(StreamShape<N2, S, false, 320, 2>{}, threads);
     if (threads <= 512) return f(StreamShape<N2, S, false, 512, 1>{}, threads);
     return f(StreamShape<2 * N2, 2, false, 512, 1>{}, static_cast<int>(cdiv(vecs, 64 * N2) * 32));
@@ -229,31 +211,28 @@ flp_status wgrad_attrs() {
     return FLP_OK;
 }
 
-template <int V, typename T>
-CkParams ck_params(void* x, int64_t ldx, const void* q, const void* scale, int64_t M, int64_t H) {
+template <typename T, bool LOOSE>
+flp_status ck_launch(bool pack, void* x, int64_t ldx, const void* q, const void* scale, int64_t M, int64_t H,
+                     cudaStream_t s, int* clear = nullptr) {
+    constexpr int V = wide_v<T>();
     CkParams p{};
     p.x = x;
     p.ldx = ldx;
     p.q = static_cast<uint8_t*>(const_cast<void*>(q));
     p.scale = static_cast<uint8_t*>(const_cast<void*>(scale));
+    p.M = M;
     p.H = static_cast<int>(H);
     p.Hp = static_cast<int>(ck_cols(H));
-    p.per_row = static_cast<unsigned>(p.Hp / V);
+    p.per_row = static_cast<unsigned>(LOOSE ? cdiv(p.Hp / V, 32) * 32 : p.Hp / V);
     p.inverse = ~0ull / p.per_row + 1;
-    p.total = M * p.per_row;
-    return p;
-}
-
-template <typename T, int V>
-flp_status ck_launch(bool pack, void* x, int64_t ldx, const void* q, const void* scale, int64_t M, int64_t H,
-                     cudaStream_t s, int* clear = nullptr) {
-    CkParams p = ck_params<V, T>(x, ldx, q, scale, M, H);
     p.clear = clear;
-    const int64_t grid = cdiv(p.total, CK_THREADS * CK_PER_THREAD);
+    const int64_t total = M * p.per_row, grid = cdiv(total, CK_THREADS * CK_PER_THREAD);
     // the row of a vector comes exactly from one multiplication while vectors x vectors per row < 2^64
-    if (grid > INT32_MAX || static_cast<double>(p.total + (1 << 20)) * p.per_row > 1.8e19) return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
-    return pack ? launch_step(flp_ck_pack_kernel<T, V>, grid, CK_THREADS, 0, s, "flp_ck_pack_kernel launch", false, p)
-                : launch_step(flp_ck_unpack_kernel<T, V>, grid, CK_THREADS, 0, s, "flp_ck_unpack_kernel launch", false, p);
+    if (grid > INT32_MAX || static_cast<double>(total + (1 << 20)) * p.per_row > 1.8e19)
+        return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
+    return pack ? launch_step(flp_ck_pack_kernel<T, LOOSE>, grid, CK_THREADS, 0, s, "flp_ck_pack_kernel launch", false, p)
+                : launch_step(flp_ck_unpack_kernel<T, LOOSE>, grid, CK_THREADS, 0, s, "flp_ck_unpack_kernel launch",
+                              false, p);
 }
 
 flp_status ck_run(bool pack, const void* x, int64_t ldx, int dtype, const void* q, const void* scale, int64_t M,
@@ -269,11 +248,13 @@ flp_status ck_run(bool pack, const void* x, int64_t ldx, int dtype, const void* 
     if (st == FLP_OK) st = check_on_current_device(x, "X");
     if (st != FLP_OK) return st;
     void* xx = const_cast<void*>(x);
-    if (dtype == FLP_BF16)
-        return rows16(x, ldx, dtype) && H % 8 == 0 ? ck_launch<bf16, 8>(pack, xx, ldx, q, scale, M, H, s)
-                                                   : ck_launch<bf16, 1>(pack, xx, ldx, q, scale, M, H, s);
-    return rows16(x, ldx, dtype) && H % 4 == 0 ? ck_launch<float, 4>(pack, xx, ldx, q, scale, M, H, s)
-                                               : ck_launch<float, 1>(pack, xx, ldx, q, scale, M, H, s);
+    const bool loose = !(rows16(x, ldx, dtype) && (H * elem(dtype)) % 16 == 0);
+    auto typed = [&](auto t) {
+        using T = decltype(t);
+        return loose ? ck_launch<T, true>(pack, xx, ldx, q, scale, M, H, s)
+                     : ck_launch<T, false>(pack, xx, ldx, q, scale, M, H, s);
+    };
+    return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
 }
 
 // ----------------------------------------------------------------- balance loss
@@ -378,34 +359,25 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
     p.scale = static_cast<uint8_t*>(scale);
     p.Hp = static_cast<int>(ck_cols(H));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool wide = rows16(X, ldx, dtype) && rows16(Y, ldy, dtype) && aligned16(weight) && aligned16(bias) &&
-                      (H * elem(dtype)) % 16 == 0;
-    auto run = [&](auto t, auto ck) -> flp_status {
+    const bool loose = !(rows16(X, ldx, dtype) && rows16(Y, ldy, dtype) && aligned16(weight) && aligned16(bias) &&
+                         (H * elem(dtype)) % 16 == 0);
+    auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
         using T = decltype(t);
-        constexpr bool CK = decltype(ck)::value;
-        const int64_t cols = CK ? p.Hp : p.H;
-        if (wide)
-            return norm_stream_shape<T, FWD_MINB>(cols, [&](auto shape, int threads) -> flp_status {
-                using X = decltype(shape);
-                constexpr int NV = X::NV, S = X::S;
-                constexpr bool WARP = X::WARP;
-                auto* kernel = flp_norm_fwd_stream_kernel<T, NV, S, CK, WARP, X::MAXT, X::MINB>;
-                const size_t smem = static_cast<size_t>(S) * NV * threads * 16;
-                int per_sm = 0;
-                const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
-                if (r != FLP_OK) return r;
-                const int64_t rows = WARP ? threads / 32 : 1;
-                return launch_step(kernel, std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count),
-                                   threads, smem, s, "flp_norm_fwd_stream_kernel launch", false, p);
-            });
-        return norm_shape(cols, [&](auto tpr, auto nv) {
-            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-            constexpr int RPB = norm_rows_per_block<TPR>();
-            return launch_step(flp_norm_fwd_kernel<T, 1, TPR, NV, CK>, cdiv(M, RPB), TPR * RPB, 0, s,
-                               "flp_norm_fwd_kernel launch", false, p);
+        constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
+        return norm_stream_shape<T, LOOSE ? 2 : 3>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
+            using X = decltype(shape);
+            auto* kernel = flp_norm_fwd_stream_kernel<T, X::NV, X::S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
+            const size_t smem = static_cast<size_t>(X::S) * X::NV * Stage<T, LOOSE>::bytes(threads);
+            int per_sm = 0;
+            const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+            if (r != FLP_OK) return r;
+            const int64_t rows = X::WARP ? threads / 32 : 1;
+            return launch_step(kernel, std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count),
+                               threads, smem, s, "flp_norm_fwd_stream_kernel launch", false, p);
         });
     };
-    auto typed = [&](auto t) { return q ? run(t, std::true_type{}) : run(t, std::false_type{}); };
+    auto aligned = [&](auto t, auto ck) { return loose ? run(t, ck, std::true_type{}) : run(t, ck, std::false_type{}); };
+    auto typed = [&](auto t) { return q ? aligned(t, std::true_type{}) : aligned(t, std::false_type{}); };
     return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
 }
 
@@ -463,46 +435,30 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
         p.dx = dX;
         p.lddx = lddx;
         p.part = static_cast<float*>(workspace);
-        // two stages of an fp32 row above 8192 elements, dY and X, do not fit
-        // shared memory: such rows go element by element
-        const bool wide = rows16(dY, lddy, dtype) && rows16(dX, lddx, dtype) && aligned16(weight) &&
-                          (!X || rows16(X, ldx, dtype)) && (H * elem(dtype)) % 16 == 0 &&
-                          (dtype == FLP_BF16 || H <= 8192);
-        auto fits = [&]() {
-            return workspace_bytes >= static_cast<size_t>(blocks) * 2 * H * 4
-                       ? FLP_OK
-                       : fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
-        };
-        auto run = [&](auto t, auto ck) -> flp_status {
+        const bool loose = !(rows16(dY, lddy, dtype) && rows16(dX, lddx, dtype) && aligned16(weight) &&
+                             (!X || rows16(X, ldx, dtype)) && (H * elem(dtype)) % 16 == 0);
+        auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
             using T = decltype(t);
-            constexpr bool CK = decltype(ck)::value;
-            if (wide)
-                return norm_stream_shape<T, BWD_MINB>(p.H, [&](auto shape, int threads) -> flp_status {
-                    using X = decltype(shape);
-                    constexpr int NV = X::NV, S = X::S;
-                    constexpr bool WARP = X::WARP;
-                    auto* kernel = flp_norm_bwd_stream_kernel<T, NV, S, CK, WARP, X::MAXT, X::MINB>;
-                    const size_t smem = static_cast<size_t>(S) * NV * threads * (16 + (CK ? wide_v<T>() : 16));
-                    int per_sm = 0;
-                    flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
-                    if (r != FLP_OK) return r;
-                    blocks = norm_bwd_blocks(M, WARP ? threads / 32 : 1, d->sm_count,
-                                             std::min<int64_t>(kNormBwdBlocksPerSm, per_sm));
-                    if ((r = fits()) != FLP_OK) return r;
-                    return launch_step(kernel, blocks, threads, smem, s, "flp_norm_bwd_stream_kernel launch", false, p);
-                });
-            return norm_shape(p.H, [&](auto tpr, auto nv) -> flp_status {
-                constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-                constexpr int RPB = norm_rows_per_block<TPR>();
-                constexpr int threads = TPR * RPB;
-                blocks = norm_bwd_blocks(M, RPB, d->sm_count, std::max(1, std::min<int>(kNormBwdBlocksPerSm, 512 / threads)));
-                const flp_status r = fits();
+            constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
+            return norm_stream_shape<T, 2>(p.H, [&](auto shape, int threads) -> flp_status {
+                using X_ = decltype(shape);
+                // two stages of an fp32 row above 8192 elements, dY and X, do not fit shared memory
+                constexpr int S = sizeof(T) == 4 && X_::NV == 8 ? 1 : X_::S;
+                auto* kernel = flp_norm_bwd_stream_kernel<T, X_::NV, S, CK, LOOSE, X_::WARP, X_::MAXT, X_::MINB>;
+                const int yb = Stage<T, LOOSE>::bytes(threads), xb = CK ? threads * wide_v<T>() : yb;
+                const size_t smem = static_cast<size_t>(S) * X_::NV * (yb + xb);
+                int per_sm = 0;
+                const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
                 if (r != FLP_OK) return r;
-                return launch_step(flp_norm_bwd_kernel<T, 1, TPR, NV, CK>, blocks, threads, 0, s,
-                                   "flp_norm_bwd_kernel launch", false, p);
+                blocks = norm_bwd_blocks(M, X_::WARP ? threads / 32 : 1, d->sm_count,
+                                         std::min<int64_t>(kNormBwdBlocksPerSm, per_sm));
+                if (workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
+                    return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
+                return launch_step(kernel, blocks, threads, smem, s, "flp_norm_bwd_stream_kernel launch", false, p);
             });
         };
-        auto typed = [&](auto t) { return q ? run(t, std::true_type{}) : run(t, std::false_type{}); };
+        auto aligned = [&](auto t, auto ck) { return loose ? run(t, ck, std::true_type{}) : run(t, ck, std::false_type{}); };
+        auto typed = [&](auto t) { return q ? aligned(t, std::true_type{}) : aligned(t, std::false_type{}); };
         st = dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
         if (st != FLP_OK) return st;
     }
@@ -567,7 +523,7 @@ extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, c
     if ((st = check_on_current_device(dY, "dY")) != FLP_OK) return st;
     // the pads of the checkpoint's last blocks are unpacked with the rest (they
     // hold zeros); the same kernel clears the error word
-    st = ck_launch<bf16, 8>(false, ws + w.off_x, w.Kp, q, scale, M, w.Kp, s, reinterpret_cast<int*>(ws));
+    st = ck_launch<bf16, false>(false, ws + w.off_x, w.Kp, q, scale, M, w.Kp, s, reinterpret_cast<int*>(ws));
     if (st != FLP_OK) return st;
     const void* y = dY;
     int64_t ldy = lddy;

@@ -1,5 +1,6 @@
-// vec.cuh - what the training-step kernels share: typed vector access, warp
-// and row reductions, and the 8-bit checkpoint's block arithmetic.
+// vec.cuh - what the training-step kernels share: rows as 16-byte vectors (for
+// aligned rows and for any others), row reductions, and the 8-bit checkpoint's
+// block arithmetic.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -8,113 +9,92 @@ namespace flp {
 
 using bf16 = __nv_bfloat16;
 
-// Elements per access: 16 bytes where rows are 16-byte aligned and hold a
-// whole number of such vectors, else one element.
+// Elements of a 16-byte vector.
 template <typename T>
 __host__ __device__ constexpr int wide_v() { return 16 / static_cast<int>(sizeof(T)); }
 
-// V elements as loaded, and their values in fp32.
-template <typename T, int V>
-struct Raw;
+// --------------------------------------------------------------- packed pairs
+
+__device__ __forceinline__ uint64_t f2_splat(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
+}
+
+// A vector as packed fp32 pairs (two lanes per instruction), and pairs rounded
+// once to a vector (nearest, ties to even).
+template <typename T>
+struct Pairs;
 template <>
-struct Raw<bf16, 8> {
-    uint4 u;
-    __device__ __forceinline__ void load(const bf16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void load_kept(const bf16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ uint4 bits() const { return u; }
-    __device__ __forceinline__ void to(float (&v)[8]) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Pairs<bf16> {
+    static constexpr int N = 4;  // pairs of a vector
+    __device__ __forceinline__ static uint64_t get(const uint4& u, int i) {
+        const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+        return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ static uint4 put(const uint64_t (&v)[4]) {
+        uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            float lo, hi;
+            f2_unpack(v[i], lo, hi);
+            w[i] = pack_bf16x2(lo, hi);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 template <>
-struct Raw<float, 4> {
-    float4 u;
-    __device__ __forceinline__ void load(const float* p) { u = __ldcs(reinterpret_cast<const float4*>(p)); }
-    __device__ __forceinline__ void load_kept(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
-    __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ uint4 bits() const {
-        return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z), __float_as_uint(u.w));
+struct Pairs<float> {
+    static constexpr int N = 2;
+    __device__ __forceinline__ static uint64_t get(const uint4& u, int i) {
+        return i == 0 ? f2_pack(__uint_as_float(u.x), __uint_as_float(u.y))
+                      : f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
     }
-    __device__ __forceinline__ void to(float (&v)[4]) const {
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    __device__ __forceinline__ static uint4 put(const uint64_t (&v)[2]) {
+        float a, b, c, d;
+        f2_unpack(v[0], a, b);
+        f2_unpack(v[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
     }
-};
-template <>
-struct Raw<bf16, 1> {
-    unsigned short u;
-    __device__ __forceinline__ void load(const bf16* p) { u = __ldcs(reinterpret_cast<const unsigned short*>(p)); }
-    __device__ __forceinline__ void load_kept(const bf16* p) { u = __ldg(reinterpret_cast<const unsigned short*>(p)); }
-    __device__ __forceinline__ void zero() { u = 0; }
-    __device__ __forceinline__ void to(float (&v)[1]) const { v[0] = __uint_as_float(static_cast<uint32_t>(u) << 16); }
-};
-template <>
-struct Raw<float, 1> {
-    float u;
-    __device__ __forceinline__ void load(const float* p) { u = __ldcs(p); }
-    __device__ __forceinline__ void load_kept(const float* p) { u = __ldg(p); }
-    __device__ __forceinline__ void zero() { u = 0.f; }
-    __device__ __forceinline__ void to(float (&v)[1]) const { v[0] = u; }
 };
 
-// Stores V values at p, rounded once to T (nearest, ties to even).
-template <int V>
-__device__ __forceinline__ void store_vec(bf16* p, const float (&v)[V]) {
-    if constexpr (V == 8)
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    else
-        *p = __float2bfloat16_rn(v[0]);
-}
-template <int V>
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
-    if constexpr (V == 4)
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-        *p = v[0];
-}
-
-// Parameters (norm weight and bias): V values of either type, kept in cache.
-template <int V>
-__device__ __forceinline__ void load_param(const void* base, bool f32, int col, float (&v)[V]) {
-    if (f32) {
-        const float* p = static_cast<const float*>(base) + col;
-        if constexpr (V % 4 == 0) {
+// V parameter values (norm weight or bias, of either type) from `col` on as
+// pairs, `none` where there are none.
+template <int V, bool LOOSE>
+__device__ __forceinline__ void param_pairs(const void* base, bool f32, int col, int cols, float none,
+                                            uint64_t (&v)[V / 2]) {
+    float w[V];
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
-                v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+    for (int i = 0; i < V; ++i) w[i] = none;
+    if (base && col < cols) {
+        if constexpr (LOOSE) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (col + i < cols)
+                    w[i] = f32 ? __ldg(static_cast<const float*>(base) + col + i)
+                               : __bfloat162float(static_cast<const bf16*>(base)[col + i]);
+            }
+        } else if (f32) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + col + i));
+                w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
             }
         } else {
-            v[0] = __ldg(p);
-        }
-    } else {
-        const unsigned short* p = static_cast<const unsigned short*>(base) + col;
-        uint32_t w[(V + 1) / 2];
-        if constexpr (V == 8) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        } else if constexpr (V == 4) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-            w[0] = u.x, w[1] = u.y;
-        } else {
-            w[0] = __ldg(p);
-        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+            for (int i = 0; i < V; i += 4) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(base) + col + i));
+                w[i] = __uint_as_float(u.x << 16), w[i + 1] = __uint_as_float(u.x & 0xffff0000u);
+                w[i + 2] = __uint_as_float(u.y << 16), w[i + 3] = __uint_as_float(u.y & 0xffff0000u);
+            }
+        }
     }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = f2_pack(w[2 * i], w[2 * i + 1]);
 }
 
-// ------------------------------------------- vectors on their way through smem
-//
-// A thread copies ahead the vectors that it will itself read, each into its own
-// 16 bytes (or 8) of shared memory, so a completed cp.async group is all the
-// synchronisation there is, and the bytes in flight are not limited by registers.
+// ------------------------------------------------------------------- accesses
 
 // Accesses with a predicate of their own instead of a branch around them.
 template <int BYTES>
@@ -128,6 +108,11 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on)
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], %2;\n\t}" ::"r"(dst),
             "l"(src), "n"(BYTES), "r"(static_cast<int>(on))
             : "memory");
+}
+// 4 bytes from src + OFF to dst + OFF.
+template <int OFF>
+__device__ __forceinline__ void cp_async_4_at(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %2], 4;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
 }
 __device__ __forceinline__ void st_global_16(void* p, uint4 u, bool on) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
@@ -172,95 +157,205 @@ __device__ __forceinline__ uint32_t ld_shared_4(uint32_t a) {
     return u;
 }
 
-// A 16-byte vector as packed fp32 pairs (two lanes per instruction).
+// ------------------------------------------- vectors on their way through smem
+//
+// Rows S ahead are copied into shared memory, so that the bytes in flight are not
+// limited by registers.  Aligned rows (16-byte base and pitch, whole vectors) move
+// 16 bytes at a time, and a thread copies exactly the vectors that it will itself
+// read: its completed cp.async group is all the synchronisation there is.
+//
+// Loose rows (any others) move 4-byte words: a warp copies the words that hold its
+// 32 consecutive vectors, lane by lane, which coalesces at any address, and reads
+// vectors from them after a warp barrier.  A bf16 row may start at an odd element;
+// then the vectors straddle words and are shifted out (one word more).
+
+// First and one past the last byte of a matrix: no word that reaches out of it is
+// accessed; its one element inside is then accessed alone.
+struct Extent {
+    const char* lo;
+    const char* hi;
+};
+
 template <typename T>
-struct Pairs;
-template <>
-struct Pairs<bf16> {
-    static constexpr int N = 4;  // pairs of a vector
-    __device__ __forceinline__ static uint64_t get(const uint4& u, int i) {
-        const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
-        return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+__device__ __forceinline__ Extent extent_of(const void* base, long long rows, long long pitch, int cols) {
+    const char* b = static_cast<const char*>(base);
+    return {b, b + ((rows - 1) * pitch + cols) * static_cast<long long>(sizeof(T))};
+}
+
+// A warp's 32 consecutive vectors in a loose row: lane `lane` holds words lane,
+// lane + 32, ... from the first word on, the last of them (i = 4) lane 0 alone.
+template <typename T>
+struct WarpWords {
+    static constexpr int V = wide_v<T>();
+    static constexpr int N = sizeof(T) == 2 ? 5 : 4;  // words per lane
+    const char* first;
+    int bytes;  // from the first word to the end of what the row holds of the vectors
+    // `src`: this lane's vector, of which and beyond the row holds `valid` elements
+    __device__ __forceinline__ WarpWords(const T* src, int valid) {
+        const int lane = threadIdx.x & 31;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(src - lane * V);
+        const int lead = static_cast<int>(at & (4 - sizeof(T)));
+        first = reinterpret_cast<const char*>(at) - lead;
+        const int left = min(32 * V, valid + lane * V);
+        bytes = left > 0 ? lead + left * static_cast<int>(sizeof(T)) : 0;
     }
-    __device__ __forceinline__ static void store(bf16* p, const uint64_t (&v)[4], bool on = true) {
-        uint32_t w[4];
+    // whether the row holds all of the warp's 32 vectors
+    __device__ __forceinline__ static bool full(int valid) { return valid >= (32 - static_cast<int>(threadIdx.x & 31)) * V; }
+    // this lane's first word
+    __device__ __forceinline__ static const char* lane_word(const T* src) {
+        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(src) & ~static_cast<uintptr_t>(3)) -
+               12 * (threadIdx.x & 31);
+    }
+    __device__ __forceinline__ bool has(int i) const {
+        const int lane = threadIdx.x & 31;
+        return 4 * (lane + 32 * i) < bytes && (i < 4 || lane == 0);
+    }
+    __device__ __forceinline__ const char* word(int i) const { return first + 4 * ((threadIdx.x & 31) + 32 * i); }
+};
+
+// The one element inside the matrix of a bf16 word that reaches out of it, in its place.
+__device__ __forceinline__ uint32_t outer_word(const char* w, const Extent& all) {
+    const int half = w < all.lo ? 2 : 0;
+    return static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(w + half)) << (8 * half);
+}
+
+// This lane's vector from the warp's words at `base` (`odd`: the first
+// word starts with an element that is not the warp's); elements past `valid` zero.
+template <typename T>
+__device__ __forceinline__ uint4 vec_of_words(uint32_t base, int valid, bool odd) {
+    const uint32_t at = base + (threadIdx.x & 31) * 16;
+    uint4 u = ld_shared_16(at);
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t next = ld_shared_4(at + 16), shift = odd ? 16u : 0u;
+        u = make_uint4(__funnelshift_r(u.x, u.y, shift), __funnelshift_r(u.y, u.z, shift),
+                       __funnelshift_r(u.z, u.w, shift), __funnelshift_r(u.w, next, shift));
+        if (valid < 8) {
+            uint32_t o[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            f2_unpack(v[i], lo, hi);
-            w[i] = pack_bf16x2(lo, hi);
+            for (int i = 0; i < 4; ++i) o[i] = 2 * i + 1 < valid ? o[i] : 2 * i < valid ? (o[i] & 0xffffu) : 0u;
+            u = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        st_global_16(p, make_uint4(w[0], w[1], w[2], w[3]), on);
+    } else if (valid < 4) {
+        u = make_uint4(valid > 0 ? u.x : 0u, valid > 1 ? u.y : 0u, valid > 2 ? u.z : 0u, 0u);
     }
-};
-template <>
-struct Pairs<float> {
-    static constexpr int N = 2;
-    __device__ __forceinline__ static uint64_t get(const uint4& u, int i) {
-        return i == 0 ? f2_pack(__uint_as_float(u.x), __uint_as_float(u.y))
-                      : f2_pack(__uint_as_float(u.z), __uint_as_float(u.w));
-    }
-    __device__ __forceinline__ static void store(float* p, const uint64_t (&v)[2], bool on = true) {
-        float4 u;
-        f2_unpack(v[0], u.x, u.y);
-        f2_unpack(v[1], u.z, u.w);
-        st_global_16(p, make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z), __float_as_uint(u.w)), on);
-    }
-};
-
-__device__ __forceinline__ uint64_t f2_splat(float v) { return f2_pack(v, v); }
-__device__ __forceinline__ float f2_sum(uint64_t v) {
-    float lo, hi;
-    f2_unpack(v, lo, hi);
-    return lo + hi;
+    return u;
 }
 
-// V parameter values from `col` on as pairs (1 or 0 where there are none).
-template <int V>
-__device__ __forceinline__ void param_pairs(const void* base, bool f32, int col, bool in, float none, uint64_t (&v)[V / 2]) {
-    float w[V];
-    if (base && in) {
-        load_param<V>(base, f32, col, w);
+constexpr int WARP_WORDS_BYTES = 544;  // 129 words, and 16 bytes before them for a store
+
+template <typename T, bool LOOSE>
+struct Stage {
+    static constexpr bool SHIFT = LOOSE && sizeof(T) == 2;
+    // shared memory of one vector of every thread of `threads`
+    __host__ __device__ static constexpr int bytes(int threads) {
+        return LOOSE ? threads / 32 * WARP_WORDS_BYTES : threads * 16;
+    }
+    // this thread's (LOOSE: warp's) place in the first vector's memory
+    __device__ __forceinline__ static uint32_t mine(uint32_t base) {
+        return base + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : threadIdx.x * 16);
+    }
+    // starts the copy of a vector from src, of which and beyond the row holds `valid`
+    // elements; `edge`: the row is the matrix's first or last
+    __device__ __forceinline__ static void fetch(uint32_t slot, const T* src, int valid, bool edge, const Extent& all) {
+        if constexpr (!LOOSE) {
+            cp_async<16>(slot, src, valid > 0);
+        } else {
+            const uint32_t lane = threadIdx.x & 31, at = slot + lane * 4;
+            if (!edge && WarpWords<T>::full(valid)) {
+                // this lane's first word: src and the warp's first vector are 16 lane bytes apart
+                const char* p = WarpWords<T>::lane_word(src);
+                cp_async_4_at<0>(at, p);
+                cp_async_4_at<128>(at, p);
+                cp_async_4_at<256>(at, p);
+                cp_async_4_at<384>(at, p);
+                if (SHIFT) cp_async<4>(at + 512, p + 512, lane == 0 && (reinterpret_cast<uintptr_t>(src) & 2));
+                return;
+            }
+            const WarpWords<T> w(src, valid);
+#pragma unroll
+            for (int i = 0; i < WarpWords<T>::N; ++i) {
+                const char* p = w.word(i);
+                const bool on = w.has(i), inside = !edge || (p >= all.lo && p + 4 <= all.hi);
+                cp_async<4>(at + i * 128, p, on && inside);
+                if (SHIFT && on && !inside)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + i * 128), "r"(outer_word(p, all)) : "memory");
+            }
+        }
+    }
+    // before the first read of a stage, after the wait for its copies
+    __device__ __forceinline__ static void arrived() {
+        if constexpr (LOOSE) __syncwarp();
+    }
+    __device__ __forceinline__ static uint4 read(uint32_t slot, int valid, bool odd) {
+        if constexpr (!LOOSE)
+            return ld_shared_16(slot);  // places past the row hold zeros (clear)
+        else
+            return vec_of_words<T>(slot, valid, odd);
+    }
+    // zeros where nothing is copied, which nothing overwrites
+    __device__ __forceinline__ static void clear(uint32_t slot, int valid) {
+        if constexpr (!LOOSE)
+            if (valid <= 0) st_shared_zero_16(slot);
+    }
+};
+
+// Stores a vector of a row whose warp holds 32 consecutive vectors, `dst` being
+// this lane's and `valid` the elements of the row from there on.  Loose rows go
+// through the warp's shared memory (WARP_WORDS_BYTES at `stage`) and are
+// written word by word, lane by lane, with single elements at the ends.
+template <typename T, bool LOOSE>
+__device__ __forceinline__ void store_row_vec(T* dst, const uint4& u, int valid, uint32_t stage) {
+    if constexpr (!LOOSE) {
+        st_global_16(dst, u, valid > 0);
     } else {
+        // the vectors lie 16 bytes into the warp's memory: the word before them may be read
+        const int lane = threadIdx.x & 31;
+        const uint32_t vecs = stage + 16;
+        st_shared_v4(vecs + lane * 16, u.x, u.y, u.z, u.w);
+        __syncwarp();
+        const uint32_t o = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(dst) & 2) ? 1 : 0;  // elements of the first word before ours
+        const uint32_t from = vecs + lane * 4, before = from - 4 * o;
+        if (WarpWords<T>::full(valid)) {
+            char* p = const_cast<char*>(WarpWords<T>::lane_word(dst));
 #pragma unroll
-        for (int i = 0; i < V; ++i) w[i] = none;
+            for (int i = 0; i < 4; ++i) {
+                uint32_t x = ld_shared_4(from + 128 * i);
+                if (sizeof(T) == 2) x = __funnelshift_r(ld_shared_4(before + 128 * i), x, 16 * o);
+                if (i > 0 || lane > 0 || o == 0) *reinterpret_cast<uint32_t*>(p + 128 * i) = x;
+            }
+            if (sizeof(T) == 2 && o && lane == 0) {
+                *reinterpret_cast<unsigned short*>(p + 2) = static_cast<unsigned short>(ld_shared_4(from));
+                *reinterpret_cast<unsigned short*>(p + 512) = static_cast<unsigned short>(ld_shared_4(from + 508) >> 16);
+            }
+        } else {
+            const WarpWords<T> w(dst, valid);
+            char* first = const_cast<char*>(w.word(0));
+#pragma unroll
+            for (int i = 0; i < WarpWords<T>::N; ++i) {
+                if (!w.has(i)) continue;
+                const int j = lane + 32 * i;
+                char* p = first + 128 * i;
+                const bool lower = j > 0 || o == 0, upper = 4 * j + 4 <= w.bytes;
+                const uint32_t hi = ld_shared_4(from + 128 * i);
+                const uint32_t x = __funnelshift_r(ld_shared_4(before + 128 * i), hi, 16 * o);
+                if (lower && upper)
+                    *reinterpret_cast<uint32_t*>(p) = x;
+                else if (lower)
+                    *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(x);
+                else if (upper)
+                    *reinterpret_cast<unsigned short*>(p + 2) = static_cast<unsigned short>(hi);
+            }
+        }
+        __syncwarp();
     }
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) v[i] = f2_pack(w[2 * i], w[2 * i + 1]);
 }
+
+// ----------------------------------------------------------------- reductions
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-}
-
-// Sums of N values over the TPR threads of a row (a warp, or the whole block);
-// every thread gets them, in the same order.  `red` holds 32 * N floats that
-// no thread of the block still reads (alternate two of them between calls).
-template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
-    if constexpr (TPR > 32) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) red[n * 32 + warp] = v[n];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float s = 0.f;
-            if constexpr (TPR <= 256) {
-#pragma unroll
-                for (int w = 0; w < TPR / 32; ++w) s += red[n * 32 + w];
-            } else {
-                s = warp_sum(lane < TPR / 32 ? red[n * 32 + lane] : 0.f);
-            }
-            v[n] = s;
-        }
-    }
 }
 
 // Sums of one or two values over a warp (kWarp) or over the whole block of up to
@@ -323,68 +418,15 @@ __device__ __forceinline__ void group_sum2(float& v0, float& v1, float* red) {
 constexpr int CK_BLOCK = 32;
 constexpr uint32_t CK_NAN = 255;
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// The scale byte of a block from the largest |x| bits in it (NaN > inf > finite).
-__device__ __forceinline__ uint32_t ck_byte(uint32_t top) {
-    return top >= 0x7f800000u ? CK_NAN : static_cast<uint32_t>(max(1, static_cast<int>(top >> 23) - 6));
-}
-
 // 1 / step and step of a scale byte.
 __device__ __forceinline__ float ck_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 __device__ __forceinline__ float ck_step(uint32_t byte) {
     return byte == CK_NAN ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
-// rint(x * inverse) in [-127, 127] as the low byte of the result: adding
-// 1.5 * 2^23 rounds to an integer (ties to even) that sits in the low mantissa
-// bits as two's complement; the product is exact, so the fma rounds once.
-__device__ __forceinline__ uint32_t ck_round(float x, float inverse) {
-    const float magic = 12582912.f;
-    return __float_as_uint(fminf(fmaxf(__fmaf_rn(x, inverse, magic), magic - 127.f), magic + 127.f));
-}
-
 // The low bytes of four words in one.
 __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-}
-
-// Four values of a q word times the step: byte b + 128 placed in the mantissa
-// of 2^23 gives 2^23 + 128 + q, from which q comes out exactly.
-__device__ __forceinline__ void ck_values4(uint32_t q, float step, float* v) {
-    const uint32_t u = q ^ 0x80808080u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 + i)) - 8388736.f) * step;
-}
-
-// Quantises one vector of a row: lanes that are consecutive in `lane` order
-// hold consecutive vectors, so CK_BLOCK / V of them share a block.  `w` gets
-// the V bytes (one word for V <= 4); returns the block's scale byte.  Every
-// lane of the warp takes part.
-template <int V>
-__device__ __forceinline__ uint32_t ck_quantise(const float (&v)[V], uint32_t (&w)[V > 4 ? 2 : 1]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) top = max(top, abs_bits(v[i]));
-#pragma unroll
-    for (int o = 1; o < CK_BLOCK / V; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t byte = ck_byte(top);
-    const float inv = byte == CK_NAN ? 0.f : ck_inverse(byte);
-    uint32_t r[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = ck_round(v[i], inv);
-    if constexpr (V == 1) {
-        w[0] = r[0] & 0xffu;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) w[i] = pack_bytes(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-    }
-    if (byte == CK_NAN) {
-#pragma unroll
-        for (int i = 0; i < (V > 4 ? 2 : 1); ++i) w[i] = 0;
-    }
-    return byte;
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -393,7 +435,12 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return m;
 }
 
-// The same for a 16-byte vector as loaded (`raw`) and as pairs.  Only a block
+// Quantises one vector, given as loaded (`raw`) and as pairs: lanes that are
+// consecutive hold consecutive vectors, so CK_BLOCK / V of them share a block.
+// `w` gets the V bytes; returns the block's scale byte.  Every lane of the warp
+// takes part.  Adding 1.5 * 2^23 to x / step rounds to an integer (ties to even)
+// that sits in the low mantissa bits as two's complement; the division is exact,
+// so the fma rounds once.  Only a block
 // whose largest value lies within half a step of 128 steps can round to 128, so
 // the clamp runs for those blocks alone (about one in 130 of normal values).
 template <typename T>
@@ -433,7 +480,8 @@ __device__ __forceinline__ uint32_t ck_quantise_pairs(const uint4& raw, const ui
 __device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[2], bool on) { st_global_8(q, w[0], w[1], on); }
 __device__ __forceinline__ void ck_store_words(uint8_t* q, const uint32_t (&w)[1], bool on) { st_global_4(q, w[0], on); }
 
-// Values of a vector's bytes as pairs.
+// Values of a vector's bytes as pairs: byte b + 128 placed in the mantissa of
+// 2^23 gives 2^23 + 128 + q, from which q comes out exactly.
 template <int V>
 __device__ __forceinline__ void ck_pairs(const uint32_t* w, float step, uint64_t (&v)[V / 2]) {
     const uint64_t off = f2_splat(-8388736.f), s = f2_splat(step);
@@ -449,46 +497,5 @@ __device__ __forceinline__ void ck_pairs(const uint32_t* w, float step, uint64_t
     }
 }
 
-template <int V>
-__device__ __forceinline__ void ck_store(uint8_t* q, const uint32_t (&w)[V > 4 ? 2 : 1]) {
-    if constexpr (V == 8)
-        *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
-    else if constexpr (V == 4)
-        *reinterpret_cast<uint32_t*>(q) = w[0];
-    else
-        *q = static_cast<uint8_t>(w[0]);
-}
-
-// V bytes of a checkpoint row and their block's scale byte.
-template <int V>
-struct RawCk {
-    uint32_t w[V > 4 ? 2 : 1];
-    uint32_t byte;
-    __device__ __forceinline__ void load(const uint8_t* q, const uint8_t* scale, int col) {
-        if constexpr (V == 8) {
-            const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q + col));
-            w[0] = u.x, w[1] = u.y;
-        } else if constexpr (V == 4) {
-            w[0] = __ldcs(reinterpret_cast<const uint32_t*>(q + col));
-        } else {
-            w[0] = __ldcs(q + col);
-        }
-        byte = __ldcs(scale + col / CK_BLOCK);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < (V > 4 ? 2 : 1); ++i) w[i] = 0;
-        byte = 1;
-    }
-    __device__ __forceinline__ void to(float (&v)[V]) const {
-        const float step = ck_step(byte);
-        if constexpr (V == 1) {
-            v[0] = (__uint_as_float(0x4b000000u | (w[0] ^ 0x80u)) - 8388736.f) * step;
-        } else {
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) ck_values4(w[i], step, v + 4 * i);
-        }
-    }
-};
 
 }  // namespace flp
