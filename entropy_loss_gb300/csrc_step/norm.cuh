@@ -31,6 +31,8 @@ struct NormFwdParams {
     uint8_t* q;  // the checkpoint of x (CK): [M, Hp], Hp = H rounded up to 32
     uint8_t* scale;
     int Hp;
+    // from a group's row to its next, in elements: rows, x, y, q, scale
+    long long step, step_x, step_y, step_q, step_s;
 };
 
 struct NormBwdParams {
@@ -51,6 +53,8 @@ struct NormBwdParams {
     void* dx;
     long long lddx;
     float* part;  // [gridDim.x][2][H] fp32 partial sums of dw and db
+    // from a group's row to its next, in elements: rows, dy, x, dx, q, scale
+    long long step, step_dy, step_x, step_dx, step_q, step_s;
 };
 
 // ---------------------------------------------------------------- streaming rows
@@ -67,36 +71,38 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
     using X = Stage<T, LOOSE>;
     constexpr int P = Pairs<T>::N, V = 2 * P;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float red[2][16];
+    __shared__ __align__(16) float red[2][32];
     __shared__ __align__(16) uint8_t out_stage[LOOSE ? Stage<T, true>::bytes(MAXT) : 16];
     const int group = WARP ? 32 : blockDim.x;
     const int groups = WARP ? blockDim.x / 32 : 1;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const long long first = static_cast<long long>(blockIdx.x) * groups + (WARP ? threadIdx.x >> 5 : 0);
-    const long long step = static_cast<long long>(gridDim.x) * groups;
+    const long long step = p.step;
     const uint32_t pitch = X::bytes(blockDim.x);  // from one vector to the next
     const uint32_t slot0 = X::mine(smem_addr(ring)), ring_end = slot0 + S * NV * pitch;
     const int apart = group * V;             // columns between this thread's vectors
     int valid[NV];                           // elements of the row from this thread's vectors on
 #pragma unroll
     for (int k = 0; k < NV; ++k) valid[k] = p.H - t * V - k * apart;
-    if (!WARP && threadIdx.x < 32) (&red[0][0])[threadIdx.x] = 0.f;
+    if (!WARP && threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
     const uint32_t stage = smem_addr(out_stage) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
     const Extent all = extent_of<T>(p.x, p.M, p.ldx, p.H);
 
     const T* ahead = static_cast<const T*>(p.x) + first * p.ldx + t * V;  // of the next row to fetch
-    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = first;
+    int rows_left = first < p.M ? static_cast<int>((p.M - first + step - 1) / step) : 0, to_fetch = rows_left;
+    long long fetch_row = first;
     // bf16 rows that start at an odd element (LOOSE), this one and whether it alternates
     bool odd = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead) & 2);
-    const bool alternates = X::SHIFT && ((step * p.ldx) & 1);
+    const bool alternates = X::SHIFT && (p.step_x & 1);
     auto fetch = [&](uint32_t slot) {
-        if (to_fetch < p.M) {
-            const bool edge = to_fetch == 0 || to_fetch == p.M - 1;
+        if (to_fetch > 0) {
+            const bool edge = LOOSE && (fetch_row == 0 || fetch_row == p.M - 1);
 #pragma unroll
             for (int k = 0; k < NV; ++k) X::fetch(slot + k * pitch, ahead + k * apart, valid[k], edge, all);
         }
-        to_fetch += step;
-        ahead += step * p.ldx;
+        --to_fetch;
+        if (LOOSE) fetch_row += step;
+        ahead += p.step_x;
         cp_async_commit();
     };
 #pragma unroll
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
             }
         }
         float mean = f2_sum(acc);
-        group_sum<WARP>(mean, red[0]);
+        group_sum<WARP ? 0 : MAXT / 32>(mean, red[0]);
         // the sum has taken every value of this stage: its slots are free
         fetch(slot);
         slot += NV * pitch;
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
             }
         }
         float rstd = f2_sum(acc);
-        group_sum<WARP>(rstd, red[1]);
+        group_sum<WARP ? 0 : MAXT / 32>(rstd, red[1]);
         rstd = rsqrtf(fmaf(rstd, p.inv_h, p.eps));
         if (t == 0) {
             if (mean_at) *mean_at = mean;
@@ -178,11 +184,11 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
             for (int i = 0; i < P; ++i) o[i] = f2_fma(f2_mul(v[k][i], r2), w[k][i], b[k][i]);
             store_row_vec<T, LOOSE>(y + k * apart, Pairs<T>::put(o), valid[k], stage);
         }
-        y += step * p.ldy;
+        y += p.step_y;
         odd ^= alternates;
         if constexpr (CK) {
-            q += step * p.Hp;
-            scale += step * blocks;
+            q += p.step_q;
+            scale += p.step_s;
         }
     }
     cp_async_wait<0>();
@@ -193,14 +199,14 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     using X = Stage<T, LOOSE>;
     constexpr int P = Pairs<T>::N, V = 2 * P;
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ __align__(16) float red[2][32];
+    __shared__ __align__(16) float red[2][64];
     __shared__ __align__(16) uint8_t out_stage[LOOSE ? Stage<T, true>::bytes(MAXT) : 16];
     const int group = WARP ? 32 : blockDim.x;
     const int groups = WARP ? blockDim.x / 32 : 1;
     const int sub = WARP ? threadIdx.x >> 5 : 0;
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const long long first = static_cast<long long>(blockIdx.x) * groups + sub;
-    const long long step = static_cast<long long>(gridDim.x) * groups;
+    const long long step = p.step;
     const uint32_t pitch_y = X::bytes(blockDim.x), pitch_x = CK ? blockDim.x * V : pitch_y;
     const uint32_t ring_x = smem_addr(ring) + S * NV * pitch_y;
     const uint32_t slot0 = X::mine(smem_addr(ring)), ring_end = slot0 + S * NV * pitch_y;
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     int valid[NV];  // elements of the row from this thread's vectors on
 #pragma unroll
     for (int k = 0; k < NV; ++k) valid[k] = p.H - t * V - k * apart;
-    if (!WARP && threadIdx.x < 32) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.f;
+    if (!WARP && threadIdx.x < 64) (&red[0][0])[threadIdx.x] = (&red[1][0])[threadIdx.x] = 0.f;
     const uint32_t stage = smem_addr(out_stage) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
     const Extent all_y = extent_of<T>(p.dy, p.M, p.lddy, p.H), all_x = extent_of<T>(p.x, p.M, p.ldx, p.H);
 
@@ -217,14 +223,15 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     const T* ahead_y = static_cast<const T*>(p.dy) + first * p.lddy + t * V;
     const T* ahead_x = CK ? nullptr : static_cast<const T*>(p.x) + first * p.ldx + t * V;
     const uint8_t* ahead_q = CK ? p.q + first * p.Hp + t * V : nullptr;
-    long long rows_left = first < p.M ? (p.M - first + step - 1) / step : 0, to_fetch = first;
+    int rows_left = first < p.M ? static_cast<int>((p.M - first + step - 1) / step) : 0, to_fetch = rows_left;
+    long long fetch_row = first;
     // bf16 rows that start at an odd element (LOOSE), these ones and whether they alternate
     bool odd_y = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_y) & 2);
     bool odd_x = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_x) & 2);
-    const bool alternates_y = X::SHIFT && ((step * p.lddy) & 1), alternates_x = X::SHIFT && ((step * p.ldx) & 1);
+    const bool alternates_y = X::SHIFT && (p.step_dy & 1), alternates_x = X::SHIFT && (p.step_x & 1);
     auto fetch = [&](uint32_t slot, uint32_t slot_x) {
-        if (to_fetch < p.M) {
-            const bool edge = to_fetch == 0 || to_fetch == p.M - 1;
+        if (to_fetch > 0) {
+            const bool edge = LOOSE && (fetch_row == 0 || fetch_row == p.M - 1);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 X::fetch(slot + k * pitch_y, ahead_y + k * apart, valid[k], edge, all_y);
@@ -234,12 +241,13 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                     X::fetch(slot_x + k * pitch_x, ahead_x + k * apart, valid[k], edge, all_x);
             }
         }
-        to_fetch += step;
-        ahead_y += step * p.lddy;
+        --to_fetch;
+        if (LOOSE) fetch_row += step;
+        ahead_y += p.step_dy;
         if constexpr (CK)
-            ahead_q += step * p.Hp;
+            ahead_q += p.step_q;
         else
-            ahead_x += step * p.ldx;
+            ahead_x += p.step_x;
         cp_async_commit();
     };
     // what a row needs beside its vectors, two rows ahead in registers (a miss takes
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
         }
         mean_at += step;
         rstd_at += step;
-        if constexpr (CK) scale += step * blocks;
+        if constexpr (CK) scale += p.step_s;
     };
     // columns past the row read as zeros: dY's (so that nothing of what is beside
     // the row enters a sum), and x's so that no NaN comes of it (a checkpoint's bytes
@@ -279,9 +287,35 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     Few even{}, other{};
     fetch_few(even, rows_left > 0);
     fetch_few(other, rows_left > 1);
-    uint64_t w[NV][P], dw[NV][P] = {}, db[NV][P] = {};
+    // where registers are short the weights wait in shared memory, each thread's own:
+    // 32768 x 5120 bf16 228 -> 188 us from a checkpoint, 203 -> 178 us otherwise (at
+    // 32768 x 4096 145 -> 122 us, but 138 -> 141 us)
+    constexpr bool W_SHARED = !WARP && (CK || MAXT == 320);
+    __shared__ ulonglong2 w_shared[W_SHARED ? NV * P / 2 : 1][W_SHARED ? MAXT : 1];
+    uint64_t w_kept[W_SHARED ? 1 : NV][P], dw[NV][P] = {}, db[NV][P] = {};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) param_pairs<V, LOOSE>(p.w, p.param_f32, t * V + k * apart, p.H, 1.f, w[k]);
+    for (int k = 0; k < NV; ++k) {
+        uint64_t w[P];
+        param_pairs<V, LOOSE>(p.w, p.param_f32, t * V + k * apart, p.H, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            if constexpr (W_SHARED)
+                w_shared[(k * P + i) / 2][threadIdx.x] = make_ulonglong2(w[i], w[i + 1]);
+            else
+                w_kept[k][i] = w[i], w_kept[k][i + 1] = w[i + 1];
+        }
+    }
+    auto weight = [&](int k, uint64_t (&w)[P]) {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            if constexpr (W_SHARED) {
+                const ulonglong2 u = w_shared[(k * P + i) / 2][threadIdx.x];
+                w[i] = u.x, w[i + 1] = u.y;
+            } else {
+                w[i] = w_kept[k][i], w[i + 1] = w_kept[k][i + 1];
+            }
+        }
+    };
     T* dx = static_cast<T*>(p.dx) + first * p.lddx + t * V;
     uint32_t slot = slot0, slot_x = slot_x0;
     int buf = 0;
@@ -310,20 +344,22 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
 #pragma unroll
                 for (int i = 0; i < P; ++i) xh[k][i] = Pairs<T>::get(rx, i);
             }
+            uint64_t w[P];
+            weight(k, w);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const uint64_t d = Pairs<T>::get(ry[k], i);
                 xh[k][i] = f2_mul(f2_add(xh[k][i], minus), r2);
                 dw[k][i] = f2_fma(d, xh[k][i], dw[k][i]);
                 db[k][i] = f2_add(db[k][i], d);
-                const uint64_t g = f2_mul(d, w[k][i]);
+                const uint64_t g = f2_mul(d, w[i]);
                 s0 = f2_add(s0, g);
                 s1 = f2_fma(g, xh[k][i], s1);
             }
         }
         fetch_few(few, rows_left > 2);
         float m1 = f2_sum(s0), m2 = f2_sum(s1);
-        group_sum2<WARP>(m1, m2, red[buf]);
+        group_sum2<WARP ? 0 : MAXT / 32>(m1, m2, red[buf]);
         buf ^= 1;
         // the sums have taken every value of this stage: its slots are free
         fetch(slot, slot_x);
@@ -333,13 +369,14 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
         const uint64_t n1 = f2_splat(-m1 * p.inv_h), n2 = f2_splat(-m2 * p.inv_h);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            uint64_t o[P];
+            uint64_t o[P], w[P];
+            weight(k, w);
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                o[i] = f2_mul(r2, f2_fma(xh[k][i], n2, f2_fma(Pairs<T>::get(ry[k], i), w[k][i], n1)));
+                o[i] = f2_mul(r2, f2_fma(xh[k][i], n2, f2_fma(Pairs<T>::get(ry[k], i), w[i], n1)));
             store_row_vec<T, LOOSE>(dx + k * apart, Pairs<T>::put(o), valid[k], stage);
         }
-        dx += step * p.lddx;
+        dx += p.step_dx;
         odd_y ^= alternates_y;
         odd_x ^= alternates_x;
         --rows_left;

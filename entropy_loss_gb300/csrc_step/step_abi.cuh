@@ -75,20 +75,22 @@ flp_status resident_blocks(const void* kernel, int threads, size_t smem, int* pe
     return FLP_OK;
 }
 
-// Streaming rows: calls f(shape, threads of a block).  16 elements a thread
-// keep a row, its parameters and the column sums in registers; rows of up to
-// 512 elements go to one warp, which needs no block barrier; rows above 8192
-// take more elements a thread.  The stages put 64 KiB or so per SM in flight in
-// every shape.  MINB blocks of up to 256 threads must fit an SM, which bounds the
-// registers: 3 for the forward (32768 x 4096 bf16 with a checkpoint: 111 us, with
-// 2 blocks 124), 2 where more would spill (the backward; loose rows).
+// Streaming rows: calls f(shape, threads of a block).  16 elements a thread keep
+// a row, its parameters and the column sums in registers while its fixed work per
+// row (about 130 instructions) is spread over enough of them: 8 elements a thread
+// (twice the warps) took 12 to 50 % longer at 32768 x 4096, 32 (half the warps)
+// 17 to 130 %.  Rows of up to 512 elements go to one warp, which needs no block
+// barrier; rows above 8192 take more elements a thread.  Two blocks of up to 320
+// threads must fit an SM, which bounds the registers (three: forward with a
+// checkpoint 119 against 107 us, backward 185 against 138 us).  The stages put
+// 64 KiB or so per SM in flight in every shape.
 template <int NV_, int S_, bool WARP_, int MAXT_, int MINB_>
 struct StreamShape {
     static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;
     static constexpr bool WARP = WARP_;
 };
 
-template <typename T, int MINB, typename F>
+template <typename T, typename F>
 flp_status norm_stream_shape(int64_t cols, F&& f) {
     constexpr int V = wide_v<T>(), N2 = 16 / V;  // N2 vectors of V = 16 elements
     constexpr int S = V == 8 ? 4 : 2;
@@ -98,7 +100,7 @@ flp_status norm_stream_shape(int64_t cols, F&& f) {
     if constexpr (V == 4)
         if (vecs <= 128) return f(StreamShape<4, 2, true, 256, 1>{}, 256);
     const int threads = static_cast<int>(cdiv(vecs, 32 * N2) * 32);
-    if (threads <= 256) return f(StreamShape<N2, S, false, 256, MINB>{}, threads);
+    if (threads <= 256) return f(StreamShape<N2, S, false, 256, 2>{}, threads);
     if (threads <= 320) return f(StreamShape<N2, S, false, 320, 2>{}, threads);
     if (threads <= 512) return f(StreamShape<N2, S, false, 512, 1>{}, threads);
     return f(StreamShape<2 * N2, 2, false, 512, 1>{}, static_cast<int>(cdiv(vecs, 64 * N2) * 32));
@@ -364,7 +366,7 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
     auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
         using T = decltype(t);
         constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-        return norm_stream_shape<T, LOOSE ? 2 : 3>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
+        return norm_stream_shape<T>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
             using X = decltype(shape);
             auto* kernel = flp_norm_fwd_stream_kernel<T, X::NV, X::S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
             const size_t smem = static_cast<size_t>(X::S) * X::NV * Stage<T, LOOSE>::bytes(threads);
@@ -372,8 +374,13 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
             const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
             if (r != FLP_OK) return r;
             const int64_t rows = X::WARP ? threads / 32 : 1;
-            return launch_step(kernel, std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count),
-                               threads, smem, s, "flp_norm_fwd_stream_kernel launch", false, p);
+            const int64_t blocks = std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count);
+            p.step = blocks * rows;
+            p.step_x = p.step * ldx;
+            p.step_y = p.step * ldy;
+            p.step_q = p.step * p.Hp;
+            p.step_s = p.step_q / CK_BLOCK;
+            return launch_step(kernel, blocks, threads, smem, s, "flp_norm_fwd_stream_kernel launch", false, p);
         });
     };
     auto aligned = [&](auto t, auto ck) { return loose ? run(t, ck, std::true_type{}) : run(t, ck, std::false_type{}); };
@@ -440,7 +447,7 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
         auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
             using T = decltype(t);
             constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-            return norm_stream_shape<T, 2>(p.H, [&](auto shape, int threads) -> flp_status {
+            return norm_stream_shape<T>(p.H, [&](auto shape, int threads) -> flp_status {
                 using X_ = decltype(shape);
                 // two stages of an fp32 row above 8192 elements, dY and X, do not fit shared memory
                 constexpr int S = sizeof(T) == 4 && X_::NV == 8 ? 1 : X_::S;
@@ -454,6 +461,12 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
                                          std::min<int64_t>(kNormBwdBlocksPerSm, per_sm));
                 if (workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
                     return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
+                p.step = blocks * (X_::WARP ? threads / 32 : 1);
+                p.step_dy = p.step * lddy;
+                p.step_x = p.step * ldx;
+                p.step_dx = p.step * lddx;
+                p.step_q = p.step * p.Hp;
+                p.step_s = p.step_q / CK_BLOCK;
                 return launch_step(kernel, blocks, threads, smem, s, "flp_norm_bwd_stream_kernel launch", false, p);
             });
         };

@@ -358,48 +358,49 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sums of one or two values over a warp (kWarp) or over the whole block of up to
-// 16 warps, known at run time; every thread gets them.  `red` holds 16 * N
-// floats, zero beyond the block's warps, that no thread still reads (alternate
-// two of them between calls).  Two values halve the shuffles: after the first
-// exchange the lower lanes sum one of them and the upper lanes the other.  The
-// warps' sums are read back four at a time by every thread, which takes less
-// time than another five shuffles.
-__device__ __forceinline__ float sum_red(const float* red, int warps) {
+// Sums of one or two values over a warp (WARPS = 0) or over a block of at most
+// WARPS warps; every thread gets them.  `red` holds 32 floats per value, zero
+// beyond the block's warps, that no thread still reads (alternate two of them
+// between calls).  Two values halve the shuffles: after the first exchange the
+// lower lanes sum one of them and the upper lanes the other.  The warps' sums are
+// read back four at a time by every thread, which takes less time than another
+// five shuffles.
+template <int WARPS>
+__device__ __forceinline__ float sum_red(const float* red) {
     uint64_t a = 0;
-#pragma unroll 2
-    for (int w = 0; w < warps; w += 4) {
+#pragma unroll
+    for (int w = 0; w < WARPS; w += 4) {
         const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(red + w);
         a = f2_add(a, f2_add(u.x, u.y));
     }
     return f2_sum(a);
 }
 
-template <bool kWarp>
+template <int WARPS>
 __device__ __forceinline__ void group_sum(float& v, float* red) {
     v = warp_sum(v);
-    if constexpr (!kWarp) {
+    if constexpr (WARPS > 0) {
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = sum_red(red, blockDim.x >> 5);
+        v = sum_red<WARPS>(red);
     }
 }
 
-template <bool kWarp>
+template <int WARPS>
 __device__ __forceinline__ void group_sum2(float& v0, float& v1, float* red) {
     const int lane = threadIdx.x & 31;
     const bool upper = lane & 16;
     float r = (upper ? v1 : v0) + __shfl_xor_sync(0xffffffffu, upper ? v0 : v1, 16);
 #pragma unroll
     for (int o = 8; o; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-    if constexpr (kWarp) {
+    if constexpr (WARPS == 0) {
         v0 = __shfl_sync(0xffffffffu, r, 0);
         v1 = __shfl_sync(0xffffffffu, r, 16);
     } else {
-        if ((lane & 15) == 0) red[lane + (threadIdx.x >> 5)] = r;
+        if ((lane & 15) == 0) red[2 * lane + (threadIdx.x >> 5)] = r;
         __syncthreads();
-        v0 = sum_red(red, blockDim.x >> 5);
-        v1 = sum_red(red + 16, blockDim.x >> 5);
+        v0 = sum_red<WARPS>(red);
+        v1 = sum_red<WARPS>(red + 32);
     }
 }
 
