@@ -18,7 +18,11 @@ struct CkParams {
 };
 
 constexpr int CK_THREADS = 256;
-constexpr int CK_PER_THREAD = 4;  // vectors in flight per thread
+// Vectors in flight per thread: writing a checkpoint 4 (32768 x 4096 bf16 62 us; 2:
+// 68, 8: 66), reading one, which stores twice what it loads, 2 (67 us; 1:
+// 72, 4: 75, 8: 94).
+constexpr int CK_PACK_N = 4;
+constexpr int CK_UNPACK_N = 2;
 
 // Row and first column of vector j.
 template <int V>
@@ -30,17 +34,17 @@ __device__ __forceinline__ long long ck_place(const CkParams& p, long long j, in
 
 // A thread's vectors.  Loose rows: a warp's 32 vectors are consecutive in one row
 // (lanes past the row's end idle), so that they can move as words.
-template <typename T, bool LOOSE>
+template <typename T, int N>
 struct CkPlaces {
     static constexpr int V = wide_v<T>();
-    long long row[CK_PER_THREAD];
-    int col[CK_PER_THREAD];
-    int valid[CK_PER_THREAD];  // elements of the row from there on; at most 0: nothing of x
-    bool on[CK_PER_THREAD];    // the checkpoint has the vector
+    long long row[N];
+    int col[N];
+    int valid[N];  // elements of the row from there on; at most 0: nothing of x
+    bool on[N];    // the checkpoint has the vector
     __device__ __forceinline__ explicit CkPlaces(const CkParams& p) {
 #pragma unroll
-        for (int k = 0; k < CK_PER_THREAD; ++k) {
-            const long long j = static_cast<long long>(blockIdx.x) * (CK_THREADS * CK_PER_THREAD) + k * CK_THREADS + threadIdx.x;
+        for (int k = 0; k < N; ++k) {
+            const long long j = static_cast<long long>(blockIdx.x) * (CK_THREADS * N) + k * CK_THREADS + threadIdx.x;
             row[k] = ck_place<V>(p, j, col[k]);
             on[k] = row[k] < p.M && col[k] < p.Hp;
             valid[k] = row[k] < p.M ? p.H - col[k] : -32 * V;
@@ -52,11 +56,11 @@ template <typename T, bool LOOSE>
 __global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams p) {
     constexpr int P = Pairs<T>::N, N = LOOSE ? WarpWords<T>::N : 4;
     __shared__ __align__(16) uint8_t words[LOOSE ? Stage<T, true>::bytes(CK_THREADS) : 16];
-    const CkPlaces<T, LOOSE> at(p);
-    const T* src[CK_PER_THREAD];
-    uint32_t r[CK_PER_THREAD][N];
+    const CkPlaces<T, CK_PACK_N> at(p);
+    const T* src[CK_PACK_N];
+    uint32_t r[CK_PACK_N][N];
 #pragma unroll
-    for (int k = 0; k < CK_PER_THREAD; ++k) {
+    for (int k = 0; k < CK_PACK_N; ++k) {
         src[k] = static_cast<const T*>(p.x) + at.row[k] * p.ldx + at.col[k];
         if constexpr (LOOSE) {
             const Extent all = extent_of<T>(p.x, p.M, p.ldx, p.H);
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams 
         }
     }
 #pragma unroll
-    for (int k = 0; k < CK_PER_THREAD; ++k) {
+    for (int k = 0; k < CK_PACK_N; ++k) {
         uint4 u = make_uint4(r[k][0], r[k][1], r[k][2], r[k][3]);
         if constexpr (LOOSE) {
             const uint32_t base = smem_addr(words) + threadIdx.x / 32 * WARP_WORDS_BYTES, lane = threadIdx.x & 31;
@@ -117,13 +121,13 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_unpack_kernel(const CkParam
     constexpr int P = Pairs<T>::N, V = 2 * P;
     __shared__ __align__(16) uint8_t words[LOOSE ? Stage<T, true>::bytes(CK_THREADS) : 16];
     const uint32_t stage = smem_addr(words) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
-    const CkPlaces<T, LOOSE> at(p);
-    uint32_t w[CK_PER_THREAD][P / 2];
-    uint32_t byte[CK_PER_THREAD];
+    const CkPlaces<T, CK_UNPACK_N> at(p);
+    uint32_t w[CK_UNPACK_N][P / 2];
+    uint32_t byte[CK_UNPACK_N];
     griddep_launch_dependents();  // the weight gradient's contraction may set up meanwhile
     if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.clear = 0;
 #pragma unroll
-    for (int k = 0; k < CK_PER_THREAD; ++k) {
+    for (int k = 0; k < CK_UNPACK_N; ++k) {
         byte[k] = 0;
 #pragma unroll
         for (int i = 0; i < P / 2; ++i) w[k][i] = 0;
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_unpack_kernel(const CkParam
         }
     }
 #pragma unroll
-    for (int k = 0; k < CK_PER_THREAD; ++k) {
+    for (int k = 0; k < CK_UNPACK_N; ++k) {
         uint64_t v[P];
         ck_pairs<V>(w[k], ck_step(byte[k]), v);
         store_row_vec<T, LOOSE>(static_cast<T*>(p.x) + at.row[k] * p.ldx + at.col[k], Pairs<T>::put(v), at.valid[k], stage);

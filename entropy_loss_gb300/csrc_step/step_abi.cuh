@@ -228,7 +228,7 @@ flp_status ck_launch(bool pack, void* x, int64_t ldx, const void* q, const void*
     p.per_row = static_cast<unsigned>(LOOSE ? cdiv(p.Hp / V, 32) * 32 : p.Hp / V);
     p.inverse = ~0ull / p.per_row + 1;
     p.clear = clear;
-    const int64_t total = M * p.per_row, grid = cdiv(total, CK_THREADS * CK_PER_THREAD);
+    const int64_t total = M * p.per_row, grid = cdiv(total, CK_THREADS * (pack ? CK_PACK_N : CK_UNPACK_N));
     // the row of a vector comes exactly from one multiplication while vectors x vectors per row < 2^64
     if (grid > INT32_MAX || static_cast<double>(total + (1 << 20)) * p.per_row > 1.8e19)
         return fail(FLP_ERR_UNSUPPORTED, "checkpoint too large for one launch");
