@@ -743,3 +743,79 @@ def fused_linear_logprob(X, W, y, ignore_index: int = -100, scale: float = 1.0,
         workspace = alloc_workspace(X.shape[0], X.shape[1], W.shape[0], compute_entropy,
                                     device=X.device)
     return FusedLinearLogprob.apply(X, W, y, ignore_index, scale, compute_entropy, workspace)
+
+
+class FusedLayerNorm(torch.autograd.Function):
+    """autograd wrapper of layer_norm; with `checkpoint` the input is kept for the
+    backward pass in 8 bits instead of its own type."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, checkpoint):
+        y, mean, rstd, *kept = layer_norm(x, weight, bias, eps=eps, checkpoint=checkpoint)
+        ctx.save_for_backward(*((kept[0].q, kept[0].scale) if checkpoint else (x, None)), weight, bias, mean, rstd)
+        ctx.kept = (x.shape[1], x.dtype) if checkpoint else None
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, scale, weight, bias, mean, rstd = ctx.saved_tensors
+        if ctx.kept is not None:
+            x = Checkpoint8(x, scale, *ctx.kept)
+        dx, dweight, dbias = layer_norm_backward(dy.contiguous(), x, weight, mean, rstd)
+        return (dx, None if weight is None else dweight.to(weight.dtype),
+                None if bias is None else dbias.to(bias.dtype), None, None)
+
+
+def fused_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint: bool = False):
+    """Differentiable layer norm of the rows of x [M, H]."""
+    return FusedLayerNorm.apply(x, weight, bias, eps, checkpoint)
+
+
+class CheckpointLinear(torch.autograd.Function):
+    """y = x W^T whose input is kept in 8 bits for the weight gradient.  The two
+    products with W are library GEMMs."""
+
+    @staticmethod
+    def forward(ctx, x, W):
+        if ctx.needs_input_grad[1]:
+            kept = checkpoint_pack(x)
+            ctx.save_for_backward(kept.q, kept.scale, W)
+        else:
+            ctx.save_for_backward(None, None, W)
+        ctx.kept = (x.shape[1], x.dtype)
+        return x @ W.t()
+
+    @staticmethod
+    def backward(ctx, dy):
+        q, scale, W = ctx.saved_tensors
+        dx = dy @ W if ctx.needs_input_grad[0] else None
+        dW = checkpoint_weight_grad(dy.contiguous(), Checkpoint8(q, scale, *ctx.kept), dw_dtype=W.dtype) \
+            if ctx.needs_input_grad[1] else None
+        return dx, dW
+
+
+def checkpoint_linear(x, W):
+    """Differentiable x W^T for bf16 x [M, K] and W [N, K] that keeps x in 8 bits."""
+    return CheckpointLinear.apply(x, W)
+
+
+class FusedBalanceLoss(torch.autograd.Function):
+    """autograd wrapper of balance_loss: (scalar loss, counts)."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, experts, mask, coef):
+        loss_out, grad, counts = balance_loss(logits, top_k, experts=experts, mask=mask, coef=coef,
+                                              grad=ctx.needs_input_grad[0])
+        ctx.save_for_backward(grad)
+        ctx.mark_non_differentiable(counts)
+        return loss_out[0], counts
+
+    @staticmethod
+    def backward(ctx, g, _):
+        grad, = ctx.saved_tensors
+        return grad * g.to(grad.dtype), None, None, None, None
+
+
+def fused_balance_loss(logits, top_k: int, experts=None, mask=None, coef: float = 1.0):
+    """Differentiable balance loss of router logits [T, E]: (scalar loss, counts [E])."""
+    return FusedBalanceLoss.apply(logits, top_k, experts, mask, coef)
