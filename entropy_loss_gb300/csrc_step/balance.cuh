@@ -196,10 +196,11 @@ __device__ __forceinline__ void choose(const uint32_t (&key)[NE], uint32_t top, 
         int total = count();
         left = 0;
         while (total > k) {
+            // keys below the bound wrap around to the largest distances
             uint32_t low = ALL;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) low = min(low, key[i] >= bound ? key[i] : ALL);
-            low = __reduce_min_sync(ALL, low);
+            for (int i = 0; i < NE; ++i) low = min(low, key[i] - bound);
+            low = bound + __reduce_min_sync(ALL, low);
             bound = low + 1;
             total = count();
             if (total < k) {  // only some of the smallest fit

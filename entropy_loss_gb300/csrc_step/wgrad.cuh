@@ -48,10 +48,13 @@ struct WgradUnit {
 // of a long sum grows with its length: 3.0e-6 of the result over 8192 rows of
 // normal values, 1.9e-5 over 32768, against 4.8e-7 over 2048.  An fp32 result is
 // therefore summed in runs of at most 2048 rows, whose sums are added in memory,
-// rounded to nearest.  Each further run drains the accumulators once more, about
-// 6 us a tile: 8192 x 8192 x 5120 takes 455 us, in one run 377 us.  A bf16
-// result's own rounding (1.7e-3) leaves nothing of that: one run.
+// rounded to nearest.  Draining the accumulators between runs costs about 6 us a
+// tile when every column goes through memory (8192 x 8192 x 5120 takes 455 us, in
+// one run 377 us); WGRAD_KEEP of a half's 256 columns are therefore summed in the
+// epilogue's registers (424 us; 64: 436, 32: 449; 128 would spill).  A bf16
+// result's own rounding (1.7e-3) leaves nothing of the error: one run.
 constexpr int WGRAD_RUN = 32;
+constexpr int WGRAD_KEEP = 96;
 
 __device__ __forceinline__ WgradUnit wgrad_unit(const WgradParams& p, int u) {
     WgradUnit t;
@@ -251,6 +254,23 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const int y0 = (partial ? t.part * PM : t.n0) + rofs;
             const bool bf16_out = !partial && p.bf16_out;
             const int cols = min(BN, p.K - t.k0 - g * BN);  // columns of dW in this half
+            // between the runs of a tile the first WGRAD_KEEP columns' sums stay in
+            // registers; the others are added to what the earlier runs stored
+            const bool runs = t.kb0 + t.run < t.kb1;
+            float kept[WGRAD_KEEP];
+            auto store32 = [&](int b, const uint32_t* v, bool add) {
+                if (b * 32 >= cols) return;  // the whole box lies past dW's last column
+                if (bf16_out) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    narrow_box_store(ring, box0, bar_box, et, r, w, out, x0 + b * 32, y0, false);
+                } else {
+                    narrow_box_store(ring, box0, bar_box, et, r, v, out, x0 + b * 32, y0, add);
+                    narrow_box_store(ring, box0, bar_box, et, r, v + 16, out, x0 + b * 32 + 16, y0, add);
+                }
+            };
             for (int kb0 = t.kb0; kb0 < t.kb1 && ok; kb0 += t.run) {
                 const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
                 // every thread of the group takes the same branch (the box barriers need all of them)
@@ -260,11 +280,22 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 phase ^= 1u;
                 tc_fence_after();
-                // a later run adds to what this thread's earlier bulk stores wrote
-                const bool add = kb0 > t.kb0 || (!partial && p.add);
-                if (kb0 > t.kb0 && et == 0) bulk_wait_group<0>();
+                const bool first = kb0 == t.kb0, adds = !partial && p.add;
+                if (runs) {
+#pragma unroll
+                    for (int b = 0; b < WGRAD_KEEP / 32; ++b) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(tbase + b * 32, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            kept[b * 32 + j] = (first ? 0.f : kept[b * 32 + j]) + __uint_as_float(v[j]);
+                    }
+                    // a later run adds to what this thread's earlier bulk stores wrote
+                    if (!first && et == 0) bulk_wait_group<0>();
+                }
 #pragma unroll 1
-                for (int b = 0; b < BN / 32; ++b) {
+                for (int b = runs ? WGRAD_KEEP / 32 : 0; b < BN / 32; ++b) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(tbase + b * 32, v);
                     tmem_wait_ld();
@@ -272,16 +303,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         tc_fence_before();
                         mbar_arrive_cluster(tempty);
                     }
-                    if (b * 32 >= cols) continue;  // the whole box lies past dW's last column
-                    if (bf16_out) {
-                        uint32_t w[16];
+                    store32(b, v, !first || adds);
+                }
+                if (runs && kb0 + t.run >= t.kb1) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                        narrow_box_store(ring, box0, bar_box, et, r, w, out, x0 + b * 32, y0, false);
-                    } else {
-                        narrow_box_store(ring, box0, bar_box, et, r, v, out, x0 + b * 32, y0, add);
-                        narrow_box_store(ring, box0, bar_box, et, r, v + 16, out, x0 + b * 32 + 16, y0, add);
+                    for (int b = 0; b < WGRAD_KEEP / 32; ++b) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(kept[b * 32 + j]);
+                        store32(b, v, adds);
                     }
                 }
             }
