@@ -2,9 +2,6 @@
 // include/flp.h: argument checks, kernel choice by size and alignment, and
 // launches.
 #pragma once
-#include <map>
-#include <tuple>
-
 #include "balance.cuh"
 #include "checkpoint.cuh"
 #include "norm.cuh"
@@ -53,25 +50,24 @@ inline bool rows16(const void* p, int64_t ld, int dtype) { return aligned16(p) &
 
 // ------------------------------------------------------------------ layer norm
 
-// Resident blocks per SM of a kernel with dynamic shared memory (its limit
-// raised where needed), asked once per kernel, block size and device.
-flp_status resident_blocks(const void* kernel, int threads, size_t smem, int* per_sm) {
-    static std::map<std::tuple<const void*, int, int>, int> known;
+// Resident blocks per SM of a kernel with `smem` bytes of dynamic shared memory,
+// asked once per kernel, block size and device; the kernel's limit is set to what
+// its largest block needs, whichever size comes first.
+template <auto* kernel>
+flp_status resident_blocks(int threads, size_t smem, size_t largest, int* per_sm) {
+    static int8_t known[kMaxDevices][1024 / 32 + 1] = {};
     int dev = 0;
-    FLP_CUDA(cudaGetDevice(&dev));
+    FLP_CUDA(cudaGetDevice(&dev));  // in range: step_device has run
     std::lock_guard<std::mutex> lk(g_mu);
-    const auto key = std::make_tuple(kernel, threads, dev);
-    const auto at = known.find(key);
-    if (at != known.end()) {
-        *per_sm = at->second;
-        return FLP_OK;
+    int8_t& at = known[dev][threads / 32];
+    if (at == 0) {
+        FLP_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(largest)));
+        int n = 0;
+        FLP_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
+        if (n < 1) return fail(FLP_ERR_UNSUPPORTED, "a block of the kernel does not fit an SM");
+        at = static_cast<int8_t>(n);
     }
-    FLP_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-    int n = 0;
-    FLP_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem));
-    if (n < 1) return fail(FLP_ERR_UNSUPPORTED, "a block of the kernel does not fit an SM");
-    known[key] = n;
-    *per_sm = n;
+    *per_sm = at;
     return FLP_OK;
 }
 
@@ -89,6 +85,14 @@ struct StreamShape {
     static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;
     static constexpr bool WARP = WARP_;
 };
+
+// Shared memory of `vecs` staged vectors per thread, beside them nothing (x: 0), as
+// many of a second matrix (1) or of its checkpoint (2).
+template <typename T, bool LOOSE>
+size_t norm_stage_bytes(int vecs, int threads, int x) {
+    const int one = Stage<T, LOOSE>::bytes(threads);
+    return static_cast<size_t>(vecs) * (one + (x == 0 ? 0 : x == 1 ? one : threads * wide_v<T>()));
+}
 
 template <typename T, typename F>
 flp_status norm_stream_shape(int64_t cols, F&& f) {
@@ -368,10 +372,11 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
         constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
         return norm_stream_shape<T>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
             using X = decltype(shape);
-            auto* kernel = flp_norm_fwd_stream_kernel<T, X::NV, X::S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
-            const size_t smem = static_cast<size_t>(X::S) * X::NV * Stage<T, LOOSE>::bytes(threads);
+            constexpr auto* kernel = flp_norm_fwd_stream_kernel<T, X::NV, X::S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
+            const size_t smem = norm_stage_bytes<T, LOOSE>(X::S * X::NV, threads, 0);
+            const size_t most = norm_stage_bytes<T, LOOSE>(X::S * X::NV, X::MAXT, 0);
             int per_sm = 0;
-            const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+            const flp_status r = resident_blocks<kernel>(threads, smem, most, &per_sm);
             if (r != FLP_OK) return r;
             const int64_t rows = X::WARP ? threads / 32 : 1;
             const int64_t blocks = std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count);
@@ -451,11 +456,11 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
                 using X_ = decltype(shape);
                 // two stages of an fp32 row above 8192 elements, dY and X, do not fit shared memory
                 constexpr int S = sizeof(T) == 4 && X_::NV == 8 ? 1 : X_::S;
-                auto* kernel = flp_norm_bwd_stream_kernel<T, X_::NV, S, CK, LOOSE, X_::WARP, X_::MAXT, X_::MINB>;
-                const int yb = Stage<T, LOOSE>::bytes(threads), xb = CK ? threads * wide_v<T>() : yb;
-                const size_t smem = static_cast<size_t>(S) * X_::NV * (yb + xb);
+                constexpr auto* kernel = flp_norm_bwd_stream_kernel<T, X_::NV, S, CK, LOOSE, X_::WARP, X_::MAXT, X_::MINB>;
+                const size_t smem = norm_stage_bytes<T, LOOSE>(S * X_::NV, threads, CK ? 2 : 1);
+                const size_t most = norm_stage_bytes<T, LOOSE>(S * X_::NV, X_::MAXT, CK ? 2 : 1);
                 int per_sm = 0;
-                const flp_status r = resident_blocks(reinterpret_cast<const void*>(kernel), threads, smem, &per_sm);
+                const flp_status r = resident_blocks<kernel>(threads, smem, most, &per_sm);
                 if (r != FLP_OK) return r;
                 blocks = norm_bwd_blocks(M, X_::WARP ? threads / 32 : 1, d->sm_count,
                                          std::min<int64_t>(kNormBwdBlocksPerSm, per_sm));
@@ -554,7 +559,8 @@ extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, c
     if ((st = tmap_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, ldy * 2, 64, 64)) != FLP_OK) return st;
     if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ws + w.off_x, w.Kp, M, w.Kp * 2, 64, 64)) != FLP_OK)
         return st;
-    const size_t part_rows = std::max<size_t>(1, static_cast<size_t>(w.rest) * w.splits) * PM;
+    const size_t part_rows = static_cast<size_t>(w.rest) * w.splits * PM;
+    if (part_rows > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
     // without split tiles (or without whole ones) one of the two output maps is
     // not used: it repeats the other
     if (w.rest &&

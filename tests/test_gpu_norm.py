@@ -148,6 +148,17 @@ def test_rows_of_one_value_large_means_and_bad_values(flp):
     assert torch.isfinite(db).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_widths_of_one_kernel_in_any_order(flp, dtype):
+    """Widths that share a kernel but not a block size, the widest before and after the others."""
+    for H in (8192, 5192, 6000, 8192, 4096, 2056, 4096, 16384, 8200, 16384, 5001, 8191):
+        x = torch.randn(3, H, device="cuda").to(dtype)
+        y, mean, rstd, kept = flp.layer_norm(x, checkpoint=True)
+        check_forward(x, None, None, 1e-5, y, mean, rstd)
+        dx, dw, db = flp.layer_norm_backward(y, x, None, mean, rstd)
+        check_backward(y, f64(x), None, mean, rstd, dx, dw, db)
+
+
 def test_no_rows(flp):
     x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
     y, mean, rstd, kept = flp.layer_norm(x, checkpoint=True)
