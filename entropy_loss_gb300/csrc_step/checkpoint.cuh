@@ -64,27 +64,20 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams 
         src[k] = static_cast<const T*>(p.x) + at.row[k] * p.ldx + at.col[k];
         if constexpr (LOOSE) {
             const Extent all = extent_of<T>(p.x, p.M, p.ldx, p.H);
-            if (at.row[k] > 0 && at.row[k] < p.M - 1 && WarpWords<T>::full(at.valid[k])) {
-                const char* a = WarpWords<T>::lane_word(src[k]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[k][i] = __ldcs(reinterpret_cast<const uint32_t*>(a + 128 * i));
-                if (N == 5) {
-                    r[k][N - 1] = 0;
-                    if ((threadIdx.x & 31) == 0 && (reinterpret_cast<uintptr_t>(src[k]) & 2))
-                        r[k][N - 1] = __ldcs(reinterpret_cast<const uint32_t*>(a + 512));
-                }
-            } else {
-                const WarpWords<T> w(src[k], at.valid[k]);
+            const WarpWords<T> w(src[k], at.valid[k]);
+            if (sizeof(T) == 4 || (at.row[k] > 0 && at.row[k] < p.M - 1)) {
+                r[k][0] = ld_global_4_at<0>(w.mine, w.has(0));
+                r[k][1] = ld_global_4_at<128>(w.mine, w.has(1));
+                r[k][2] = ld_global_4_at<256>(w.mine, w.has(2));
+                r[k][3] = ld_global_4_at<384>(w.mine, w.has(3));
+                if (N == 5) r[k][N - 1] = ld_global_4_at<512>(w.mine, w.has(4));
+            } else {  // the first or last row, of which a word may reach out of the matrix
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const char* a = w.word(i);
+                    const char* a = w.mine + 128 * i;
                     r[k][i] = 0;
-                    if (w.has(i)) {
-                        if (sizeof(T) == 4 || (a >= all.lo && a + 4 <= all.hi))
-                            r[k][i] = __ldcs(reinterpret_cast<const uint32_t*>(a));
-                        else
-                            r[k][i] = outer_word(a, all);
-                    }
+                    if (w.has(i))
+                        r[k][i] = a >= all.lo && a + 4 <= all.hi ? *reinterpret_cast<const uint32_t*>(a) : outer_word(a, all);
                 }
             }
         } else {

@@ -160,12 +160,17 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
             // zeros past the row stay zeros
             const uint64_t off = valid[k] > 0 ? minus : 0;
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                uint64_t o = off;
-                if constexpr (LOOSE) o = 2 * i + 1 < valid[k] ? off : 2 * i < valid[k] ? f2_pack(-mean, 0.f) : 0;
-                v[k][i] = f2_add(v[k][i], o);
-                acc = f2_fma(v[k][i], v[k][i], acc);
+            for (int i = 0; i < P; ++i) v[k][i] = f2_add(v[k][i], off);
+            if (LOOSE && valid[k] < V) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    float lo, hi;
+                    f2_unpack(v[k][i], lo, hi);
+                    v[k][i] = f2_pack(2 * i < valid[k] ? lo : 0.f, 2 * i + 1 < valid[k] ? hi : 0.f);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc = f2_fma(v[k][i], v[k][i], acc);
         }
         float rstd = f2_sum(acc);
         group_sum<WARP ? 0 : MAXT / 32>(rstd, red[1]);
@@ -250,8 +255,9 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
             ahead_x += p.step_x;
         cp_async_commit();
     };
-    // what a row needs beside its vectors, two rows ahead in registers (a miss takes
-    // longer than a row)
+    // what a row needs beside its vectors, AHEAD rows before it in registers: two, as a
+    // miss takes longer than a row, unless the loop's body is too long to have twice
+    constexpr int AHEAD = LOOSE ? 1 : 2;
     struct Few {
         float mean, rstd;
         uint32_t byte[CK ? NV : 1];
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     for (int s = 0; s < S; ++s) fetch(slot0 + s * NV * pitch_y, slot_x0 + s * NV * pitch_x);
     Few even{}, other{};
     fetch_few(even, rows_left > 0);
-    fetch_few(other, rows_left > 1);
+    if (AHEAD == 2) fetch_few(other, rows_left > 1);
     // where registers are short the weights wait in shared memory, each thread's own:
     // 32768 x 5120 bf16 228 -> 188 us from a checkpoint, 203 -> 178 us otherwise (at
     // 32768 x 4096 145 -> 122 us, but 138 -> 141 us)
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                 s1 = f2_fma(g, xh[k][i], s1);
             }
         }
-        fetch_few(few, rows_left > 2);
+        fetch_few(few, rows_left > AHEAD);
         float m1 = f2_sum(s0), m2 = f2_sum(s1);
         group_sum2<WARP ? 0 : MAXT / 32>(m1, m2, red[buf]);
         buf ^= 1;
@@ -383,7 +389,9 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     };
     while (rows_left > 0) {
         one_row(even);
-        if (rows_left > 0) one_row(other);
+        if constexpr (AHEAD == 2) {
+            if (rows_left > 0) one_row(other);
+        }
     }
     cp_async_wait<0>();
     griddep_launch_dependents();

@@ -111,8 +111,20 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool on)
 }
 // 4 bytes from src + OFF to dst + OFF.
 template <int OFF>
-__device__ __forceinline__ void cp_async_4_at(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %2], 4;" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
+__device__ __forceinline__ void cp_async_4_at(uint32_t dst, const void* src, bool on) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.ca.shared.global [%0 + %2], [%1 + %2], 4;\n\t}" ::"r"(dst),
+        "l"(src), "n"(OFF), "r"(static_cast<int>(on))
+        : "memory");
+}
+// The word at p + OFF, or 0.
+template <int OFF>
+__device__ __forceinline__ uint32_t ld_global_4_at(const void* p, bool on) {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.cs.b32 %0, [%1 + %2];\n\t}"
+                 : "=&r"(x)
+                 : "l"(p), "n"(OFF), "r"(static_cast<int>(on)));
+    return x;
 }
 __device__ __forceinline__ void st_global_16(void* p, uint4 u, bool on) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
@@ -182,35 +194,28 @@ __device__ __forceinline__ Extent extent_of(const void* base, long long rows, lo
     return {b, b + ((rows - 1) * pitch + cols) * static_cast<long long>(sizeof(T))};
 }
 
-// A warp's 32 consecutive vectors in a loose row: lane `lane` holds words lane,
-// lane + 32, ... from the first word on, the last of them (i = 4) lane 0 alone.
+// A warp's 32 consecutive vectors in a loose row, of which lane `lane` moves words
+// lane, lane + 32, ... counted from the one that holds the first element.
 template <typename T>
 struct WarpWords {
     static constexpr int V = wide_v<T>();
-    static constexpr int N = sizeof(T) == 2 ? 5 : 4;  // words per lane
-    const char* first;
-    int bytes;  // from the first word to the end of what the row holds of the vectors
+    static constexpr int N = sizeof(T) == 2 ? 5 : 4;  // words per lane, the last of five lane 0's alone
+    const char* mine;  // this lane's first word
+    int bytes;         // from there to the end of what the row holds of the vectors
+    bool odd;          // the first word starts with an element that is not the warp's
     // `src`: this lane's vector, of which and beyond the row holds `valid` elements
     __device__ __forceinline__ WarpWords(const T* src, int valid) {
         const int lane = threadIdx.x & 31;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(src - lane * V);
-        const int lead = static_cast<int>(at & (4 - sizeof(T)));
-        first = reinterpret_cast<const char*>(at) - lead;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+        odd = sizeof(T) == 2 && (at & 2);
+        // the vectors of two lanes are 16 bytes apart, their words 4
+        mine = reinterpret_cast<const char*>(at & ~static_cast<uintptr_t>(3)) - 12 * lane;
         const int left = min(32 * V, valid + lane * V);
-        bytes = left > 0 ? lead + left * static_cast<int>(sizeof(T)) : 0;
+        bytes = (left > 0 ? left * static_cast<int>(sizeof(T)) - 4 * lane : -512) + (odd ? 2 : 0);
     }
-    // whether the row holds all of the warp's 32 vectors
-    __device__ __forceinline__ static bool full(int valid) { return valid >= (32 - static_cast<int>(threadIdx.x & 31)) * V; }
-    // this lane's first word
-    __device__ __forceinline__ static const char* lane_word(const T* src) {
-        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(src) & ~static_cast<uintptr_t>(3)) -
-               12 * (threadIdx.x & 31);
-    }
-    __device__ __forceinline__ bool has(int i) const {
-        const int lane = threadIdx.x & 31;
-        return 4 * (lane + 32 * i) < bytes && (i < 4 || lane == 0);
-    }
-    __device__ __forceinline__ const char* word(int i) const { return first + 4 * ((threadIdx.x & 31) + 32 * i); }
+    // whether word i holds an element of the row, and whether it holds nothing else behind it
+    __device__ __forceinline__ bool has(int i) const { return bytes > 128 * i; }
+    __device__ __forceinline__ bool whole(int i) const { return bytes >= 128 * i + 4; }
 };
 
 // The one element inside the matrix of a bf16 word that reaches out of it, in its place.
@@ -241,6 +246,21 @@ __device__ __forceinline__ uint4 vec_of_words(uint32_t base, int valid, bool odd
     return u;
 }
 
+// The words of the matrix's first or last row, of which one may reach out of it
+// (out of line: two rows need it).
+template <typename T>
+__device__ __noinline__ void fetch_edge_words(uint32_t at, const T* src, int valid, const char* lo, const char* hi) {
+    const WarpWords<T> w(src, valid);
+#pragma unroll
+    for (int i = 0; i < WarpWords<T>::N; ++i) {
+        const char* p = w.mine + 128 * i;
+        const bool inside = p >= lo && p + 4 <= hi;
+        cp_async<4>(at + i * 128, p, w.has(i) && inside);
+        if (sizeof(T) == 2 && w.has(i) && !inside)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + i * 128), "r"(outer_word(p, Extent{lo, hi})) : "memory");
+    }
+}
+
 constexpr int WARP_WORDS_BYTES = 544;  // 129 words, and 16 bytes before them for a store
 
 template <typename T, bool LOOSE>
@@ -260,25 +280,16 @@ struct Stage {
         if constexpr (!LOOSE) {
             cp_async<16>(slot, src, valid > 0);
         } else {
-            const uint32_t lane = threadIdx.x & 31, at = slot + lane * 4;
-            if (!edge && WarpWords<T>::full(valid)) {
-                // this lane's first word: src and the warp's first vector are 16 lane bytes apart
-                const char* p = WarpWords<T>::lane_word(src);
-                cp_async_4_at<0>(at, p);
-                cp_async_4_at<128>(at, p);
-                cp_async_4_at<256>(at, p);
-                cp_async_4_at<384>(at, p);
-                if (SHIFT) cp_async<4>(at + 512, p + 512, lane == 0 && (reinterpret_cast<uintptr_t>(src) & 2));
-                return;
-            }
-            const WarpWords<T> w(src, valid);
-#pragma unroll
-            for (int i = 0; i < WarpWords<T>::N; ++i) {
-                const char* p = w.word(i);
-                const bool on = w.has(i), inside = !edge || (p >= all.lo && p + 4 <= all.hi);
-                cp_async<4>(at + i * 128, p, on && inside);
-                if (SHIFT && on && !inside)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + i * 128), "r"(outer_word(p, all)) : "memory");
+            const uint32_t at = slot + (threadIdx.x & 31) * 4;
+            if (edge) {
+                fetch_edge_words<T>(at, src, valid, all.lo, all.hi);
+            } else {
+                const WarpWords<T> w(src, valid);
+                cp_async_4_at<0>(at, w.mine, w.has(0));
+                cp_async_4_at<128>(at, w.mine, w.has(1));
+                cp_async_4_at<256>(at, w.mine, w.has(2));
+                cp_async_4_at<384>(at, w.mine, w.has(3));
+                if (SHIFT) cp_async_4_at<512>(at, w.mine, w.has(4));
             }
         }
     }
@@ -313,37 +324,23 @@ __device__ __forceinline__ void store_row_vec(T* dst, const uint4& u, int valid,
         const uint32_t vecs = stage + 16;
         st_shared_v4(vecs + lane * 16, u.x, u.y, u.z, u.w);
         __syncwarp();
-        const uint32_t o = sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(dst) & 2) ? 1 : 0;  // elements of the first word before ours
-        const uint32_t from = vecs + lane * 4, before = from - 4 * o;
-        if (WarpWords<T>::full(valid)) {
-            char* p = const_cast<char*>(WarpWords<T>::lane_word(dst));
+        const WarpWords<T> w(dst, valid);
+        char* p = const_cast<char*>(w.mine);
+        const uint32_t shift = w.odd ? 16u : 0u, from = vecs + lane * 4, before = from - (w.odd ? 4 : 0);
+        const bool leads = w.odd && lane == 0;  // its first word starts with another's element
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t x = ld_shared_4(from + 128 * i);
-                if (sizeof(T) == 2) x = __funnelshift_r(ld_shared_4(before + 128 * i), x, 16 * o);
-                if (i > 0 || lane > 0 || o == 0) *reinterpret_cast<uint32_t*>(p + 128 * i) = x;
-            }
-            if (sizeof(T) == 2 && o && lane == 0) {
-                *reinterpret_cast<unsigned short*>(p + 2) = static_cast<unsigned short>(ld_shared_4(from));
-                *reinterpret_cast<unsigned short*>(p + 512) = static_cast<unsigned short>(ld_shared_4(from + 508) >> 16);
-            }
-        } else {
-            const WarpWords<T> w(dst, valid);
-            char* first = const_cast<char*>(w.word(0));
-#pragma unroll
-            for (int i = 0; i < WarpWords<T>::N; ++i) {
-                if (!w.has(i)) continue;
-                const int j = lane + 32 * i;
-                char* p = first + 128 * i;
-                const bool lower = j > 0 || o == 0, upper = 4 * j + 4 <= w.bytes;
-                const uint32_t hi = ld_shared_4(from + 128 * i);
-                const uint32_t x = __funnelshift_r(ld_shared_4(before + 128 * i), hi, 16 * o);
-                if (lower && upper)
-                    *reinterpret_cast<uint32_t*>(p) = x;
-                else if (lower)
-                    *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(x);
-                else if (upper)
-                    *reinterpret_cast<unsigned short*>(p + 2) = static_cast<unsigned short>(hi);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x = ld_shared_4(from + 128 * i);
+            if (sizeof(T) == 2) x = __funnelshift_r(ld_shared_4(before + 128 * i), x, shift);
+            st_global_4(p + 128 * i, x, w.whole(i) && !(i == 0 && leads));
+        }
+        if (sizeof(T) == 2) {
+            // single elements: the first, behind another's, and the last, before another's
+            if (leads && w.bytes >= 4) *reinterpret_cast<unsigned short*>(p + 2) = static_cast<unsigned short>(ld_shared_4(from));
+            if ((w.bytes & 127) == 2 && w.bytes > 0) {
+                const int i = w.bytes >> 7;
+                *reinterpret_cast<unsigned short*>(p + 128 * i) = static_cast<unsigned short>(
+                    __funnelshift_r(ld_shared_4(before + 128 * i), ld_shared_4(from + 128 * i), shift));
             }
         }
         __syncwarp();
