@@ -63,23 +63,8 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams 
     for (int k = 0; k < CK_PACK_N; ++k) {
         src[k] = static_cast<const T*>(p.x) + at.row[k] * p.ldx + at.col[k];
         if constexpr (LOOSE) {
-            const Extent all = extent_of<T>(p.x, p.M, p.ldx, p.H);
-            const WarpWords<T> w(src[k], at.valid[k]);
-            if (sizeof(T) == 4 || (at.row[k] > 0 && at.row[k] < p.M - 1)) {
-                r[k][0] = ld_global_4_at<0>(w.mine, w.has(0));
-                r[k][1] = ld_global_4_at<128>(w.mine, w.has(1));
-                r[k][2] = ld_global_4_at<256>(w.mine, w.has(2));
-                r[k][3] = ld_global_4_at<384>(w.mine, w.has(3));
-                if (N == 5) r[k][N - 1] = ld_global_4_at<512>(w.mine, w.has(4));
-            } else {  // the first or last row, of which a word may reach out of the matrix
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const char* a = w.mine + 128 * i;
-                    r[k][i] = 0;
-                    if (w.has(i))
-                        r[k][i] = a >= all.lo && a + 4 <= all.hi ? *reinterpret_cast<const uint32_t*>(a) : outer_word(a, all);
-                }
-            }
+            load_words<T>(r[k], src[k], at.valid[k], at.row[k] == 0 || at.row[k] >= p.M - 1,
+                          extent_of<T>(p.x, p.M, p.ldx, p.H));
         } else {
             const uint4 u = at.valid[k] > 0 ? __ldcs(reinterpret_cast<const uint4*>(src[k])) : make_uint4(0, 0, 0, 0);
             r[k][0] = u.x, r[k][1] = u.y, r[k][2] = u.z, r[k][3] = u.w;
@@ -87,17 +72,11 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams 
     }
 #pragma unroll
     for (int k = 0; k < CK_PACK_N; ++k) {
-        uint4 u = make_uint4(r[k][0], r[k][1], r[k][2], r[k][3]);
-        if constexpr (LOOSE) {
-            const uint32_t base = smem_addr(words) + threadIdx.x / 32 * WARP_WORDS_BYTES, lane = threadIdx.x & 31;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i < 4 || lane == 0)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (lane + 32 * i) * 4), "r"(r[k][i]) : "memory");
-            __syncwarp();
-            u = vec_of_words<T>(base, at.valid[k], sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(src[k]) & 2));
-            __syncwarp();
-        }
+        uint4 u;
+        if constexpr (LOOSE)
+            u = settle_words<T>(r[k], src[k], at.valid[k], smem_addr(words) + threadIdx.x / 32 * WARP_WORDS_BYTES);
+        else
+            u = make_uint4(r[k][0], r[k][1], r[k][2], r[k][3]);
         uint32_t w[P / 2];
         uint64_t v[P];
 #pragma unroll
@@ -141,6 +120,26 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_unpack_kernel(const CkParam
         uint64_t v[P];
         ck_pairs<V>(w[k], ck_step(byte[k]), v);
         store_row_vec<T, LOOSE>(static_cast<T*>(p.x) + at.row[k] * p.ldx + at.col[k], Pairs<T>::put(v), at.valid[k], stage);
+    }
+}
+
+// Loose bf16 rows copied to rows of Hp elements at `q`, 16-byte aligned, zeros behind
+// each row's H elements.
+__global__ void __launch_bounds__(CK_THREADS) flp_align_rows_kernel(const CkParams p) {
+    __shared__ __align__(16) uint8_t words[Stage<bf16, true>::bytes(CK_THREADS)];
+    const CkPlaces<bf16, CK_PACK_N> at(p);
+    const bf16* src[CK_PACK_N];
+    uint32_t r[CK_PACK_N][WarpWords<bf16>::N];
+#pragma unroll
+    for (int k = 0; k < CK_PACK_N; ++k) {
+        src[k] = static_cast<const bf16*>(p.x) + at.row[k] * p.ldx + at.col[k];
+        load_words<bf16>(r[k], src[k], at.valid[k], at.row[k] == 0 || at.row[k] >= p.M - 1,
+                         extent_of<bf16>(p.x, p.M, p.ldx, p.H));
+    }
+#pragma unroll
+    for (int k = 0; k < CK_PACK_N; ++k) {
+        const uint4 u = settle_words<bf16>(r[k], src[k], at.valid[k], smem_addr(words) + threadIdx.x / 32 * WARP_WORDS_BYTES);
+        st_global_16(reinterpret_cast<bf16*>(p.q) + at.row[k] * p.Hp + at.col[k], u, at.on[k]);
     }
 }
 

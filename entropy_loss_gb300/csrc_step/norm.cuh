@@ -53,6 +53,9 @@ struct NormBwdParams {
     void* dx;
     long long lddx;
     float* part;  // [gridDim.x][2][H] fp32 partial sums of dw and db
+    bool cluster;  // the blocks are one cluster and join their sums themselves, into
+    float* dw;     // these (NULL: not written)
+    float* db;
     // from a group's row to its next, in elements: rows, dy, x, dx, q, scale
     long long step, step_dy, step_x, step_dx, step_q, step_s;
 };
@@ -397,9 +400,11 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     griddep_launch_dependents();
     // this block's sums; with a row per warp, the warps join first (the ring is free)
     float* join = reinterpret_cast<float*>(ring);
+    float* sums = join + (WARP ? (MAXT / 32) * (NV * 32 * V) : 0);  // [2][H] of a cluster's block
+    if (p.cluster) __syncthreads();  // every warp is done with the ring
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        float* out = p.part + (static_cast<long long>(blockIdx.x) * 2 + which) * p.H;
+        float* out = p.cluster ? sums + which * p.H : p.part + (static_cast<long long>(blockIdx.x) * 2 + which) * p.H;
         if constexpr (WARP) __syncthreads();
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -425,6 +430,21 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                 out[c] = a;
             }
         }
+    }
+    if (p.cluster) {
+        cluster_sync();
+        const unsigned blocks_in = gridDim.x;
+        for (unsigned c = blockIdx.x * blockDim.x + threadIdx.x; c < 2u * p.H; c += blocks_in * blockDim.x) {
+            float a = 0.f;
+            for (unsigned r = 0; r < blocks_in; ++r) {
+                float v;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_addr(sums + c), r)) : "memory");
+                a += v;
+            }
+            float* to = c < static_cast<unsigned>(p.H) ? p.dw : p.db;
+            if (to) to[c < static_cast<unsigned>(p.H) ? c : c - p.H] = a;
+        }
+        cluster_sync();  // no block leaves while its sums are read
     }
 }
 

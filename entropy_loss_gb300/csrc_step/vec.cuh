@@ -263,6 +263,41 @@ __device__ __noinline__ void fetch_edge_words(uint32_t at, const T* src, int val
 
 constexpr int WARP_WORDS_BYTES = 544;  // 129 words, and 16 bytes before them for a store
 
+// A warp's 32 vectors in a loose row straight into registers: first the words (so that
+// several loads can be under way), then this lane's vector, through the warp's shared
+// memory at `base`.
+template <typename T>
+__device__ __forceinline__ void load_words(uint32_t (&r)[WarpWords<T>::N], const T* src, int valid, bool edge,
+                                           const Extent& all) {
+    const WarpWords<T> w(src, valid);
+    if (sizeof(T) == 4 || !edge) {
+        r[0] = ld_global_4_at<0>(w.mine, w.has(0));
+        r[1] = ld_global_4_at<128>(w.mine, w.has(1));
+        r[2] = ld_global_4_at<256>(w.mine, w.has(2));
+        r[3] = ld_global_4_at<384>(w.mine, w.has(3));
+        if (sizeof(T) == 2) r[WarpWords<T>::N - 1] = ld_global_4_at<512>(w.mine, w.has(4));
+    } else {  // the matrix's first or last row, of which a word may reach out of it
+#pragma unroll
+        for (int i = 0; i < WarpWords<T>::N; ++i) {
+            const char* a = w.mine + 128 * i;
+            r[i] = 0;
+            if (w.has(i)) r[i] = a >= all.lo && a + 4 <= all.hi ? *reinterpret_cast<const uint32_t*>(a) : outer_word(a, all);
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 settle_words(const uint32_t (&r)[WarpWords<T>::N], const T* src, int valid, uint32_t base) {
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < WarpWords<T>::N; ++i)
+        if (i < 4 || lane == 0)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (lane + 32 * i) * 4), "r"(r[i]) : "memory");
+    __syncwarp();
+    const uint4 u = vec_of_words<T>(base, valid, sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(src) & 2));
+    __syncwarp();
+    return u;
+}
+
 template <typename T, bool LOOSE>
 struct Stage {
     static constexpr bool SHIFT = LOOSE && sizeof(T) == 2;

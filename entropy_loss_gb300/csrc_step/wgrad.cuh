@@ -346,50 +346,47 @@ __global__ void __launch_bounds__(WJ_THREADS) flp_wgrad_join_kernel(const WgradJ
     griddep_wait();
     const bool bad = (*p.err & ERR_TIMEOUT) != 0;
     const float* base = p.part + static_cast<long long>(tile) * p.g.splits * (PM * 2 * BN);
-    // dW rows are 16-byte (fp32) or 8-byte (bf16) aligned four columns at a time
-    const bool vec = p.g.K % 4 == 0;
     static_assert(WJ_ROWS * 2 * BN / 4 == WJ_THREADS, "four columns a thread");
-    {
-        const int r = r0 + threadIdx.x / (2 * BN / 4), c = threadIdx.x % (2 * BN / 4) * 4;
-        const int n = t.n0 + r, k = t.k0 + c;
-        if (n >= p.g.N || k >= p.g.K) return;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float* at = base + static_cast<long long>(r) * (2 * BN) + c;
+    __shared__ __align__(16) float rows[WJ_ROWS][2 * BN];
+    const int in_block = threadIdx.x / (2 * BN / 4), at = threadIdx.x % (2 * BN / 4);
+    const int n = t.n0 + r0 + in_block, k = t.k0 + 4 * at;
+    const bool on = n < p.g.N && k < p.g.K;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+        const float* from = base + static_cast<long long>(r0 + in_block) * (2 * BN) + 4 * at;
 #pragma unroll 8
         for (int j = 0; j < p.g.splits; ++j) {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(at + static_cast<long long>(j) * (PM * 2 * BN)));
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(from + static_cast<long long>(j) * (PM * 2 * BN)));
             s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
         }
-        float v[4] = {s.x, s.y, s.z, s.w};
+        if (bad) s.x = s.y = s.z = s.w = __uint_as_float(0x7fc00000u);
+    }
+    if (p.g.K % 4 == 0) {  // dW rows are aligned to four columns (16 bytes, or 8 in bf16)
+        if (!on) return;
         const long long o = static_cast<long long>(n) * p.g.K + k;
-        const int live = min(4, p.g.K - k);
-        if (bad) v[0] = v[1] = v[2] = v[3] = __uint_as_float(0x7fc00000u);
         if (p.g.bf16_out) {
-            bf16* d = static_cast<bf16*>(p.dw) + o;
-            if (vec) {
-                *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-            } else {
-                for (int j = 0; j < live; ++j) d[j] = __float2bfloat16_rn(v[j]);
-            }
+            *reinterpret_cast<uint2*>(static_cast<bf16*>(p.dw) + o) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
         } else {
-            float* d = static_cast<float*>(p.dw) + o;
-            if (vec) {
-                float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (p.add) old = *reinterpret_cast<float4*>(d);
-                *reinterpret_cast<float4*>(d) = make_float4(old.x + v[0], old.y + v[1], old.z + v[2], old.w + v[3]);
-            } else {
-                for (int j = 0; j < live; ++j) d[j] = (p.add ? d[j] : 0.f) + v[j];
-            }
+            float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.dw) + o);
+            float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.add) old = *d;
+            *d = make_float4(old.x + s.x, old.y + s.y, old.z + s.z, old.w + s.w);
+        }
+    } else {  // through shared memory, so that neighbouring threads write neighbouring columns
+        *reinterpret_cast<float4*>(&rows[in_block][4 * at]) = s;
+        __syncthreads();
+        if (n >= p.g.N) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = at + i * (2 * BN / 4);
+            if (t.k0 + c >= p.g.K) break;
+            const long long o = static_cast<long long>(n) * p.g.K + t.k0 + c;
+            if (p.g.bf16_out)
+                static_cast<bf16*>(p.dw)[o] = __float2bfloat16_rn(rows[in_block][c]);
+            else
+                static_cast<float*>(p.dw)[o] = (p.add ? static_cast<float*>(p.dw)[o] : 0.f) + rows[in_block][c];
         }
     }
-}
-
-// dY rows at a pitch and base that TMA can read (both multiples of 16 bytes).
-__global__ void __launch_bounds__(256) flp_wgrad_align_kernel(const bf16* __restrict__ src, long long ld, int N,
-                                                              bf16* __restrict__ dst, long long ldd) {
-    const long long row = blockIdx.x;
-    for (int c = threadIdx.x; c < ldd; c += 256)
-        dst[row * ldd + c] = c < N ? src[row * ld + c] : __float2bfloat16_rn(0.f);
 }
 
 }  // namespace flp

@@ -433,7 +433,7 @@ flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, const void* wei
                           int param_dtype, int64_t M, int64_t H, float eps, void* Y, int64_t ldy,
                           float* mean, float* rstd, void* q, void* scale, void* stream);
 
-/* Workspace bytes of flp_layer_norm_backward on the current device. */
+/* Workspace bytes of flp_layer_norm_backward on the current device (0 for few rows). */
 flp_status flp_layer_norm_workspace(int64_t M, int64_t H, size_t* bytes);
 
 /*

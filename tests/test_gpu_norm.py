@@ -61,7 +61,7 @@ def check_backward(dy, X, w, mean, rstd, dx, dw, db):
 
 
 SIZES = [(1, 1), (1, 8), (3, 31), (5, 33), (7, 255), (2, 256), (129, 257), (64, 512), (31, 768), (300, 1000), (33, 1023),
-         (400, 1024), (9, 2048), (17, 4096), (700, 4104), (11, 5120), (4, 8192), (5, 12001), (3, 16384)]
+         (400, 1024), (700, 256), (600, 511), (1500, 33), (512, 512), (64, 2048), (65, 2048), (9, 2048), (17, 4096), (700, 4104), (11, 5120), (4, 8192), (5, 12001), (3, 16384)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -279,6 +279,8 @@ def test_refusals(flp):
         flp.layer_norm_backward(y, kept._replace(cols=96), w, mean, rstd)
     with pytest.raises(ValueError):
         flp.layer_norm_backward(y, x, w, mean[:3], rstd)
+    x = torch.randn(1000, 64, device="cuda")
+    y, mean, rstd = flp.layer_norm(x, w)
     with pytest.raises(flp.FlpError) as e:
         flp.layer_norm_backward(y, x, w, mean, rstd, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == flp.FLP_ERR_WORKSPACE
