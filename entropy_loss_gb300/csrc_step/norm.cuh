@@ -258,9 +258,11 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
             ahead_x += p.step_x;
         cp_async_commit();
     };
-    // what a row needs beside its vectors, AHEAD rows before it in registers: two, as a
-    // miss takes longer than a row, unless the loop's body is too long to have twice
-    constexpr int AHEAD = LOOSE ? 1 : 2;
+    // what a row needs beside its vectors, AHEAD rows before it in registers: two where
+    // rows are short or registers are left for it (a miss takes longer than a row), else
+    // one (32768 x 4096 bf16 139 -> 127 us, 16384 x 8192 160 -> 135 us, 32768 x 5120
+    // 173 -> 158 us; from a checkpoint 188 -> 173 us, but at 32768 x 4096 122 -> 126 us)
+    constexpr int AHEAD = !LOOSE && (WARP || (CK && MAXT != 320)) ? 2 : 1;
     struct Few {
         float mean, rstd;
         uint32_t byte[CK ? NV : 1];

@@ -96,10 +96,13 @@ flp_status resident_blocks(int threads, size_t smem, size_t largest, int* per_sm
 // row (about 130 instructions) is spread over enough of them: 8 elements a thread
 // (twice the warps) took 12 to 50 % longer at 32768 x 4096, 32 (half the warps)
 // 17 to 130 %.  Rows of up to 512 elements go to one warp, which needs no block
-// barrier; rows above 8192 take more elements a thread.  Two blocks of up to 320
-// threads must fit an SM, which bounds the registers (three: forward with a
-// checkpoint 119 against 107 us, backward 185 against 138 us).  The stages put
-// 64 KiB or so per SM in flight in every shape.
+// barrier; rows above 8192 take more elements a thread.  Two blocks of up to TWO
+// threads must fit an SM, which bounds the registers (three of up to 256: forward
+// with a checkpoint 119 against 107 us, backward 185 against 138 us).  The bf16
+// forward has registers to spare: two blocks of 384 threads instead of one take
+// 16384 x 6144 from 82 to 64 us, with a checkpoint from 104 to 83 us (fp32 from 125
+// to 136), two of 512 take 16384 x 8192 from 96 to 85 us (with a checkpoint from 131
+// to 153).  The stages put 64 KiB or so per SM in flight in every shape.
 template <int NV_, int S_, bool WARP_, int MAXT_, int MINB_>
 struct StreamShape {
     static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;
@@ -114,7 +117,7 @@ size_t norm_stage_bytes(int vecs, int threads, int x) {
     return static_cast<size_t>(vecs) * (one + (x == 0 ? 0 : x == 1 ? one : threads * wide_v<T>()));
 }
 
-template <typename T, typename F>
+template <typename T, int TWO, typename F>
 flp_status norm_stream_shape(int64_t cols, F&& f) {
     constexpr int V = wide_v<T>(), N2 = 16 / V;  // N2 vectors of V = 16 elements
     constexpr int S = V == 8 ? 4 : 2;
@@ -126,7 +129,9 @@ flp_status norm_stream_shape(int64_t cols, F&& f) {
     const int threads = static_cast<int>(cdiv(vecs, 32 * N2) * 32);
     if (threads <= 256) return f(StreamShape<N2, S, false, 256, 2>{}, threads);
     if (threads <= 320) return f(StreamShape<N2, S, false, 320, 2>{}, threads);
-    if (threads <= 512) return f(StreamShape<N2, S, false, 512, 1>{}, threads);
+    if constexpr (TWO >= 384)
+        if (threads <= 384) return f(StreamShape<N2, S, false, 384, 2>{}, threads);
+    if (threads <= 512) return f(StreamShape<N2, S, false, 512, TWO >= 512 ? 2 : 1>{}, threads);
     return f(StreamShape<2 * N2, 2, false, 512, 1>{}, static_cast<int>(cdiv(vecs, 64 * N2) * 32));
 }
 
@@ -408,7 +413,8 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
     auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
         using T = decltype(t);
         constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-        return norm_stream_shape<T>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
+        constexpr int TWO = sizeof(T) == 4 ? 320 : CK ? 384 : 512;
+        return norm_stream_shape<T, TWO>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
             using X = decltype(shape);
             constexpr auto* kernel = flp_norm_fwd_stream_kernel<T, X::NV, X::S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
             const size_t smem = norm_stage_bytes<T, LOOSE>(X::S * X::NV, threads, 0);
@@ -496,7 +502,7 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
         auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
             using T = decltype(t);
             constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-            return norm_stream_shape<T>(p.H, [&](auto shape, int threads) -> flp_status {
+            return norm_stream_shape<T, 320>(p.H, [&](auto shape, int threads) -> flp_status {
                 using X_ = decltype(shape);
                 // two stages of an fp32 row above 8192 elements, dY and X, do not fit shared memory
                 constexpr int S = sizeof(T) == 4 && X_::NV == 8 ? 1 : X_::S;
