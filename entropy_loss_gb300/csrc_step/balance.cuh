@@ -52,7 +52,7 @@ struct BalParams {
 };
 
 // An integer that orders floats: larger float, larger key (NaN excluded; the
-// two zeros are equal).  -inf has the key below BAL_LOWEST.
+// two zeros are equal).  The lowest finite value's is BAL_LOWEST, -inf's the one below.
 constexpr uint32_t BAL_LOWEST = 0x00800000u;
 __device__ __forceinline__ uint32_t order_key(float z) {
     const uint32_t b = __float_as_uint(z + 0.f);  // -0 -> +0
@@ -63,15 +63,34 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
+// The larger of two, NaN if either is; and the largest over a row's lanes.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 template <int L>
-__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
+__device__ __forceinline__ float group_max_nan(float v) {
     if constexpr (L == 32) {
-        return __reduce_max_sync(0xffffffffu, v);
+        float m;
+        asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+        return m;
     } else {
 #pragma unroll
-        for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        for (int o = L / 2; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
         return v;
     }
+}
+// Largest and smallest over a warp (no NaN).
+__device__ __forceinline__ float warp_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+__device__ __forceinline__ float warp_min(float v) {
+    float m;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
@@ -92,36 +111,41 @@ __device__ __forceinline__ int expert(int l, int i) {
     return i / V * (L * V) + l * V + i % V;
 }
 
-// A lane's logits as loaded (V per access), and in fp32.
+// A lane's logits as loaded (V per access), or -inf, and in fp32.
 template <typename T, int V>
 struct Logits;
 template <>
 struct Logits<float, 1> {
     float u;
+    __device__ __forceinline__ void none() { u = -INFINITY; }
     __device__ __forceinline__ void load(const float* p) { u = __ldg(p); }
     __device__ __forceinline__ void to(float* v) const { v[0] = u; }
 };
 template <>
 struct Logits<float, 2> {
     float2 u;
+    __device__ __forceinline__ void none() { u = make_float2(-INFINITY, -INFINITY); }
     __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float2*>(p)); }
     __device__ __forceinline__ void to(float* v) const { v[0] = u.x, v[1] = u.y; }
 };
 template <>
 struct Logits<float, 4> {
     float4 u;
+    __device__ __forceinline__ void none() { u = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ void load(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void to(float* v) const { v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w; }
 };
 template <>
 struct Logits<bf16, 1> {
     unsigned short u;
+    __device__ __forceinline__ void none() { u = 0xff80; }
     __device__ __forceinline__ void load(const bf16* p) { u = __ldg(reinterpret_cast<const unsigned short*>(p)); }
     __device__ __forceinline__ void to(float* v) const { v[0] = __uint_as_float(static_cast<uint32_t>(u) << 16); }
 };
 template <>
 struct Logits<bf16, 2> {
     uint32_t u;
+    __device__ __forceinline__ void none() { u = 0xff80ff80u; }
     __device__ __forceinline__ void load(const bf16* p) { u = __ldg(reinterpret_cast<const uint32_t*>(p)); }
     __device__ __forceinline__ void to(float* v) const {
         v[0] = __uint_as_float(u << 16), v[1] = __uint_as_float(u & 0xffff0000u);
@@ -130,6 +154,7 @@ struct Logits<bf16, 2> {
 template <>
 struct Logits<bf16, 4> {
     uint2 u;
+    __device__ __forceinline__ void none() { u = make_uint2(0xff80ff80u, 0xff80ff80u); }
     __device__ __forceinline__ void load(const bf16* p) { u = __ldg(reinterpret_cast<const uint2*>(p)); }
     __device__ __forceinline__ void to(float* v) const {
         v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
@@ -156,10 +181,10 @@ __device__ __forceinline__ void store_grad(bf16* p, const float* v) {
         *p = __float2bfloat16_rn(v[0]);
 }
 
-// Adds 1 to cnt[i] for the row's k largest keys, ties to the lowest expert.
-// One expert per lane, L lanes: a lane's rank is the number of lanes before it.
+// Whether this lane's expert is among its row's k largest keys, ties to the lowest
+// expert.  One expert per lane, L lanes: a lane's rank is the number of lanes before it.
 template <int L>
-__device__ __forceinline__ void choose_by_rank(uint32_t key, int l, int k, int& cnt) {
+__device__ __forceinline__ bool chosen_by_rank(uint32_t key, int l, int k) {
     int before = 0;
 #pragma unroll
     for (int o = 1; o < L; ++o) {
@@ -167,55 +192,70 @@ __device__ __forceinline__ void choose_by_rank(uint32_t key, int l, int k, int& 
         const uint32_t other = __shfl_sync(0xffffffffu, key, from, L);
         before += (other > key || (other == key && from < l)) ? 1 : 0;
     }
-    cnt += (key >= BAL_LOWEST && before < k) ? 1 : 0;
+    return key >= BAL_LOWEST && before < k;
 }
 
-// The same for a warp with NE experts per lane.  The k-th largest of the lanes'
-// maxima bounds the k-th largest key from below: keys above the bound are
-// candidates, and the smallest are dropped until k are left (about one for 256
-// experts and k = 8).  Above 16 the experts are taken one at a time, which drops
-// nothing when many of the largest share a lane.
+// The same for a warp with NE experts per lane (no NaN, no +inf): a lane's chosen
+// experts are marked in fields of 4 bits, eight to a word, so that adding the word
+// counts them all at once (and its set bits are their number).
+//
+// The k-th largest of the lanes' maxima bounds the k-th largest logit from below: those
+// at or above the bound are candidates, and the smallest are dropped until k are left
+// (about one for 256 experts and k = 8).  Above 16 the experts are taken one at a
+// time, which drops nothing when many of the largest share a lane.
+// `top`: the lane's largest logit, `most`: the row's.
+template <int NE>
+__host__ __device__ constexpr int bal_words() { return (NE + 7) / 8; }
+
 template <int NE, int V>
-__device__ __forceinline__ void choose(const uint32_t (&key)[NE], uint32_t top, int l, int k, int (&cnt)[NE]) {
+__device__ __forceinline__ void choose(const float (&v)[NE], float top, float most, int l, int k,
+                                       uint32_t (&marks)[bal_words<NE>()]) {
     constexpr uint32_t ALL = 0xffffffffu;
-    uint32_t bound = BAL_LOWEST;
-    int left = k;   // experts still to take among the keys equal to `tie`
-    uint32_t tie = 0;
+    constexpr float LOWEST = -3.402823466e38f;
+    int left = k;  // experts still to take: all, or among the logits equal to `tie`
+    float tie = 0.f;
+#pragma unroll
+    for (int w = 0; w < bal_words<NE>(); ++w) marks[w] = 0;
     if (k <= 16) {
-        for (int j = 0; j < k; ++j) {
-            bound = __reduce_max_sync(ALL, top);
-            if (top == bound) top = 0;
+        float bound = most;
+        for (int j = 1; j < k; ++j) {
+            if (top == bound) top = -INFINITY;
+            bound = warp_max(top);
         }
-        bound = max(bound, BAL_LOWEST);
-        auto count = [&]() {  // keys at or above the bound
+        bound = fmaxf(bound, LOWEST);
+        auto mark = [&]() {  // logits at or above the bound
             int mine = 0;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) mine += key[i] >= bound ? 1 : 0;
+            for (int w = 0; w < bal_words<NE>(); ++w) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 8 * w; i < NE && i < 8 * w + 8; ++i) m += v[i] >= bound ? 1u << (4 * (i % 8)) : 0u;
+                marks[w] = m;
+                mine += __popc(m);
+            }
             return __reduce_add_sync(ALL, mine);
         };
-        int total = count();
+        int total = mark();
         left = 0;
         while (total > k) {
-            // keys below the bound wrap around to the largest distances
-            uint32_t low = ALL;
+            float low = INFINITY;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) low = min(low, key[i] - bound);
-            low = bound + __reduce_min_sync(ALL, low);
-            bound = low + 1;
-            total = count();
+            for (int i = 0; i < NE; ++i)
+                if (v[i] >= bound) low = fminf(low, v[i]);
+            low = warp_min(low);
+            bound = key_value(order_key(low) + 1);
+            total = mark();
             if (total < k) {  // only some of the smallest fit
                 tie = low;
                 left = k - total;
             }
         }
-#pragma unroll
-        for (int i = 0; i < NE; ++i) cnt[i] += key[i] >= bound ? 1 : 0;
+        if (left == 0) return;
     }
-    if (left == 0) return;
-    // one at a time: the largest key that is left (the tie above, or any for large k)
+    // one at a time: the lowest expert of the ties, or the largest that is left
     uint32_t rest[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) rest[i] = tie == 0 ? key[i] : key[i] == tie ? tie : 0u;
+    for (int i = 0; i < NE; ++i) rest[i] = k > 16 || v[i] == tie ? order_key(v[i]) : 0u;
     for (int j = 0; j < left; ++j) {
         uint32_t m = rest[0];
 #pragma unroll
@@ -230,7 +270,7 @@ __device__ __forceinline__ void choose(const uint32_t (&key)[NE], uint32_t top, 
 #pragma unroll
         for (int i = 0; i < NE; ++i)
             if (static_cast<uint32_t>(expert<32, V>(l, i)) == at) {
-                ++cnt[i];
+                marks[i / 8] += 1u << (4 * (i % 8));
                 rest[i] = 0;
             }
     }
@@ -257,21 +297,22 @@ __device__ __forceinline__ BalSums bal_sums(uint32_t* dyn, int E) {
 template <typename T, int L, int NE, int V>
 struct RowLogits {
     Logits<T, V> u[NE / V];
-    __device__ __forceinline__ void load(const BalParams& p, long long row, int l) {
-        const T* z = static_cast<const T*>(p.z) + row * p.ld;
+    __device__ __forceinline__ RowLogits() {
+#pragma unroll
+        for (int i = 0; i < NE / V; ++i) u[i].none();
+    }
+    // `z`: the row's logits from this lane's first on
+    __device__ __forceinline__ void load(const BalParams& p, const T* z, bool on, int l) {
 #pragma unroll
         for (int i = 0; i < NE; i += V)
-            if (row < p.T && expert<L, V>(l, i) < p.E) u[i / V].load(z + expert<L, V>(l, i));
+            if (on && expert<L, V>(l, i) < p.E) u[i / V].load(z + i * L);
     }
-    __device__ __forceinline__ void to(const BalParams& p, int l, bool wanted, float (&v)[NE]) const {
+    __device__ __forceinline__ void to(bool wanted, float (&v)[NE]) const {
 #pragma unroll
         for (int i = 0; i < NE; i += V) {
-            if (wanted && expert<L, V>(l, i) < p.E) {
-                u[i / V].to(v + i);
-            } else {
+            u[i / V].to(v + i);
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[i + j] = -INFINITY;
-            }
+            for (int j = 0; j < V; ++j) v[i + j] = wanted ? v[i + j] : -INFINITY;
         }
     }
 };
@@ -288,49 +329,63 @@ __device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& 
     __syncthreads();
     const int l = threadIdx.x % L, sub = threadIdx.x / L;
     float psum[NE] = {};
-    int cnt[NE] = {};
+    // experts chosen in up to 15 rows (fewer than 32 lanes a row: in all rows)
+    uint32_t cnt[bal_words<NE>()] = {};
+    int since = 0;
+    auto count = [&]() {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const int e = expert<L, V>(l, i);
+            const int c = NE == 1 ? cnt[0] : (cnt[i / 8] >> (4 * (i % 8))) & 15u;
+            if (c && e < p.E) atomicAdd(&sums.c[e], c);  // integers: any order gives the same sum
+        }
+    };
     int live_rows = 0;
     const long long stride = static_cast<long long>(blocks) * RPB;
+    const long long stride_z = stride * p.ld;
     // every lane of a warp makes the same trips: the row groups of a warp move together
     long long base = static_cast<long long>(block) * RPB;
+    const T* z = static_cast<const T*>(p.z) + (base + sub) * p.ld + l * V;
     RowLogits<T, L, NE, V> next;
-    next.load(p, base + sub, l);
+    next.load(p, z, base + sub < p.T, l);
     bool kept_next = base + sub < p.T && (!p.mask || p.mask[base + sub]);
     for (int own = sub; base < p.T; base += stride, own += RPB) {
         const long long row = base + sub;
         const bool kept = kept_next;
         float v[NE];
-        next.to(p, l, kept, v);
-        next.load(p, row + stride, l);
-        kept_next = row + stride < p.T && (!p.mask || p.mask[row + stride]);
-        bool odd = false;  // NaN or +inf
-        uint32_t key[NE], top = 0;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            odd |= !(v[i] < INFINITY);
-            key[i] = order_key(v[i]);
-            top = max(top, key[i]);
+        next.to(L == 32 || kept, v);
+        z += stride_z;
+        const bool more = row + stride < p.T;
+        next.load(p, z, more, l);
+        kept_next = more && (!p.mask || p.mask[row + stride]);
+        if (L == 32 && !kept) {  // the whole warp's row
+            if (l == 0 && row < p.T) stat[kLocal ? own : row] = make_float2(0.f, 0.f);
+            continue;
         }
-        if constexpr (L == 32) {
-            odd = __any_sync(0xffffffffu, odd);
+        float top = v[0];
+#pragma unroll
+        for (int i = 1; i < NE; ++i) top = max_nan(top, v[i]);
+        const float most = group_max_nan<L>(top);
+        // a row without any logit gets maximum 0: all its exponentials are 0; with a NaN
+        // or +inf in a row some are NaN
+        const bool live = !(most == -INFINITY), whole = most < INFINITY;
+        const float m = live ? most : 0.f;
+        // the difference is formed first: its error grows with its own size alone
+        float ex[NE], s = 0.f;
+        if constexpr (NE == 1) {
+            s = ex[0] = ex2_approx((v[0] - m) * LOG2E);
         } else {
-            const uint32_t votes = __ballot_sync(0xffffffffu, odd) >> ((threadIdx.x & 31) / L * L);
-            odd = (votes & ((1u << L) - 1u)) != 0u;
-        }
-        const uint32_t most = group_umax<L>(top);
-        const bool live = odd || most >= BAL_LOWEST;
-        // a row without any logit gets maximum 0: all its exponentials are 0
-        const float m = live ? key_value(most) : 0.f;
-        float s = 0.f;
-        float ex[NE];
+            const uint64_t minus = f2_splat(-m), log2e = f2_splat(LOG2E);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            // the difference is formed first: its error grows with its own size alone
-            ex[i] = ex2_approx((v[i] - m) * LOG2E);
-            s += ex[i];
+            for (int i = 0; i < NE; i += 2) {
+                f2_unpack(f2_mul(f2_add(f2_pack(v[i], v[i + 1]), minus), log2e), ex[i], ex[i + 1]);
+                ex[i] = ex2_approx(ex[i]);
+                ex[i + 1] = ex2_approx(ex[i + 1]);
+                s += ex[i] + ex[i + 1];
+            }
         }
         s = group_sum<L>(s);
-        const float inv = odd ? __uint_as_float(0x7fc00000u) : live ? rcp_approx(s) : 0.f;
+        const float inv = live ? rcp_approx(s) : 0.f;
 #pragma unroll
         for (int i = 0; i < NE; ++i) psum[i] = fmaf(ex[i], inv, psum[i]);
         if (l == 0 && row < p.T) {
@@ -341,21 +396,26 @@ __device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& 
             if (live)
                 for (int j = l; j < p.k; j += L) {
                     const long long e = p.experts[row * p.k + j];
-                    if (e >= 0 && e < p.E) atomicAdd(&sums.c[e], 1);  // integers: any order gives the same sum
+                    if (e >= 0 && e < p.E) atomicAdd(&sums.c[e], 1);
                 }
         } else if constexpr (L < 32) {
-            choose_by_rank<L>(odd ? 0u : key[0], l, p.k, cnt[0]);
-        } else {
-            if (live && !odd) choose<NE, V>(key, top, l, p.k, cnt);  // the same in the whole warp
+            cnt[0] += chosen_by_rank<L>(whole ? order_key(v[0]) : 0u, l, p.k) ? 1u : 0u;
+        } else if (live && whole) {  // the same in the whole warp
+            uint32_t marks[bal_words<NE>()];
+            choose<NE, V>(v, top, most, l, p.k, marks);
+#pragma unroll
+            for (int w = 0; w < bal_words<NE>(); ++w) cnt[w] += marks[w];
+            if (++since == 15) {
+                count();
+#pragma unroll
+                for (int w = 0; w < bal_words<NE>(); ++w) cnt[w] = 0;
+                since = 0;
+            }
         }
     }
-    // counts in any order, the fp32 sums in a fixed one: lanes of a warp that
-    // hold the same experts, then the warps
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        const int e = expert<L, V>(l, i);
-        if (e < p.E && cnt[i]) atomicAdd(&sums.c[e], cnt[i]);
-    }
+    // the fp32 sums in a fixed order: lanes of a warp that hold the same experts, then
+    // the warps
+    count();
     if (l == 0 && live_rows) atomicAdd(sums.n, live_rows);
 #pragma unroll
     for (int i = 0; i < NE; ++i)
@@ -449,16 +509,19 @@ __device__ __forceinline__ void balance_grad(const BalParams& p, const float2* s
     const int l = threadIdx.x % L, sub = threadIdx.x / L;
     const long long stride = static_cast<long long>(blocks) * RPB;
     long long base = static_cast<long long>(block) * RPB;
+    const long long stride_z = stride * p.ld;
+    const T* z = static_cast<const T*>(p.z) + (base + sub) * p.ld + l * V;
     RowLogits<T, L, NE, V> next;
-    next.load(p, base + sub, l);
+    next.load(p, z, base + sub < p.T, l);
     float2 st_next = base + sub < p.T ? stat[kLocal ? sub : base + sub] : make_float2(0.f, 0.f);
     for (int own = sub; base < p.T; base += stride, own += RPB) {
         const long long row = base + sub;
         const float2 st = st_next;
         float pr[NE];
         // a row that is not live (1 / sum = 0) has exponentials of 0 whatever it holds
-        next.to(p, l, !(st.y == 0.f), pr);
-        next.load(p, row + stride, l);
+        next.to(!(st.y == 0.f), pr);
+        z += stride_z;
+        next.load(p, z, row + stride < p.T, l);
         if (row + stride < p.T) st_next = stat[kLocal ? own + RPB : row + stride];
         float dot = 0.f;
 #pragma unroll
