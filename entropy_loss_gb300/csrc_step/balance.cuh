@@ -20,6 +20,14 @@
 // A row belongs to L lanes of a warp, lane l holding vectors l, l + L, ... of V
 // experts: the sums per expert then stay in the same registers from row to row.
 // The next row's logits are loaded before this row's are worked on.
+//
+// The floor is one read of the logits and one write of the gradient.  Few tokens are
+// bound by the launch and the cluster's exchange (64 x 8: 8 us), many by the rows'
+// pass, whose choice of experts takes most of the instructions: 65536 x 256 fp32, top
+// 8, takes 51 us, about 30 in the rows' pass (65 % of the issue slots; its 67 MB would
+// take 10), 4 in the join and 18 in the gradient's, against a floor of 20 us; top 24
+// takes 134 us.  The gradient needs the counts of all rows, and so a second read of the
+// logits (of which an SM's share, 441 KB in that case, does not fit its shared memory).
 #pragma once
 #include "vec.cuh"
 
@@ -27,6 +35,7 @@ namespace flp {
 
 constexpr int BAL_MAX_E = 1024;
 constexpr int BAL_THREADS = 512;
+constexpr int BAL_BOUND_K = 24;  // experts of a row up to which they are chosen by a bound
 constexpr int BAL_CLUSTER = 8;  // blocks of the one-launch form
 constexpr int BAL_CLUSTER_TRIPS = 4;  // trips of its row loop up to which it is the faster one
 
@@ -201,8 +210,9 @@ __device__ __forceinline__ bool chosen_by_rank(uint32_t key, int l, int k) {
 //
 // The k-th largest of the lanes' maxima bounds the k-th largest logit from below: those
 // at or above the bound are candidates, and the smallest are dropped until k are left
-// (about one for 256 experts and k = 8).  Above 16 the experts are taken one at a
-// time, which drops nothing when many of the largest share a lane.
+// (about one for 256 experts and k = 8).  Above BAL_BOUND_K the experts are taken one at
+// a time, which drops nothing when many of the largest share a lane (65536 x 256 fp32:
+// k = 20 takes 99 us by the bound, 132 one at a time, k = 24 134 and 149).
 // `top`: the lane's largest logit, `most`: the row's.
 template <int NE>
 __host__ __device__ constexpr int bal_words() { return (NE + 7) / 8; }
@@ -216,7 +226,7 @@ __device__ __forceinline__ void choose(const float (&v)[NE], float top, float mo
     float tie = 0.f;
 #pragma unroll
     for (int w = 0; w < bal_words<NE>(); ++w) marks[w] = 0;
-    if (k <= 16) {
+    if (k <= BAL_BOUND_K) {
         float bound = most;
         for (int j = 1; j < k; ++j) {
             if (top == bound) top = -INFINITY;
@@ -255,7 +265,7 @@ __device__ __forceinline__ void choose(const float (&v)[NE], float top, float mo
     // one at a time: the lowest expert of the ties, or the largest that is left
     uint32_t rest[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) rest[i] = k > 16 || v[i] == tie ? order_key(v[i]) : 0u;
+    for (int i = 0; i < NE; ++i) rest[i] = k > BAL_BOUND_K || v[i] == tie ? order_key(v[i]) : 0u;
     for (int j = 0; j < left; ++j) {
         uint32_t m = rest[0];
 #pragma unroll
@@ -292,6 +302,11 @@ __device__ __forceinline__ BalSums bal_sums(uint32_t* dyn, int E) {
     s.n = s.c + E;
     return s;
 }
+
+// Whether the next row's logits are loaded before this row is worked on: not where
+// that spills (1024 experts).
+template <int NE>
+constexpr bool BAL_AHEAD = NE <= 16;
 
 // The lane's logits of a row; -inf where there is no expert.
 template <typename T, int L, int NE, int V>
@@ -347,16 +362,17 @@ __device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& 
     long long base = static_cast<long long>(block) * RPB;
     const T* z = static_cast<const T*>(p.z) + (base + sub) * p.ld + l * V;
     RowLogits<T, L, NE, V> next;
-    next.load(p, z, base + sub < p.T, l);
+    if (BAL_AHEAD<NE>) next.load(p, z, base + sub < p.T, l);
     bool kept_next = base + sub < p.T && (!p.mask || p.mask[base + sub]);
     for (int own = sub; base < p.T; base += stride, own += RPB) {
         const long long row = base + sub;
         const bool kept = kept_next;
         float v[NE];
+        if (!BAL_AHEAD<NE>) next.load(p, z, kept, l);
         next.to(L == 32 || kept, v);
         z += stride_z;
         const bool more = row + stride < p.T;
-        next.load(p, z, more, l);
+        if (BAL_AHEAD<NE>) next.load(p, z, more, l);
         kept_next = more && (!p.mask || p.mask[row + stride]);
         if (L == 32 && !kept) {  // the whole warp's row
             if (l == 0 && row < p.T) stat[kLocal ? own : row] = make_float2(0.f, 0.f);
@@ -370,6 +386,31 @@ __device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& 
         // or +inf in a row some are NaN
         const bool live = !(most == -INFINITY), whole = most < INFINITY;
         const float m = live ? most : 0.f;
+        auto choice = [&]() {
+            if (p.experts) {
+                if (live)
+                    for (int j = l; j < p.k; j += L) {
+                        const long long e = p.experts[row * p.k + j];
+                        if (e >= 0 && e < p.E) atomicAdd(&sums.c[e], 1);
+                    }
+            } else if constexpr (L < 32) {
+                cnt[0] += chosen_by_rank<L>(whole ? order_key(v[0]) : 0u, l, p.k) ? 1u : 0u;
+            } else if (live && whole) {  // the same in the whole warp
+                uint32_t marks[bal_words<NE>()];
+                choose<NE, V>(v, top, most, l, p.k, marks);
+#pragma unroll
+                for (int w = 0; w < bal_words<NE>(); ++w) cnt[w] += marks[w];
+                if (++since == 15) {
+                    count();
+#pragma unroll
+                    for (int w = 0; w < bal_words<NE>(); ++w) cnt[w] = 0;
+                    since = 0;
+                }
+            }
+        };
+        // 16 or more experts a lane: first, while their logits are all that is held
+        // (1024 experts 310 -> 173 us with the loads below; 256 would go from 53 to 54.5 us)
+        if constexpr (NE >= 16) choice();
         // the difference is formed first: its error grows with its own size alone
         float ex[NE], s = 0.f;
         if constexpr (NE == 1) {
@@ -392,26 +433,7 @@ __device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& 
             stat[kLocal ? own : row] = make_float2(m, inv);
             live_rows += live;
         }
-        if (p.experts) {
-            if (live)
-                for (int j = l; j < p.k; j += L) {
-                    const long long e = p.experts[row * p.k + j];
-                    if (e >= 0 && e < p.E) atomicAdd(&sums.c[e], 1);
-                }
-        } else if constexpr (L < 32) {
-            cnt[0] += chosen_by_rank<L>(whole ? order_key(v[0]) : 0u, l, p.k) ? 1u : 0u;
-        } else if (live && whole) {  // the same in the whole warp
-            uint32_t marks[bal_words<NE>()];
-            choose<NE, V>(v, top, most, l, p.k, marks);
-#pragma unroll
-            for (int w = 0; w < bal_words<NE>(); ++w) cnt[w] += marks[w];
-            if (++since == 15) {
-                count();
-#pragma unroll
-                for (int w = 0; w < bal_words<NE>(); ++w) cnt[w] = 0;
-                since = 0;
-            }
-        }
+        if constexpr (NE < 16) choice();
     }
     // the fp32 sums in a fixed order: lanes of a warp that hold the same experts, then
     // the warps
@@ -512,16 +534,17 @@ __device__ __forceinline__ void balance_grad(const BalParams& p, const float2* s
     const long long stride_z = stride * p.ld;
     const T* z = static_cast<const T*>(p.z) + (base + sub) * p.ld + l * V;
     RowLogits<T, L, NE, V> next;
-    next.load(p, z, base + sub < p.T, l);
+    if (BAL_AHEAD<NE>) next.load(p, z, base + sub < p.T, l);
     float2 st_next = base + sub < p.T ? stat[kLocal ? sub : base + sub] : make_float2(0.f, 0.f);
     for (int own = sub; base < p.T; base += stride, own += RPB) {
         const long long row = base + sub;
         const float2 st = st_next;
         float pr[NE];
         // a row that is not live (1 / sum = 0) has exponentials of 0 whatever it holds
+        if (!BAL_AHEAD<NE>) next.load(p, z, row < p.T, l);
         next.to(!(st.y == 0.f), pr);
         z += stride_z;
-        next.load(p, z, row + stride < p.T, l);
+        if (BAL_AHEAD<NE>) next.load(p, z, row + stride < p.T, l);
         if (row + stride < p.T) st_next = stat[kLocal ? own + RPB : row + stride];
         float dot = 0.f;
 #pragma unroll

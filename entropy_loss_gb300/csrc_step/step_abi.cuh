@@ -322,13 +322,15 @@ flp_status balance_shape(int64_t E, bool vec, F&& f) {
         FLP_SHAPE(32, 2, 2)
         FLP_SHAPE(32, 4, 4)
         FLP_SHAPE(32, 8, 4)
+        FLP_SHAPE(32, 16, 4)
+        FLP_SHAPE(32, 32, 4)
     } else {
         FLP_SHAPE(32, 2, 1)
         FLP_SHAPE(32, 4, 1)
         FLP_SHAPE(32, 8, 1)
+        FLP_SHAPE(32, 16, 1)
+        FLP_SHAPE(32, 32, 1)
     }
-    FLP_SHAPE(32, 16, 1)
-    FLP_SHAPE(32, 32, 1)
 #undef FLP_SHAPE
     return fail(FLP_ERR_UNSUPPORTED, "at most 1024 experts");
 }

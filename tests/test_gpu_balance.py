@@ -66,6 +66,34 @@ def test_loss_gradient_and_counts(flp, T, E, k, dtype):
     check(flp, z, k, coef=0.01, mask=(torch.rand(T, generator=g) < 0.7).cuda())
 
 
+@pytest.mark.parametrize("E,k", [(30, 5), (33, 20), (64, 24), (130, 17), (256, 24), (256, 25), (300, 32), (1000, 20)])
+def test_many_chosen_of_odd_rows(flp, E, k):
+    """More experts a token than any lane's share, and rows that hold ties, few
+    numbers, the type's lowest value, or values that are none."""
+    g = torch.Generator().manual_seed(E + k)
+    z = torch.randn(600, E, generator=g)
+    z[10:20] = torch.randint(0, 3, (10, E), generator=g).float()
+    z[20:30, : E // 2] = -float("inf")
+    z[30] = -float("inf")
+    z[31, 3:] = -float("inf")
+    z[32] = torch.finfo(torch.float32).min
+    z[33, ::2] = torch.finfo(torch.float32).min
+    z[34, 1::2] = 0.0
+    z[34, ::2] = -0.0
+    z[35] = z[35].sort().values               # the largest are neighbours
+    z[36] *= 1e-40                            # subnormal numbers
+    check(flp, z.cuda(), k)
+    check(flp, z.to(torch.bfloat16).cuda(), k)
+    z[40, 0], z[41, E - 1], z[42, 1] = float("nan"), float("inf"), -float("nan")
+    check(flp, z.cuda(), k)
+
+
+def test_many_rows_of_one_warp(flp):
+    g = torch.Generator().manual_seed(4)
+    for T, E, k in ((90000, 33, 5), (90000, 20, 20), (200000, 8, 2)):
+        check(flp, torch.randn(T, E, generator=g).cuda(), k)
+
+
 def test_ties_go_to_the_lowest_index(flp):
     for E in (3, 8, 40, 200):
         z = torch.zeros(50, E, device="cuda")
