@@ -512,11 +512,11 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
                 // a cluster's block holds its warps' sums (a row per warp) and its own after the rows
                 constexpr size_t kJoin = X_::WARP ? static_cast<size_t>(X_::MAXT) * X_::NV * wide_v<T>() * 4 : 0;
                 constexpr size_t kMostSums = kJoin + 8ull * (X_::WARP ? 32 : X_::MAXT) * X_::NV * wide_v<T>();
-                const size_t smem = std::max(norm_stage_bytes<T, LOOSE>(S * X_::NV, threads, CK ? 2 : 1),
-                                             cluster ? kJoin + 8 * static_cast<size_t>(H) : 0);
+                const size_t staged = norm_stage_bytes<T, LOOSE>(S * X_::NV, threads, CK ? 2 : 1);
+                const size_t smem = std::max(staged, cluster ? kJoin + 8 * static_cast<size_t>(H) : 0);
                 const size_t most = std::max(norm_stage_bytes<T, LOOSE>(S * X_::NV, X_::MAXT, CK ? 2 : 1), kMostSums);
                 int per_sm = 0;
-                const flp_status r = resident_blocks<kernel>(threads, smem, most, &per_sm);
+                const flp_status r = resident_blocks<kernel>(threads, staged, most, &per_sm);
                 if (r != FLP_OK) return r;
                 blocks = cluster ? kNormBwdCluster
                                  : norm_bwd_blocks(M, X_::WARP ? threads / 32 : 1, d->sm_count,

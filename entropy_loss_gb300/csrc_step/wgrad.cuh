@@ -15,6 +15,12 @@
 // of the last, incomplete round would leave most pairs idle for a whole tile,
 // so their rows of dY and X^ are split into S runs that go to separate fp32
 // partial tiles, which a small kernel joins in a fixed order (no atomics).
+//
+// Bound by the tensor cores: 8192 x 8192 x 5120 (dY rows, dW rows, dW columns) with an
+// fp32 dW takes 424 us, 1620 TFLOP/s or 86 % of the measured matrix rate: 392 us in this
+// kernel (the tensor pipe busy 75 % of it; the rest is draining the accumulators between
+// the four runs of each tile), 21 us unpacking and 11 us in the join.  A bf16 dW, which
+// needs no runs, takes 377 us.
 #pragma once
 #include "../csrc/kernels.cuh"
 #include "vec.cuh"

@@ -813,6 +813,7 @@ class FusedBalanceLoss(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g, _):
         grad, = ctx.saved_tensors
+        # with bf16 logits g and the product are rounded to bf16, as in any chain of bf16 gradients
         return grad * g.to(grad.dtype), None, None, None, None
 
 
