@@ -24,8 +24,8 @@
 // The floor is one read of the logits and one write of the gradient.  Few tokens are
 // bound by the launch and the cluster's exchange (64 x 8: 8 us), many by the rows'
 // pass, whose choice of experts takes most of the instructions: 65536 x 256 fp32, top
-// 8, takes 51 us, about 30 in the rows' pass (65 % of the issue slots; its 67 MB would
-// take 10), 4 in the join and 18 in the gradient's, against a floor of 20 us; top 24
+// 8, takes 51 us, 28 of them in the rows' pass (64 % of the issue slots; its 67 MB would
+// take 10), the rest in the join and the gradient's, against a floor of 20 us; top 24
 // takes 134 us.  The gradient needs the counts of all rows, and so a second read of the
 // logits (of which an SM's share, 441 KB in that case, does not fit its shared memory).
 #pragma once

@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
 // rows stay in registers until the last row, then go to the block's row of `part`.
 // 32768 x 4096 bf16 127 us, 94 % of the measured copy rate; from a checkpoint 122 us,
 // 82 % (its bytes are turned into pairs, 54 % of the issue slots); 32768 x 5120 from a
-// checkpoint 173 us, 71 %.  Above 8192 elements a row and its sums exceed the
-// registers: 16384 x 16384 runs at 44 to 74 %.
+// checkpoint 173 us, 72 %.  Above 8192 elements a row and its sums exceed the
+// registers: 8192 x 16384 runs at 43 to 74 %.
 template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
     using X = Stage<T, LOOSE>;
