@@ -207,6 +207,10 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
     cp_async_wait<0>();
 }
 
+// Whether a thread has more elements of a row than its registers hold sums for.
+template <typename T, int NV>
+__host__ __device__ constexpr bool norm_bwd_wide() { return NV * wide_v<T>() > 16; }
+
 // Backward: both sums of a row in one exchange, so one barrier a row; the sums over
 // rows stay in registers until the last row, then go to the block's row of `part`.
 // 32768 x 4096 bf16 127 us, 94 % of the measured copy rate; from a checkpoint 122 us,
@@ -312,9 +316,12 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     // where registers are short the weights wait in shared memory, each thread's own:
     // 32768 x 5120 bf16 228 -> 188 us from a checkpoint, 203 -> 178 us otherwise (at
     // 32768 x 4096 145 -> 122 us, but 138 -> 141 us)
-    constexpr bool W_SHARED = !WARP && (CK || MAXT == 320);
+    // (above 8192 columns the sums of dy wait there too)
+    constexpr bool DB_SHARED = norm_bwd_wide<T, NV>();
+    constexpr bool W_SHARED = !WARP && (CK || MAXT == 320 || (DB_SHARED && sizeof(T) == 2));
     __shared__ ulonglong2 w_shared[W_SHARED ? NV * P / 2 : 1][W_SHARED ? MAXT : 1];
-    uint64_t w_kept[W_SHARED ? 1 : NV][P], dw[NV][P] = {}, db[NV][P] = {};
+    __shared__ ulonglong2 db_shared[DB_SHARED ? NV * P / 2 : 1][DB_SHARED ? MAXT : 1];
+    uint64_t w_kept[W_SHARED ? 1 : NV][P], dw[NV][P] = {}, db[DB_SHARED ? 1 : NV][P] = {};
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         uint64_t w[P];
@@ -325,6 +332,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                 w_shared[(k * P + i) / 2][threadIdx.x] = make_ulonglong2(w[i], w[i + 1]);
             else
                 w_kept[k][i] = w[i], w_kept[k][i + 1] = w[i + 1];
+            if constexpr (DB_SHARED) db_shared[(k * P + i) / 2][threadIdx.x] = make_ulonglong2(0, 0);
         }
     }
     auto weight = [&](int k, uint64_t (&w)[P]) {
@@ -373,10 +381,17 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                 const uint64_t d = Pairs<T>::get(ry[k], i);
                 xh[k][i] = f2_mul(f2_add(xh[k][i], minus), r2);
                 dw[k][i] = f2_fma(d, xh[k][i], dw[k][i]);
-                db[k][i] = f2_add(db[k][i], d);
+                if constexpr (!DB_SHARED) db[k][i] = f2_add(db[k][i], d);
                 const uint64_t g = f2_mul(d, w[i]);
                 s0 = f2_add(s0, g);
                 s1 = f2_fma(g, xh[k][i], s1);
+            }
+            if constexpr (DB_SHARED) {
+#pragma unroll
+                for (int i = 0; i < P; i += 2) {
+                    ulonglong2& u = db_shared[(k * P + i) / 2][threadIdx.x];
+                    u = make_ulonglong2(f2_add(u.x, Pairs<T>::get(ry[k], i)), f2_add(u.y, Pairs<T>::get(ry[k], i + 1)));
+                }
             }
         }
         fetch_few(few, rows_left > AHEAD);
@@ -425,8 +440,15 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
             float* at = WARP ? join + sub * (NV * 32 * V) + col : out + col;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
+                uint64_t of_dy;
+                if constexpr (DB_SHARED) {
+                    const ulonglong2 u = db_shared[(k * P + i) / 2][threadIdx.x];
+                    of_dy = i % 2 ? u.y : u.x;
+                } else {
+                    of_dy = db[k][i];
+                }
                 float2 a;
-                f2_unpack(which ? db[k][i] : dw[k][i], a.x, a.y);
+                f2_unpack(which ? of_dy : dw[k][i], a.x, a.y);
                 if (!LOOSE || WARP) {
                     if (WARP || valid[k] > 0) *reinterpret_cast<float2*>(at + 2 * i) = a;
                 } else {

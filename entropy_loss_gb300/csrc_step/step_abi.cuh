@@ -168,10 +168,11 @@ int64_t norm_bwd_blocks(int64_t M, int64_t rows_per_block, int sm_count, int64_t
 // Few rows: one cluster of blocks joins its column sums through distributed shared
 // memory, without the workspace and the second launch (a row per warp up to 512
 // columns, else per block): a call of 256 x 256 takes 18.5 us instead of 22, on the
-// GPU 5.0 instead of 4.4; at the rule's end, 64 x 4096, 10.1 instead of 6.9.
+// GPU 5.0 instead of 4.4; at the rule's end, 64 x 4096, 10.1 instead of 6.9.  Above
+// 8192 columns the sums do not fit beside the rows.
 constexpr int kNormBwdCluster = 8, kNormBwdClusterTrips = 8;
 bool norm_bwd_cluster(int64_t M, int64_t H) {
-    return M <= kNormBwdCluster * kNormBwdClusterTrips * (H <= 512 ? 8 : 1);
+    return M <= kNormBwdCluster * kNormBwdClusterTrips * (H <= 512 ? 8 : 1) && H <= 8192;
 }
 
 constexpr int64_t kNormBwdBlocksPerSm = 8;  // the most any shape uses: what the workspace query allows for
@@ -506,12 +507,15 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
             constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
             return norm_stream_shape<T, 320>(p.H, [&](auto shape, int threads) -> flp_status {
                 using X_ = decltype(shape);
-                // two stages of an fp32 row above 8192 elements, dY and X, do not fit shared memory
-                constexpr int S = sizeof(T) == 4 && X_::NV == 8 ? 1 : X_::S;
+                // above 8192 columns one stage fits beside the weights and sums; two of aligned
+                // bf16 rows with a checkpoint
+                constexpr bool WIDE = norm_bwd_wide<T, X_::NV>();
+                constexpr int S = WIDE && !(CK && !LOOSE && sizeof(T) == 2) ? 1 : X_::S;
                 constexpr auto* kernel = flp_norm_bwd_stream_kernel<T, X_::NV, S, CK, LOOSE, X_::WARP, X_::MAXT, X_::MINB>;
                 // a cluster's block holds its warps' sums (a row per warp) and its own after the rows
                 constexpr size_t kJoin = X_::WARP ? static_cast<size_t>(X_::MAXT) * X_::NV * wide_v<T>() * 4 : 0;
-                constexpr size_t kMostSums = kJoin + 8ull * (X_::WARP ? 32 : X_::MAXT) * X_::NV * wide_v<T>();
+                constexpr size_t kMostSums =
+                    WIDE ? 0 : kJoin + 8ull * (X_::WARP ? 32 : X_::MAXT) * X_::NV * wide_v<T>();
                 const size_t staged = norm_stage_bytes<T, LOOSE>(S * X_::NV, threads, CK ? 2 : 1);
                 const size_t smem = std::max(staged, cluster ? kJoin + 8 * static_cast<size_t>(H) : 0);
                 const size_t most = std::max(norm_stage_bytes<T, LOOSE>(S * X_::NV, X_::MAXT, CK ? 2 : 1), kMostSums);

@@ -96,6 +96,14 @@ def test_checkpoint_of_the_input(flp, M, H, dtype):
     check_backward(dy, ref.unpack(q, scale, H), w, mean, rstd, dx, dw, db)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,H", [(500, 8200), (330, 10001), (460, 12288), (200, 16384), (170, 16383)])
+def test_several_wide_rows_a_block(flp, M, H, dtype):
+    """Rows whose sums over rows do not all stay in registers, more than the blocks."""
+    test_forward_and_backward(flp, M, H, dtype)
+    test_checkpoint_of_the_input(flp, M, H, dtype)
+
+
 @pytest.mark.parametrize("pitch,offset", [(0, 0), (8, 0), (8, 8), (5, 0), (0, 1), (3, 2)])
 @pytest.mark.parametrize("H", [64, 1000, 1001])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
