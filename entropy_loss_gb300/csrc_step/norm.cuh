@@ -215,8 +215,10 @@ __host__ __device__ constexpr bool norm_bwd_wide() { return NV * wide_v<T>() > 1
 // rows stay in registers until the last row, then go to the block's row of `part`.
 // 32768 x 4096 bf16 127 us, 94 % of the measured copy rate; from a checkpoint 122 us,
 // 82 % (its bytes are turned into pairs, 54 % of the issue slots); 32768 x 5120 from a
-// checkpoint 173 us, 72 %.  Above 8192 elements a row and its sums exceed the
-// registers: 8192 x 16384 runs at 43 to 74 %.
+// checkpoint 173 us, 72 %.  Above 8192 columns the weights (bf16) and the sums of dy
+// wait in shared memory, which leaves room for one row in flight: 8192 x 16384 bf16
+// 158 us, 75 % (265 us with both in registers, which spilled), from a checkpoint
+// 180 us, 55 %; fp32 274 us, 87 % (319 us).
 template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
     using X = Stage<T, LOOSE>;
@@ -276,8 +278,9 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     // what a row needs beside its vectors, AHEAD rows before it in registers: two where
     // rows are short or registers are left for it (a miss takes longer than a row), else
     // one (32768 x 4096 bf16 139 -> 127 us, 16384 x 8192 160 -> 135 us, 32768 x 5120
-    // 173 -> 158 us; from a checkpoint 188 -> 173 us, but at 32768 x 4096 122 -> 126 us)
-    constexpr int AHEAD = !LOOSE && (WARP || (CK && MAXT != 320)) ? 2 : 1;
+    // 173 -> 158 us; from a checkpoint 188 -> 173 us, 8192 x 16384 210 -> 180 us, but at
+    // 32768 x 4096 122 -> 126 us)
+    constexpr int AHEAD = !LOOSE && (WARP || (CK && MAXT != 320 && !norm_bwd_wide<T, NV>())) ? 2 : 1;
     struct Few {
         float mean, rstd;
         uint32_t byte[CK ? NV : 1];
