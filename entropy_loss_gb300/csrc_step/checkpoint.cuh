@@ -129,7 +129,9 @@ __global__ void __launch_bounds__(CK_THREADS) flp_ck_unpack_kernel(const CkParam
 }
 
 // Loose bf16 rows copied to rows of Hp elements at `q`, 16-byte aligned, zeros behind
-// each row's H elements.
+// each row's H elements: TMA reads the weight gradient's dY from there.  Bound by the
+// words' loads as in the kernels above (loose rows of 4095 are packed at 64 % of the
+// copy rate), a few percent of the contraction that follows.
 __global__ void __launch_bounds__(CK_THREADS) flp_align_rows_kernel(const CkParams p) {
     __shared__ __align__(16) uint8_t words[Stage<bf16, true>::bytes(CK_THREADS)];
     const CkPlaces<bf16, CK_PACK_N> at(p);
