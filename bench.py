@@ -120,11 +120,15 @@ def strip_comments(src: str) -> str:
 
 
 def kernel_sources_digest() -> str:
-    """sha256 over the CUDA sources' names and code (sorted by name), comments
-    left out: a profile stays valid while only the comments change."""
+    """sha256 over the compiler's flags and the CUDA sources' names and code
+    (sorted by name), comments left out: a profile stays valid while only the
+    comments change."""
     import glob
     import hashlib
+
+    from entropy_loss_gb300 import build
     h = hashlib.sha256()
+    h.update("\0".join(build.FLAGS).encode() + b"\0")
     for f in sorted(glob.glob(os.path.join(ROOT, "entropy_loss_gb300", "csrc", "*"))):
         with open(f, encoding="utf-8") as fh:
             code = strip_comments(fh.read())
