@@ -2,7 +2,7 @@
 // rows, and read back.  vec.cuh has the block arithmetic.
 //
 // One pass, bound by the bytes: 32768 x 4096 bf16 is written in 62 us (97 % of the
-// measured copy rate) and read back in 67 us (90 %).  A thread takes a vector, so a
+// measured copy rate) and read back in 60 us (100 %).  A thread takes a vector, so a
 // block of 32 columns is four (bf16) or eight (fp32) neighbouring lanes, whose largest
 // magnitude is exchanged by shuffles; no shared memory and nothing read twice.
 #pragma once
@@ -24,10 +24,13 @@ struct CkParams {
 
 constexpr int CK_THREADS = 256;
 // Vectors in flight per thread: writing a checkpoint 4 (32768 x 4096 bf16 62 us; 2:
-// 68, 8: 66), reading one, which stores twice what it loads, 2 (67 us; 1:
-// 72, 4: 75, 8: 94).
+// 68, 8: 66), reading one, which stores twice what it loads, 2 (4 took 12 % longer, 1
+// 7 %).
 constexpr int CK_PACK_N = 4;
 constexpr int CK_UNPACK_N = 2;
+// Blocks an SM must hold of the writing kernel: 5 bound the registers of aligned rows
+// (bf16 65 -> 62 us, fp32 110 -> 101 us); loose ones need more (0: no bound).
+constexpr int ck_pack_blocks(bool loose) { return loose ? 0 : 5; }
 
 // Row and first column of vector j.
 template <int V>
@@ -58,7 +61,7 @@ struct CkPlaces {
 };
 
 template <typename T, bool LOOSE>
-__global__ void __launch_bounds__(CK_THREADS) flp_ck_pack_kernel(const CkParams p) {
+__global__ void __launch_bounds__(CK_THREADS, ck_pack_blocks(LOOSE)) flp_ck_pack_kernel(const CkParams p) {
     constexpr int P = Pairs<T>::N, N = LOOSE ? WarpWords<T>::N : 4;
     __shared__ __align__(16) uint8_t words[LOOSE ? Stage<T, true>::bytes(CK_THREADS) : 16];
     const CkPlaces<T, CK_PACK_N> at(p);

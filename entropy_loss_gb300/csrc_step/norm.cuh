@@ -71,7 +71,7 @@ struct NormBwdParams {
 //
 // The floor is one read and one write of the rows.  What is left above it is issue
 // slots (45 to 60 % of them are used) and the two row sums, each a block barrier.
-// Forward at 32768 x 4096 bf16: 96 us, 83 % of the measured copy rate; with a
+// Forward at 32768 x 4096 bf16: 82 us, 96 % of the measured copy rate; with a
 // checkpoint 106 us, 94 %; one row of 4096 6 us (launch, one read, two barriers).
 
 template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
@@ -211,14 +211,24 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
 template <typename T, int NV>
 __host__ __device__ constexpr bool norm_bwd_wide() { return NV * wide_v<T>() > 16; }
 
+// Whether the sums of dy wait in shared memory: for such rows, and where a block has 320
+// threads, of which two leave 96 registers (bf16, one stage less in flight: 32768 x 5120
+// 186 -> 161 us, from a checkpoint 175 -> 166, 20000 x 5001 266 -> 191; fp32 from a
+// checkpoint 16384 x 5120 128 -> 120 us; but fp32 16384 x 4608 135 -> 147 us, and loose
+// rows from a checkpoint, 20000 x 5001, 212 -> 221).
+template <typename T, int NV, int MAXT, bool CK, bool LOOSE>
+__host__ __device__ constexpr bool norm_bwd_db_shared() {
+    return norm_bwd_wide<T, NV>() || (MAXT == 320 && (sizeof(T) == 2 || (CK && !LOOSE)));
+}
+
 // Backward: both sums of a row in one exchange, so one barrier a row; the sums over
 // rows stay in registers until the last row, then go to the block's row of `part`.
-// 32768 x 4096 bf16 127 us, 94 % of the measured copy rate; from a checkpoint 122 us,
-// 82 % (its bytes are turned into pairs, 54 % of the issue slots); 32768 x 5120 from a
-// checkpoint 173 us, 72 %.  Above 8192 columns the weights (bf16) and the sums of dy
+// 32768 x 4096 bf16 127 us, 94 % of the measured copy rate; from a checkpoint 120 us,
+// 83 % (its bytes are turned into pairs, 54 % of the issue slots); 32768 x 5120 161 us,
+// 93 %, from a checkpoint 166 us, 75 %.  Above 8192 columns the weights (bf16) and the sums of dy
 // wait in shared memory, which leaves room for one row in flight: 8192 x 16384 bf16
-// 158 us, 75 % (265 us with both in registers, which spilled), from a checkpoint
-// 180 us, 55 %; fp32 274 us, 87 % (319 us).
+// 158 us, 75 % (265 us with both in registers), from a checkpoint 181 us, 55 %; fp32
+// 271 us, 88 % (319 us), although that form and the loose ones still spill a few values.
 template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
     using X = Stage<T, LOOSE>;
@@ -277,10 +287,11 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     };
     // what a row needs beside its vectors, AHEAD rows before it in registers: two where
     // rows are short or registers are left for it (a miss takes longer than a row), else
-    // one (32768 x 4096 bf16 139 -> 127 us, 16384 x 8192 160 -> 135 us, 32768 x 5120
-    // 173 -> 158 us; from a checkpoint 188 -> 173 us, 8192 x 16384 210 -> 180 us, but at
-    // 32768 x 4096 122 -> 126 us)
-    constexpr int AHEAD = !LOOSE && (WARP || (CK && MAXT != 320 && !norm_bwd_wide<T, NV>())) ? 2 : 1;
+    // one (32768 x 4096 bf16 139 -> 127 us, 16384 x 8192 159 -> 136 us; from a checkpoint
+    // 32768 x 5120 193 -> 175 us, 8192 x 16384 210 -> 180 us, but at 32768 x 4096 122 -> 126
+    // us, and loose bf16 rows of 12000 x 10001 374 -> 419 us)
+    constexpr bool WIDE = norm_bwd_wide<T, NV>();
+    constexpr int AHEAD = (LOOSE ? CK && WIDE && sizeof(T) == 2 : WARP || (CK && MAXT != 320 && !WIDE)) ? 2 : 1;
     struct Few {
         float mean, rstd;
         uint32_t byte[CK ? NV : 1];
@@ -317,11 +328,10 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     fetch_few(even, rows_left > 0);
     if (AHEAD == 2) fetch_few(other, rows_left > 1);
     // where registers are short the weights wait in shared memory, each thread's own:
-    // 32768 x 5120 bf16 228 -> 188 us from a checkpoint, 203 -> 178 us otherwise (at
-    // 32768 x 4096 145 -> 122 us, but 138 -> 141 us)
-    // (above 8192 columns the sums of dy wait there too)
-    constexpr bool DB_SHARED = norm_bwd_wide<T, NV>();
-    constexpr bool W_SHARED = !WARP && (CK || MAXT == 320 || (DB_SHARED && sizeof(T) == 2));
+    // 32768 x 5120 bf16 228 -> 188 us from a checkpoint (at 32768 x 4096 145 -> 122 us, but
+    // 138 -> 141 us without one), and the sums of dy as well (norm_bwd_db_shared)
+    constexpr bool DB_SHARED = norm_bwd_db_shared<T, NV, MAXT, CK, LOOSE>();
+    constexpr bool W_SHARED = !WARP && (CK || MAXT == 320 || (WIDE && sizeof(T) == 2));
     __shared__ ulonglong2 w_shared[W_SHARED ? NV * P / 2 : 1][W_SHARED ? MAXT : 1];
     __shared__ ulonglong2 db_shared[DB_SHARED ? NV * P / 2 : 1][DB_SHARED ? MAXT : 1];
     uint64_t w_kept[W_SHARED ? 1 : NV][P], dw[NV][P] = {}, db[DB_SHARED ? 1 : NV][P] = {};
@@ -397,10 +407,15 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
                 }
             }
         }
-        fetch_few(few, rows_left > AHEAD);
+        // before the row's exchange, or behind it in one block of 512 threads of aligned bf16
+        // rows (16384 x 8192 140 -> 136 us, 8192 x 6144 65 -> 63; but 32768 x 4096 127 -> 162,
+        // loose 16000 x 8001 254 -> 262)
+        constexpr bool LATE = sizeof(T) == 2 && !CK && !LOOSE && MAXT == 512 && !WIDE;
+        if constexpr (!LATE) fetch_few(few, rows_left > AHEAD);
         float m1 = f2_sum(s0), m2 = f2_sum(s1);
         group_sum2<WARP ? 0 : MAXT / 32>(m1, m2, red[buf]);
         buf ^= 1;
+        if constexpr (LATE) fetch_few(few, rows_left > AHEAD);
         // the sums have taken every value of this stage: its slots are free
         fetch(slot, slot_x);
         slot += NV * pitch_y;

@@ -98,11 +98,12 @@ flp_status resident_blocks(int threads, size_t smem, size_t largest, int* per_sm
 // 17 to 130 %.  Rows of up to 512 elements go to one warp, which needs no block
 // barrier; rows above 8192 take more elements a thread.  Two blocks of up to TWO
 // threads must fit an SM, which bounds the registers (three of up to 256: forward
-// with a checkpoint 119 against 107 us, backward 185 against 138 us).  The bf16
-// forward has registers to spare: two blocks of 384 threads instead of one take
-// 16384 x 6144 from 82 to 64 us, with a checkpoint from 104 to 83 us (fp32 from 125
-// to 136), two of 512 take 16384 x 8192 from 96 to 85 us (with a checkpoint from 131
-// to 153).  The stages put 64 KiB or so per SM in flight in every shape.
+// with a checkpoint 119 against 107 us, backward 185 against 138 us).  For the bf16
+// forward that pays up to 512 threads, although the loose form of 512 spills: two
+// blocks of 384 threads instead of one take 16384 x 6144 from 82 to 64 us, with a
+// checkpoint from 104 to 83 us (fp32 from 125 to 136; loose rows with a checkpoint,
+// 20000 x 6001, from 204 to 233), two of 512 take 16384 x 8192 from 96 to 83 us (with
+// a checkpoint from 131 to 153).  The stages put 32 to 64 KiB per SM in flight.
 template <int NV_, int S_, bool WARP_, int MAXT_, int MINB_>
 struct StreamShape {
     static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;
@@ -117,10 +118,10 @@ size_t norm_stage_bytes(int vecs, int threads, int x) {
     return static_cast<size_t>(vecs) * (one + (x == 0 ? 0 : x == 1 ? one : threads * wide_v<T>()));
 }
 
-template <typename T, int TWO, typename F>
+template <typename T, int TWO, int S16, typename F>
 flp_status norm_stream_shape(int64_t cols, F&& f) {
     constexpr int V = wide_v<T>(), N2 = 16 / V;  // N2 vectors of V = 16 elements
-    constexpr int S = V == 8 ? 4 : 2;
+    constexpr int S = V == 8 ? S16 : 2;          // S16: stages of bf16 rows
     const int64_t vecs = cdiv(cols, V);
     if (vecs <= 32) return f(StreamShape<1, 4, true, 256, 1>{}, 256);
     if (vecs <= 64) return f(StreamShape<2, 4, true, 256, 1>{}, 256);
@@ -416,8 +417,11 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
     auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
         using T = decltype(t);
         constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-        constexpr int TWO = sizeof(T) == 4 ? 320 : CK ? 384 : 512;
-        return norm_stream_shape<T, TWO>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
+        constexpr int TWO = sizeof(T) == 4 || (CK && LOOSE) ? 320 : CK ? 384 : 512;
+        // bf16 rows ahead: 32768 x 4096 takes 96, 94, 82 us with 4, 3, 2 of them, with a
+        // checkpoint 109, 105, 110 (32768 x 2048: 61, 59, 56; 16384 x 4608: 62, 62, 64)
+        constexpr int S16 = CK ? 3 : 2;
+        return norm_stream_shape<T, TWO, S16>(CK ? p.Hp : p.H, [&](auto shape, int threads) -> flp_status {
             using X = decltype(shape);
             constexpr auto* kernel = flp_norm_fwd_stream_kernel<T, X::NV, X::S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
             const size_t smem = norm_stage_bytes<T, LOOSE>(X::S * X::NV, threads, 0);
@@ -505,12 +509,15 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
         auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
             using T = decltype(t);
             constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-            return norm_stream_shape<T, 320>(p.H, [&](auto shape, int threads) -> flp_status {
+            return norm_stream_shape<T, 320, 4>(p.H, [&](auto shape, int threads) -> flp_status {
                 using X_ = decltype(shape);
                 // above 8192 columns one stage fits beside the weights and sums; two of aligned
                 // bf16 rows with a checkpoint (8192 x 8200 119 us, one stage: 133)
                 constexpr bool WIDE = norm_bwd_wide<T, X_::NV>();
-                constexpr int S = WIDE && !(CK && !LOOSE && sizeof(T) == 2) ? 1 : X_::S;
+                // and two of bf16 where the sums of dy wait there too (norm_bwd_db_shared)
+                constexpr int S = WIDE && !(CK && !LOOSE && sizeof(T) == 2)                                       ? 1
+                                  : sizeof(T) == 2 && norm_bwd_db_shared<T, X_::NV, X_::MAXT, CK, LOOSE>() ? 2
+                                                                                                              : X_::S;
                 constexpr auto* kernel = flp_norm_bwd_stream_kernel<T, X_::NV, S, CK, LOOSE, X_::WARP, X_::MAXT, X_::MINB>;
                 // a cluster's block holds its warps' sums (a row per warp) and its own after the rows
                 constexpr size_t kJoin = X_::WARP ? static_cast<size_t>(X_::MAXT) * X_::NV * wide_v<T>() * 4 : 0;
