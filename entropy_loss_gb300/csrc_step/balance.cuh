@@ -6,7 +6,8 @@
 //   chosen    : the top_k largest logits (equal ones: lowest index first; -inf
 //               never; none in a row that holds NaN or +inf), or the caller's
 //   c_e       = times e is chosen, C = sum c_e
-//   loss      = coef E sum_e (c_e / C) (1/N) sum_t p_te        (0 if N or C is 0)
+//   loss      = coef E sum_e (c_e / C) (1/N) sum_t p_te        (0 if N or C is 0, but NaN
+//               whenever a live row holds a NaN or +inf)
 //   d loss / d z_tj = coef / N  p_tj (a_j - sum_e p_te a_e),  a_e = (E c_e - C) / C
 // (a_e is centred: subtracting a constant changes nothing because sum p = 1,
 // and keeps the difference free of cancellation when the load is near even.)
@@ -517,8 +518,10 @@ __device__ __forceinline__ float balance_loads(const BalParams& p, bool first, l
             part += static_cast<double>(p.E * tot_c(e) - C) * tot_p(e);
         }
         part = bal_block_sum(part, red_d);
+        // nothing chosen: every factor of `part` is 0, and 0 times a row's NaN is NaN (rows
+        // that all hold one choose nothing)
         if (threadIdx.x == 0)
-            *p.loss = any ? static_cast<float>(p.coef * (1. + part / (static_cast<double>(N) * static_cast<double>(C)))) : 0.f;
+            *p.loss = static_cast<float>(any ? p.coef * (1. + part / (static_cast<double>(N) * static_cast<double>(C))) : part);
     }
     return any ? static_cast<float>(p.coef / static_cast<double>(N)) : 0.f;
 }

@@ -496,13 +496,13 @@ flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, const void* 
  *              non-NULL (values outside [0, E) are dropped slots)
  *   c_e      = times expert e is chosen, C = sum_e c_e
  *   loss     = coef E sum_e (c_e / C) (sum_t p_te / N)   (coef when the load is
- *              even; 0 when N or C is 0)
+ *              even; 0 when N or C is 0 and no live row holds a NaN or +inf)
  *   grad_te  = coef E / (N C) p_te (c_e - sum_f c_f p_tf), 0 on other rows
  * The counts are constants of the gradient.  logits: bf16 or fp32 [T, E] at
  * pitch ld; mask: bytes [T]; experts: int64 [T, top_k]; loss: one fp32; grad:
  * the logits' type, contiguous [T, E], or NULL; counts: int64 [E].  A NaN or
- * +inf in a live row makes the loss and that row's gradient NaN; what masked
- * rows hold is not looked at.  Few rows need no workspace (the query says 0).
+ * +inf in a live row makes the loss and that row's gradient NaN, whether or not
+ * anything is chosen; what masked rows hold is not looked at.  Few rows need no workspace (the query says 0).
  */
 flp_status flp_balance_loss_workspace(int64_t T, int64_t E, size_t* bytes);
 flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype, const uint8_t* mask,
