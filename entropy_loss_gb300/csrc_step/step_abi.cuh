@@ -200,7 +200,8 @@ WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t
     w.tk = static_cast<int>(cdiv(K, 2 * BN));
     const int64_t tiles = static_cast<int64_t>(w.tn) * w.tk;
     const int64_t KB = std::max<int64_t>(1, cdiv(M, BK));
-    const bool direct = (K * elem(dw_dtype)) % 16 == 0;  // a TMA store's row pitch
+    // a TMA store's row pitch; and a bf16 result of many rows is joined from fp32 sums
+    const bool direct = (K * elem(dw_dtype)) % 16 == 0 && !(dw_dtype == FLP_BF16 && KB > WGRAD_BF16_RUN);
     w.whole = direct ? static_cast<int>(tiles / pairs * pairs) : 0;
     int64_t rest = tiles - w.whole;
     w.splits = 1;

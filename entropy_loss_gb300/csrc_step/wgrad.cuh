@@ -52,14 +52,19 @@ struct WgradUnit {
 
 // The tensor cores round an accumulator toward zero at every step, so the error
 // of a long sum grows with its length: 3.0e-6 of the result over 8192 rows of
-// normal values, 1.9e-5 over 32768, against 4.8e-7 over 2048.  An fp32 result is
+// centred normal values, 1.9e-5 over 32768, 1.1e-3 over 1048576, against 4.8e-7
+// over 2048 (values with an offset of half their spread: twice that; a product of
+// the same values in fp32 arithmetic 1e-7 to 5e-7).  An fp32 result is
 // therefore summed in runs of at most 2048 rows, whose sums are added in memory,
 // rounded to nearest.  Draining the accumulators between runs costs about 6 us a
 // tile when every column goes through memory (8192 x 8192 x 5120 takes 455 us, in
 // one run 377 us); WGRAD_KEEP of a half's 256 columns are therefore summed in the
-// epilogue's registers (424 us; 64: 436, 32: 449; 128 would spill).  A bf16
-// result's own rounding (1.7e-3) leaves nothing of the error: one run.
+// epilogue's registers (424 us; 64: 436, 32: 449; 128 would spill more).  A bf16
+// result's own rounding (1.7e-3) leaves nothing of the error of up to 131072 rows (1e-4):
+// one run, stored directly.  Above that the error also has a direction (every value
+// 1e-3 too small over 1048576 rows), so the result is joined from fp32 sums of runs.
 constexpr int WGRAD_RUN = 32;
+constexpr int WGRAD_BF16_RUN = 2048;
 constexpr int WGRAD_KEEP = 96;
 
 __device__ __forceinline__ WgradUnit wgrad_unit(const WgradParams& p, int u) {

@@ -66,3 +66,18 @@ def test_runs_stay_inside_their_buffers(flp):  # noqa: F811
     for guarded in (raw, ws):
         assert (guarded[:4096] == 0xA5).all() and (guarded[-4096:] == 0xA5).all()
     assert flp.get_error(ws[4096:]) == flp.FLP_OK
+
+
+def test_bf16_of_very_many_rows_has_no_bias(flp):  # noqa: F811
+    """A sum that is truncated at every step comes out too small: over 2^20 rows in
+    one run by 1e-3 of itself.  Rounding to bf16 has no direction: 2^-9 of each
+    value at most, 64 x 2048 of them, below 1e-4 on average."""
+    M, N, K = (1 << 20) - 37, 5120, 2048
+    dy = torch.empty(M, N, dtype=torch.bfloat16, device="cuda").normal_()
+    kept = flp.checkpoint_pack(torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_())
+    dw = flp.checkpoint_weight_grad(dy, kept, dw_dtype=torch.bfloat16)
+    x = flp.checkpoint_unpack(kept)
+    want = sum(dy[i:i + 65536, :64].double().t() @ x[i:i + 65536].double() for i in range(0, M, 65536))
+    off = dw[:64].double() - want
+    assert abs(float((off * want.sign()).mean() / want.abs().mean())) <= 1e-4
+    assert float((off.abs() - 2.0 ** -8 * want.abs()).max()) <= 1e-6 * float(want.abs().max())
