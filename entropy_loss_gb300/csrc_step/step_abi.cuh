@@ -254,6 +254,60 @@ flp_status wgrad_attrs() {
     return FLP_OK;
 }
 
+// The contraction and the join, dY (pitch ldy) and X^ (in the workspace) being there.
+flp_status wgrad_contract(const WgradPlan& w, const void* y, int64_t ldy, uint8_t* ws, int64_t M, int64_t N, int64_t K,
+                          void* dW, int dw_dtype, int accumulate, int pairs, int run, unsigned long long wait_limit_ns,
+                          int stall_after, cudaStream_t s) {
+    flp_status st;
+    const int64_t es = elem(dw_dtype);
+    const bool b16 = dw_dtype == FLP_BF16;
+    CUtensorMap my, mx, mw, mp;
+    if ((st = tmap_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, ldy * 2, 64, 64)) != FLP_OK) return st;
+    if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ws + w.off_x, w.Kp, M, w.Kp * 2, 64, 64)) != FLP_OK)
+        return st;
+    const size_t part_rows = static_cast<size_t>(w.rest) * w.splits * PM;
+    if (part_rows > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
+    // without split tiles (or without whole ones) one of the two output maps is
+    // not used: it repeats the other
+    if (w.rest &&
+        (st = tmap_2d(&mp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + w.off_part, 2 * BN, part_rows, 2 * BN * 4, 16, BM,
+                      CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
+        return st;
+    if (w.whole &&
+        (st = tmap_2d(&mw, b16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dW, K, N, K * es,
+                      b16 ? 32 : 16, BM, CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
+        return st;
+    if (!w.rest) mp = mw;
+    if (!w.whole) mw = mp;
+    WgradParams p{};
+    p.tn = w.tn;
+    p.tk = w.tk;
+    p.group = std::min(w.tn, 8);
+    p.whole = w.whole;
+    p.splits = w.splits;
+    p.units = w.units;
+    p.KB = static_cast<int>(cdiv(M, BK));
+    p.run = run;
+    p.N = static_cast<int>(N);
+    p.K = static_cast<int>(K);
+    p.add = accumulate ? 1 : 0;
+    p.bf16_out = b16 ? 1 : 0;
+    p.err = reinterpret_cast<int*>(ws);
+    p.wait_limit_ns = wait_limit_ns;
+    p.stall_after = stall_after;
+    const int grid = 2 * static_cast<int>(std::min<int64_t>(w.units, pairs));
+    st = launch_pairs_n(flp_wgrad_kernel, grid, WIDE_THREADS, s, "flp_wgrad_kernel launch", true, my, mx, mw, mp, p, dW);
+    if (st != FLP_OK || !w.rest) return st;
+    WgradJoinParams j{};
+    j.part = reinterpret_cast<const float*>(ws + w.off_part);
+    j.g = p;
+    j.dw = dW;
+    j.add = p.add;
+    j.err = p.err;
+    return launch_step(flp_wgrad_join_kernel, static_cast<int64_t>(w.rest) * (PM / WJ_ROWS), WJ_THREADS, 0, s,
+                       "flp_wgrad_join_kernel launch", true, j);
+}
+
 // How the vectors of V elements of the rows in p are dealt to threads, `each` per thread.
 flp_status ck_places(CkParams& p, int V, bool loose, int each, int64_t* grid) {
     p.per_row = static_cast<unsigned>(loose ? cdiv(p.Hp / V, 32) * 32 : p.Hp / V);
@@ -632,53 +686,37 @@ extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, c
         st = launch_step(flp_align_rows_kernel, grid, CK_THREADS, 0, s, "flp_align_rows_kernel launch", false, a);
         if (st != FLP_OK) return st;
     }
-    const int64_t es = elem(dW_dtype);
-    const bool b16 = dW_dtype == FLP_BF16;
-    CUtensorMap my, mx, mw, mp;
-    if ((st = tmap_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, ldy * 2, 64, 64)) != FLP_OK) return st;
-    if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ws + w.off_x, w.Kp, M, w.Kp * 2, 64, 64)) != FLP_OK)
-        return st;
-    const size_t part_rows = static_cast<size_t>(w.rest) * w.splits * PM;
-    if (part_rows > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
-    // without split tiles (or without whole ones) one of the two output maps is
-    // not used: it repeats the other
-    if (w.rest &&
-        (st = tmap_2d(&mp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + w.off_part, 2 * BN, part_rows, 2 * BN * 4, 16, BM,
-                      CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
-        return st;
-    if (w.whole &&
-        (st = tmap_2d(&mw, b16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dW, K, N, K * es,
-                      b16 ? 32 : 16, BM, CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
-        return st;
-    if (!w.rest) mp = mw;
-    if (!w.whole) mw = mp;
-    WgradParams p{};
-    p.tn = w.tn;
-    p.tk = w.tk;
-    p.group = std::min(w.tn, 8);
-    p.whole = w.whole;
-    p.splits = w.splits;
-    p.units = w.units;
-    p.KB = static_cast<int>(cdiv(M, BK));
+    const int KB = static_cast<int>(cdiv(M, BK));
     // equal runs of at most WGRAD_RUN blocks
-    p.run = static_cast<int>(cdiv(p.KB, cdiv(p.KB, WGRAD_RUN)));
-    p.N = static_cast<int>(N);
-    p.K = static_cast<int>(K);
-    p.add = accumulate_dW ? 1 : 0;
-    p.bf16_out = b16 ? 1 : 0;
-    p.err = reinterpret_cast<int*>(ws);
-    p.wait_limit_ns = kWaitLimitNs;
-    const int grid = 2 * static_cast<int>(std::min<int64_t>(w.units, d->pairs));
-    st = launch_pairs_n(flp_wgrad_kernel, grid, WIDE_THREADS, s, "flp_wgrad_kernel launch", true, my, mx, mw, mp, p);
-    if (st != FLP_OK || !w.rest) return st;
-    WgradJoinParams j{};
-    j.part = reinterpret_cast<const float*>(ws + w.off_part);
-    j.g = p;
-    j.dw = dW;
-    j.add = p.add;
-    j.err = p.err;
-    return launch_step(flp_wgrad_join_kernel, static_cast<int64_t>(w.rest) * (PM / WJ_ROWS), WJ_THREADS, 0, s,
-                       "flp_wgrad_join_kernel launch", true, j);
+    const int run = static_cast<int>(cdiv(KB, cdiv(KB, WGRAD_RUN)));
+    return wgrad_contract(w, y, ldy, ws, M, N, K, dW, dW_dtype, accumulate_dW, d->pairs, run, kWaitLimitNs, -1, s);
+}
+
+extern "C" flp_status flp_selftest_weight_grad_timeout(void* workspace, size_t workspace_bytes, int odd, int stall_after,
+                                                       int64_t wait_limit_ns, void* stream) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < FLP_SELFTEST_WEIGHT_GRAD_BYTES)
+        return fail(FLP_ERR_WORKSPACE, "self-test needs FLP_SELFTEST_WEIGHT_GRAD_BYTES of workspace");
+    if (wait_limit_ns <= 0 || wait_limit_ns > 60ll * 1000 * 1000 * 1000)
+        return fail(FLP_ERR_INVALID_ARG, "wait_limit_ns must be in (0, 60 s]");
+    DevInfo* d;
+    flp_status st = check_device(&d);
+    if (st != FLP_OK) return st;
+    if ((st = check_on_current_device(workspace, "workspace")) != FLP_OK) return st;
+    if ((st = wgrad_attrs()) != FLP_OK) return st;
+    const int64_t M = 192, N = 136, K = odd ? 521 : 520;
+    const WgradPlan w = plan_wgrad(nullptr, N, M, N, K, FLP_F32, 1);
+    const size_t off_dy = align_up(w.bytes, 1024);
+    if (off_dy + M * N * 2 > FLP_SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET ||
+        FLP_SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET + N * K * 4 > FLP_SELFTEST_WEIGHT_GRAD_BYTES)
+        return fail(FLP_ERR_UNSUPPORTED, "self-test layout exceeds its workspace");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t* dw = ws + FLP_SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    FLP_CUDA(cudaMemsetAsync(ws, 0, off_dy + M * N * 2, s));  // error word, X^, partial tiles, dY
+    FLP_CUDA(cudaMemsetAsync(dw, 0x3f, N * K * 4, s));        // what the result has to replace
+    st = wgrad_contract(w, ws + off_dy, N, ws, M, N, K, dw, FLP_F32, 0, 1, 1, static_cast<unsigned long long>(wait_limit_ns),
+                        stall_after < 0 ? -1 : stall_after, s);
+    return st == FLP_OK ? flp_get_error(workspace, stream) : st;
 }
 
 extern "C" flp_status flp_balance_loss_workspace(int64_t T, int64_t E, size_t* bytes) {

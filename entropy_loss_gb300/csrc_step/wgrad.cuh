@@ -40,6 +40,7 @@ struct WgradParams {
     int bf16_out;  // dW in bf16 (else fp32)
     int* err;
     unsigned long long wait_limit_ns;
+    int stall_after;  // < 0: off; else the producers stop after this many blocks (self-test)
 };
 
 struct WgradUnit {
@@ -91,12 +92,31 @@ __device__ __forceinline__ WgradUnit wgrad_unit(const WgradParams& p, int u) {
     return t;
 }
 
+// NaN in what an epilogue group (half g of a tile, the 128 rows from `rofs` on) would
+// still have written to dW, from unit u on: what a timed-out contraction leaves there is
+// what dW held, or some of its runs.  Split tiles are left to the join.  Out of line.
+__device__ __noinline__ void wgrad_fill_nan(const WgradParams& p, void* dw, int u, int npairs, int g, int rofs, int et) {
+    for (; u < p.whole; u += npairs) {
+        const WgradUnit t = wgrad_unit(p, u);
+        const int k0 = t.k0 + g * BN, n0 = t.n0 + rofs;
+        const int cols = min(BN, p.K - k0), rows = min(BM, p.N - n0);
+        for (int r = 0; r < rows; ++r)
+            for (int c = et; c < cols; c += EPI_THREADS) {
+                const long long o = static_cast<long long>(n0 + r) * p.K + k0 + c;
+                if (p.bf16_out)
+                    static_cast<unsigned short*>(dw)[o] = 0x7fc0;
+                else
+                    static_cast<uint32_t*>(dw)[o] = 0x7fc00000u;
+            }
+    }
+}
+
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     flp_wgrad_kernel(const __grid_constant__ CUtensorMap tmY,     // dY, MN-major A (64 x 64 boxes)
                      const __grid_constant__ CUtensorMap tmX,     // X^, MN-major B (64 x 64)
                      const __grid_constant__ CUtensorMap tmDw,    // dW store boxes (128 rows x 64 bytes)
                      const __grid_constant__ CUtensorMap tmPart,  // partial tiles, fp32 [.., 512] (128 x 64 bytes)
-                     const WgradParams p) {
+                     const __grid_constant__ WgradParams p, void* dw) {
     extern __shared__ uint8_t smem_raw[];
     const Smem sm = smem_layout(smem_raw);
     const int warp = threadIdx.x >> 5;
@@ -122,12 +142,16 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         if (lane == 0) {
-            int stage = 0;
+            int stage = 0, issued = 0;
             uint32_t phase = 0;
-            bool ok = true;
+            bool ok = true, stalled = false;
             for (int u = pair; u < p.units && ok; u += npairs) {
                 const WgradUnit t = wgrad_unit(p, u);
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (p.stall_after >= 0 && issued++ == p.stall_after) {
+                        ok = false, stalled = true;  // stop feeding the MMA
+                        break;
+                    }
                     if (!mbar_wait(&sm.empty[stage], phase ^ 1u, limit, abort_flag)) {
                         ok = false;
                         break;
@@ -152,7 +176,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     }
                 }
             }
-            if (!ok) raise_abort(sm, p.err);
+            if (!ok && !stalled) raise_abort(sm, p.err);
         }
     } else if (warp == 1) {
         // ---------------------------------------------- MMA issuer (leader)
@@ -256,7 +280,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         StoreRing ring;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = pair; u < p.units; u += npairs) {
+        int u = pair;
+        for (; u < p.units; u += npairs) {
             const WgradUnit t = wgrad_unit(p, u);
             if (g >= t.halves) continue;
             const bool partial = t.part >= 0;
@@ -330,6 +355,10 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         }
         if (!ok) raise_abort(sm, p.err);
         if (et == 0) bulk_wait_group<0>();
+        if (!ok) {
+            named_bar_sync(bar_vote, EPI_THREADS);  // behind the group's earlier stores
+            wgrad_fill_nan(p, dw, u, npairs, g, rofs, et);
+        }
     }
 
     pair_epilogue(sm, warp, tmem_base);
@@ -345,8 +374,9 @@ struct WgradJoinParams {
 
 // Sums the partial tiles' splits in order and writes their part of dW (adding
 // to what is there, in fp32, when asked).  One block per 2 rows of a tile.
-// After a timeout of the contraction the sums are NaN, so that no incomplete
-// value passes for a result.  4 splits of 16 tiles (33 MB) take 11 us with cold caches,
+// After a timeout of the contraction the sums are NaN, like what that kernel fills the
+// tiles with that it should have written itself, so that no incomplete value passes for
+// a result.  4 splits of 16 tiles (33 MB) take 11 us with cold caches,
 // bound by the bytes of one short wave of loads.
 constexpr int WJ_THREADS = 256;
 constexpr int WJ_ROWS = 2;

@@ -33,7 +33,7 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_backward_plan", "flp_backward_schedule", "flp_selftest_dependency_timeout",
            "flp_selftest_dz_wait_timeout", "flp_policy_loss", "flp_layer_norm", "flp_layer_norm_workspace",
            "flp_layer_norm_backward", "flp_checkpoint_pack", "flp_checkpoint_unpack",
-           "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad",
+           "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad", "flp_selftest_weight_grad_timeout",
            "flp_balance_loss_workspace", "flp_balance_loss")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
@@ -44,6 +44,8 @@ FLP_AGG_TOKEN_MEAN = 0
 FLP_AGG_SEQUENCE_MEAN = 1
 FLP_AGG_SUM_OVER = 2
 SELFTEST_WORKSPACE_BYTES = 1 << 20
+SELFTEST_WEIGHT_GRAD_BYTES = 3 << 20
+SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET = 2 << 20
 SELFTEST_OUTPUT_OFFSET = 768 << 10  # the forward self-test's logprob, lse, entropy (fp32 [256] each)
 STATIC_SCRATCH_BYTES = 16 << 20
 FLP_BWD_AUTO = 0
@@ -121,6 +123,7 @@ def load(path: str = LIB_PATH):
             ("flp_checkpoint_unpack", [p, p, i64, i64, p, i64, i32, p]),
             ("flp_checkpoint_weight_grad_workspace", [p, i64, i64, i64, i64, i32, size]),
             ("flp_checkpoint_weight_grad", [p, i64, p, p, i64, i64, i64, p, i32, i32, p, ctypes.c_size_t, p]),
+            ("flp_selftest_weight_grad_timeout", [p, ctypes.c_size_t, i32, i32, i64, p]),
             ("flp_balance_loss_workspace", [i64, i64, size]),
             ("flp_balance_loss", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, p, p, ctypes.c_size_t, p])):
         fn = getattr(lib, name)
@@ -370,6 +373,17 @@ def selftest_dependency_timeout(broken: bool, wait_limit_ns: int, workspace=None
     return int(load().flp_selftest_dependency_timeout(_ptr(workspace), _nbytes(workspace),
                                                       int(bool(broken)), wait_limit_ns,
                                                       _stream(stream)))
+
+
+def selftest_weight_grad_timeout(odd: bool, stall_after: int, wait_limit_ns: int, workspace=None, stream=None) -> int:
+    """Run a small weight gradient with its producers stopped after
+    `stall_after` 64-row blocks (< 0: no stall) and every wait bounded by
+    `wait_limit_ns`; with `odd` its dW is written through partial tiles.
+    Returns the error status the run leaves."""
+    if workspace is None:
+        workspace = torch.empty(SELFTEST_WEIGHT_GRAD_BYTES, dtype=torch.uint8, device="cuda")
+    return int(load().flp_selftest_weight_grad_timeout(_ptr(workspace), _nbytes(workspace), int(bool(odd)), stall_after,
+                                                       wait_limit_ns, _stream(stream)))
 
 
 def loss(logprob, y, kind=FLP_LOSS_NLL_MEAN, *, ignore_index: int = -100, old_logprob=None,
@@ -643,7 +657,8 @@ def checkpoint_unpack(kept: Checkpoint8, *, dtype=None, out=None, stream=None):
 def checkpoint_weight_grad(dY, kept: Checkpoint8, *, dW=None, dw_dtype=torch.float32, accumulate: bool = False,
                            workspace=None, stream=None):
     """dW [N, K] = dY^T x of a linear layer whose input x [M, K] was kept as a
-    checkpoint; dY bf16 [M, N].  With `accumulate` it is added to dW (fp32)."""
+    checkpoint; dY bf16 [M, N].  With `accumulate` it is added to dW (fp32).  A
+    timeout on the GPU leaves NaN in dW and FLP_ERR_TIMEOUT in the workspace."""
     if stream is not None:
         return _on_stream(stream, checkpoint_weight_grad, dY, kept, dW=dW, dw_dtype=dw_dtype, accumulate=accumulate,
                           workspace=workspace)

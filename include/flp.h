@@ -475,7 +475,8 @@ flp_status flp_checkpoint_unpack(const void* q, const void* scale, int64_t M, in
  * (added to when accumulate_dW != 0) or bf16 (overwritten; accumulating into
  * it is FLP_ERR_UNSUPPORTED), contiguous, 16-byte aligned.  M == 0 writes
  * zeros (or adds nothing).  The workspace's first word is the error word of
- * flp_get_error (FLP_ERR_TIMEOUT).  The workspace query takes dY for its
+ * flp_get_error (FLP_ERR_TIMEOUT); after a timeout every tile of dW that was
+ * not finished is NaN.  The workspace query takes dY for its
  * alignment only.
  */
 flp_status flp_checkpoint_weight_grad_workspace(const void* dY, int64_t lddy, int64_t M, int64_t N,
@@ -484,6 +485,23 @@ flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, const void* 
                                       int64_t M, int64_t N, int64_t K, void* dW, int dW_dtype,
                                       int accumulate_dW, void* workspace, size_t workspace_bytes,
                                       void* stream);
+
+/*
+ * Self-test of the contraction's bounded waits, like flp_selftest_wait_timeout
+ * (a diagnostic): a weight gradient of M = 192, N = 136 and K = 520 (two tiles
+ * of dW, one of 512 columns, written directly) or, with odd != 0, K = 521
+ * (through partial tiles), all zeros, on one CTA pair in runs of one 64-row
+ * block, laid out in `workspace` (at least FLP_SELFTEST_WEIGHT_GRAD_BYTES).
+ * With stall_after >= 0 its TMA producers stop after that many blocks, of which
+ * a tile has three.  The result, fp32 [N, K], is left at byte offset
+ * FLP_SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET: zeros, or NaN where the stall kept a
+ * tile from being finished (with odd, in every tile).  Synchronises `stream` and
+ * returns the error word (FLP_ERR_TIMEOUT or FLP_OK), or an argument / CUDA error.
+ */
+#define FLP_SELFTEST_WEIGHT_GRAD_BYTES (3u << 20)
+#define FLP_SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET (2u << 20)
+flp_status flp_selftest_weight_grad_timeout(void* workspace, size_t workspace_bytes, int odd, int stall_after,
+                                            int64_t wait_limit_ns, void* stream);
 
 /*
  * Balance loss of a mixture-of-experts router over T tokens and E experts
