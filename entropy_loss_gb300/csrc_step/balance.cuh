@@ -53,7 +53,7 @@ struct BalParams {
     long long* counts;  // [E]
     float2* stat;       // [T]
     float* part_p;      // [blocks][E]
-    int* part_c;        // [blocks][E]
+    int* part_c;        // [blocks][E]; 2^31 of one block would need 5 TB of given experts
     int* part_n;        // [blocks]
     double* tot_p;      // [E]
     long long* tot_c;   // [E]
@@ -582,13 +582,13 @@ __global__ void __launch_bounds__(BAL_THREADS) flp_balance_rows_kernel(const Bal
 // share of the partials.
 __global__ void __launch_bounds__(1024) flp_balance_join_kernel(const BalParams p) {
     __shared__ float wp[2][32][33];
-    __shared__ int wc[32][33];
+    __shared__ long long wc[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x * 32 + lane;
     griddep_wait();
     griddep_launch_dependents();
     float hi = 0.f, lo = 0.f;
-    int c = 0;  // at most T < 2^31 for one expert
+    long long c = 0;  // up to T top_k where the given experts of a row repeat
     if (e < p.E) {
 #pragma unroll 4
         for (int b = warp; b < p.blocks; b += 32) {
