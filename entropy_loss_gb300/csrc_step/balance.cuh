@@ -48,7 +48,8 @@ struct BalParams {
     long long T;
     int E, k;
     double coef;
-    void* grad;  // [T, E] in the logits' type; NULL: not wanted
+    void* grad;      // [T, E] in the logits' type, or fp32; NULL: not wanted
+    bool grad_f32;
     float* loss;
     long long* counts;  // [E]
     float2* stat;       // [T]
@@ -558,12 +559,17 @@ __device__ __forceinline__ void balance_grad(const BalParams& p, const float2* s
             dot = fmaf(pr[i], a[i], dot);
         }
         dot = group_sum<L>(dot);
-        T* g = static_cast<T*>(p.grad) + row * p.E;
 #pragma unroll
         for (int i = 0; i < NE; ++i) pr[i] *= (a[i] - dot) * scale;
+        auto store = [&](auto* g) {
 #pragma unroll
-        for (int i = 0; i < NE; i += V)
-            if (row < p.T && expert<L, V>(l, i) < p.E) store_grad<V>(g + expert<L, V>(l, i), pr + i);
+            for (int i = 0; i < NE; i += V)
+                if (row < p.T && expert<L, V>(l, i) < p.E) store_grad<V>(g + row * p.E + expert<L, V>(l, i), pr + i);
+        };
+        if (sizeof(T) == 4 || p.grad_f32)
+            store(static_cast<float*>(p.grad));
+        else
+            store(static_cast<T*>(p.grad));
     }
 }
 

@@ -734,13 +734,23 @@ extern "C" flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype
                                        const int64_t* experts, int64_t T, int64_t E, int64_t top_k, float coef,
                                        float* loss, void* grad, int64_t* counts, void* workspace,
                                        size_t workspace_bytes, void* stream) {
+    return flp_balance_loss_ex(logits, ld, dtype, mask, experts, T, E, top_k, coef, loss, grad, dtype, counts, workspace,
+                               workspace_bytes, stream);
+}
+
+extern "C" flp_status flp_balance_loss_ex(const void* logits, int64_t ld, int dtype, const uint8_t* mask,
+                                          const int64_t* experts, int64_t T, int64_t E, int64_t top_k, float coef,
+                                          float* loss, void* grad, int grad_dtype, int64_t* counts, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
     flp_status st = balance_checks(T, E, top_k);
     if (st != FLP_OK) return st;
     if (!is_dtype(dtype)) return fail(FLP_ERR_INVALID_ARG, "dtype is FLP_F32 or FLP_BF16");
+    if (grad_dtype != dtype && grad_dtype != FLP_F32)
+        return fail(FLP_ERR_INVALID_ARG, "grad_dtype is the logits' type or FLP_F32");
     if (!loss || !counts) return fail(FLP_ERR_INVALID_ARG, "loss and counts must be non-null");
     if (!std::isfinite(coef)) return fail(FLP_ERR_INVALID_ARG, "coef must be finite");
     if (T > 0 && (st = row_checks(logits, ld, E, dtype, "logits must be non-null")) != FLP_OK) return st;
-    if (reinterpret_cast<uintptr_t>(grad) % elem(dtype))
+    if (reinterpret_cast<uintptr_t>(grad) % elem(grad_dtype))
         return fail(FLP_ERR_INVALID_ARG, "grad must be aligned to its elements");
     DevInfo* d;
     st = step_device(&d);
@@ -761,6 +771,7 @@ extern "C" flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype
     p.k = static_cast<int>(top_k);
     p.coef = coef;
     p.grad = grad;
+    p.grad_f32 = grad_dtype == FLP_F32;
     p.loss = loss;
     p.counts = reinterpret_cast<long long*>(counts);
     p.stat = reinterpret_cast<float2*>(ws);
@@ -774,9 +785,8 @@ extern "C" flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype
     const size_t smem = bal_smem(E);
     auto typed = [&](auto t) -> flp_status {
         using T_ = decltype(t);
-        const size_t four = 4 * static_cast<size_t>(elem(dtype));
-        const bool vec = E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % four == 0 &&
-                         reinterpret_cast<uintptr_t>(grad) % four == 0;
+        const bool vec = E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * elem(dtype)) == 0 &&
+                         reinterpret_cast<uintptr_t>(grad) % (4 * elem(grad_dtype)) == 0;
         return balance_shape(E, vec, [&](auto l, auto ne, auto v) -> flp_status {
             constexpr int L = decltype(l)::value, NE = decltype(ne)::value, V = decltype(v)::value;
             if (b.cluster)

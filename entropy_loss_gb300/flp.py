@@ -34,7 +34,7 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_selftest_dz_wait_timeout", "flp_policy_loss", "flp_layer_norm", "flp_layer_norm_workspace",
            "flp_layer_norm_backward", "flp_checkpoint_pack", "flp_checkpoint_unpack",
            "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad", "flp_selftest_weight_grad_timeout",
-           "flp_balance_loss_workspace", "flp_balance_loss")
+           "flp_balance_loss_workspace", "flp_balance_loss", "flp_balance_loss_ex")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
 FLP_LOSS_NLL_SUM = 3
@@ -125,7 +125,8 @@ def load(path: str = LIB_PATH):
             ("flp_checkpoint_weight_grad", [p, i64, p, p, i64, i64, i64, p, i32, i32, p, ctypes.c_size_t, p]),
             ("flp_selftest_weight_grad_timeout", [p, ctypes.c_size_t, i32, i32, i64, p]),
             ("flp_balance_loss_workspace", [i64, i64, size]),
-            ("flp_balance_loss", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, p, p, ctypes.c_size_t, p])):
+            ("flp_balance_loss", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, p, p, ctypes.c_size_t, p]),
+            ("flp_balance_loss_ex", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, i32, p, p, ctypes.c_size_t, p])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32
     lib.flp_get_error.argtypes = [p, p]
@@ -686,15 +687,15 @@ def checkpoint_weight_grad(dY, kept: Checkpoint8, *, dW=None, dw_dtype=torch.flo
     return dW
 
 
-def balance_loss(logits, top_k: int, *, experts=None, mask=None, coef: float = 1.0, grad: bool = True, workspace=None,
-                 stream=None):
+def balance_loss(logits, top_k: int, *, experts=None, mask=None, coef: float = 1.0, grad: bool = True, grad_dtype=None,
+                 workspace=None, stream=None):
     """Balance loss of router logits [T, E]: (loss [1], its gradient by the
-    logits or None, counts int64 [E]).  mask: bool [T], the tokens that count;
+    logits in their type or fp32 (grad_dtype), or None, counts int64 [E]).  mask: bool [T], the tokens that count;
     experts: int64 [T, top_k], the router's own choice (default: the top_k
     largest logits, ties to the lowest index)."""
     if stream is not None:
         return _on_stream(stream, balance_loss, logits, top_k, experts=experts, mask=mask, coef=coef, grad=grad,
-                          workspace=workspace)
+                          grad_dtype=grad_dtype, workspace=workspace)
     zp, ld = _rows(logits, "logits")
     T, E = shape = logits.shape
     code, dev = _dtype(logits, "logits"), logits.device
@@ -704,14 +705,17 @@ def balance_loss(logits, top_k: int, *, experts=None, mask=None, coef: float = 1
         _need(experts, torch.int64, (T, top_k), "experts")
     loss_out = torch.empty(1, dtype=torch.float32, device=dev)
     counts = torch.empty(E, dtype=torch.int64, device=dev)
-    g = torch.empty(shape, dtype=logits.dtype, device=dev) if grad else None
+    grad_dtype = logits.dtype if grad_dtype is None else grad_dtype
+    if grad_dtype not in (logits.dtype, torch.float32):
+        raise ValueError(f"grad_dtype: expected {logits.dtype} or fp32, got {grad_dtype}")
+    g = torch.empty(shape, dtype=grad_dtype, device=dev) if grad else None
     device = dev.index
     ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
                                    _workspace_bytes("flp_balance_loss_workspace", device, T, E))
-    status = load().flp_balance_loss(zp, ld, code, None if mask is None else mask.data_ptr(),
-                                     None if experts is None else experts.data_ptr(), T, E, top_k, coef,
-                                     loss_out.data_ptr(), None if g is None else g.data_ptr(), counts.data_ptr(), ws,
-                                     ws_bytes, _raw_stream(device))
+    status = load().flp_balance_loss_ex(zp, ld, code, None if mask is None else mask.data_ptr(),
+                                        None if experts is None else experts.data_ptr(), T, E, top_k, coef,
+                                        loss_out.data_ptr(), None if g is None else g.data_ptr(), _DTYPE[grad_dtype],
+                                        counts.data_ptr(), ws, ws_bytes, _raw_stream(device))
     if status:
         _check(status, "flp_balance_loss")
     return loss_out, g, counts
@@ -819,17 +823,19 @@ class FusedBalanceLoss(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, top_k, experts, mask, coef):
+        # kept in fp32: a gradient rounded to bf16 and then scaled is rounded twice, and a
+        # factor near 1 is lost altogether
         loss_out, grad, counts = balance_loss(logits, top_k, experts=experts, mask=mask, coef=coef,
-                                              grad=ctx.needs_input_grad[0])
+                                              grad=ctx.needs_input_grad[0], grad_dtype=torch.float32)
         ctx.save_for_backward(grad)
+        ctx.dtype = logits.dtype
         ctx.mark_non_differentiable(counts)
         return loss_out[0], counts
 
     @staticmethod
     def backward(ctx, g, _):
         grad, = ctx.saved_tensors
-        # with bf16 logits g and the product are rounded to bf16, as in any chain of bf16 gradients
-        return grad * g.to(grad.dtype), None, None, None, None
+        return torch.mul(grad, g.view(1, 1), out=torch.empty_like(grad, dtype=ctx.dtype)), None, None, None, None
 
 
 def fused_balance_loss(logits, top_k: int, experts=None, mask=None, coef: float = 1.0):

@@ -527,6 +527,12 @@ flp_status flp_balance_loss(const void* logits, int64_t ld, int dtype, const uin
                             const int64_t* experts, int64_t T, int64_t E, int64_t top_k, float coef,
                             float* loss, void* grad, int64_t* counts, void* workspace,
                             size_t workspace_bytes, void* stream);
+/* The same with the gradient in the logits' type or in fp32 (grad_dtype): for a
+ * gradient that is multiplied by an upstream one before it is rounded. */
+flp_status flp_balance_loss_ex(const void* logits, int64_t ld, int dtype, const uint8_t* mask,
+                               const int64_t* experts, int64_t T, int64_t E, int64_t top_k, float coef,
+                               float* loss, void* grad, int grad_dtype, int64_t* counts, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* flp_status_string(flp_status status);

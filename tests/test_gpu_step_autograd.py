@@ -1,0 +1,54 @@
+"""The differentiable wrappers of the training-step operators: types, scales, and
+what they refuse or leave out.
+
+Tolerance of the bf16 balance gradient: each value is rounded to bf16 by half a
+unit, and carries the fp32 kernel's error (test_gpu_balance.py): below 2^-7 of
+itself.  Rounding to nearest has no direction, so the mean over 4000 values of the
+relative error stays below 2^-9 / 8.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def flp():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from entropy_loss_gb300 import build, flp as _flp
+    build.build()
+    _flp.load()
+    return _flp
+
+
+@pytest.mark.parametrize("scale", [1.0, 1.00390625 - 2.0 ** -9, 1 / 3, 1000.7])
+def test_balance_gradient_in_bf16_is_scaled_without_a_shift(flp, scale):
+    g = torch.Generator().manual_seed(2)
+    z = torch.randn(500, 8, generator=g).to(torch.bfloat16).cuda().requires_grad_()
+    loss, counts = flp.fused_balance_loss(z, 2, coef=0.3)
+    (loss * scale).backward()
+    assert z.grad.dtype is torch.bfloat16
+    p = torch.softmax(z.detach().double(), 1)
+    a = 8 * counts.double() / counts.sum() - 1
+    want = scale * 0.3 / 500 * p * (a - (p * a).sum(1, keepdim=True))
+    off = (z.grad.double() - want) / want.abs().clamp(min=1e-30) * want.sign()
+    assert float(off.abs()[want.abs() > 1e-3 * want.abs().max()].max()) <= 2.0 ** -7
+    assert abs(float(off[want.abs() > 1e-3 * want.abs().max()].mean())) <= 2.0 ** -12
+    # the kernel's fp32 gradient, multiplied in fp32 and rounded once
+    _, grad, _ = flp.balance_loss(z.detach(), 2, coef=0.3, grad_dtype=torch.float32)
+    assert torch.equal(z.grad, (grad * scale).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,E", [(1, 1), (40, 7), (40, 8), (100, 64), (700, 100), (700, 101), (3000, 16), (5000, 256), (900, 1000)])
+def test_balance_gradient_in_fp32_of_bf16_logits(flp, T, E):
+    """In either type the same gradient; the kernel's own bf16 one is its rounding."""
+    z = torch.randn(T, E, device="cuda").to(torch.bfloat16)
+    loss, full, counts = flp.balance_loss(z, 1, grad_dtype=torch.float32)
+    l2, half, c2 = flp.balance_loss(z, 1)
+    assert full.dtype is torch.float32 and half.dtype is torch.bfloat16
+    assert torch.equal(loss, l2) and torch.equal(counts, c2) and torch.equal(full.to(torch.bfloat16), half)
+    # the 32-bit logits of the same values
+    assert torch.allclose(flp.balance_loss(z.float(), 1)[1], full, rtol=1e-5, atol=0)
+    with pytest.raises(ValueError):
+        flp.balance_loss(z.float(), 1, grad_dtype=torch.bfloat16)
