@@ -764,6 +764,24 @@ def fused_linear_logprob(X, W, y, ignore_index: int = -100, scale: float = 1.0,
     return FusedLinearLogprob.apply(X, W, y, ignore_index, scale, compute_entropy, workspace)
 
 
+class _Once(torch.autograd.Function):
+    """The tensors that fn() gives, which depend on `inputs` in a way that autograd
+    does not see: differentiating them is an error."""
+
+    @staticmethod
+    def forward(ctx, fn, *inputs):
+        return fn()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of the training-step operators cannot be differentiated again")
+
+
+def _once(fn, *inputs):
+    """fn() inside a backward pass, whose gradients with create_graph must not pass for constants."""
+    return _Once.apply(fn, *inputs) if torch.is_grad_enabled() else fn()
+
+
 class FusedLayerNorm(torch.autograd.Function):
     """autograd wrapper of layer_norm; with `checkpoint` the input is kept for the
     backward pass in 8 bits instead of its own type."""
@@ -777,10 +795,9 @@ class FusedLayerNorm(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
-        x, scale, weight, bias, mean, rstd = ctx.saved_tensors
-        if ctx.kept is not None:
-            x = Checkpoint8(x, scale, *ctx.kept)
-        dx, dweight, dbias = layer_norm_backward(dy.contiguous(), x, weight, mean, rstd)
+        saved, scale, weight, bias, mean, rstd = ctx.saved_tensors
+        x = saved if ctx.kept is None else Checkpoint8(saved, scale, *ctx.kept)
+        dx, dweight, dbias = _once(lambda: layer_norm_backward(dy.contiguous(), x, weight, mean, rstd), dy, saved, weight)
         return (dx, None if weight is None else dweight.to(weight.dtype),
                 None if bias is None else dbias.to(bias.dtype), None, None)
 
@@ -808,8 +825,10 @@ class CheckpointLinear(torch.autograd.Function):
     def backward(ctx, dy):
         q, scale, W = ctx.saved_tensors
         dx = dy @ W if ctx.needs_input_grad[0] else None
-        dW = checkpoint_weight_grad(dy.contiguous(), Checkpoint8(q, scale, *ctx.kept), dw_dtype=W.dtype) \
-            if ctx.needs_input_grad[1] else None
+        dW = None
+        if ctx.needs_input_grad[1]:
+            dW = _once(lambda: checkpoint_weight_grad(dy.contiguous(), Checkpoint8(q, scale, *ctx.kept),
+                                                      dw_dtype=W.dtype), dy)
         return dx, dW
 
 
@@ -827,15 +846,15 @@ class FusedBalanceLoss(torch.autograd.Function):
         # factor near 1 is lost altogether
         loss_out, grad, counts = balance_loss(logits, top_k, experts=experts, mask=mask, coef=coef,
                                               grad=ctx.needs_input_grad[0], grad_dtype=torch.float32)
-        ctx.save_for_backward(grad)
-        ctx.dtype = logits.dtype
+        ctx.save_for_backward(logits, grad)
         ctx.mark_non_differentiable(counts)
         return loss_out[0], counts
 
     @staticmethod
     def backward(ctx, g, _):
-        grad, = ctx.saved_tensors
-        return torch.mul(grad, g.view(1, 1), out=torch.empty_like(grad, dtype=ctx.dtype)), None, None, None, None
+        logits, grad = ctx.saved_tensors
+        dz = _once(lambda: torch.mul(grad, g.view(1, 1), out=torch.empty_like(grad, dtype=logits.dtype)), g, logits)
+        return dz, None, None, None, None
 
 
 def fused_balance_loss(logits, top_k: int, experts=None, mask=None, coef: float = 1.0):

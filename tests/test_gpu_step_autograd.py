@@ -52,3 +52,52 @@ def test_balance_gradient_in_fp32_of_bf16_logits(flp, T, E):
     assert torch.allclose(flp.balance_loss(z.float(), 1)[1], full, rtol=1e-5, atol=0)
     with pytest.raises(ValueError):
         flp.balance_loss(z.float(), 1, grad_dtype=torch.bfloat16)
+
+
+# --------------------------------------------------- gradients of gradients
+
+TWICE = "cannot be differentiated again"
+
+
+def test_balance_gradient_is_not_a_constant_of_the_logits(flp):
+    z = torch.randn(50, 8, device="cuda", requires_grad=True)
+    w = torch.tensor(2.0, device="cuda", requires_grad=True)
+    loss, _ = flp.fused_balance_loss(z, 2)
+    dz, = torch.autograd.grad(loss * w, z, create_graph=True)
+    with pytest.raises(RuntimeError, match=TWICE):
+        torch.autograd.grad(dz.square().sum() + z.sum(), z)
+    # the same where the upstream gradient is a constant
+    loss, _ = flp.fused_balance_loss(z, 2)
+    dz, = torch.autograd.grad(loss, z, create_graph=True)
+    with pytest.raises(RuntimeError, match=TWICE):
+        torch.autograd.grad(dz.square().sum() + z.sum(), z)
+    # the gradient itself is the one without create_graph
+    loss, _ = flp.fused_balance_loss(z, 2)
+    assert torch.equal(dz.detach(), torch.autograd.grad(loss, z)[0])
+
+
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_norm_gradient_is_not_a_constant(flp, checkpoint):
+    x = torch.randn(20, 64, device="cuda", requires_grad=True)
+    w = torch.rand(64, device="cuda", requires_grad=True)
+    y = flp.fused_layer_norm(x, w, None, checkpoint=checkpoint)
+    dx, dw = torch.autograd.grad(y.square().sum(), (x, w), create_graph=True)
+    for d in (dx, dw):
+        with pytest.raises(RuntimeError, match=TWICE):
+            torch.autograd.grad(d.square().sum() + x.sum() + w.sum(), (x, w), retain_graph=True)
+    y = flp.fused_layer_norm(x, w, None, checkpoint=checkpoint)
+    once = torch.autograd.grad(y.square().sum(), (x, w))
+    assert torch.equal(dx.detach(), once[0]) and torch.equal(dw.detach(), once[1])
+
+
+def test_linear_gradients_of_gradients(flp):
+    """dx = dy W is an ordinary product and can be differentiated, dW cannot."""
+    x = torch.randn(32, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    W = torch.randn(16, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    dx, dW = torch.autograd.grad(flp.checkpoint_linear(x, W).float().square().sum(), (x, W), create_graph=True)
+    with pytest.raises(RuntimeError, match=TWICE):
+        torch.autograd.grad(dW.float().square().sum(), W, retain_graph=True)
+    twice, = torch.autograd.grad(dx.float().sum(), x)
+    want, = torch.autograd.grad((x.double() @ W.double().t()).square().sum(), x, create_graph=True)
+    want, = torch.autograd.grad(want.sum(), x)
+    assert float((twice.double() - want.double()).norm() / want.double().norm()) <= 0.02
