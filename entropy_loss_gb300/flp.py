@@ -540,9 +540,13 @@ def _on_stream(stream, fn, *args, **kw):
         return fn(*args, **kw)
 
 
-# The current stream's handle, without the Stream object around it (which costs
-# as much as a small launch).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The current stream's handle, where torch has it without the Stream object around
+# it (which costs as much as a small launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, checkpoint: bool = False, out=None, stream=None):

@@ -101,3 +101,10 @@ def test_linear_gradients_of_gradients(flp):
     want, = torch.autograd.grad((x.double() @ W.double().t()).square().sum(), x, create_graph=True)
     want, = torch.autograd.grad(want.sum(), x)
     assert float((twice.double() - want.double()).norm() / want.double().norm()) <= 0.02
+
+
+def test_the_stream_of_a_device_without_the_short_way(flp):
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert flp._stream_of(0) == flp._raw_stream(0) == side.cuda_stream
+    assert flp._stream_of(0) == flp._raw_stream(0) == torch.cuda.current_stream().cuda_stream
