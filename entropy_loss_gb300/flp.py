@@ -818,6 +818,9 @@ class CheckpointLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, W):
         if ctx.needs_input_grad[1]:
+            for t, name in ((x, "x"), (W, "W")):
+                if t.dtype is not torch.bfloat16:
+                    raise ValueError(f"{name}: expected bf16 (its gradient is taken on the tensor cores), got {t.dtype}")
             kept = checkpoint_pack(x)
             ctx.save_for_backward(kept.q, kept.scale, W)
         else:
@@ -837,7 +840,8 @@ class CheckpointLinear(torch.autograd.Function):
 
 
 def checkpoint_linear(x, W):
-    """Differentiable x W^T for bf16 x [M, K] and W [N, K] that keeps x in 8 bits."""
+    """Differentiable x W^T for bf16 x [M, K] and W [N, K] that keeps x in 8 bits
+    (where W needs no gradient, of any type, and x is not kept)."""
     return CheckpointLinear.apply(x, W)
 
 

@@ -103,6 +103,20 @@ def test_linear_gradients_of_gradients(flp):
     assert float((twice.double() - want.double()).norm() / want.double().norm()) <= 0.02
 
 
+def test_linear_refuses_what_its_backward_cannot_do(flp):
+    x = torch.randn(32, 64, device="cuda")
+    W = torch.randn(16, 64, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError):
+        flp.checkpoint_linear(x, W)
+    with pytest.raises(ValueError):
+        flp.checkpoint_linear(x.to(torch.bfloat16), W)
+    # without a gradient by W nothing is kept
+    frozen = W.detach()
+    x.requires_grad_()
+    flp.checkpoint_linear(x, frozen).sum().backward()
+    assert torch.equal(x.grad, torch.ones(32, 16, device="cuda") @ frozen)
+
+
 def test_the_stream_of_a_device_without_the_short_way(flp):
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
