@@ -176,7 +176,68 @@ bool norm_bwd_cluster(int64_t M, int64_t H) {
     return M <= kNormBwdCluster * kNormBwdClusterTrips * (H <= 512 ? 8 : 1) && H <= 8192;
 }
 
-constexpr int64_t kNormBwdBlocksPerSm = 8;  // the most any shape uses: what the workspace query allows for
+// The backward's kernel for rows of H columns: calls f(kernel, form), form being what a
+// launch of it needs.
+struct NormBwdForm {
+    int threads;
+    int64_t rows;   // of a block at a time
+    size_t staged;  // shared memory of the rows under way
+    size_t join;    // and of the warps' sums of a cluster's block, before its own 8 H bytes
+    size_t most;    // what the kernel's largest block needs
+};
+template <auto* K>
+struct NormBwdKernel {
+    static constexpr auto* kernel = K;
+};
+
+template <typename T, bool CK, bool LOOSE, typename F>
+flp_status norm_bwd_form(int64_t H, F&& f) {
+    return norm_stream_shape<T, 320, 4>(H, [&](auto shape, int threads) -> flp_status {
+        using X = decltype(shape);
+        // above 8192 columns one stage fits beside the weights and sums; two of aligned
+        // bf16 rows with a checkpoint (8192 x 8200 119 us, one stage: 133)
+        // and two of bf16 where the sums of dy wait there too (norm_bwd_db_shared)
+        constexpr bool WIDE = norm_bwd_wide<T, X::NV>();
+        constexpr bool TWO = sizeof(T) == 2 && norm_bwd_db_shared<T, X::NV, X::MAXT, CK, LOOSE>();
+        constexpr int S = WIDE && !(CK && !LOOSE && sizeof(T) == 2) ? 1 : TWO ? 2 : X::S;
+        constexpr auto* kernel = flp_norm_bwd_stream_kernel<T, X::NV, S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
+        // a cluster's block holds its warps' sums (a row per warp) and its own after the rows
+        constexpr size_t kJoin = X::WARP ? static_cast<size_t>(X::MAXT) * X::NV * wide_v<T>() * 4 : 0;
+        constexpr size_t kMostSums = WIDE ? 0 : kJoin + 8ull * (X::WARP ? 32 : X::MAXT) * X::NV * wide_v<T>();
+        NormBwdForm form;
+        form.threads = threads;
+        form.rows = X::WARP ? threads / 32 : 1;
+        form.staged = norm_stage_bytes<T, LOOSE>(S * X::NV, threads, CK ? 2 : 1);
+        form.join = kJoin;
+        form.most = std::max(norm_stage_bytes<T, LOOSE>(S * X::NV, X::MAXT, CK ? 2 : 1), kMostSums);
+        return f(NormBwdKernel<kernel>{}, form);
+    });
+}
+
+// Blocks of the backward's grid in any of its forms (either type, from X or from its
+// checkpoint, aligned or loose rows): what the workspace query allows for.
+flp_status norm_bwd_most_blocks(int64_t M, int64_t H, int sm_count, int64_t* most) {
+    *most = 0;
+    auto one = [&](auto t, auto ck, auto loose) {
+        return norm_bwd_form<decltype(t), decltype(ck)::value, decltype(loose)::value>(
+            H, [&](auto k, const NormBwdForm& form) -> flp_status {
+                int per_sm = 0;
+                const flp_status st = resident_blocks<decltype(k)::kernel>(form.threads, form.staged, form.most, &per_sm);
+                *most = std::max(*most, norm_bwd_blocks(M, form.rows, sm_count, per_sm));
+                return st;
+            });
+    };
+    auto rows = [&](auto t, auto ck) {
+        const flp_status st = one(t, ck, std::true_type{});
+        return st == FLP_OK ? one(t, ck, std::false_type{}) : st;
+    };
+    auto typed = [&](auto t) {
+        const flp_status st = rows(t, std::true_type{});
+        return st == FLP_OK ? rows(t, std::false_type{}) : st;
+    };
+    const flp_status st = typed(bf16{});
+    return st == FLP_OK ? typed(float{}) : st;
+}
 
 // -------------------------------------------------------------- weight gradient
 
@@ -506,9 +567,11 @@ extern "C" flp_status flp_layer_norm_workspace(int64_t M, int64_t H, size_t* byt
     DevInfo* d;
     st = step_device(&d);
     if (st != FLP_OK) return st;
-    *bytes = norm_bwd_cluster(M, H)
-                 ? 0
-                 : static_cast<size_t>(norm_bwd_blocks(M, 1, d->sm_count, kNormBwdBlocksPerSm)) * 2 * H * 4;
+    *bytes = 0;
+    if (norm_bwd_cluster(M, H)) return FLP_OK;
+    int64_t blocks = 0;
+    if ((st = norm_bwd_most_blocks(M, H, d->sm_count, &blocks)) != FLP_OK) return st;
+    *bytes = static_cast<size_t>(blocks) * 2 * H * 4;
     return FLP_OK;
 }
 
@@ -564,40 +627,24 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
         auto run = [&](auto t, auto ck, auto is_loose) -> flp_status {
             using T = decltype(t);
             constexpr bool CK = decltype(ck)::value, LOOSE = decltype(is_loose)::value;
-            return norm_stream_shape<T, 320, 4>(p.H, [&](auto shape, int threads) -> flp_status {
-                using X_ = decltype(shape);
-                // above 8192 columns one stage fits beside the weights and sums; two of aligned
-                // bf16 rows with a checkpoint (8192 x 8200 119 us, one stage: 133)
-                constexpr bool WIDE = norm_bwd_wide<T, X_::NV>();
-                // and two of bf16 where the sums of dy wait there too (norm_bwd_db_shared)
-                constexpr int S = WIDE && !(CK && !LOOSE && sizeof(T) == 2)                                       ? 1
-                                  : sizeof(T) == 2 && norm_bwd_db_shared<T, X_::NV, X_::MAXT, CK, LOOSE>() ? 2
-                                                                                                              : X_::S;
-                constexpr auto* kernel = flp_norm_bwd_stream_kernel<T, X_::NV, S, CK, LOOSE, X_::WARP, X_::MAXT, X_::MINB>;
-                // a cluster's block holds its warps' sums (a row per warp) and its own after the rows
-                constexpr size_t kJoin = X_::WARP ? static_cast<size_t>(X_::MAXT) * X_::NV * wide_v<T>() * 4 : 0;
-                constexpr size_t kMostSums =
-                    WIDE ? 0 : kJoin + 8ull * (X_::WARP ? 32 : X_::MAXT) * X_::NV * wide_v<T>();
-                const size_t staged = norm_stage_bytes<T, LOOSE>(S * X_::NV, threads, CK ? 2 : 1);
-                const size_t smem = std::max(staged, cluster ? kJoin + 8 * static_cast<size_t>(H) : 0);
-                const size_t most = std::max(norm_stage_bytes<T, LOOSE>(S * X_::NV, X_::MAXT, CK ? 2 : 1), kMostSums);
+            return norm_bwd_form<T, CK, LOOSE>(H, [&](auto k, const NormBwdForm& form) -> flp_status {
+                constexpr auto* kernel = decltype(k)::kernel;
+                const size_t smem = std::max(form.staged, cluster ? form.join + 8 * static_cast<size_t>(H) : 0);
                 int per_sm = 0;
-                const flp_status r = resident_blocks<kernel>(threads, staged, most, &per_sm);
+                const flp_status r = resident_blocks<kernel>(form.threads, form.staged, form.most, &per_sm);
                 if (r != FLP_OK) return r;
-                blocks = cluster ? kNormBwdCluster
-                                 : norm_bwd_blocks(M, X_::WARP ? threads / 32 : 1, d->sm_count,
-                                                   std::min<int64_t>(kNormBwdBlocksPerSm, per_sm));
+                blocks = cluster ? kNormBwdCluster : norm_bwd_blocks(M, form.rows, d->sm_count, per_sm);
                 if (!cluster && workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
                     return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
-                p.step = blocks * (X_::WARP ? threads / 32 : 1);
+                p.step = blocks * form.rows;
                 p.step_dy = p.step * lddy;
                 p.step_x = p.step * ldx;
                 p.step_dx = p.step * lddx;
                 p.step_q = p.step * p.Hp;
                 p.step_s = p.step_q / CK_BLOCK;
-                return cluster ? launch_cluster<NormBwdParams>(kernel, kNormBwdCluster, threads, smem, s,
+                return cluster ? launch_cluster<NormBwdParams>(kernel, kNormBwdCluster, form.threads, smem, s,
                                                                "flp_norm_bwd_stream_kernel launch", p)
-                               : launch_step(kernel, blocks, threads, smem, s, "flp_norm_bwd_stream_kernel launch",
+                               : launch_step(kernel, blocks, form.threads, smem, s, "flp_norm_bwd_stream_kernel launch",
                                              false, p);
             });
         };
