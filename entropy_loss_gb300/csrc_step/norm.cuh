@@ -52,7 +52,8 @@ struct NormBwdParams {
     float inv_h;
     void* dx;
     long long lddx;
-    float* part;  // [gridDim.x][2][H] fp32 partial sums of dw and db
+    bool sums;     // dw or db is wanted
+    float* part;   // [gridDim.x][2][H] fp32 partial sums of dw and db
     bool cluster;  // the blocks are one cluster and join their sums themselves, into
     float* dw;     // these (NULL: not written)
     float* db;
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     }
     cp_async_wait<0>();
     griddep_launch_dependents();
+    if (!p.sums) return;
     // this block's sums; with a row per warp, the warps join first (the ring is free)
     float* join = reinterpret_cast<float*>(ring);
     float* sums = join + (WARP ? (MAXT / 32) * (NV * 32 * V) : 0);  // [2][H] of a cluster's block

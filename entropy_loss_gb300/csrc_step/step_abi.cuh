@@ -599,9 +599,11 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
     int64_t blocks = 0;
     if (M > 0) {
         const bool cluster = norm_bwd_cluster(M, H);
-        if (!cluster && (!workspace || !aligned16(workspace)))
+        const bool parts = sums && !cluster;
+        if (parts && (!workspace || !aligned16(workspace)))
             return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace null or misaligned");
         NormBwdParams p{};
+        p.sums = sums;
         p.cluster = cluster;
         p.dw = dweight;
         p.db = dbias;
@@ -634,7 +636,7 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
                 const flp_status r = resident_blocks<kernel>(form.threads, form.staged, form.most, &per_sm);
                 if (r != FLP_OK) return r;
                 blocks = cluster ? kNormBwdCluster : norm_bwd_blocks(M, form.rows, d->sm_count, per_sm);
-                if (!cluster && workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
+                if (parts && workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
                     return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
                 p.step = blocks * form.rows;
                 p.step_dy = p.step * lddy;

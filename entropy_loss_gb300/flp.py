@@ -582,12 +582,15 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, checkpoint: bool
     return (out, mean, rstd, kept) if checkpoint else (out, mean, rstd)
 
 
-def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, workspace=None, stream=None):
+def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, want_dweight: bool = True, want_dbias: bool = True,
+                        workspace=None, stream=None):
     """(dx, dweight, dbias) of layer_norm; x is the activation (dy's type) or
     its Checkpoint8, mean and rstd the forward's.  dx has dy's type, dweight
-    and dbias are fp32.  Without a weight its gradient is the one of all ones."""
+    and dbias are fp32, or None where they are not wanted.  Without a weight its
+    gradient is the one of all ones."""
     if stream is not None:
-        return _on_stream(stream, layer_norm_backward, dy, x, weight, mean, rstd, dx=dx, workspace=workspace)
+        return _on_stream(stream, layer_norm_backward, dy, x, weight, mean, rstd, dx=dx, want_dweight=want_dweight,
+                          want_dbias=want_dbias, workspace=workspace)
     dyp, lddy = _rows(dy, "dy")
     M, H = shape = dy.shape
     dt, dev = dy.dtype, dy.device
@@ -610,14 +613,15 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, workspace=None, s
         dxp, lddx = dx.data_ptr(), H
     else:
         dxp, lddx = _rows(dx, "dx", shape, dt)
-    dweight = torch.empty(H, dtype=torch.float32, device=dev)
-    dbias = torch.empty(H, dtype=torch.float32, device=dev)
+    dweight = torch.empty(H, dtype=torch.float32, device=dev) if want_dweight else None
+    dbias = torch.empty(H, dtype=torch.float32, device=dev) if want_dbias else None
     device = dev.index
-    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None or not (want_dweight or want_dbias) else
                                    _workspace_bytes("flp_layer_norm_workspace", device, M, H))
     status = load().flp_layer_norm_backward(dyp, lddy, xp, ldx, qp, sp, code, wp, code if wt is None else wt,
-                                            mean.data_ptr(), rstd.data_ptr(), M, H, dxp, lddx, dweight.data_ptr(),
-                                            dbias.data_ptr(), ws, ws_bytes, _raw_stream(device))
+                                            mean.data_ptr(), rstd.data_ptr(), M, H, dxp, lddx,
+                                            dweight.data_ptr() if want_dweight else None,
+                                            dbias.data_ptr() if want_dbias else None, ws, ws_bytes, _raw_stream(device))
     if status:
         _check(status, "flp_layer_norm_backward")
     return dx, dweight, dbias
@@ -801,9 +805,12 @@ class FusedLayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         saved, scale, weight, bias, mean, rstd = ctx.saved_tensors
         x = saved if ctx.kept is None else Checkpoint8(saved, scale, *ctx.kept)
-        dx, dweight, dbias = _once(lambda: layer_norm_backward(dy.contiguous(), x, weight, mean, rstd), dy, saved, weight)
-        return (dx, None if weight is None else dweight.to(weight.dtype),
-                None if bias is None else dbias.to(bias.dtype), None, None)
+        _, want_dweight, want_dbias, _, _ = ctx.needs_input_grad
+        dx, dweight, dbias = _once(lambda: layer_norm_backward(dy.contiguous(), x, weight, mean, rstd,
+                                                               want_dweight=want_dweight, want_dbias=want_dbias),
+                                   dy, saved, weight)
+        return (dx, dweight.to(weight.dtype) if want_dweight else None,
+                dbias.to(bias.dtype) if want_dbias else None, None, None)
 
 
 def fused_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint: bool = False):

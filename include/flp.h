@@ -442,7 +442,8 @@ flp_status flp_layer_norm_workspace(int64_t M, int64_t H, size_t* bytes);
  *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy   (fp32 [H])
  * The activations come as X (the type of dY) or as their checkpoint q, scale
  * (exactly one of the two); mean and rstd are the forward's.  dweight and
- * dbias may be NULL.  M == 0 writes zeros to them.  dX may be dY itself.
+ * dbias may be NULL (with both NULL no workspace is needed).  M == 0 writes
+ * zeros to them.  dX may be dY itself.
  */
 flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* q,
                                    const void* scale, int dtype, const void* weight, int param_dtype,

@@ -38,3 +38,36 @@ def test_enough_for_every_form(flp, M, H, dtype):  # noqa: F811
             values = f64(x) if acts is x else f64(flp.checkpoint_unpack(kept, dtype=torch.float32))
             check_backward(dy, values, None, mean, rstd, dx, dw, db)
     assert (ws[need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("M,H", [(3, 64), (60, 520), (700, 300), (700, 1023), (700, 4096), (330, 16384)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sums_that_are_not_wanted(flp, M, H, dtype):  # noqa: F811
+    """dx is the same without them, they are the same alone, and without any no
+    workspace is needed: neither by the binding nor by the C entry."""
+    g = torch.Generator().manual_seed(M + H)
+    x, dy = (torch.randn(M, H, generator=g).to(dtype).cuda() for _ in range(2))
+    w = torch.rand(H, generator=g).to(dtype).cuda()
+    y, mean, rstd, kept = flp.layer_norm(x, w, checkpoint=True)
+    for acts in (x, kept):
+        dx, dw, db = flp.layer_norm_backward(dy, acts, w, mean, rstd)
+        a, none, db1 = flp.layer_norm_backward(dy, acts, w, mean, rstd, want_dweight=False)
+        b, dw1, none2 = flp.layer_norm_backward(dy, acts, w, mean, rstd, want_dbias=False)
+        tiny = torch.empty(0, dtype=torch.uint8, device="cuda")
+        c, none3, none4 = flp.layer_norm_backward(dy, acts, w, mean, rstd, want_dweight=False, want_dbias=False,
+                                                  workspace=tiny)
+        assert none is none2 is none3 is none4 is None
+        assert torch.equal(db, db1) and torch.equal(dw, dw1)
+        assert torch.equal(dx, a) and torch.equal(dx, b) and torch.equal(dx, c)
+
+
+def test_a_frozen_norm_takes_no_sums(flp, monkeypatch):  # noqa: F811
+    x = torch.randn(2000, 256, device="cuda", requires_grad=True)
+    w, b = torch.rand(256, device="cuda"), torch.rand(256, device="cuda", requires_grad=True)
+    seen = []
+    real = flp.layer_norm_backward
+    monkeypatch.setattr(flp, "layer_norm_backward", lambda *a, **k: seen.append(k) or real(*a, **k))
+    flp.fused_layer_norm(x, w, b.detach()).sum().backward()
+    flp.fused_layer_norm(x, w, b).sum().backward()
+    assert seen[0] == dict(want_dweight=False, want_dbias=False) and seen[1] == dict(want_dweight=False, want_dbias=True)
+    assert float((b.grad - 2000).abs().max()) == 0
