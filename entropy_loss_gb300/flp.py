@@ -796,6 +796,7 @@ class FusedLayerNorm(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps, checkpoint):
+        checkpoint = checkpoint and any(ctx.needs_input_grad)  # a checkpoint only for a backward pass
         y, mean, rstd, *kept = layer_norm(x, weight, bias, eps=eps, checkpoint=checkpoint)
         ctx.save_for_backward(*((kept[0].q, kept[0].scale) if checkpoint else (x, None)), weight, bias, mean, rstd)
         ctx.kept = (x.shape[1], x.dtype) if checkpoint else None
@@ -815,7 +816,8 @@ class FusedLayerNorm(torch.autograd.Function):
 
 def fused_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, checkpoint: bool = False):
     """Differentiable layer norm of the rows of x [M, H]."""
-    return FusedLayerNorm.apply(x, weight, bias, eps, checkpoint)
+    # a Function's forward cannot tell that nothing is recorded
+    return FusedLayerNorm.apply(x, weight, bias, eps, checkpoint and torch.is_grad_enabled())
 
 
 class CheckpointLinear(torch.autograd.Function):
@@ -849,7 +851,7 @@ class CheckpointLinear(torch.autograd.Function):
 def checkpoint_linear(x, W):
     """Differentiable x W^T for bf16 x [M, K] and W [N, K] that keeps x in 8 bits
     (where W needs no gradient, of any type, and x is not kept)."""
-    return CheckpointLinear.apply(x, W)
+    return CheckpointLinear.apply(x, W) if torch.is_grad_enabled() else x @ W.t()
 
 
 class FusedBalanceLoss(torch.autograd.Function):
@@ -874,4 +876,7 @@ class FusedBalanceLoss(torch.autograd.Function):
 
 def fused_balance_loss(logits, top_k: int, experts=None, mask=None, coef: float = 1.0):
     """Differentiable balance loss of router logits [T, E]: (scalar loss, counts [E])."""
+    if not torch.is_grad_enabled():
+        loss_out, _, counts = balance_loss(logits, top_k, experts=experts, mask=mask, coef=coef, grad=False)
+        return loss_out[0], counts
     return FusedBalanceLoss.apply(logits, top_k, experts, mask, coef)

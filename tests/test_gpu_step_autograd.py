@@ -122,3 +122,35 @@ def test_the_stream_of_a_device_without_the_short_way(flp):
     with torch.cuda.stream(side):
         assert flp._stream_of(0) == flp._raw_stream(0) == side.cuda_stream
     assert flp._stream_of(0) == flp._raw_stream(0) == torch.cuda.current_stream().cuda_stream
+
+
+def test_only_a_backward_pass_is_prepared_for(flp, monkeypatch):
+    """Without one no checkpoint is written and no gradient taken, in eval loops
+    (no_grad) as well as where no input needs a gradient."""
+    seen = []
+    norm, pack, balance = flp.layer_norm, flp.checkpoint_pack, flp.balance_loss
+    monkeypatch.setattr(flp, "layer_norm", lambda *a, **k: seen.append(k["checkpoint"]) or norm(*a, **k))
+    monkeypatch.setattr(flp, "checkpoint_pack", lambda *a, **k: seen.append("pack") or pack(*a, **k))
+    monkeypatch.setattr(flp, "balance_loss", lambda *a, **k: seen.append(k["grad"]) or balance(*a, **k))
+    x, w = torch.randn(40, 64, device="cuda").to(torch.bfloat16), torch.rand(64, device="cuda")
+    W = torch.randn(16, 64, device="cuda").to(torch.bfloat16)
+
+    def forward():
+        n = flp.fused_layer_norm(x, w, None, checkpoint=True)
+        z = flp.checkpoint_linear(n, W)
+        return (n, z, *flp.fused_balance_loss(z, 2))
+
+    plain = forward()
+    assert seen == [False, False]
+    for t in (x, w, W):
+        t.requires_grad_()
+    seen.clear()
+    with torch.no_grad():
+        off = forward()
+    assert seen == [False, False] and not any(t.requires_grad for t in off)
+    seen.clear()
+    on = forward()
+    assert seen == [True, "pack", True]
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(plain, off, on))
+    (on[1].float().sum() + on[2]).backward()
+    assert all(t.grad is not None for t in (x, w, W))
