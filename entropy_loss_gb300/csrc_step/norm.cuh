@@ -31,7 +31,8 @@ struct NormFwdParams {
     uint8_t* q;  // the checkpoint of x (CK): [M, Hp], Hp = H rounded up to 32
     uint8_t* scale;
     int Hp;
-    // from a group's row to its next, in elements: rows, x, y, q, scale
+    // from a group's row to its next (an even number of rows, if there is a next), in
+    // elements: rows, x, y, q, scale
     long long step, step_x, step_y, step_q, step_s;
 };
 
@@ -57,7 +58,8 @@ struct NormBwdParams {
     bool cluster;  // the blocks are one cluster and join their sums themselves, into
     float* dw;     // these (NULL: not written)
     float* db;
-    // from a group's row to its next, in elements: rows, dy, x, dx, q, scale
+    // from a group's row to its next (an even number of rows, if there is a next), in
+    // elements: rows, dy, x, dx, q, scale
     long long step, step_dy, step_x, step_dx, step_q, step_s;
 };
 
@@ -100,9 +102,8 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
     const T* ahead = static_cast<const T*>(p.x) + first * p.ldx + t * V;  // of the next row to fetch
     int rows_left = first < p.M ? static_cast<int>((p.M - first + step - 1) / step) : 0, to_fetch = rows_left;
     long long fetch_row = first;
-    // bf16 rows that start at an odd element (LOOSE), this one and whether it alternates
-    bool odd = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead) & 2);
-    const bool alternates = X::SHIFT && (p.step_x & 1);
+    // bf16 rows that start at an odd element (LOOSE): all of this group's, step being even
+    const bool odd = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead) & 2);
     auto fetch = [&](uint32_t slot) {
         if (to_fetch > 0) {
             const bool edge = LOOSE && (fetch_row == 0 || fetch_row == p.M - 1);
@@ -199,7 +200,6 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_fwd_stream_kernel(const N
             store_row_vec<T, LOOSE>(y + k * apart, Pairs<T>::put(o), valid[k], stage);
         }
         y += p.step_y;
-        odd ^= alternates;
         if constexpr (CK) {
             q += p.step_q;
             scale += p.step_s;
@@ -261,10 +261,9 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     const uint8_t* ahead_q = CK ? p.q + first * p.Hp + t * V : nullptr;
     int rows_left = first < p.M ? static_cast<int>((p.M - first + step - 1) / step) : 0, to_fetch = rows_left;
     long long fetch_row = first;
-    // bf16 rows that start at an odd element (LOOSE), these ones and whether they alternate
-    bool odd_y = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_y) & 2);
-    bool odd_x = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_x) & 2);
-    const bool alternates_y = X::SHIFT && (p.step_dy & 1), alternates_x = X::SHIFT && (p.step_x & 1);
+    // bf16 rows that start at an odd element (LOOSE): all of this group's, step being even
+    const bool odd_y = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_y) & 2);
+    const bool odd_x = X::SHIFT && (reinterpret_cast<uintptr_t>(ahead_x) & 2);
     auto fetch = [&](uint32_t slot, uint32_t slot_x) {
         if (to_fetch > 0) {
             const bool edge = LOOSE && (fetch_row == 0 || fetch_row == p.M - 1);
@@ -433,8 +432,6 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
             store_row_vec<T, LOOSE>(dx + k * apart, Pairs<T>::put(o), valid[k], stage);
         }
         dx += p.step_dx;
-        odd_y ^= alternates_y;
-        odd_x ^= alternates_x;
         --rows_left;
     };
     while (rows_left > 0) {

@@ -160,10 +160,12 @@ flp_status row_checks(const void* p, int64_t ld, int64_t H, int dtype, const cha
     return FLP_OK;
 }
 
-// Blocks of the norm backward: each writes 2 H partial sums, so no more than
-// fill the device.
-int64_t norm_bwd_blocks(int64_t M, int64_t rows_per_block, int sm_count, int64_t blocks_per_sm) {
-    return std::max<int64_t>(1, std::min(cdiv(M, rows_per_block), sm_count * blocks_per_sm));
+// Blocks of a streaming grid: as many as the rows fill, or fit the device.  A group takes
+// a second row in the second case alone, `blocks` times the block's rows further on: an
+// even number, so that a loose bf16 row of an odd pitch starts at the parity of the one
+// before (the SMs come in pairs).
+int64_t norm_blocks(int64_t M, int64_t rows_per_block, int sm_count, int64_t blocks_per_sm) {
+    return std::max<int64_t>(1, std::min(cdiv(M, rows_per_block), sm_count / 2 * 2 * blocks_per_sm));
 }
 
 // Few rows: one cluster of blocks joins its column sums through distributed shared
@@ -223,7 +225,7 @@ flp_status norm_bwd_most_blocks(int64_t M, int64_t H, int sm_count, int64_t* mos
             H, [&](auto k, const NormBwdForm& form) -> flp_status {
                 int per_sm = 0;
                 const flp_status st = resident_blocks<decltype(k)::kernel>(form.threads, form.staged, form.most, &per_sm);
-                *most = std::max(*most, norm_bwd_blocks(M, form.rows, sm_count, per_sm));
+                *most = std::max(*most, norm_blocks(M, form.rows, sm_count, per_sm));
                 return st;
             });
     };
@@ -546,7 +548,7 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
             const flp_status r = resident_blocks<kernel>(threads, smem, most, &per_sm);
             if (r != FLP_OK) return r;
             const int64_t rows = X::WARP ? threads / 32 : 1;
-            const int64_t blocks = std::min<int64_t>(cdiv(M, rows), static_cast<int64_t>(per_sm) * d->sm_count);
+            const int64_t blocks = norm_blocks(M, rows, d->sm_count, per_sm);
             p.step = blocks * rows;
             p.step_x = p.step * ldx;
             p.step_y = p.step * ldy;
@@ -635,7 +637,7 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
                 int per_sm = 0;
                 const flp_status r = resident_blocks<kernel>(form.threads, form.staged, form.most, &per_sm);
                 if (r != FLP_OK) return r;
-                blocks = cluster ? kNormBwdCluster : norm_bwd_blocks(M, form.rows, d->sm_count, per_sm);
+                blocks = cluster ? kNormBwdCluster : norm_blocks(M, form.rows, d->sm_count, per_sm);
                 if (parts && workspace_bytes < static_cast<size_t>(blocks) * 2 * H * 4)
                     return fail(FLP_ERR_WORKSPACE, "layer norm backward workspace too small");
                 p.step = blocks * form.rows;
