@@ -170,13 +170,14 @@ int64_t norm_blocks(int64_t M, int64_t rows_per_block, int sm_count, int64_t blo
 
 // Few rows: one cluster of blocks joins its column sums through distributed shared
 // memory, without the workspace and the second launch (a row per warp up to 512
-// columns, else per block): a call of 256 x 256 takes 18.5 us instead of 22, on the
-// GPU 5.0 instead of 4.4; at the rule's end, 64 x 4096, 10.1 instead of 6.9.  Above
-// 8192 columns the sums do not fit beside the rows.
-constexpr int kNormBwdCluster = 8, kNormBwdClusterTrips = 8;
-bool norm_bwd_cluster(int64_t M, int64_t H) {
-    return M <= kNormBwdCluster * kNormBwdClusterTrips * (H <= 512 ? 8 : 1) && H <= 8192;
-}
+// columns, else per block).  A call takes 20 us instead of 23.  On the GPU it is the
+// faster form up to 64 rows of 512 columns or fewer and 16 rows of 4096 or more; the
+// rule goes on while it takes at most 1 us more (256 x 256 4.8 against 4.0, 256 x 512
+// 6.1 against 4.9, 16 x 1024 4.4 against 3.7, 16 x 8192 7.9 against 10.1; twice as many
+// rows 5.9 against 4.2, 7.7 against 5.1, 5.2 against 3.8, 9.7 against 10.4, but fp32 10.4
+// against 7.8).  Above 8192 columns the sums do not fit beside the rows.
+constexpr int kNormBwdCluster = 8;
+bool norm_bwd_cluster(int64_t M, int64_t H) { return M <= kNormBwdCluster * (H <= 512 ? 32 : 2) && H <= 8192; }
 
 // The backward's kernel for rows of H columns: calls f(kernel, form), form being what a
 // launch of it needs.

@@ -71,3 +71,24 @@ def test_a_frozen_norm_takes_no_sums(flp, monkeypatch):  # noqa: F811
     flp.fused_layer_norm(x, w, b).sum().backward()
     assert seen[0] == dict(want_dweight=False, want_dbias=False) and seen[1] == dict(want_dweight=False, want_dbias=True)
     assert float((b.grad - 2000).abs().max()) == 0
+
+
+def test_few_rows_take_one_launch(flp):  # noqa: F811
+    """They need no workspace; more rows, whose cluster would take longer, do."""
+    for M, H in ((1, 1), (256, 256), (256, 512), (16, 520), (16, 1024), (16, 8192)):
+        assert query(flp, M, H) == 0, (M, H)
+    for M, H in ((257, 256), (257, 512), (17, 520), (64, 1024), (64, 4096), (17, 8192), (1, 8200)):
+        assert query(flp, M, H) > 0, (M, H)
+
+
+@pytest.mark.parametrize("M,H", [(255, 512), (256, 33), (257, 512), (15, 1023), (16, 5120), (17, 5120), (9, 8192), (18, 8192)])
+def test_both_sides_of_the_rule(flp, M, H):  # noqa: F811
+    g = torch.Generator().manual_seed(M + H)
+    for dtype in (torch.bfloat16, torch.float32):
+        x, dy = (torch.randn(M, H, generator=g).to(dtype).cuda() for _ in range(2))
+        w = torch.rand(H, generator=g).to(dtype).cuda()
+        y, mean, rstd, kept = flp.layer_norm(x, w, checkpoint=True)
+        dx, dw, db = flp.layer_norm_backward(dy, x, w, mean, rstd)
+        check_backward(dy, f64(x), w, mean, rstd, dx, dw, db)
+        dx, dw, db = flp.layer_norm_backward(dy, kept, w, mean, rstd)
+        check_backward(dy, f64(flp.checkpoint_unpack(kept, dtype=torch.float32)), w, mean, rstd, dx, dw, db)
