@@ -63,6 +63,7 @@ flp_status step_device(DevInfo** d) {
 
 inline bool is_dtype(int t) { return t == FLP_F32 || t == FLP_BF16; }
 inline int64_t elem(int t) { return t == FLP_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 inline int64_t ck_cols(int64_t H) { return cdiv(H, CK_BLOCK) * CK_BLOCK; }
 
 // Whether rows at this base and pitch (in elements) are 16-byte aligned.
@@ -141,8 +142,7 @@ flp_status norm_checks(int64_t M, int64_t H, int dtype, int param_dtype, const v
     if (!is_dtype(dtype) || !is_dtype(param_dtype)) return fail(FLP_ERR_INVALID_ARG, "dtypes are FLP_F32 or FLP_BF16");
     if (M > kMaxRows) return fail(FLP_ERR_UNSUPPORTED, "more than 2^31 - 1 rows");
     if (H > NORM_MAX_H) return fail(FLP_ERR_UNSUPPORTED, "layer norm rows hold at most 16384 elements");
-    if ((weight && reinterpret_cast<uintptr_t>(weight) % elem(param_dtype)) ||
-        (bias && reinterpret_cast<uintptr_t>(bias) % elem(param_dtype)))
+    if (!aligned_to(weight, elem(param_dtype)) || !aligned_to(bias, elem(param_dtype)))
         return fail(FLP_ERR_INVALID_ARG, "weight and bias must be aligned to their elements");
     return FLP_OK;
 }
@@ -155,7 +155,7 @@ flp_status ck_checks(const void* q, const void* scale) {
 
 flp_status row_checks(const void* p, int64_t ld, int64_t H, int dtype, const char* what) {
     if (!p) return fail(FLP_ERR_INVALID_ARG, what);
-    if (ld < H || reinterpret_cast<uintptr_t>(p) % elem(dtype))
+    if (ld < H || !aligned_to(p, elem(dtype)))
         return fail(FLP_ERR_INVALID_ARG, "row pitch below the width, or a pointer not aligned to its elements");
     return FLP_OK;
 }
@@ -301,7 +301,7 @@ flp_status wgrad_checks(const void* dY, int64_t lddy, int64_t M, int64_t N, int6
         return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
     if (!is_dtype(dw_dtype)) return fail(FLP_ERR_INVALID_ARG, "dW_dtype is FLP_F32 or FLP_BF16");
     if (M > 0 && lddy < N) return fail(FLP_ERR_INVALID_ARG, "row pitch of dY below N");
-    if (reinterpret_cast<uintptr_t>(dY) % 2) return fail(FLP_ERR_INVALID_ARG, "dY must be aligned to its elements");
+    if (!aligned_to(dY, 2)) return fail(FLP_ERR_INVALID_ARG, "dY must be aligned to its elements");
     return FLP_OK;
 }
 
@@ -505,6 +505,8 @@ extern "C" flp_status flp_layer_norm(const void* X, int64_t ldx, int dtype, cons
     flp_status st = norm_checks(M, H, dtype, param_dtype, weight, bias);
     if (st != FLP_OK) return st;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(FLP_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!aligned_to(mean, 4) || !aligned_to(rstd, 4))
+        return fail(FLP_ERR_INVALID_ARG, "mean and rstd must be aligned to their elements");
     if (M == 0) return FLP_OK;
     st = row_checks(X, ldx, H, dtype, "X must be non-null");
     if (st == FLP_OK) st = row_checks(Y, ldy, H, dtype, "Y must be non-null");
@@ -585,6 +587,8 @@ extern "C" flp_status flp_layer_norm_backward(const void* dY, int64_t lddy, cons
                                               size_t workspace_bytes, void* stream) {
     flp_status st = norm_checks(M, H, dtype, param_dtype, weight, nullptr);
     if (st != FLP_OK) return st;
+    if (!aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
+        return fail(FLP_ERR_INVALID_ARG, "mean, rstd, dweight and dbias must be aligned to their elements");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     DevInfo* d;
     if (M > 0) {
@@ -800,9 +804,11 @@ extern "C" flp_status flp_balance_loss_ex(const void* logits, int64_t ld, int dt
     if (grad_dtype != dtype && grad_dtype != FLP_F32)
         return fail(FLP_ERR_INVALID_ARG, "grad_dtype is the logits' type or FLP_F32");
     if (!loss || !counts) return fail(FLP_ERR_INVALID_ARG, "loss and counts must be non-null");
+    if (!aligned_to(loss, 4) || !aligned_to(counts, 8) || !aligned_to(experts, 8))
+        return fail(FLP_ERR_INVALID_ARG, "loss, counts and experts must be aligned to their elements");
     if (!std::isfinite(coef)) return fail(FLP_ERR_INVALID_ARG, "coef must be finite");
     if (T > 0 && (st = row_checks(logits, ld, E, dtype, "logits must be non-null")) != FLP_OK) return st;
-    if (reinterpret_cast<uintptr_t>(grad) % elem(grad_dtype))
+    if (!aligned_to(grad, elem(grad_dtype)))
         return fail(FLP_ERR_INVALID_ARG, "grad must be aligned to its elements");
     DevInfo* d;
     st = step_device(&d);
@@ -837,8 +843,7 @@ extern "C" flp_status flp_balance_loss_ex(const void* logits, int64_t ld, int dt
     const size_t smem = bal_smem(E);
     auto typed = [&](auto t) -> flp_status {
         using T_ = decltype(t);
-        const bool vec = E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * elem(dtype)) == 0 &&
-                         reinterpret_cast<uintptr_t>(grad) % (4 * elem(grad_dtype)) == 0;
+        const bool vec = E % 4 == 0 && ld % 4 == 0 && aligned_to(logits, 4 * elem(dtype)) && aligned_to(grad, 4 * elem(grad_dtype));
         return balance_shape(E, vec, [&](auto l, auto ne, auto v) -> flp_status {
             constexpr int L = decltype(l)::value, NE = decltype(ne)::value, V = decltype(v)::value;
             if (b.cluster)

@@ -415,8 +415,8 @@ flp_status flp_selftest_dz_wait_timeout(void* workspace, size_t workspace_bytes,
  * conventions above (asynchronous on `stream`, caller-owned memory,
  * deterministic, argument errors returned before any launch) except that rows
  * may have a pitch (ld*, in elements, at least the width) and any width and
- * alignment: 16-byte vectors are used where base, pitch and width allow, else
- * single elements.
+ * alignment: rows move as 16-byte vectors where base, pitch and width allow,
+ * else as 4-byte words.  Every pointer is aligned to its elements.
  */
 
 /*
