@@ -297,7 +297,7 @@ WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t
 flp_status wgrad_checks(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t K, int dw_dtype) {
     if (M < 0 || N < 1 || K < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0, N >= 1 and K >= 1 required");
     if (M > kMaxRows - 256 || N > kMaxRows - 1024 || K > kMaxRows - 1024 ||
-        cdiv(N, PM) * cdiv(K, 2 * BN) > (1 << 24))
+        cdiv(N, PM) * cdiv(K, 2 * BN) >= (1 << 23))  // partial tiles: below 2^31 rows (more than 4 x pairs are not split)
         return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
     if (!is_dtype(dw_dtype)) return fail(FLP_ERR_INVALID_ARG, "dW_dtype is FLP_F32 or FLP_BF16");
     if (M > 0 && lddy < N) return fail(FLP_ERR_INVALID_ARG, "row pitch of dY below N");
@@ -330,7 +330,6 @@ flp_status wgrad_contract(const WgradPlan& w, const void* y, int64_t ldy, uint8_
     if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ws + w.off_x, w.Kp, M, w.Kp * 2, 64, 64)) != FLP_OK)
         return st;
     const size_t part_rows = static_cast<size_t>(w.rest) * w.splits * PM;
-    if (part_rows > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
     // without split tiles (or without whole ones) one of the two output maps is
     // not used: it repeats the other
     if (w.rest &&

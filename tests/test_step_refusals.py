@@ -58,3 +58,11 @@ def test_weight_gradient_selftest(flp, b):
     assert f(b + 4, 1 << 30, 0, 1, 1000, None) == flp.FLP_ERR_WORKSPACE
     for limit in (0, -5, 61 * 10**9):
         assert f(b, 1 << 30, 0, 1, limit, None) == flp.FLP_ERR_INVALID_ARG
+
+
+def test_weight_gradient_sizes_beyond_the_tiling(flp, b):
+    """2^23 tiles of 256 x 512 (4 TB of dW): refused like every other argument, before a device is touched."""
+    need = ctypes.c_size_t(0)
+    N, K = 256 << 12, 512 << 11
+    assert flp.load().flp_checkpoint_weight_grad(b, N, b, b, 8, N, K, b, 0, 0, b, 4096, None) == flp.FLP_ERR_UNSUPPORTED
+    assert flp.load().flp_checkpoint_weight_grad_workspace(b, N, 8, N, K, 0, ctypes.byref(need)) == flp.FLP_ERR_UNSUPPORTED
