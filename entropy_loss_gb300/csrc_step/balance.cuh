@@ -25,9 +25,9 @@
 // The floor is one read of the logits and one write of the gradient.  Few tokens are
 // bound by the launch and the cluster's exchange (64 x 8: 8 us), many by the rows'
 // pass, whose choice of experts takes most of the instructions: 65536 x 256 fp32, top
-// 8, takes 51 us, 28 of them in the rows' pass (64 % of the issue slots; its 67 MB would
-// take 10), the rest in the join and the gradient's, against a floor of 20 us; top 24
-// takes 134 us.  The gradient needs the counts of all rows, and so a second read of the
+// 8, takes 48 us, 26 of them in the rows' pass (66 % of the issue slots; its 67 MB would
+// take 10), the rest in the join and the gradient's, against a floor of 20 us; bf16, half
+// the bytes, 49 us against 10; top 24 takes 132 us.  The gradient needs the counts of all rows, and so a second read of the
 // logits (of which an SM's share, 441 KB in that case, does not fit its shared memory).
 #pragma once
 #include "vec.cuh"
@@ -214,7 +214,8 @@ __device__ __forceinline__ bool chosen_by_rank(uint32_t key, int l, int k) {
 // at or above the bound are candidates, and the smallest are dropped until k are left
 // (about one for 256 experts and k = 8).  Above BAL_BOUND_K the experts are taken one at
 // a time, which drops nothing when many of the largest share a lane (65536 x 256 fp32:
-// k = 20 takes 99 us by the bound, 132 one at a time, k = 24 134 and 149).
+// k = 20 takes 95 us by the bound, 125 one at a time, k = 24 132 and 143, k = 28 199 and
+// 163; bf16 102 and 124, 146 and 142, 288 and 160).
 // `top`: the lane's largest logit, `most`: the row's.
 template <int NE>
 __host__ __device__ constexpr int bal_words() { return (NE + 7) / 8; }
@@ -305,8 +306,8 @@ __device__ __forceinline__ BalSums bal_sums(uint32_t* dyn, int E) {
     return s;
 }
 
-// Whether the next row's logits are loaded before this row is worked on: not where
-// that spills (1024 experts).
+// Whether the next row's logits are loaded before this row is worked on: not with 1024
+// experts, whose rows spill as it is (fp32 177 -> 196 us; bf16 161 -> 154).
 template <int NE>
 constexpr bool BAL_AHEAD = NE <= 16;
 
@@ -410,8 +411,8 @@ __device__ __forceinline__ void balance_rows(const BalParams& p, const BalSums& 
                 }
             }
         };
-        // 16 or more experts a lane: first, while their logits are all that is held
-        // (1024 experts 310 -> 173 us with the loads below; 256 would go from 53 to 54.5 us)
+        // 16 or more experts a lane: first, while their logits are all that is held (1024
+        // bf16 experts 164 -> 161 us; 256 stay at 49)
         if constexpr (NE >= 16) choice();
         // the difference is formed first: its error grows with its own size alone
         float ex[NE], s = 0.f;

@@ -23,9 +23,8 @@ struct CkParams {
 };
 
 constexpr int CK_THREADS = 256;
-// Vectors in flight per thread: writing a checkpoint 4 (32768 x 4096 bf16 62 us; 2:
-// 68, 8: 66), reading one, which stores twice what it loads, 2 (4 took 12 % longer, 1
-// 7 %).
+// Vectors in flight per thread: writing a checkpoint 4 (32768 x 4096 bf16 62 us; 2: 67, 8
+// spill), reading one, which stores twice what it loads, 2 (60 us; 1: 72, 4: 63).
 constexpr int CK_PACK_N = 4;
 constexpr int CK_UNPACK_N = 2;
 // Blocks an SM must hold of the writing kernel: 5 bound the registers of aligned rows

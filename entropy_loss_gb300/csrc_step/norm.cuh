@@ -228,8 +228,9 @@ __host__ __device__ constexpr bool norm_bwd_db_shared() {
 // 83 % (its bytes are turned into pairs, 54 % of the issue slots); 32768 x 5120 161 us,
 // 93 %, from a checkpoint 166 us, 75 %.  Above 8192 columns the weights (bf16) and the sums of dy
 // wait in shared memory, which leaves room for one row in flight: 8192 x 16384 bf16
-// 158 us, 75 % (265 us with both in registers), from a checkpoint 181 us, 55 %; fp32
-// 271 us, 88 % (319 us), although that form and the loose ones still spill a few values.
+// 158 us, 75 % (195 us with the sums in registers, 202 with the weights), from a
+// checkpoint 181 us, 55 % (222); fp32 273 us, 87 % (320), although that form and the
+// loose ones still spill a few values.
 template <typename T, int NV, int S, bool CK, bool LOOSE, bool WARP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const NormBwdParams p) {
     using X = Stage<T, LOOSE>;
@@ -287,9 +288,9 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     };
     // what a row needs beside its vectors, AHEAD rows before it in registers: two where
     // rows are short or registers are left for it (a miss takes longer than a row), else
-    // one (32768 x 4096 bf16 139 -> 127 us, 16384 x 8192 159 -> 136 us; from a checkpoint
-    // 32768 x 5120 193 -> 175 us, 8192 x 16384 210 -> 180 us, but at 32768 x 4096 122 -> 126
-    // us, and loose bf16 rows of 12000 x 10001 374 -> 419 us)
+    // one (one instead of two: 32768 x 4096 bf16 139 -> 127 us, 16384 x 8192 162 -> 136,
+    // 8192 x 16384 164 -> 158; from a checkpoint 32768 x 5120 171 -> 165, 8192 x 16384
+    // 220 -> 181, but 32768 x 4096 120 -> 122 and loose bf16 rows of 12000 x 10001 324 -> 419)
     constexpr bool WIDE = norm_bwd_wide<T, NV>();
     constexpr int AHEAD = (LOOSE ? CK && WIDE && sizeof(T) == 2 : WARP || (CK && MAXT != 320 && !WIDE)) ? 2 : 1;
     struct Few {
@@ -327,9 +328,10 @@ __global__ void __launch_bounds__(MAXT, MINB) flp_norm_bwd_stream_kernel(const N
     Few even{}, other{};
     fetch_few(even, rows_left > 0);
     if (AHEAD == 2) fetch_few(other, rows_left > 1);
-    // where registers are short the weights wait in shared memory, each thread's own:
-    // 32768 x 5120 bf16 228 -> 188 us from a checkpoint (at 32768 x 4096 145 -> 122 us, but
-    // 138 -> 141 us without one), and the sums of dy as well (norm_bwd_db_shared)
+    // where registers are short the weights wait in shared memory, each thread's own
+    // (from a checkpoint 32768 x 4096 bf16 149 -> 120 us, 32768 x 5120 173 -> 165, 16384 x
+    // 8192 167 -> 128; 8192 x 16384 without one 202 -> 158; but fp32 16384 x 6144 without one
+    // 175 -> 190), and the sums of dy as well (norm_bwd_db_shared)
     constexpr bool DB_SHARED = norm_bwd_db_shared<T, NV, MAXT, CK, LOOSE>();
     constexpr bool W_SHARED = !WARP && (CK || MAXT == 320 || (WIDE && sizeof(T) == 2));
     __shared__ ulonglong2 w_shared[W_SHARED ? NV * P / 2 : 1][W_SHARED ? MAXT : 1];

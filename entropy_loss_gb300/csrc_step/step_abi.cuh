@@ -99,12 +99,12 @@ flp_status resident_blocks(int threads, size_t smem, size_t largest, int* per_sm
 // 17 to 130 %.  Rows of up to 512 elements go to one warp, which needs no block
 // barrier; rows above 8192 take more elements a thread.  Two blocks of up to TWO
 // threads must fit an SM, which bounds the registers (three of up to 256: forward
-// with a checkpoint 119 against 107 us, backward 185 against 138 us).  For the bf16
+// with a checkpoint 118 against 105 us, backward 239 against 127 us).  For the bf16
 // forward that pays up to 512 threads, although the loose form of 512 spills: two
-// blocks of 384 threads instead of one take 16384 x 6144 from 82 to 64 us, with a
-// checkpoint from 104 to 83 us (fp32 from 125 to 136; loose rows with a checkpoint,
-// 20000 x 6001, from 204 to 233), two of 512 take 16384 x 8192 from 96 to 83 us (with
-// a checkpoint from 131 to 153).  The stages put 32 to 64 KiB per SM in flight.
+// blocks of 384 threads instead of one take 16384 x 6144 from 79 to 64 us, with a
+// checkpoint from 94 to 82 us (fp32 from 124 to 134; loose rows with a checkpoint,
+// 20000 x 6001, from 204 to 233), two of 512 take 16384 x 8192 from 95 to 83 us (with
+// a checkpoint from 112 to 153).  The stages put 32 to 64 KiB per SM in flight.
 template <int NV_, int S_, bool WARP_, int MAXT_, int MINB_>
 struct StreamShape {
     static constexpr int NV = NV_, S = S_, MAXT = MAXT_, MINB = MINB_;

@@ -17,10 +17,11 @@
 // partial tiles, which a small kernel joins in a fixed order (no atomics).
 //
 // Bound by the tensor cores: 8192 x 8192 x 5120 (dY rows, dW rows, dW columns) with an
-// fp32 dW takes 424 us, 1620 TFLOP/s or 86 % of the measured matrix rate: 392 us in this
-// kernel (the tensor pipe busy 75 % of it; the rest is draining the accumulators between
-// the four runs of each tile), 21 us unpacking and 11 us in the join.  A bf16 dW, which
-// needs no runs, takes 361 us in all.
+// fp32 dW takes 410 us, 1680 TFLOP/s or 89 % of the measured matrix rate: 380 us in this
+// kernel (the tensor pipe busy 77 % of it; the rest is draining the accumulators between
+// the four runs of each tile), 20 us unpacking and 11 us in the join.  A bf16 dW, which
+// needs no runs, takes 357 us in all.  (A loop of a second or more meets the power cap:
+// 450 us at 1885 MHz.)
 #pragma once
 #include "../csrc/kernels.cuh"
 #include "vec.cuh"
@@ -57,10 +58,11 @@ struct WgradUnit {
 // over 2048 (values with an offset of half their spread: twice that; a product of
 // the same values in fp32 arithmetic 1e-7 to 5e-7).  An fp32 result is
 // therefore summed in runs of at most 2048 rows, whose sums are added in memory,
-// rounded to nearest.  Draining the accumulators between runs costs about 6 us a
-// tile when every column goes through memory (8192 x 8192 x 5120 takes 455 us, in
-// one run 377 us); WGRAD_KEEP of a half's 256 columns are therefore summed in the
-// epilogue's registers (424 us; 64: 436, 32: 449; 128 would spill more).  A bf16
+// rounded to nearest (of 4096: 8192 x 8192 x 5120 takes 380 us instead of 410, in one
+// run 366, at errors of 1.2e-6 and 3.0e-6).  Draining the accumulators between runs
+// costs most when every column goes through memory, so WGRAD_KEEP of a half's 256
+// columns are summed in the epilogue's registers (96: 410 us, 64: 420, 32: 432; 128
+// spills 148 bytes: 418).  A bf16
 // result's own rounding (1.7e-3) leaves nothing of the error of up to 131072 rows (1e-4):
 // one run, stored directly.  Above that the error also has a direction (every value
 // 1e-3 too small over 1048576 rows), so the result is joined from fp32 sums of runs.
