@@ -197,12 +197,12 @@ template <typename T, bool CK, bool LOOSE, typename F>
 flp_status norm_bwd_form(int64_t H, F&& f) {
     return norm_stream_shape<T, 320, 4>(H, [&](auto shape, int threads) -> flp_status {
         using X = decltype(shape);
-        // above 8192 columns one stage fits beside the weights and sums; two of aligned
-        // bf16 rows with a checkpoint (8192 x 8200 119 us, one stage: 133)
-        // and two of bf16 where the sums of dy wait there too (norm_bwd_db_shared)
-        constexpr bool WIDE = norm_bwd_wide<T, X::NV>();
-        constexpr bool TWO = sizeof(T) == 2 && norm_bwd_db_shared<T, X::NV, X::MAXT, CK, LOOSE>();
-        constexpr int S = WIDE && !(CK && !LOOSE && sizeof(T) == 2) ? 1 : TWO ? 2 : X::S;
+        // above 8192 columns one stage fits beside the weights and sums, or two of aligned
+        // bf16 rows with a checkpoint (8192 x 8200 118 us, one stage: 133); two of bf16
+        // also where the sums of dy wait there in narrower rows (norm_bwd_db_shared)
+        constexpr bool WIDE = norm_bwd_wide<T, X::NV>(), B16 = sizeof(T) == 2;
+        constexpr bool DB_SHARED = norm_bwd_db_shared<T, X::NV, X::MAXT, CK, LOOSE>();
+        constexpr int S = WIDE && !(CK && !LOOSE && B16) ? 1 : B16 && DB_SHARED ? 2 : X::S;
         constexpr auto* kernel = flp_norm_bwd_stream_kernel<T, X::NV, S, CK, LOOSE, X::WARP, X::MAXT, X::MINB>;
         // a cluster's block holds its warps' sums (a row per warp) and its own after the rows
         constexpr size_t kJoin = X::WARP ? static_cast<size_t>(X::MAXT) * X::NV * wide_v<T>() * 4 : 0;
