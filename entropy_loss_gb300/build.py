@@ -1,9 +1,9 @@
 """Builds the CUDA library ``libflp.so`` in-tree with nvcc for sm_103a.
 
-The library is one translation unit (``csrc_step/libflp.cu``: the fused head in
-``csrc/`` and the training-step operators in ``csrc_step/``) that holds the C
-ABI of ``include/flp.h`` and the kernels.  Rebuilt when any source, or this
-file, is newer than the shared object.
+The library holds the C ABI of ``include/flp.h`` and the kernels: the fused head
+in ``csrc/`` and the operators beside it in ``csrc_step/``.  Their ``.cu`` files
+are the translation units, compiled at the same time.  Rebuilt when any source,
+or this file, is newer than the shared object.
 """
 from __future__ import annotations
 
@@ -36,8 +36,9 @@ def nvcc_path() -> str:
 
 
 def command(out: str, extra: list[str] | None = None) -> list[str]:
-    return [nvcc_path(), *FLAGS, "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"),
-            "-o", out, os.path.join(PKG, "csrc_step", "libflp.cu")] + (extra or [])
+    units = [s for s in sources() if s.endswith(".cu")]
+    return [nvcc_path(), *FLAGS, f"--threads={len(units)}", "-Xcompiler", "-fPIC", "-shared",
+            "-I" + os.path.join(ROOT, "include"), "-o", out, *units] + (extra or [])
 
 
 def stale() -> bool:

@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
+#include "../csrc/ptx.cuh"
 
 namespace flp {
 

@@ -23,7 +23,7 @@
 // needs no runs, takes 357 us in all.  (A loop of a second or more meets the power cap:
 // 450 us at 1885 MHz.)
 #pragma once
-#include "../csrc/kernels.cuh"
+#include "../csrc/pair.cuh"
 #include "vec.cuh"
 
 namespace flp {
