@@ -34,7 +34,8 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_selftest_dz_wait_timeout", "flp_policy_loss", "flp_layer_norm", "flp_layer_norm_workspace",
            "flp_layer_norm_backward", "flp_checkpoint_pack", "flp_checkpoint_unpack",
            "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad", "flp_selftest_weight_grad_timeout",
-           "flp_balance_loss_workspace", "flp_balance_loss", "flp_balance_loss_ex")
+           "flp_balance_loss_workspace", "flp_balance_loss", "flp_balance_loss_ex", "flp_expert_sort_workspace",
+           "flp_expert_sort", "flp_expert_gather", "flp_expert_combine", "flp_expert_combine_backward")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
 FLP_LOSS_NLL_SUM = 3
@@ -126,7 +127,12 @@ def load(path: str = LIB_PATH):
             ("flp_selftest_weight_grad_timeout", [p, ctypes.c_size_t, i32, i32, i64, p]),
             ("flp_balance_loss_workspace", [i64, i64, size]),
             ("flp_balance_loss", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, p, p, ctypes.c_size_t, p]),
-            ("flp_balance_loss_ex", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, i32, p, p, ctypes.c_size_t, p])):
+            ("flp_balance_loss_ex", [p, i64, i32, p, p, i64, i64, i64, f32, p, p, i32, p, p, ctypes.c_size_t, p]),
+            ("flp_expert_sort_workspace", [i64, i64, i64, size]),
+            ("flp_expert_sort", [p, i64, i64, i64, p, p, p, p, p, ctypes.c_size_t, p]),
+            ("flp_expert_gather", [p, i64, i32, i64, i64, i64, p, p, p, i64, p]),
+            ("flp_expert_combine", [p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p]),
+            ("flp_expert_combine_backward", [p, i64, p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p, p])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32
     lib.flp_get_error.argtypes = [p, p]
@@ -729,6 +735,150 @@ def balance_loss(logits, top_k: int, *, experts=None, mask=None, coef: float = 1
     return loss_out, g, counts
 
 
+class ExpertOrder(NamedTuple):
+    """Slots sorted by expert: rows int32 [T, k] (the position of each slot), slots
+    int32 [T k] (the slot at each position), counts int64 [E] and offsets int64
+    [E + 1].  Slots without an expert come last, from offsets[E] on."""
+    rows: torch.Tensor
+    slots: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+
+
+def expert_sort(experts, num_experts: int, *, workspace=None, stream=None) -> ExpertOrder:
+    """The slots of experts [T, k] (int64; values outside [0, num_experts) are
+    dropped slots) in the order of their experts, equal ones in their own order."""
+    if stream is not None:
+        return _on_stream(stream, expert_sort, experts, num_experts, workspace=workspace)
+    if experts.dim() != 2:
+        raise ValueError(f"experts: expected int64 [T, k], got shape {tuple(experts.shape)}")
+    T, k = experts.shape
+    _need(experts, torch.int64, (T, k), "experts")
+    dev = experts.device
+    rows = torch.empty((T, k), dtype=torch.int32, device=dev)
+    slots = torch.empty(T * k, dtype=torch.int32, device=dev)
+    counts = torch.empty(num_experts, dtype=torch.int64, device=dev)
+    offsets = torch.empty(num_experts + 1, dtype=torch.int64, device=dev)
+    device = dev.index
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+                                   _workspace_bytes("flp_expert_sort_workspace", device, T, k, num_experts))
+    status = load().flp_expert_sort(experts.data_ptr(), T, k, num_experts, rows.data_ptr(), slots.data_ptr(),
+                                    counts.data_ptr(), offsets.data_ptr(), ws, ws_bytes, _raw_stream(device))
+    if status:
+        _check(status, "flp_expert_sort")
+    return ExpertOrder(rows, slots, counts, offsets)
+
+
+def _expert_order(order, dev):
+    """(T, k, address of rows, address of the number of kept slots) of an ExpertOrder on `dev`."""
+    rows, offsets = order.rows, order.offsets
+    if (rows.dtype is not torch.int32 or rows.dim() != 2 or not rows.is_contiguous() or rows.device != dev
+            or offsets.dtype is not torch.int64 or offsets.dim() != 1 or len(offsets) < 1 or not offsets.is_contiguous()
+            or offsets.device != dev):
+        raise ValueError(f"order: not the order of slots on {dev}: rows {rows.dtype} {tuple(rows.shape)} on {rows.device}, "
+                         f"offsets {offsets.dtype} {tuple(offsets.shape)} on {offsets.device}")
+    T, k = rows.shape
+    return T, k, rows.data_ptr(), offsets.data_ptr() + 8 * (len(offsets) - 1)
+
+
+def _expert_weights(weights, T, k, dev):
+    if weights is None:
+        return None, FLP_F32
+    code = _dtype(weights, "weights")
+    if weights.shape != (T, k) or weights.device != dev or not weights.is_contiguous():
+        raise ValueError(f"weights: expected contiguous bf16 or fp32 of shape {(T, k)} on {dev}, got {tuple(weights.shape)} "
+                         f"on {weights.device}")
+    return weights.data_ptr(), code
+
+
+def _on(t, dev, name):
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got one on {t.device}")
+
+
+def expert_gather(x, order: ExpertOrder, *, out=None, stream=None):
+    """The rows of x [T, H] (bf16 or fp32) in the experts' order, [T k, H]: row p is
+    that of slot p's token, zeros for the slots without an expert."""
+    if stream is not None:
+        return _on_stream(stream, expert_gather, x, order, out=out)
+    xp, ldx = _rows(x, "x")
+    dev, dt = x.device, x.dtype
+    T, k, rows, total = _expert_order(order, dev)
+    H = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, the order {T} tokens")
+    code = _dtype(x, "x")
+    if out is None:
+        out = torch.empty((T * k, H), dtype=dt, device=dev)
+        op, ldo = out.data_ptr(), H
+    else:
+        op, ldo = _rows(out, "out", (T * k, H), dt)
+        _on(out, dev, "out")
+    status = load().flp_expert_gather(xp, ldx, code, T, H, k, rows, total, op, ldo, _raw_stream(dev.index))
+    if status:
+        _check(status, "flp_expert_gather")
+    return out
+
+
+def expert_combine(ys, order: ExpertOrder, weights=None, *, out=None, stream=None):
+    """The tokens' rows [T, H] from those in the experts' order: the sum of each
+    token's rows of ys [T k, H] times weights [T, k] (bf16 or fp32; None: 1), slots
+    without an expert left out.  Without weights it is the gradient of expert_gather."""
+    if stream is not None:
+        return _on_stream(stream, expert_combine, ys, order, weights, out=out)
+    yp, ldy = _rows(ys, "ys")
+    dev, dt = ys.device, ys.dtype
+    T, k, rows, total = _expert_order(order, dev)
+    H = ys.shape[1]
+    if ys.shape[0] != T * k:
+        raise ValueError(f"ys has {ys.shape[0]} rows, the order {T * k} slots")
+    code = _dtype(ys, "ys")
+    wp, wt = _expert_weights(weights, T, k, dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=dt, device=dev)
+        op, ldo = out.data_ptr(), H
+    else:
+        op, ldo = _rows(out, "out", (T, H), dt)
+        _on(out, dev, "out")
+    status = load().flp_expert_combine(yp, ldy, code, wp, wt, T, H, k, rows, total, op, ldo, _raw_stream(dev.index))
+    if status:
+        _check(status, "flp_expert_combine")
+    return out
+
+
+def expert_combine_backward(dy, ys, order: ExpertOrder, weights=None, *, out=None, want_dweights: bool = True, stream=None):
+    """(dys, dweights) of expert_combine: dys [T k, H] in dy's type, dweights fp32
+    [T, k], or None where they are not wanted (ys is then not read and may be None)."""
+    if stream is not None:
+        return _on_stream(stream, expert_combine_backward, dy, ys, order, weights, out=out, want_dweights=want_dweights)
+    dyp, lddy = _rows(dy, "dy")
+    dev, dt = dy.device, dy.dtype
+    T, k, rows, total = _expert_order(order, dev)
+    H = dy.shape[1]
+    if dy.shape[0] != T:
+        raise ValueError(f"dy has {dy.shape[0]} rows, the order {T} tokens")
+    code = _dtype(dy, "dy")
+    wp, wt = _expert_weights(weights, T, k, dev)
+    yp, ldy, dweights = None, 0, None
+    if want_dweights:
+        if ys is None:
+            raise ValueError("the gradient of the weights needs ys")
+        yp, ldy = _rows(ys, "ys", (T * k, H), dt)
+        _on(ys, dev, "ys")
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    if out is None:
+        out = torch.empty((T * k, H), dtype=dt, device=dev)
+        op, ldo = out.data_ptr(), H
+    else:
+        op, ldo = _rows(out, "out", (T * k, H), dt)
+        _on(out, dev, "out")
+    status = load().flp_expert_combine_backward(dyp, lddy, yp, ldy, code, wp, wt, T, H, k, rows, total, op, ldo,
+                                                dweights.data_ptr() if want_dweights else None, _raw_stream(dev.index))
+    if status:
+        _check(status, "flp_expert_combine_backward")
+    return out, dweights
+
+
 def get_error(workspace, stream=None) -> int:
     """Synchronise the stream and return the workspace's error status code."""
     return int(load().flp_get_error(_ptr(workspace), _stream(stream)))
@@ -880,3 +1030,44 @@ def fused_balance_loss(logits, top_k: int, experts=None, mask=None, coef: float 
         loss_out, _, counts = balance_loss(logits, top_k, experts=experts, mask=mask, coef=coef, grad=False)
         return loss_out[0], counts
     return FusedBalanceLoss.apply(logits, top_k, experts, mask, coef)
+
+
+class FusedExpertGather(torch.autograd.Function):
+    """autograd wrapper of expert_gather."""
+
+    @staticmethod
+    def forward(ctx, x, order):
+        ctx.order = order
+        return expert_gather(x, order)
+
+    @staticmethod
+    def backward(ctx, dxs):
+        return _once(lambda: expert_combine(dxs.contiguous(), ctx.order), dxs), None
+
+
+def fused_expert_gather(x, order: ExpertOrder):
+    """Differentiable rows of x [T, H] in the experts' order, [T k, H]."""
+    return FusedExpertGather.apply(x, order)
+
+
+class FusedExpertCombine(torch.autograd.Function):
+    """autograd wrapper of expert_combine."""
+
+    @staticmethod
+    def forward(ctx, ys, weights, order):
+        ctx.order = order
+        ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights)
+        return expert_combine(ys, order, weights)
+
+    @staticmethod
+    def backward(ctx, dy):
+        ys, weights = ctx.saved_tensors
+        want = ctx.needs_input_grad[1]
+        dys, dw = _once(lambda: expert_combine_backward(dy.contiguous(), ys, ctx.order, weights, want_dweights=want),
+                        dy, ys, weights)
+        return dys, dw.to(weights.dtype) if want else None, None
+
+
+def fused_expert_combine(ys, order: ExpertOrder, weights=None):
+    """Differentiable sum of each token's rows of ys [T k, H] times weights [T, k]: [T, H]."""
+    return FusedExpertCombine.apply(ys, weights, order)

@@ -535,6 +535,47 @@ flp_status flp_balance_loss_ex(const void* logits, int64_t ld, int dtype, const 
                                float* loss, void* grad, int grad_dtype, int64_t* counts, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/*
+ * Tokens sorted by expert.  T tokens choose k experts each; slot t k + j is
+ * token t's j-th choice.  experts: int64 [T, k], values outside [0, E) are
+ * dropped slots (1 <= E <= 1024, T k < 2^31).  A stable counting sort, dropped
+ * slots last:
+ *   rows    int32 [T, k]  the position of every slot
+ *   slots   int32 [T k]   the slot at every position
+ *   counts  int64 [E]     slots of each expert
+ *   offsets int64 [E + 1] where each expert's positions begin; offsets[E] is the
+ *                         number of slots that were not dropped
+ * The same expert may be chosen more than once by a token.  Few slots need no
+ * workspace (the query says 0).
+ */
+flp_status flp_expert_sort_workspace(int64_t T, int64_t k, int64_t E, size_t* bytes);
+flp_status flp_expert_sort(const int64_t* experts, int64_t T, int64_t k, int64_t E, int32_t* rows, int32_t* slots,
+                           int64_t* counts, int64_t* offsets, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rows brought to the experts and back, by the sort's rows and its
+ * total = &offsets[E] (on the device):
+ *   gather             XS[rows[t, j]] = X[t]; positions from total on get zeros
+ *   combine            Y[t] = sum_j weights[t, j] YS[rows[t, j]] over the positions
+ *                      below total (fp32, in the order of j, rounded once; 0 if none)
+ *   combine backward   dYS[rows[t, j]] = weights[t, j] dY[t], zeros from total on
+ *                      dweights[t, j] = <dY[t], YS[rows[t, j]]>, 0 for dropped slots
+ * X, Y, dY: [T, H]; XS, YS, dYS: [T k, H], bf16 or fp32 (dtype).  What rows of
+ * YS from total on hold is not looked at.  weights: [T, k] in weight_dtype, or
+ * NULL: 1 (combine without weights is the gradient of gather).  dweights: fp32,
+ * or NULL (YS is then not read and may be NULL).  An entry of rows that is no
+ * position is passed over.  Inputs and outputs must not overlap.
+ */
+flp_status flp_expert_gather(const void* X, int64_t ldx, int dtype, int64_t T, int64_t H, int64_t k,
+                             const int32_t* rows, const int64_t* total, void* XS, int64_t ldxs, void* stream);
+flp_status flp_expert_combine(const void* YS, int64_t ldys, int dtype, const void* weights, int weight_dtype,
+                              int64_t T, int64_t H, int64_t k, const int32_t* rows, const int64_t* total, void* Y,
+                              int64_t ldy, void* stream);
+flp_status flp_expert_combine_backward(const void* dY, int64_t lddy, const void* YS, int64_t ldys, int dtype,
+                                       const void* weights, int weight_dtype, int64_t T, int64_t H, int64_t k,
+                                       const int32_t* rows, const int64_t* total, void* dYS, int64_t lddys,
+                                       float* dweights, void* stream);
+
 /* Static description of a status code. */
 const char* flp_status_string(flp_status status);
 

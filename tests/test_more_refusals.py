@@ -1,0 +1,87 @@
+"""Refusals of the expert, linear and given-logits entry points, on the CPU: argument
+errors are returned before a device is touched."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def flp():
+    from entropy_loss_gb300 import build, flp as _flp
+    build.build()
+    _flp.load()
+    return _flp
+
+
+@pytest.fixture(scope="module")
+def b():
+    buf = ctypes.create_string_buffer(8192 + 16)
+    yield (ctypes.addressof(buf) + 15) // 16 * 16
+
+
+def test_expert_sort(flp, b):
+    def call(**o):
+        a = dict(e=b, T=4, k=2, E=8, rows=b, slots=b, counts=b, offsets=b, ws=b, n=8192)
+        a.update(o)
+        return flp.load().flp_expert_sort(a["e"], a["T"], a["k"], a["E"], a["rows"], a["slots"], a["counts"], a["offsets"],
+                                          a["ws"], a["n"], None)
+
+    for o in (dict(T=-1), dict(k=0), dict(E=0), dict(e=None), dict(rows=None), dict(slots=None), dict(counts=None),
+              dict(offsets=None), dict(e=b + 4), dict(rows=b + 2), dict(slots=b + 1), dict(counts=b + 4), dict(offsets=b + 4)):
+        assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
+    for o in (dict(E=1025), dict(T=2 ** 31), dict(T=2 ** 30, k=2), dict(T=2 ** 40, k=2 ** 40)):
+        assert call(**o) == flp.FLP_ERR_UNSUPPORTED, o
+    for o in (dict(T=5000, ws=None), dict(T=5000, n=4096), dict(T=5000, ws=b + 4)):
+        assert call(**o) == flp.FLP_ERR_WORKSPACE, o
+    need = ctypes.c_size_t(7)
+    query = flp.load().flp_expert_sort_workspace
+    assert query(100, 2, 8, ctypes.byref(need)) == flp.FLP_OK and need.value == 0
+    assert query(5000, 2, 8, ctypes.byref(need)) == flp.FLP_OK and need.value > 0
+    assert query(5000, 2, 8, None) == flp.FLP_ERR_INVALID_ARG
+    assert query(5000, 2, 1025, ctypes.byref(need)) == flp.FLP_ERR_UNSUPPORTED
+
+
+def test_expert_rows(flp, b):
+    lib = flp.load()
+
+    def gather(**o):
+        a = dict(x=b, ldx=64, dt=1, T=4, H=64, k=2, rows=b, total=b, xs=b, ldxs=64, w=None, wt=0)
+        a.update(o)
+        return lib.flp_expert_gather(a["x"], a["ldx"], a["dt"], a["T"], a["H"], a["k"], a["rows"], a["total"], a["xs"], a["ldxs"],
+                                     None)
+
+    def combine(**o):
+        a = dict(x=b, ldx=64, dt=1, T=4, H=64, k=2, rows=b, total=b, xs=b, ldxs=64, w=b, wt=0)
+        a.update(o)
+        return lib.flp_expert_combine(a["xs"], a["ldxs"], a["dt"], a["w"], a["wt"], a["T"], a["H"], a["k"], a["rows"], a["total"],
+                                      a["x"], a["ldx"], None)
+
+    def backward(**o):
+        a = dict(x=b, ldx=64, dt=1, T=4, H=64, k=2, rows=b, total=b, xs=b, ldxs=64, w=b, wt=0, dys=b, lddys=64, dw=b)
+        a.update(o)
+        return lib.flp_expert_combine_backward(a["x"], a["ldx"], a["xs"], a["ldxs"], a["dt"], a["w"], a["wt"], a["T"], a["H"],
+                                               a["k"], a["rows"], a["total"], a["dys"], a["lddys"], a["dw"], None)
+
+    for f in (gather, combine, backward):
+        for o in (dict(T=-1), dict(H=0), dict(k=0), dict(dt=2), dict(x=None), dict(xs=None), dict(rows=None), dict(total=None),
+                  dict(rows=b + 2), dict(total=b + 4), dict(ldx=63), dict(ldxs=63), dict(x=b + 1), dict(xs=b + 1)):
+            assert f(**o) == flp.FLP_ERR_INVALID_ARG, (f, o)
+        assert f(T=2 ** 30, k=2) == flp.FLP_ERR_UNSUPPORTED
+        assert f(T=0, x=None, xs=None, rows=None, total=None) == flp.FLP_OK
+    for f in (combine, backward):
+        for o in (dict(wt=2), dict(w=b + 2), dict(w=b + 1, wt=1)):
+            assert f(**o) == flp.FLP_ERR_INVALID_ARG, (f, o)
+    for o in (dict(dys=None), dict(lddys=1), dict(dys=b + 1), dict(dw=b + 2)):
+        assert backward(**o) == flp.FLP_ERR_INVALID_ARG, o
+
+
+def test_binding_refuses_before_loading_anything_on_a_device(flp):
+    import torch
+    x = torch.zeros(4, 64)
+    order = flp.ExpertOrder(torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int64),
+                            torch.zeros(3, dtype=torch.int64))
+    for f in (lambda: flp.expert_sort(torch.zeros(4, 2, dtype=torch.int64), 2), lambda: flp.expert_sort(torch.zeros(4), 2),
+              lambda: flp.expert_gather(x, order), lambda: flp.expert_combine(x, order),
+              lambda: flp.expert_combine_backward(x, x, order)):
+        with pytest.raises(ValueError):
+            f()
