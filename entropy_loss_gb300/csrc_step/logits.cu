@@ -1,0 +1,134 @@
+// logits.cu - host side of the given-logits operators declared in include/flp.h.
+#include "logits.cuh"
+#include "step_host.cuh"
+
+namespace {
+
+flp_status tlp_checks(const void* logits, int64_t ld, int dtype, const int64_t* targets, int64_t M, int64_t V, float scale) {
+    if (M < 0 || V < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0 and V >= 1 required");
+    if (!is_dtype(dtype)) return fail(FLP_ERR_INVALID_ARG, "dtype is FLP_F32 or FLP_BF16");
+    if (!(scale > 0.f) || !std::isfinite(scale * LOG2E))
+        return fail(FLP_ERR_INVALID_ARG, "scale must be positive and finite");
+    if (V > INT32_MAX - 65536) return fail(FLP_ERR_UNSUPPORTED, "rows of more than 2^31 elements");
+    if (M > kMaxRows / TLP_CLUSTER) return fail(FLP_ERR_UNSUPPORTED, "too many rows for one launch");
+    if (M == 0) return FLP_OK;
+    if (!targets || !aligned_to(targets, 8)) return fail(FLP_ERR_INVALID_ARG, "targets must be non-null and aligned");
+    return row_checks(logits, ld, V, dtype, "logits must be non-null");
+}
+
+// Blocks of a row: as many as finish the rows soonest, in vectors that a resident block
+// reads (two blocks of 512 threads an SM), each block costing as much as 1024 vectors.
+int tlp_cluster(int64_t M, int64_t vecs, int sm_count) {
+    int best = 1;
+    double least = 1e300;
+    for (int c = 1; c <= TLP_CLUSTER; c *= 2) {
+        const double cost = static_cast<double>(cdiv(M * c, 2 * sm_count)) * (static_cast<double>(vecs) / c + 1024);
+        if (cost < least) least = cost, best = c;
+    }
+    return best;
+}
+
+template <typename T, bool LOOSE>
+flp_status tlp_launch(TlpParams& p, int sm_count, cudaStream_t s) {
+    const int64_t vecs = cdiv(p.V, wide_v<T>());
+    const bool small = vecs <= 512;  // a block of 128 threads reads the row at once
+    p.cluster = small ? 1 : tlp_cluster(p.M, vecs, sm_count);
+    p.per = static_cast<int>(cdiv(cdiv(vecs, p.cluster), 32) * 32);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.M * p.cluster));
+    cfg.blockDim = dim3(small ? 128 : 512);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    const cudaError_t e = small ? cudaLaunchKernelEx(&cfg, flp_token_logprob_kernel<T, LOOSE, 128>, p)
+                                : cudaLaunchKernelEx(&cfg, flp_token_logprob_kernel<T, LOOSE, 512>, p);
+    return e == cudaSuccess ? FLP_OK : cuda_fail(e, "flp_token_logprob_kernel launch");
+}
+
+}  // namespace
+
+extern "C" flp_status flp_token_logprob(const void* logits, int64_t ld, int dtype, const int64_t* targets, int64_t M,
+                                        int64_t V, int64_t ignore_index, float scale, float* logprob, float* lse,
+                                        float* entropy, int64_t top, float* top_logprob, int64_t* top_index, void* stream) {
+    flp_status st = tlp_checks(logits, ld, dtype, targets, M, V, scale);
+    if (st != FLP_OK) return st;
+    if (top < 0 || top > V) return fail(FLP_ERR_INVALID_ARG, "0 <= top <= V required");
+    if (top > TLP_MAX_TOP) return fail(FLP_ERR_UNSUPPORTED, "at most 32 alternatives");
+    if (M == 0) return FLP_OK;
+    if (!logprob || !lse || (top > 0 && (!top_logprob || !top_index)))
+        return fail(FLP_ERR_INVALID_ARG, "logprob, lse and the alternatives' outputs must be non-null");
+    if (!aligned_to(logprob, 4) || !aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(top_logprob, 4) ||
+        !aligned_to(top_index, 8))
+        return fail(FLP_ERR_INVALID_ARG, "outputs must be aligned to their elements");
+    DevInfo* d;
+    if ((st = step_device(&d)) != FLP_OK) return st;
+    if ((st = check_on_current_device(logits, "logits")) != FLP_OK) return st;
+    TlpParams p{};
+    p.x = logits;
+    p.ld = ld;
+    p.y = reinterpret_cast<const long long*>(targets);
+    p.M = M;
+    p.V = static_cast<int>(V);
+    p.top = static_cast<int>(top);
+    p.ignore_index = ignore_index;
+    p.scale = scale;
+    p.c = scale * LOG2E;
+    p.logprob = logprob;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.top_value = top_logprob;
+    p.top_index = reinterpret_cast<long long*>(top_index);
+    const bool loose = !(rows16(logits, ld, dtype) && (V * elem(dtype)) % 16 == 0);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto typed = [&](auto t) {
+        return loose ? tlp_launch<decltype(t), true>(p, d->sm_count, s) : tlp_launch<decltype(t), false>(p, d->sm_count, s);
+    };
+    return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
+}
+
+extern "C" flp_status flp_token_logprob_backward(const void* logits, int64_t ld, int dtype, const int64_t* targets,
+                                                 int64_t M, int64_t V, int64_t ignore_index, float scale, const float* lse,
+                                                 const float* entropy, const float* grad_logprob, const float* grad_entropy,
+                                                 void* dlogits, int64_t lddl, void* stream) {
+    flp_status st = tlp_checks(logits, ld, dtype, targets, M, V, scale);
+    if (st != FLP_OK || M == 0) return st;
+    if (!lse) return fail(FLP_ERR_INVALID_ARG, "lse must be non-null");
+    if (grad_entropy && !entropy) return fail(FLP_ERR_INVALID_ARG, "the gradient of the entropy needs the entropy");
+    if (!aligned_to(lse, 4) || !aligned_to(entropy, 4) || !aligned_to(grad_logprob, 4) || !aligned_to(grad_entropy, 4))
+        return fail(FLP_ERR_INVALID_ARG, "row values must be aligned to their elements");
+    if ((st = row_checks(dlogits, lddl, V, dtype, "dlogits must be non-null")) != FLP_OK) return st;
+    DevInfo* d;
+    if ((st = step_device(&d)) != FLP_OK) return st;
+    if ((st = check_on_current_device(logits, "logits")) != FLP_OK) return st;
+    TlpBwdParams p{};
+    p.x = logits;
+    p.ld = ld;
+    p.y = reinterpret_cast<const long long*>(targets);
+    p.M = M;
+    p.V = static_cast<int>(V);
+    p.ignore_index = ignore_index;
+    p.scale = scale;
+    p.lse = lse;
+    p.entropy = entropy;
+    p.g_lp = grad_logprob;
+    p.g_ent = grad_entropy;
+    p.dx = dlogits;
+    p.lddx = lddl;
+    const bool vec = rows16(logits, ld, dtype) && rows16(dlogits, lddl, dtype) && (V * elem(dtype)) % 16 == 0;
+    p.chunks = static_cast<int>(cdiv(V, TLPB_NV * 32 * (16 / elem(dtype))));
+    const int64_t grid = cdiv(M * p.chunks, TLPB_THREADS / 32);
+    if (grid * (TLPB_THREADS / 32) > INT32_MAX) return fail(FLP_ERR_UNSUPPORTED, "matrix too large for one launch");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto* kernel) {
+        return launch_step(kernel, grid, TLPB_THREADS, 0, s, "flp_token_logprob_bwd_kernel launch", false, p);
+    };
+    auto typed = [&](auto t) {
+        return vec ? go(flp_token_logprob_bwd_kernel<decltype(t), false>) : go(flp_token_logprob_bwd_kernel<decltype(t), true>);
+    };
+    return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
+}

@@ -1,0 +1,503 @@
+// logits.cuh - log-probabilities of given tokens from logits that are in memory, with
+// the entropy and the top alternatives, and the gradient by the logits.
+//
+// With z = s x for a row x of logits (s > 0), M = max x and c = s log2 e:
+//     S = sum_j 2^((x_j - M) c),   A = sum_j 2^((x_j - M) c) (x_j - M) c
+//     lse = s M + ln S,   logprob = s (x_y - M) - ln S,   entropy = ln S - ln 2 A / S
+// (lse and z_y, both large, are not subtracted: the log-probability keeps its digits).
+// One pass: a thread holds (M, S, A) of what it has read and rescales S and A when its
+// maximum grows; threads, warps and the blocks of a row (a cluster, joined through
+// distributed shared memory) are merged at the end.
+//
+// The alternatives come out of the same pass.  A thread's maximum is an element of the
+// row, so the k-th largest of 32 maxima over disjoint parts of it is a bound that at
+// least k elements reach; elements below it cannot be among the k largest.  With the
+// parts interleaved that bound lets through little more than k elements of what was read
+// so far, and it is taken again whenever the amount read has doubled.  What passes goes
+// to a list in shared memory, in whatever order, and is ranked at the end by value and
+// column, so that equal logits come out in the order of their columns.  A list that
+// overflows (many equal logits) is dropped, and the block reads its part again,
+// taking the largest left of each chunk in turn.
+#pragma once
+#include "vec.cuh"
+
+namespace flp {
+
+constexpr int TLP_MAX_TOP = 32;
+constexpr int TLP_LIST = 1024;     // candidates a block can hold
+constexpr int TLP_CLUSTER = 8;     // blocks of a row at most
+
+struct TlpParams {
+    const void* x;
+    long long ld;
+    const long long* y;
+    long long M;
+    int V;
+    int per;      // vectors of a row that one block of its cluster reads, a multiple of 32
+    int cluster;  // blocks of a row
+    int top;
+    long long ignore_index;
+    float scale, c;  // s, s log2 e
+    float* logprob;
+    float* lse;
+    float* entropy;    // or null
+    float* top_value;  // [M, top]
+    long long* top_index;
+};
+
+struct TlpStats {
+    float m, s, a;
+};
+
+__device__ __forceinline__ TlpStats tlp_merge(TlpStats u, TlpStats v, float c) {
+    const float m = fmaxf(u.m, v.m);
+    // a part that holds nothing above -inf brings nothing (or the NaN that it met)
+    const float du = u.m == -INFINITY ? 0.f : (u.m - m) * c, dv = v.m == -INFINITY ? 0.f : (v.m - m) * c;
+    const float fu = ex2_approx(du), fv = ex2_approx(dv);
+    // a part so far below that its factor is 0 brings nothing, however large du is
+    TlpStats r;
+    r.m = m;
+    r.s = u.s * fu + v.s * fv;
+    r.a = (fu > 0.f ? fu * (u.a + du * u.s) : 0.f) + (fv > 0.f ? fv * (v.a + dv * v.s) : 0.f);
+    return r;
+}
+
+// A key orders by value, then by column, lower ones first; 0 is no key.
+__device__ __forceinline__ unsigned long long tlp_key(float x, int col) {
+    const uint32_t b = __float_as_uint(x + 0.f);  // -0 and 0 are equal
+    const uint32_t o = b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+    return static_cast<unsigned long long>(o) << 32 | (0xffffffffu - static_cast<uint32_t>(col));
+}
+__device__ __forceinline__ float tlp_key_value(unsigned long long key) {
+    const uint32_t o = static_cast<uint32_t>(key >> 32);
+    return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int tlp_key_col(unsigned long long key) {
+    return static_cast<int>(0xffffffffu - static_cast<uint32_t>(key));
+}
+
+// Element i of a vector's words.
+template <typename T>
+__device__ __forceinline__ float tlp_elem(const uint32_t* w, int i) {
+    if constexpr (sizeof(T) == 2)
+        return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else
+        return __uint_as_float(w[i]);
+}
+
+// The largest element of N words; NaN are passed over.
+template <typename T, int N>
+__device__ __forceinline__ float tlp_max(const uint32_t (&w)[N]) {
+    if constexpr (sizeof(T) == 2) {
+        __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        return fmaxf(__low2float(m), __high2float(m));
+    } else {
+        float m = __uint_as_float(w[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+        return m;
+    }
+}
+
+// NV vectors of a thread, THREADS apart: words in flight, then elements.
+template <typename T, bool LOOSE, int NV, int THREADS>
+struct TlpChunk {
+    static constexpr int V = wide_v<T>();
+    static constexpr int W = LOOSE ? WarpWords<T>::N : 4;
+    uint32_t r[NV][W];
+    __device__ __forceinline__ void load(const T* row, int v0, int end, bool edge, const Extent& all) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (v0 + i * THREADS) * V;
+            const T* src = row + col;
+            if constexpr (LOOSE) {
+                load_words<T>(r[i], src, end - col, edge, all);
+            } else {
+                const bool on = col < end;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+                    "mov.b32 %3, 0;\n\t@p ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                    : "=&r"(r[i][0]), "=&r"(r[i][1]), "=&r"(r[i][2]), "=&r"(r[i][3])
+                    : "l"(src), "r"(static_cast<int>(on)));
+            }
+        }
+    }
+    // the vectors as words, -inf in the places past `end`
+    __device__ __forceinline__ void settle(uint32_t (&w)[4 * NV], const T* row, int v0, int end, uint32_t stage) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (v0 + i * THREADS) * V, valid = end - col;
+            uint4 u;
+            if constexpr (LOOSE)
+                u = settle_words<T>(r[i], row + col, valid, stage);
+            else
+                u = make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            if (valid < V) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t& x = w[4 * i + q];
+                    if constexpr (sizeof(T) == 2)
+                        x = 2 * q + 1 < valid ? x : 2 * q < valid ? (x & 0xffffu) | 0xff800000u : 0xff80ff80u;
+                    else
+                        x = q < valid ? x : 0xff800000u;
+                }
+            }
+        }
+    }
+};
+
+template <int THREADS>
+struct TlpShared {
+    static constexpr int WARPS = THREADS / 32;
+    unsigned long long list[TLP_LIST];
+    unsigned long long best[TLP_MAX_TOP];   // this block's, in order; 0: none
+    unsigned long long warp_key[WARPS];
+    float part[2][WARPS][32];               // maxima of 32 parts by warp, two generations
+    TlpStats warp_stats[WARPS];
+    TlpStats stats;                         // this block's
+    int n;
+};
+
+// The k-th largest of the 32 lanes' values, equal ones counted by lane.
+__device__ __forceinline__ float tlp_kth(float g, int k) {
+    const int lane = threadIdx.x & 31;
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float o = __shfl_sync(0xffffffffu, g, j);
+        above += o > g || (o == g && j < lane) ? 1 : 0;
+    }
+    return __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == k - 1)) - 1);
+}
+
+// best[] from the n keys of the list: a key's place is how many are above it.
+template <int THREADS>
+__device__ __forceinline__ void tlp_rank(TlpShared<THREADS>& sh, int n, int k) {
+    if (threadIdx.x < TLP_MAX_TOP) sh.best[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+        const unsigned long long key = sh.list[i];
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) above += sh.list[j] > key ? 1 : 0;
+        if (above < k && key) sh.best[above] = key;
+    }
+    __syncthreads();
+}
+
+// The block's k largest, one after another, chunk by chunk (the list has overflowed).
+template <typename T, bool LOOSE, int NV, int THREADS>
+__device__ __noinline__ void tlp_again(TlpShared<THREADS>& sh, const T* row, int v0, int v1, int end, bool edge,
+                                       const Extent& all, uint32_t stage, int k) {
+    constexpr int V = wide_v<T>();
+    if (threadIdx.x < TLP_MAX_TOP) sh.best[threadIdx.x] = 0;
+    __syncthreads();
+    for (int v = v0; v < v1; v += THREADS * NV) {
+        TlpChunk<T, LOOSE, NV, THREADS> c;
+        uint32_t w[4 * NV];
+        const int mine = v + threadIdx.x;
+        c.load(row, mine, end, edge, all);
+        c.settle(w, row, mine, end, stage);
+        unsigned long long last = ~0ull;
+        for (int round = 0; round < k; ++round) {
+            unsigned long long top = sh.best[k - 1];  // none at or below it is wanted
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const float x = tlp_elem<T>(w + 4 * i, q);
+                    if (!(x > -INFINITY)) continue;
+                    const unsigned long long key = tlp_key(x, (mine + i * THREADS) * V + q);
+                    if (key < last && key > top) top = key;
+                }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const unsigned long long u = __shfl_xor_sync(0xffffffffu, top, o);
+                top = u > top ? u : top;
+            }
+            if ((threadIdx.x & 31) == 0) sh.warp_key[threadIdx.x >> 5] = top;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < THREADS / 32; ++i) top = sh.warp_key[i] > top ? sh.warp_key[i] : top;
+            const bool none = top == sh.best[k - 1];
+            __syncthreads();
+            if (none) break;
+            last = top;
+            if (threadIdx.x == 0) {
+                int at = k - 1;
+                for (; at > 0 && sh.best[at - 1] < top; --at) sh.best[at] = sh.best[at - 1];
+                sh.best[at] = top;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+__device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <typename T, bool LOOSE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_kernel(const TlpParams p) {
+    constexpr int V = wide_v<T>(), NV = LOOSE ? 2 : 4, P = Pairs<T>::N, WARPS = THREADS / 32;
+    __shared__ TlpShared<THREADS> sh;
+    __shared__ __align__(16) uint8_t words[LOOSE ? WARPS * WARP_WORDS_BYTES : 16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage = smem_addr(words) + (LOOSE ? warp * WARP_WORDS_BYTES : 0);
+    const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const long long at = blockIdx.x / p.cluster;
+    const T* row = static_cast<const T*>(p.x) + at * p.ld;
+    const bool edge = at == 0 || at == p.M - 1;
+    const Extent all = extent_of<T>(p.x, p.M, p.ld, p.V);
+    const int vecs = (p.V + V - 1) / V;
+    const int v0 = min(vecs, rank * p.per), v1 = min(vecs, v0 + p.per);
+    const int end = min(p.V, v1 * V);  // one past the last column of this block
+    if (threadIdx.x == 0) sh.n = 0;
+    long long y = 0;
+    float xy = 0.f;
+    if (rank == 0 && threadIdx.x == 0) {
+        y = p.y[at];
+        if (y >= 0 && y < p.V) xy = static_cast<float>(row[y]);
+    }
+    __syncthreads();
+
+    TlpStats st{-INFINITY, 0.f, 0.f};
+    float bound = -INFINITY;
+    TlpChunk<T, LOOSE, NV, THREADS> next;
+    next.load(row, v0 + threadIdx.x, end, edge, all);
+    int generation = 0;
+    unsigned chunk = 0;
+    for (int v = v0; v < v1; v += THREADS * NV, ++chunk) {
+        const int mine = v + threadIdx.x;
+        uint32_t w[4 * NV];
+        next.settle(w, row, mine, end, stage);
+        if (v + THREADS * NV < v1) next.load(row, mine + THREADS * NV, end, edge, all);
+        const float top = tlp_max<T>(w), m = fmaxf(st.m, top);
+        const float base = m == -INFINITY ? 0.f : m;  // nothing above -inf yet: every term is 0
+        const uint64_t minus = f2_splat(-base), c2 = f2_splat(p.c);
+        uint64_t s2 = 0, a2 = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint4 u = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const uint64_t t = f2_mul(f2_add(Pairs<T>::get(u, q), minus), c2);
+                float lo, hi;
+                f2_unpack(t, lo, hi);
+                const uint64_t e = f2_pack(ex2_approx(lo), ex2_approx(hi));
+                s2 = f2_add(s2, e);
+                a2 = f2_fma(e, t, a2);
+            }
+        }
+        TlpStats now{m, f2_sum(s2), f2_sum(a2)};
+        if (now.a != now.a && now.s == now.s) {  // an infinite exponent times its 0: those terms are 0
+            now.a = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int q = 0; q < V; ++q) {
+                    const float t = (tlp_elem<T>(w + 4 * i, q) - base) * p.c, e = ex2_approx(t);
+                    now.a += e > 0.f ? e * t : 0.f;
+                }
+        }
+        const float below = st.m;
+        if (m > below) {
+            st = tlp_merge(st, now, p.c);
+        } else {
+            st.s += now.s, st.a += now.a;
+        }
+        if (p.top > 0) {
+            const float old = bound;
+            if ((chunk & (chunk + 1)) == 0) {  // 1, 2, 4, ... chunks read
+                sh.part[generation][warp][lane] = st.m;
+                __syncthreads();
+                float g = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) g = fmaxf(g, sh.part[generation][i][lane]);
+                generation ^= 1;
+                bound = tlp_kth(g, p.top);
+            }
+            // a later element equal to the old bound lies behind k others that reach it
+            if (top > old && top >= bound) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        const float x = tlp_elem<T>(w + 4 * i, q);
+                        if (x > old && x >= bound) {
+                            const int n = atomicAdd(&sh.n, 1);
+                            if (n < TLP_LIST) sh.list[n] = tlp_key(x, (mine + i * THREADS) * V + q);
+                        }
+                    }
+            }
+        }
+    }
+
+    // the threads' sums, then the warps'
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        TlpStats u;
+        u.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+        u.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+        u.a = __shfl_xor_sync(0xffffffffu, st.a, o);
+        st = tlp_merge(st, u, p.c);
+    }
+    if (lane == 0) sh.warp_stats[warp] = st;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        st = sh.warp_stats[0];
+        for (int i = 1; i < WARPS; ++i) st = tlp_merge(st, sh.warp_stats[i], p.c);
+        sh.stats = st;
+    }
+    if (p.top > 0) {
+        const int n = sh.n;
+        if (n > TLP_LIST)
+            tlp_again<T, LOOSE, NV, THREADS>(sh, row, v0, v1, end, edge, all, stage, p.top);
+        else
+            tlp_rank(sh, n, p.top);
+    }
+    if (p.cluster > 1) {
+        __syncthreads();
+        cluster_sync();
+        if (rank == 0) {
+            if (threadIdx.x == 0) {
+                const uint32_t mine = smem_addr(&sh.stats);
+                for (int i = 1; i < p.cluster; ++i) {
+                    const uint32_t from = mapa_shared(mine, i);
+                    const TlpStats u{ld_cluster_f32(from), ld_cluster_f32(from + 4), ld_cluster_f32(from + 8)};
+                    st = tlp_merge(st, u, p.c);
+                }
+                sh.stats = st;
+            }
+            if (p.top > 0) {
+                const int n = p.cluster * p.top;
+                for (int i = threadIdx.x; i < n; i += THREADS)
+                    sh.list[i] = ld_cluster_u64(mapa_shared(smem_addr(&sh.best[i % p.top]), i / p.top));
+                __syncthreads();
+                tlp_rank(sh, n, p.top);
+            }
+            __syncthreads();
+        }
+        cluster_sync();  // no block leaves while its results are read
+    }
+    if (rank != 0) return;
+    __syncthreads();
+    st = sh.stats;
+    const bool empty = st.m == -INFINITY && st.s == 0.f;  // a row with nothing above -inf
+    const float ln_s = empty ? 0.f : logf(st.s);
+    if (threadIdx.x == 0) {
+        const bool skip = y == p.ignore_index, bad = y < 0 || y >= p.V;
+        p.lse[at] = empty ? -INFINITY : fmaf(p.scale, st.m, ln_s);
+        // st.s is NaN when the row holds a NaN or +inf
+        const float lp = empty ? -INFINITY : st.s != st.s ? st.s : p.scale * (xy - st.m) - ln_s;
+        p.logprob[at] = skip ? 0.f : bad ? __uint_as_float(0x7fc00000u) : lp;
+        const float h = ln_s - LN2 * (st.a / st.s);
+        if (p.entropy) p.entropy[at] = skip || empty ? 0.f : h < 0.f ? 0.f : h;
+    }
+    if (threadIdx.x < p.top) {
+        const unsigned long long key = st.s != st.s ? 0 : sh.best[threadIdx.x];
+        const float none = st.s != st.s ? st.s : -INFINITY;
+        p.top_value[at * p.top + threadIdx.x] = key ? p.scale * (tlp_key_value(key) - st.m) - ln_s : none;
+        p.top_index[at * p.top + threadIdx.x] = key ? tlp_key_col(key) : -1;
+    }
+}
+
+// ------------------------------------------------------------------- gradient
+//
+// With a_j = z_j - lse = ln p_j and H the entropy,
+//     d z_j = s [ 1[j = y] g_lp - p_j (g_lp + g_ent (a_j + H)) ]:
+// one product per element on top of the exponential.
+
+struct TlpBwdParams {
+    const void* x;
+    long long ld;
+    const long long* y;
+    long long M;
+    int V;
+    int chunks;  // of a row, each a warp's
+    long long ignore_index;
+    float scale;
+    const float* lse;
+    const float* entropy;  // or null: no gradient of it
+    const float* g_lp;     // or null: 0
+    const float* g_ent;
+    void* dx;
+    long long lddx;
+};
+
+constexpr int TLPB_THREADS = 256;
+constexpr int TLPB_NV = 4;
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+template <typename T, bool LOOSE>
+__global__ void __launch_bounds__(TLPB_THREADS) flp_token_logprob_bwd_kernel(const TlpBwdParams p) {
+    constexpr int V = wide_v<T>(), NV = TLPB_NV, P = Pairs<T>::N;
+    __shared__ __align__(16) uint8_t words[LOOSE ? TLPB_THREADS / 32 * WARP_WORDS_BYTES : 16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage = smem_addr(words) + (LOOSE ? warp * WARP_WORDS_BYTES : 0);
+    const unsigned unit = blockIdx.x * (TLPB_THREADS / 32) + warp, in_row = unit / static_cast<unsigned>(p.chunks);
+    const long long at = in_row;
+    if (at >= p.M) return;
+    const int v0 = static_cast<int>(unit - in_row * p.chunks) * 32 * NV + lane;
+    const T* row = static_cast<const T*>(p.x) + at * p.ld;
+    T* out = static_cast<T*>(p.dx) + at * p.lddx;
+    const long long y = p.y[at];
+    const float lse = p.lse[at];
+    const bool zero = y == p.ignore_index || lse == -INFINITY;
+    TlpChunk<T, LOOSE, NV, 32> x;
+    uint32_t w[4 * NV];
+    if (!zero) {
+        x.load(row, v0, p.V, at == 0 || at == p.M - 1, extent_of<T>(p.x, p.M, p.ld, p.V));
+        x.settle(w, row, v0, p.V, stage);
+    }
+    const float g_lp = p.g_lp ? p.g_lp[at] : 0.f;
+    const float g_ent = p.entropy && p.g_ent ? p.g_ent[at] : 0.f, h = p.entropy ? p.entropy[at] : 0.f;
+    const uint64_t s2 = f2_splat(p.scale), off = f2_splat(-lse), log2e = f2_splat(LOG2E);
+    const uint64_t k0 = f2_splat(-p.scale * (g_lp + g_ent * h)), k1 = f2_splat(-p.scale * g_ent);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (v0 + 32 * i) * V;
+        uint64_t g[P];
+        if (zero) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) g[q] = 0;
+        } else {
+            const uint4 u = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                float lo, hi;
+                f2_unpack(f2_fma(Pairs<T>::get(u, q), s2, off), lo, hi);
+                // p is 0 from -150 on; a finite exponent keeps it so in the product below
+                const uint64_t a = f2_pack(max_nan(lo, -1000.f), max_nan(hi, -1000.f));
+                f2_unpack(f2_mul(a, log2e), lo, hi);
+                g[q] = f2_mul(f2_pack(ex2_approx(lo), ex2_approx(hi)), f2_fma(a, k1, k0));
+            }
+            const long long hit = y - col;
+            if (hit >= 0 && hit < V) {
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    const float one = p.scale * g_lp;
+                    if (hit >> 1 == q) g[q] = f2_add(g[q], f2_pack(hit & 1 ? 0.f : one, hit & 1 ? one : 0.f));
+                }
+            }
+        }
+        store_row_vec<T, LOOSE>(out + col, Pairs<T>::put(g), p.V - col, stage);
+    }
+}
+
+}  // namespace flp

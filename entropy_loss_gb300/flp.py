@@ -35,7 +35,8 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_layer_norm_backward", "flp_checkpoint_pack", "flp_checkpoint_unpack",
            "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad", "flp_selftest_weight_grad_timeout",
            "flp_balance_loss_workspace", "flp_balance_loss", "flp_balance_loss_ex", "flp_expert_sort_workspace",
-           "flp_expert_sort", "flp_expert_gather", "flp_expert_combine", "flp_expert_combine_backward")
+           "flp_expert_sort", "flp_expert_gather", "flp_expert_combine", "flp_expert_combine_backward",
+           "flp_token_logprob", "flp_token_logprob_backward")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
 FLP_LOSS_NLL_SUM = 3
@@ -132,7 +133,9 @@ def load(path: str = LIB_PATH):
             ("flp_expert_sort", [p, i64, i64, i64, p, p, p, p, p, ctypes.c_size_t, p]),
             ("flp_expert_gather", [p, i64, i32, i64, i64, i64, p, p, p, i64, p]),
             ("flp_expert_combine", [p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p]),
-            ("flp_expert_combine_backward", [p, i64, p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p, p])):
+            ("flp_expert_combine_backward", [p, i64, p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p, p]),
+            ("flp_token_logprob", [p, i64, i32, p, i64, i64, i64, f32, p, p, p, i64, p, p, p]),
+            ("flp_token_logprob_backward", [p, i64, i32, p, i64, i64, i64, f32, p, p, p, p, p, i64, p])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32
     lib.flp_get_error.argtypes = [p, p]
@@ -879,6 +882,73 @@ def expert_combine_backward(dy, ys, order: ExpertOrder, weights=None, *, out=Non
     return out, dweights
 
 
+def _row_values(t, M, dev, name, dtype=torch.float32):
+    """Address of a value per row: contiguous [M] on `dev`, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (M,) or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} of shape ({M},) on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def token_logprob(logits, y, *, top: int = 0, scale: float = 1.0, ignore_index: int = -100, compute_entropy: bool = True,
+                  stream=None):
+    """Log-probabilities of the tokens y [M] under softmax(scale * logits), logits
+    [M, V] bf16 or fp32: (logprob, lse, entropy or None, the top largest
+    log-probabilities [M, top], their columns int64 [M, top]), the last two None
+    for top = 0.  Equal logits come in the order of their columns; -inf is not an
+    alternative (index -1)."""
+    if stream is not None:
+        return _on_stream(stream, token_logprob, logits, y, top=top, scale=scale, ignore_index=ignore_index,
+                          compute_entropy=compute_entropy)
+    zp, ld = _rows(logits, "logits")
+    M, V = logits.shape
+    code, dev = _dtype(logits, "logits"), logits.device
+    yp = _row_values(y, M, dev, "targets", torch.int64)
+    out = torch.empty((3 if compute_entropy else 2, M), dtype=torch.float32, device=dev)
+    logprob, lse = out[0], out[1]
+    entropy = out[2] if compute_entropy else None
+    values = index = None
+    if top > 0:
+        values = torch.empty((M, top), dtype=torch.float32, device=dev)
+        index = torch.empty((M, top), dtype=torch.int64, device=dev)
+    status = load().flp_token_logprob(zp, ld, code, yp, M, V, ignore_index, scale, logprob.data_ptr(), lse.data_ptr(),
+                                      entropy.data_ptr() if compute_entropy else None, top,
+                                      values.data_ptr() if top > 0 else None, index.data_ptr() if top > 0 else None,
+                                      _raw_stream(dev.index))
+    if status:
+        _check(status, "flp_token_logprob")
+    return logprob, lse, entropy, values, index
+
+
+def token_logprob_backward(logits, y, lse, entropy, grad_logprob, grad_entropy=None, *, scale: float = 1.0,
+                           ignore_index: int = -100, out=None, stream=None):
+    """The gradient by the logits, in their type, for upstream gradients of logprob
+    and entropy (None: zero).  out may be logits itself."""
+    if stream is not None:
+        return _on_stream(stream, token_logprob_backward, logits, y, lse, entropy, grad_logprob, grad_entropy, scale=scale,
+                          ignore_index=ignore_index, out=out)
+    zp, ld = _rows(logits, "logits")
+    M, V = shape = logits.shape
+    code, dev, dt = _dtype(logits, "logits"), logits.device, logits.dtype
+    yp = _row_values(y, M, dev, "targets", torch.int64)
+    if lse is None:
+        raise ValueError("lse: the forward's is needed")
+    rows = [_row_values(t, M, dev, name) for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"),
+                                                         (grad_entropy, "grad_entropy"))]
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+        op, ldo = out.data_ptr(), V
+    else:
+        op, ldo = _rows(out, "out", shape, dt)
+        _on(out, dev, "out")
+    status = load().flp_token_logprob_backward(zp, ld, code, yp, M, V, ignore_index, scale, *rows, op, ldo,
+                                               _raw_stream(dev.index))
+    if status:
+        _check(status, "flp_token_logprob_backward")
+    return out
+
+
 def get_error(workspace, stream=None) -> int:
     """Synchronise the stream and return the workspace's error status code."""
     return int(load().flp_get_error(_ptr(workspace), _stream(stream)))
@@ -1071,3 +1141,34 @@ class FusedExpertCombine(torch.autograd.Function):
 def fused_expert_combine(ys, order: ExpertOrder, weights=None):
     """Differentiable sum of each token's rows of ys [T k, H] times weights [T, k]: [T, H]."""
     return FusedExpertCombine.apply(ys, weights, order)
+
+
+class FusedTokenLogprob(torch.autograd.Function):
+    """autograd wrapper of token_logprob; the alternatives are not differentiated."""
+
+    @staticmethod
+    def forward(ctx, logits, y, top, scale, ignore_index, compute_entropy):
+        logprob, lse, entropy, values, index = token_logprob(logits, y, top=top, scale=scale, ignore_index=ignore_index,
+                                                             compute_entropy=compute_entropy)
+        ctx.save_for_backward(logits, y, lse, entropy)
+        ctx.cfg = (scale, ignore_index)
+        ctx.mark_non_differentiable(*(t for t in (values, index) if t is not None))
+        ctx.set_materialize_grads(False)
+        return logprob, entropy, values, index
+
+    @staticmethod
+    def backward(ctx, g_lp, g_ent, *_):
+        logits, y, lse, entropy = ctx.saved_tensors
+        scale, ignore_index = ctx.cfg
+        if g_lp is None and g_ent is None:
+            return None, None, None, None, None, None
+        g_lp, g_ent = (None if g is None else g.contiguous() for g in (g_lp, g_ent))
+        dz = _once(lambda: token_logprob_backward(logits, y, lse, entropy, g_lp, g_ent, scale=scale, ignore_index=ignore_index),
+                   logits, *(g for g in (g_lp, g_ent) if g is not None))
+        return dz, None, None, None, None, None
+
+
+def fused_token_logprob(logits, y, top: int = 0, scale: float = 1.0, ignore_index: int = -100, compute_entropy: bool = True):
+    """Differentiable (logprob, entropy or None, top log-probabilities or None, their
+    columns or None) of token_logprob; gradients flow through the first two."""
+    return FusedTokenLogprob.apply(logits, y, top, scale, ignore_index, compute_entropy)

@@ -576,6 +576,37 @@ flp_status flp_expert_combine_backward(const void* dY, int64_t lddy, const void*
                                        const int32_t* rows, const int64_t* total, void* dYS, int64_t lddys,
                                        float* dweights, void* stream);
 
+/*
+ * Log-probabilities of given tokens from logits [M, V] in memory (bf16 or fp32,
+ * row pitch ld): with z = scale * logits (scale > 0, finite),
+ *   lse = log sum_j exp(z_j),   logprob = z_y - lse,
+ *   entropy = lse - sum_j p_j z_j,   p_j = exp(z_j - lse)      (fp32 [M])
+ * entropy may be NULL.  The `top` largest logits of each row (0 <= top <=
+ * min(V, 32); equal ones by their column, lowest first) are written as
+ * top_logprob [M, top] (fp32, z - lse) and top_index [M, top] (int64).  -inf is
+ * never among them: where fewer are left, the value is -inf and the index -1.
+ * An ignored row (target == ignore_index) has logprob = entropy = 0; its lse and
+ * alternatives are still written.  Any other target outside [0, V) gives
+ * logprob = NaN.  A row with a NaN or +inf gives NaN (and index -1) throughout;
+ * a row with nothing above -inf gives lse = logprob = -inf and entropy 0.
+ * No workspace is needed.
+ */
+flp_status flp_token_logprob(const void* logits, int64_t ld, int dtype, const int64_t* targets, int64_t M,
+                             int64_t V, int64_t ignore_index, float scale, float* logprob, float* lse,
+                             float* entropy, int64_t top, float* top_logprob, int64_t* top_index, void* stream);
+
+/*
+ * Its gradient by the logits, from the forward's lse and entropy:
+ *   dlogits_j = scale [ g_lp (1[j = y] - p_j) - g_ent p_j (z_j - lse + entropy) ]
+ * in the logits' type (dlogits may be logits itself).  grad_logprob and
+ * grad_entropy (fp32 [M]) may be NULL: 0; grad_entropy needs entropy.  Ignored
+ * rows and rows of lse = -inf get zeros; a target outside [0, V) has no 1[j = y].
+ */
+flp_status flp_token_logprob_backward(const void* logits, int64_t ld, int dtype, const int64_t* targets, int64_t M,
+                                      int64_t V, int64_t ignore_index, float scale, const float* lse,
+                                      const float* entropy, const float* grad_logprob, const float* grad_entropy,
+                                      void* dlogits, int64_t lddl, void* stream);
+
 /* Static description of a status code. */
 const char* flp_status_string(flp_status status);
 

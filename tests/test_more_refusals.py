@@ -75,6 +75,36 @@ def test_expert_rows(flp, b):
         assert backward(**o) == flp.FLP_ERR_INVALID_ARG, o
 
 
+def test_token_logprob(flp, b):
+    def call(**o):
+        a = dict(x=b, ld=64, dt=1, y=b, M=4, V=64, s=1.0, lp=b, lse=b, e=b, k=2, tv=b, ti=b)
+        a.update(o)
+        return flp.load().flp_token_logprob(a["x"], a["ld"], a["dt"], a["y"], a["M"], a["V"], -100, a["s"], a["lp"], a["lse"], a["e"],
+                                            a["k"], a["tv"], a["ti"], None)
+
+    for o in (dict(M=-1), dict(V=0), dict(dt=2), dict(x=None), dict(y=None), dict(y=b + 4), dict(ld=63), dict(x=b + 1), dict(s=0.0),
+              dict(s=-1.0), dict(s=float("nan")), dict(s=float("inf")), dict(s=3e38), dict(lp=None), dict(lse=None), dict(k=-1),
+              dict(k=65), dict(V=1, k=2), dict(tv=None), dict(ti=None), dict(lp=b + 2), dict(lse=b + 2), dict(e=b + 1),
+              dict(tv=b + 2), dict(ti=b + 4)):
+        assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
+    for o in (dict(k=33), dict(M=2 ** 31), dict(V=2 ** 31, ld=2 ** 31)):
+        assert call(**o) == flp.FLP_ERR_UNSUPPORTED, o
+    assert call(M=0, x=None, y=None, lp=None, lse=None, tv=None, ti=None) == flp.FLP_OK
+
+
+def test_token_logprob_backward(flp, b):
+    def call(**o):
+        a = dict(x=b, ld=64, dt=1, y=b, M=4, V=64, s=1.0, lse=b, e=b, gl=b, ge=b, dx=b, lddx=64)
+        a.update(o)
+        return flp.load().flp_token_logprob_backward(a["x"], a["ld"], a["dt"], a["y"], a["M"], a["V"], -100, a["s"], a["lse"], a["e"],
+                                                     a["gl"], a["ge"], a["dx"], a["lddx"], None)
+
+    for o in (dict(M=-1), dict(V=0), dict(dt=5), dict(x=None), dict(y=None), dict(ld=1), dict(s=0.0), dict(lse=None), dict(e=None),
+              dict(lse=b + 1), dict(e=b + 2), dict(gl=b + 2), dict(ge=b + 2), dict(dx=None), dict(lddx=63), dict(dx=b + 1)):
+        assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
+    assert call(M=0, x=None, y=None, lse=None, dx=None) == flp.FLP_OK
+
+
 def test_binding_refuses_before_loading_anything_on_a_device(flp):
     import torch
     x = torch.zeros(4, 64)
@@ -82,6 +112,7 @@ def test_binding_refuses_before_loading_anything_on_a_device(flp):
                             torch.zeros(3, dtype=torch.int64))
     for f in (lambda: flp.expert_sort(torch.zeros(4, 2, dtype=torch.int64), 2), lambda: flp.expert_sort(torch.zeros(4), 2),
               lambda: flp.expert_gather(x, order), lambda: flp.expert_combine(x, order),
-              lambda: flp.expert_combine_backward(x, x, order)):
+              lambda: flp.expert_combine_backward(x, x, order), lambda: flp.token_logprob(x, x[:, 0].long()),
+              lambda: flp.token_logprob_backward(x, x[:, 0].long(), x[:, 0], None, None)):
         with pytest.raises(ValueError):
             f()
