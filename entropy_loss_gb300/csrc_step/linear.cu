@@ -1,0 +1,388 @@
+// linear.cu - host side of the linear layer declared in include/flp.h.
+#include "linear.cuh"
+#include "step_host.cuh"
+
+namespace {
+
+// ------------------------------------------------------------------ product
+
+struct LinPlan {
+    int tm, tn, whole, rest, splits, units, KB, rows;
+    size_t part_bytes;
+};
+
+// Whole rounds of tiles write their outputs; the rest are split into the number of runs
+// that costs least, in the time of a 64-deep block of a tile (0.54 us): the blocks of a
+// run and two for its start and end, and for joining 4 (a launch) and the partial tiles'
+// bytes, written and read back at 2 MB a block.
+LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
+    LinPlan l{};
+    pairs = std::max(1, pairs);
+    l.tm = static_cast<int>(cdiv(M, PM));
+    l.tn = static_cast<int>(cdiv(N, 2 * BN));
+    l.KB = static_cast<int>(cdiv(depth, BK));
+    l.rows = static_cast<int>(std::min<int64_t>(M, PM));
+    const int64_t tiles = static_cast<int64_t>(l.tm) * l.tn;
+    l.whole = static_cast<int>(tiles / pairs * pairs);
+    int64_t rest = tiles - l.whole;
+    l.splits = 1;
+    if (rest > 0) {
+        const double tile_mb = static_cast<double>(l.rows) * 2 * BN * 4 * 2 / 1e6;
+        double best = 1e300;
+        const int64_t most = std::min<int64_t>(l.KB, std::max<int64_t>(1, 4 * pairs / rest));
+        for (int64_t s = 1; s <= most; ++s) {
+            const double joined = s > 1 ? 4.0 + tile_mb / 2 * static_cast<double>(rest * s) : 0.0;
+            const double cost = static_cast<double>(cdiv(rest * s, pairs) * (cdiv(l.KB, s) + 2)) + joined;
+            if (cost < best - 1e-9) {
+                best = cost;
+                l.splits = static_cast<int>(s);
+            }
+        }
+        if (l.splits == 1) {
+            l.whole = static_cast<int>(tiles);
+            rest = 0;
+        }
+    }
+    l.rest = static_cast<int>(rest);
+    l.units = l.whole + l.rest * l.splits;
+    l.part_bytes = static_cast<size_t>(l.rest) * l.splits * l.rows * 2 * BN * 4;
+    return l;
+}
+
+// The products' shared memory, once per device.
+flp_status linear_attrs() {
+    static bool done[kMaxDevices] = {};
+    int dev = 0;
+    FLP_CUDA(cudaGetDevice(&dev));  // in range: check_device has run
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!done[dev]) {
+        FLP_CUDA(cudaFuncSetAttribute(flp_linear_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        FLP_CUDA(cudaFuncSetAttribute(flp_linear_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        done[dev] = true;
+    }
+    return FLP_OK;
+}
+
+// One product and, for split tiles, its join: A [M, depth] and W (w_mn: [depth, N], else
+// [N, depth]), rows aligned to 16 bytes.
+flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const void* w, int64_t ldw, bool w_mn, int64_t M,
+                          int64_t N, int64_t depth, const LinEpilogue& e, void* part, int* err, int pairs,
+                          unsigned long long wait_limit_ns, int stall_after, bool after_kernel, cudaStream_t s) {
+    constexpr auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap ma, mb, my, mp;
+    flp_status st = tmap_2d(&ma, BF, a, depth, M, lda * 2, BK, BM);
+    if (st == FLP_OK) st = w_mn ? tmap_2d(&mb, BF, w, N, depth, ldw * 2, 64, 64) : tmap_2d(&mb, BF, w, depth, N, ldw * 2, BK, BNH);
+    if (st != FLP_OK) return st;
+    my = mp = ma;  // where no bulk store writes
+    if (e.vec && (st = tmap_2d(&my, BF, e.y, N, M, e.ldy * 2, 32, BM, CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK) return st;
+    if (e.vec && e.pre && (st = tmap_2d(&mp, BF, e.pre, N, M, e.ldpre * 2, 32, BM, CU_TENSOR_MAP_SWIZZLE_64B)) != FLP_OK)
+        return st;
+    LinParams p{};
+    p.tm = l.tm;
+    p.tn = l.tn;
+    p.group = std::min(l.tm, 8);
+    p.whole = l.whole;
+    p.splits = l.splits;
+    p.units = l.units;
+    p.KB = l.KB;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.part = static_cast<float*>(part);
+    p.rows = l.rows;
+    p.e = e;
+    p.err = err;
+    p.wait_limit_ns = wait_limit_ns;
+    p.stall_after = stall_after;
+    const int grid = 2 * static_cast<int>(std::min<int64_t>(l.units, pairs));
+    st = launch_pairs_n(w_mn ? flp_linear_kernel<1> : flp_linear_kernel<0>, grid, WIDE_THREADS, s, "flp_linear_kernel launch",
+                        after_kernel, ma, mb, my, mp, p);
+    if (st != FLP_OK || !l.rest) return st;
+    return launch_step(flp_linear_join_kernel, static_cast<int64_t>(l.rest) * l.rows, LJ_THREADS, 0, s,
+                       "flp_linear_join_kernel launch", true, p);
+}
+
+flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 1 || K < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0, N >= 1 and K >= 1 required");
+    const int64_t most = kMaxRows - 1024;
+    if (M > most || N > most || K > most || cdiv(M, PM) * cdiv(N, 2 * BN) > (1 << 22) || cdiv(M, PM) * cdiv(K, 2 * BN) > (1 << 22))
+        return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
+    return FLP_OK;
+}
+
+flp_status linear_act(int activation) {
+    return activation >= FLP_ACT_NONE && activation <= FLP_ACT_SILU ? FLP_OK : fail(FLP_ERR_INVALID_ARG, "unknown activation");
+}
+static_assert(FLP_ACT_NONE == LIN_NONE && FLP_ACT_RELU == LIN_RELU && FLP_ACT_GELU == LIN_GELU &&
+                  FLP_ACT_GELU_TANH == LIN_GELU_TANH && FLP_ACT_SILU == LIN_SILU,
+              "one numbering");
+
+inline bool rows_bf16(const void* p, int64_t ld) { return rows16(p, ld, FLP_BF16); }
+inline int64_t pad8(int64_t n) { return cdiv(n, 8) * 8; }
+
+// Regions of a workspace, 1 KiB aligned.
+struct Regions {
+    size_t bytes = 0;
+    size_t take(size_t n) {
+        const size_t at = bytes;
+        bytes += align_up(n, 1024);
+        return at;
+    }
+};
+
+struct LinearLayout {
+    LinPlan l;
+    size_t off_x, off_w, off_part, bytes;
+    bool copy_x, copy_w;
+};
+
+LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K, int pairs) {
+    LinearLayout f{};
+    f.l = plan_linear(M, N, K, pairs);
+    f.copy_x = !rows_bf16(X, ldx);
+    f.copy_w = !rows_bf16(W, ldw);
+    Regions r;
+    f.off_x = r.take(f.copy_x ? M * pad8(K) * 2 : 0);
+    f.off_w = r.take(f.copy_w ? N * pad8(K) * 2 : 0);
+    f.off_part = r.take(f.l.part_bytes);
+    f.bytes = r.bytes;
+    return f;
+}
+
+struct LinearGradLayout {
+    LinPlan l;  // of dx
+    size_t off_dw, off_x, off_w, off_d, off_part, off_sums, bytes;
+    bool copy_x, copy_w, make_d, sums;
+    int blocks, rows;  // of the column sums
+};
+
+// Row blocks of the pass over dy: enough for every SM to hold two blocks of threads, of
+// at least 32 rows (the warps' and their loads').
+LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                    int activation, bool want_dx, bool want_dw, bool want_db, int64_t M, int64_t N, int64_t K,
+                                    int dw_dtype, int sm_count, int pairs) {
+    LinearGradLayout g{};
+    g.l = plan_linear(M, K, N, pairs);
+    g.copy_x = want_dw && !rows_bf16(X, ldx);
+    g.copy_w = want_dx && !rows_bf16(W, ldw);
+    g.make_d = (want_dx || want_dw) && (activation != FLP_ACT_NONE || !rows_bf16(dY, lddy));
+    g.sums = want_db;
+    const int64_t strips = cdiv(N, 256);
+    g.rows = static_cast<int>(std::max<int64_t>(32, cdiv(cdiv(M, std::max<int64_t>(1, cdiv(8 * sm_count, strips))), 32) * 32));
+    while (cdiv(M, g.rows) > 65535) g.rows *= 2;
+    g.blocks = static_cast<int>(cdiv(M, g.rows));
+    Regions r;
+    r.take(kHeaderBytes);  // the error word
+    g.off_dw = 0;          // whose region it begins
+    if (want_dw) r.bytes = align_up(std::max(r.bytes, weight_grad_bytes(M, N, K, dw_dtype, pairs)), 1024);
+    g.off_x = r.take(g.copy_x ? M * pad8(K) * 2 : 0);
+    g.off_w = r.take(g.copy_w ? N * pad8(K) * 2 : 0);
+    g.off_d = r.take(g.make_d ? M * pad8(N) * 2 : 0);
+    g.off_part = r.take(want_dx ? g.l.part_bytes : 0);
+    g.off_sums = r.take(g.sums ? static_cast<size_t>(g.blocks) * N * 4 : 0);
+    g.bytes = r.bytes;
+    return g;
+}
+
+}  // namespace
+
+extern "C" flp_status flp_linear_workspace(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N,
+                                           int64_t K, size_t* bytes) {
+    if (!bytes) return fail(FLP_ERR_INVALID_ARG, "bytes must be non-null");
+    flp_status st = linear_sizes(M, N, K);
+    if (st != FLP_OK) return st;
+    DevInfo* d;
+    if ((st = check_device(&d)) != FLP_OK) return st;
+    *bytes = M == 0 ? 0 : linear_layout(X, ldx, W, ldw, M, N, K, d->pairs).bytes;
+    return FLP_OK;
+}
+
+extern "C" flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, const void* bias, int bias_dtype,
+                                 int activation, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K, void* Y,
+                                 int64_t ldy, void* pre, int64_t ldpre, void* workspace, size_t workspace_bytes, void* stream) {
+    flp_status st = linear_sizes(M, N, K);
+    if (st == FLP_OK) st = linear_act(activation);
+    if (st != FLP_OK) return st;
+    if (bias && (!is_dtype(bias_dtype) || !aligned_to(bias, elem(bias_dtype))))
+        return fail(FLP_ERR_INVALID_ARG, "bias is FLP_F32 or FLP_BF16 and aligned to its elements");
+    if (M == 0) return FLP_OK;
+    st = row_checks(X, ldx, K, FLP_BF16, "X must be non-null");
+    if (st == FLP_OK) st = row_checks(W, ldw, K, FLP_BF16, "W must be non-null");
+    if (st == FLP_OK) st = row_checks(Y, ldy, N, FLP_BF16, "Y must be non-null");
+    if (st == FLP_OK && residual) st = row_checks(residual, ldr, N, FLP_BF16, "residual must be non-null");
+    if (st == FLP_OK && pre) st = row_checks(pre, ldpre, N, FLP_BF16, "pre must be non-null");
+    DevInfo* d;
+    if (st == FLP_OK) st = check_device(&d);
+    if (st == FLP_OK) st = check_on_current_device(X, "X");
+    if (st == FLP_OK) st = linear_attrs();
+    if (st != FLP_OK) return st;
+    const LinearLayout f = linear_layout(X, ldx, W, ldw, M, N, K, d->pairs);
+    if (f.bytes > 0 && (!workspace || workspace_bytes < f.bytes || !aligned16(workspace)))
+        return fail(FLP_ERR_WORKSPACE, "linear workspace null, misaligned or too small");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    bool after = false;
+    if (f.copy_x) {
+        if ((st = align_rows(X, ldx, M, K, ws + f.off_x, pad8(K), s)) != FLP_OK) return st;
+        X = ws + f.off_x, ldx = pad8(K), after = true;
+    }
+    if (f.copy_w) {
+        if ((st = align_rows(W, ldw, N, K, ws + f.off_w, pad8(K), s)) != FLP_OK) return st;
+        W = ws + f.off_w, ldw = pad8(K), after = true;
+    }
+    LinEpilogue e{};
+    e.bias = bias;
+    e.bias_f32 = bias_dtype == FLP_F32;
+    e.act = activation;
+    e.residual = static_cast<const bf16*>(residual);
+    e.ldr = ldr;
+    e.y = static_cast<bf16*>(Y);
+    e.ldy = ldy;
+    e.pre = static_cast<bf16*>(pre);
+    e.ldpre = ldpre;
+    e.vec = rows_bf16(Y, ldy) && N % 8 == 0 && (!residual || rows_bf16(residual, ldr)) && (!pre || rows_bf16(pre, ldpre));
+    e.bias_vec = aligned16(bias);
+    return linear_product(f.l, X, ldx, W, ldw, false, M, N, K, e, ws + f.off_part, nullptr, d->pairs, kWaitLimitNs, -1, after, s);
+}
+
+extern "C" flp_status flp_linear_backward_workspace(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W,
+                                                    int64_t ldw, int activation, int want_dX, int want_dW, int want_dbias,
+                                                    int64_t M, int64_t N, int64_t K, int dW_dtype, size_t* bytes) {
+    if (!bytes) return fail(FLP_ERR_INVALID_ARG, "bytes must be non-null");
+    flp_status st = linear_sizes(M, N, K);
+    if (st == FLP_OK) st = linear_act(activation);
+    if (st == FLP_OK) st = weight_grad_checks(M, N, K, dW_dtype);
+    if (st != FLP_OK) return st;
+    DevInfo* d;
+    if ((st = check_device(&d)) != FLP_OK) return st;
+    *bytes = M == 0 ? 0 : linear_grad_layout(dY, lddy, X, ldx, W, ldw, activation, want_dX, want_dW, want_dbias, M, N, K, dW_dtype,
+                                             d->sm_count, d->pairs).bytes;
+    return FLP_OK;
+}
+
+extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                          const void* pre, int64_t ldpre, int activation, int64_t M, int64_t N, int64_t K,
+                                          void* dX, int64_t lddx, void* dW, int dW_dtype, float* dbias, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+    flp_status st = linear_sizes(M, N, K);
+    if (st == FLP_OK) st = linear_act(activation);
+    if (st == FLP_OK) st = weight_grad_checks(M, N, K, dW_dtype);
+    if (st != FLP_OK) return st;
+    if (!aligned16(dW)) return fail(FLP_ERR_INVALID_ARG, "dW must be 16-byte aligned");
+    if (!aligned_to(dbias, 4)) return fail(FLP_ERR_INVALID_ARG, "dbias must be aligned to its elements");
+    if (M > 0) {
+        st = row_checks(dY, lddy, N, FLP_BF16, "dY must be non-null");
+        if (st == FLP_OK && dW) st = row_checks(X, ldx, K, FLP_BF16, "dW needs X");
+        if (st == FLP_OK && dX) st = row_checks(W, ldw, K, FLP_BF16, "dX needs W");
+        if (st == FLP_OK && dX) st = row_checks(dX, lddx, K, FLP_BF16, "dX must be non-null");
+        if (st == FLP_OK && activation != FLP_ACT_NONE)
+            st = row_checks(pre, ldpre, N, FLP_BF16, "an activation's gradient needs pre");
+        if (st != FLP_OK) return st;
+    }
+    if (!dX && !dW && !dbias) return FLP_OK;
+    DevInfo* d;
+    st = check_device(&d);
+    if (st == FLP_OK) st = check_on_current_device(M > 0 ? dY : dW ? dW : dbias, "dY");
+    if (st == FLP_OK) st = linear_attrs();
+    if (st != FLP_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (dW) FLP_CUDA(cudaMemsetAsync(dW, 0, static_cast<size_t>(N) * K * elem(dW_dtype), s));
+        if (dbias) FLP_CUDA(cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 4, s));
+        return FLP_OK;
+    }
+    const LinearGradLayout g = linear_grad_layout(dY, lddy, X, ldx, W, ldw, activation, dX, dW, dbias, M, N, K, dW_dtype, d->sm_count,
+                                                  d->pairs);
+    if (!workspace || workspace_bytes < g.bytes || !aligned16(workspace))
+        return fail(FLP_ERR_WORKSPACE, "linear backward workspace null, misaligned or too small");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int* err = reinterpret_cast<int*>(ws);
+    FLP_CUDA(cudaMemsetAsync(err, 0, sizeof(int), s));
+    bool after = false;
+    if (g.copy_x) {
+        if ((st = align_rows(X, ldx, M, K, ws + g.off_x, pad8(K), s)) != FLP_OK) return st;
+        X = ws + g.off_x, ldx = pad8(K), after = true;
+    }
+    if (g.copy_w) {
+        if ((st = align_rows(W, ldw, N, K, ws + g.off_w, pad8(K), s)) != FLP_OK) return st;
+        W = ws + g.off_w, ldw = pad8(K), after = true;
+    }
+    const bool vec = rows_bf16(dY, lddy) && N % 8 == 0 && (activation == FLP_ACT_NONE || rows_bf16(pre, ldpre));
+    if (g.make_d || g.sums) {
+        LinGradParams p{};
+        p.dy = static_cast<const bf16*>(dY);
+        p.lddy = lddy;
+        p.pre = activation == FLP_ACT_NONE ? nullptr : static_cast<const bf16*>(pre);
+        p.ldpre = ldpre;
+        p.act = activation;
+        p.M = static_cast<int>(M);
+        p.N = static_cast<int>(N);
+        p.d = g.make_d ? reinterpret_cast<bf16*>(ws + g.off_d) : nullptr;
+        p.Np = static_cast<int>(pad8(N));
+        p.part = g.sums ? g.blocks == 1 ? dbias : reinterpret_cast<float*>(ws + g.off_sums) : nullptr;
+        p.rows = g.rows;
+        const dim3 grid(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(g.blocks));
+        if (vec)
+            flp_linear_grad_kernel<false><<<grid, LG_THREADS, 0, s>>>(p);
+        else
+            flp_linear_grad_kernel<true><<<grid, LG_THREADS, 0, s>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e, "flp_linear_grad_kernel launch");
+        if (g.make_d) dY = ws + g.off_d, lddy = pad8(N);
+        if (g.sums && g.blocks > 1) {
+            st = launch_step(flp_linear_bias_join_kernel, cdiv(N, 32), 32 * LB_WAYS, 0, s, "flp_linear_bias_join_kernel launch", true,
+                             reinterpret_cast<const float*>(ws + g.off_sums), g.blocks, static_cast<int>(N), dbias);
+            if (st != FLP_OK) return st;
+        }
+        after = true;
+    }
+    if (dX) {
+        LinEpilogue e{};
+        e.y = static_cast<bf16*>(dX);
+        e.ldy = lddx;
+        e.vec = rows_bf16(dX, lddx) && K % 8 == 0;
+        st = linear_product(g.l, dY, lddy, W, ldw, true, M, K, N, e, ws + g.off_part, err, d->pairs, kWaitLimitNs, -1, after, s);
+        if (st != FLP_OK) return st;
+        after = true;
+    }
+    return dW ? weight_grad(dY, lddy, X, ldx, M, N, K, dW, dW_dtype, ws + g.off_dw, d->pairs, after, s) : FLP_OK;
+}
+
+// M = 192 rows, N = 520 columns (two 256 x 512 tiles, the second of 8 columns), 192 deep:
+// three blocks a tile, on one CTA pair; split: both tiles through partial tiles of one block.
+extern "C" flp_status flp_selftest_linear_timeout(void* workspace, size_t workspace_bytes, int split, int stall_after,
+                                                  int64_t wait_limit_ns, void* stream) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < FLP_SELFTEST_LINEAR_BYTES)
+        return fail(FLP_ERR_WORKSPACE, "self-test needs FLP_SELFTEST_LINEAR_BYTES of workspace");
+    if (wait_limit_ns <= 0 || wait_limit_ns > 60ll * 1000 * 1000 * 1000)
+        return fail(FLP_ERR_INVALID_ARG, "wait_limit_ns must be in (0, 60 s]");
+    DevInfo* d;
+    flp_status st = check_device(&d);
+    if (st == FLP_OK) st = check_on_current_device(workspace, "workspace");
+    if (st == FLP_OK) st = linear_attrs();
+    if (st != FLP_OK) return st;
+    const int64_t M = 192, N = 520, K = 192;
+    LinPlan l = plan_linear(M, N, K, 1);
+    l.splits = split ? 3 : 1;
+    l.whole = split ? 0 : 2;
+    l.rest = split ? 2 : 0;
+    l.units = l.whole + l.rest * l.splits;
+    Regions r;
+    r.take(kHeaderBytes);
+    const size_t off_x = r.take(M * K * 2), off_w = r.take(N * K * 2);
+    const size_t zero = r.bytes;
+    const size_t off_part = r.take(2ull * 3 * M * 2 * BN * 4);
+    if (r.bytes > FLP_SELFTEST_LINEAR_OUTPUT_OFFSET || FLP_SELFTEST_LINEAR_OUTPUT_OFFSET + M * N * 2 > FLP_SELFTEST_LINEAR_BYTES)
+        return fail(FLP_ERR_UNSUPPORTED, "self-test layout exceeds its workspace");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LinEpilogue e{};
+    e.y = reinterpret_cast<bf16*>(ws + FLP_SELFTEST_LINEAR_OUTPUT_OFFSET);
+    e.ldy = N;
+    e.vec = 1;
+    FLP_CUDA(cudaMemsetAsync(ws, 0, zero, s));                       // error word, x, W
+    FLP_CUDA(cudaMemsetAsync(ws + off_part, 0x3f, r.bytes - off_part, s));  // what the partial tiles
+    FLP_CUDA(cudaMemsetAsync(e.y, 0x3f, M * N * 2, s));              // and the result have to replace
+    st = linear_product(l, ws + off_x, K, ws + off_w, K, false, M, N, K, e, ws + off_part, reinterpret_cast<int*>(ws), 1,
+                        static_cast<unsigned long long>(wait_limit_ns), stall_after < 0 ? -1 : stall_after, false, s);
+    return st == FLP_OK ? flp_get_error(workspace, stream) : st;
+}

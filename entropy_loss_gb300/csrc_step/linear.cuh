@@ -1,0 +1,643 @@
+// linear.cuh - a linear layer with bias, activation and residual in its epilogue, and
+// what its gradients need:
+//     forward   v = x W^T + b,  y = act(v) + r,  v kept in bf16 for the backward pass
+//     backward  d = dy act'(v),  dx = d W,  dW = d^T x,  db = column sums of d
+// x [M, K], W [N, K], y [M, N] in bf16, sums and everything up to the one rounding of
+// each output in fp32 (so y does not carry the rounding of v).
+//
+// The products x W^T and d W run in one kernel on CTA pairs: 256 x 512 tiles in both TMEM
+// accumulators, four 48 KiB slots fed by TMA, the halves staggered at the tile ends, one
+// epilogue group per accumulator; W is the K-major operand of the first and the MN-major
+// one of the second.  Whole rounds of tiles over the resident pairs write their outputs
+// themselves; the tiles of the last, incomplete round (all of them, when rows are few)
+// are split along the contraction into fp32 partial tiles, which a small kernel joins in
+// a fixed order and takes through the same epilogue.  d is rounded to bf16 once, by a
+// pass over dy and v that also sums db from the unrounded values; dW is the contraction
+// of wgrad.cuh.
+#pragma once
+#include "../csrc/pair.cuh"
+#include "vec.cuh"
+
+namespace flp {
+
+constexpr int LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4;
+
+// ------------------------------------------------------------------ activation
+
+constexpr float LIN_SQRT_HALF = 0.7071067811865476f;
+constexpr float LIN_INV_SQRT_2PI = 0.3989422804014327f;
+constexpr float LIN_TANH_U = 1.5957691216057308f;   // gelu_tanh(v) = v sigmoid(u), u = sqrt(8 / pi) (v + 0.044715 v^3)
+constexpr float LIN_TANH_3 = 0.044715f;
+
+__device__ __forceinline__ float lin_sigmoid(float u) { return __fdividef(1.f, 1.f + ex2_approx(-LOG2E * u)); }
+
+// Phi(v) = erfc(-v / sqrt 2) / 2 keeps the digits of negative v that 1 + erf loses.
+__device__ __forceinline__ float lin_act(float v, int kind) {
+    switch (kind) {
+        case LIN_RELU: return v < 0.f ? 0.f : v;
+        case LIN_GELU: return 0.5f * v * erfcf(-LIN_SQRT_HALF * v);
+        case LIN_GELU_TANH: return v * lin_sigmoid(LIN_TANH_U * (v + LIN_TANH_3 * v * v * v));
+        case LIN_SILU: return v * lin_sigmoid(v);
+        default: return v;
+    }
+}
+
+// act'.  Far from 0 it is 0 or 1 to the last bit, and v^2 times a vanishing factor no number.
+__device__ __forceinline__ float lin_slope(float v, int kind) {
+    if (kind == LIN_RELU) return v > 0.f ? 1.f : 0.f;
+    v = v > 20.f ? 20.f : v < -20.f ? -20.f : v;  // NaN stays
+    if (kind == LIN_GELU)
+        return 0.5f * erfcf(-LIN_SQRT_HALF * v) + v * LIN_INV_SQRT_2PI * ex2_approx(-0.5f * LOG2E * v * v);
+    float u = v, du = 1.f;
+    if (kind == LIN_GELU_TANH) {
+        u = LIN_TANH_U * (v + LIN_TANH_3 * v * v * v);
+        du = LIN_TANH_U * (1.f + 3.f * LIN_TANH_3 * v * v);
+    }
+    const float p = lin_sigmoid(u);
+    return p + v * du * p * lin_sigmoid(-u);
+}
+
+// ------------------------------------------------------------------ product
+
+struct LinEpilogue {
+    const void* bias;  // [N], or null
+    int bias_f32;
+    int act;
+    const bf16* residual;  // [M, N], or null
+    long long ldr;
+    bf16* y;
+    long long ldy;
+    bf16* pre;  // or null
+    long long ldpre;
+    int vec;       // the rows of y, residual and pre are aligned to 16 bytes
+    int bias_vec;  // and so is the bias
+};
+
+struct LinParams {
+    int tm, tn;   // 256-row and 512-column tiles
+    int group;    // row tiles that share their column tiles while both are in L2
+    int whole;    // tiles that are written directly (units 0 .. whole - 1)
+    int splits;   // runs of each other tile
+    int units;
+    int KB;       // 64-deep blocks of the contraction
+    int M, N;
+    float* part;  // partial tiles [tile][split][rows][512]
+    int rows;     // of a partial tile: min(M, 256)
+    LinEpilogue e;
+    int* err;     // error word, or null
+    unsigned long long wait_limit_ns;
+    int stall_after;  // < 0: off; else the producers stop after this many blocks (self-test)
+};
+
+struct LinUnit {
+    int m0, n0;    // first row and column of the tile
+    int kb0, kb1;  // blocks of the contraction
+    int part;      // partial tile index, -1: the outputs are written
+    int halves;    // 256-column halves that hold columns
+};
+
+__device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
+    LinUnit t;
+    int tile = u;
+    t.part = -1;
+    t.kb0 = 0;
+    t.kb1 = p.KB;
+    if (u >= p.whole) {
+        t.part = u - p.whole;
+        tile = p.whole + t.part / p.splits;
+        const int s = t.part % p.splits;
+        t.kb0 = static_cast<int>(static_cast<long long>(p.KB) * s / p.splits);
+        t.kb1 = static_cast<int>(static_cast<long long>(p.KB) * (s + 1) / p.splits);
+    }
+    const int per = p.group * p.tn;
+    const int g = tile / per;
+    const int rows = min(p.group, p.tm - g * p.group);
+    const int r = tile - g * per;
+    t.n0 = r / rows * (2 * BN);
+    t.m0 = (g * p.group + r % rows) * PM;
+    t.halves = t.n0 + BN < p.N ? 2 : 1;
+    return t;
+}
+
+// Bias values of 32 columns from c0 on (0 past N or without a bias), added to v.
+__device__ __forceinline__ void lin_add_bias(const LinEpilogue& e, int c0, int N, float (&v)[32]) {
+    if (!e.bias) return;
+    if (e.bias_vec && c0 + 32 <= N) {
+        if (e.bias_f32) {
+            const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + c0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 u = __ldg(b + i);
+                v[4 * i] += u.x, v[4 * i + 1] += u.y, v[4 * i + 2] += u.z, v[4 * i + 3] += u.w;
+            }
+        } else {
+            const uint4* b = reinterpret_cast<const uint4*>(static_cast<const bf16*>(e.bias) + c0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 u = __ldg(b + i);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+                    v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
+        }
+    } else {
+        const int c = c0 + (threadIdx.x & 31);  // a lane's column, passed around
+        float mine = 0.f;
+        if (c < N)
+            mine = e.bias_f32 ? static_cast<const float*>(e.bias)[c] : __bfloat162float(static_cast<const bf16*>(e.bias)[c]);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
+    }
+}
+
+// A warp's 32 rows x 32 columns between its part of a box (64 bytes a row, swizzled) and
+// rows in memory at any alignment: a row at a time, one column a lane.
+__device__ __forceinline__ uint32_t lin_box_word(uint32_t row_addr, int r, int word) {
+    return row_addr + (((word >> 2) ^ ((r >> 1) & 3)) << 4) + (word & 3) * 4;
+}
+__device__ __forceinline__ void lin_rows_out(uint32_t box, const uint32_t (&w)[16], bf16* out, long long ld, int row0, int rows,
+                                             int c0, int N) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        st_shared_v4(lin_box_word(box + lane * 64, lane, 4 * i), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncwarp();
+    const int n = min(32, rows - row0);
+    if (c0 + lane < N) {
+        bf16* o = out + row0 * ld + c0 + lane;
+#pragma unroll 4
+        for (int r = 0; r < n; ++r) {
+            const uint32_t u = ld_shared_4(lin_box_word(box + r * 64, r, lane >> 1));
+            *reinterpret_cast<unsigned short*>(o + r * ld) = static_cast<unsigned short>(lane & 1 ? u >> 16 : u);
+        }
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void lin_rows_in(uint32_t box, uint32_t (&w)[16], const bf16* in, long long ld, int row0, int rows,
+                                            int c0, int N) {
+    const int lane = threadIdx.x & 31;
+    const int n = min(32, rows - row0);
+    const bool on = c0 + lane < N;
+    const bf16* o = in + row0 * ld + c0 + lane;
+#pragma unroll 4
+    for (int r = 0; r < n; ++r) {
+        const unsigned short u = on ? *reinterpret_cast<const unsigned short*>(o + r * ld) : 0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(lin_box_word(box + r * 64, r, lane >> 1) + 2 * (lane & 1)), "h"(u) : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 u = ld_shared_16(lin_box_word(box + lane * 64, lane, 4 * i));
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void lin_pack(const float (&v)[32], uint32_t (&w)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+}
+
+// NaN in what an epilogue group (half g of a tile, the 128 rows from `rofs` on) has not
+// finished, from unit u on: what a timed-out product leaves there is no result.
+__device__ __noinline__ void lin_fill_nan(const LinParams& p, int u, int npairs, int g, int rofs, int et) {
+    for (; u < p.units; u += npairs) {
+        const LinUnit t = lin_unit(p, u);
+        if (g >= t.halves) continue;
+        const int m0 = t.m0 + rofs, n0 = t.n0 + g * BN;
+        const int rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
+        for (int r = 0; r < rows; ++r)
+            for (int c = et; c < cols; c += EPI_THREADS) {
+                if (t.part >= 0) {
+                    p.part[(static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + g * BN + c] = __uint_as_float(0x7fc00000u);
+                } else {
+                    p.e.y[static_cast<long long>(m0 + r) * p.e.ldy + n0 + c] = __ushort_as_bfloat16(0x7fc0);
+                    if (p.e.pre) p.e.pre[static_cast<long long>(m0 + r) * p.e.ldpre + n0 + c] = __ushort_as_bfloat16(0x7fc0);
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ void lin_raise(const Smem& sm, int* err) {
+    if (err) {
+        raise_abort(sm, err);
+    } else {
+        *sm.abort_flag = 1;
+        st_shared_cluster_u32(mapa_shared(smem_addr(const_cast<int*>(sm.abort_flag)), cluster_ctarank() ^ 1u), 1u);
+    }
+}
+
+template <int B_MN>
+__global__ void __launch_bounds__(WIDE_THREADS, 1)
+    flp_linear_kernel(const __grid_constant__ CUtensorMap tmA,    // x or d, K-major (64 x 128 boxes)
+                      const __grid_constant__ CUtensorMap tmB,    // W, K-major (64 x 128) or MN-major (64 x 64)
+                      const __grid_constant__ CUtensorMap tmY,    // y store boxes (128 rows x 64 bytes)
+                      const __grid_constant__ CUtensorMap tmPre,  // v, the same
+                      const __grid_constant__ LinParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const Smem sm = smem_layout(smem_raw);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = (rank == 0);
+    const int rofs = static_cast<int>(rank) * BM;
+    const int pair = blockIdx.x >> 1;
+    const int npairs = gridDim.x >> 1;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmY);
+        tma_prefetch_desc(&tmPre);
+    }
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const uint32_t tmem_base = pair_prologue(sm, warp);
+    griddep_wait();  // aligned copies, d and the cleared error word are complete from here on
+    const uint64_t limit = p.wait_limit_ns;
+    volatile int* abort_flag = sm.abort_flag;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true, stalled = false;
+            for (int u = pair; u < p.units && ok; u += npairs) {
+                const LinUnit t = lin_unit(p, u);
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (p.stall_after >= 0 && issued++ == p.stall_after) {
+                        ok = false, stalled = true;  // stop feeding the MMA
+                        break;
+                    }
+                    if (!mbar_wait(&sm.empty[stage], phase ^ 1u, limit, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader)
+                        mbar_arrive_expect_tx(&sm.full[stage], 2 * (A_STAGE_BYTES + t.halves * B_STAGE_BYTES));
+                    const uint32_t bar = mapa_shared(smem_addr(&sm.full[stage]), 0);
+                    uint8_t* b = sm.base + slot_b(true, stage);
+                    tma_load_2d_pair(sm.base + slot_a(true, stage), &tmA, kb * BK, t.m0 + rofs, bar);
+                    for (int h = 0; h < t.halves; ++h) {
+                        const int col = t.n0 + h * BN + rofs;
+                        if (B_MN == 0) {
+                            tma_load_2d_pair(b + h * B_STAGE_BYTES, &tmB, kb * BK, col, bar);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < BNH / 64; ++j)
+                                tma_load_2d_pair(b + h * B_STAGE_BYTES + j * 8192, &tmB, col + j * 64, kb * BK, bar);
+                        }
+                    }
+                    if (++stage == STAGES_W) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok && !stalled) lin_raise(sm, p.err);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------- MMA issuer (leader)
+        if (lane == 0 && leader) {
+            constexpr uint32_t idesc = idesc_bf16_f32(PM, BN, 0, B_MN);
+            uint32_t gk = 0;    // k-blocks consumed so far
+            uint32_t uses = 0;  // bit h: parity of the uses of accumulator h so far
+            bool ok = true;
+            auto issue = [&](uint32_t g, int h, bool first) {
+                const int s = static_cast<int>(g % STAGES_W);
+                const uint32_t a = smem_addr(sm.base + slot_a(true, s));
+                const uint32_t b = smem_addr(sm.base + slot_b(true, s)) + h * B_STAGE_BYTES;
+#pragma unroll
+                for (int k = 0; k < BK / UMMA_K; ++k)
+                    umma_bf16_pair(tmem_base + static_cast<uint32_t>(h * BN), operand_desc<0>(a, k),
+                                   operand_desc<B_MN>(b, k), idesc, (!first || k > 0) ? 1u : 0u);
+            };
+            auto wait_full = [&](uint32_t g) {
+                if (!mbar_wait(&sm.full[g % STAGES_W], (g / STAGES_W) & 1u, limit, abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            };
+            auto release = [&](uint32_t g) { umma_commit_pair_mc(&sm.empty[g % STAGES_W], PAIR_MASK); };
+            auto wait_tempty = [&](int h) {
+                if (!mbar_wait(&sm.tempty[h], ((uses >> h) & 1u) ^ 1u, limit, abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            };
+            auto publish = [&](int h) {
+                umma_commit_pair_mc(&sm.tfull[h], PAIR_MASK);
+                uses ^= 1u << h;
+            };
+            for (int u = pair; u < p.units && ok; u += npairs) {
+                const LinUnit t = lin_unit(p, u);
+                const int KB = t.kb1 - t.kb0;
+                ok = wait_tempty(0);
+                if (!ok) break;
+                if (t.halves == 1) {
+                    for (int kb = 0; kb < KB && ok; ++kb) {
+                        ok = wait_full(gk + kb);
+                        if (!ok) break;
+                        issue(gk + kb, 0, kb == 0);
+                        release(gk + kb);
+                    }
+                    if (ok) publish(0);
+                } else {
+                    // halves staggered at both ends of the tile: half 0 completes (and is
+                    // drained) under the last half-1 MMAs, and fills while the previous
+                    // tile's half 1 is still drained
+                    const int head = min(WIDE_EDGE, KB);
+                    const int tail0 = max(head, KB - WIDE_EDGE);
+                    for (int kb = 0; kb < head && ok; ++kb) {
+                        ok = wait_full(gk + kb);
+                        if (ok) issue(gk + kb, 0, kb == 0);
+                    }
+                    if (!ok) break;
+                    if (head == KB) publish(0);
+                    ok = wait_tempty(1);
+                    if (!ok) break;
+                    for (int kb = 0; kb < head; ++kb) {
+                        issue(gk + kb, 1, kb == 0);
+                        release(gk + kb);
+                    }
+                    for (int kb = head; kb < tail0 && ok; ++kb) {
+                        ok = wait_full(gk + kb);
+                        if (!ok) break;
+                        issue(gk + kb, 0, false);
+                        issue(gk + kb, 1, false);
+                        release(gk + kb);
+                    }
+                    for (int kb = tail0; kb < KB && ok; ++kb) {
+                        ok = wait_full(gk + kb);
+                        if (ok) issue(gk + kb, 0, false);
+                    }
+                    if (!ok) break;
+                    if (head < KB) publish(0);
+                    for (int kb = tail0; kb < KB; ++kb) {
+                        issue(gk + kb, 1, false);
+                        release(gk + kb);
+                    }
+                    publish(1);
+                }
+                gk += static_cast<uint32_t>(KB);
+            }
+            if (!ok) lin_raise(sm, p.err);
+            umma_commit_pair_mc(sm.drain, 0x1);  // every MMA issued so far has completed
+            volatile int no_abort = 0;
+            mbar_wait(sm.drain, 0, limit, &no_abort);
+        }
+    } else {
+        // ------------------------- epilogue: group g drains accumulator g
+        const int g = (warp - 2) >> 2;
+        const int et = threadIdx.x - 64 - g * EPI_THREADS;  // thread 0 issues the bulk stores
+        const int q = warp & 3;
+        const int r = q * 32 + lane;  // accumulator row == TMEM lane
+        const uint32_t tbase = tmem_base + static_cast<uint32_t>(g * BN) + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t tempty = mapa_shared(smem_addr(&sm.tempty[g]), 0);
+        const uint32_t bar_box = 1 + 2 * g, bar_vote = 2 + 2 * g;
+        uint8_t* box0 = sm.base + SMEM_STG + g * (2 * NBOX_BYTES);
+        // the warp's rows of the group's boxes, for rows that no bulk store can write (then
+        // none reads the boxes)
+        const uint32_t box_in = smem_addr(box0) + q * (32 * 64), box_out = box_in + NBOX_BYTES;
+        StoreRing ring;
+        uint32_t phase = 0;
+        bool ok = true;
+        int u = pair;
+        for (; u < p.units; u += npairs) {
+            const LinUnit t = lin_unit(p, u);
+            if (g >= t.halves) continue;
+            const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
+            // every thread of the group takes the same branch (the box barriers need all of them)
+            if (!named_bar_all(bar_vote, EPI_THREADS, ready)) {
+                ok = false;
+                break;
+            }
+            phase ^= 1u;
+            tc_fence_after();
+            const int m0 = t.m0 + rofs, n0 = t.n0 + g * BN;
+            const int row = m0 + r;
+            const int boxes = min(BN / 32, (p.N - n0 + 31) / 32);  // the others lie past the last column
+#pragma unroll 1
+            for (int b = 0; b < boxes; ++b) {
+                uint32_t raw[32];
+                tmem_ld_32x32b_x32(tbase + b * 32, raw);
+                tmem_wait_ld();
+                if (b == boxes - 1) {
+                    tc_fence_before();
+                    mbar_arrive_cluster(tempty);
+                }
+                if (t.part >= 0) {
+                    if (row < p.M) {
+                        float4* o = reinterpret_cast<float4*>(
+                            p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + g * BN + b * 32);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[i] = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]),
+                                               __uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3]));
+                    }
+                    continue;
+                }
+                const int c0 = n0 + b * 32;
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                lin_add_bias(p.e, c0, p.N, v);
+                uint32_t w[16];
+                if (p.e.pre) {
+                    lin_pack(v, w);
+                    if (p.e.vec)
+                        narrow_box_store(ring, box0, bar_box, et, r, w, &tmPre, c0, m0, false);
+                    else if (m0 + q * 32 < p.M)
+                        lin_rows_out(box_out, w, p.e.pre, p.e.ldpre, m0 + q * 32, p.M, c0, p.N);
+                }
+                if (p.e.act != LIN_NONE) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = lin_act(v[j], p.e.act);
+                }
+                if (p.e.residual) {
+                    if (p.e.vec) {
+                        const uint4* from = reinterpret_cast<const uint4*>(p.e.residual + row * p.e.ldr + c0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 x = row < p.M && c0 + 8 * i < p.N ? from[i] : make_uint4(0, 0, 0, 0);
+                            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+                        }
+                    } else if (m0 + q * 32 < p.M) {
+                        lin_rows_in(box_in, w, p.e.residual, p.e.ldr, m0 + q * 32, p.M, c0, p.N);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = 0;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[2 * j] += __uint_as_float(w[j] << 16);
+                        v[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+                    }
+                }
+                lin_pack(v, w);
+                if (p.e.vec)
+                    narrow_box_store(ring, box0, bar_box, et, r, w, &tmY, c0, m0, false);
+                else if (m0 + q * 32 < p.M)
+                    lin_rows_out(box_out, w, p.e.y, p.e.ldy, m0 + q * 32, p.M, c0, p.N);
+            }
+        }
+        if (!ok) lin_raise(sm, p.err);
+        if (et == 0) bulk_wait_group<0>();
+        if (!ok) {
+            named_bar_sync(bar_vote, EPI_THREADS);  // behind the group's earlier stores
+            lin_fill_nan(p, u, npairs, g, rofs, et);
+        }
+    }
+
+    pair_epilogue(sm, warp, tmem_base);
+}
+
+// Sums the partial tiles' splits in order and takes the result through the epilogue.  One
+// block per row of a tile; columns a warp apart, so that any alignment coalesces.
+constexpr int LJ_THREADS = 128;
+__global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __grid_constant__ LinParams p) {
+    const int tile = blockIdx.x / p.rows, r = blockIdx.x % p.rows;
+    const LinUnit t = lin_unit(p, p.whole + tile * p.splits);
+    griddep_wait();
+    const long long row = t.m0 + r;
+    if (row >= p.M) return;
+    const long long step = static_cast<long long>(p.rows) * (2 * BN);
+    const float* from = p.part + static_cast<long long>(tile) * p.splits * step + static_cast<long long>(r) * (2 * BN);
+    constexpr int C = 2 * BN / LJ_THREADS;
+    float v[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = 0.f;
+    bool on[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) on[i] = t.n0 + static_cast<int>(threadIdx.x) + i * LJ_THREADS < p.N;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (on[i]) v[i] += __ldcs(from + s * step + threadIdx.x + i * LJ_THREADS);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        if (!on[i]) continue;
+        const int c = t.n0 + static_cast<int>(threadIdx.x) + i * LJ_THREADS;
+        float x = v[i];
+        if (p.e.bias)
+            x += p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[c] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[c]);
+        if (p.e.pre) p.e.pre[row * p.e.ldpre + c] = __float2bfloat16_rn(x);
+        x = lin_act(x, p.e.act);
+        if (p.e.residual) x += __bfloat162float(p.e.residual[row * p.e.ldr + c]);
+        p.e.y[row * p.e.ldy + c] = __float2bfloat16_rn(x);
+    }
+}
+
+// ------------------------------------------------------------------ d and db
+
+struct LinGradParams {
+    const bf16* dy;
+    long long lddy;
+    const bf16* pre;  // or null: no activation
+    long long ldpre;
+    int act;
+    int M, N;
+    bf16* d;  // [M, Np], or null: not written
+    int Np;
+    float* part;  // [row blocks][N]: column sums, or null
+    int rows;     // of a row block
+};
+
+constexpr int LG_THREADS = 256;
+constexpr int LG_WARPS = LG_THREADS / 32;
+constexpr int LG_ROWS = 4;  // rows a warp has under way
+
+// 256 columns x `rows` rows a block, a row at a time a warp.
+template <bool LOOSE>
+__global__ void __launch_bounds__(LG_THREADS) flp_linear_grad_kernel(const __grid_constant__ LinGradParams p) {
+    constexpr int P = 4;
+    __shared__ __align__(16) uint8_t words[LOOSE ? LG_WARPS * WARP_WORDS_BYTES : 16];
+    __shared__ float sums[LG_WARPS][256];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage = smem_addr(words) + (LOOSE ? warp * WARP_WORDS_BYTES : 0);
+    const int col = blockIdx.x * 256 + lane * 8, left = p.N - col;
+    const int first = blockIdx.y * p.rows, last = min(p.M, first + p.rows);
+    griddep_launch_dependents();
+    const Extent all_dy = extent_of<bf16>(p.dy, p.M, p.lddy, p.N), all_pre = extent_of<bf16>(p.pre, p.M, p.ldpre, p.N);
+    uint64_t sum[P] = {0, 0, 0, 0};
+    for (int r0 = first + warp; r0 < last; r0 += LG_WARPS * LG_ROWS) {
+        uint32_t a[LG_ROWS][WarpWords<bf16>::N], b[LG_ROWS][WarpWords<bf16>::N];
+        auto fetch = [&](uint32_t(&x)[WarpWords<bf16>::N], const bf16* src, bool on, bool edge, const Extent& all) {
+            if constexpr (LOOSE) {
+                load_words<bf16>(x, src, on ? left : -256, edge, all);
+            } else {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (on && left > 0) u = __ldcs(reinterpret_cast<const uint4*>(src));
+                x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+            }
+        };
+        auto value = [&](const uint32_t(&x)[WarpWords<bf16>::N], const bf16* src) {
+            if constexpr (LOOSE)
+                return settle_words<bf16>(x, src, left, stage);
+            else
+                return make_uint4(x[0], x[1], x[2], x[3]);
+        };
+#pragma unroll
+        for (int i = 0; i < LG_ROWS; ++i) {
+            const int r = r0 + i * LG_WARPS;
+            const bool on = r < last, edge = r == 0 || r == p.M - 1;
+            fetch(a[i], p.dy + r * p.lddy + col, on, edge, all_dy);
+            if (p.pre) fetch(b[i], p.pre + r * p.ldpre + col, on, edge, all_pre);
+        }
+#pragma unroll
+        for (int i = 0; i < LG_ROWS; ++i) {
+            const int r = r0 + i * LG_WARPS;
+            if (r >= last) break;  // the whole warp
+            const uint4 u = value(a[i], p.dy + r * p.lddy + col);
+            uint64_t d[P];
+#pragma unroll
+            for (int j = 0; j < P; ++j) d[j] = Pairs<bf16>::get(u, j);
+            if (p.pre) {
+                const uint4 x = value(b[i], p.pre + r * p.ldpre + col);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    float lo, hi;
+                    f2_unpack(Pairs<bf16>::get(x, j), lo, hi);
+                    d[j] = f2_mul(d[j], f2_pack(lin_slope(lo, p.act), lin_slope(hi, p.act)));
+                }
+            }
+            if (p.d) st_global_16(p.d + static_cast<long long>(r) * p.Np + col, Pairs<bf16>::put(d), left > 0);
+#pragma unroll
+            for (int j = 0; j < P; ++j) sum[j] = f2_add(sum[j], d[j]);
+        }
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int j = 0; j < P; ++j) f2_unpack(sum[j], sums[warp][lane * 8 + 2 * j], sums[warp][lane * 8 + 2 * j + 1]);
+    __syncthreads();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= p.N) return;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < LG_WARPS; ++w) s += sums[w][threadIdx.x];
+    p.part[static_cast<long long>(blockIdx.y) * p.N + c] = s;
+}
+
+// db from the row blocks' sums, in order.
+constexpr int LB_WAYS = 32;
+__global__ void __launch_bounds__(32 * LB_WAYS) flp_linear_bias_join_kernel(const float* part, int blocks, int N, float* db) {
+    __shared__ float sums[LB_WAYS][33];
+    const int lane = threadIdx.x & 31, way = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    griddep_launch_dependents();
+    griddep_wait();
+    float s = 0.f;
+    if (c < N)
+        for (int b = way; b < blocks; b += LB_WAYS) s += part[static_cast<long long>(b) * N + c];
+    sums[way][lane] = s;
+    __syncthreads();
+    if (way == 0 && c < N) {
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < LB_WAYS; ++w) s += sums[w][lane];
+        db[c] = s;
+    }
+}
+
+}  // namespace flp

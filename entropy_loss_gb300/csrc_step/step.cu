@@ -171,7 +171,9 @@ struct WgradPlan {
 // of runs that costs least, in the time of a 64-row block of a tile (0.54 us):
 // the blocks of a run, and for joining 5 (a launch) and a quarter per partial
 // tile (512 KiB written and read back).
-WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t K, int dw_dtype, int pairs) {
+// `unpack`: X^ comes from a checkpoint and lies in the workspace.
+WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t K, int dw_dtype, int pairs,
+                     bool unpack = true) {
     WgradPlan w{};
     pairs = std::max(1, pairs);
     w.Kp = ck_cols(K);
@@ -204,7 +206,7 @@ WgradPlan plan_wgrad(const void* dY, int64_t lddy, int64_t M, int64_t N, int64_t
     w.rest = static_cast<int>(rest);
     w.units = w.whole + w.rest * w.splits;
     w.off_x = kHeaderBytes;
-    w.off_y = w.off_x + align_up(static_cast<size_t>(std::max<int64_t>(M, 1)) * w.Kp * 2, 1024);
+    w.off_y = w.off_x + (unpack ? align_up(static_cast<size_t>(std::max<int64_t>(M, 1)) * w.Kp * 2, 1024) : 0);
     w.off_part = w.off_y + align_up(static_cast<size_t>(M) * w.Np * 2, 1024);
     w.bytes = w.off_part + static_cast<size_t>(w.rest) * w.splits * PM * 2 * BN * 4;
     return w;
@@ -221,6 +223,12 @@ flp_status wgrad_checks(const void* dY, int64_t lddy, int64_t M, int64_t N, int6
     return FLP_OK;
 }
 
+// Equal runs of at most WGRAD_RUN blocks.
+int wgrad_run(int64_t M) {
+    const int64_t KB = cdiv(M, BK);
+    return static_cast<int>(cdiv(KB, cdiv(KB, WGRAD_RUN)));
+}
+
 // The contraction's shared memory, once per device.
 flp_status wgrad_attrs() {
     static bool done[kMaxDevices] = {};
@@ -234,17 +242,16 @@ flp_status wgrad_attrs() {
     return FLP_OK;
 }
 
-// The contraction and the join, dY (pitch ldy) and X^ (in the workspace) being there.
-flp_status wgrad_contract(const WgradPlan& w, const void* y, int64_t ldy, uint8_t* ws, int64_t M, int64_t N, int64_t K,
-                          void* dW, int dw_dtype, int accumulate, int pairs, int run, unsigned long long wait_limit_ns,
-                          int stall_after, cudaStream_t s) {
+// The contraction and the join, dY (pitch ldy) and X^ (cols columns, pitch ldx) being there.
+flp_status wgrad_contract(const WgradPlan& w, const void* y, int64_t ldy, const void* x, int64_t cols, int64_t ldx,
+                          uint8_t* ws, int64_t M, int64_t N, int64_t K, void* dW, int dw_dtype, int accumulate, int pairs,
+                          int run, unsigned long long wait_limit_ns, int stall_after, bool after_kernel, cudaStream_t s) {
     flp_status st;
     const int64_t es = elem(dw_dtype);
     const bool b16 = dw_dtype == FLP_BF16;
     CUtensorMap my, mx, mw, mp;
     if ((st = tmap_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, N, M, ldy * 2, 64, 64)) != FLP_OK) return st;
-    if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ws + w.off_x, w.Kp, M, w.Kp * 2, 64, 64)) != FLP_OK)
-        return st;
+    if ((st = tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, cols, M, ldx * 2, 64, 64)) != FLP_OK) return st;
     const size_t part_rows = static_cast<size_t>(w.rest) * w.splits * PM;
     // without split tiles (or without whole ones) one of the two output maps is
     // not used: it repeats the other
@@ -275,7 +282,7 @@ flp_status wgrad_contract(const WgradPlan& w, const void* y, int64_t ldy, uint8_
     p.wait_limit_ns = wait_limit_ns;
     p.stall_after = stall_after;
     const int grid = 2 * static_cast<int>(std::min<int64_t>(w.units, pairs));
-    st = launch_pairs_n(flp_wgrad_kernel, grid, WIDE_THREADS, s, "flp_wgrad_kernel launch", true, my, mx, mw, mp, p, dW);
+    st = launch_pairs_n(flp_wgrad_kernel, grid, WIDE_THREADS, s, "flp_wgrad_kernel launch", after_kernel, my, mx, mw, mp, p, dW);
     if (st != FLP_OK || !w.rest) return st;
     WgradJoinParams j{};
     j.part = reinterpret_cast<const float*>(ws + w.off_part);
@@ -411,6 +418,39 @@ flp_status balance_checks(int64_t T, int64_t E, int64_t top_k) {
 }
 
 }  // namespace
+
+// ------------------------------------------------- for the library's other units
+
+flp_status flp::align_rows(const void* src, int64_t ld, int64_t M, int64_t H, void* dst, int64_t Hp, cudaStream_t s) {
+    CkParams a{};
+    a.x = const_cast<void*>(src);
+    a.ldx = ld;
+    a.q = static_cast<uint8_t*>(dst);
+    a.M = M;
+    a.H = static_cast<int>(H);
+    a.Hp = static_cast<int>(Hp);
+    int64_t grid = 0;
+    const flp_status st = ck_places(a, 8, true, CK_PACK_N, &grid);
+    if (st != FLP_OK) return st;
+    return launch_step(flp_align_rows_kernel, grid, CK_THREADS, 0, s, "flp_align_rows_kernel launch", false, a);
+}
+
+flp_status flp::weight_grad_checks(int64_t M, int64_t N, int64_t K, int dw_dtype) {
+    return wgrad_checks(nullptr, N, M, N, K, dw_dtype);
+}
+
+size_t flp::weight_grad_bytes(int64_t M, int64_t N, int64_t K, int dw_dtype, int pairs) {
+    return plan_wgrad(nullptr, cdiv(N, 8) * 8, M, N, K, dw_dtype, pairs, false).bytes;
+}
+
+flp_status flp::weight_grad(const void* dY, int64_t ldy, const void* X, int64_t ldx, int64_t M, int64_t N, int64_t K,
+                            void* dW, int dw_dtype, uint8_t* ws, int pairs, bool after_kernel, cudaStream_t s) {
+    const flp_status st = wgrad_attrs();
+    if (st != FLP_OK) return st;
+    const WgradPlan w = plan_wgrad(dY, ldy, M, N, K, dw_dtype, pairs, false);
+    return wgrad_contract(w, dY, ldy, X, K, ldx, ws, M, N, K, dW, dw_dtype, 0, pairs, wgrad_run(M), kWaitLimitNs, -1,
+                          after_kernel, s);
+}
 
 // =================================================================== C ABI
 
@@ -645,22 +685,11 @@ extern "C" flp_status flp_checkpoint_weight_grad(const void* dY, int64_t lddy, c
     if (w.Np) {
         y = ws + w.off_y;
         ldy = w.Np;
-        CkParams a{};
-        a.x = const_cast<void*>(dY);
-        a.ldx = lddy;
-        a.q = ws + w.off_y;
-        a.M = M;
-        a.H = static_cast<int>(N);
-        a.Hp = static_cast<int>(w.Np);
-        int64_t grid = 0;
-        if ((st = ck_places(a, 8, true, CK_PACK_N, &grid)) != FLP_OK) return st;
-        st = launch_step(flp_align_rows_kernel, grid, CK_THREADS, 0, s, "flp_align_rows_kernel launch", false, a);
-        if (st != FLP_OK) return st;
+        if ((st = align_rows(dY, lddy, M, N, ws + w.off_y, w.Np, s)) != FLP_OK) return st;
     }
-    const int KB = static_cast<int>(cdiv(M, BK));
-    // equal runs of at most WGRAD_RUN blocks
-    const int run = static_cast<int>(cdiv(KB, cdiv(KB, WGRAD_RUN)));
-    return wgrad_contract(w, y, ldy, ws, M, N, K, dW, dW_dtype, accumulate_dW, d->pairs, run, kWaitLimitNs, -1, s);
+    const int run = wgrad_run(M);
+    return wgrad_contract(w, y, ldy, ws + w.off_x, w.Kp, w.Kp, ws, M, N, K, dW, dW_dtype, accumulate_dW, d->pairs, run,
+                          kWaitLimitNs, -1, true, s);
 }
 
 extern "C" flp_status flp_selftest_weight_grad_timeout(void* workspace, size_t workspace_bytes, int odd, int stall_after,
@@ -685,8 +714,8 @@ extern "C" flp_status flp_selftest_weight_grad_timeout(void* workspace, size_t w
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     FLP_CUDA(cudaMemsetAsync(ws, 0, off_dy + M * N * 2, s));  // error word, X^, partial tiles, dY
     FLP_CUDA(cudaMemsetAsync(dw, 0x3f, N * K * 4, s));        // what the result has to replace
-    st = wgrad_contract(w, ws + off_dy, N, ws, M, N, K, dw, FLP_F32, 0, 1, 1, static_cast<unsigned long long>(wait_limit_ns),
-                        stall_after < 0 ? -1 : stall_after, s);
+    st = wgrad_contract(w, ws + off_dy, N, ws + w.off_x, w.Kp, w.Kp, ws, M, N, K, dw, FLP_F32, 0, 1, 1,
+                        static_cast<unsigned long long>(wait_limit_ns), stall_after < 0 ? -1 : stall_after, true, s);
     return st == FLP_OK ? flp_get_error(workspace, stream) : st;
 }
 

@@ -36,7 +36,8 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_checkpoint_weight_grad_workspace", "flp_checkpoint_weight_grad", "flp_selftest_weight_grad_timeout",
            "flp_balance_loss_workspace", "flp_balance_loss", "flp_balance_loss_ex", "flp_expert_sort_workspace",
            "flp_expert_sort", "flp_expert_gather", "flp_expert_combine", "flp_expert_combine_backward",
-           "flp_token_logprob", "flp_token_logprob_backward")
+           "flp_token_logprob", "flp_token_logprob_backward", "flp_linear_workspace", "flp_linear",
+           "flp_linear_backward_workspace", "flp_linear_backward", "flp_selftest_linear_timeout")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
 FLP_LOSS_NLL_SUM = 3
@@ -48,6 +49,8 @@ FLP_AGG_SUM_OVER = 2
 SELFTEST_WORKSPACE_BYTES = 1 << 20
 SELFTEST_WEIGHT_GRAD_BYTES = 3 << 20
 SELFTEST_WEIGHT_GRAD_OUTPUT_OFFSET = 2 << 20
+SELFTEST_LINEAR_BYTES = 4 << 20
+SELFTEST_LINEAR_OUTPUT_OFFSET = 3 << 20
 SELFTEST_OUTPUT_OFFSET = 768 << 10  # the forward self-test's logprob, lse, entropy (fp32 [256] each)
 STATIC_SCRATCH_BYTES = 16 << 20
 FLP_BWD_AUTO = 0
@@ -135,7 +138,13 @@ def load(path: str = LIB_PATH):
             ("flp_expert_combine", [p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p]),
             ("flp_expert_combine_backward", [p, i64, p, i64, i32, p, i32, i64, i64, i64, p, p, p, i64, p, p]),
             ("flp_token_logprob", [p, i64, i32, p, i64, i64, i64, f32, p, p, p, i64, p, p, p]),
-            ("flp_token_logprob_backward", [p, i64, i32, p, i64, i64, i64, f32, p, p, p, p, p, i64, p])):
+            ("flp_token_logprob_backward", [p, i64, i32, p, i64, i64, i64, f32, p, p, p, p, p, i64, p]),
+            ("flp_linear_workspace", [p, i64, p, i64, i64, i64, i64, size]),
+            ("flp_linear", [p, i64, p, i64, p, i32, i32, p, i64, i64, i64, i64, p, i64, p, i64, p, ctypes.c_size_t, p]),
+            ("flp_linear_backward_workspace", [p, i64, p, i64, p, i64, i32, i32, i32, i32, i64, i64, i64, i32, size]),
+            ("flp_linear_backward", [p, i64, p, i64, p, i64, p, i64, i32, i64, i64, i64, p, i64, p, i32, p, p, ctypes.c_size_t,
+                                     p]),
+            ("flp_selftest_linear_timeout", [p, ctypes.c_size_t, i32, i32, i64, p])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32
     lib.flp_get_error.argtypes = [p, p]
@@ -394,6 +403,16 @@ def selftest_weight_grad_timeout(odd: bool, stall_after: int, wait_limit_ns: int
         workspace = torch.empty(SELFTEST_WEIGHT_GRAD_BYTES, dtype=torch.uint8, device="cuda")
     return int(load().flp_selftest_weight_grad_timeout(_ptr(workspace), _nbytes(workspace), int(bool(odd)), stall_after,
                                                        wait_limit_ns, _stream(stream)))
+
+
+def selftest_linear_timeout(split: bool, stall_after: int, wait_limit_ns: int, workspace=None, stream=None) -> int:
+    """Run a small linear layer with its producers stopped after `stall_after`
+    64-deep blocks (< 0: no stall) and every wait bounded by `wait_limit_ns`; with
+    `split` through partial tiles.  Returns the error status the run leaves."""
+    if workspace is None:
+        workspace = torch.empty(SELFTEST_LINEAR_BYTES, dtype=torch.uint8, device="cuda")
+    return int(load().flp_selftest_linear_timeout(_ptr(workspace), _nbytes(workspace), int(bool(split)), stall_after,
+                                                  wait_limit_ns, _stream(stream)))
 
 
 def loss(logprob, y, kind=FLP_LOSS_NLL_MEAN, *, ignore_index: int = -100, old_logprob=None,
@@ -882,6 +901,110 @@ def expert_combine_backward(dy, ys, order: ExpertOrder, weights=None, *, out=Non
     return out, dweights
 
 
+ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(name) -> int:
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {name!r}")
+    return code
+
+
+def _linear_weight(x, W):
+    """(address and pitch of x, of W, M, N, K, device) of bf16 x [M, K] and W [N, K]."""
+    xp, ldx = _rows(x, "x", dtype=torch.bfloat16)
+    wp, ldw = _rows(W, "W", dtype=torch.bfloat16)
+    dev = x.device
+    _on(W, dev, "W")
+    (M, K), (N, Kw) = x.shape, W.shape
+    if K != Kw:
+        raise ValueError(f"x has {K} columns, W {Kw}")
+    return xp, ldx, wp, ldw, M, N, K, dev
+
+
+def linear(x, W, bias=None, *, activation=None, residual=None, keep: bool = False, out=None, workspace=None, stream=None):
+    """act(x W^T + bias) + residual for bf16 x [M, K], W [N, K] and residual [M, N],
+    bias [N] in bf16 or fp32, activation None, "relu", "gelu", "gelu_tanh" or "silu".
+    With `keep`: (y, the activation's argument in bf16, for linear_backward).  out
+    may be the residual itself."""
+    if stream is not None:
+        return _on_stream(stream, linear, x, W, bias, activation=activation, residual=residual, keep=keep, out=out,
+                          workspace=workspace)
+    act = _activation(activation)
+    xp, ldx, wp, ldw, M, N, K, dev = _linear_weight(x, W)
+    bp, bt = _norm_param(bias, N, torch.bfloat16, "bias")
+    if bias is not None:
+        _on(bias, dev, "bias")
+    rp, ldr = None, 0
+    if residual is not None:
+        rp, ldr = _rows(residual, "residual", (M, N), torch.bfloat16)
+        _on(residual, dev, "residual")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        yp, ldy = out.data_ptr(), N
+    else:
+        yp, ldy = _rows(out, "out", (M, N), torch.bfloat16)
+        _on(out, dev, "out")
+    pp = None
+    if keep:
+        pre = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        pp = pre.data_ptr()
+    device = dev.index
+    # of the addresses only their alignment matters
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+                                   _workspace_bytes("flp_linear_workspace", device, xp % 16, ldx, wp % 16, ldw, M, N, K))
+    status = load().flp_linear(xp, ldx, wp, ldw, bp, FLP_F32 if bt is None else bt, act, rp, ldr, M, N, K, yp, ldy, pp, N,
+                               ws, ws_bytes, _raw_stream(device))
+    if status:
+        _check(status, "flp_linear")
+    return (out, pre) if keep else out
+
+
+def linear_backward(dy, x, W, pre=None, *, activation=None, dw_dtype=torch.float32, want_dx: bool = True, want_dW: bool = True,
+                    want_dbias: bool = True, dx=None, workspace=None, stream=None):
+    """(dx, dW, dbias) of linear, each None where it is not wanted: dx bf16 [M, K], dW
+    [N, K] in dw_dtype, dbias fp32 [N].  pre is what linear kept (activation None:
+    not needed).  The residual's gradient is dy itself."""
+    if stream is not None:
+        return _on_stream(stream, linear_backward, dy, x, W, pre, activation=activation, dw_dtype=dw_dtype, want_dx=want_dx,
+                          want_dW=want_dW, want_dbias=want_dbias, dx=dx, workspace=workspace)
+    act = _activation(activation)
+    xp, ldx, wp, ldw, M, N, K, dev = _linear_weight(x, W)
+    dyp, lddy = _rows(dy, "dy", (M, N), torch.bfloat16)
+    _on(dy, dev, "dy")
+    pp, ldp = None, 0
+    if act:
+        if pre is None:
+            raise ValueError("the gradient of an activation needs pre")
+        pp, ldp = _rows(pre, "pre", (M, N), torch.bfloat16)
+        _on(pre, dev, "pre")
+    if dw_dtype not in _DTYPE:
+        raise ValueError(f"dw_dtype: expected bf16 or fp32, got {dw_dtype}")
+    dxp, lddx = None, 0
+    if want_dx:
+        if dx is None:
+            dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+            dxp, lddx = dx.data_ptr(), K
+        else:
+            dxp, lddx = _rows(dx, "dx", (M, K), torch.bfloat16)
+            _on(dx, dev, "dx")
+    else:
+        dx = None
+    dW = torch.empty((N, K), dtype=dw_dtype, device=dev) if want_dW else None
+    dbias = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
+    device, code = dev.index, _DTYPE[dw_dtype]
+    ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
+                                   _workspace_bytes("flp_linear_backward_workspace", device, dyp % 16, lddy, xp % 16, ldx, wp % 16,
+                                                    ldw, act, want_dx, want_dW, want_dbias, M, N, K, code))
+    status = load().flp_linear_backward(dyp, lddy, xp, ldx, wp, ldw, pp, ldp, act, M, N, K, dxp, lddx,
+                                        dW.data_ptr() if want_dW else None, code, dbias.data_ptr() if want_dbias else None,
+                                        ws, ws_bytes, _raw_stream(device))
+    if status:
+        _check(status, "flp_linear_backward")
+    return dx, dW, dbias
+
+
 def _row_values(t, M, dev, name, dtype=torch.float32):
     """Address of a value per row: contiguous [M] on `dev`, or None."""
     if t is None:
@@ -1172,3 +1295,33 @@ def fused_token_logprob(logits, y, top: int = 0, scale: float = 1.0, ignore_inde
     """Differentiable (logprob, entropy or None, top log-probabilities or None, their
     columns or None) of token_logprob; gradients flow through the first two."""
     return FusedTokenLogprob.apply(logits, y, top, scale, ignore_index, compute_entropy)
+
+
+class FusedLinear(torch.autograd.Function):
+    """autograd wrapper of linear."""
+
+    @staticmethod
+    def forward(ctx, x, W, bias, residual, activation, recorded):
+        want_x, want_W, want_b, _, _, _ = ctx.needs_input_grad
+        keep = recorded and activation is not None and (want_x or want_W or want_b)
+        y = linear(x, W, bias, activation=activation, residual=residual, keep=keep)
+        y, pre = y if keep else (y, None)
+        ctx.save_for_backward(x, W, bias, pre)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, W, bias, pre = ctx.saved_tensors
+        want_x, want_W, want_b, want_r, _, _ = ctx.needs_input_grad
+        dx = dW = db = None
+        if want_x or want_W or want_b:
+            dx, dW, db = _once(lambda: linear_backward(dy.contiguous(), x, W, pre, activation=ctx.activation, dw_dtype=W.dtype,
+                                                       want_dx=want_x, want_dW=want_W, want_dbias=want_b),
+                               dy, x, W, *(() if bias is None else (bias,)))
+        return dx, dW, db.to(bias.dtype) if want_b else None, dy if want_r else None, None, None
+
+
+def fused_linear(x, W, bias=None, activation=None, residual=None):
+    """Differentiable act(x W^T + bias) + residual for bf16 x [M, K], W [N, K]."""
+    return FusedLinear.apply(x, W, bias, residual, activation, torch.is_grad_enabled())

@@ -607,6 +607,60 @@ flp_status flp_token_logprob_backward(const void* logits, int64_t ld, int dtype,
                                       const float* entropy, const float* grad_logprob, const float* grad_entropy,
                                       void* dlogits, int64_t lddl, void* stream);
 
+/*
+ * Linear layer with its epilogue, bf16 x [M, K], W [N, K] and y [M, N] (rows at
+ * any pitch and alignment; rows of X or W that are not aligned to 16 bytes are
+ * copied to the workspace first):
+ *   v = x W^T + bias,   y = act(v) + residual
+ * in fp32 up to one rounding.  bias: [N], bf16 or fp32 (bias_dtype), or NULL;
+ * residual: [M, N] bf16, or NULL (Y may be the residual itself); pre: v rounded
+ * to bf16, for the backward pass, or NULL.  Activations: relu, gelu (v Phi(v)),
+ * gelu_tanh (v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))), silu
+ * (v sigmoid(v)).  The workspace query takes X and W for their alignment only and
+ * may say 0.  A kernel's bounded wait that runs out leaves NaN in every tile of
+ * the outputs that was not finished.
+ */
+typedef enum { FLP_ACT_NONE = 0, FLP_ACT_RELU = 1, FLP_ACT_GELU = 2, FLP_ACT_GELU_TANH = 3, FLP_ACT_SILU = 4 } flp_activation;
+flp_status flp_linear_workspace(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                                size_t* bytes);
+flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, const void* bias, int bias_dtype,
+                      int activation, const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K, void* Y,
+                      int64_t ldy, void* pre, int64_t ldpre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, with d = dY act'(pre) (pre as the forward kept it; not read
+ * without an activation; relu' is 1 for v > 0 and else 0):
+ *   dX = d W (bf16),   dW [N, K] = d^T X (fp32 or bf16, contiguous, 16-byte
+ *   aligned),   dbias [N] = column sums of d (fp32)
+ * d enters the two products rounded to bf16 and dbias unrounded.  Each output may
+ * be NULL: it is not computed, and X (for dW) or W (for dX) is not read.  The
+ * residual's gradient is dY.  M == 0 writes zeros to dW and dbias.  The
+ * workspace's first word is the error word of flp_get_error (FLP_ERR_TIMEOUT);
+ * after a timeout what was not finished is NaN.
+ */
+flp_status flp_linear_backward_workspace(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                         int activation, int want_dX, int want_dW, int want_dbias, int64_t M, int64_t N,
+                                         int64_t K, int dW_dtype, size_t* bytes);
+flp_status flp_linear_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                               const void* pre, int64_t ldpre, int activation, int64_t M, int64_t N, int64_t K, void* dX,
+                               int64_t lddx, void* dW, int dW_dtype, float* dbias, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Self-test of the product's bounded waits, like flp_selftest_wait_timeout (a
+ * diagnostic): M = 192, N = 520, K = 192 (two tiles of three 64-deep blocks), all
+ * zeros, on one CTA pair, laid out in `workspace` (at least
+ * FLP_SELFTEST_LINEAR_BYTES); with split != 0 through partial tiles of one block.
+ * With stall_after >= 0 the TMA producers stop after that many blocks.  y, bf16
+ * [M, N], is left at byte offset FLP_SELFTEST_LINEAR_OUTPUT_OFFSET: zeros, or NaN
+ * where the stall kept a tile from being finished.  Synchronises `stream` and
+ * returns the error word (FLP_ERR_TIMEOUT or FLP_OK), or an argument / CUDA error.
+ */
+#define FLP_SELFTEST_LINEAR_BYTES (4u << 20)
+#define FLP_SELFTEST_LINEAR_OUTPUT_OFFSET (3u << 20)
+flp_status flp_selftest_linear_timeout(void* workspace, size_t workspace_bytes, int split, int stall_after,
+                                       int64_t wait_limit_ns, void* stream);
+
 /* Static description of a status code. */
 const char* flp_status_string(flp_status status);
 

@@ -105,6 +105,48 @@ def test_token_logprob_backward(flp, b):
     assert call(M=0, x=None, y=None, lse=None, dx=None) == flp.FLP_OK
 
 
+def test_linear(flp, b):
+    def call(**o):
+        a = dict(x=b, ldx=64, w=b, ldw=64, bias=b, bt=1, act=2, r=b, ldr=32, M=4, N=32, K=64, y=b, ldy=32, pre=b, ldp=32)
+        a.update(o)
+        return flp.load().flp_linear(a["x"], a["ldx"], a["w"], a["ldw"], a["bias"], a["bt"], a["act"], a["r"], a["ldr"], a["M"], a["N"],
+                                     a["K"], a["y"], a["ldy"], a["pre"], a["ldp"], b, 8192, None)
+
+    for o in (dict(M=-1), dict(N=0), dict(K=0), dict(x=None), dict(w=None), dict(y=None), dict(ldx=63), dict(ldw=63), dict(ldy=31),
+              dict(ldr=31), dict(ldp=31), dict(x=b + 1), dict(w=b + 1), dict(y=b + 1), dict(r=b + 1), dict(pre=b + 1), dict(act=5),
+              dict(act=-1), dict(bt=2), dict(bias=b + 2, bt=0), dict(bias=b + 1)):
+        assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
+    for o in (dict(M=2 ** 31), dict(K=2 ** 31, ldx=2 ** 31, ldw=2 ** 31), dict(N=2 ** 31), dict(M=2 ** 28, N=2 ** 24)):
+        assert call(**o) == flp.FLP_ERR_UNSUPPORTED, o
+    assert call(M=0, x=None, y=None) == flp.FLP_OK
+    assert flp.load().flp_linear_workspace(b, 64, b, 64, 4, 32, 64, None) == flp.FLP_ERR_INVALID_ARG
+
+
+def test_linear_backward(flp, b):
+    def call(**o):
+        a = dict(dy=b, lddy=32, x=b, ldx=64, w=b, ldw=64, pre=b, ldp=32, act=2, M=4, N=32, K=64, dx=b, lddx=64, dw=b, dwt=0, db=b)
+        a.update(o)
+        return flp.load().flp_linear_backward(a["dy"], a["lddy"], a["x"], a["ldx"], a["w"], a["ldw"], a["pre"], a["ldp"], a["act"],
+                                              a["M"], a["N"], a["K"], a["dx"], a["lddx"], a["dw"], a["dwt"], a["db"], b, 8192, None)
+
+    for o in (dict(M=-1), dict(N=0), dict(K=0), dict(dy=None), dict(x=None), dict(w=None), dict(pre=None), dict(lddy=31), dict(ldx=63),
+              dict(ldw=63), dict(ldp=31), dict(lddx=63), dict(dy=b + 1), dict(x=b + 1), dict(w=b + 1), dict(pre=b + 1), dict(dx=b + 1),
+              dict(dw=b + 4), dict(db=b + 2), dict(act=9), dict(dwt=3)):
+        assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
+    assert call(M=2 ** 31) == flp.FLP_ERR_UNSUPPORTED
+    assert call(dx=None, dw=None, db=None, x=None, w=None) == flp.FLP_OK
+    assert flp.load().flp_linear_backward_workspace(b, 32, b, 64, b, 64, 2, 1, 1, 1, 4, 32, 64, 0, None) == flp.FLP_ERR_INVALID_ARG
+
+
+def test_linear_selftest(flp, b):
+    f = flp.load().flp_selftest_linear_timeout
+    assert f(None, 1 << 30, 0, 1, 1000, None) == flp.FLP_ERR_WORKSPACE
+    assert f(b, 8192, 0, 1, 1000, None) == flp.FLP_ERR_WORKSPACE
+    assert f(b + 4, 1 << 30, 0, 1, 1000, None) == flp.FLP_ERR_WORKSPACE
+    for limit in (0, -5, 61 * 10 ** 9):
+        assert f(b, 1 << 30, 0, 1, limit, None) == flp.FLP_ERR_INVALID_ARG
+
+
 def test_binding_refuses_before_loading_anything_on_a_device(flp):
     import torch
     x = torch.zeros(4, 64)
@@ -113,6 +155,8 @@ def test_binding_refuses_before_loading_anything_on_a_device(flp):
     for f in (lambda: flp.expert_sort(torch.zeros(4, 2, dtype=torch.int64), 2), lambda: flp.expert_sort(torch.zeros(4), 2),
               lambda: flp.expert_gather(x, order), lambda: flp.expert_combine(x, order),
               lambda: flp.expert_combine_backward(x, x, order), lambda: flp.token_logprob(x, x[:, 0].long()),
-              lambda: flp.token_logprob_backward(x, x[:, 0].long(), x[:, 0], None, None)):
+              lambda: flp.token_logprob_backward(x, x[:, 0].long(), x[:, 0], None, None),
+              lambda: flp.linear(x.bfloat16(), x.bfloat16()), lambda: flp.linear(x, x, activation="tanh"),
+              lambda: flp.linear_backward(x, x, x)):
         with pytest.raises(ValueError):
             f()
