@@ -74,12 +74,7 @@ __device__ __forceinline__ float key_value(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
-// The larger of two, NaN if either is; and the largest over a row's lanes.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float m;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-    return m;
-}
+// The largest over a row's lanes, NaN if one is.
 template <int L>
 __device__ __forceinline__ float group_max_nan(float v) {
     if constexpr (L == 32) {
@@ -108,12 +103,6 @@ __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // Expert i of lane l.

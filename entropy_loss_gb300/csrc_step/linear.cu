@@ -56,8 +56,14 @@ flp_status linear_attrs() {
     FLP_CUDA(cudaGetDevice(&dev));  // in range: check_device has run
     std::lock_guard<std::mutex> lk(g_mu);
     if (!done[dev]) {
-        FLP_CUDA(cudaFuncSetAttribute(flp_linear_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
-        FLP_CUDA(cudaFuncSetAttribute(flp_linear_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        FLP_CUDA(cudaFuncSetAttribute(flp_linear_kernel<1, LIN_NONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        for (int act = LIN_NONE; act <= LIN_SILU; ++act) {
+            const cudaError_t e = lin_with_act(act, [](auto a) {
+                return cudaFuncSetAttribute(flp_linear_kernel<0, decltype(a)::value>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            SMEM_ALLOC);
+            });
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        }
         done[dev] = true;
     }
     return FLP_OK;
@@ -94,11 +100,34 @@ flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const vo
     p.wait_limit_ns = wait_limit_ns;
     p.stall_after = stall_after;
     const int grid = 2 * static_cast<int>(std::min<int64_t>(l.units, pairs));
-    st = launch_pairs_n(w_mn ? flp_linear_kernel<1> : flp_linear_kernel<0>, grid, WIDE_THREADS, s, "flp_linear_kernel launch",
-                        after_kernel, ma, mb, my, mp, p);
+    auto go = [&](auto* kernel) {
+        return launch_pairs_n(kernel, grid, WIDE_THREADS, s, "flp_linear_kernel launch", after_kernel, ma, mb, my, mp, p);
+    };
+    st = w_mn ? go(flp_linear_kernel<1, LIN_NONE>)
+              : lin_with_act(e.act, [&](auto act) { return go(flp_linear_kernel<0, decltype(act)::value>); });
     if (st != FLP_OK || !l.rest) return st;
     return launch_step(flp_linear_join_kernel, static_cast<int64_t>(l.rest) * l.rows, LJ_THREADS, 0, s,
                        "flp_linear_join_kernel launch", true, p);
+}
+
+// Up to this many rows W is read by the rows kernel.
+constexpr int64_t kLinFewRows = 8;
+
+flp_status linear_rows(LinRowsParams& p, bool loose, int sm_count, bool after_kernel, cudaStream_t s) {
+    // warps of the grid: eight an SM before a row's contraction is split
+    p.kw = 1;
+    while (p.kw < LR_WARPS && cdiv(p.N, LR_ROWS) * p.kw < 8 * sm_count && p.K > 256 * p.kw) p.kw *= 2;
+    p.chunk = static_cast<int>(cdiv(cdiv(p.K, p.kw), 256) * 256);
+    const int64_t grid = cdiv(p.N, LR_ROWS * (LR_WARPS / p.kw));
+    auto rows = [&](auto mt) {
+        constexpr int MT = decltype(mt)::value;
+        return launch_step(loose ? flp_linear_rows_kernel<MT, true> : flp_linear_rows_kernel<MT, false>, grid, LR_THREADS, 0, s,
+                           "flp_linear_rows_kernel launch", after_kernel, p);
+    };
+    return p.M == 1   ? rows(std::integral_constant<int, 1>{})
+           : p.M == 2 ? rows(std::integral_constant<int, 2>{})
+           : p.M <= 4 ? rows(std::integral_constant<int, 4>{})
+                      : rows(std::integral_constant<int, 8>{});
 }
 
 flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
@@ -132,14 +161,15 @@ struct Regions {
 struct LinearLayout {
     LinPlan l;
     size_t off_x, off_w, off_part, bytes;
-    bool copy_x, copy_w;
+    bool few, copy_x, copy_w;
 };
 
 LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K, int pairs) {
     LinearLayout f{};
-    f.l = plan_linear(M, N, K, pairs);
-    f.copy_x = !rows_bf16(X, ldx);
-    f.copy_w = !rows_bf16(W, ldw);
+    f.few = M <= kLinFewRows;
+    if (!f.few) f.l = plan_linear(M, N, K, pairs);
+    f.copy_x = !rows_bf16(X, ldx) || (f.few && K % 8 != 0);  // whole vectors of x
+    f.copy_w = !f.few && !rows_bf16(W, ldw);
     Regions r;
     f.off_x = r.take(f.copy_x ? M * pad8(K) * 2 : 0);
     f.off_w = r.take(f.copy_w ? N * pad8(K) * 2 : 0);
@@ -241,6 +271,18 @@ extern "C" flp_status flp_linear(const void* X, int64_t ldx, const void* W, int6
     e.ldpre = ldpre;
     e.vec = rows_bf16(Y, ldy) && N % 8 == 0 && (!residual || rows_bf16(residual, ldr)) && (!pre || rows_bf16(pre, ldpre));
     e.bias_vec = aligned16(bias);
+    if (f.few) {
+        LinRowsParams p{};
+        p.x = static_cast<const bf16*>(X);
+        p.ldx = ldx;
+        p.w = static_cast<const bf16*>(W);
+        p.ldw = ldw;
+        p.M = static_cast<int>(M);
+        p.N = static_cast<int>(N);
+        p.K = static_cast<int>(K);
+        p.e = e;
+        return linear_rows(p, !(rows_bf16(W, ldw) && K % 8 == 0), d->sm_count, after, s);
+    }
     return linear_product(f.l, X, ldx, W, ldw, false, M, N, K, e, ws + f.off_part, nullptr, d->pairs, kWaitLimitNs, -1, after, s);
 }
 
@@ -313,7 +355,6 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         p.lddy = lddy;
         p.pre = activation == FLP_ACT_NONE ? nullptr : static_cast<const bf16*>(pre);
         p.ldpre = ldpre;
-        p.act = activation;
         p.M = static_cast<int>(M);
         p.N = static_cast<int>(N);
         p.d = g.make_d ? reinterpret_cast<bf16*>(ws + g.off_d) : nullptr;
@@ -321,11 +362,13 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         p.part = g.sums ? g.blocks == 1 ? dbias : reinterpret_cast<float*>(ws + g.off_sums) : nullptr;
         p.rows = g.rows;
         const dim3 grid(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(g.blocks));
-        if (vec)
-            flp_linear_grad_kernel<false><<<grid, LG_THREADS, 0, s>>>(p);
-        else
-            flp_linear_grad_kernel<true><<<grid, LG_THREADS, 0, s>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = lin_with_act(activation, [&](auto a) {
+            if (vec)
+                flp_linear_grad_kernel<false, decltype(a)::value><<<grid, LG_THREADS, 0, s>>>(p);
+            else
+                flp_linear_grad_kernel<true, decltype(a)::value><<<grid, LG_THREADS, 0, s>>>(p);
+            return cudaGetLastError();
+        });
         if (e != cudaSuccess) return cuda_fail(e, "flp_linear_grad_kernel launch");
         if (g.make_d) dY = ws + g.off_d, lddy = pad8(N);
         if (g.sums && g.blocks > 1) {

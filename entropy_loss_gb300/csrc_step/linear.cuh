@@ -15,6 +15,7 @@
 // pass over dy and v that also sums db from the unrounded values; dW is the contraction
 // of wgrad.cuh.
 #pragma once
+#include <type_traits>
 #include "../csrc/pair.cuh"
 #include "vec.cuh"
 
@@ -24,37 +25,107 @@ constexpr int LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_S
 
 // ------------------------------------------------------------------ activation
 
-constexpr float LIN_SQRT_HALF = 0.7071067811865476f;
+// All on packed pairs: the epilogues of the products are bound by their instructions.
+
 constexpr float LIN_INV_SQRT_2PI = 0.3989422804014327f;
-constexpr float LIN_TANH_U = 1.5957691216057308f;   // gelu_tanh(v) = v sigmoid(u), u = sqrt(8 / pi) (v + 0.044715 v^3)
+constexpr float LIN_TANH_U = 1.5957691216057308f;  // gelu_tanh(v) = v sigmoid(u), u = sqrt(8 / pi) (v + 0.044715 v^3)
 constexpr float LIN_TANH_3 = 0.044715f;
 
-__device__ __forceinline__ float lin_sigmoid(float u) { return __fdividef(1.f, 1.f + ex2_approx(-LOG2E * u)); }
+template <typename F>
+__device__ __forceinline__ uint64_t f2_map(uint64_t v, F f) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return f2_pack(f(lo), f(hi));
+}
+__device__ __forceinline__ uint64_t f2_ex2(uint64_t v) { return f2_map(v, [](float x) { return ex2_approx(x); }); }
+__device__ __forceinline__ uint64_t f2_rcp(uint64_t v) { return f2_map(v, [](float x) { return rcp_approx(x); }); }
+__device__ __forceinline__ uint64_t f2_abs(uint64_t v) { return v & 0x7fffffff7fffffffull; }
 
-// Phi(v) = erfc(-v / sqrt 2) / 2 keeps the digits of negative v that 1 + erf loses.
-__device__ __forceinline__ float lin_act(float v, int kind) {
-    switch (kind) {
-        case LIN_RELU: return v < 0.f ? 0.f : v;
-        case LIN_GELU: return 0.5f * v * erfcf(-LIN_SQRT_HALF * v);
-        case LIN_GELU_TANH: return v * lin_sigmoid(LIN_TANH_U * (v + LIN_TANH_3 * v * v * v));
-        case LIN_SILU: return v * lin_sigmoid(v);
-        default: return v;
-    }
+// exp(-v^2 / 2), and h = Phi(-|v|) = exp(-v^2 / 2) erfcx(|v| / sqrt 2) / 2, whose relative
+// error is that of erfcx: with t = 1 / (1 + 0.425 x), erfcx(x) / 2 = t P(t) for 0 <= x <=
+// 9.6 to 7.3e-6, P of degree 5 from a weighted least-squares fit (beyond, h vanishes).
+__device__ __forceinline__ void lin_normal_tail(uint64_t v, uint64_t& e, uint64_t& h) {
+    e = f2_ex2(f2_mul(f2_mul(v, v), f2_splat(-0.5f * LOG2E)));
+    const uint64_t t = f2_rcp(f2_fma(f2_abs(v), f2_splat(0.425f * 0.7071067811865476f), f2_splat(1.f)));
+    uint64_t q = f2_splat(0.5f * -0.154721429f);
+    q = f2_fma(q, t, f2_splat(0.5f * 0.430636568f));
+    q = f2_fma(q, t, f2_splat(0.5f * -0.0328755014f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.288526839f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.22786909f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.240571746f));
+    h = f2_mul(f2_mul(q, t), e);
 }
 
-// act'.  Far from 0 it is 0 or 1 to the last bit, and v^2 times a vanishing factor no number.
-__device__ __forceinline__ float lin_slope(float v, int kind) {
-    if (kind == LIN_RELU) return v > 0.f ? 1.f : 0.f;
-    v = v > 20.f ? 20.f : v < -20.f ? -20.f : v;  // NaN stays
-    if (kind == LIN_GELU)
-        return 0.5f * erfcf(-LIN_SQRT_HALF * v) + v * LIN_INV_SQRT_2PI * ex2_approx(-0.5f * LOG2E * v * v);
-    float u = v, du = 1.f;
-    if (kind == LIN_GELU_TANH) {
-        u = LIN_TANH_U * (v + LIN_TANH_3 * v * v * v);
-        du = LIN_TANH_U * (1.f + 3.f * LIN_TANH_3 * v * v);
+// -log2(e) u of the two that are v sigmoid(u).
+template <int ACT>
+__device__ __forceinline__ uint64_t lin_exponent(uint64_t v) {
+    if constexpr (ACT == LIN_SILU) return f2_mul(v, f2_splat(-LOG2E));
+    return f2_mul(v, f2_fma(f2_mul(v, v), f2_splat(-LOG2E * LIN_TANH_U * LIN_TANH_3), f2_splat(-LOG2E * LIN_TANH_U)));
+}
+
+template <int ACT>
+__device__ __forceinline__ uint64_t lin_act2(uint64_t v) {
+    if constexpr (ACT == LIN_RELU) return f2_map(v, [](float x) { return max_nan(x, 0.f); });
+    if constexpr (ACT == LIN_GELU) {  // v Phi(v) = max(v, 0) - |v| Phi(-|v|)
+        uint64_t e, h;
+        lin_normal_tail(v, e, h);
+        const uint64_t a = f2_map(f2_abs(v), [](float x) { return fminf(x, 1e4f); });  // h is 0 by then
+        return f2_fma(f2_mul(a, f2_splat(-1.f)), h, f2_map(v, [](float x) { return max_nan(x, 0.f); }));
     }
-    const float p = lin_sigmoid(u);
-    return p + v * du * p * lin_sigmoid(-u);
+    if constexpr (ACT == LIN_GELU_TANH || ACT == LIN_SILU)
+        return f2_mul(v, f2_rcp(f2_add(f2_ex2(lin_exponent<ACT>(v)), f2_splat(1.f))));
+    return v;
+}
+
+// act'.  Where |v| is cut off it is 0 or 1 to the last bit, and e = exp(-u) still finite,
+// which gives 1 - p = e p without another exponential.
+template <int ACT>
+__device__ __forceinline__ uint64_t lin_slope2(uint64_t v) {
+    if constexpr (ACT == LIN_RELU) return f2_map(v, [](float x) { return x > 0.f ? 1.f : 0.f; });
+    v = f2_map(v, [](float x) {
+        constexpr float END = ACT == LIN_GELU_TANH ? 9.f : ACT == LIN_GELU ? 13.f : 80.f;
+        return max_nan(min_nan(x, END), -END);
+    });
+    if constexpr (ACT == LIN_GELU) {
+        uint64_t e, h;
+        lin_normal_tail(v, e, h);
+        float v0, v1, h0, h1;
+        f2_unpack(v, v0, v1);
+        f2_unpack(h, h0, h1);
+        const uint64_t phi = f2_pack(v0 < 0.f ? h0 : 1.f - h0, v1 < 0.f ? h1 : 1.f - h1);
+        return f2_fma(f2_mul(v, f2_splat(LIN_INV_SQRT_2PI)), e, phi);
+    }
+    uint64_t vdu = v;
+    if constexpr (ACT == LIN_GELU_TANH)
+        vdu = f2_mul(v, f2_fma(f2_mul(v, v), f2_splat(3.f * LIN_TANH_U * LIN_TANH_3), f2_splat(LIN_TANH_U)));
+    const uint64_t e = f2_ex2(lin_exponent<ACT>(v)), p = f2_rcp(f2_add(e, f2_splat(1.f)));
+    return f2_fma(f2_mul(vdu, f2_mul(e, p)), p, p);
+}
+
+// The same where a few outputs alone are computed: one copy of the code.
+__device__ __forceinline__ float lin_act_of(float x, int act) {
+    uint64_t v = f2_pack(x, 0.f);
+    switch (act) {
+        case LIN_RELU: v = lin_act2<LIN_RELU>(v); break;
+        case LIN_GELU: v = lin_act2<LIN_GELU>(v); break;
+        case LIN_GELU_TANH: v = lin_act2<LIN_GELU_TANH>(v); break;
+        case LIN_SILU: v = lin_act2<LIN_SILU>(v); break;
+    }
+    float hi;
+    f2_unpack(v, x, hi);
+    return x;
+}
+
+// Calls f with the activation as a constant.
+template <typename F>
+auto lin_with_act(int act, F&& f) {
+    switch (act) {
+        case LIN_RELU: return f(std::integral_constant<int, LIN_RELU>{});
+        case LIN_GELU: return f(std::integral_constant<int, LIN_GELU>{});
+        case LIN_GELU_TANH: return f(std::integral_constant<int, LIN_GELU_TANH>{});
+        case LIN_SILU: return f(std::integral_constant<int, LIN_SILU>{});
+        default: return f(std::integral_constant<int, LIN_NONE>{});
+    }
 }
 
 // ------------------------------------------------------------------ product
@@ -120,27 +191,24 @@ __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
 }
 
 // Bias values of 32 columns from c0 on (0 past N or without a bias), added to v.
-__device__ __forceinline__ void lin_add_bias(const LinEpilogue& e, int c0, int N, float (&v)[32]) {
+__device__ __forceinline__ void lin_add_bias(const LinEpilogue& e, int c0, int N, uint64_t (&v)[16]) {
     if (!e.bias) return;
     if (e.bias_vec && c0 + 32 <= N) {
         if (e.bias_f32) {
-            const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + c0);
+            const uint4* b = reinterpret_cast<const uint4*>(static_cast<const float*>(e.bias) + c0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float4 u = __ldg(b + i);
-                v[4 * i] += u.x, v[4 * i + 1] += u.y, v[4 * i + 2] += u.z, v[4 * i + 3] += u.w;
+                const uint4 u = __ldg(b + i);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) v[2 * i + j] = f2_add(v[2 * i + j], Pairs<float>::get(u, j));
             }
         } else {
             const uint4* b = reinterpret_cast<const uint4*>(static_cast<const bf16*>(e.bias) + c0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint4 u = __ldg(b + i);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
-                    v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-                }
+                for (int j = 0; j < 4; ++j) v[4 * i + j] = f2_add(v[4 * i + j], Pairs<bf16>::get(u, j));
             }
         }
     } else {
@@ -149,7 +217,8 @@ __device__ __forceinline__ void lin_add_bias(const LinEpilogue& e, int c0, int N
         if (c < N)
             mine = e.bias_f32 ? static_cast<const float*>(e.bias)[c] : __bfloat162float(static_cast<const bf16*>(e.bias)[c]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, mine, j);
+        for (int j = 0; j < 16; ++j)
+            v[j] = f2_add(v[j], f2_pack(__shfl_sync(0xffffffffu, mine, 2 * j), __shfl_sync(0xffffffffu, mine, 2 * j + 1)));
     }
 }
 
@@ -196,9 +265,13 @@ __device__ __forceinline__ void lin_rows_in(uint32_t box, uint32_t (&w)[16], con
     __syncwarp();
 }
 
-__device__ __forceinline__ void lin_pack(const float (&v)[32], uint32_t (&w)[16]) {
+__device__ __forceinline__ void lin_pack(const uint64_t (&v)[16], uint32_t (&w)[16]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < 16; ++j) {
+        float lo, hi;
+        f2_unpack(v[j], lo, hi);
+        w[j] = pack_bf16x2(lo, hi);
+    }
 }
 
 // NaN in what an epilogue group (half g of a tile, the 128 rows from `rofs` on) has not
@@ -230,7 +303,7 @@ __device__ __forceinline__ void lin_raise(const Smem& sm, int* err) {
     }
 }
 
-template <int B_MN>
+template <int B_MN, int ACT>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     flp_linear_kernel(const __grid_constant__ CUtensorMap tmA,    // x or d, K-major (64 x 128 boxes)
                       const __grid_constant__ CUtensorMap tmB,    // W, K-major (64 x 128) or MN-major (64 x 64)
@@ -439,9 +512,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     continue;
                 }
                 const int c0 = n0 + b * 32;
-                float v[32];
+                uint64_t v[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                for (int j = 0; j < 16; ++j) v[j] = f2_pack(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1]));
                 lin_add_bias(p.e, c0, p.N, v);
                 uint32_t w[16];
                 if (p.e.pre) {
@@ -451,10 +524,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     else if (m0 + q * 32 < p.M)
                         lin_rows_out(box_out, w, p.e.pre, p.e.ldpre, m0 + q * 32, p.M, c0, p.N);
                 }
-                if (p.e.act != LIN_NONE) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = lin_act(v[j], p.e.act);
-                }
+                for (int j = 0; j < 16; ++j) v[j] = lin_act2<ACT>(v[j]);
                 if (p.e.residual) {
                     if (p.e.vec) {
                         const uint4* from = reinterpret_cast<const uint4*>(p.e.residual + row * p.e.ldr + c0);
@@ -470,10 +541,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         for (int j = 0; j < 16; ++j) w[j] = 0;
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[2 * j] += __uint_as_float(w[j] << 16);
-                        v[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = f2_add(v[j], f2_pack(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)));
                 }
                 lin_pack(v, w);
                 if (p.e.vec)
@@ -524,9 +593,119 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
         if (p.e.bias)
             x += p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[c] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[c]);
         if (p.e.pre) p.e.pre[row * p.e.ldpre + c] = __float2bfloat16_rn(x);
-        x = lin_act(x, p.e.act);
+        x = lin_act_of(x, p.e.act);
         if (p.e.residual) x += __bfloat162float(p.e.residual[row * p.e.ldr + c]);
         p.e.y[row * p.e.ldy + c] = __float2bfloat16_rn(x);
+    }
+}
+
+// ------------------------------------------------------------------ few rows
+//
+// A row of W meets every row of x while it is in registers, so the call reads W once, at
+// the pace of memory: a warp takes R rows of W at a time, 8 elements a lane, and keeps R x
+// MT sums in pairs.  x, read again for every R rows, comes from the caches.  Where W has
+// too few rows for all warps, KW warps of a block share rows and split the contraction.
+
+struct LinRowsParams {
+    const bf16* x;
+    long long ldx;
+    const bf16* w;
+    long long ldw;
+    int M, N, K;
+    int kw;     // warps that share rows: 1, 2, 4, 8
+    int chunk;  // of the contraction, each such warp's: a multiple of 256
+    LinEpilogue e;
+};
+
+constexpr int LR_THREADS = 256;
+constexpr int LR_WARPS = LR_THREADS / 32;
+constexpr int LR_ROWS = 4;
+
+template <int MT, bool LOOSE>
+__global__ void __launch_bounds__(LR_THREADS) flp_linear_rows_kernel(const __grid_constant__ LinRowsParams p) {
+    constexpr int R = LR_ROWS, U = MT >= 8 ? 1 : 2;  // U steps of 256 elements under way
+    __shared__ __align__(16) uint8_t words[LOOSE ? LR_WARPS * WARP_WORDS_BYTES : 16];
+    __shared__ float sums[LR_WARPS][R * MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stage = smem_addr(words) + (LOOSE ? warp * WARP_WORDS_BYTES : 0);
+    const int teams = LR_WARPS / p.kw, team = warp / p.kw, part = warp % p.kw;
+    const int n0 = (blockIdx.x * teams + team) * R;
+    const int k0 = part * p.chunk, k1 = min(p.K, k0 + p.chunk);
+    griddep_wait();  // an aligned copy of x
+    uint64_t acc[R][MT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] = 0;
+    const Extent all = extent_of<bf16>(p.w, p.N, p.ldw, p.K);
+    if (n0 < p.N) {
+        for (int k = k0; k < k1; k += 256 * U) {
+            uint32_t w[U][R][WarpWords<bf16>::N];
+            const bf16* src[U][R];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int n = min(n0 + r, p.N - 1), at = k + u * 256 + lane * 8, left = k1 - at;
+                    src[u][r] = p.w + n * p.ldw + at;
+                    if constexpr (LOOSE) {
+                        load_words<bf16>(w[u][r], src[u][r], left, n == 0 || n == p.N - 1, all);
+                    } else {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (left > 0) v = __ldcs(reinterpret_cast<const uint4*>(src[u][r]));
+                        w[u][r][0] = v.x, w[u][r][1] = v.y, w[u][r][2] = v.z, w[u][r][3] = v.w;
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = k + u * 256 + lane * 8, left = k1 - at;
+                uint64_t wp[R][4];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    uint4 v;
+                    if constexpr (LOOSE)
+                        v = settle_words<bf16>(w[u][r], src[u][r], left, stage);
+                    else
+                        v = make_uint4(w[u][r][0], w[u][r][1], w[u][r][2], w[u][r][3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) wp[r][j] = Pairs<bf16>::get(v, j);
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    // rows of x are aligned and padded to vectors; what lies behind K is zero in
+                    // a padded copy, and meets zeros of W
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (left > 0) v = __ldg(reinterpret_cast<const uint4*>(p.x + min(m, p.M - 1) * p.ldx + at));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint64_t xv = Pairs<bf16>::get(v, j);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) acc[r][m] = f2_fma(wp[r][j], xv, acc[r][m]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float s = warp_sum(f2_sum(acc[r][m]));
+            if (lane == 0) sums[warp][r * MT + m] = s;
+        }
+    __syncthreads();
+    // one thread per output of the block
+    for (int i = threadIdx.x; i < teams * R * MT; i += LR_THREADS) {
+        const int m = i / (teams * R), j = i % (teams * R), c = blockIdx.x * teams * R + j;
+        if (m >= p.M || c >= p.N) continue;
+        float v = 0.f;
+        for (int q = 0; q < p.kw; ++q) v += sums[j / R * p.kw + q][j % R * MT + m];
+        if (p.e.bias)
+            v += p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[c] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[c]);
+        if (p.e.pre) p.e.pre[m * p.e.ldpre + c] = __float2bfloat16_rn(v);
+        v = lin_act_of(v, p.e.act);
+        if (p.e.residual) v += __bfloat162float(p.e.residual[m * p.e.ldr + c]);
+        p.e.y[m * p.e.ldy + c] = __float2bfloat16_rn(v);
     }
 }
 
@@ -535,9 +714,8 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
 struct LinGradParams {
     const bf16* dy;
     long long lddy;
-    const bf16* pre;  // or null: no activation
+    const bf16* pre;  // with an activation
     long long ldpre;
-    int act;
     int M, N;
     bf16* d;  // [M, Np], or null: not written
     int Np;
@@ -550,7 +728,7 @@ constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int LG_ROWS = 4;  // rows a warp has under way
 
 // 256 columns x `rows` rows a block, a row at a time a warp.
-template <bool LOOSE>
+template <bool LOOSE, int ACT>
 __global__ void __launch_bounds__(LG_THREADS) flp_linear_grad_kernel(const __grid_constant__ LinGradParams p) {
     constexpr int P = 4;
     __shared__ __align__(16) uint8_t words[LOOSE ? LG_WARPS * WARP_WORDS_BYTES : 16];
@@ -584,7 +762,7 @@ __global__ void __launch_bounds__(LG_THREADS) flp_linear_grad_kernel(const __gri
             const int r = r0 + i * LG_WARPS;
             const bool on = r < last, edge = r == 0 || r == p.M - 1;
             fetch(a[i], p.dy + r * p.lddy + col, on, edge, all_dy);
-            if (p.pre) fetch(b[i], p.pre + r * p.ldpre + col, on, edge, all_pre);
+            if (ACT != LIN_NONE) fetch(b[i], p.pre + r * p.ldpre + col, on, edge, all_pre);
         }
 #pragma unroll
         for (int i = 0; i < LG_ROWS; ++i) {
@@ -594,14 +772,10 @@ __global__ void __launch_bounds__(LG_THREADS) flp_linear_grad_kernel(const __gri
             uint64_t d[P];
 #pragma unroll
             for (int j = 0; j < P; ++j) d[j] = Pairs<bf16>::get(u, j);
-            if (p.pre) {
+            if constexpr (ACT != LIN_NONE) {
                 const uint4 x = value(b[i], p.pre + r * p.ldpre + col);
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    float lo, hi;
-                    f2_unpack(Pairs<bf16>::get(x, j), lo, hi);
-                    d[j] = f2_mul(d[j], f2_pack(lin_slope(lo, p.act), lin_slope(hi, p.act)));
-                }
+                for (int j = 0; j < P; ++j) d[j] = f2_mul(d[j], lin_slope2<ACT>(Pairs<bf16>::get(x, j)));
             }
             if (p.d) st_global_16(p.d + static_cast<long long>(r) * p.Np + col, Pairs<bf16>::put(d), left > 0);
 #pragma unroll

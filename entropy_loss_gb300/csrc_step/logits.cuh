@@ -438,12 +438,6 @@ struct TlpBwdParams {
 constexpr int TLPB_THREADS = 256;
 constexpr int TLPB_NV = 4;
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 template <typename T, bool LOOSE>
 __global__ void __launch_bounds__(TLPB_THREADS) flp_token_logprob_bwd_kernel(const TlpBwdParams p) {
     constexpr int V = wide_v<T>(), NV = TLPB_NV, P = Pairs<T>::N;
