@@ -31,13 +31,6 @@ constexpr float LIN_INV_SQRT_2PI = 0.3989422804014327f;
 constexpr float LIN_TANH_U = 1.5957691216057308f;  // gelu_tanh(v) = v sigmoid(u), u = sqrt(8 / pi) (v + 0.044715 v^3)
 constexpr float LIN_TANH_3 = 0.044715f;
 
-template <typename F>
-__device__ __forceinline__ uint64_t f2_map(uint64_t v, F f) {
-    float lo, hi;
-    f2_unpack(v, lo, hi);
-    return f2_pack(f(lo), f(hi));
-}
-__device__ __forceinline__ uint64_t f2_ex2(uint64_t v) { return f2_map(v, [](float x) { return ex2_approx(x); }); }
 __device__ __forceinline__ uint64_t f2_rcp(uint64_t v) { return f2_map(v, [](float x) { return rcp_approx(x); }); }
 __device__ __forceinline__ uint64_t f2_abs(uint64_t v) { return v & 0x7fffffff7fffffffull; }
 

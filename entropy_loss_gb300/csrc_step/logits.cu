@@ -17,26 +17,30 @@ flp_status tlp_checks(const void* logits, int64_t ld, int dtype, const int64_t* 
 }
 
 // Blocks of a row: as many as finish the rows soonest, in vectors that a resident block
-// reads (two blocks of 512 threads an SM), each block costing as much as 1024 vectors.
-int tlp_cluster(int64_t M, int64_t vecs, int sm_count) {
+// reads, a row's end costing a block as much as 3000 vectors (2048 rows of 131072 take 108
+// us in one block each, 146 in two; 64 rows 15 us in eight blocks each).
+int tlp_cluster(int64_t M, int64_t vecs, int64_t resident) {
     int best = 1;
     double least = 1e300;
     for (int c = 1; c <= TLP_CLUSTER; c *= 2) {
-        const double cost = static_cast<double>(cdiv(M * c, 2 * sm_count)) * (static_cast<double>(vecs) / c + 1024);
+        const double cost = static_cast<double>(cdiv(M * c, resident)) * (static_cast<double>(vecs) / c + 3000);
         if (cost < least) least = cost, best = c;
     }
     return best;
 }
 
-template <typename T, bool LOOSE>
+template <typename T, bool LOOSE, int THREADS>
 flp_status tlp_launch(TlpParams& p, int sm_count, cudaStream_t s) {
+    constexpr auto* kernel = flp_token_logprob_kernel<T, LOOSE, THREADS>;
     const int64_t vecs = cdiv(p.V, wide_v<T>());
-    const bool small = vecs <= 512;  // a block of 128 threads reads the row at once
-    p.cluster = small ? 1 : tlp_cluster(p.M, vecs, sm_count);
+    int per_sm = 0;
+    const flp_status st = resident_blocks<kernel>(THREADS, 0, 0, &per_sm);
+    if (st != FLP_OK) return st;
+    p.cluster = vecs <= 4 * THREADS ? 1 : tlp_cluster(p.M, vecs, static_cast<int64_t>(per_sm) * sm_count);
     p.per = static_cast<int>(cdiv(cdiv(vecs, p.cluster), 32) * 32);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.M * p.cluster));
-    cfg.blockDim = dim3(small ? 128 : 512);
+    cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -45,8 +49,7 @@ flp_status tlp_launch(TlpParams& p, int sm_count, cudaStream_t s) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    const cudaError_t e = small ? cudaLaunchKernelEx(&cfg, flp_token_logprob_kernel<T, LOOSE, 128>, p)
-                                : cudaLaunchKernelEx(&cfg, flp_token_logprob_kernel<T, LOOSE, 512>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e == cudaSuccess ? FLP_OK : cuda_fail(e, "flp_token_logprob_kernel launch");
 }
 
@@ -86,7 +89,11 @@ extern "C" flp_status flp_token_logprob(const void* logits, int64_t ld, int dtyp
     const bool loose = !(rows16(logits, ld, dtype) && (V * elem(dtype)) % 16 == 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto typed = [&](auto t) {
-        return loose ? tlp_launch<decltype(t), true>(p, d->sm_count, s) : tlp_launch<decltype(t), false>(p, d->sm_count, s);
+        using T = decltype(t);
+        // rows that a block of 128 threads reads at once
+        if (V <= 4 * 128 * wide_v<T>())
+            return loose ? tlp_launch<T, true, 128>(p, d->sm_count, s) : tlp_launch<T, false, 128>(p, d->sm_count, s);
+        return loose ? tlp_launch<T, true, 256>(p, d->sm_count, s) : tlp_launch<T, false, 256>(p, d->sm_count, s);
     };
     return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
 }

@@ -9,22 +9,31 @@
 // maximum grows; threads, warps and the blocks of a row (a cluster, joined through
 // distributed shared memory) are merged at the end.
 //
-// The alternatives come out of the same pass.  A thread's maximum is an element of the
-// row, so the k-th largest of 32 maxima over disjoint parts of it is a bound that at
-// least k elements reach; elements below it cannot be among the k largest.  With the
-// parts interleaved that bound lets through little more than k elements of what was read
-// so far, and it is taken again whenever the amount read has doubled.  What passes goes
-// to a list in shared memory, in whatever order, and is ranked at the end by value and
-// column, so that equal logits come out in the order of their columns.  A list that
-// overflows (many equal logits) is dropped, and the block reads its part again,
-// taking the largest left of each chunk in turn.
+// The alternatives come out of the same pass.  The largest element that a group of threads
+// has read is an element of the row, so the k-th largest of such maxima, over groups that
+// read different elements, is a bound that at least k elements reach; elements below it
+// are not among the k largest.  With 16 or 32 groups little more than k elements of what
+// was read pass it, and it is taken again whenever the amount has doubled, from what the warps have left in shared memory by then (an older maximum is
+// still an element: no barrier).  A vector whose largest element passes goes to a list in
+// shared memory; at the end the listed vectors are read again (from the L2), and what of them
+// passes the last bound is ranked by value and column, so that equal logits come out
+// in the order of their columns.  When a list overflows (many equal logits), the block
+// reads its part again, taking the largest left of each chunk in turn.
+//
+// Bound by memory and, close behind it, by instructions: 8192 rows of 131072 bf16 logits
+// (317 us at the measured copy rate) take 328 us without alternatives, 388 with 8, 416 with
+// 20: what they add is each row's end, which its block's loads do not overlap.  Four blocks
+// of 256 threads an SM (two of 512: 371 and 490 with 8; three of 256: 349 and 424); 4
+// vectors a thread at a time (2: 388 and 461).  Rows taken by resident blocks in turn, the
+// next ones copied ahead through shared memory, took 396 and 468.
 #pragma once
+#include <cfloat>
 #include "vec.cuh"
 
 namespace flp {
 
 constexpr int TLP_MAX_TOP = 32;
-constexpr int TLP_LIST = 1024;     // candidates a block can hold
+constexpr int TLP_LIST = 512;      // vectors, and then elements, that a block can list
 constexpr int TLP_CLUSTER = 8;     // blocks of a row at most
 
 struct TlpParams {
@@ -49,19 +58,6 @@ struct TlpStats {
     float m, s, a;
 };
 
-__device__ __forceinline__ TlpStats tlp_merge(TlpStats u, TlpStats v, float c) {
-    const float m = fmaxf(u.m, v.m);
-    // a part that holds nothing above -inf brings nothing (or the NaN that it met)
-    const float du = u.m == -INFINITY ? 0.f : (u.m - m) * c, dv = v.m == -INFINITY ? 0.f : (v.m - m) * c;
-    const float fu = ex2_approx(du), fv = ex2_approx(dv);
-    // a part so far below that its factor is 0 brings nothing, however large du is
-    TlpStats r;
-    r.m = m;
-    r.s = u.s * fu + v.s * fv;
-    r.a = (fu > 0.f ? fu * (u.a + du * u.s) : 0.f) + (fv > 0.f ? fv * (v.a + dv * v.s) : 0.f);
-    return r;
-}
-
 // A key orders by value, then by column, lower ones first; 0 is no key.
 __device__ __forceinline__ unsigned long long tlp_key(float x, int col) {
     const uint32_t b = __float_as_uint(x + 0.f);  // -0 and 0 are equal
@@ -85,19 +81,34 @@ __device__ __forceinline__ float tlp_elem(const uint32_t* w, int i) {
         return __uint_as_float(w[i]);
 }
 
-// The largest element of N words; NaN are passed over.
-template <typename T, int N>
-__device__ __forceinline__ float tlp_max(const uint32_t (&w)[N]) {
+// The largest element of a vector; NaN are passed over.
+template <typename T>
+__device__ __forceinline__ float tlp_max(const uint32_t* w) {
     if constexpr (sizeof(T) == 2) {
         __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
 #pragma unroll
-        for (int i = 1; i < N; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        for (int i = 1; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
         return fmaxf(__low2float(m), __high2float(m));
     } else {
-        float m = __uint_as_float(w[0]);
+        return fmaxf(fmax3(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2])), __uint_as_float(w[3]));
+    }
+}
+
+__device__ __forceinline__ float redux_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// -inf in the places of a vector from `valid` on.
+template <typename T>
+__device__ __forceinline__ void tlp_cut(uint32_t* w, int valid) {
 #pragma unroll
-        for (int i = 1; i < N; ++i) m = fmaxf(m, __uint_as_float(w[i]));
-        return m;
+    for (int q = 0; q < 4; ++q) {
+        if constexpr (sizeof(T) == 2)
+            w[q] = 2 * q + 1 < valid ? w[q] : 2 * q < valid ? (w[q] & 0xffffu) | 0xff800000u : 0xff80ff80u;
+        else
+            w[q] = q < valid ? w[q] : 0xff800000u;
     }
 }
 
@@ -135,42 +146,81 @@ struct TlpChunk {
             else
                 u = make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
             w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-            if (valid < V) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t& x = w[4 * i + q];
-                    if constexpr (sizeof(T) == 2)
-                        x = 2 * q + 1 < valid ? x : 2 * q < valid ? (x & 0xffffu) | 0xff800000u : 0xff80ff80u;
-                    else
-                        x = q < valid ? x : 0xff800000u;
-                }
-            }
+            if (valid < V) tlp_cut<T>(w + 4 * i, valid);
         }
     }
 };
+
+// A of a chunk some of whose elements are masked: a term whose exponential is 0 is 0.
+// Out of line, from the chunk read once more, so that the loop need not keep it.
+template <typename T, bool LOOSE, int NV, int THREADS>
+__device__ __noinline__ float tlp_masked(const T* row, int v0, int end, bool edge, const Extent& all, uint32_t stage,
+                                         float base, float c) {
+    constexpr int V = wide_v<T>();
+    float a = 0.f;
+    for (int i = 0; i < NV; ++i) {
+        TlpChunk<T, LOOSE, 1, THREADS> one;
+        uint32_t w[4];
+        one.load(row, v0 + i * THREADS, end, edge, all);
+        one.settle(w, row, v0 + i * THREADS, end, stage);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            const float t = (tlp_elem<T>(w, q) - base) * c, e = ex2_approx(t);
+            a += e > 0.f ? e * t : 0.f;
+        }
+    }
+    return a;
+}
 
 template <int THREADS>
 struct TlpShared {
     static constexpr int WARPS = THREADS / 32;
     unsigned long long list[TLP_LIST];
-    unsigned long long best[TLP_MAX_TOP];   // this block's, in order; 0: none
+    unsigned long long best[TLP_MAX_TOP];  // this block's, in order; 0: none
     unsigned long long warp_key[WARPS];
-    float part[2][WARPS][32];               // maxima of 32 parts by warp, two generations
+    __align__(16) float group[32];         // the largest that each group of threads has read
     TlpStats warp_stats[WARPS];
-    TlpStats stats;                         // this block's
-    int n;
+    TlpStats stats;                        // this block's
+    int vecs[TLP_LIST];
+    int n_vecs, n;                         // vectors and elements listed
+    float bound;                           // the latest
 };
 
-// The k-th largest of the 32 lanes' values, equal ones counted by lane.
-__device__ __forceinline__ float tlp_kth(float g, int k) {
-    const int lane = threadIdx.x & 31;
-    int above = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const float o = __shfl_sync(0xffffffffu, g, j);
-        above += o > g || (o == g && j < lane) ? 1 : 0;
+// Leaves the largest that each group of `lanes` threads has read.
+template <int THREADS>
+__device__ __forceinline__ void tlp_put_maxima(TlpShared<THREADS>& sh, float m, int lanes) {
+    volatile float* group = sh.group;
+    if (lanes == 32) {
+        m = redux_max(m);
+    } else {
+        for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    return __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, above == k - 1)) - 1);
+    if (threadIdx.x % lanes == 0) group[threadIdx.x / lanes] = m;
+}
+
+// The k-th largest of the groups' maxima: the largest that k of them reach; above -inf.
+template <int THREADS>
+__device__ __forceinline__ float tlp_bound(const TlpShared<THREADS>& sh, int k, int lanes) {
+    const int lane = threadIdx.x & 31, groups = THREADS / lanes;
+    const volatile float* group = sh.group;
+    const float mine = lane < groups ? group[lane] : -INFINITY;
+    int reach = 0;
+    for (int i0 = 0; i0 < groups; i0 += 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reach += __shfl_sync(0xffffffffu, mine, i0 + i) >= mine ? 1 : 0;
+    return redux_max(reach >= k ? fmaxf(mine, -FLT_MAX) : -FLT_MAX);
+}
+
+// A warp's statistics in one, in every lane.
+__device__ __forceinline__ TlpStats tlp_warp(TlpStats u, float c) {
+    TlpStats r;
+    r.m = redux_max(u.m);
+    // a part that holds nothing above -inf brings nothing (or the NaN that it met), and one
+    // so far below that its factor is 0 nothing, however large d is
+    const float d = u.m == -INFINITY ? 0.f : (u.m - r.m) * c, f = ex2_approx(d);
+    r.s = warp_sum(u.s * f);
+    r.a = warp_sum(f > 0.f ? f * (u.a + d * u.s) : 0.f);
+    return r;
 }
 
 // best[] from the n keys of the list: a key's place is how many are above it.
@@ -189,10 +239,12 @@ __device__ __forceinline__ void tlp_rank(TlpShared<THREADS>& sh, int n, int k) {
 }
 
 // The block's k largest, one after another, chunk by chunk (the list has overflowed).
-template <typename T, bool LOOSE, int NV, int THREADS>
+template <typename T, bool LOOSE, int THREADS>
 __device__ __noinline__ void tlp_again(TlpShared<THREADS>& sh, const T* row, int v0, int v1, int end, bool edge,
-                                       const Extent& all, uint32_t stage, int k) {
-    constexpr int V = wide_v<T>();
+                                       const Extent& all, int k) {
+    constexpr int V = wide_v<T>(), NV = 2;
+    __shared__ __align__(16) uint8_t words[LOOSE ? THREADS / 32 * WARP_WORDS_BYTES : 16];
+    const uint32_t stage = smem_addr(words) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
     if (threadIdx.x < TLP_MAX_TOP) sh.best[threadIdx.x] = 0;
     __syncthreads();
     for (int v = v0; v < v1; v += THREADS * NV) {
@@ -262,7 +314,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
     const int vecs = (p.V + V - 1) / V;
     const int v0 = min(vecs, rank * p.per), v1 = min(vecs, v0 + p.per);
     const int end = min(p.V, v1 * V);  // one past the last column of this block
-    if (threadIdx.x == 0) sh.n = 0;
+    const int lanes = THREADS / (p.top <= 16 ? 16 : 32);  // of a group: more groups than alternatives
+    if (threadIdx.x == 0) sh.n = sh.n_vecs = 0, sh.bound = -FLT_MAX;
     long long y = 0;
     float xy = 0.f;
     if (rank == 0 && threadIdx.x == 0) {
@@ -275,14 +328,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
     float bound = -INFINITY;
     TlpChunk<T, LOOSE, NV, THREADS> next;
     next.load(row, v0 + threadIdx.x, end, edge, all);
-    int generation = 0;
     unsigned chunk = 0;
     for (int v = v0; v < v1; v += THREADS * NV, ++chunk) {
         const int mine = v + threadIdx.x;
         uint32_t w[4 * NV];
         next.settle(w, row, mine, end, stage);
         if (v + THREADS * NV < v1) next.load(row, mine + THREADS * NV, end, edge, all);
-        const float top = tlp_max<T>(w), m = fmaxf(st.m, top);
+        float tops[NV], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) tops[i] = tlp_max<T>(w + 4 * i), top = fmaxf(top, tops[i]);
+        const float m = fmaxf(st.m, top);
         const float base = m == -INFINITY ? 0.f : m;  // nothing above -inf yet: every term is 0
         const uint64_t minus = f2_splat(-base), c2 = f2_splat(p.c);
         uint64_t s2 = 0, a2 = 0;
@@ -291,78 +346,82 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
             const uint4 u = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                const uint64_t t = f2_mul(f2_add(Pairs<T>::get(u, q), minus), c2);
-                float lo, hi;
-                f2_unpack(t, lo, hi);
-                const uint64_t e = f2_pack(ex2_approx(lo), ex2_approx(hi));
+                const uint64_t t = f2_mul(f2_add(Pairs<T>::get(u, q), minus), c2), e = f2_ex2(t);
                 s2 = f2_add(s2, e);
                 a2 = f2_fma(e, t, a2);
             }
         }
         TlpStats now{m, f2_sum(s2), f2_sum(a2)};
-        if (now.a != now.a && now.s == now.s) {  // an infinite exponent times its 0: those terms are 0
-            now.a = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    const float t = (tlp_elem<T>(w + 4 * i, q) - base) * p.c, e = ex2_approx(t);
-                    now.a += e > 0.f ? e * t : 0.f;
-                }
-        }
-        const float below = st.m;
-        if (m > below) {
-            st = tlp_merge(st, now, p.c);
+        // an infinite exponent times its 0
+        if (__any_sync(0xffffffffu, now.a != now.a && now.s == now.s))
+            now.a = tlp_masked<T, LOOSE, NV, THREADS>(row, mine, end, edge, all, stage, base, p.c);
+        if (m > st.m) {
+            const float d = st.m == -INFINITY ? 0.f : (st.m - m) * p.c, f = ex2_approx(d);
+            now.a += f > 0.f ? f * (st.a + d * st.s) : 0.f;
+            now.s += f * st.s;
+            st = now;
         } else {
             st.s += now.s, st.a += now.a;
         }
         if (p.top > 0) {
-            const float old = bound;
             if ((chunk & (chunk + 1)) == 0) {  // 1, 2, 4, ... chunks read
-                sh.part[generation][warp][lane] = st.m;
-                __syncthreads();
-                float g = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < WARPS; ++i) g = fmaxf(g, sh.part[generation][i][lane]);
-                generation ^= 1;
-                bound = tlp_kth(g, p.top);
+                tlp_put_maxima(sh, st.m, lanes);
+                if (chunk == 0) __syncthreads();
+                // one warp takes the new bound, the others when they come by; the first is everybody's
+                if (chunk == 0 || chunk % WARPS == warp) {
+                    __syncwarp();
+                    bound = tlp_bound(sh, p.top, lanes);
+                    if (lane == 0) *static_cast<volatile float*>(&sh.bound) = bound;
+                }
             }
-            // a later element equal to the old bound lies behind k others that reach it
-            if (top > old && top >= bound) {
+            bound = fmaxf(bound, *static_cast<volatile float*>(&sh.bound));
+            if (top >= bound) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int q = 0; q < V; ++q) {
-                        const float x = tlp_elem<T>(w + 4 * i, q);
-                        if (x > old && x >= bound) {
-                            const int n = atomicAdd(&sh.n, 1);
-                            if (n < TLP_LIST) sh.list[n] = tlp_key(x, (mine + i * THREADS) * V + q);
-                        }
+                for (int i = 0; i < NV; ++i) {
+                    if (tops[i] >= bound) {
+                        const int n = atomicAdd(&sh.n_vecs, 1);
+                        if (n < TLP_LIST) sh.vecs[n] = mine + i * THREADS;
                     }
+                }
             }
         }
     }
 
-    // the threads' sums, then the warps'
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        TlpStats u;
-        u.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        u.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        u.a = __shfl_xor_sync(0xffffffffu, st.a, o);
-        st = tlp_merge(st, u, p.c);
-    }
+    // the threads' sums in one, then the warps', then the blocks'
+    const float thread_max = st.m;
+    st = tlp_warp(st, p.c);
     if (lane == 0) sh.warp_stats[warp] = st;
+    if (p.top > 0) tlp_put_maxima(sh, thread_max, lanes);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        st = sh.warp_stats[0];
-        for (int i = 1; i < WARPS; ++i) st = tlp_merge(st, sh.warp_stats[i], p.c);
-        sh.stats = st;
+    const TlpStats nothing{-INFINITY, 0.f, 0.f};
+    if (warp == 0) {
+        st = tlp_warp(lane < WARPS ? sh.warp_stats[lane] : nothing, p.c);
+        if (lane == 0) sh.stats = st;
     }
     if (p.top > 0) {
+        bound = tlp_bound(sh, p.top, lanes);
+        const int listed = sh.n_vecs;
+        for (int i = threadIdx.x; i < min(listed, TLP_LIST); i += THREADS) {
+            const int col = sh.vecs[i] * V;
+            uint32_t w[4] = {0, 0, 0, 0};
+            if constexpr (!LOOSE) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + col));
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            }
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                if (col + q >= end) break;
+                const float x = LOOSE ? static_cast<float>(row[col + q]) : tlp_elem<T>(w, q);
+                if (x >= bound) {
+                    const int n = atomicAdd(&sh.n, 1);
+                    if (n < TLP_LIST) sh.list[n] = tlp_key(x, col + q);
+                }
+            }
+        }
+        __syncthreads();
         const int n = sh.n;
-        if (n > TLP_LIST)
-            tlp_again<T, LOOSE, NV, THREADS>(sh, row, v0, v1, end, edge, all, stage, p.top);
+        if (listed > TLP_LIST || n > TLP_LIST)
+            tlp_again<T, LOOSE, THREADS>(sh, row, v0, v1, end, edge, all, p.top);
         else
             tlp_rank(sh, n, p.top);
     }
@@ -370,14 +429,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
         __syncthreads();
         cluster_sync();
         if (rank == 0) {
-            if (threadIdx.x == 0) {
-                const uint32_t mine = smem_addr(&sh.stats);
-                for (int i = 1; i < p.cluster; ++i) {
-                    const uint32_t from = mapa_shared(mine, i);
-                    const TlpStats u{ld_cluster_f32(from), ld_cluster_f32(from + 4), ld_cluster_f32(from + 8)};
-                    st = tlp_merge(st, u, p.c);
+            if (warp == 0) {
+                TlpStats u = nothing;
+                if (lane < p.cluster) {
+                    const uint32_t from = mapa_shared(smem_addr(&sh.stats), lane);
+                    u = TlpStats{ld_cluster_f32(from), ld_cluster_f32(from + 4), ld_cluster_f32(from + 8)};
                 }
-                sh.stats = st;
+                st = tlp_warp(u, p.c);
             }
             if (p.top > 0) {
                 const int n = p.cluster * p.top;
@@ -386,29 +444,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
                 __syncthreads();
                 tlp_rank(sh, n, p.top);
             }
-            __syncthreads();
         }
+        __syncthreads();
         cluster_sync();  // no block leaves while its results are read
+        if (rank != 0) return;
     }
-    if (rank != 0) return;
-    __syncthreads();
-    st = sh.stats;
+    // warp 0 writes the row: its lanes hold the sums, and what it ranked lies in best[]
+    if (warp != 0) return;
     const bool empty = st.m == -INFINITY && st.s == 0.f;  // a row with nothing above -inf
+    const bool nan = st.s != st.s;                        // one with a NaN or +inf
     const float ln_s = empty ? 0.f : logf(st.s);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
         const bool skip = y == p.ignore_index, bad = y < 0 || y >= p.V;
         p.lse[at] = empty ? -INFINITY : fmaf(p.scale, st.m, ln_s);
-        // st.s is NaN when the row holds a NaN or +inf
-        const float lp = empty ? -INFINITY : st.s != st.s ? st.s : p.scale * (xy - st.m) - ln_s;
+        const float lp = empty ? -INFINITY : nan ? st.s : p.scale * (xy - st.m) - ln_s;
         p.logprob[at] = skip ? 0.f : bad ? __uint_as_float(0x7fc00000u) : lp;
         const float h = ln_s - LN2 * (st.a / st.s);
         if (p.entropy) p.entropy[at] = skip || empty ? 0.f : h < 0.f ? 0.f : h;
     }
-    if (threadIdx.x < p.top) {
-        const unsigned long long key = st.s != st.s ? 0 : sh.best[threadIdx.x];
-        const float none = st.s != st.s ? st.s : -INFINITY;
-        p.top_value[at * p.top + threadIdx.x] = key ? p.scale * (tlp_key_value(key) - st.m) - ln_s : none;
-        p.top_index[at * p.top + threadIdx.x] = key ? tlp_key_col(key) : -1;
+    if (lane < p.top) {
+        const unsigned long long key = nan ? 0 : sh.best[lane];
+        p.top_value[at * p.top + lane] = key ? p.scale * (tlp_key_value(key) - st.m) - ln_s : nan ? st.s : -INFINITY;
+        p.top_index[at * p.top + lane] = key ? tlp_key_col(key) : -1;
     }
 }
 

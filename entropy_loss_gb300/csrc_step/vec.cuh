@@ -23,6 +23,14 @@ __device__ __forceinline__ float f2_sum(uint64_t v) {
     return lo + hi;
 }
 
+template <typename F>
+__device__ __forceinline__ uint64_t f2_map(uint64_t v, F f) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return f2_pack(f(lo), f(hi));
+}
+__device__ __forceinline__ uint64_t f2_ex2(uint64_t v) { return f2_map(v, [](float x) { return ex2_approx(x); }); }
+
 // A vector as packed fp32 pairs (two lanes per instruction), and pairs rounded
 // once to a vector (nearest, ties to even).
 template <typename T>
