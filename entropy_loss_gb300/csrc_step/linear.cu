@@ -7,46 +7,45 @@ namespace {
 // ------------------------------------------------------------------ product
 
 struct LinPlan {
-    int tm, tn, whole, rest, splits, units, KB, rows;
+    int width, tm, tn, whole, rest, splits, units, KB, rows;
     size_t part_bytes;
 };
 
-// Whole rounds of tiles write their outputs; the rest are split into the number of runs
-// that costs least, in the time of a 64-deep block of a tile (0.54 us): the blocks of a
-// run and two for its start and end, and for joining 4 (a launch) and the partial tiles'
-// bytes, written and read back at 2 MB a block.
+// Tiles of 256 x 512, or of 256 x 256 where they fill the pairs better.  Whole rounds of
+// tiles write their outputs; the rest are split into runs.  The least of what these cost:
+// 0.66 us for a 64-deep block of a wide tile and 0.37 us of a narrow one (the rate at which
+// its operands arrive), 3 us for a run's start and end, and for joining 4 us (a launch) and
+// the partial tiles' bytes, written and read back at 4 TB/s.
 LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
-    LinPlan l{};
+    LinPlan best{};
+    double least = 1e300;
     pairs = std::max(1, pairs);
-    l.tm = static_cast<int>(cdiv(M, PM));
-    l.tn = static_cast<int>(cdiv(N, 2 * BN));
-    l.KB = static_cast<int>(cdiv(depth, BK));
-    l.rows = static_cast<int>(std::min<int64_t>(M, PM));
-    const int64_t tiles = static_cast<int64_t>(l.tm) * l.tn;
-    l.whole = static_cast<int>(tiles / pairs * pairs);
-    int64_t rest = tiles - l.whole;
-    l.splits = 1;
-    if (rest > 0) {
-        const double tile_mb = static_cast<double>(l.rows) * 2 * BN * 4 * 2 / 1e6;
-        double best = 1e300;
-        const int64_t most = std::min<int64_t>(l.KB, std::max<int64_t>(1, 4 * pairs / rest));
+    for (int width = 2 * BN; width >= BN; width -= BN) {
+        LinPlan l{};
+        l.width = width;
+        l.tm = static_cast<int>(cdiv(M, PM));
+        l.tn = static_cast<int>(cdiv(N, width));
+        l.KB = static_cast<int>(cdiv(depth, BK));
+        l.rows = static_cast<int>(std::min<int64_t>(M, PM));
+        const double block = width > BN ? 0.66 : 0.37;
+        const int64_t tiles = static_cast<int64_t>(l.tm) * l.tn, whole = tiles / pairs * pairs, rest = tiles - whole;
+        const double tile_mb = static_cast<double>(l.rows) * width * 4 * 2 / 1e6;
+        const int64_t most = rest == 0 ? 1 : std::min<int64_t>(l.KB, std::max<int64_t>(1, 4 * pairs / rest));
         for (int64_t s = 1; s <= most; ++s) {
-            const double joined = s > 1 ? 4.0 + tile_mb / 2 * static_cast<double>(rest * s) : 0.0;
-            const double cost = static_cast<double>(cdiv(rest * s, pairs) * (cdiv(l.KB, s) + 2)) + joined;
-            if (cost < best - 1e-9) {
-                best = cost;
-                l.splits = static_cast<int>(s);
-            }
-        }
-        if (l.splits == 1) {
-            l.whole = static_cast<int>(tiles);
-            rest = 0;
+            const double joined = s > 1 ? 4.0 + tile_mb / 4 * static_cast<double>(rest * s) : 0.0;
+            const double cost = static_cast<double>(whole / pairs) * l.KB * block +
+                                static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(l.KB, s)) * block + 3.0) + joined;
+            if (cost >= least - 1e-9) continue;
+            least = cost;
+            l.splits = static_cast<int>(s);
+            l.whole = static_cast<int>(s > 1 ? whole : tiles);
+            l.rest = static_cast<int>(s > 1 ? rest : 0);
+            l.units = l.whole + l.rest * l.splits;
+            l.part_bytes = static_cast<size_t>(l.rest) * l.splits * l.rows * 2 * BN * 4;
+            best = l;
         }
     }
-    l.rest = static_cast<int>(rest);
-    l.units = l.whole + l.rest * l.splits;
-    l.part_bytes = static_cast<size_t>(l.rest) * l.splits * l.rows * 2 * BN * 4;
-    return l;
+    return best;
 }
 
 // The products' shared memory, once per device.
@@ -57,6 +56,8 @@ flp_status linear_attrs() {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!done[dev]) {
         FLP_CUDA(cudaFuncSetAttribute(flp_linear_kernel<1, LIN_NONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        FLP_CUDA(cudaFuncSetAttribute(flp_linear_turned_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
+        FLP_CUDA(cudaFuncSetAttribute(flp_linear_turned_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC));
         for (int act = LIN_NONE; act <= LIN_SILU; ++act) {
             const cudaError_t e = lin_with_act(act, [](auto a) {
                 return cudaFuncSetAttribute(flp_linear_kernel<0, decltype(a)::value>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -86,6 +87,7 @@ flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const vo
     LinParams p{};
     p.tm = l.tm;
     p.tn = l.tn;
+    p.width = l.width;
     p.group = std::min(l.tm, 8);
     p.whole = l.whole;
     p.splits = l.splits;
@@ -110,8 +112,79 @@ flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const vo
                        "flp_linear_join_kernel launch", true, p);
 }
 
-// Up to this many rows W is read by the rows kernel.
-constexpr int64_t kLinFewRows = 8;
+// ---------------------------------------------------------------- turned tiles
+
+struct LinTurnPlan {
+    int nt, tiles_t, tiles_w, split, stages;
+    size_t smem;
+};
+
+// Rows of x in as few tiles as hold them, evenly; the contraction split over as many CTAs
+// as are resident (two an SM while their stages fit its shared memory).
+LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
+    LinTurnPlan t{};
+    t.tiles_t = static_cast<int>(cdiv(M, LT_MAX_T));
+    t.nt = static_cast<int>(cdiv(cdiv(M, t.tiles_t), 16) * 16);
+    t.tiles_w = static_cast<int>(cdiv(N, 128));
+    const int64_t KB = cdiv(depth, BK), tiles = static_cast<int64_t>(t.tiles_t) * t.tiles_w;
+    const int per_sm = t.nt <= 128 ? 2 : 1;
+    t.split = 1;
+    while (t.split < 8 && tiles * t.split * 2 <= per_sm * sm_count && t.split * 2 <= KB) t.split *= 2;
+    const size_t room = per_sm == 2 ? 108 * 1024 : 216 * 1024, stage = lin_turn_stage(t.nt);
+    t.stages = static_cast<int>(std::min<int64_t>({LT_STAGES, static_cast<int64_t>(room / stage), cdiv(KB, t.split)}));
+    t.smem = std::max<size_t>(t.stages * stage, static_cast<size_t>(t.nt) * 128 * 4) + 1024;
+    return t;
+}
+
+flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const void* w, int64_t ldw, bool w_mn, int64_t M,
+                         int64_t N, int64_t depth, const LinEpilogue& e, int* err, unsigned long long wait_limit_ns,
+                         int stall_after, bool after_kernel, cudaStream_t s) {
+    constexpr auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap mw, mx;
+    flp_status st = w_mn ? tmap_2d(&mw, BF, w, N, depth, ldw * 2, 64, 64) : tmap_2d(&mw, BF, w, depth, N, ldw * 2, BK, 128);
+    if (st == FLP_OK) st = tmap_2d(&mx, BF, x, depth, M, ldx * 2, BK, static_cast<uint32_t>(t.nt));
+    if (st != FLP_OK) return st;
+    LinTurnParams p{};
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.KB = static_cast<int>(cdiv(depth, BK));
+    p.nt = t.nt;
+    p.tiles_t = t.tiles_t;
+    p.split = t.split;
+    p.stages = t.stages;
+    for (p.cols = 32; p.cols < static_cast<uint32_t>(t.nt);) p.cols *= 2;
+    p.e = e;
+    p.err = err;
+    p.wait_limit_ns = wait_limit_ns;
+    p.stall_after = stall_after;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(t.tiles_t * t.tiles_w * t.split));
+    cfg.blockDim = dim3(LT_THREADS);
+    cfg.dynamicSmemBytes = t.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (t.split > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(t.split);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (after_kernel) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    const cudaError_t r = w_mn ? cudaLaunchKernelEx(&cfg, flp_linear_turned_kernel<1>, mw, mx, p)
+                               : cudaLaunchKernelEx(&cfg, flp_linear_turned_kernel<0>, mw, mx, p);
+    return r == cudaSuccess ? FLP_OK : cuda_fail(r, "flp_linear_turned_kernel launch");
+}
+
+// Up to this many rows W is read by the rows kernel, and up to this many by turned tiles.
+constexpr int64_t kLinTurnedRows = 256;
+
+constexpr int64_t kLinFewRows = 1;
 
 flp_status linear_rows(LinRowsParams& p, bool loose, int sm_count, bool after_kernel, cudaStream_t s) {
     // warps of the grid: eight an SM before a row's contraction is split
@@ -133,7 +206,7 @@ flp_status linear_rows(LinRowsParams& p, bool loose, int sm_count, bool after_ke
 flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 1 || K < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0, N >= 1 and K >= 1 required");
     const int64_t most = kMaxRows - 1024;
-    if (M > most || N > most || K > most || cdiv(M, PM) * cdiv(N, 2 * BN) > (1 << 22) || cdiv(M, PM) * cdiv(K, 2 * BN) > (1 << 22))
+    if (M > most || N > most || K > most || cdiv(M, PM) * cdiv(N, BN) > (1 << 23) || cdiv(M, PM) * cdiv(K, BN) > (1 << 23))
         return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
     return FLP_OK;
 }
@@ -160,14 +233,20 @@ struct Regions {
 
 struct LinearLayout {
     LinPlan l;
+    LinTurnPlan t;
     size_t off_x, off_w, off_part, bytes;
-    bool few, copy_x, copy_w;
+    bool few, turned, copy_x, copy_w;
 };
 
-LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K, int pairs) {
+LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K, int sm_count,
+                           int pairs) {
     LinearLayout f{};
     f.few = M <= kLinFewRows;
-    if (!f.few) f.l = plan_linear(M, N, K, pairs);
+    f.turned = !f.few && M <= kLinTurnedRows;
+    if (f.turned)
+        f.t = plan_turned(M, N, K, sm_count);
+    else if (!f.few)
+        f.l = plan_linear(M, N, K, pairs);
     f.copy_x = !rows_bf16(X, ldx) || (f.few && K % 8 != 0);  // whole vectors of x
     f.copy_w = !f.few && !rows_bf16(W, ldw);
     Regions r;
@@ -179,7 +258,9 @@ LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ld
 }
 
 struct LinearGradLayout {
-    LinPlan l;  // of dx
+    LinPlan l;  // of dx, or
+    LinTurnPlan t;
+    bool turned;
     size_t off_dw, off_x, off_w, off_d, off_part, off_sums, bytes;
     bool copy_x, copy_w, make_d, sums;
     int blocks, rows;  // of the column sums
@@ -191,7 +272,11 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
                                     int activation, bool want_dx, bool want_dw, bool want_db, int64_t M, int64_t N, int64_t K,
                                     int dw_dtype, int sm_count, int pairs) {
     LinearGradLayout g{};
-    g.l = plan_linear(M, K, N, pairs);
+    g.turned = M <= kLinTurnedRows;
+    if (g.turned)
+        g.t = plan_turned(M, K, N, sm_count);
+    else
+        g.l = plan_linear(M, K, N, pairs);
     g.copy_x = want_dw && !rows_bf16(X, ldx);
     g.copy_w = want_dx && !rows_bf16(W, ldw);
     g.make_d = (want_dx || want_dw) && (activation != FLP_ACT_NONE || !rows_bf16(dY, lddy));
@@ -222,7 +307,7 @@ extern "C" flp_status flp_linear_workspace(const void* X, int64_t ldx, const voi
     if (st != FLP_OK) return st;
     DevInfo* d;
     if ((st = check_device(&d)) != FLP_OK) return st;
-    *bytes = M == 0 ? 0 : linear_layout(X, ldx, W, ldw, M, N, K, d->pairs).bytes;
+    *bytes = M == 0 ? 0 : linear_layout(X, ldx, W, ldw, M, N, K, d->sm_count, d->pairs).bytes;
     return FLP_OK;
 }
 
@@ -245,7 +330,7 @@ extern "C" flp_status flp_linear(const void* X, int64_t ldx, const void* W, int6
     if (st == FLP_OK) st = check_on_current_device(X, "X");
     if (st == FLP_OK) st = linear_attrs();
     if (st != FLP_OK) return st;
-    const LinearLayout f = linear_layout(X, ldx, W, ldw, M, N, K, d->pairs);
+    const LinearLayout f = linear_layout(X, ldx, W, ldw, M, N, K, d->sm_count, d->pairs);
     if (f.bytes > 0 && (!workspace || workspace_bytes < f.bytes || !aligned16(workspace)))
         return fail(FLP_ERR_WORKSPACE, "linear workspace null, misaligned or too small");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -283,6 +368,7 @@ extern "C" flp_status flp_linear(const void* X, int64_t ldx, const void* W, int6
         p.e = e;
         return linear_rows(p, !(rows_bf16(W, ldw) && K % 8 == 0), d->sm_count, after, s);
     }
+    if (f.turned) return linear_turned(f.t, X, ldx, W, ldw, false, M, N, K, e, nullptr, kWaitLimitNs, -1, after, s);
     return linear_product(f.l, X, ldx, W, ldw, false, M, N, K, e, ws + f.off_part, nullptr, d->pairs, kWaitLimitNs, -1, after, s);
 }
 
@@ -383,7 +469,8 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         e.y = static_cast<bf16*>(dX);
         e.ldy = lddx;
         e.vec = rows_bf16(dX, lddx) && K % 8 == 0;
-        st = linear_product(g.l, dY, lddy, W, ldw, true, M, K, N, e, ws + g.off_part, err, d->pairs, kWaitLimitNs, -1, after, s);
+        st = g.turned ? linear_turned(g.t, dY, lddy, W, ldw, true, M, K, N, e, err, kWaitLimitNs, -1, after, s)
+                      : linear_product(g.l, dY, lddy, W, ldw, true, M, K, N, e, ws + g.off_part, err, d->pairs, kWaitLimitNs, -1, after, s);
         if (st != FLP_OK) return st;
         after = true;
     }
@@ -391,13 +478,15 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
 }
 
 // M = 192 rows, N = 520 columns (two 256 x 512 tiles, the second of 8 columns), 192 deep:
-// three blocks a tile, on one CTA pair; split: both tiles through partial tiles of one block.
-extern "C" flp_status flp_selftest_linear_timeout(void* workspace, size_t workspace_bytes, int split, int stall_after,
+// three blocks a tile, on one CTA pair; form 1: both tiles through partial tiles of one
+// block; forms 2 and 3: turned tiles, in 3 over three CTAs of one block each.
+extern "C" flp_status flp_selftest_linear_timeout(void* workspace, size_t workspace_bytes, int form, int stall_after,
                                                   int64_t wait_limit_ns, void* stream) {
     if (!workspace || !aligned16(workspace) || workspace_bytes < FLP_SELFTEST_LINEAR_BYTES)
         return fail(FLP_ERR_WORKSPACE, "self-test needs FLP_SELFTEST_LINEAR_BYTES of workspace");
     if (wait_limit_ns <= 0 || wait_limit_ns > 60ll * 1000 * 1000 * 1000)
         return fail(FLP_ERR_INVALID_ARG, "wait_limit_ns must be in (0, 60 s]");
+    if (form < 0 || form > 3) return fail(FLP_ERR_INVALID_ARG, "form must be 0 to 3");
     DevInfo* d;
     flp_status st = check_device(&d);
     if (st == FLP_OK) st = check_on_current_device(workspace, "workspace");
@@ -405,6 +494,9 @@ extern "C" flp_status flp_selftest_linear_timeout(void* workspace, size_t worksp
     if (st != FLP_OK) return st;
     const int64_t M = 192, N = 520, K = 192;
     LinPlan l = plan_linear(M, N, K, 1);
+    l.width = 2 * BN;
+    l.tn = 2;
+    const bool split = form == 1;
     l.splits = split ? 3 : 1;
     l.whole = split ? 0 : 2;
     l.rest = split ? 2 : 0;
@@ -425,7 +517,16 @@ extern "C" flp_status flp_selftest_linear_timeout(void* workspace, size_t worksp
     FLP_CUDA(cudaMemsetAsync(ws, 0, zero, s));                       // error word, x, W
     FLP_CUDA(cudaMemsetAsync(ws + off_part, 0x3f, r.bytes - off_part, s));  // what the partial tiles
     FLP_CUDA(cudaMemsetAsync(e.y, 0x3f, M * N * 2, s));              // and the result have to replace
-    st = linear_product(l, ws + off_x, K, ws + off_w, K, false, M, N, K, e, ws + off_part, reinterpret_cast<int*>(ws), 1,
-                        static_cast<unsigned long long>(wait_limit_ns), stall_after < 0 ? -1 : stall_after, false, s);
+    const unsigned long long limit = static_cast<unsigned long long>(wait_limit_ns);
+    const int stall = stall_after < 0 ? -1 : stall_after;
+    int* err = reinterpret_cast<int*>(ws);
+    if (form >= 2) {
+        LinTurnPlan turned = plan_turned(M, N, K, 1);
+        turned.split = form == 3 ? 3 : 1;
+        turned.stages = 2;
+        st = linear_turned(turned, ws + off_x, K, ws + off_w, K, false, M, N, K, e, err, limit, stall, false, s);
+        return st == FLP_OK ? flp_get_error(workspace, stream) : st;
+    }
+    st = linear_product(l, ws + off_x, K, ws + off_w, K, false, M, N, K, e, ws + off_part, err, 1, limit, stall, false, s);
     return st == FLP_OK ? flp_get_error(workspace, stream) : st;
 }

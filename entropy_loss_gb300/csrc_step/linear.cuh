@@ -138,7 +138,8 @@ struct LinEpilogue {
 };
 
 struct LinParams {
-    int tm, tn;   // 256-row and 512-column tiles
+    int tm, tn;   // tiles of 256 rows and of `width` columns
+    int width;    // 512, or 256: tiles of one half, in the two accumulators by turns
     int group;    // row tiles that share their column tiles while both are in L2
     int whole;    // tiles that are written directly (units 0 .. whole - 1)
     int splits;   // runs of each other tile
@@ -160,6 +161,14 @@ struct LinUnit {
     int halves;    // 256-column halves that hold columns
 };
 
+// The accumulator (and epilogue group) of the one half of a pair's `it`-th tile, and the
+// half of a tile that epilogue group g drains (-1: none).
+__device__ __forceinline__ int lin_single(const LinParams& p, int it) { return p.width == BN ? it & 1 : 0; }
+__device__ __forceinline__ int lin_half(const LinParams& p, const LinUnit& t, int g, int it) {
+    if (t.halves == 2) return g;
+    return g == lin_single(p, it) ? 0 : -1;
+}
+
 __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
     LinUnit t;
     int tile = u;
@@ -177,9 +186,9 @@ __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
     const int g = tile / per;
     const int rows = min(p.group, p.tm - g * p.group);
     const int r = tile - g * per;
-    t.n0 = r / rows * (2 * BN);
+    t.n0 = r / rows * p.width;
     t.m0 = (g * p.group + r % rows) * PM;
-    t.halves = t.n0 + BN < p.N ? 2 : 1;
+    t.halves = p.width > BN && t.n0 + BN < p.N ? 2 : 1;
     return t;
 }
 
@@ -267,18 +276,19 @@ __device__ __forceinline__ void lin_pack(const uint64_t (&v)[16], uint32_t (&w)[
     }
 }
 
-// NaN in what an epilogue group (half g of a tile, the 128 rows from `rofs` on) has not
-// finished, from unit u on: what a timed-out product leaves there is no result.
-__device__ __noinline__ void lin_fill_nan(const LinParams& p, int u, int npairs, int g, int rofs, int et) {
-    for (; u < p.units; u += npairs) {
+// NaN in what epilogue group g (of the 128 rows from `rofs` on) has not finished, from
+// unit u on, its pair's `it`-th: what a timed-out product leaves there is no result.
+__device__ __noinline__ void lin_fill_nan(const LinParams& p, int u, int it, int npairs, int g, int rofs, int et) {
+    for (; u < p.units; u += npairs, ++it) {
         const LinUnit t = lin_unit(p, u);
-        if (g >= t.halves) continue;
-        const int m0 = t.m0 + rofs, n0 = t.n0 + g * BN;
+        const int half = lin_half(p, t, g, it);
+        if (half < 0) continue;
+        const int m0 = t.m0 + rofs, n0 = t.n0 + half * BN;
         const int rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
         for (int r = 0; r < rows; ++r)
             for (int c = et; c < cols; c += EPI_THREADS) {
                 if (t.part >= 0) {
-                    p.part[(static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + g * BN + c] = __uint_as_float(0x7fc00000u);
+                    p.part[(static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + half * BN + c] = __uint_as_float(0x7fc00000u);
                 } else {
                     p.e.y[static_cast<long long>(m0 + r) * p.e.ldy + n0 + c] = __ushort_as_bfloat16(0x7fc0);
                     if (p.e.pre) p.e.pre[static_cast<long long>(m0 + r) * p.e.ldpre + n0 + c] = __ushort_as_bfloat16(0x7fc0);
@@ -372,13 +382,13 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             uint32_t gk = 0;    // k-blocks consumed so far
             uint32_t uses = 0;  // bit h: parity of the uses of accumulator h so far
             bool ok = true;
-            auto issue = [&](uint32_t g, int h, bool first) {
+            auto issue = [&](uint32_t g, int acc, int half, bool first) {
                 const int s = static_cast<int>(g % STAGES_W);
                 const uint32_t a = smem_addr(sm.base + slot_a(true, s));
-                const uint32_t b = smem_addr(sm.base + slot_b(true, s)) + h * B_STAGE_BYTES;
+                const uint32_t b = smem_addr(sm.base + slot_b(true, s)) + half * B_STAGE_BYTES;
 #pragma unroll
                 for (int k = 0; k < BK / UMMA_K; ++k)
-                    umma_bf16_pair(tmem_base + static_cast<uint32_t>(h * BN), operand_desc<0>(a, k),
+                    umma_bf16_pair(tmem_base + static_cast<uint32_t>(acc * BN), operand_desc<0>(a, k),
                                    operand_desc<B_MN>(b, k), idesc, (!first || k > 0) ? 1u : 0u);
             };
             auto wait_full = [&](uint32_t g) {
@@ -396,20 +406,23 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 umma_commit_pair_mc(&sm.tfull[h], PAIR_MASK);
                 uses ^= 1u << h;
             };
-            for (int u = pair; u < p.units && ok; u += npairs) {
+            int it = 0;
+            for (int u = pair; u < p.units && ok; u += npairs, ++it) {
                 const LinUnit t = lin_unit(p, u);
                 const int KB = t.kb1 - t.kb0;
-                ok = wait_tempty(0);
-                if (!ok) break;
                 if (t.halves == 1) {
+                    const int acc = lin_single(p, it);
+                    ok = wait_tempty(acc);
                     for (int kb = 0; kb < KB && ok; ++kb) {
                         ok = wait_full(gk + kb);
                         if (!ok) break;
-                        issue(gk + kb, 0, kb == 0);
+                        issue(gk + kb, acc, 0, kb == 0);
                         release(gk + kb);
                     }
-                    if (ok) publish(0);
+                    if (ok) publish(acc);
                 } else {
+                    ok = wait_tempty(0);
+                    if (!ok) break;
                     // halves staggered at both ends of the tile: half 0 completes (and is
                     // drained) under the last half-1 MMAs, and fills while the previous
                     // tile's half 1 is still drained
@@ -417,31 +430,31 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     const int tail0 = max(head, KB - WIDE_EDGE);
                     for (int kb = 0; kb < head && ok; ++kb) {
                         ok = wait_full(gk + kb);
-                        if (ok) issue(gk + kb, 0, kb == 0);
+                        if (ok) issue(gk + kb, 0, 0, kb == 0);
                     }
                     if (!ok) break;
                     if (head == KB) publish(0);
                     ok = wait_tempty(1);
                     if (!ok) break;
                     for (int kb = 0; kb < head; ++kb) {
-                        issue(gk + kb, 1, kb == 0);
+                        issue(gk + kb, 1, 1, kb == 0);
                         release(gk + kb);
                     }
                     for (int kb = head; kb < tail0 && ok; ++kb) {
                         ok = wait_full(gk + kb);
                         if (!ok) break;
-                        issue(gk + kb, 0, false);
-                        issue(gk + kb, 1, false);
+                        issue(gk + kb, 0, 0, false);
+                        issue(gk + kb, 1, 1, false);
                         release(gk + kb);
                     }
                     for (int kb = tail0; kb < KB && ok; ++kb) {
                         ok = wait_full(gk + kb);
-                        if (ok) issue(gk + kb, 0, false);
+                        if (ok) issue(gk + kb, 0, 0, false);
                     }
                     if (!ok) break;
                     if (head < KB) publish(0);
                     for (int kb = tail0; kb < KB; ++kb) {
-                        issue(gk + kb, 1, false);
+                        issue(gk + kb, 1, 1, false);
                         release(gk + kb);
                     }
                     publish(1);
@@ -469,10 +482,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         StoreRing ring;
         uint32_t phase = 0;
         bool ok = true;
-        int u = pair;
-        for (; u < p.units; u += npairs) {
+        int u = pair, it = 0;
+        for (; u < p.units; u += npairs, ++it) {
             const LinUnit t = lin_unit(p, u);
-            if (g >= t.halves) continue;
+            const int half = lin_half(p, t, g, it);
+            if (half < 0) continue;
             const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
             // every thread of the group takes the same branch (the box barriers need all of them)
             if (!named_bar_all(bar_vote, EPI_THREADS, ready)) {
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
             phase ^= 1u;
             tc_fence_after();
-            const int m0 = t.m0 + rofs, n0 = t.n0 + g * BN;
+            const int m0 = t.m0 + rofs, n0 = t.n0 + half * BN;
             const int row = m0 + r;
             const int boxes = min(BN / 32, (p.N - n0 + 31) / 32);  // the others lie past the last column
 #pragma unroll 1
@@ -496,7 +510,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 if (t.part >= 0) {
                     if (row < p.M) {
                         float4* o = reinterpret_cast<float4*>(
-                            p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + g * BN + b * 32);
+                            p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + half * BN + b * 32);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             o[i] = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]),
@@ -548,7 +562,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         if (et == 0) bulk_wait_group<0>();
         if (!ok) {
             named_bar_sync(bar_vote, EPI_THREADS);  // behind the group's earlier stores
-            lin_fill_nan(p, u, npairs, g, rofs, et);
+            lin_fill_nan(p, u, it, npairs, g, rofs, et);
         }
     }
 
@@ -572,7 +586,10 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
     for (int i = 0; i < C; ++i) v[i] = 0.f;
     bool on[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) on[i] = t.n0 + static_cast<int>(threadIdx.x) + i * LJ_THREADS < p.N;
+    for (int i = 0; i < C; ++i) {
+        const int at = static_cast<int>(threadIdx.x) + i * LJ_THREADS;
+        on[i] = at < p.width && t.n0 + at < p.N;
+    }
 #pragma unroll 4
     for (int s = 0; s < p.splits; ++s)
 #pragma unroll
@@ -589,6 +606,222 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
         x = lin_act_of(x, p.e.act);
         if (p.e.residual) x += __bfloat162float(p.e.residual[row * p.e.ldr + c]);
         p.e.y[row * p.e.ldy + c] = __float2bfloat16_rn(x);
+    }
+}
+
+// ------------------------------------------------------------------ turned tiles
+//
+// For few rows of x: W's rows are the 128 rows of a tile and x's (up to 256, a multiple of
+// 16) its columns, so that a tile moves next to nothing but W, and a CTA by itself holds
+// 128 columns of y, one a thread.  The `split` CTAs of a cluster share a tile, each with a
+// part of the contraction; their fp32 sums are joined through distributed shared memory,
+// each CTA taking a part of the rows of x through the epilogue.  A bounded wait that runs
+// out makes the tile NaN.
+
+constexpr int LT_THREADS = 192;
+constexpr int LT_STAGES = 12;  // at most
+constexpr int LT_MAX_T = 256;
+constexpr uint32_t LT_A_BYTES = 128 * BK * 2;
+
+struct LinTurnParams {
+    int M, N;
+    int KB;      // 64-deep blocks of the contraction
+    int nt;      // rows of x in a tile
+    int tiles_t; // tiles along the rows of x
+    int split;   // CTAs of a tile
+    int stages;
+    uint32_t cols;  // of TMEM
+    LinEpilogue e;
+    int* err;
+    unsigned long long wait_limit_ns;
+    int stall_after;
+};
+
+struct LinTurnShared {
+    uint64_t full[LT_STAGES], empty[LT_STAGES], done, drain;
+    uint32_t tmem;
+    int abort, bad;  // bad: this CTA's sums are incomplete
+};
+
+// Bytes of a stage, and of the shared memory of a launch.
+__host__ __device__ inline uint32_t lin_turn_stage(int nt) { return LT_A_BYTES + static_cast<uint32_t>(nt) * (BK * 2); }
+
+// Column r of the tile through the epilogue, for this CTA's share of the rows of x: the
+// CTAs' sums [nt][128] added in order.
+template <int ACT>
+__device__ __forceinline__ void lin_turn_out(const LinTurnParams& p, uint32_t sums, int rank, int n, int t0, bool bad) {
+    constexpr int G = 4;  // rows under way
+    const int rows = min(p.nt, p.M - t0);
+    float bias = 0.f;
+    if (p.e.bias)
+        bias = p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[n] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[n]);
+    if (bad) bias = __uint_as_float(0x7fc00000u);
+    for (int c = rank; c < rows; c += G * p.split) {
+        float v[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) v[g] = 0.f;
+        for (int i = 0; i < p.split; ++i) {
+            const uint32_t from = mapa_shared(sums, i);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (c + g * p.split < rows) v[g] += ld_cluster_f32(from + (c + g * p.split) * 512);
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) v[g] += bias;
+        if (p.e.pre) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (c + g * p.split < rows) p.e.pre[(t0 + c + g * p.split) * p.e.ldpre + n] = __float2bfloat16_rn(v[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < G; g += 2) f2_unpack(lin_act2<ACT>(f2_pack(v[g], v[g + 1])), v[g], v[g + 1]);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (c + g * p.split >= rows) continue;
+            const long long m = t0 + c + g * p.split;
+            if (p.e.residual) v[g] += __bfloat162float(p.e.residual[m * p.e.ldr + n]);
+            p.e.y[m * p.e.ldy + n] = __float2bfloat16_rn(v[g]);
+        }
+    }
+}
+
+template <int A_MN>
+__global__ void __launch_bounds__(LT_THREADS)
+    flp_linear_turned_kernel(const __grid_constant__ CUtensorMap tmW,  // K-major (64 x 128 boxes) or MN-major (64 x 64)
+                             const __grid_constant__ CUtensorMap tmX,  // K-major (64 x nt)
+                             const __grid_constant__ LinTurnParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ LinTurnShared sh;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int tile = blockIdx.x / p.split;
+    const int n0 = tile / p.tiles_t * 128, t0 = tile % p.tiles_t * p.nt;
+    const int kb0 = static_cast<int>(static_cast<long long>(p.KB) * rank / p.split);
+    const int kb1 = static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / p.split);
+    const uint32_t stage_bytes = lin_turn_stage(p.nt);
+    volatile int* abort_flag = &sh.abort;
+    const uint64_t limit = p.wait_limit_ns;
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        mbar_init(&sh.done, 1);
+        mbar_init(&sh.drain, 1);
+        sh.abort = sh.bad = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem, p.cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    griddep_wait();  // aligned copies and the cleared error word are complete from here on
+    auto raise = [&]() {
+        if (p.err) atomicOr(p.err, ERR_TIMEOUT);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (p.stall_after >= 0 && kb - kb0 == p.stall_after) break;  // stop feeding the MMA
+                if (!mbar_wait(&sh.empty[stage], phase ^ 1u, limit, abort_flag)) {
+                    raise();
+                    break;
+                }
+                uint8_t* a = base + stage * stage_bytes;
+                mbar_arrive_expect_tx(&sh.full[stage], stage_bytes);
+                if (A_MN == 0) {
+                    tma_load_2d(a, &tmW, kb * BK, n0, &sh.full[stage]);
+                } else {
+                    tma_load_2d(a, &tmW, n0, kb * BK, &sh.full[stage]);
+                    tma_load_2d(a + 8192, &tmW, n0 + 64, kb * BK, &sh.full[stage]);
+                }
+                tma_load_2d(a + LT_A_BYTES, &tmX, kb * BK, t0, &sh.full[stage]);
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_f32(128, p.nt, A_MN, 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                ok = mbar_wait(&sh.full[stage], phase, limit, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a = smem_addr(base + stage * stage_bytes), b = a + LT_A_BYTES;
+#pragma unroll
+                for (int k = 0; k < BK / UMMA_K; ++k)
+                    umma_bf16(tmem, operand_desc<A_MN>(a, k), operand_desc<0>(b, k), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+                umma_commit(&sh.empty[stage]);
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+            if (ok)
+                umma_commit(&sh.done);
+            else
+                raise();
+            umma_commit(&sh.drain);  // every MMA issued so far has completed
+            volatile int no_abort = 0;
+            mbar_wait(&sh.drain, 0, limit, &no_abort);
+        }
+    } else {
+        const int q = warp & 3, r = q * 32 + lane;  // accumulator row == TMEM lane
+        const bool ok = named_bar_all(1, EPI_THREADS, mbar_wait(&sh.done, 0, limit, abort_flag));
+        if (ok) {
+            tc_fence_after();
+            float* part = reinterpret_cast<float*>(base);  // [nt][128]: every MMA has read its operands
+            const int rows = min(p.nt, p.M - t0);
+            for (int c = 0; c < rows; c += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + c + (static_cast<uint32_t>(q * 32) << 16), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c + j < p.nt) part[(c + j) * 128 + r] = __uint_as_float(v[j]);
+            }
+        } else {
+            raise();
+            sh.bad = 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (p.split > 1) cluster_sync();  // every CTA's sums are there
+    const int n = n0 + static_cast<int>(threadIdx.x);
+    if (threadIdx.x < 128 && n < p.N) {
+        uint32_t bad = 0;
+        for (int i = 0; i < p.split; ++i) bad |= ld_cluster_u32(mapa_shared(smem_addr(&sh.bad), i));
+        const uint32_t sums = smem_addr(base) + threadIdx.x * 4;
+        switch (p.e.act) {
+            case LIN_RELU: lin_turn_out<LIN_RELU>(p, sums, rank, n, t0, bad); break;
+            case LIN_GELU: lin_turn_out<LIN_GELU>(p, sums, rank, n, t0, bad); break;
+            case LIN_GELU_TANH: lin_turn_out<LIN_GELU_TANH>(p, sums, rank, n, t0, bad); break;
+            case LIN_SILU: lin_turn_out<LIN_SILU>(p, sums, rank, n, t0, bad); break;
+            default: lin_turn_out<LIN_NONE>(p, sums, rank, n, t0, bad);
+        }
+    }
+    if (*abort_flag) {  // copies in flight get a bounded grace period
+        const uint64_t start = globaltimer_ns();
+        while (globaltimer_ns() - start < 2000000ull) {
+        }
+    }
+    __syncthreads();
+    if (p.split > 1) cluster_sync();  // no CTA leaves while its sums are read
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, p.cols);
     }
 }
 

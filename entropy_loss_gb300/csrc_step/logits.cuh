@@ -293,12 +293,6 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 template <typename T, bool LOOSE, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_kernel(const TlpParams p) {
     constexpr int V = wide_v<T>(), NV = LOOSE ? 2 : 4, P = Pairs<T>::N, WARPS = THREADS / 32;

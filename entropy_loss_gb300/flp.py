@@ -405,13 +405,14 @@ def selftest_weight_grad_timeout(odd: bool, stall_after: int, wait_limit_ns: int
                                                        wait_limit_ns, _stream(stream)))
 
 
-def selftest_linear_timeout(split: bool, stall_after: int, wait_limit_ns: int, workspace=None, stream=None) -> int:
+def selftest_linear_timeout(form: int, stall_after: int, wait_limit_ns: int, workspace=None, stream=None) -> int:
     """Run a small linear layer with its producers stopped after `stall_after`
-    64-deep blocks (< 0: no stall) and every wait bounded by `wait_limit_ns`; with
-    `split` through partial tiles.  Returns the error status the run leaves."""
+    64-deep blocks (< 0: no stall) and every wait bounded by `wait_limit_ns`; form 0
+    whole tiles, 1 partial tiles, 2 the tiles of few rows, 3 those split over a
+    cluster.  Returns the error status the run leaves."""
     if workspace is None:
         workspace = torch.empty(SELFTEST_LINEAR_BYTES, dtype=torch.uint8, device="cuda")
-    return int(load().flp_selftest_linear_timeout(_ptr(workspace), _nbytes(workspace), int(bool(split)), stall_after,
+    return int(load().flp_selftest_linear_timeout(_ptr(workspace), _nbytes(workspace), int(form), stall_after,
                                                   wait_limit_ns, _stream(stream)))
 
 

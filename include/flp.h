@@ -650,15 +650,16 @@ flp_status flp_linear_backward(const void* dY, int64_t lddy, const void* X, int6
  * Self-test of the product's bounded waits, like flp_selftest_wait_timeout (a
  * diagnostic): M = 192, N = 520, K = 192 (two tiles of three 64-deep blocks), all
  * zeros, on one CTA pair, laid out in `workspace` (at least
- * FLP_SELFTEST_LINEAR_BYTES); with split != 0 through partial tiles of one block.
- * With stall_after >= 0 the TMA producers stop after that many blocks.  y, bf16
+ * FLP_SELFTEST_LINEAR_BYTES); with form 1 through partial tiles of one block, with
+ * form 2 in the tiles of few rows, with form 3 in those split over three CTAs of a
+ * block each.  With stall_after >= 0 the TMA producers stop after that many blocks.  y, bf16
  * [M, N], is left at byte offset FLP_SELFTEST_LINEAR_OUTPUT_OFFSET: zeros, or NaN
  * where the stall kept a tile from being finished.  Synchronises `stream` and
  * returns the error word (FLP_ERR_TIMEOUT or FLP_OK), or an argument / CUDA error.
  */
 #define FLP_SELFTEST_LINEAR_BYTES (4u << 20)
 #define FLP_SELFTEST_LINEAR_OUTPUT_OFFSET (3u << 20)
-flp_status flp_selftest_linear_timeout(void* workspace, size_t workspace_bytes, int split, int stall_after,
+flp_status flp_selftest_linear_timeout(void* workspace, size_t workspace_bytes, int form, int stall_after,
                                        int64_t wait_limit_ns, void* stream);
 
 /* Static description of a status code. */

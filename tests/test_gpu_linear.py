@@ -91,7 +91,7 @@ def run_forward(flp, M, N, K, act, bias, residual, keep, pads=(0, 0, 0, 0), offs
 
 
 SHAPES = [(1, 1, 1), (1, 8, 8), (1, 4096, 4096), (2, 513, 40), (3, 7, 1000), (8, 1000, 64), (9, 520, 65), (33, 256, 128), (128, 512, 264),
-          (129, 264, 72), (255, 1023, 63), (256, 512, 64), (257, 513, 129), (300, 2047, 1000), (777, 2047, 100), (1000, 1536, 512)]
+          (129, 264, 72), (255, 1023, 63), (256, 512, 64), (257, 513, 129), (300, 2047, 1000), (777, 2047, 100), (1000, 1536, 512), (16, 300, 4096), (17, 4096, 200), (48, 640, 1024), (144, 1000, 328), (600, 1100, 520)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -292,18 +292,20 @@ def test_workspaces(flp):
     assert flp.get_error(big) == flp.FLP_OK
 
 
-@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("form", [0, 1, 2, 3])
 @pytest.mark.parametrize("stall", [-1, 0, 1, 2, 3, 4])
-def test_bounded_waits(flp, split, stall):
+def test_bounded_waits(flp, form, stall):
+    """Whole tiles, partial tiles, the tiles of few rows, and those of a cluster: two tiles
+    (five of few rows) of three blocks, one block a CTA in the last form."""
     ws = torch.empty(flp.SELFTEST_LINEAR_BYTES, dtype=torch.uint8, device="cuda")
-    status = flp.selftest_linear_timeout(split, stall, 20_000_000, workspace=ws)
+    status = flp.selftest_linear_timeout(form, stall, 20_000_000, workspace=ws)
     at = flp.SELFTEST_LINEAR_OUTPUT_OFFSET
     y = ws[at:at + 192 * 520 * 2].view(torch.bfloat16).view(192, 520)
-    if stall < 0:
+    if stall < 0 or stall >= {0: 6, 1: 6, 2: 3, 3: 1}[form]:
         assert status == flp.FLP_OK and bool((y == 0).all())
         return
     assert status == flp.FLP_ERR_TIMEOUT
-    first, second = y[:, :512], y[:, 512:]  # three blocks each
-    assert bool((first == 0).all() if stall >= 3 else torch.isnan(first.float()).all())
+    first, second = y[:, :512], y[:, 512:]
+    assert bool((first == 0).all() if form < 2 and stall >= 3 else torch.isnan(first.float()).all())
     assert bool(torch.isnan(second.float()).all())
-    assert flp.selftest_linear_timeout(split, -1, 10 ** 9, workspace=ws) == flp.FLP_OK
+    assert flp.selftest_linear_timeout(form, -1, 10 ** 9, workspace=ws) == flp.FLP_OK

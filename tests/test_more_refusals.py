@@ -145,6 +145,8 @@ def test_linear_selftest(flp, b):
     assert f(b + 4, 1 << 30, 0, 1, 1000, None) == flp.FLP_ERR_WORKSPACE
     for limit in (0, -5, 61 * 10 ** 9):
         assert f(b, 1 << 30, 0, 1, limit, None) == flp.FLP_ERR_INVALID_ARG
+    for form in (-1, 4):
+        assert f(b, 1 << 30, form, 1, 1000, None) == flp.FLP_ERR_INVALID_ARG
 
 
 def test_binding_refuses_before_loading_anything_on_a_device(flp):
