@@ -12,7 +12,8 @@ struct LinPlan {
 };
 
 // Tiles of 256 x 512, or of 256 x 256 where they fill the pairs better.  Whole rounds of
-// tiles write their outputs; the rest are split into runs.  The least of what these cost:
+// tiles write their outputs; the rest do so too, or are split into their halves (0 splits)
+// or along the contraction.  The least of what these cost:
 // 0.66 us for a 64-deep block of a wide tile and 0.37 us of a narrow one (the rate at which
 // its operands arrive), 3 us for a run's start and end, and for joining 4 us (a launch) and
 // the partial tiles' bytes, written and read back at 4 TB/s.
@@ -31,16 +32,17 @@ LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
         const int64_t tiles = static_cast<int64_t>(l.tm) * l.tn, whole = tiles / pairs * pairs, rest = tiles - whole;
         const double tile_mb = static_cast<double>(l.rows) * width * 4 * 2 / 1e6;
         const int64_t most = rest == 0 ? 1 : std::min<int64_t>(l.KB, std::max<int64_t>(1, 4 * pairs / rest));
-        for (int64_t s = 1; s <= most; ++s) {
+        for (int64_t s = width > BN && rest > 0 ? 0 : 1; s <= most; ++s) {
             const double joined = s > 1 ? 4.0 + tile_mb / 4 * static_cast<double>(rest * s) : 0.0;
-            const double cost = static_cast<double>(whole / pairs) * l.KB * block +
-                                static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(l.KB, s)) * block + 3.0) + joined;
+            const double last = s == 0 ? static_cast<double>(cdiv(2 * rest, pairs)) * (l.KB * 0.37 + 3.0)
+                                       : static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(l.KB, s)) * block + 3.0);
+            const double cost = static_cast<double>(whole / pairs) * l.KB * block + last + joined;
             if (cost >= least - 1e-9) continue;
             least = cost;
             l.splits = static_cast<int>(s);
-            l.whole = static_cast<int>(s > 1 ? whole : tiles);
+            l.whole = static_cast<int>(s == 1 ? tiles : whole);
             l.rest = static_cast<int>(s > 1 ? rest : 0);
-            l.units = l.whole + l.rest * l.splits;
+            l.units = l.whole + (s == 0 ? static_cast<int>(2 * rest) : l.rest * l.splits);
             l.part_bytes = static_cast<size_t>(l.rest) * l.splits * l.rows * 2 * BN * 4;
             best = l;
         }

@@ -142,7 +142,7 @@ struct LinParams {
     int width;    // 512, or 256: tiles of one half, in the two accumulators by turns
     int group;    // row tiles that share their column tiles while both are in L2
     int whole;    // tiles that are written directly (units 0 .. whole - 1)
-    int splits;   // runs of each other tile
+    int splits;   // runs of each other tile; 0: its two halves, written directly
     int units;
     int KB;       // 64-deep blocks of the contraction
     int M, N;
@@ -158,15 +158,15 @@ struct LinUnit {
     int m0, n0;    // first row and column of the tile
     int kb0, kb1;  // blocks of the contraction
     int part;      // partial tile index, -1: the outputs are written
-    int halves;    // 256-column halves that hold columns
+    int halves;    // 256-column halves that hold columns (0: none)
 };
 
 // The accumulator (and epilogue group) of the one half of a pair's `it`-th tile, and the
 // half of a tile that epilogue group g drains (-1: none).
-__device__ __forceinline__ int lin_single(const LinParams& p, int it) { return p.width == BN ? it & 1 : 0; }
-__device__ __forceinline__ int lin_half(const LinParams& p, const LinUnit& t, int g, int it) {
+__device__ __forceinline__ int lin_single(int it) { return it & 1; }
+__device__ __forceinline__ int lin_half(const LinUnit& t, int g, int it) {
     if (t.halves == 2) return g;
-    return g == lin_single(p, it) ? 0 : -1;
+    return t.halves == 1 && g == lin_single(it) ? 0 : -1;
 }
 
 __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
@@ -175,7 +175,12 @@ __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
     t.part = -1;
     t.kb0 = 0;
     t.kb1 = p.KB;
-    if (u >= p.whole) {
+    int from = 0, width = p.width;  // of the tile, the unit's columns
+    if (u >= p.whole && p.splits == 0) {
+        tile = p.whole + (u - p.whole) / 2;
+        from = (u - p.whole) % 2 * BN;
+        width = BN;
+    } else if (u >= p.whole) {
         t.part = u - p.whole;
         tile = p.whole + t.part / p.splits;
         const int s = t.part % p.splits;
@@ -186,9 +191,10 @@ __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
     const int g = tile / per;
     const int rows = min(p.group, p.tm - g * p.group);
     const int r = tile - g * per;
-    t.n0 = r / rows * p.width;
+    t.n0 = r / rows * p.width + from;
     t.m0 = (g * p.group + r % rows) * PM;
-    t.halves = p.width > BN && t.n0 + BN < p.N ? 2 : 1;
+    t.halves = t.n0 >= p.N ? 0 : width > BN && t.n0 + BN < p.N ? 2 : 1;
+    if (t.halves == 0) t.kb1 = t.kb0;  // a half past the last column
     return t;
 }
 
@@ -239,7 +245,7 @@ __device__ __forceinline__ void lin_rows_out(uint32_t box, const uint32_t (&w)[1
     const int n = min(32, rows - row0);
     if (c0 + lane < N) {
         bf16* o = out + row0 * ld + c0 + lane;
-#pragma unroll 4
+#pragma unroll 8
         for (int r = 0; r < n; ++r) {
             const uint32_t u = ld_shared_4(lin_box_word(box + r * 64, r, lane >> 1));
             *reinterpret_cast<unsigned short*>(o + r * ld) = static_cast<unsigned short>(lane & 1 ? u >> 16 : u);
@@ -253,16 +259,17 @@ __device__ __forceinline__ void lin_rows_in(uint32_t box, uint32_t (&w)[16], con
     const int n = min(32, rows - row0);
     const bool on = c0 + lane < N;
     const bf16* o = in + row0 * ld + c0 + lane;
-#pragma unroll 4
-    for (int r = 0; r < n; ++r) {
-        const unsigned short u = on ? *reinterpret_cast<const unsigned short*>(o + r * ld) : 0;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(lin_box_word(box + r * 64, r, lane >> 1) + 2 * (lane & 1)), "h"(u) : "memory");
-    }
+    unsigned short u[32];  // every row's load under way at once
+#pragma unroll
+    for (int r = 0; r < 32; ++r) u[r] = on && r < n ? *reinterpret_cast<const unsigned short*>(o + r * ld) : 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(lin_box_word(box + r * 64, r, lane >> 1) + 2 * (lane & 1)), "h"(u[r]) : "memory");
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint4 u = ld_shared_16(lin_box_word(box + lane * 64, lane, 4 * i));
-        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        const uint4 x = ld_shared_16(lin_box_word(box + lane * 64, lane, 4 * i));
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
     }
     __syncwarp();
 }
@@ -281,7 +288,7 @@ __device__ __forceinline__ void lin_pack(const uint64_t (&v)[16], uint32_t (&w)[
 __device__ __noinline__ void lin_fill_nan(const LinParams& p, int u, int it, int npairs, int g, int rofs, int et) {
     for (; u < p.units; u += npairs, ++it) {
         const LinUnit t = lin_unit(p, u);
-        const int half = lin_half(p, t, g, it);
+        const int half = lin_half(t, g, it);
         if (half < 0) continue;
         const int m0 = t.m0 + rofs, n0 = t.n0 + half * BN;
         const int rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
@@ -410,8 +417,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             for (int u = pair; u < p.units && ok; u += npairs, ++it) {
                 const LinUnit t = lin_unit(p, u);
                 const int KB = t.kb1 - t.kb0;
+                if (t.halves == 0) continue;
                 if (t.halves == 1) {
-                    const int acc = lin_single(p, it);
+                    const int acc = lin_single(it);
                     ok = wait_tempty(acc);
                     for (int kb = 0; kb < KB && ok; ++kb) {
                         ok = wait_full(gk + kb);
@@ -485,7 +493,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         int u = pair, it = 0;
         for (; u < p.units; u += npairs, ++it) {
             const LinUnit t = lin_unit(p, u);
-            const int half = lin_half(p, t, g, it);
+            const int half = lin_half(t, g, it);
             if (half < 0) continue;
             const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
             // every thread of the group takes the same branch (the box barriers need all of them)
@@ -498,26 +506,39 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const int m0 = t.m0 + rofs, n0 = t.n0 + half * BN;
             const int row = m0 + r;
             const int boxes = min(BN / 32, (p.N - n0 + 31) / 32);  // the others lie past the last column
+            auto release = [&]() {
+                tc_fence_before();
+                mbar_arrive_cluster(tempty);
+            };
+            if (t.part >= 0) {
+                float4* o = reinterpret_cast<float4*>(
+                    p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + half * BN);
 #pragma unroll 1
-            for (int b = 0; b < boxes; ++b) {
-                uint32_t raw[32];
-                tmem_ld_32x32b_x32(tbase + b * 32, raw);
-                tmem_wait_ld();
-                if (b == boxes - 1) {
-                    tc_fence_before();
-                    mbar_arrive_cluster(tempty);
-                }
-                if (t.part >= 0) {
+                for (int b = 0; b < boxes; ++b) {
+                    uint32_t raw[32];
+                    tmem_ld_32x32b_x32(tbase + b * 32, raw);
+                    tmem_wait_ld();
+                    if (b == boxes - 1) release();
                     if (row < p.M) {
-                        float4* o = reinterpret_cast<float4*>(
-                            p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + half * BN + b * 32);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            o[i] = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]),
-                                               __uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3]));
+                            o[b * 8 + i] = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]),
+                                                       __uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3]));
                     }
-                    continue;
                 }
+                continue;
+            }
+            uint4 res[4];  // the next box's residual
+            auto fetch = [&](int b) {
+                const int c0 = n0 + b * 32;
+                const uint4* from = reinterpret_cast<const uint4*>(p.e.residual + row * p.e.ldr + c0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) res[i] = row < p.M && c0 + 8 * i < p.N ? from[i] : make_uint4(0, 0, 0, 0);
+            };
+            const bool direct_res = p.e.residual && p.e.vec;
+            if (direct_res) fetch(0);
+            auto drain = [&](int b, uint32_t(&raw)[32]) {
+                if (b >= boxes) return;
                 const int c0 = n0 + b * 32;
                 uint64_t v[16];
 #pragma unroll
@@ -534,13 +555,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = lin_act2<ACT>(v[j]);
                 if (p.e.residual) {
-                    if (p.e.vec) {
-                        const uint4* from = reinterpret_cast<const uint4*>(p.e.residual + row * p.e.ldr + c0);
+                    if (direct_res) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 x = row < p.M && c0 + 8 * i < p.N ? from[i] : make_uint4(0, 0, 0, 0);
-                            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            w[4 * i] = res[i].x, w[4 * i + 1] = res[i].y, w[4 * i + 2] = res[i].z, w[4 * i + 3] = res[i].w;
+                        if (b + 1 < boxes) fetch(b + 1);
                     } else if (m0 + q * 32 < p.M) {
                         lin_rows_in(box_in, w, p.e.residual, p.e.ldr, m0 + q * 32, p.M, c0, p.N);
                     } else {
@@ -556,6 +575,29 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     narrow_box_store(ring, box0, bar_box, et, r, w, &tmY, c0, m0, false);
                 else if (m0 + q * 32 < p.M)
                     lin_rows_out(box_out, w, p.e.y, p.e.ldy, m0 + q * 32, p.M, c0, p.N);
+            };
+            // a box ahead, so that the accumulator is free for the next tile while two boxes still
+            // go through the epilogue
+            uint32_t even[32], odd[32];
+            auto arrived = [&](uint32_t(&x)[32]) {
+                tmem_wait_ld();
+                tmem_pin(x);
+            };
+            tmem_ld_32x32b_x32(tbase, even);
+#pragma unroll 1
+            for (int b = 0; b < BN / 32; b += 2) {
+                arrived(even);
+                tmem_ld_32x32b_x32(tbase + b * 32 + 32, odd);
+                if (b + 2 == BN / 32) {
+                    arrived(odd);
+                    release();
+                }
+                drain(b, even);
+                if (b + 2 < BN / 32) {
+                    arrived(odd);
+                    tmem_ld_32x32b_x32(tbase + b * 32 + 64, even);
+                }
+                drain(b + 1, odd);
             }
         }
         if (!ok) lin_raise(sm, p.err);
