@@ -122,17 +122,16 @@ struct LinTurnPlan {
 };
 
 // Rows of x in as few tiles as hold them, evenly; the contraction split over as many CTAs
-// as are resident (two an SM while their stages fit its shared memory).
+// as are resident, two an SM.
 LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
     LinTurnPlan t{};
     t.tiles_t = static_cast<int>(cdiv(M, LT_MAX_T));
     t.nt = static_cast<int>(cdiv(cdiv(M, t.tiles_t), 16) * 16);
     t.tiles_w = static_cast<int>(cdiv(N, 128));
     const int64_t KB = cdiv(depth, BK), tiles = static_cast<int64_t>(t.tiles_t) * t.tiles_w;
-    const int per_sm = t.nt <= 128 ? 2 : 1;
     t.split = 1;
-    while (t.split < 8 && tiles * t.split * 2 <= per_sm * sm_count && t.split * 2 <= KB) t.split *= 2;
-    const size_t room = per_sm == 2 ? 108 * 1024 : 216 * 1024, stage = lin_turn_stage(t.nt);
+    while (t.split < 8 && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
+    const size_t room = 108 * 1024, stage = lin_turn_stage(t.nt);
     t.stages = static_cast<int>(std::min<int64_t>({LT_STAGES, static_cast<int64_t>(room / stage), cdiv(KB, t.split)}));
     t.smem = std::max<size_t>(t.stages * stage, static_cast<size_t>(t.nt) * 128 * 4) + 1024;
     return t;
@@ -183,26 +182,18 @@ flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const
     return r == cudaSuccess ? FLP_OK : cuda_fail(r, "flp_linear_turned_kernel launch");
 }
 
-// Up to this many rows W is read by the rows kernel, and up to this many by turned tiles.
-constexpr int64_t kLinTurnedRows = 256;
+// Turned tiles where they keep up: while memory sets the pace, or they do not need more
+// than one an SM (4096 x 4096: 512 rows 35 us, 39 in pairs' tiles, 1024 rows 48 and 39; 16384
+// x 4096: 64 rows 42 and 50, 256 rows 58 and 50).
+bool linear_turns(int64_t M, int64_t N, int sm_count) { return M <= 64 || cdiv(M, LT_MAX_T) * cdiv(N, 128) <= sm_count; }
 
-constexpr int64_t kLinFewRows = 1;
-
-flp_status linear_rows(LinRowsParams& p, bool loose, int sm_count, bool after_kernel, cudaStream_t s) {
+flp_status linear_row(LinRowParams& p, bool loose, int sm_count, bool after_kernel, cudaStream_t s) {
     // warps of the grid: eight an SM before a row's contraction is split
     p.kw = 1;
     while (p.kw < LR_WARPS && cdiv(p.N, LR_ROWS) * p.kw < 8 * sm_count && p.K > 256 * p.kw) p.kw *= 2;
     p.chunk = static_cast<int>(cdiv(cdiv(p.K, p.kw), 256) * 256);
-    const int64_t grid = cdiv(p.N, LR_ROWS * (LR_WARPS / p.kw));
-    auto rows = [&](auto mt) {
-        constexpr int MT = decltype(mt)::value;
-        return launch_step(loose ? flp_linear_rows_kernel<MT, true> : flp_linear_rows_kernel<MT, false>, grid, LR_THREADS, 0, s,
-                           "flp_linear_rows_kernel launch", after_kernel, p);
-    };
-    return p.M == 1   ? rows(std::integral_constant<int, 1>{})
-           : p.M == 2 ? rows(std::integral_constant<int, 2>{})
-           : p.M <= 4 ? rows(std::integral_constant<int, 4>{})
-                      : rows(std::integral_constant<int, 8>{});
+    return launch_step(loose ? flp_linear_row_kernel<true> : flp_linear_row_kernel<false>, cdiv(p.N, LR_ROWS * (LR_WARPS / p.kw)),
+                       LR_THREADS, 0, s, "flp_linear_row_kernel launch", after_kernel, p);
 }
 
 flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
@@ -237,20 +228,20 @@ struct LinearLayout {
     LinPlan l;
     LinTurnPlan t;
     size_t off_x, off_w, off_part, bytes;
-    bool few, turned, copy_x, copy_w;
+    bool one, turned, copy_x, copy_w;
 };
 
 LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K, int sm_count,
                            int pairs) {
     LinearLayout f{};
-    f.few = M <= kLinFewRows;
-    f.turned = !f.few && M <= kLinTurnedRows;
+    f.one = M == 1;
+    f.turned = !f.one && linear_turns(M, N, sm_count);
     if (f.turned)
         f.t = plan_turned(M, N, K, sm_count);
-    else if (!f.few)
+    else if (!f.one)
         f.l = plan_linear(M, N, K, pairs);
-    f.copy_x = !rows_bf16(X, ldx) || (f.few && K % 8 != 0);  // whole vectors of x
-    f.copy_w = !f.few && !rows_bf16(W, ldw);
+    f.copy_x = !rows_bf16(X, ldx) || (f.one && K % 8 != 0);  // whole vectors of x
+    f.copy_w = !f.one && !rows_bf16(W, ldw);
     Regions r;
     f.off_x = r.take(f.copy_x ? M * pad8(K) * 2 : 0);
     f.off_w = r.take(f.copy_w ? N * pad8(K) * 2 : 0);
@@ -274,7 +265,7 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
                                     int activation, bool want_dx, bool want_dw, bool want_db, int64_t M, int64_t N, int64_t K,
                                     int dw_dtype, int sm_count, int pairs) {
     LinearGradLayout g{};
-    g.turned = M <= kLinTurnedRows;
+    g.turned = linear_turns(M, K, sm_count);
     if (g.turned)
         g.t = plan_turned(M, K, N, sm_count);
     else
@@ -358,17 +349,15 @@ extern "C" flp_status flp_linear(const void* X, int64_t ldx, const void* W, int6
     e.ldpre = ldpre;
     e.vec = rows_bf16(Y, ldy) && N % 8 == 0 && (!residual || rows_bf16(residual, ldr)) && (!pre || rows_bf16(pre, ldpre));
     e.bias_vec = aligned16(bias);
-    if (f.few) {
-        LinRowsParams p{};
+    if (f.one) {
+        LinRowParams p{};
         p.x = static_cast<const bf16*>(X);
-        p.ldx = ldx;
         p.w = static_cast<const bf16*>(W);
         p.ldw = ldw;
-        p.M = static_cast<int>(M);
         p.N = static_cast<int>(N);
         p.K = static_cast<int>(K);
         p.e = e;
-        return linear_rows(p, !(rows_bf16(W, ldw) && K % 8 == 0), d->sm_count, after, s);
+        return linear_row(p, !(rows_bf16(W, ldw) && K % 8 == 0), d->sm_count, after, s);
     }
     if (f.turned) return linear_turned(f.t, X, ldx, W, ldw, false, M, N, K, e, nullptr, kWaitLimitNs, -1, after, s);
     return linear_product(f.l, X, ldx, W, ldw, false, M, N, K, e, ws + f.off_part, nullptr, d->pairs, kWaitLimitNs, -1, after, s);

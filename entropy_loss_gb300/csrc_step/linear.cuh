@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
 
 // ------------------------------------------------------------------ turned tiles
 //
-// For few rows of x: W's rows are the 128 rows of a tile and x's (up to 256, a multiple of
+// For few rows of x: W's rows are the 128 rows of a tile and x's (up to 128, a multiple of
 // 16) its columns, so that a tile moves next to nothing but W, and a CTA by itself holds
 // 128 columns of y, one a thread.  The `split` CTAs of a cluster share a tile, each with a
 // part of the contraction; their fp32 sums are joined through distributed shared memory,
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
 
 constexpr int LT_THREADS = 192;
 constexpr int LT_STAGES = 12;  // at most
-constexpr int LT_MAX_T = 256;
+constexpr int LT_MAX_T = 128;
 constexpr uint32_t LT_A_BYTES = 128 * BK * 2;
 
 struct LinTurnParams {
@@ -702,11 +702,18 @@ __device__ __forceinline__ void lin_turn_out(const LinTurnParams& p, uint32_t su
         float v[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) v[g] = 0.f;
-        for (int i = 0; i < p.split; ++i) {
-            const uint32_t from = mapa_shared(sums, i);
+        for (int i0 = 0; i0 < p.split; i0 += 4) {
+            float u[4][G];  // 16 loads under way
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (c + g * p.split < rows) v[g] += ld_cluster_f32(from + (c + g * p.split) * 512);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t from = mapa_shared(sums, min(i0 + i, p.split - 1));
+#pragma unroll
+                for (int g = 0; g < G; ++g) u[i][g] = ld_cluster_f32(from + min(c + g * p.split, rows - 1) * 512);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int g = 0; g < G; ++g) v[g] += i0 + i < p.split ? u[i][g] : 0.f;
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) v[g] += bias;
@@ -867,19 +874,18 @@ __global__ void __launch_bounds__(LT_THREADS)
     }
 }
 
-// ------------------------------------------------------------------ few rows
+// ------------------------------------------------------------------ one row
 //
-// A row of W meets every row of x while it is in registers, so the call reads W once, at
-// the pace of memory: a warp takes R rows of W at a time, 8 elements a lane, and keeps R x
-// MT sums in pairs.  x, read again for every R rows, comes from the caches.  Where W has
-// too few rows for all warps, KW warps of a block share rows and split the contraction.
+// One row of x: W is read once, at the pace of memory.  A warp takes R rows of W at a time,
+// 8 elements a lane, and keeps their sums in pairs; x, read again for every R rows, comes
+// from the caches.  Where W has too few rows for all warps, KW warps of a block share rows
+// and split the contraction.
 
-struct LinRowsParams {
+struct LinRowParams {
     const bf16* x;
-    long long ldx;
     const bf16* w;
     long long ldw;
-    int M, N, K;
+    int N, K;
     int kw;     // warps that share rows: 1, 2, 4, 8
     int chunk;  // of the contraction, each such warp's: a multiple of 256
     LinEpilogue e;
@@ -888,23 +894,22 @@ struct LinRowsParams {
 constexpr int LR_THREADS = 256;
 constexpr int LR_WARPS = LR_THREADS / 32;
 constexpr int LR_ROWS = 4;
+constexpr int LR_STEPS = 2;  // of 256 elements, under way at once
 
-template <int MT, bool LOOSE>
-__global__ void __launch_bounds__(LR_THREADS) flp_linear_rows_kernel(const __grid_constant__ LinRowsParams p) {
-    constexpr int R = LR_ROWS, U = MT >= 8 ? 1 : 2;  // U steps of 256 elements under way
+template <bool LOOSE>
+__global__ void __launch_bounds__(LR_THREADS) flp_linear_row_kernel(const __grid_constant__ LinRowParams p) {
+    constexpr int R = LR_ROWS, U = LR_STEPS;
     __shared__ __align__(16) uint8_t words[LOOSE ? LR_WARPS * WARP_WORDS_BYTES : 16];
-    __shared__ float sums[LR_WARPS][R * MT];
+    __shared__ float sums[LR_WARPS][R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t stage = smem_addr(words) + (LOOSE ? warp * WARP_WORDS_BYTES : 0);
     const int teams = LR_WARPS / p.kw, team = warp / p.kw, part = warp % p.kw;
     const int n0 = (blockIdx.x * teams + team) * R;
     const int k0 = part * p.chunk, k1 = min(p.K, k0 + p.chunk);
     griddep_wait();  // an aligned copy of x
-    uint64_t acc[R][MT];
+    uint64_t acc[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[r][m] = 0;
+    for (int r = 0; r < R; ++r) acc[r] = 0;
     const Extent all = extent_of<bf16>(p.w, p.N, p.ldw, p.K);
     if (n0 < p.N) {
         for (int k = k0; k < k1; k += 256 * U) {
@@ -927,7 +932,10 @@ __global__ void __launch_bounds__(LR_THREADS) flp_linear_rows_kernel(const __gri
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = k + u * 256 + lane * 8, left = k1 - at;
-                uint64_t wp[R][4];
+                // x is aligned and padded to vectors; what lies behind K is zero in a padded
+                // copy, and meets zeros of W
+                uint4 xv = make_uint4(0, 0, 0, 0);
+                if (left > 0) xv = __ldg(reinterpret_cast<const uint4*>(p.x + at));
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     uint4 v;
@@ -936,45 +944,28 @@ __global__ void __launch_bounds__(LR_THREADS) flp_linear_rows_kernel(const __gri
                     else
                         v = make_uint4(w[u][r][0], w[u][r][1], w[u][r][2], w[u][r][3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) wp[r][j] = Pairs<bf16>::get(v, j);
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    // rows of x are aligned and padded to vectors; what lies behind K is zero in
-                    // a padded copy, and meets zeros of W
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (left > 0) v = __ldg(reinterpret_cast<const uint4*>(p.x + min(m, p.M - 1) * p.ldx + at));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint64_t xv = Pairs<bf16>::get(v, j);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) acc[r][m] = f2_fma(wp[r][j], xv, acc[r][m]);
-                    }
+                    for (int j = 0; j < 4; ++j) acc[r] = f2_fma(Pairs<bf16>::get(v, j), Pairs<bf16>::get(xv, j), acc[r]);
                 }
             }
         }
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float s = warp_sum(f2_sum(acc[r][m]));
-            if (lane == 0) sums[warp][r * MT + m] = s;
-        }
+    for (int r = 0; r < R; ++r) {
+        const float s = warp_sum(f2_sum(acc[r]));
+        if (lane == 0) sums[warp][r] = s;
+    }
     __syncthreads();
     // one thread per output of the block
-    for (int i = threadIdx.x; i < teams * R * MT; i += LR_THREADS) {
-        const int m = i / (teams * R), j = i % (teams * R), c = blockIdx.x * teams * R + j;
-        if (m >= p.M || c >= p.N) continue;
-        float v = 0.f;
-        for (int q = 0; q < p.kw; ++q) v += sums[j / R * p.kw + q][j % R * MT + m];
-        if (p.e.bias)
-            v += p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[c] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[c]);
-        if (p.e.pre) p.e.pre[m * p.e.ldpre + c] = __float2bfloat16_rn(v);
-        v = lin_act_of(v, p.e.act);
-        if (p.e.residual) v += __bfloat162float(p.e.residual[m * p.e.ldr + c]);
-        p.e.y[m * p.e.ldy + c] = __float2bfloat16_rn(v);
-    }
+    const int j = threadIdx.x, c = blockIdx.x * teams * R + j;
+    if (j >= teams * R || c >= p.N) return;
+    float v = 0.f;
+    for (int q = 0; q < p.kw; ++q) v += sums[j / R * p.kw + q][j % R];
+    if (p.e.bias)
+        v += p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[c] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[c]);
+    if (p.e.pre) p.e.pre[c] = __float2bfloat16_rn(v);
+    v = lin_act_of(v, p.e.act);
+    if (p.e.residual) v += __bfloat162float(p.e.residual[c]);
+    p.e.y[c] = __float2bfloat16_rn(v);
 }
 
 // ------------------------------------------------------------------ d and db
