@@ -193,7 +193,10 @@ extern "C" flp_status flp_expert_combine_backward(const void* dY, int64_t lddy, 
     p.dweights = dweights;
     int64_t grid;
     if ((st = move_grid(p, CBWD_NV, dtype, &grid)) != FLP_OK) return st;
-    const bool warp = p.chunks <= 2;  // so short rows would leave most of a block idle
+    // A warp by itself needs no barrier and has no chunks left over: 32768 x 4 x 5120 takes 447
+    // us, a block 572, 4096 tokens 68 and 82; of few tokens it would leave most of the GPU idle
+    // (1024 x 4 x 4096 25 and 23, 256 x 8 x 7168 50 and 19), unless rows are short.
+    const bool warp = T >= 2048 || p.chunks <= 2;
     const bool loose = !(rows_vec(dY, lddy, H, dtype) && rows_vec(dYS, lddys, H, dtype) &&
                          (!dweights || rows_vec(YS, ldys, H, dtype)));
     return move_typed(dtype, loose, [&](auto t, auto is_loose) {

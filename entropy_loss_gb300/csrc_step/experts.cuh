@@ -341,10 +341,11 @@ __global__ void __launch_bounds__(MOVE_THREADS) flp_expert_combine_kernel(const 
         store_row_vec<T, LOOSE>(dst + i * 32 * V, Pairs<T>::put(sum[i]), u.left - i * 32 * V, stage);
 }
 
-// A token per block, or per warp (WARP): its k products with dy need the whole row.
+// A token per block, or per warp (WARP): its k products with dy need the whole row.  Three
+// blocks an SM (65536 x 8 x 512 takes 175 us, with the registers of two 197).
 constexpr int CBWD_NV = 2, CBWD_J = 4;
 template <typename T, bool LOOSE, bool WARP>
-__global__ void __launch_bounds__(MOVE_THREADS) flp_expert_combine_bwd_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(MOVE_THREADS, 3) flp_expert_combine_bwd_kernel(const MoveParams p) {
     constexpr int NV = CBWD_NV, J = CBWD_J, V = wide_v<T>(), P = V / 2;
     __shared__ float red[J][MOVE_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -988,7 +988,7 @@ constexpr int LG_ROWS = 4;  // rows a warp has under way
 
 // 256 columns x `rows` rows a block, a row at a time a warp.
 template <bool LOOSE, int ACT>
-__global__ void __launch_bounds__(LG_THREADS) flp_linear_grad_kernel(const __grid_constant__ LinGradParams p) {
+__global__ void __launch_bounds__(LG_THREADS, LOOSE ? 2 : 4) flp_linear_grad_kernel(const __grid_constant__ LinGradParams p) {
     constexpr int P = 4;
     __shared__ __align__(16) uint8_t words[LOOSE ? LG_WARPS * WARP_WORDS_BYTES : 16];
     __shared__ float sums[LG_WARPS][256];

@@ -795,13 +795,14 @@ def expert_sort(experts, num_experts: int, *, workspace=None, stream=None) -> Ex
 def _expert_order(order, dev):
     """(T, k, address of rows, address of the number of kept slots) of an ExpertOrder on `dev`."""
     rows, offsets = order.rows, order.offsets
-    if (rows.dtype is not torch.int32 or rows.dim() != 2 or not rows.is_contiguous() or rows.device != dev
-            or offsets.dtype is not torch.int64 or offsets.dim() != 1 or len(offsets) < 1 or not offsets.is_contiguous()
+    shape, ends = rows.shape, offsets.shape
+    if (rows.dtype is not torch.int32 or len(shape) != 2 or not rows.is_contiguous() or rows.device != dev
+            or offsets.dtype is not torch.int64 or len(ends) != 1 or ends[0] < 1 or not offsets.is_contiguous()
             or offsets.device != dev):
         raise ValueError(f"order: not the order of slots on {dev}: rows {rows.dtype} {tuple(rows.shape)} on {rows.device}, "
                          f"offsets {offsets.dtype} {tuple(offsets.shape)} on {offsets.device}")
-    T, k = rows.shape
-    return T, k, rows.data_ptr(), offsets.data_ptr() + 8 * (len(offsets) - 1)
+    T, k = shape
+    return T, k, rows.data_ptr(), offsets.data_ptr() + 8 * (ends[0] - 1)
 
 
 def _expert_weights(weights, T, k, dev):
@@ -1029,9 +1030,8 @@ def token_logprob(logits, y, *, top: int = 0, scale: float = 1.0, ignore_index: 
     M, V = logits.shape
     code, dev = _dtype(logits, "logits"), logits.device
     yp = _row_values(y, M, dev, "targets", torch.int64)
-    out = torch.empty((3 if compute_entropy else 2, M), dtype=torch.float32, device=dev)
-    logprob, lse = out[0], out[1]
-    entropy = out[2] if compute_entropy else None
+    logprob, lse, *entropy = torch.empty((3 if compute_entropy else 2, M), dtype=torch.float32, device=dev).unbind(0)
+    entropy = entropy[0] if compute_entropy else None
     values = index = None
     if top > 0:
         values = torch.empty((M, top), dtype=torch.float32, device=dev)
