@@ -254,8 +254,8 @@ struct LinearGradLayout {
     LinPlan l;  // of dx, or
     LinTurnPlan t;
     bool turned;
-    size_t off_dw, off_x, off_w, off_d, off_part, off_sums, bytes;
-    bool copy_x, copy_w, make_d, sums;
+    size_t off_dw, off_x, off_w, off_d, off_lo, off_part, off_sums, bytes;
+    bool copy_x, copy_w, make_d, two, sums;  // two: d as the sum of two bf16 numbers, for dW
     int blocks, rows;  // of the column sums
 };
 
@@ -273,6 +273,7 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
     g.copy_x = want_dw && !rows_bf16(X, ldx);
     g.copy_w = want_dx && !rows_bf16(W, ldw);
     g.make_d = (want_dx || want_dw) && (activation != FLP_ACT_NONE || !rows_bf16(dY, lddy));
+    g.two = want_dw && activation != FLP_ACT_NONE && dw_dtype == FLP_F32;
     g.sums = want_db;
     const int64_t strips = cdiv(N, 256);
     g.rows = static_cast<int>(std::max<int64_t>(32, cdiv(cdiv(M, std::max<int64_t>(1, cdiv(8 * sm_count, strips))), 32) * 32));
@@ -285,6 +286,7 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
     g.off_x = r.take(g.copy_x ? M * pad8(K) * 2 : 0);
     g.off_w = r.take(g.copy_w ? N * pad8(K) * 2 : 0);
     g.off_d = r.take(g.make_d ? M * pad8(N) * 2 : 0);
+    g.off_lo = r.take(g.two ? M * pad8(N) * 2 : 0);
     g.off_part = r.take(want_dx ? g.l.part_bytes : 0);
     g.off_sums = r.take(g.sums ? static_cast<size_t>(g.blocks) * N * 4 : 0);
     g.bytes = r.bytes;
@@ -435,6 +437,7 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         p.M = static_cast<int>(M);
         p.N = static_cast<int>(N);
         p.d = g.make_d ? reinterpret_cast<bf16*>(ws + g.off_d) : nullptr;
+        p.lo = g.two ? reinterpret_cast<bf16*>(ws + g.off_lo) : nullptr;
         p.Np = static_cast<int>(pad8(N));
         p.part = g.sums ? g.blocks == 1 ? dbias : reinterpret_cast<float*>(ws + g.off_sums) : nullptr;
         p.rows = g.rows;
@@ -465,7 +468,10 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         if (st != FLP_OK) return st;
         after = true;
     }
-    return dW ? weight_grad(dY, lddy, X, ldx, M, N, K, dW, dW_dtype, ws + g.off_dw, d->pairs, after, s) : FLP_OK;
+    if (!dW) return FLP_OK;
+    st = weight_grad(dY, lddy, X, ldx, M, N, K, dW, dW_dtype, 0, ws + g.off_dw, d->pairs, after, s);
+    if (st != FLP_OK || !g.two) return st;
+    return weight_grad(ws + g.off_lo, lddy, X, ldx, M, N, K, dW, dW_dtype, 1, ws + g.off_dw, d->pairs, true, s);
 }
 
 // M = 192 rows, N = 520 columns (two 256 x 512 tiles, the second of 8 columns), 192 deep:

@@ -11,9 +11,11 @@
 // one of the second.  Whole rounds of tiles over the resident pairs write their outputs
 // themselves; the tiles of the last, incomplete round (all of them, when rows are few)
 // are split along the contraction into fp32 partial tiles, which a small kernel joins in
-// a fixed order and takes through the same epilogue.  d is rounded to bf16 once, by a
-// pass over dy and v that also sums db from the unrounded values; dW is the contraction
-// of wgrad.cuh.
+// a fixed order and takes through the same epilogue.  d is rounded to bf16 by a pass over
+// dy and v that also sums db from the unrounded values; dW is the contraction of
+// wgrad.cuh.  The rounding (2^-9 of each value) leaves bf16 results their own, but not an
+// fp32 dW: for that one d is written as the sum of two bf16 numbers (2^-17 of it), whose
+// products are added.
 #pragma once
 #include <type_traits>
 #include "../csrc/pair.cuh"
@@ -35,17 +37,18 @@ __device__ __forceinline__ uint64_t f2_rcp(uint64_t v) { return f2_map(v, [](flo
 __device__ __forceinline__ uint64_t f2_abs(uint64_t v) { return v & 0x7fffffff7fffffffull; }
 
 // exp(-v^2 / 2), and h = Phi(-|v|) = exp(-v^2 / 2) erfcx(|v| / sqrt 2) / 2, whose relative
-// error is that of erfcx: with t = 1 / (1 + 0.425 x), erfcx(x) / 2 = t P(t) for 0 <= x <=
-// 9.6 to 7.3e-6, P of degree 5 from a weighted least-squares fit (beyond, h vanishes).
+// error is that of erfcx: with t = 1 / (1 + 0.375 x), erfcx(x) / 2 = t P(t) for 0 <= x <=
+// 9.6 to 6.4e-7, P of degree 6 from a weighted least-squares fit (beyond, h vanishes).
 __device__ __forceinline__ void lin_normal_tail(uint64_t v, uint64_t& e, uint64_t& h) {
     e = f2_ex2(f2_mul(f2_mul(v, v), f2_splat(-0.5f * LOG2E)));
-    const uint64_t t = f2_rcp(f2_fma(f2_abs(v), f2_splat(0.425f * 0.7071067811865476f), f2_splat(1.f)));
-    uint64_t q = f2_splat(0.5f * -0.154721429f);
-    q = f2_fma(q, t, f2_splat(0.5f * 0.430636568f));
-    q = f2_fma(q, t, f2_splat(0.5f * -0.0328755014f));
-    q = f2_fma(q, t, f2_splat(0.5f * 0.288526839f));
-    q = f2_fma(q, t, f2_splat(0.5f * 0.22786909f));
-    q = f2_fma(q, t, f2_splat(0.5f * 0.240571746f));
+    const uint64_t t = f2_rcp(f2_fma(f2_abs(v), f2_splat(0.375f * 0.7071067811865476f), f2_splat(1.f)));
+    uint64_t q = f2_splat(0.5f * -0.135095946f);
+    q = f2_fma(q, t, f2_splat(0.5f * 0.387937988f));
+    q = f2_fma(q, t, f2_splat(0.5f * -0.129597526f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.2830617f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.166664508f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.21568919f));
+    q = f2_fma(q, t, f2_splat(0.5f * 0.211339448f));
     h = f2_mul(f2_mul(q, t), e);
 }
 
@@ -976,7 +979,8 @@ struct LinGradParams {
     const bf16* pre;  // with an activation
     long long ldpre;
     int M, N;
-    bf16* d;  // [M, Np], or null: not written
+    bf16* d;   // [M, Np], or null: not written
+    bf16* lo;  // what the rounding to bf16 takes from it, or null
     int Np;
     float* part;  // [row blocks][N]: column sums, or null
     int rows;     // of a row block
@@ -1036,7 +1040,17 @@ __global__ void __launch_bounds__(LG_THREADS, LOOSE ? 2 : 4) flp_linear_grad_ker
 #pragma unroll
                 for (int j = 0; j < P; ++j) d[j] = f2_mul(d[j], lin_slope2<ACT>(Pairs<bf16>::get(x, j)));
             }
-            if (p.d) st_global_16(p.d + static_cast<long long>(r) * p.Np + col, Pairs<bf16>::put(d), left > 0);
+            if (p.d) {
+                const uint4 hi = Pairs<bf16>::put(d);
+                const long long at = static_cast<long long>(r) * p.Np + col;
+                st_global_16(p.d + at, hi, left > 0);
+                if (p.lo) {
+                    uint64_t rest[P];
+#pragma unroll
+                    for (int j = 0; j < P; ++j) rest[j] = f2_fma(Pairs<bf16>::get(hi, j), f2_splat(-1.f), d[j]);
+                    st_global_16(p.lo + at, Pairs<bf16>::put(rest), left > 0);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < P; ++j) sum[j] = f2_add(sum[j], d[j]);
         }

@@ -444,11 +444,12 @@ size_t flp::weight_grad_bytes(int64_t M, int64_t N, int64_t K, int dw_dtype, int
 }
 
 flp_status flp::weight_grad(const void* dY, int64_t ldy, const void* X, int64_t ldx, int64_t M, int64_t N, int64_t K,
-                            void* dW, int dw_dtype, uint8_t* ws, int pairs, bool after_kernel, cudaStream_t s) {
+                            void* dW, int dw_dtype, int accumulate, uint8_t* ws, int pairs, bool after_kernel,
+                            cudaStream_t s) {
     const flp_status st = wgrad_attrs();
     if (st != FLP_OK) return st;
     const WgradPlan w = plan_wgrad(dY, ldy, M, N, K, dw_dtype, pairs, false);
-    return wgrad_contract(w, dY, ldy, X, K, ldx, ws, M, N, K, dW, dw_dtype, 0, pairs, wgrad_run(M), kWaitLimitNs, -1,
+    return wgrad_contract(w, dY, ldy, X, K, ldx, ws, M, N, K, dW, dw_dtype, accumulate, pairs, wgrad_run(M), kWaitLimitNs, -1,
                           after_kernel, s);
 }
 

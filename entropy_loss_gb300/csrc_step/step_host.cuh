@@ -10,12 +10,12 @@ namespace flp {  // step.cu
 // multiple of 8, 16-byte aligned, zeros behind each row.
 flp_status align_rows(const void* src, int64_t ld, int64_t M, int64_t H, void* dst, int64_t Hp, cudaStream_t s);
 
-// dW [N, K] = dY^T X for bf16 rows aligned to 16 bytes; the workspace's first word is the
+// dW [N, K] (+)= dY^T X for bf16 rows aligned to 16 bytes; the workspace's first word is the
 // error word, which the caller has cleared.
 flp_status weight_grad_checks(int64_t M, int64_t N, int64_t K, int dw_dtype);
 size_t weight_grad_bytes(int64_t M, int64_t N, int64_t K, int dw_dtype, int pairs);
 flp_status weight_grad(const void* dY, int64_t ldy, const void* X, int64_t ldx, int64_t M, int64_t N, int64_t K, void* dW,
-                       int dw_dtype, uint8_t* ws, int pairs, bool after_kernel, cudaStream_t s);
+                       int dw_dtype, int accumulate, uint8_t* ws, int pairs, bool after_kernel, cudaStream_t s);
 
 }  // namespace flp
 

@@ -8,7 +8,8 @@ between -0.13 and 1.13), their own arithmetic is off by below 2^-18 of their arg
 size (fp32 polynomials, a 2^-22 exponential and quotient; the exponent of gelu_tanh,
 up to 90 where its result still counts, is rounded by 2^-24 of it), and y is rounded
 to bf16 once: half a step, 2^-8 of the value.  In the backward pass d is rounded to
-bf16 (2^-8 of each of its values) and dx, dW (bf16) once more; dbias sums unrounded d:
+bf16 (2^-8 of each of its values; for an fp32 dW with an activation it is the sum of two
+bf16 numbers, off by 2^-8 of 2^-8 of it) and dx, dW (bf16) once more; dbias sums unrounded d:
 2^-24 (rows / 8 + 64) of the sum of the magnitudes at most, the slopes being off by
 below 2^-17.
 """
@@ -185,11 +186,14 @@ def run_backward(flp, M, N, K, act, dw_dtype=torch.float32, pads=(0, 0, 0, 0, 0)
     if act:
         d = d * act64(pre.double(), act)[1]
         e = 2.0 ** -17 * dy.double().abs()
-    each = e + 2.0 ** -8 * (d.abs() + e) if act else e  # d as the products see it
-    for got, a, b, rows, last in ((dx, d, W.double(), N, 2.0 ** -8), (dW, d.t(), x.double(), M, 2.0 ** -8 if dw_dtype is torch.bfloat16 else 2.0 ** -24)):
+    fine = dw_dtype is torch.float32
+    # d as the products see it, and the additions: of one product, or of the two of a sum of two
+    off = [e + rounded * (d.abs() + e) if act else e for rounded in (2.0 ** -8, 2.0 ** -16 if fine else 2.0 ** -8)]
+    for got, a, b, each, rows, last in ((dx, d, W.double(), off[0], N, 2.0 ** -8),
+                                        (dW, d.t(), x.double(), off[1].t(), 2 * M if fine and act else M, 2.0 ** -24 if fine else 2.0 ** -8)):
         want = a @ b
         size = a.abs() @ b.abs()
-        slack = (each if a is d else each.t()) @ b.abs() + (rows / 16 + 2) * 2.0 ** -23 * size * 1.01
+        slack = each @ b.abs() + (rows / 16 + 2) * 2.0 ** -23 * size * 1.01
         assert bool(((got.double() - want).abs() <= slack + last * (want.abs() + slack)).all())
     want = d.sum(0)
     assert bool(((db.double() - want).abs() <= e.sum(0) + 2.0 ** -24 * (M / 8 + 64) * d.abs().sum(0)).all())
