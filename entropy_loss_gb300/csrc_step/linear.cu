@@ -130,7 +130,7 @@ LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
     t.tiles_w = static_cast<int>(cdiv(N, 128));
     const int64_t KB = cdiv(depth, BK), tiles = static_cast<int64_t>(t.tiles_t) * t.tiles_w;
     t.split = 1;
-    while (t.split < 8 && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
+    while (t.split < 4 && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
     const size_t room = 108 * 1024, stage = lin_turn_stage(t.nt);
     t.stages = static_cast<int>(std::min<int64_t>({LT_STAGES, static_cast<int64_t>(room / stage), cdiv(KB, t.split)}));
     t.smem = std::max<size_t>(t.stages * stage, static_cast<size_t>(t.nt) * 128 * 4) + 1024;

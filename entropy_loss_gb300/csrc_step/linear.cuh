@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
 // each CTA taking a part of the rows of x through the epilogue.  A bounded wait that runs
 // out makes the tile NaN.
 
-constexpr int LT_THREADS = 192;
+constexpr int LT_THREADS = 256;
+constexpr int LT_WAYS = LT_THREADS / 128;  // threads that share a column's rows of x
 constexpr int LT_STAGES = 12;  // at most
 constexpr int LT_MAX_T = 128;
 constexpr uint32_t LT_A_BYTES = 128 * BK * 2;
@@ -691,49 +692,48 @@ struct LinTurnShared {
 // Bytes of a stage, and of the shared memory of a launch.
 __host__ __device__ inline uint32_t lin_turn_stage(int nt) { return LT_A_BYTES + static_cast<uint32_t>(nt) * (BK * 2); }
 
-// Column r of the tile through the epilogue, for this CTA's share of the rows of x: the
-// CTAs' sums [nt][128] added in order.
+// Column n through the epilogue, for every LT_WAYS * split-th row of x of the tile from
+// `first` on: the CTAs' sums [nt][128] added in order.
 template <int ACT>
-__device__ __forceinline__ void lin_turn_out(const LinTurnParams& p, uint32_t sums, int rank, int n, int t0, bool bad) {
-    constexpr int G = 4;  // rows under way
+__device__ __forceinline__ void lin_turn_out(const LinTurnParams& p, uint32_t sums, int first, int n, int t0, bool bad) {
+    constexpr int G = 8;  // rows under way
     const int rows = min(p.nt, p.M - t0);
     float bias = 0.f;
     if (p.e.bias)
         bias = p.e.bias_f32 ? static_cast<const float*>(p.e.bias)[n] : __bfloat162float(static_cast<const bf16*>(p.e.bias)[n]);
     if (bad) bias = __uint_as_float(0x7fc00000u);
-    for (int c = rank; c < rows; c += G * p.split) {
-        float v[G];
+    const int step = LT_WAYS * p.split;
+    for (int c0 = first; c0 < rows; c0 += G * step) {
+        float v[G], add[G];
+        int c[G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) v[g] = 0.f;
-        for (int i0 = 0; i0 < p.split; i0 += 4) {
-            float u[4][G];  // 16 loads under way
+        for (int g = 0; g < G; ++g) {
+            c[g] = c0 + g * step;
+            v[g] = add[g] = 0.f;
+            if (p.e.residual && c[g] < rows) add[g] = __bfloat162float(p.e.residual[(t0 + c[g]) * p.e.ldr + n]);
+        }
+        for (int i = 0; i < p.split; i += 2) {
+            const uint32_t one = mapa_shared(sums, i), two = mapa_shared(sums, i + 1 < p.split ? i + 1 : i);
+            float u[2][G];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t from = mapa_shared(sums, min(i0 + i, p.split - 1));
-#pragma unroll
-                for (int g = 0; g < G; ++g) u[i][g] = ld_cluster_f32(from + min(c + g * p.split, rows - 1) * 512);
+            for (int g = 0; g < G; ++g) {
+                u[0][g] = u[1][g] = 0.f;
+                if (c[g] < rows) u[0][g] = ld_cluster_f32(one + c[g] * 512);
+                if (c[g] < rows && i + 1 < p.split) u[1][g] = ld_cluster_f32(two + c[g] * 512);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int g = 0; g < G; ++g) v[g] += i0 + i < p.split ? u[i][g] : 0.f;
+            for (int g = 0; g < G; ++g) v[g] = v[g] + u[0][g] + u[1][g];
         }
 #pragma unroll
-        for (int g = 0; g < G; ++g) v[g] += bias;
-        if (p.e.pre) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (c + g * p.split < rows) p.e.pre[(t0 + c + g * p.split) * p.e.ldpre + n] = __float2bfloat16_rn(v[g]);
+        for (int g = 0; g < G; ++g) {
+            v[g] += bias;
+            if (p.e.pre && c[g] < rows) p.e.pre[(t0 + c[g]) * p.e.ldpre + n] = __float2bfloat16_rn(v[g]);
         }
 #pragma unroll
         for (int g = 0; g < G; g += 2) f2_unpack(lin_act2<ACT>(f2_pack(v[g], v[g + 1])), v[g], v[g + 1]);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (c + g * p.split >= rows) continue;
-            const long long m = t0 + c + g * p.split;
-            if (p.e.residual) v[g] += __bfloat162float(p.e.residual[m * p.e.ldr + n]);
-            p.e.y[m * p.e.ldy + n] = __float2bfloat16_rn(v[g]);
-        }
+        for (int g = 0; g < G; ++g)
+            if (c[g] < rows) p.e.y[(t0 + c[g]) * p.e.ldy + n] = __float2bfloat16_rn(v[g] + add[g]);
     }
 }
 
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(LT_THREADS)
             volatile int no_abort = 0;
             mbar_wait(&sh.drain, 0, limit, &no_abort);
         }
-    } else {
+    } else if (warp < 6) {
         const int q = warp & 3, r = q * 32 + lane;  // accumulator row == TMEM lane
         const bool ok = named_bar_all(1, EPI_THREADS, mbar_wait(&sh.done, 0, limit, abort_flag));
         if (ok) {
@@ -851,17 +851,18 @@ __global__ void __launch_bounds__(LT_THREADS)
     tc_fence_before();
     __syncthreads();
     if (p.split > 1) cluster_sync();  // every CTA's sums are there
-    const int n = n0 + static_cast<int>(threadIdx.x);
-    if (threadIdx.x < 128 && n < p.N) {
+    const int r = threadIdx.x % 128, n = n0 + r;
+    if (n < p.N) {
         uint32_t bad = 0;
         for (int i = 0; i < p.split; ++i) bad |= ld_cluster_u32(mapa_shared(smem_addr(&sh.bad), i));
-        const uint32_t sums = smem_addr(base) + threadIdx.x * 4;
+        const uint32_t sums = smem_addr(base) + r * 4;
+        const int first = rank + static_cast<int>(threadIdx.x) / 128 * p.split;
         switch (p.e.act) {
-            case LIN_RELU: lin_turn_out<LIN_RELU>(p, sums, rank, n, t0, bad); break;
-            case LIN_GELU: lin_turn_out<LIN_GELU>(p, sums, rank, n, t0, bad); break;
-            case LIN_GELU_TANH: lin_turn_out<LIN_GELU_TANH>(p, sums, rank, n, t0, bad); break;
-            case LIN_SILU: lin_turn_out<LIN_SILU>(p, sums, rank, n, t0, bad); break;
-            default: lin_turn_out<LIN_NONE>(p, sums, rank, n, t0, bad);
+            case LIN_RELU: lin_turn_out<LIN_RELU>(p, sums, first, n, t0, bad); break;
+            case LIN_GELU: lin_turn_out<LIN_GELU>(p, sums, first, n, t0, bad); break;
+            case LIN_GELU_TANH: lin_turn_out<LIN_GELU_TANH>(p, sums, first, n, t0, bad); break;
+            case LIN_SILU: lin_turn_out<LIN_SILU>(p, sums, first, n, t0, bad); break;
+            default: lin_turn_out<LIN_NONE>(p, sums, first, n, t0, bad);
         }
     }
     if (*abort_flag) {  // copies in flight get a bounded grace period
