@@ -105,8 +105,10 @@ __device__ __forceinline__ void raise_abort(const Smem& sm, int* err) {
 // makes the peer's barriers visible before any remote arrive or TMA signal.
 // sched_arrivals: arrivals that free a slot of the unit hand-off ring (the
 // peer's producer, the MMA issuer and every epilogue thread of both CTAs).
+// drain_arrivals: threads of both CTAs that drain an accumulator.
 __device__ __forceinline__ uint32_t pair_prologue(const Smem& sm, int warp,
-                                                  uint32_t sched_arrivals = 2 + 2 * EPI_THREADS) {
+                                                  uint32_t sched_arrivals = 2 + 2 * EPI_THREADS,
+                                                  uint32_t drain_arrivals = 2 * EPI_THREADS) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sm.full[s], 1);
@@ -114,7 +116,7 @@ __device__ __forceinline__ uint32_t pair_prologue(const Smem& sm, int warp,
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sm.tfull[a], 1);
-            mbar_init(&sm.tempty[a], 2 * EPI_THREADS);
+            mbar_init(&sm.tempty[a], drain_arrivals);
         }
         mbar_init(sm.drain, 1);
         for (int s = 0; s < SCHED_SLOTS; ++s) {

@@ -15,7 +15,8 @@ struct LinPlan {
 // tiles write their outputs; the rest do so too, or are split into their halves (0 splits)
 // or along the contraction.  The least of what these cost:
 // 0.66 us for a 64-deep block of a wide tile and 0.37 us of a narrow one (the rate at which
-// its operands arrive), 3 us for a run's start and end, and for joining 4 us (a launch) and
+// its operands arrive), 3 us for a run's start and end (5 for a half that one epilogue
+// group drains by itself), and for joining 4 us (a launch) and
 // the partial tiles' bytes, written and read back at 4 TB/s.
 LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
     LinPlan best{};
@@ -34,7 +35,7 @@ LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
         const int64_t most = rest == 0 ? 1 : std::min<int64_t>(l.KB, std::max<int64_t>(1, 4 * pairs / rest));
         for (int64_t s = width > BN && rest > 0 ? 0 : 1; s <= most; ++s) {
             const double joined = s > 1 ? 4.0 + tile_mb / 4 * static_cast<double>(rest * s) : 0.0;
-            const double last = s == 0 ? static_cast<double>(cdiv(2 * rest, pairs)) * (l.KB * 0.37 + 3.0)
+            const double last = s == 0 ? static_cast<double>(cdiv(2 * rest, pairs)) * (l.KB * 0.37 + 5.0)
                                        : static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(l.KB, s)) * block + 3.0);
             const double cost = static_cast<double>(whole / pairs) * l.KB * block + last + joined;
             if (cost >= least - 1e-9) continue;
@@ -130,7 +131,10 @@ LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
     t.tiles_w = static_cast<int>(cdiv(N, 128));
     const int64_t KB = cdiv(depth, BK), tiles = static_cast<int64_t>(t.tiles_t) * t.tiles_w;
     t.split = 1;
-    while (t.split < 4 && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
+    // up to four CTAs a tile, eight of few tiles (4096 x 4096, 16 rows: 19 us with four, 21 with
+    // eight; 8192 -> 1024: 21 and 17)
+    const int most = tiles * 8 <= sm_count ? 8 : 4;
+    while (t.split < most && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
     const size_t room = 108 * 1024, stage = lin_turn_stage(t.nt);
     t.stages = static_cast<int>(std::min<int64_t>({LT_STAGES, static_cast<int64_t>(room / stage), cdiv(KB, t.split)}));
     t.smem = std::max<size_t>(t.stages * stage, static_cast<size_t>(t.nt) * 128 * 4) + 1024;

@@ -164,12 +164,28 @@ struct LinUnit {
     int halves;    // 256-column halves that hold columns (0: none)
 };
 
-// The accumulator (and epilogue group) of the one half of a pair's `it`-th tile, and the
-// half of a tile that epilogue group g drains (-1: none).
+// The accumulator of the one half of a pair's `it`-th tile.
 __device__ __forceinline__ int lin_single(int it) { return it & 1; }
-__device__ __forceinline__ int lin_half(const LinUnit& t, int g, int it) {
-    if (t.halves == 2) return g;
-    return t.halves == 1 && g == lin_single(it) ? 0 : -1;
+
+// What epilogue group g drains of a pair's `it`-th tile: the half of a wide tile that lies
+// in accumulator g, 128 columns of every tile of one half in a launch of such tiles, or
+// the one half of another tile if accumulator g holds it.
+struct LinShare {
+    int acc;    // -1: nothing
+    int col;    // first column, in the tile
+    int boxes;  // of 32 columns, up to BN / 32
+};
+__device__ __forceinline__ LinShare lin_share(const LinParams& p, const LinUnit& t, int g, int it) {
+    LinShare s{-1, 0, BN / 32};
+    if (p.width == BN) {
+        s.acc = lin_single(it), s.col = g * (BN / 2), s.boxes = BN / 64;
+    } else if (t.halves == 2) {
+        s.acc = g, s.col = g * BN;
+    } else if (t.halves == 1 && g == lin_single(it)) {
+        s.acc = g;
+    }
+    s.boxes = max(0, min(s.boxes, (p.N - t.n0 - s.col + 31) / 32));  // the others lie past the last column
+    return s;
 }
 
 __device__ __forceinline__ LinUnit lin_unit(const LinParams& p, int u) {
@@ -291,14 +307,14 @@ __device__ __forceinline__ void lin_pack(const uint64_t (&v)[16], uint32_t (&w)[
 __device__ __noinline__ void lin_fill_nan(const LinParams& p, int u, int it, int npairs, int g, int rofs, int et) {
     for (; u < p.units; u += npairs, ++it) {
         const LinUnit t = lin_unit(p, u);
-        const int half = lin_half(t, g, it);
-        if (half < 0) continue;
-        const int m0 = t.m0 + rofs, n0 = t.n0 + half * BN;
-        const int rows = min(BM, p.M - m0), cols = min(BN, p.N - n0);
+        const LinShare s = lin_share(p, t, g, it);
+        if (s.acc < 0) continue;
+        const int m0 = t.m0 + rofs, n0 = t.n0 + s.col;
+        const int rows = min(BM, p.M - m0), cols = min(32 * s.boxes, p.N - n0);
         for (int r = 0; r < rows; ++r)
             for (int c = et; c < cols; c += EPI_THREADS) {
                 if (t.part >= 0) {
-                    p.part[(static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + half * BN + c] = __uint_as_float(0x7fc00000u);
+                    p.part[(static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + s.col + c] = __uint_as_float(0x7fc00000u);
                 } else {
                     p.e.y[static_cast<long long>(m0 + r) * p.e.ldy + n0 + c] = __ushort_as_bfloat16(0x7fc0);
                     if (p.e.pre) p.e.pre[static_cast<long long>(m0 + r) * p.e.ldpre + n0 + c] = __ushort_as_bfloat16(0x7fc0);
@@ -340,7 +356,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         tma_prefetch_desc(&tmPre);
     }
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const uint32_t tmem_base = pair_prologue(sm, warp);
+    const uint32_t tmem_base =
+        pair_prologue(sm, warp, 2 + 2 * EPI_THREADS, (p.width == BN ? 4 : 2) * EPI_THREADS);
     griddep_wait();  // aligned copies, d and the cleared error word are complete from here on
     const uint64_t limit = p.wait_limit_ns;
     volatile int* abort_flag = sm.abort_flag;
@@ -478,50 +495,50 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             mbar_wait(sm.drain, 0, limit, &no_abort);
         }
     } else {
-        // ------------------------- epilogue: group g drains accumulator g
+        // ------------------------------------------------- epilogue (lin_share)
         const int g = (warp - 2) >> 2;
         const int et = threadIdx.x - 64 - g * EPI_THREADS;  // thread 0 issues the bulk stores
         const int q = warp & 3;
         const int r = q * 32 + lane;  // accumulator row == TMEM lane
-        const uint32_t tbase = tmem_base + static_cast<uint32_t>(g * BN) + (static_cast<uint32_t>(q * 32) << 16);
-        const uint32_t tempty = mapa_shared(smem_addr(&sm.tempty[g]), 0);
         const uint32_t bar_box = 1 + 2 * g, bar_vote = 2 + 2 * g;
         uint8_t* box0 = sm.base + SMEM_STG + g * (2 * NBOX_BYTES);
         // the warp's rows of the group's boxes, for rows that no bulk store can write (then
         // none reads the boxes)
         const uint32_t box_in = smem_addr(box0) + q * (32 * 64), box_out = box_in + NBOX_BYTES;
         StoreRing ring;
-        uint32_t phase = 0;
+        uint32_t phase = 0;  // bit a: of accumulator a
         bool ok = true;
         int u = pair, it = 0;
         for (; u < p.units; u += npairs, ++it) {
             const LinUnit t = lin_unit(p, u);
-            const int half = lin_half(t, g, it);
-            if (half < 0) continue;
-            const bool ready = mbar_wait(&sm.tfull[g], phase, limit, abort_flag);
+            const LinShare share = lin_share(p, t, g, it);
+            if (share.acc < 0) continue;
+            const bool ready = mbar_wait(&sm.tfull[share.acc], phase >> share.acc & 1u, limit, abort_flag);
             // every thread of the group takes the same branch (the box barriers need all of them)
             if (!named_bar_all(bar_vote, EPI_THREADS, ready)) {
                 ok = false;
                 break;
             }
-            phase ^= 1u;
+            phase ^= 1u << share.acc;
             tc_fence_after();
-            const int m0 = t.m0 + rofs, n0 = t.n0 + half * BN;
+            const int m0 = t.m0 + rofs, n0 = t.n0 + share.col;
             const int row = m0 + r;
-            const int boxes = min(BN / 32, (p.N - n0 + 31) / 32);  // the others lie past the last column
+            const int boxes = share.boxes, ahead = p.width == BN ? BN / 64 : BN / 32;
+            const uint32_t tbase = tmem_base + static_cast<uint32_t>(share.acc * BN + (p.width == BN ? share.col : 0)) +
+                                   (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t tempty = mapa_shared(smem_addr(&sm.tempty[share.acc]), 0);
             auto release = [&]() {
                 tc_fence_before();
                 mbar_arrive_cluster(tempty);
             };
             if (t.part >= 0) {
                 float4* o = reinterpret_cast<float4*>(
-                    p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + half * BN);
+                    p.part + (static_cast<long long>(t.part) * p.rows + rofs + r) * (2 * BN) + share.col);
 #pragma unroll 1
                 for (int b = 0; b < boxes; ++b) {
                     uint32_t raw[32];
                     tmem_ld_32x32b_x32(tbase + b * 32, raw);
                     tmem_wait_ld();
-                    if (b == boxes - 1) release();
                     if (row < p.M) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -529,6 +546,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                                                        __uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3]));
                     }
                 }
+                release();
                 continue;
             }
             uint4 res[4];  // the next box's residual
@@ -588,15 +606,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             };
             tmem_ld_32x32b_x32(tbase, even);
 #pragma unroll 1
-            for (int b = 0; b < BN / 32; b += 2) {
+            for (int b = 0; b < ahead; b += 2) {
                 arrived(even);
                 tmem_ld_32x32b_x32(tbase + b * 32 + 32, odd);
-                if (b + 2 == BN / 32) {
+                if (b + 2 == ahead) {
                     arrived(odd);
                     release();
                 }
                 drain(b, even);
-                if (b + 2 < BN / 32) {
+                if (b + 2 < ahead) {
                     arrived(odd);
                     tmem_ld_32x32b_x32(tbase + b * 32 + 64, even);
                 }
