@@ -29,14 +29,14 @@ int tlp_cluster(int64_t M, int64_t vecs, int64_t resident) {
     return best;
 }
 
-template <typename T, bool LOOSE, int THREADS>
+template <typename T, int THREADS>
 flp_status tlp_launch(TlpParams& p, int sm_count, cudaStream_t s) {
-    constexpr auto* kernel = flp_token_logprob_kernel<T, LOOSE, THREADS>;
-    const int64_t vecs = cdiv(p.V, wide_v<T>());
+    constexpr auto* kernel = flp_token_logprob_kernel<T, THREADS>;
+    const int64_t vecs = cdiv(p.V + wide_v<T>() - 1, wide_v<T>());  // at any alignment
     int per_sm = 0;
     const flp_status st = resident_blocks<kernel>(THREADS, 0, 0, &per_sm);
     if (st != FLP_OK) return st;
-    p.cluster = vecs <= 4 * THREADS ? 1 : tlp_cluster(p.M, vecs, static_cast<int64_t>(per_sm) * sm_count);
+    p.cluster = vecs <= TLP_NV * THREADS ? 1 : tlp_cluster(p.M, vecs, static_cast<int64_t>(per_sm) * sm_count);
     p.per = static_cast<int>(cdiv(cdiv(vecs, p.cluster), 32) * 32);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.M * p.cluster));
@@ -86,14 +86,11 @@ extern "C" flp_status flp_token_logprob(const void* logits, int64_t ld, int dtyp
     p.entropy = entropy;
     p.top_value = top_logprob;
     p.top_index = reinterpret_cast<long long*>(top_index);
-    const bool loose = !(rows16(logits, ld, dtype) && (V * elem(dtype)) % 16 == 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto typed = [&](auto t) {
         using T = decltype(t);
         // rows that a block of 128 threads reads at once
-        if (V <= 4 * 128 * wide_v<T>())
-            return loose ? tlp_launch<T, true, 128>(p, d->sm_count, s) : tlp_launch<T, false, 128>(p, d->sm_count, s);
-        return loose ? tlp_launch<T, true, 256>(p, d->sm_count, s) : tlp_launch<T, false, 256>(p, d->sm_count, s);
+        return V <= TLP_NV * 128 * wide_v<T>() ? tlp_launch<T, 128>(p, d->sm_count, s) : tlp_launch<T, 256>(p, d->sm_count, s);
     };
     return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
 }

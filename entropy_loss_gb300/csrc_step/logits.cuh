@@ -35,6 +35,7 @@ namespace flp {
 constexpr int TLP_MAX_TOP = 32;
 constexpr int TLP_LIST = 512;      // vectors, and then elements, that a block can list
 constexpr int TLP_CLUSTER = 8;     // blocks of a row at most
+constexpr int TLP_NV = 4;          // vectors that a thread takes at a time
 
 struct TlpParams {
     const void* x;
@@ -100,71 +101,53 @@ __device__ __forceinline__ float redux_max(float v) {
     return m;
 }
 
-// -inf in the places of a vector from `valid` on.
+// A row as the 16-byte vectors of memory that hold it, counted from the one with its first
+// element; `head` elements of that one lie before the row.  A row needs no alignment: the
+// vectors at its ends are read element by element.
 template <typename T>
-__device__ __forceinline__ void tlp_cut(uint32_t* w, int valid) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        if constexpr (sizeof(T) == 2)
-            w[q] = 2 * q + 1 < valid ? w[q] : 2 * q < valid ? (w[q] & 0xffffu) | 0xff800000u : 0xff80ff80u;
-        else
-            w[q] = q < valid ? w[q] : 0xff800000u;
-    }
-}
-
-// NV vectors of a thread, THREADS apart: words in flight, then elements.
-template <typename T, bool LOOSE, int NV, int THREADS>
-struct TlpChunk {
+struct TlpRow {
     static constexpr int V = wide_v<T>();
-    static constexpr int W = LOOSE ? WarpWords<T>::N : 4;
-    uint32_t r[NV][W];
-    __device__ __forceinline__ void load(const T* row, int v0, int end, bool edge, const Extent& all) {
+    const T* x;
+    int cols, head;
+    __device__ __forceinline__ TlpRow(const T* row, int n)
+        : x(row), cols(n), head(static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T))) {}
+    __device__ __forceinline__ int vecs() const { return (head + cols + V - 1) / V; }
+    __device__ __forceinline__ int col(int v) const { return v * V - head; }
+    // vector v (if `on`) as words, -inf in the places past the row's ends
+    __device__ __forceinline__ void load(uint32_t* w, int v, bool on) const {
+        constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+        const int c = col(v);
+        const bool inner = c >= 0 && c + V <= cols;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, %6;\n\tmov.b32 %1, %6;\n\tmov.b32 %2, %6;\n\t"
+            "mov.b32 %3, %6;\n\t@p ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
+            : "l"(x + c), "r"(static_cast<int>(on && inner)), "n"(none));
+        if (on && !inner) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (v0 + i * THREADS) * V;
-            const T* src = row + col;
-            if constexpr (LOOSE) {
-                load_words<T>(r[i], src, end - col, edge, all);
-            } else {
-                const bool on = col < end;
-                asm volatile(
-                    "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
-                    "mov.b32 %3, 0;\n\t@p ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-                    : "=&r"(r[i][0]), "=&r"(r[i][1]), "=&r"(r[i][2]), "=&r"(r[i][3])
-                    : "l"(src), "r"(static_cast<int>(on)));
+            for (int q = 0; q < V; ++q) {
+                if (c + q < 0 || c + q >= cols) continue;
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t e = reinterpret_cast<const unsigned short*>(x)[c + q];
+                    w[q / 2] = q & 1 ? (w[q / 2] & 0xffffu) | e << 16 : (w[q / 2] & 0xffff0000u) | e;
+                } else {
+                    w[q] = __float_as_uint(x[c + q]);
+                }
             }
-        }
-    }
-    // the vectors as words, -inf in the places past `end`
-    __device__ __forceinline__ void settle(uint32_t (&w)[4 * NV], const T* row, int v0, int end, uint32_t stage) const {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (v0 + i * THREADS) * V, valid = end - col;
-            uint4 u;
-            if constexpr (LOOSE)
-                u = settle_words<T>(r[i], row + col, valid, stage);
-            else
-                u = make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
-            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-            if (valid < V) tlp_cut<T>(w + 4 * i, valid);
         }
     }
 };
 
 // A of a chunk some of whose elements are masked: a term whose exponential is 0 is 0.
 // Out of line, from the chunk read once more, so that the loop need not keep it.
-template <typename T, bool LOOSE, int NV, int THREADS>
-__device__ __noinline__ float tlp_masked(const T* row, int v0, int end, bool edge, const Extent& all, uint32_t stage,
-                                         float base, float c) {
-    constexpr int V = wide_v<T>();
+template <typename T, int NV, int THREADS>
+__device__ __noinline__ float tlp_masked(const TlpRow<T> row, int v0, int v1, float base, float c) {
     float a = 0.f;
     for (int i = 0; i < NV; ++i) {
-        TlpChunk<T, LOOSE, 1, THREADS> one;
         uint32_t w[4];
-        one.load(row, v0 + i * THREADS, end, edge, all);
-        one.settle(w, row, v0 + i * THREADS, end, stage);
+        row.load(w, v0 + i * THREADS, v0 + i * THREADS < v1);
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
+        for (int q = 0; q < TlpRow<T>::V; ++q) {
             const float t = (tlp_elem<T>(w, q) - base) * c, e = ex2_approx(t);
             a += e > 0.f ? e * t : 0.f;
         }
@@ -239,20 +222,16 @@ __device__ __forceinline__ void tlp_rank(TlpShared<THREADS>& sh, int n, int k) {
 }
 
 // The block's k largest, one after another, chunk by chunk (the list has overflowed).
-template <typename T, bool LOOSE, int THREADS>
-__device__ __noinline__ void tlp_again(TlpShared<THREADS>& sh, const T* row, int v0, int v1, int end, bool edge,
-                                       const Extent& all, int k) {
-    constexpr int V = wide_v<T>(), NV = 2;
-    __shared__ __align__(16) uint8_t words[LOOSE ? THREADS / 32 * WARP_WORDS_BYTES : 16];
-    const uint32_t stage = smem_addr(words) + (LOOSE ? threadIdx.x / 32 * WARP_WORDS_BYTES : 0);
+template <typename T, int THREADS>
+__device__ __noinline__ void tlp_again(TlpShared<THREADS>& sh, const TlpRow<T> row, int v0, int v1, int k) {
+    constexpr int V = TlpRow<T>::V, NV = 2;
     if (threadIdx.x < TLP_MAX_TOP) sh.best[threadIdx.x] = 0;
     __syncthreads();
     for (int v = v0; v < v1; v += THREADS * NV) {
-        TlpChunk<T, LOOSE, NV, THREADS> c;
         uint32_t w[4 * NV];
         const int mine = v + threadIdx.x;
-        c.load(row, mine, end, edge, all);
-        c.settle(w, row, mine, end, stage);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) row.load(w + 4 * i, mine + i * THREADS, mine + i * THREADS < v1);
         unsigned long long last = ~0ull;
         for (int round = 0; round < k; ++round) {
             unsigned long long top = sh.best[k - 1];  // none at or below it is wanted
@@ -262,7 +241,7 @@ __device__ __noinline__ void tlp_again(TlpShared<THREADS>& sh, const T* row, int
                 for (int q = 0; q < V; ++q) {
                     const float x = tlp_elem<T>(w + 4 * i, q);
                     if (!(x > -INFINITY)) continue;
-                    const unsigned long long key = tlp_key(x, (mine + i * THREADS) * V + q);
+                    const unsigned long long key = tlp_key(x, row.col(mine + i * THREADS) + q);
                     if (key < last && key > top) top = key;
                 }
 #pragma unroll
@@ -293,41 +272,41 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
     return v;
 }
-template <typename T, bool LOOSE, int THREADS>
+template <typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_kernel(const TlpParams p) {
-    constexpr int V = wide_v<T>(), NV = LOOSE ? 2 : 4, P = Pairs<T>::N, WARPS = THREADS / 32;
+    constexpr int V = wide_v<T>(), NV = TLP_NV, P = Pairs<T>::N, WARPS = THREADS / 32;
     __shared__ TlpShared<THREADS> sh;
-    __shared__ __align__(16) uint8_t words[LOOSE ? WARPS * WARP_WORDS_BYTES : 16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t stage = smem_addr(words) + (LOOSE ? warp * WARP_WORDS_BYTES : 0);
     const int rank = p.cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const long long at = blockIdx.x / p.cluster;
-    const T* row = static_cast<const T*>(p.x) + at * p.ld;
-    const bool edge = at == 0 || at == p.M - 1;
-    const Extent all = extent_of<T>(p.x, p.M, p.ld, p.V);
-    const int vecs = (p.V + V - 1) / V;
+    const TlpRow<T> row(static_cast<const T*>(p.x) + at * p.ld, p.V);
+    const int vecs = row.vecs();
     const int v0 = min(vecs, rank * p.per), v1 = min(vecs, v0 + p.per);
-    const int end = min(p.V, v1 * V);  // one past the last column of this block
     const int lanes = THREADS / (p.top <= 16 ? 16 : 32);  // of a group: more groups than alternatives
     if (threadIdx.x == 0) sh.n = sh.n_vecs = 0, sh.bound = -FLT_MAX;
     long long y = 0;
     float xy = 0.f;
     if (rank == 0 && threadIdx.x == 0) {
         y = p.y[at];
-        if (y >= 0 && y < p.V) xy = static_cast<float>(row[y]);
+        if (y >= 0 && y < p.V) xy = static_cast<float>(row.x[y]);
     }
     __syncthreads();
 
     TlpStats st{-INFINITY, 0.f, 0.f};
     float bound = -INFINITY;
-    TlpChunk<T, LOOSE, NV, THREADS> next;
-    next.load(row, v0 + threadIdx.x, end, edge, all);
+    uint32_t next[4 * NV];
+    auto load = [&](int v) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) row.load(next + 4 * i, v + i * THREADS, v + i * THREADS < v1);
+    };
+    load(v0 + threadIdx.x);
     unsigned chunk = 0;
     for (int v = v0; v < v1; v += THREADS * NV, ++chunk) {
         const int mine = v + threadIdx.x;
         uint32_t w[4 * NV];
-        next.settle(w, row, mine, end, stage);
-        if (v + THREADS * NV < v1) next.load(row, mine + THREADS * NV, end, edge, all);
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) w[i] = next[i];
+        if (v + THREADS * NV < v1) load(mine + THREADS * NV);
         float tops[NV], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) tops[i] = tlp_max<T>(w + 4 * i), top = fmaxf(top, tops[i]);
@@ -348,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
         TlpStats now{m, f2_sum(s2), f2_sum(a2)};
         // an infinite exponent times its 0
         if (__any_sync(0xffffffffu, now.a != now.a && now.s == now.s))
-            now.a = tlp_masked<T, LOOSE, NV, THREADS>(row, mine, end, edge, all, stage, base, p.c);
+            now.a = tlp_masked<T, NV, THREADS>(row, mine, v1, base, p.c);
         if (m > st.m) {
             const float d = st.m == -INFINITY ? 0.f : (st.m - m) * p.c, f = ex2_approx(d);
             now.a += f > 0.f ? f * (st.a + d * st.s) : 0.f;
@@ -396,16 +375,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
         bound = tlp_bound(sh, p.top, lanes);
         const int listed = sh.n_vecs;
         for (int i = threadIdx.x; i < min(listed, TLP_LIST); i += THREADS) {
-            const int col = sh.vecs[i] * V;
-            uint32_t w[4] = {0, 0, 0, 0};
-            if constexpr (!LOOSE) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + col));
-                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-            }
+            const int col = row.col(sh.vecs[i]);
+            uint32_t w[4];
+            row.load(w, sh.vecs[i], true);
 #pragma unroll
             for (int q = 0; q < V; ++q) {
-                if (col + q >= end) break;
-                const float x = LOOSE ? static_cast<float>(row[col + q]) : tlp_elem<T>(w, q);
+                const float x = tlp_elem<T>(w, q);
                 if (x >= bound) {
                     const int n = atomicAdd(&sh.n, 1);
                     if (n < TLP_LIST) sh.list[n] = tlp_key(x, col + q);
@@ -415,7 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
         __syncthreads();
         const int n = sh.n;
         if (listed > TLP_LIST || n > TLP_LIST)
-            tlp_again<T, LOOSE, THREADS>(sh, row, v0, v1, end, edge, all, p.top);
+            tlp_again(sh, row, v0, v1, p.top);
         else
             tlp_rank(sh, n, p.top);
     }
@@ -504,12 +479,9 @@ __global__ void __launch_bounds__(TLPB_THREADS) flp_token_logprob_bwd_kernel(con
     const long long y = p.y[at];
     const float lse = p.lse[at];
     const bool zero = y == p.ignore_index || lse == -INFINITY;
-    TlpChunk<T, LOOSE, NV, 32> x;
-    uint32_t w[4 * NV];
-    if (!zero) {
-        x.load(row, v0, p.V, at == 0 || at == p.M - 1, extent_of<T>(p.x, p.M, p.ld, p.V));
-        x.settle(w, row, v0, p.V, stage);
-    }
+    const T* src = row + v0 * V;
+    RowVecs<T, LOOSE, NV> x;
+    x.load(src, p.V - v0 * V, !zero, at == 0 || at == p.M - 1, extent_of<T>(p.x, p.M, p.ld, p.V));
     const float g_lp = p.g_lp ? p.g_lp[at] : 0.f;
     const float g_ent = p.entropy && p.g_ent ? p.g_ent[at] : 0.f, h = p.entropy ? p.entropy[at] : 0.f;
     const uint64_t s2 = f2_splat(p.scale), off = f2_splat(-lse), log2e = f2_splat(LOG2E);
@@ -522,7 +494,7 @@ __global__ void __launch_bounds__(TLPB_THREADS) flp_token_logprob_bwd_kernel(con
 #pragma unroll
             for (int q = 0; q < P; ++q) g[q] = 0;
         } else {
-            const uint4 u = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            const uint4 u = x.get(i, src, p.V - v0 * V, stage);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 float lo, hi;

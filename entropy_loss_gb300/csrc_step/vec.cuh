@@ -135,6 +135,15 @@ __device__ __forceinline__ uint32_t ld_global_4_at(const void* p, bool on) {
                  : "l"(p), "n"(OFF), "r"(static_cast<int>(on)));
     return x;
 }
+__device__ __forceinline__ uint4 ld_global_16(const void* p, bool on) {
+    uint4 u;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+        : "l"(p), "r"(static_cast<int>(on)));
+    return u;
+}
 __device__ __forceinline__ void st_global_16(void* p, uint4 u, bool on) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
                  "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w), "r"(static_cast<int>(on))
@@ -390,6 +399,33 @@ __device__ __forceinline__ void store_row_vec(T* dst, const uint4& u, int valid,
         __syncwarp();
     }
 }
+
+// NV x 32 consecutive vectors of a row, NV a lane: loads first, then vectors.
+template <typename T, bool LOOSE, int NV>
+struct RowVecs {
+    static constexpr int V = wide_v<T>();
+    static constexpr int W = LOOSE ? WarpWords<T>::N : 4;
+    uint32_t r[NV][W];
+    // src: this lane's first vector, of which and beyond the row holds `left` elements
+    __device__ __forceinline__ void load(const T* src, int left, bool on, bool edge, const Extent& all) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int valid = on ? left - i * 32 * V : -32 * V;
+            if constexpr (LOOSE) {
+                load_words<T>(r[i], src + i * 32 * V, valid, edge, all);
+            } else {
+                const uint4 u = ld_global_16(src + i * 32 * V, valid > 0);
+                r[i][0] = u.x, r[i][1] = u.y, r[i][2] = u.z, r[i][3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ uint4 get(int i, const T* src, int left, uint32_t stage) const {
+        if constexpr (LOOSE)
+            return settle_words<T>(r[i], src + i * 32 * V, left - i * 32 * V, stage);
+        else
+            return make_uint4(r[i][0], r[i][1], r[i][2], r[i][3]);
+    }
+};
 
 // ----------------------------------------------------------------- reductions
 
