@@ -89,8 +89,12 @@ extern "C" flp_status flp_token_logprob(const void* logits, int64_t ld, int dtyp
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto typed = [&](auto t) {
         using T = decltype(t);
-        // rows that a block of 128 threads reads at once
-        return V <= TLP_NV * 128 * wide_v<T>() ? tlp_launch<T, 128>(p, d->sm_count, s) : tlp_launch<T, 256>(p, d->sm_count, s);
+        // Short rows in smaller blocks, of which an SM holds more, where there are enough rows
+        // to fill it; a row of up to 4 vectors a thread at once in any case.
+        const int64_t vecs = cdiv(V, wide_v<T>());
+        if (M >= 32 * d->sm_count && vecs <= 1024) return tlp_launch<T, 32>(p, d->sm_count, s);
+        if (vecs <= TLP_NV * 128 || (M >= 8 * d->sm_count && vecs <= 4096)) return tlp_launch<T, 128>(p, d->sm_count, s);
+        return tlp_launch<T, 256>(p, d->sm_count, s);
     };
     return dtype == FLP_BF16 ? typed(bf16{}) : typed(float{});
 }

@@ -33,7 +33,9 @@
 namespace flp {
 
 constexpr int TLP_MAX_TOP = 32;
-constexpr int TLP_LIST = 512;      // vectors, and then elements, that a block can list
+// vectors, and then elements, that a block can list
+template <int THREADS>
+constexpr int TLP_LIST = THREADS == 32 ? 256 : 512;
 constexpr int TLP_CLUSTER = 8;     // blocks of a row at most
 constexpr int TLP_NV = 4;          // vectors that a thread takes at a time
 
@@ -158,13 +160,13 @@ __device__ __noinline__ float tlp_masked(const TlpRow<T> row, int v0, int v1, fl
 template <int THREADS>
 struct TlpShared {
     static constexpr int WARPS = THREADS / 32;
-    unsigned long long list[TLP_LIST];
+    unsigned long long list[TLP_LIST<THREADS>];
     unsigned long long best[TLP_MAX_TOP];  // this block's, in order; 0: none
     unsigned long long warp_key[WARPS];
     __align__(16) float group[32];         // the largest that each group of threads has read
     TlpStats warp_stats[WARPS];
     TlpStats stats;                        // this block's
-    int vecs[TLP_LIST];
+    int vecs[TLP_LIST<THREADS>];
     int n_vecs, n;                         // vectors and elements listed
     float bound;                           // the latest
 };
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
                 for (int i = 0; i < NV; ++i) {
                     if (tops[i] >= bound) {
                         const int n = atomicAdd(&sh.n_vecs, 1);
-                        if (n < TLP_LIST) sh.vecs[n] = mine + i * THREADS;
+                        if (n < TLP_LIST<THREADS>) sh.vecs[n] = mine + i * THREADS;
                     }
                 }
             }
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
     if (p.top > 0) {
         bound = tlp_bound(sh, p.top, lanes);
         const int listed = sh.n_vecs;
-        for (int i = threadIdx.x; i < min(listed, TLP_LIST); i += THREADS) {
+        for (int i = threadIdx.x; i < min(listed, TLP_LIST<THREADS>); i += THREADS) {
             const int col = row.col(sh.vecs[i]);
             uint32_t w[4];
             row.load(w, sh.vecs[i], true);
@@ -383,13 +385,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
                 const float x = tlp_elem<T>(w, q);
                 if (x >= bound) {
                     const int n = atomicAdd(&sh.n, 1);
-                    if (n < TLP_LIST) sh.list[n] = tlp_key(x, col + q);
+                    if (n < TLP_LIST<THREADS>) sh.list[n] = tlp_key(x, col + q);
                 }
             }
         }
         __syncthreads();
         const int n = sh.n;
-        if (listed > TLP_LIST || n > TLP_LIST)
+        if (listed > TLP_LIST<THREADS> || n > TLP_LIST<THREADS>)
             tlp_again(sh, row, v0, v1, p.top);
         else
             tlp_rank(sh, n, p.top);
