@@ -119,8 +119,15 @@ flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const vo
 
 struct LinTurnPlan {
     int nt, tiles_t, tiles_w, split, stages;
+    uint32_t cols;  // of TMEM
     size_t smem;
 };
+
+// CTAs of a cluster wait for one another while they hold TMEM.  None may wait for TMEM
+// itself, or clusters could keep each other from starting: every CTA asks for its columns'
+// share of an SM's shared memory, so that those that fit an SM together, of any of these
+// launches, find their 512 columns (a CTA of a pair takes the whole SM).
+constexpr size_t kSmemPerTmemColumn = 228 * 1024 / 512;
 
 // Rows of x in as few tiles as hold them, evenly; the contraction split over as many CTAs
 // as are resident, two an SM.
@@ -137,7 +144,8 @@ LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
     while (t.split < most && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
     const size_t room = 108 * 1024, stage = lin_turn_stage(t.nt);
     t.stages = static_cast<int>(std::min<int64_t>({LT_STAGES, static_cast<int64_t>(room / stage), cdiv(KB, t.split)}));
-    t.smem = std::max<size_t>(t.stages * stage, static_cast<size_t>(t.nt) * 128 * 4) + 1024;
+    for (t.cols = 32; t.cols < static_cast<uint32_t>(t.nt);) t.cols *= 2;
+    t.smem = std::max<size_t>({t.stages * stage + 1024, static_cast<size_t>(t.nt) * 128 * 4 + 1024, t.cols * kSmemPerTmemColumn});
     return t;
 }
 
@@ -157,7 +165,7 @@ flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const
     p.tiles_t = t.tiles_t;
     p.split = t.split;
     p.stages = t.stages;
-    for (p.cols = 32; p.cols < static_cast<uint32_t>(t.nt);) p.cols *= 2;
+    p.cols = t.cols;
     p.e = e;
     p.err = err;
     p.wait_limit_ns = wait_limit_ns;

@@ -1030,8 +1030,9 @@ def token_logprob(logits, y, *, top: int = 0, scale: float = 1.0, ignore_index: 
     M, V = logits.shape
     code, dev = _dtype(logits, "logits"), logits.device
     yp = _row_values(y, M, dev, "targets", torch.int64)
-    logprob, lse, *entropy = torch.empty((3 if compute_entropy else 2, M), dtype=torch.float32, device=dev).unbind(0)
-    entropy = entropy[0] if compute_entropy else None
+    logprob = torch.empty(M, dtype=torch.float32, device=dev)
+    lse = torch.empty(M, dtype=torch.float32, device=dev)
+    entropy = torch.empty(M, dtype=torch.float32, device=dev) if compute_entropy else None
     values = index = None
     if top > 0:
         values = torch.empty((M, top), dtype=torch.float32, device=dev)

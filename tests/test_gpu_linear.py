@@ -110,6 +110,27 @@ def test_layouts(flp, bias, residual, keep, pads, offsets):
     run_forward(flp, 200, 296, 136, "silu", bias, residual, keep, pads, offsets)
 
 
+@pytest.mark.parametrize("M", [1, 2, 80, 128, 129])
+@pytest.mark.parametrize("K", [64, 203, 1001])
+def test_few_rows_at_odd_places(flp, M, K):
+    run_forward(flp, M, 300, K, "gelu_tanh", torch.bfloat16, True, True, (1, 3, 5, 2), (3, 1, 2, 1))
+    run_forward(flp, M, 2051, K, "silu", torch.float32, False, False)
+
+
+def test_few_rows_on_many_streams(flp):
+    """Clusters that hold tensor memory beside one another: each launch fits wherever it lands."""
+    g = torch.Generator().manual_seed(1)
+    x = [matrix(M, 128, gen=g)[1] for M in (16, 80, 128)]
+    _, W = matrix(9000, 128, gen=g, scale=0.1)
+    want = [flp.linear(v, W) for v in x]
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    got = [(i % 3, flp.linear(x[i % 3], W, stream=streams[i % 6])) for i in range(48)]
+    torch.cuda.synchronize()
+    for i, y in got:
+        assert torch.equal(y, want[i])
+
+
 @pytest.mark.parametrize("N", [19456, 19457])
 def test_more_tiles_than_pairs(flp, N):
     """Whole tiles written directly beside split ones: 3 x 38 tiles on 76 pairs."""
