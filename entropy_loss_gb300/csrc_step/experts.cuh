@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(SORT_THREADS) flp_expert_count_kernel(const So
 
 // Positions.  A block knows what all blocks count of each expert, so it finds where its
 // own slots of each expert begin without another pass; a warp then ranks its slots in
-// order, 32 at a time.
+// order, 32 at a time.  Bound by the chain of its phases: 32 slots take 6 us in one block,
+// 524288 slots of 256 experts 4 us of counting and 13 here, of which their 8 MB would take
+// 1.2.
 __global__ void __launch_bounds__(SORT_THREADS) flp_expert_place_kernel(const SortParams p) {
     extern __shared__ int hist[];
     __shared__ int total[SORT_MAX_E + 1], before[SORT_MAX_E + 1], sums[SORT_WARPS];
