@@ -67,6 +67,13 @@ inline bool rows_vec(const void* p, int64_t ld, int64_t H, int dtype) {
     return rows16(p, ld, dtype) && (H * elem(dtype)) % 16 == 0;
 }
 
+// Vectors of aligned rows that are short, else 0.  The short kernels number their threads in
+// 32 bits: the tokens of one that would have more go the long rows' way.
+inline int64_t short_vecs(const MoveParams& p, int dtype, bool loose) {
+    const int64_t vecs = p.H * elem(dtype) / 16;
+    return !loose && vecs <= SHORT_VECS && p.T <= INT32_MAX / SHORT_VECS ? vecs : 0;
+}
+
 template <typename F>
 flp_status move_typed(int dtype, bool loose, F&& f) {
     auto typed = [&](auto t) { return loose ? f(t, std::true_type{}) : f(t, std::false_type{}); };
@@ -139,7 +146,12 @@ extern "C" flp_status flp_expert_gather(const void* X, int64_t ldx, int dtype, i
     p.ld_many = ldxs;
     int64_t grid;
     if ((st = move_grid(p, GATHER_NV, dtype, &grid)) != FLP_OK) return st;
-    return move_typed(dtype, !(rows_vec(X, ldx, H, dtype) && rows_vec(XS, ldxs, H, dtype)), [&](auto t, auto loose) {
+    const bool is_loose = !(rows_vec(X, ldx, H, dtype) && rows_vec(XS, ldxs, H, dtype));
+    const int64_t vecs = short_vecs(p, dtype, is_loose);
+    return move_typed(dtype, is_loose, [&](auto t, auto loose) {
+        if (vecs)
+            return launch_step(flp_expert_gather_short_kernel<decltype(t)>, cdiv(T * vecs, MOVE_THREADS), MOVE_THREADS, 0,
+                               static_cast<cudaStream_t>(stream), "flp_expert_gather_short_kernel launch", false, p);
         return launch_step(flp_expert_gather_kernel<decltype(t), decltype(loose)::value>, grid, MOVE_THREADS, 0,
                            static_cast<cudaStream_t>(stream), "flp_expert_gather_kernel launch", false, p);
     });
@@ -163,7 +175,12 @@ extern "C" flp_status flp_expert_combine(const void* YS, int64_t ldys, int dtype
     p.ld_one = ldy;
     int64_t grid;
     if ((st = move_grid(p, COMBINE_NV, dtype, &grid)) != FLP_OK) return st;
-    return move_typed(dtype, !(rows_vec(YS, ldys, H, dtype) && rows_vec(Y, ldy, H, dtype)), [&](auto t, auto loose) {
+    const bool is_loose = !(rows_vec(YS, ldys, H, dtype) && rows_vec(Y, ldy, H, dtype));
+    const int64_t vecs = short_vecs(p, dtype, is_loose);
+    return move_typed(dtype, is_loose, [&](auto t, auto loose) {
+        if (vecs)
+            return launch_step(flp_expert_combine_short_kernel<decltype(t)>, cdiv(T * vecs, MOVE_THREADS), MOVE_THREADS, 0,
+                               static_cast<cudaStream_t>(stream), "flp_expert_combine_short_kernel launch", false, p);
         return launch_step(flp_expert_combine_kernel<decltype(t), decltype(loose)::value>, grid, MOVE_THREADS, 0,
                            static_cast<cudaStream_t>(stream), "flp_expert_combine_kernel launch", false, p);
     });
@@ -199,7 +216,13 @@ extern "C" flp_status flp_expert_combine_backward(const void* dY, int64_t lddy, 
     const bool warp = T >= 2048 || p.chunks <= 2;
     const bool loose = !(rows_vec(dY, lddy, H, dtype) && rows_vec(dYS, lddys, H, dtype) &&
                          (!dweights || rows_vec(YS, ldys, H, dtype)));
+    const int64_t vecs = short_vecs(p, dtype, loose);
+    int lanes = 1;
+    while (lanes < vecs) lanes *= 2;
     return move_typed(dtype, loose, [&](auto t, auto is_loose) {
+        if (vecs)
+            return launch_step(flp_expert_combine_bwd_short_kernel<decltype(t)>, cdiv(T * lanes, MOVE_THREADS), MOVE_THREADS, 0,
+                               static_cast<cudaStream_t>(stream), "flp_expert_combine_bwd_short_kernel launch", false, p, lanes);
         constexpr bool LOOSE = decltype(is_loose)::value;
         auto go = [&](auto* kernel, int64_t blocks) {
             return launch_step(kernel, blocks, MOVE_THREADS, 0, static_cast<cudaStream_t>(stream),

@@ -396,4 +396,108 @@ __global__ void __launch_bounds__(MOVE_THREADS, LOOSE ? 2 : 3) flp_expert_combin
     }
 }
 
+// ------------------------------------------------------------- short rows
+//
+// Aligned rows of up to 32 vectors would leave lanes of the warp a token has idle, or give it
+// less than the latency of its rows is worth: a thread takes one vector of one token instead,
+// and in the backward `lanes` of a warp (a power of two that holds a row) a token.  Bound by
+// latency and issue.  Gather, combine and its backward, long way -> short way (graph replay,
+// some 5 us of each an empty one): 65536 x 8 x 64 bf16 37 -> 17, 56 -> 23, 113 -> 37 us (the
+// bytes 11, 11, 21); 65536 x 4 x 256 bf16, 32 vectors, 33 -> 31, 46 -> 42, 76 -> 66; at 48
+// vectors, 40000 x 2 x 384, it would be 21 -> 21, 29 -> 30, 46 -> 62.
+
+constexpr int SHORT_VECS = 32;
+
+template <typename T>
+__global__ void __launch_bounds__(MOVE_THREADS) flp_expert_gather_short_kernel(const MoveParams p) {
+    constexpr int V = wide_v<T>();
+    const unsigned vecs = static_cast<unsigned>(p.H / V), i = blockIdx.x * MOVE_THREADS + threadIdx.x, token = i / vecs;
+    if (token >= p.T) return;
+    const int col = static_cast<int>(i - token * vecs) * V;
+    const long long total = *p.total, S = p.T * p.k;
+    const uint4 v = ld_global_16(static_cast<const T*>(p.one) + token * p.ld_one + col, true);
+    const int* rows = p.rows + static_cast<long long>(token) * p.k;
+    for (int j = 0; j < p.k; ++j) {
+        const int pos = rows[j];
+        if (static_cast<unsigned>(pos) >= S) continue;  // not a position
+        st_global_16(static_cast<T*>(p.many) + pos * p.ld_many + col, pos < total ? v : make_uint4(0, 0, 0, 0), true);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(MOVE_THREADS) flp_expert_combine_short_kernel(const MoveParams p) {
+    constexpr int V = wide_v<T>(), P = V / 2, J = 4;
+    const unsigned vecs = static_cast<unsigned>(p.H / V), i = blockIdx.x * MOVE_THREADS + threadIdx.x, token = i / vecs;
+    if (token >= p.T) return;
+    const int col = static_cast<int>(i - token * vecs) * V;
+    const long long total = *p.total, S = p.T * p.k, slot = static_cast<long long>(token) * p.k;
+    uint64_t sum[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) sum[q] = 0;
+    for (int j = 0; j < p.k; j += J) {
+        uint4 v[J];
+        float w[J];
+        bool on[J];
+#pragma unroll
+        for (int c = 0; c < J; ++c) {
+            const int pos = j + c < p.k ? p.rows[slot + j + c] : -1;
+            on[c] = static_cast<unsigned>(pos) < S && pos < total;
+            w[c] = on[c] ? move_weight(p, slot + j + c) : 0.f;
+            v[c] = ld_global_16(static_cast<const T*>(p.many) + pos * p.ld_many + col, on[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < J; ++c) {
+            if (!on[c]) continue;
+#pragma unroll
+            for (int q = 0; q < P; ++q) sum[q] = f2_fma(Pairs<T>::get(v[c], q), f2_splat(w[c]), sum[q]);
+        }
+    }
+    st_global_16(static_cast<T*>(p.one) + token * p.ld_one + col, Pairs<T>::put(sum), true);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(MOVE_THREADS) flp_expert_combine_bwd_short_kernel(const MoveParams p, int lanes) {
+    constexpr int V = wide_v<T>(), P = V / 2, J = 4;
+    const unsigned i = blockIdx.x * MOVE_THREADS + threadIdx.x, at = i / static_cast<unsigned>(lanes);
+    const bool here = at < p.T;
+    const long long token = here ? at : p.T - 1;  // the lanes past the last token help its warp's sums
+    const int col = (threadIdx.x & (lanes - 1)) * V;
+    const bool mine = here && col < p.H;
+    const long long total = *p.total, S = p.T * p.k, slot = token * p.k;
+    const uint4 dv = ld_global_16(static_cast<const T*>(p.one) + token * p.ld_one + col, mine);
+    uint64_t d[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) d[q] = Pairs<T>::get(dv, q);
+    const bool dots = p.dweights != nullptr;
+    for (int j = 0; j < p.k; j += J) {
+        uint4 v[J];
+        int pos[J];
+        float w[J];
+        bool on[J];
+#pragma unroll
+        for (int c = 0; c < J; ++c) {
+            pos[c] = j + c < p.k ? p.rows[slot + j + c] : -1;
+            on[c] = static_cast<unsigned>(pos[c]) < S && pos[c] < total;
+            w[c] = on[c] ? move_weight(p, slot + j + c) : 0.f;
+            v[c] = ld_global_16(static_cast<const T*>(p.many) + pos[c] * p.ld_many + col, dots && mine && on[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < J; ++c) {
+            uint64_t g[P], dot = 0;
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                dot = f2_fma(Pairs<T>::get(v[c], q), d[q], dot);
+                g[q] = on[c] ? f2_mul(d[q], f2_splat(w[c])) : 0ull;
+            }
+            st_global_16(static_cast<T*>(p.out) + pos[c] * p.ld_out + col, Pairs<T>::put(g),
+                         mine && static_cast<unsigned>(pos[c]) < S);
+            if (dots) {  // the whole grid
+                float s = on[c] && mine ? f2_sum(dot) : 0.f;
+                for (int o = lanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (here && col == 0 && j + c < p.k) p.dweights[slot + j + c] = s;
+            }
+        }
+    }
+}
+
 }  // namespace flp

@@ -84,8 +84,8 @@ def untouched(buf, view, before):
 
 
 # width, extra pitch and offset of the tokens' matrix and of the slots'
-LAYOUTS = [(8, 0, 0, 0, 0), (64, 0, 0, 0, 0), (2048, 0, 0, 8, 0), (5120, 0, 8, 0, 0), (1, 0, 0, 0, 0), (7, 1, 0, 0, 0), (33, 0, 1, 5, 3),
-           (257, 0, 0, 2, 1), (1000, 4, 0, 1, 0), (2047, 0, 1, 0, 0), (520, 0, 0, 1, 1)]
+LAYOUTS = [(8, 0, 0, 0, 0), (24, 0, 8, 16, 0), (64, 0, 0, 0, 0), (120, 8, 0, 0, 8), (256, 0, 0, 0, 0), (2048, 0, 0, 8, 0),
+           (5120, 0, 8, 0, 0), (1, 0, 0, 0, 0), (7, 1, 0, 0, 0), (33, 0, 1, 5, 3), (257, 0, 0, 2, 1), (1000, 4, 0, 1, 0), (2047, 0, 1, 0, 0), (520, 0, 0, 1, 1)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -110,7 +110,7 @@ def test_gather_is_a_copy(flp, dtype, H, pad1, off1, pad2, off2):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("H,pad1,off1,pad2,off2", LAYOUTS)
 def test_combine_and_its_gradient(flp, dtype, weights, H, pad1, off1, pad2, off2):
-    for T, k, E in ((29, 3, 5), (6, 9, 9)):
+    for T, k, E in ((29, 3, 5), (6, 9, 9), (2100, 2, 7)):
         g = torch.Generator().manual_seed(H)
         e = choices(T, k, E, seed=H, dropped=0.3)
         e[1] = -1  # a token without an expert
