@@ -6,7 +6,9 @@ namespace {
 
 flp_status expert_sizes(int64_t T, int64_t k) {
     if (T < 0 || k < 1) return fail(FLP_ERR_INVALID_ARG, "T >= 0 and k >= 1 required");
-    if (T > kMaxRows || k > kMaxRows || T * k > kMaxRows) return fail(FLP_ERR_UNSUPPORTED, "more than 2^31 - 1 slots");
+    // the movers count a token's choices in steps of up to 32, in 32 bits
+    if (k > 1 << 30) return fail(FLP_ERR_UNSUPPORTED, "more than 2^30 choices a token");
+    if (T > kMaxRows || T * k > kMaxRows) return fail(FLP_ERR_UNSUPPORTED, "more than 2^31 - 1 slots");
     return FLP_OK;
 }
 

@@ -538,7 +538,7 @@ flp_status flp_balance_loss_ex(const void* logits, int64_t ld, int dtype, const 
 /*
  * Tokens sorted by expert.  T tokens choose k experts each; slot t k + j is
  * token t's j-th choice.  experts: int64 [T, k], values outside [0, E) are
- * dropped slots (1 <= E <= 1024, T k < 2^31).  A stable counting sort, dropped
+ * dropped slots (1 <= E <= 1024, k <= 2^30, T k < 2^31).  A stable counting sort, dropped
  * slots last:
  *   rows    int32 [T, k]  the position of every slot
  *   slots   int32 [T k]   the slot at every position

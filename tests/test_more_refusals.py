@@ -29,7 +29,8 @@ def test_expert_sort(flp, b):
     for o in (dict(T=-1), dict(k=0), dict(E=0), dict(e=None), dict(rows=None), dict(slots=None), dict(counts=None),
               dict(offsets=None), dict(e=b + 4), dict(rows=b + 2), dict(slots=b + 1), dict(counts=b + 4), dict(offsets=b + 4)):
         assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
-    for o in (dict(E=1025), dict(T=2 ** 31), dict(T=2 ** 30, k=2), dict(T=2 ** 40, k=2 ** 40)):
+    for o in (dict(E=1025), dict(T=2 ** 31), dict(T=2 ** 30, k=2), dict(T=2 ** 40, k=2 ** 40),
+              dict(T=1, k=2 ** 31 - 1), dict(T=1, k=2 ** 30 + 1)):
         assert call(**o) == flp.FLP_ERR_UNSUPPORTED, o
     for o in (dict(T=5000, ws=None), dict(T=5000, n=4096), dict(T=5000, ws=b + 4)):
         assert call(**o) == flp.FLP_ERR_WORKSPACE, o
@@ -66,7 +67,8 @@ def test_expert_rows(flp, b):
         for o in (dict(T=-1), dict(H=0), dict(k=0), dict(dt=2), dict(x=None), dict(xs=None), dict(rows=None), dict(total=None),
                   dict(rows=b + 2), dict(total=b + 4), dict(ldx=63), dict(ldxs=63), dict(x=b + 1), dict(xs=b + 1)):
             assert f(**o) == flp.FLP_ERR_INVALID_ARG, (f, o)
-        assert f(T=2 ** 30, k=2) == flp.FLP_ERR_UNSUPPORTED
+        for o in (dict(T=2 ** 30, k=2), dict(T=1, k=2 ** 31 - 1), dict(T=1, k=2 ** 30 + 1)):
+            assert f(**o) == flp.FLP_ERR_UNSUPPORTED, (f, o)
         assert f(T=0, x=None, xs=None, rows=None, total=None) == flp.FLP_OK
     for f in (combine, backward):
         for o in (dict(wt=2), dict(w=b + 2), dict(w=b + 1, wt=1)):
