@@ -210,7 +210,7 @@ flp_status linear_row(LinRowParams& p, bool loose, int sm_count, bool after_kern
 
 flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 1 || K < 1) return fail(FLP_ERR_INVALID_ARG, "M >= 0, N >= 1 and K >= 1 required");
-    const int64_t most = kMaxRows - 1024;
+    const int64_t most = kMaxRows - 4096;  // eight chunks of a contraction, each rounded up to 256, end within 32 bits
     if (M > most || N > most || K > most || cdiv(M, PM) * cdiv(N, BN) > (1 << 23) || cdiv(M, PM) * cdiv(K, BN) > (1 << 23))
         return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
     return FLP_OK;

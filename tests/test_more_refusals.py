@@ -118,7 +118,8 @@ def test_linear(flp, b):
               dict(ldr=31), dict(ldp=31), dict(x=b + 1), dict(w=b + 1), dict(y=b + 1), dict(r=b + 1), dict(pre=b + 1), dict(act=5),
               dict(act=-1), dict(bt=2), dict(bias=b + 2, bt=0), dict(bias=b + 1)):
         assert call(**o) == flp.FLP_ERR_INVALID_ARG, o
-    for o in (dict(M=2 ** 31), dict(K=2 ** 31, ldx=2 ** 31, ldw=2 ** 31), dict(N=2 ** 31), dict(M=2 ** 28, N=2 ** 24)):
+    for o in (dict(M=2 ** 31), dict(K=2 ** 31, ldx=2 ** 31, ldw=2 ** 31), dict(N=2 ** 31), dict(M=2 ** 28, N=2 ** 24),
+              dict(K=2 ** 31 - 2000, ldx=2 ** 31, ldw=2 ** 31)):
         assert call(**o) == flp.FLP_ERR_UNSUPPORTED, o
     assert call(M=0, x=None, y=None) == flp.FLP_OK
     assert flp.load().flp_linear_workspace(b, 64, b, 64, 4, 32, 64, None) == flp.FLP_ERR_INVALID_ARG
