@@ -267,7 +267,8 @@ struct LinearGradLayout {
     LinTurnPlan t;
     bool turned;
     size_t off_dw, off_x, off_w, off_d, off_lo, off_part, off_sums, bytes;
-    bool copy_x, copy_w, make_d, two, sums;  // two: d as the sum of two bf16 numbers, for dW
+    bool copy_x, copy_w, make_d, two, sums;  // two: d as the sum of two bf16 numbers, for dW,
+    bool stack;                              // one below the other with x twice: one product
     int blocks, rows;  // of the column sums
 };
 
@@ -286,6 +287,11 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
     g.copy_w = want_dx && !rows_bf16(W, ldw);
     g.make_d = (want_dx || want_dw) && (activation != FLP_ACT_NONE || !rows_bf16(dY, lddy));
     g.two = want_dw && activation != FLP_ACT_NONE && dw_dtype == FLP_F32;
+    // x twice costs its copies, 6 M K bytes; a second product a launch and reading and writing dW,
+    // 8 N K (two products and one, backward through gelu_tanh: 1 row 4096 -> 16384 213 us and 103,
+    // 1024 rows 396 and 314, 2048 rows 2048 -> 2048 91 and 80; 4096 rows 4096 -> 4096 314 and 328,
+    // 8192 rows 4096 -> 16384 2060 and 2065)
+    g.stack = g.two && M <= N && (M <= 2048 || 4 * M <= N);
     g.sums = want_db;
     const int64_t strips = cdiv(N, 256);
     g.rows = static_cast<int>(std::max<int64_t>(32, cdiv(cdiv(M, std::max<int64_t>(1, cdiv(8 * sm_count, strips))), 32) * 32));
@@ -294,11 +300,11 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
     Regions r;
     r.take(kHeaderBytes);  // the error word
     g.off_dw = 0;          // whose region it begins
-    if (want_dw) r.bytes = align_up(std::max(r.bytes, weight_grad_bytes(M, N, K, dw_dtype, pairs)), 1024);
-    g.off_x = r.take(g.copy_x ? M * pad8(K) * 2 : 0);
+    if (want_dw) r.bytes = align_up(std::max(r.bytes, weight_grad_bytes(g.stack ? 2 * M : M, N, K, dw_dtype, pairs)), 1024);
+    g.off_x = r.take(g.stack ? 2 * M * pad8(K) * 2 : g.copy_x ? M * pad8(K) * 2 : 0);
     g.off_w = r.take(g.copy_w ? N * pad8(K) * 2 : 0);
-    g.off_d = r.take(g.make_d ? M * pad8(N) * 2 : 0);
-    g.off_lo = r.take(g.two ? M * pad8(N) * 2 : 0);
+    g.off_d = r.take(g.make_d ? (g.two ? 2 : 1) * M * pad8(N) * 2 : 0);
+    g.off_lo = g.off_d + M * pad8(N) * 2;
     g.off_part = r.take(want_dx ? g.l.part_bytes : 0);
     g.off_sums = r.take(g.sums ? static_cast<size_t>(g.blocks) * N * 4 : 0);
     g.bytes = r.bytes;
@@ -431,8 +437,9 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
     int* err = reinterpret_cast<int*>(ws);
     FLP_CUDA(cudaMemsetAsync(err, 0, sizeof(int), s));
     bool after = false;
-    if (g.copy_x) {
-        if ((st = align_rows(X, ldx, M, K, ws + g.off_x, pad8(K), s)) != FLP_OK) return st;
+    if (g.copy_x || g.stack) {
+        for (int i = 0; i < (g.stack ? 2 : 1); ++i)
+            if ((st = align_rows(X, ldx, M, K, ws + g.off_x + i * M * pad8(K) * 2, pad8(K), s)) != FLP_OK) return st;
         X = ws + g.off_x, ldx = pad8(K), after = true;
     }
     if (g.copy_w) {
@@ -481,8 +488,8 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         after = true;
     }
     if (!dW) return FLP_OK;
-    st = weight_grad(dY, lddy, X, ldx, M, N, K, dW, dW_dtype, 0, ws + g.off_dw, d->pairs, after, s);
-    if (st != FLP_OK || !g.two) return st;
+    st = weight_grad(dY, lddy, X, ldx, g.stack ? 2 * M : M, N, K, dW, dW_dtype, 0, ws + g.off_dw, d->pairs, after, s);
+    if (st != FLP_OK || !g.two || g.stack) return st;
     return weight_grad(ws + g.off_lo, lddy, X, ldx, M, N, K, dW, dW_dtype, 1, ws + g.off_dw, d->pairs, true, s);
 }
 
