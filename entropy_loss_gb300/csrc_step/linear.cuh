@@ -13,9 +13,9 @@
 // are split along the contraction into fp32 partial tiles, which a small kernel joins in
 // a fixed order and takes through the same epilogue.  d is rounded to bf16 by a pass over
 // dy and v that also sums db from the unrounded values; dW is the contraction of
-// wgrad.cuh.  The rounding (2^-9 of each value) leaves bf16 results their own, but not an
-// fp32 dW: for that one d is written as the sum of two bf16 numbers (2^-17 of it), whose
-// products are added.
+// wgrad.cuh.  The rounding (2^-8 of each value) leaves bf16 results their own, but not an
+// fp32 dW: for that one d is written as the sum of two bf16 numbers (2^-16 of it), and
+// both are contracted with x, below one another in one product or in two.
 //
 // Bound by the tensor cores at many rows: 8192 x 4096 -> 16384 (582 us at the measured
 // matrix rate) takes 568 us plain, 611 with a bias and gelu_tanh, 724 with v kept as well
