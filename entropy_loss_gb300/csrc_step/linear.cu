@@ -131,7 +131,7 @@ constexpr size_t kSmemPerTmemColumn = 228 * 1024 / 512;
 
 // Rows of x in as few tiles as hold them, evenly; the contraction split over as many CTAs
 // as are resident, two an SM.
-LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
+LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count, bool low = false) {
     LinTurnPlan t{};
     t.tiles_t = static_cast<int>(cdiv(M, LT_MAX_T));
     t.nt = static_cast<int>(cdiv(cdiv(M, t.tiles_t), 16) * 16);
@@ -142,7 +142,7 @@ LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
     // eight; 8192 -> 1024: 21 and 17)
     const int most = tiles * 8 <= sm_count ? 8 : 4;
     while (t.split < most && tiles * t.split * 2 <= 2 * sm_count && t.split * 2 <= KB) t.split *= 2;
-    const size_t room = 108 * 1024, stage = lin_turn_stage(t.nt);
+    const size_t room = 108 * 1024, stage = lin_turn_stage(t.nt, low);
     t.stages = static_cast<int>(std::min<int64_t>({LT_STAGES, static_cast<int64_t>(room / stage), cdiv(KB, t.split)}));
     for (t.cols = 32; t.cols < static_cast<uint32_t>(t.nt);) t.cols *= 2;
     t.smem = std::max<size_t>({t.stages * stage + 1024, static_cast<size_t>(t.nt) * 128 * 4 + 1024, t.cols * kSmemPerTmemColumn});
@@ -151,11 +151,11 @@ LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count) {
 
 flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const void* w, int64_t ldw, bool w_mn, int64_t M,
                          int64_t N, int64_t depth, const LinEpilogue& e, int* err, unsigned long long wait_limit_ns,
-                         int stall_after, bool after_kernel, cudaStream_t s) {
+                         int stall_after, bool after_kernel, cudaStream_t s, bool low = false) {
     constexpr auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap mw, mx;
     flp_status st = w_mn ? tmap_2d(&mw, BF, w, N, depth, ldw * 2, 64, 64) : tmap_2d(&mw, BF, w, depth, N, ldw * 2, BK, 128);
-    if (st == FLP_OK) st = tmap_2d(&mx, BF, x, depth, M, ldx * 2, BK, static_cast<uint32_t>(t.nt));
+    if (st == FLP_OK) st = tmap_2d(&mx, BF, x, depth, low ? 2 * M : M, ldx * 2, BK, static_cast<uint32_t>(t.nt));
     if (st != FLP_OK) return st;
     LinTurnParams p{};
     p.M = static_cast<int>(M);
@@ -166,6 +166,7 @@ flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const
     p.split = t.split;
     p.stages = t.stages;
     p.cols = t.cols;
+    p.low = low ? static_cast<int>(M) : 0;
     p.e = e;
     p.err = err;
     p.wait_limit_ns = wait_limit_ns;
@@ -193,6 +194,10 @@ flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const
                                : cudaLaunchKernelEx(&cfg, flp_linear_turned_kernel<0>, mw, mx, p);
     return r == cudaSuccess ? FLP_OK : cuda_fail(r, "flp_linear_turned_kernel launch");
 }
+
+// Rows of d that stay the sum of two bf16 numbers in every product: one 64-deep block of dW's,
+// and turned tiles.
+constexpr int64_t LIN_FEW = 64;
 
 // Turned tiles where they keep up: while memory sets the pace, or they do not need more
 // than one an SM (4096 x 4096: 512 rows 35 us, 39 in pairs' tiles, 1024 rows 48 and 39; 16384
@@ -267,8 +272,9 @@ struct LinearGradLayout {
     LinTurnPlan t;
     bool turned;
     size_t off_dw, off_x, off_w, off_d, off_lo, off_part, off_sums, bytes;
-    bool copy_x, copy_w, make_d, two, sums;  // two: d as the sum of two bf16 numbers, for dW,
-    bool stack;                              // one below the other with x twice: one product
+    bool copy_x, copy_w, make_d, sums;
+    bool two_x, two;  // d as the sum of two bf16 numbers, for dX, and for dW,
+    bool stack;       // one below the other with x twice: one product
     int blocks, rows;  // of the column sums
 };
 
@@ -279,19 +285,22 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
                                     int dw_dtype, int sm_count, int pairs) {
     LinearGradLayout g{};
     g.turned = linear_turns(M, K, sm_count);
+    const bool rounds = activation != FLP_ACT_NONE && activation != FLP_ACT_RELU;  // whose slopes are 0 and 1
+    const bool few = rounds && M <= LIN_FEW;
+    g.two_x = want_dx && few;
     if (g.turned)
-        g.t = plan_turned(M, K, N, sm_count);
+        g.t = plan_turned(M, K, N, sm_count, g.two_x);
     else
         g.l = plan_linear(M, K, N, pairs);
     g.copy_x = want_dw && !rows_bf16(X, ldx);
     g.copy_w = want_dx && !rows_bf16(W, ldw);
     g.make_d = (want_dx || want_dw) && (activation != FLP_ACT_NONE || !rows_bf16(dY, lddy));
-    g.two = want_dw && activation != FLP_ACT_NONE && dw_dtype == FLP_F32;
+    g.two = want_dw && (few || (rounds && dw_dtype == FLP_F32));
     // x twice costs its copies, 6 M K bytes; a second product a launch and reading and writing dW,
     // 8 N K (two products and one, backward through gelu_tanh: 1 row 4096 -> 16384 213 us and 103,
     // 1024 rows 396 and 314, 2048 rows 2048 -> 2048 91 and 80; 4096 rows 4096 -> 4096 314 and 328,
     // 8192 rows 4096 -> 16384 2060 and 2065)
-    g.stack = g.two && M <= N && (M <= 2048 || 4 * M <= N);
+    g.stack = g.two && (few || (M <= N && (M <= 2048 || 4 * M <= N)));
     g.sums = want_db;
     const int64_t strips = cdiv(N, 256);
     g.rows = static_cast<int>(std::max<int64_t>(32, cdiv(cdiv(M, std::max<int64_t>(1, cdiv(8 * sm_count, strips))), 32) * 32));
@@ -303,7 +312,7 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
     if (want_dw) r.bytes = align_up(std::max(r.bytes, weight_grad_bytes(g.stack ? 2 * M : M, N, K, dw_dtype, pairs)), 1024);
     g.off_x = r.take(g.stack ? 2 * M * pad8(K) * 2 : g.copy_x ? M * pad8(K) * 2 : 0);
     g.off_w = r.take(g.copy_w ? N * pad8(K) * 2 : 0);
-    g.off_d = r.take(g.make_d ? (g.two ? 2 : 1) * M * pad8(N) * 2 : 0);
+    g.off_d = r.take(g.make_d ? (g.two || g.two_x ? 2 : 1) * M * pad8(N) * 2 : 0);
     g.off_lo = g.off_d + M * pad8(N) * 2;
     g.off_part = r.take(want_dx ? g.l.part_bytes : 0);
     g.off_sums = r.take(g.sums ? static_cast<size_t>(g.blocks) * N * 4 : 0);
@@ -456,7 +465,7 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         p.M = static_cast<int>(M);
         p.N = static_cast<int>(N);
         p.d = g.make_d ? reinterpret_cast<bf16*>(ws + g.off_d) : nullptr;
-        p.lo = g.two ? reinterpret_cast<bf16*>(ws + g.off_lo) : nullptr;
+        p.lo = g.two || g.two_x ? reinterpret_cast<bf16*>(ws + g.off_lo) : nullptr;
         p.Np = static_cast<int>(pad8(N));
         p.part = g.sums ? g.blocks == 1 ? dbias : reinterpret_cast<float*>(ws + g.off_sums) : nullptr;
         p.rows = g.rows;
@@ -482,7 +491,7 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         e.y = static_cast<bf16*>(dX);
         e.ldy = lddx;
         e.vec = rows_bf16(dX, lddx) && K % 8 == 0;
-        st = g.turned ? linear_turned(g.t, dY, lddy, W, ldw, true, M, K, N, e, err, kWaitLimitNs, -1, after, s)
+        st = g.turned ? linear_turned(g.t, dY, lddy, W, ldw, true, M, K, N, e, err, kWaitLimitNs, -1, after, s, g.two_x)
                       : linear_product(g.l, dY, lddy, W, ldw, true, M, K, N, e, ws + g.off_part, err, d->pairs, kWaitLimitNs, -1, after, s);
         if (st != FLP_OK) return st;
         after = true;

@@ -13,9 +13,10 @@
 // are split along the contraction into fp32 partial tiles, which a small kernel joins in
 // a fixed order and takes through the same epilogue.  d is rounded to bf16 by a pass over
 // dy and v that also sums db from the unrounded values; dW is the contraction of
-// wgrad.cuh.  The rounding (2^-8 of each value) leaves bf16 results their own, but not an
-// fp32 dW: for that one d is written as the sum of two bf16 numbers (2^-16 of it), and
-// both are contracted with x, below one another in one product or in two.
+// wgrad.cuh.  The rounding (2^-8 of each value) is no more than a bf16 result's own, but an
+// fp32 dW would show it: for that one d is written as the sum of two bf16 numbers (2^-16 of
+// it), and both are contracted with x, below one another in one product or in two.  Of few
+// rows, where W and dW are what takes time, every result is made so.
 //
 // Bound by the tensor cores at many rows: 8192 x 4096 -> 16384 (582 us at the measured
 // matrix rate) takes 568 us plain, 611 with a bias and gelu_tanh, 724 with v kept as well
@@ -685,8 +686,9 @@ __global__ void __launch_bounds__(LJ_THREADS) flp_linear_join_kernel(const __gri
 // 16) its columns, so that a tile moves next to nothing but W, and a CTA by itself holds
 // 128 columns of y, one a thread.  The `split` CTAs of a cluster share a tile, each with a
 // part of the contraction; their fp32 sums are joined through distributed shared memory,
-// each CTA taking a part of the rows of x through the epilogue.  A bounded wait that runs
-// out makes the tile NaN.
+// each CTA taking a part of the rows of x through the epilogue.  Rows that are the sum of
+// two bf16 numbers meet each block of W twice.  A bounded wait that runs out makes the tile
+// NaN.
 
 constexpr int LT_THREADS = 256;
 constexpr int LT_WAYS = LT_THREADS / 128;  // threads that share a column's rows of x
@@ -702,6 +704,7 @@ struct LinTurnParams {
     int split;   // CTAs of a tile
     int stages;
     uint32_t cols;  // of TMEM
+    int low;        // rows from a row of x to its low part, a second number to be added, or 0
     LinEpilogue e;
     int* err;
     unsigned long long wait_limit_ns;
@@ -715,7 +718,9 @@ struct LinTurnShared {
 };
 
 // Bytes of a stage, and of the shared memory of a launch.
-__host__ __device__ inline uint32_t lin_turn_stage(int nt) { return LT_A_BYTES + static_cast<uint32_t>(nt) * (BK * 2); }
+__host__ __device__ inline uint32_t lin_turn_stage(int nt, bool low) {
+    return LT_A_BYTES + static_cast<uint32_t>(nt) * (BK * 2) * (low ? 2 : 1);
+}
 
 // Column n through the epilogue, for every LT_WAYS * split-th row of x of the tile from
 // `first` on: the CTAs' sums [nt][128] added in order.
@@ -776,7 +781,7 @@ __global__ void __launch_bounds__(LT_THREADS)
     const int n0 = tile / p.tiles_t * 128, t0 = tile % p.tiles_t * p.nt;
     const int kb0 = static_cast<int>(static_cast<long long>(p.KB) * rank / p.split);
     const int kb1 = static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / p.split);
-    const uint32_t stage_bytes = lin_turn_stage(p.nt);
+    const uint32_t stage_bytes = lin_turn_stage(p.nt, p.low != 0), x_bytes = static_cast<uint32_t>(p.nt) * (BK * 2);
     volatile int* abort_flag = &sh.abort;
     const uint64_t limit = p.wait_limit_ns;
     if (warp == 0 && lane == 0) {
@@ -824,6 +829,7 @@ __global__ void __launch_bounds__(LT_THREADS)
                     tma_load_2d(a + 8192, &tmW, n0 + 64, kb * BK, &sh.full[stage]);
                 }
                 tma_load_2d(a + LT_A_BYTES, &tmX, kb * BK, t0, &sh.full[stage]);
+                if (p.low) tma_load_2d(a + LT_A_BYTES + x_bytes, &tmX, kb * BK, t0 + p.low, &sh.full[stage]);
                 if (++stage == p.stages) stage = 0, phase ^= 1u;
             }
         }
@@ -841,6 +847,11 @@ __global__ void __launch_bounds__(LT_THREADS)
 #pragma unroll
                 for (int k = 0; k < BK / UMMA_K; ++k)
                     umma_bf16(tmem, operand_desc<A_MN>(a, k), operand_desc<0>(b, k), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+                if (p.low) {
+#pragma unroll
+                    for (int k = 0; k < BK / UMMA_K; ++k)
+                        umma_bf16(tmem, operand_desc<A_MN>(a, k), operand_desc<0>(b + x_bytes, k), idesc, 1u);
+                }
                 umma_commit(&sh.empty[stage]);
                 if (++stage == p.stages) stage = 0, phase ^= 1u;
             }

@@ -632,10 +632,10 @@ flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, co
  * without an activation; relu' is 1 for v > 0 and else 0):
  *   dX = d W (bf16),   dW [N, K] = d^T X (fp32 or bf16, contiguous, 16-byte
  *   aligned),   dbias [N] = column sums of d (fp32)
- * d enters the two products rounded to bf16 (for an fp32 dW with an activation as
- * the sum of two bf16 numbers) and dbias unrounded.  Each output may be NULL: it is
- * not computed, and X (for dW) or W (for dX) is not read.  The
- * residual's gradient is dY.  M == 0 writes zeros to dW and dbias.  The
+ * d enters the two products rounded to bf16 (where that changes it, as the sum of
+ * two bf16 numbers for an fp32 dW, and for both where M <= 64) and dbias unrounded.
+ * Each output may be NULL: it is not computed, and X (for dW) or W (for dX) is not
+ * read.  The residual's gradient is dY.  M == 0 writes zeros to dW and dbias.  The
  * workspace's first word is the error word of flp_get_error (FLP_ERR_TIMEOUT);
  * after a timeout what was not finished is NaN.
  */

@@ -226,6 +226,25 @@ def run_backward(flp, M, N, K, act, dw_dtype=torch.float32, pads=(0, 0, 0, 0, 0)
             assert torch.equal(a, b) if want else a is None
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,N,K", [(1, 72, 64), (1, 1000, 2047), (5, 4096, 1000), (16, 33, 520), (33, 2048, 4096), (64, 264, 136),
+                                   (64, 1, 8)])
+def test_backward_of_few_rows_rounds_once(flp, M, N, K, act):
+    # d is exact to 2^-8 of 2^-8 of it, so that dx and dW in bf16 are the 64-bit ones to
+    # half a step, on top of 2^-23 of the magnitudes a step of the accumulator
+    g = torch.Generator().manual_seed(M + N + K)
+    x, W, dy, pre = (matrix(*shape, 0, 0, g, scale)[1] for shape, scale in (((M, K), 1.0), ((N, K), K ** -0.5), ((M, N), 1.0),
+                                                                            ((M, N), 1.5)))
+    dx, dW, _ = flp.linear_backward(dy, x, W, pre, activation=act, dw_dtype=torch.bfloat16)
+    d = dy.double() * act64(pre.double(), act)[1]
+    e = 2.0 ** -17 * dy.double().abs()
+    each = e + 2.0 ** -16 * (d.abs() + e)
+    for got, a, b, off, terms in ((dx, d, W.double(), each, 2 * N), (dW, d.t(), x.double(), each.t(), 2 * M)):
+        want = a @ b
+        slack = off @ b.abs() + (terms / 16 + 2) * 2.0 ** -23 * (a.abs() @ b.abs()) * 1.01
+        assert bool(((got.double() - want).abs() <= slack + 2.0 ** -8 * (want.abs() + slack)).all())
+
+
 @pytest.mark.parametrize("M,N,K", SHAPES)
 @pytest.mark.parametrize("act", ACTS)
 def test_backward(flp, M, N, K, act):
