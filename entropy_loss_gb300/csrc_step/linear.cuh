@@ -1027,6 +1027,15 @@ constexpr int LG_THREADS = 256;
 constexpr int LG_WARPS = LG_THREADS / 32;
 constexpr int LG_ROWS = 4;  // rows a warp has under way
 
+// What the high numbers leave of d; nothing where one is infinite (inf - inf would be NaN,
+// and the products infinite by it alone).
+__device__ __forceinline__ uint64_t lin_rest(uint64_t hi, uint64_t d) {
+    float h0, h1, r0, r1;
+    f2_unpack(hi, h0, h1);
+    f2_unpack(f2_fma(hi, f2_splat(-1.f), d), r0, r1);
+    return f2_pack(fabsf(h0) == INFINITY ? 0.f : r0, fabsf(h1) == INFINITY ? 0.f : r1);
+}
+
 // 256 columns x `rows` rows a block, a row at a time a warp.
 template <bool LOOSE, int ACT>
 __global__ void __launch_bounds__(LG_THREADS, LOOSE ? 2 : 4) flp_linear_grad_kernel(const __grid_constant__ LinGradParams p) {
@@ -1084,7 +1093,7 @@ __global__ void __launch_bounds__(LG_THREADS, LOOSE ? 2 : 4) flp_linear_grad_ker
                 if (p.lo) {
                     uint64_t rest[P];
 #pragma unroll
-                    for (int j = 0; j < P; ++j) rest[j] = f2_fma(Pairs<bf16>::get(hi, j), f2_splat(-1.f), d[j]);
+                    for (int j = 0; j < P; ++j) rest[j] = lin_rest(Pairs<bf16>::get(hi, j), d[j]);
                     st_global_16(p.lo + at, Pairs<bf16>::put(rest), left > 0);
                 }
             }

@@ -634,6 +634,8 @@ flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, co
  *   aligned),   dbias [N] = column sums of d (fp32)
  * d enters the two products rounded to bf16 (where that changes it, as the sum of
  * two bf16 numbers for an fp32 dW, and for both where M <= 64) and dbias unrounded.
+ * An infinite d makes its row of dX and of dW infinite as in the formulas; an infinite X
+ * or W meets both numbers, and may leave NaN where the formula has an infinity.
  * Each output may be NULL: it is not computed, and X (for dW) or W (for dX) is not
  * read.  The residual's gradient is dY.  M == 0 writes zeros to dW and dbias.  The
  * workspace's first word is the error word of flp_get_error (FLP_ERR_TIMEOUT);
