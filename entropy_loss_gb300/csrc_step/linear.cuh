@@ -81,13 +81,15 @@ __device__ __forceinline__ uint64_t lin_act2(uint64_t v) {
     return v;
 }
 
-// act'.  Where |v| is cut off it is 0 or 1 to the last bit, and e = exp(-u) still finite,
-// which gives 1 - p = e p without another exponential.
+// act'.  Where |v| is cut off it is 0 or 1 exactly: gelu's exponential has vanished (below
+// 2^-126 it is 0), and of the two others e = exp(-u) lies between 2^126, from where its
+// reciprocal is 0, and 2^128, so that e p, which gives 1 - p without another exponential,
+// is still no NaN.
 template <int ACT>
 __device__ __forceinline__ uint64_t lin_slope2(uint64_t v) {
     if constexpr (ACT == LIN_RELU) return f2_map(v, [](float x) { return x > 0.f ? 1.f : 0.f; });
     v = f2_map(v, [](float x) {
-        constexpr float END = ACT == LIN_GELU_TANH ? 9.f : ACT == LIN_GELU ? 13.f : 80.f;
+        constexpr float END = ACT == LIN_GELU_TANH ? 10.03f : ACT == LIN_GELU ? 14.f : 88.f;
         return max_nan(min_nan(x, END), -END);
     });
     if constexpr (ACT == LIN_GELU) {

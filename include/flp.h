@@ -616,9 +616,10 @@ flp_status flp_token_logprob_backward(const void* logits, int64_t ld, int dtype,
  * residual: [M, N] bf16, or NULL (Y may be the residual itself); pre: v rounded
  * to bf16, for the backward pass, or NULL.  Activations: relu, gelu (v Phi(v)),
  * gelu_tanh (v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))), silu
- * (v sigmoid(v)).  The workspace query takes X and W for their alignment only and
- * may say 0.  A kernel's bounded wait that runs out leaves NaN in every tile of
- * the outputs that was not finished.
+ * (v sigmoid(v)).  At v = -inf they are 0, 0 (the limit), NaN and NaN (the products).
+ * The workspace query takes X and W for their alignment only and may say 0.  A
+ * kernel's bounded wait that runs out leaves NaN in every tile of the outputs that
+ * was not finished.
  */
 typedef enum { FLP_ACT_NONE = 0, FLP_ACT_RELU = 1, FLP_ACT_GELU = 2, FLP_ACT_GELU_TANH = 3, FLP_ACT_SILU = 4 } flp_activation;
 flp_status flp_linear_workspace(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
@@ -629,7 +630,8 @@ flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, co
 
 /*
  * Its gradients, with d = dY act'(pre) (pre as the forward kept it; not read
- * without an activation; relu' is 1 for v > 0 and else 0):
+ * without an activation; relu' is 1 for v > 0 and else 0, the others' slopes are 0 at
+ * -inf and 1 at inf):
  *   dX = d W (bf16),   dW [N, K] = d^T X (fp32 or bf16, contiguous, 16-byte
  *   aligned),   dbias [N] = column sums of d (fp32)
  * d enters the two products rounded to bf16 (where that changes it, as the sum of

@@ -50,3 +50,28 @@ def test_infinite_upstream_gradient(flp, act, dw_dtype, M, N, K, value):  # noqa
         assert bool(((got.double()[keep] - want).abs() <= slack + last * (want.abs() + slack)).all())
     want = d.sum(0)
     assert bool(((db.double() - want).abs() <= e.sum(0) + 2.0 ** -24 * (M / 8 + 64) * d.abs().sum(0))[cols].all())
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [1, 3, 200])
+def test_infinite_arguments(flp, act, M):  # noqa: F811
+    v = torch.tensor([2.0, -2.0, 0.0, -0.0, 1e-30, -1e30, 0.5, -0.5])
+    x = torch.zeros(M, 8, dtype=torch.bfloat16, device="cuda")
+    x[0, 0] = INF
+    W = torch.zeros(8, 8, dtype=torch.bfloat16, device="cuda")
+    W[:, 0] = v.to(torch.bfloat16)
+    y, pre = flp.linear(x, W, activation=act, keep=True)
+    sign = torch.sign(W[:, 0].float())
+    kept = torch.where(sign == 0, math.nan, sign * INF)  # 0 inf
+    assert torch.equal(torch.nan_to_num(pre[0].float(), 7.0), torch.nan_to_num(kept, 7.0))
+    low = {None: -INF, "relu": 0.0, "gelu": 0.0, "gelu_tanh": math.nan, "silu": math.nan}[act]
+    want = torch.where(sign == 0, math.nan, torch.where(sign > 0, INF, low))
+    assert torch.equal(torch.nan_to_num(y[0].float(), 7.0), torch.nan_to_num(want, 7.0))
+    assert bool((y[1:] == 0).all()) and bool((pre[1:] == 0).all())
+    if act:
+        # slopes 0 and 1 at the ends
+        dy = torch.ones(M, 8, dtype=torch.bfloat16, device="cuda")
+        _, _, db = flp.linear_backward(dy[:1], x[:1], W, pre[:1], activation=act, want_dx=False, want_dW=False)
+        assert torch.equal(db[sign != 0], (sign[sign != 0] > 0).float())
+        for far in (11.0, 14.0, 100.0, 1e30) if act == "gelu_tanh" else (100.0, 1e30) if act == "silu" else (14.0, 100.0, 1e30):
+            pre[0] = far * sign
+            _, _, db = flp.linear_backward(dy[:1], x[:1], W, pre[:1], activation=act, want_dx=False, want_dW=False)
+            assert torch.equal(db[sign != 0], (sign[sign != 0] > 0).float()), far
