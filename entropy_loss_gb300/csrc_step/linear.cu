@@ -6,6 +6,14 @@ namespace {
 
 // ------------------------------------------------------------------ product
 
+// A step of a tensor core cuts each of its 16 products to a quarter of the last place of the
+// accumulator, and their sum to that place, toward zero: 2.4 of these places on average (one
+// product of 16 0.4), so a long sum comes out too small.  Of positive products 7e-4 over
+// 131072 and 2.8e-3 over 524288; of centred ones 1e-4 over 131072.  A bf16 result's own
+// rounding is 1.7e-3: longer contractions are joined from fp32 sums of runs of at most 2048
+// 64-deep blocks, as the weight gradient's are.
+constexpr int64_t LIN_RUN = 2048;
+
 struct LinPlan {
     int width, tm, tn, whole, rest, splits, units, KB, rows;
     size_t part_bytes;
@@ -18,6 +26,9 @@ struct LinPlan {
 // its operands arrive), 3 us for a run's start and end (5 for a half that one epilogue
 // group drains by itself), and for joining 4 us (a launch) and
 // the partial tiles' bytes, written and read back at 4 TB/s.
+// Longer contractions than LIN_RUN blocks are split everywhere, into runs of at most that and
+// at least a quarter of it (4096 x 151936 -> 4096 in one run 2607 us, in two 3179, in more
+// 2757).
 LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
     LinPlan best{};
     double least = 1e300;
@@ -30,10 +41,11 @@ LinPlan plan_linear(int64_t M, int64_t N, int64_t depth, int pairs) {
         l.KB = static_cast<int>(cdiv(depth, BK));
         l.rows = static_cast<int>(std::min<int64_t>(M, PM));
         const double block = width > BN ? 0.66 : 0.37;
-        const int64_t tiles = static_cast<int64_t>(l.tm) * l.tn, whole = tiles / pairs * pairs, rest = tiles - whole;
+        const int64_t runs = cdiv(l.KB, LIN_RUN), tiles = static_cast<int64_t>(l.tm) * l.tn;
+        const int64_t whole = runs > 1 ? 0 : tiles / pairs * pairs, rest = tiles - whole;
         const double tile_mb = static_cast<double>(l.rows) * width * 4 * 2 / 1e6;
-        const int64_t most = rest == 0 ? 1 : std::min<int64_t>(l.KB, std::max<int64_t>(1, 4 * pairs / rest));
-        for (int64_t s = width > BN && rest > 0 ? 0 : 1; s <= most; ++s) {
+        const int64_t most = rest == 0 ? 1 : std::min<int64_t>(l.KB, std::max<int64_t>(runs > 1 ? 4 * runs : 1, 4 * pairs / rest));
+        for (int64_t s = width > BN && rest > 0 && runs == 1 ? 0 : runs; s <= most; ++s) {
             const double joined = s > 1 ? 4.0 + tile_mb / 4 * static_cast<double>(rest * s) : 0.0;
             const double last = s == 0 ? static_cast<double>(cdiv(2 * rest, pairs)) * (l.KB * 0.37 + 5.0)
                                        : static_cast<double>(cdiv(rest * s, pairs)) * (static_cast<double>(cdiv(l.KB, s)) * block + 3.0);
@@ -138,6 +150,7 @@ LinTurnPlan plan_turned(int64_t M, int64_t N, int64_t depth, int sm_count, bool 
     t.tiles_w = static_cast<int>(cdiv(N, 128));
     const int64_t KB = cdiv(depth, BK), tiles = static_cast<int64_t>(t.tiles_t) * t.tiles_w;
     t.split = 1;
+    while (t.split * LIN_RUN < (low ? 2 : 1) * KB) t.split *= 2;  // at most 8: linear_turns
     // up to four CTAs a tile, eight of few tiles (4096 x 4096, 16 rows: 19 us with four, 21 with
     // eight; 8192 -> 1024: 21 and 17)
     const int most = tiles * 8 <= sm_count ? 8 : 4;
@@ -202,7 +215,11 @@ constexpr int64_t LIN_FEW = 64;
 // Turned tiles where they keep up: while memory sets the pace, or they do not need more
 // than one an SM (4096 x 4096: 512 rows 35 us, 39 in pairs' tiles, 1024 rows 48 and 39; 16384
 // x 4096: 64 rows 42 and 50, 256 rows 58 and 50).
-bool linear_turns(int64_t M, int64_t N, int sm_count) { return M <= 64 || cdiv(M, LT_MAX_T) * cdiv(N, 128) <= sm_count; }
+// A cluster's eight CTAs hold eight runs.
+bool linear_turns(int64_t M, int64_t N, int64_t depth, int sm_count, bool low = false) {
+    if ((low ? 2 : 1) * cdiv(depth, BK) > 8 * LIN_RUN) return false;
+    return M <= 64 || cdiv(M, LT_MAX_T) * cdiv(N, 128) <= sm_count;
+}
 
 flp_status linear_row(LinRowParams& p, bool loose, int sm_count, bool after_kernel, cudaStream_t s) {
     // warps of the grid: eight an SM before a row's contraction is split
@@ -218,6 +235,13 @@ flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
     const int64_t most = kMaxRows - 4096;  // eight chunks of a contraction, each rounded up to 256, end within 32 bits
     if (M > most || N > most || K > most || cdiv(M, PM) * cdiv(N, BN) > (1 << 23) || cdiv(M, PM) * cdiv(K, BN) > (1 << 23))
         return fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling");
+    // partial tiles of a contraction that is split everywhere (512 KiB each)
+    auto partial = [](int64_t M, int64_t N, int64_t depth) {
+        const int64_t runs = cdiv(depth, BK * LIN_RUN);
+        return runs > 1 ? runs * cdiv(M, PM) * cdiv(N, BN) : 0;
+    };
+    if (partial(M, N, K) > 1 << 22 || partial(M, K, N) > 1 << 22)
+        return fail(FLP_ERR_UNSUPPORTED, "contraction too deep for so many outputs");
     return FLP_OK;
 }
 
@@ -252,7 +276,7 @@ LinearLayout linear_layout(const void* X, int64_t ldx, const void* W, int64_t ld
                            int pairs) {
     LinearLayout f{};
     f.one = M == 1;
-    f.turned = !f.one && linear_turns(M, N, sm_count);
+    f.turned = !f.one && linear_turns(M, N, K, sm_count);
     if (f.turned)
         f.t = plan_turned(M, N, K, sm_count);
     else if (!f.one)
@@ -284,10 +308,10 @@ LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X,
                                     int activation, bool want_dx, bool want_dw, bool want_db, int64_t M, int64_t N, int64_t K,
                                     int dw_dtype, int sm_count, int pairs) {
     LinearGradLayout g{};
-    g.turned = linear_turns(M, K, sm_count);
     const bool rounds = activation != FLP_ACT_NONE && activation != FLP_ACT_RELU;  // whose slopes are 0 and 1
     const bool few = rounds && M <= LIN_FEW;
-    g.two_x = want_dx && few;
+    g.two_x = want_dx && few && linear_turns(M, K, N, sm_count, true);
+    g.turned = linear_turns(M, K, N, sm_count, g.two_x);
     if (g.turned)
         g.t = plan_turned(M, K, N, sm_count, g.two_x);
     else

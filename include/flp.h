@@ -612,10 +612,11 @@ flp_status flp_token_logprob_backward(const void* logits, int64_t ld, int dtype,
  * any pitch and alignment; rows of X or W that are not aligned to 16 bytes are
  * copied to the workspace first):
  *   v = x W^T + bias,   y = act(v) + residual
- * in fp32 up to one rounding.  bias: [N], bf16 or fp32 (bias_dtype), or NULL;
- * residual: [M, N] bf16, or NULL (Y may be the residual itself); pre: v rounded
- * to bf16, for the backward pass, or NULL.  Activations: relu, gelu (v Phi(v)),
- * gelu_tanh (v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))), silu
+ * in fp32 up to one rounding (contractions above 131072 as fp32 sums of shorter runs;
+ * those of more than 2^22 runs of 256 x 256 outputs are refused).  bias: [N], bf16 or
+ * fp32 (bias_dtype), or NULL; residual: [M, N] bf16, or NULL (Y may be the residual
+ * itself); pre: v rounded to bf16, for the backward pass, or NULL.  Activations: relu,
+ * gelu (v Phi(v)), gelu_tanh (v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))), silu
  * (v sigmoid(v)).  At v = -inf they are 0, 0 (the limit), NaN and NaN (the products).
  * The workspace query takes X and W for their alignment only and may say 0.  A
  * kernel's bounded wait that runs out leaves NaN in every tile of the outputs that
