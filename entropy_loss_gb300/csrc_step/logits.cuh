@@ -17,8 +17,10 @@
 // still an element: no barrier).  A vector whose largest element passes goes to a list in
 // shared memory; at the end the listed vectors are read again (from the L2), and what of them
 // passes the last bound is ranked by value and column, so that equal logits come out
-// in the order of their columns.  When a list overflows (many equal logits), the block
-// reads its part again, taking the largest left of each chunk in turn.
+// in the order of their columns.  When a list overflows under bounds that came too late
+// (rising logits), the block reads its part again and lists it by the last one.  When more
+// pass that than the list holds (many equal logits), it reads its part once more, taking
+// the largest left of each chunk in turn.
 //
 // Bound by memory and, close behind it, by instructions: 8192 rows of 131072 bf16 logits
 // (317 us at the measured copy rate) take 328 us without alternatives, 388 with 8, 416 with
@@ -168,19 +170,16 @@ struct TlpShared {
     TlpStats stats;                        // this block's
     int vecs[TLP_LIST<THREADS>];
     int n_vecs, n;                         // vectors and elements listed
-    float bound;                           // the latest
+    float bound, first;                    // the latest, and the first that meant something
 };
 
-// Leaves the largest that each group of `lanes` threads has read.
+// Leaves the largest that each group of `lanes` threads has read, and returns it.
 template <int THREADS>
-__device__ __forceinline__ void tlp_put_maxima(TlpShared<THREADS>& sh, float m, int lanes) {
+__device__ __forceinline__ float tlp_put_maxima(TlpShared<THREADS>& sh, float m, int lanes) {
     volatile float* group = sh.group;
-    if (lanes == 32) {
-        m = redux_max(m);
-    } else {
-        for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
+    for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (threadIdx.x % lanes == 0) group[threadIdx.x / lanes] = m;
+    return m;
 }
 
 // The k-th largest of the groups' maxima: the largest that k of them reach; above -inf.
@@ -269,6 +268,29 @@ __device__ __noinline__ void tlp_again(TlpShared<THREADS>& sh, const TlpRow<T> r
     }
 }
 
+// Lists the block's vectors that reach `bound` (its last), when the list that was built under
+// the bounds of the way has overflowed.  Returns how many there are.
+template <typename T, int THREADS>
+__device__ __noinline__ int tlp_relist(TlpShared<THREADS>& sh, const TlpRow<T> row, int v0, int v1, float bound) {
+    constexpr int NV = 2;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n_vecs = 0;
+    __syncthreads();
+    for (int v = v0 + threadIdx.x; v < v1; v += THREADS * NV) {
+        uint32_t w[4 * NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) row.load(w + 4 * i, v + i * THREADS, v + i * THREADS < v1);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!(tlp_max<T>(w + 4 * i) >= bound)) continue;
+            const int n = atomicAdd(&sh.n_vecs, 1);
+            if (n < TLP_LIST<THREADS>) sh.vecs[n] = v + i * THREADS;
+        }
+    }
+    __syncthreads();
+    return sh.n_vecs;
+}
+
 __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
     unsigned long long v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
@@ -296,6 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
 
     TlpStats st{-INFINITY, 0.f, 0.f};
     float bound = -INFINITY;
+    bool late = true;  // the whole block's: fewer groups than alternatives have read anything
     uint32_t next[4 * NV];
     auto load = [&](int v) {
 #pragma unroll
@@ -339,14 +362,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
             st.s += now.s, st.a += now.a;
         }
         if (p.top > 0) {
-            if ((chunk & (chunk + 1)) == 0) {  // 1, 2, 4, ... chunks read
-                tlp_put_maxima(sh, st.m, lanes);
-                if (chunk == 0) __syncthreads();
-                // one warp takes the new bound, the others when they come by; the first is everybody's
-                if (chunk == 0 || chunk % WARPS == warp) {
+            if (late || (chunk & (chunk + 1)) == 0) {  // 1, 2, 4, ... chunks read
+                const float m = tlp_put_maxima(sh, st.m, lanes);
+                // the first bound is everybody's, and so is every one until it means something (a
+                // masked beginning); then one warp takes the new one, the others when they come by
+                const bool all = late;
+                if (late) late = __syncthreads_count(threadIdx.x % lanes == 0 && m > -FLT_MAX) < p.top;
+                if (all || chunk % WARPS == warp) {
                     __syncwarp();
                     bound = tlp_bound(sh, p.top, lanes);
                     if (lane == 0) *static_cast<volatile float*>(&sh.bound) = bound;
+                    if (all && threadIdx.x == 0) sh.first = bound;
                 }
             }
             bound = fmaxf(bound, *static_cast<volatile float*>(&sh.bound));
@@ -375,7 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flp_token_logprob_ker
     }
     if (p.top > 0) {
         bound = tlp_bound(sh, p.top, lanes);
-        const int listed = sh.n_vecs;
+        int listed = sh.n_vecs;
+        if (listed > TLP_LIST<THREADS> && bound > sh.first) listed = tlp_relist(sh, row, v0, v1, bound);
         for (int i = threadIdx.x; i < min(listed, TLP_LIST<THREADS>); i += THREADS) {
             const int col = row.col(sh.vecs[i]);
             uint32_t w[4];
