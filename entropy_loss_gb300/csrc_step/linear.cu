@@ -86,13 +86,14 @@ flp_status linear_attrs() {
 }
 
 // One product and, for split tiles, its join: A [M, depth] and W (w_mn: [depth, N], else
-// [N, depth]), rows aligned to 16 bytes.
+// [N, depth]), rows aligned to 16 bytes; `low`: the M rows below A's are added to them.
 flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const void* w, int64_t ldw, bool w_mn, int64_t M,
                           int64_t N, int64_t depth, const LinEpilogue& e, void* part, int* err, int pairs,
-                          unsigned long long wait_limit_ns, int stall_after, bool after_kernel, cudaStream_t s) {
+                          unsigned long long wait_limit_ns, int stall_after, bool after_kernel, cudaStream_t s,
+                          bool low = false) {
     constexpr auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap ma, mb, my, mp;
-    flp_status st = tmap_2d(&ma, BF, a, depth, M, lda * 2, BK, BM);
+    flp_status st = tmap_2d(&ma, BF, a, depth, low ? 2 * M : M, lda * 2, BK, BM);
     if (st == FLP_OK) st = w_mn ? tmap_2d(&mb, BF, w, N, depth, ldw * 2, 64, 64) : tmap_2d(&mb, BF, w, depth, N, ldw * 2, BK, BNH);
     if (st != FLP_OK) return st;
     my = mp = ma;  // where no bulk store writes
@@ -108,6 +109,8 @@ flp_status linear_product(const LinPlan& l, const void* a, int64_t lda, const vo
     p.splits = l.splits;
     p.units = l.units;
     p.KB = l.KB;
+    p.fold = static_cast<int>(cdiv(depth, BK));
+    p.low = low ? static_cast<int>(M) : 0;
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(N);
     p.part = static_cast<float*>(part);
@@ -208,8 +211,8 @@ flp_status linear_turned(const LinTurnPlan& t, const void* x, int64_t ldx, const
     return r == cudaSuccess ? FLP_OK : cuda_fail(r, "flp_linear_turned_kernel launch");
 }
 
-// Rows of d that stay the sum of two bf16 numbers in every product: one 64-deep block of dW's,
-// and turned tiles.
+// Rows of d that stay the sum of two bf16 numbers in every product unless the caller says
+// otherwise: one 64-deep block of dW's, and turned tiles.
 constexpr int64_t LIN_FEW = 64;
 
 // Turned tiles where they keep up: while memory sets the pace, or they do not need more
@@ -240,9 +243,14 @@ flp_status linear_sizes(int64_t M, int64_t N, int64_t K) {
         const int64_t runs = cdiv(depth, BK * LIN_RUN);
         return runs > 1 ? runs * cdiv(M, PM) * cdiv(N, BN) : 0;
     };
-    if (partial(M, N, K) > 1 << 22 || partial(M, K, N) > 1 << 22)
+    if (partial(M, N, K) > 1 << 22 || partial(M, K, 2 * N) > 1 << 22)
         return fail(FLP_ERR_UNSUPPORTED, "contraction too deep for so many outputs");
     return FLP_OK;
+}
+
+flp_status linear_terms(int d_terms, int64_t M) {
+    if (d_terms < 0 || d_terms > 2) return fail(FLP_ERR_INVALID_ARG, "d_terms is 0, 1 or 2");
+    return d_terms == 2 && M > 1 << 29 ? fail(FLP_ERR_UNSUPPORTED, "sizes beyond the 32-bit tiling") : FLP_OK;
 }
 
 flp_status linear_act(int activation) {
@@ -305,26 +313,26 @@ struct LinearGradLayout {
 // Row blocks of the pass over dy: enough for every SM to hold two blocks of threads, of
 // at least 32 rows (the warps' and their loads').
 LinearGradLayout linear_grad_layout(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
-                                    int activation, bool want_dx, bool want_dw, bool want_db, int64_t M, int64_t N, int64_t K,
-                                    int dw_dtype, int sm_count, int pairs) {
+                                    int activation, int d_terms, bool want_dx, bool want_dw, bool want_db, int64_t M, int64_t N,
+                                    int64_t K, int dw_dtype, int sm_count, int pairs) {
     LinearGradLayout g{};
     const bool rounds = activation != FLP_ACT_NONE && activation != FLP_ACT_RELU;  // whose slopes are 0 and 1
-    const bool few = rounds && M <= LIN_FEW;
-    g.two_x = want_dx && few && linear_turns(M, K, N, sm_count, true);
+    const bool two = rounds && (d_terms == 2 || (d_terms == 0 && M <= LIN_FEW));
+    g.two_x = want_dx && two;
     g.turned = linear_turns(M, K, N, sm_count, g.two_x);
     if (g.turned)
         g.t = plan_turned(M, K, N, sm_count, g.two_x);
     else
-        g.l = plan_linear(M, K, N, pairs);
+        g.l = plan_linear(M, K, g.two_x ? 2 * BK * cdiv(N, BK) : N, pairs);
     g.copy_x = want_dw && !rows_bf16(X, ldx);
     g.copy_w = want_dx && !rows_bf16(W, ldw);
     g.make_d = (want_dx || want_dw) && (activation != FLP_ACT_NONE || !rows_bf16(dY, lddy));
-    g.two = want_dw && (few || (rounds && dw_dtype == FLP_F32));
+    g.two = want_dw && (two || (rounds && d_terms == 0 && dw_dtype == FLP_F32));
     // x twice costs its copies, 6 M K bytes; a second product a launch and reading and writing dW,
     // 8 N K (two products and one, backward through gelu_tanh: 1 row 4096 -> 16384 213 us and 103,
     // 1024 rows 396 and 314, 2048 rows 2048 -> 2048 91 and 80; 4096 rows 4096 -> 4096 314 and 328,
-    // 8192 rows 4096 -> 16384 2060 and 2065)
-    g.stack = g.two && (few || (M <= N && (M <= 2048 || 4 * M <= N)));
+    // 8192 rows 4096 -> 16384 2060 and 2065).  A second product would round a bf16 dW twice.
+    g.stack = g.two && (dw_dtype == FLP_BF16 || M <= LIN_FEW || (M <= N && (M <= 2048 || 4 * M <= N)));
     g.sums = want_db;
     const int64_t strips = cdiv(N, 256);
     g.rows = static_cast<int>(std::max<int64_t>(32, cdiv(cdiv(M, std::max<int64_t>(1, cdiv(8 * sm_count, strips))), 32) * 32));
@@ -416,27 +424,44 @@ extern "C" flp_status flp_linear(const void* X, int64_t ldx, const void* W, int6
     return linear_product(f.l, X, ldx, W, ldw, false, M, N, K, e, ws + f.off_part, nullptr, d->pairs, kWaitLimitNs, -1, after, s);
 }
 
-extern "C" flp_status flp_linear_backward_workspace(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W,
-                                                    int64_t ldw, int activation, int want_dX, int want_dW, int want_dbias,
-                                                    int64_t M, int64_t N, int64_t K, int dW_dtype, size_t* bytes) {
+extern "C" flp_status flp_linear_backward_workspace_ex(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W,
+                                                       int64_t ldw, int activation, int d_terms, int want_dX, int want_dW,
+                                                       int want_dbias, int64_t M, int64_t N, int64_t K, int dW_dtype, size_t* bytes) {
     if (!bytes) return fail(FLP_ERR_INVALID_ARG, "bytes must be non-null");
     flp_status st = linear_sizes(M, N, K);
     if (st == FLP_OK) st = linear_act(activation);
+    if (st == FLP_OK) st = linear_terms(d_terms, M);
     if (st == FLP_OK) st = weight_grad_checks(M, N, K, dW_dtype);
     if (st != FLP_OK) return st;
     DevInfo* d;
     if ((st = check_device(&d)) != FLP_OK) return st;
-    *bytes = M == 0 ? 0 : linear_grad_layout(dY, lddy, X, ldx, W, ldw, activation, want_dX, want_dW, want_dbias, M, N, K, dW_dtype,
-                                             d->sm_count, d->pairs).bytes;
+    *bytes = M == 0 ? 0 : linear_grad_layout(dY, lddy, X, ldx, W, ldw, activation, d_terms, want_dX, want_dW, want_dbias, M, N, K,
+                                             dW_dtype, d->sm_count, d->pairs).bytes;
     return FLP_OK;
+}
+
+extern "C" flp_status flp_linear_backward_workspace(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W,
+                                                    int64_t ldw, int activation, int want_dX, int want_dW, int want_dbias,
+                                                    int64_t M, int64_t N, int64_t K, int dW_dtype, size_t* bytes) {
+    return flp_linear_backward_workspace_ex(dY, lddy, X, ldx, W, ldw, activation, 0, want_dX, want_dW, want_dbias, M, N, K, dW_dtype,
+                                            bytes);
 }
 
 extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
                                           const void* pre, int64_t ldpre, int activation, int64_t M, int64_t N, int64_t K,
                                           void* dX, int64_t lddx, void* dW, int dW_dtype, float* dbias, void* workspace,
                                           size_t workspace_bytes, void* stream) {
+    return flp_linear_backward_ex(dY, lddy, X, ldx, W, ldw, pre, ldpre, activation, 0, M, N, K, dX, lddx, dW, dW_dtype, dbias,
+                                  workspace, workspace_bytes, stream);
+}
+
+extern "C" flp_status flp_linear_backward_ex(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                             const void* pre, int64_t ldpre, int activation, int d_terms, int64_t M, int64_t N,
+                                             int64_t K, void* dX, int64_t lddx, void* dW, int dW_dtype, float* dbias,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
     flp_status st = linear_sizes(M, N, K);
     if (st == FLP_OK) st = linear_act(activation);
+    if (st == FLP_OK) st = linear_terms(d_terms, M);
     if (st == FLP_OK) st = weight_grad_checks(M, N, K, dW_dtype);
     if (st != FLP_OK) return st;
     if (!aligned16(dW)) return fail(FLP_ERR_INVALID_ARG, "dW must be 16-byte aligned");
@@ -462,8 +487,8 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         if (dbias) FLP_CUDA(cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 4, s));
         return FLP_OK;
     }
-    const LinearGradLayout g = linear_grad_layout(dY, lddy, X, ldx, W, ldw, activation, dX, dW, dbias, M, N, K, dW_dtype, d->sm_count,
-                                                  d->pairs);
+    const LinearGradLayout g = linear_grad_layout(dY, lddy, X, ldx, W, ldw, activation, d_terms, dX, dW, dbias, M, N, K, dW_dtype,
+                                                  d->sm_count, d->pairs);
     if (!workspace || workspace_bytes < g.bytes || !aligned16(workspace))
         return fail(FLP_ERR_WORKSPACE, "linear backward workspace null, misaligned or too small");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -516,7 +541,8 @@ extern "C" flp_status flp_linear_backward(const void* dY, int64_t lddy, const vo
         e.ldy = lddx;
         e.vec = rows_bf16(dX, lddx) && K % 8 == 0;
         st = g.turned ? linear_turned(g.t, dY, lddy, W, ldw, true, M, K, N, e, err, kWaitLimitNs, -1, after, s, g.two_x)
-                      : linear_product(g.l, dY, lddy, W, ldw, true, M, K, N, e, ws + g.off_part, err, d->pairs, kWaitLimitNs, -1, after, s);
+                      : linear_product(g.l, dY, lddy, W, ldw, true, M, K, N, e, ws + g.off_part, err, d->pairs, kWaitLimitNs, -1, after, s,
+                                       g.two_x);
         if (st != FLP_OK) return st;
         after = true;
     }

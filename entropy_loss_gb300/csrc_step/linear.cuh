@@ -16,7 +16,8 @@
 // wgrad.cuh.  The rounding (2^-8 of each value) is no more than a bf16 result's own, but an
 // fp32 dW would show it: for that one d is written as the sum of two bf16 numbers (2^-16 of
 // it), and both are contracted with x, below one another in one product or in two.  Of few
-// rows, where W and dW are what takes time, every result is made so.
+// rows, where W and dW are what takes time, every result is made so; the caller may ask for
+// one number or two in all.
 //
 // Bound by the tensor cores at many rows: 8192 x 4096 -> 16384 (582 us at the measured
 // matrix rate) takes 568 us plain, 611 with a bias and gelu_tanh, 724 with v kept as well
@@ -157,7 +158,9 @@ struct LinParams {
     int whole;    // tiles that are written directly (units 0 .. whole - 1)
     int splits;   // runs of each other tile; 0: its two halves, written directly
     int units;
-    int KB;       // 64-deep blocks of the contraction
+    int KB;       // 64-deep blocks of the contraction, over both numbers of d where there are two
+    int fold;     // and over one: from here on the blocks of d's low numbers meet those of W again
+    int low;      // rows from a row of d to its low numbers (dx alone)
     int M, N;
     float* part;  // partial tiles [tile][split][rows][512]
     int rows;     // of a partial tile: min(M, 256)
@@ -393,15 +396,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         mbar_arrive_expect_tx(&sm.full[stage], 2 * (A_STAGE_BYTES + t.halves * B_STAGE_BYTES));
                     const uint32_t bar = mapa_shared(smem_addr(&sm.full[stage]), 0);
                     uint8_t* b = sm.base + slot_b(true, stage);
-                    tma_load_2d_pair(sm.base + slot_a(true, stage), &tmA, kb * BK, t.m0 + rofs, bar);
+                    const bool again = B_MN == 1 && kb >= p.fold;
+                    const int at = (again ? kb - p.fold : kb) * BK;
+                    tma_load_2d_pair(sm.base + slot_a(true, stage), &tmA, at, t.m0 + rofs + (again ? p.low : 0), bar);
                     for (int h = 0; h < t.halves; ++h) {
                         const int col = t.n0 + h * BN + rofs;
                         if (B_MN == 0) {
-                            tma_load_2d_pair(b + h * B_STAGE_BYTES, &tmB, kb * BK, col, bar);
+                            tma_load_2d_pair(b + h * B_STAGE_BYTES, &tmB, at, col, bar);
                         } else {
 #pragma unroll
                             for (int j = 0; j < BNH / 64; ++j)
-                                tma_load_2d_pair(b + h * B_STAGE_BYTES + j * 8192, &tmB, col + j * 64, kb * BK, bar);
+                                tma_load_2d_pair(b + h * B_STAGE_BYTES + j * 8192, &tmB, col + j * 64, at, bar);
                         }
                     }
                     if (++stage == STAGES_W) {

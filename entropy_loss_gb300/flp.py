@@ -37,7 +37,8 @@ EXPORTS = ("flp_workspace_query", "flp_workspace_query_ex", "flp_forward", "flp_
            "flp_balance_loss_workspace", "flp_balance_loss", "flp_balance_loss_ex", "flp_expert_sort_workspace",
            "flp_expert_sort", "flp_expert_gather", "flp_expert_combine", "flp_expert_combine_backward",
            "flp_token_logprob", "flp_token_logprob_backward", "flp_linear_workspace", "flp_linear",
-           "flp_linear_backward_workspace", "flp_linear_backward", "flp_selftest_linear_timeout")
+           "flp_linear_backward_workspace", "flp_linear_backward", "flp_linear_backward_workspace_ex",
+           "flp_linear_backward_ex", "flp_selftest_linear_timeout")
 FLP_LOSS_NLL_MEAN = 1
 FLP_LOSS_CLIPPED_SURROGATE = 2
 FLP_LOSS_NLL_SUM = 3
@@ -144,6 +145,9 @@ def load(path: str = LIB_PATH):
             ("flp_linear_backward_workspace", [p, i64, p, i64, p, i64, i32, i32, i32, i32, i64, i64, i64, i32, size]),
             ("flp_linear_backward", [p, i64, p, i64, p, i64, p, i64, i32, i64, i64, i64, p, i64, p, i32, p, p, ctypes.c_size_t,
                                      p]),
+            ("flp_linear_backward_workspace_ex", [p, i64, p, i64, p, i64, i32, i32, i32, i32, i32, i64, i64, i64, i32, size]),
+            ("flp_linear_backward_ex", [p, i64, p, i64, p, i64, p, i64, i32, i32, i64, i64, i64, p, i64, p, i32, p, p,
+                                        ctypes.c_size_t, p]),
             ("flp_selftest_linear_timeout", [p, ctypes.c_size_t, i32, i32, i64, p])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32
@@ -964,13 +968,15 @@ def linear(x, W, bias=None, *, activation=None, residual=None, keep: bool = Fals
 
 
 def linear_backward(dy, x, W, pre=None, *, activation=None, dw_dtype=torch.float32, want_dx: bool = True, want_dW: bool = True,
-                    want_dbias: bool = True, dx=None, workspace=None, stream=None):
+                    want_dbias: bool = True, d_terms: int = 0, dx=None, workspace=None, stream=None):
     """(dx, dW, dbias) of linear, each None where it is not wanted: dx bf16 [M, K], dW
     [N, K] in dw_dtype, dbias fp32 [N].  pre is what linear kept (activation None:
-    not needed).  The residual's gradient is dy itself."""
+    not needed).  The residual's gradient is dy itself.  d = dy act'(pre) enters both
+    products as `d_terms` bf16 numbers: 1 (off by 2^-8 of it), 2 (2^-16, at twice the
+    operations), or 0: two for an fp32 dW and for up to 64 rows, else one."""
     if stream is not None:
         return _on_stream(stream, linear_backward, dy, x, W, pre, activation=activation, dw_dtype=dw_dtype, want_dx=want_dx,
-                          want_dW=want_dW, want_dbias=want_dbias, dx=dx, workspace=workspace)
+                          want_dW=want_dW, want_dbias=want_dbias, d_terms=d_terms, dx=dx, workspace=workspace)
     act = _activation(activation)
     xp, ldx, wp, ldw, M, N, K, dev = _linear_weight(x, W)
     dyp, lddy = _rows(dy, "dy", (M, N), torch.bfloat16)
@@ -997,13 +1003,13 @@ def linear_backward(dy, x, W, pre=None, *, activation=None, dw_dtype=torch.float
     dbias = torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None
     device, code = dev.index, _DTYPE[dw_dtype]
     ws, ws_bytes, _keep = _scratch(workspace, dev, 0 if workspace is not None else
-                                   _workspace_bytes("flp_linear_backward_workspace", device, dyp % 16, lddy, xp % 16, ldx, wp % 16,
-                                                    ldw, act, want_dx, want_dW, want_dbias, M, N, K, code))
-    status = load().flp_linear_backward(dyp, lddy, xp, ldx, wp, ldw, pp, ldp, act, M, N, K, dxp, lddx,
-                                        dW.data_ptr() if want_dW else None, code, dbias.data_ptr() if want_dbias else None,
-                                        ws, ws_bytes, _raw_stream(device))
+                                   _workspace_bytes("flp_linear_backward_workspace_ex", device, dyp % 16, lddy, xp % 16, ldx,
+                                                    wp % 16, ldw, act, d_terms, want_dx, want_dW, want_dbias, M, N, K, code))
+    status = load().flp_linear_backward_ex(dyp, lddy, xp, ldx, wp, ldw, pp, ldp, act, d_terms, M, N, K, dxp, lddx,
+                                           dW.data_ptr() if want_dW else None, code, dbias.data_ptr() if want_dbias else None,
+                                           ws, ws_bytes, _raw_stream(device))
     if status:
-        _check(status, "flp_linear_backward")
+        _check(status, "flp_linear_backward_ex")
     return dx, dW, dbias
 
 
@@ -1303,27 +1309,28 @@ class FusedLinear(torch.autograd.Function):
     """autograd wrapper of linear."""
 
     @staticmethod
-    def forward(ctx, x, W, bias, residual, activation, recorded):
-        want_x, want_W, want_b, _, _, _ = ctx.needs_input_grad
+    def forward(ctx, x, W, bias, residual, activation, recorded, d_terms):
+        want_x, want_W, want_b, _, _, _, _ = ctx.needs_input_grad
         keep = recorded and activation is not None and (want_x or want_W or want_b)
         y = linear(x, W, bias, activation=activation, residual=residual, keep=keep)
         y, pre = y if keep else (y, None)
         ctx.save_for_backward(x, W, bias, pre)
-        ctx.activation = activation
+        ctx.activation, ctx.d_terms = activation, d_terms
         return y
 
     @staticmethod
     def backward(ctx, dy):
         x, W, bias, pre = ctx.saved_tensors
-        want_x, want_W, want_b, want_r, _, _ = ctx.needs_input_grad
+        want_x, want_W, want_b, want_r, _, _, _ = ctx.needs_input_grad
         dx = dW = db = None
         if want_x or want_W or want_b:
             dx, dW, db = _once(lambda: linear_backward(dy.contiguous(), x, W, pre, activation=ctx.activation, dw_dtype=W.dtype,
-                                                       want_dx=want_x, want_dW=want_W, want_dbias=want_b),
+                                                       want_dx=want_x, want_dW=want_W, want_dbias=want_b, d_terms=ctx.d_terms),
                                dy, x, W, *(() if bias is None else (bias,)))
-        return dx, dW, db.to(bias.dtype) if want_b else None, dy if want_r else None, None, None
+        return dx, dW, db.to(bias.dtype) if want_b else None, dy if want_r else None, None, None, None
 
 
-def fused_linear(x, W, bias=None, activation=None, residual=None):
-    """Differentiable act(x W^T + bias) + residual for bf16 x [M, K], W [N, K]."""
-    return FusedLinear.apply(x, W, bias, residual, activation, torch.is_grad_enabled())
+def fused_linear(x, W, bias=None, activation=None, residual=None, d_terms: int = 0):
+    """Differentiable act(x W^T + bias) + residual for bf16 x [M, K], W [N, K]; d_terms as
+    in linear_backward."""
+    return FusedLinear.apply(x, W, bias, residual, activation, torch.is_grad_enabled(), d_terms)

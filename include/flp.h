@@ -635,8 +635,10 @@ flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, co
  * -inf and 1 at inf):
  *   dX = d W (bf16),   dW [N, K] = d^T X (fp32 or bf16, contiguous, 16-byte
  *   aligned),   dbias [N] = column sums of d (fp32)
- * d enters the two products rounded to bf16 (where that changes it, as the sum of
- * two bf16 numbers for an fp32 dW, and for both where M <= 64) and dbias unrounded.
+ * d enters the two products rounded to bf16 (2^-8 of it; where that changes it, as the
+ * sum of two bf16 numbers, 2^-16 of it, for an fp32 dW, and for both where M <= 64) and
+ * dbias unrounded.  The _ex forms take the choice: d_terms 0 is this rule, 1 one number
+ * in both products, 2 two numbers in both (twice the operations; M <= 2^29).
  * An infinite d makes its row of dX and of dW infinite as in the formulas; an infinite X
  * or W meets both numbers, and may leave NaN where the formula has an infinity.
  * Each output may be NULL: it is not computed, and X (for dW) or W (for dX) is not
@@ -651,6 +653,13 @@ flp_status flp_linear_backward(const void* dY, int64_t lddy, const void* X, int6
                                const void* pre, int64_t ldpre, int activation, int64_t M, int64_t N, int64_t K, void* dX,
                                int64_t lddx, void* dW, int dW_dtype, float* dbias, void* workspace, size_t workspace_bytes,
                                void* stream);
+flp_status flp_linear_backward_workspace_ex(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                            int activation, int d_terms, int want_dX, int want_dW, int want_dbias, int64_t M,
+                                            int64_t N, int64_t K, int dW_dtype, size_t* bytes);
+flp_status flp_linear_backward_ex(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                  const void* pre, int64_t ldpre, int activation, int d_terms, int64_t M, int64_t N, int64_t K,
+                                  void* dX, int64_t lddx, void* dW, int dW_dtype, float* dbias, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * Self-test of the product's bounded waits, like flp_selftest_wait_timeout (a
