@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int u = pair; u < p.total && ok; u += npairs) {
-                ok = wide_tile_mma(sm, tmem_base, gk, acc_phase, p.KB_h, limit, abort_flag);
+                ok = wide_tile_mma(sm, tmem_base, gk, acc_phase, acc_phase, p.KB_h, limit, abort_flag);
                 acc_phase ^= 1u;
             }
             if (!ok) raise_abort(sm, p.err);

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             for (int u = pair; u < p.units && ok; u += npairs) {
                 const Unit t = decode_unit(p, u);
                 for (int nt = t.n0; nt < t.n1 && ok; ++nt) {
-                    ok = wide_tile_mma(sm, tmem_base, gk, acc_phase, p.KB, limit, abort_flag);
+                    ok = wide_tile_mma(sm, tmem_base, gk, acc_phase, acc_phase, p.KB, limit, abort_flag);
                     acc_phase ^= 1u;
                 }
             }

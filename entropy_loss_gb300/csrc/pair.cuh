@@ -287,19 +287,20 @@ __device__ __forceinline__ void load_wide_kblock(const Smem& sm, int stage, bool
         tma_load_2d_pair(sm.base + slot_b(true, stage) + h * B_STAGE_BYTES, tmB, kb * BK, b_row + h * BN, bar);
 }
 
-// MMA issuer: every MMA of one wide tile with K-major operands (KB k-blocks),
-// half h into accumulator h, then tfull[h] per half.  `gk` counts the
-// k-blocks consumed so far (slot gk % STAGES_W, fill parity
-// (gk / STAGES_W) & 1) and advances by KB; acc_phase is this tile's use
-// parity of the accumulators.  The first and last WIDE_EDGE k-blocks are
+// MMA issuer: every MMA of one wide tile with K-major A and K-major or (B_MN)
+// MN-major B (KB k-blocks), half h into accumulator h, then tfull[h] per half.
+// `gk` counts the k-blocks consumed so far (slot gk % STAGES_W, fill parity
+// (gk / STAGES_W) & 1) and advances by KB; phase0 and phase1 are this tile's
+// use parities of the accumulators.  The first and last WIDE_EDGE k-blocks are
 // issued half by half: at the end of the tile half 0 completes (and its
 // epilogue starts) while the half-1 MMAs of those k-blocks still run, and at
 // the start half 0 fills while the previous tile's half 1 is still drained.
 // Returns false when a wait ran out.
+template <int B_MN = 0>
 __device__ __forceinline__ bool wide_tile_mma(const Smem& sm, uint32_t tmem_base, uint32_t& gk,
-                                              uint32_t acc_phase, int KB, uint64_t limit,
+                                              uint32_t phase0, uint32_t phase1, int KB, uint64_t limit,
                                               volatile int* abort_flag) {
-    constexpr uint32_t idesc = idesc_bf16_f32(PM, BN, 0, 0);
+    constexpr uint32_t idesc = idesc_bf16_f32(PM, BN, 0, B_MN);
     auto issue = [&](uint32_t g, int h, int kb) {
         const int s = static_cast<int>(g % STAGES_W);
         const uint32_t a_base = smem_addr(sm.base + slot_a(true, s));
@@ -307,7 +308,7 @@ __device__ __forceinline__ bool wide_tile_mma(const Smem& sm, uint32_t tmem_base
 #pragma unroll
         for (int k = 0; k < BK / UMMA_K; ++k)
             umma_bf16_pair(tmem_base + static_cast<uint32_t>(h * BN), operand_desc<0>(a_base, k),
-                           operand_desc<0>(b_base, k), idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                           operand_desc<B_MN>(b_base, k), idesc, (kb > 0 || k > 0) ? 1u : 0u);
     };
     auto wait_full = [&](uint32_t g) {
         if (!mbar_wait(&sm.full[g % STAGES_W], (g / STAGES_W) & 1u, limit, abort_flag)) return false;
@@ -319,14 +320,14 @@ __device__ __forceinline__ bool wide_tile_mma(const Smem& sm, uint32_t tmem_base
     };
     const int head = min(WIDE_EDGE, KB);
     const int tail0 = max(head, KB - WIDE_EDGE);
-    if (!mbar_wait(&sm.tempty[0], acc_phase ^ 1u, limit, abort_flag)) return false;
+    if (!mbar_wait(&sm.tempty[0], phase0 ^ 1u, limit, abort_flag)) return false;
     tc_fence_after();
     for (int kb = 0; kb < head; ++kb) {
         if (!wait_full(gk + kb)) return false;
         issue(gk + kb, 0, kb);
     }
     if (head == KB) umma_commit_pair_mc(&sm.tfull[0], PAIR_MASK);
-    if (!mbar_wait(&sm.tempty[1], acc_phase ^ 1u, limit, abort_flag)) return false;
+    if (!mbar_wait(&sm.tempty[1], phase1 ^ 1u, limit, abort_flag)) return false;
     tc_fence_after();
     for (int kb = 0; kb < head; ++kb) {
         issue(gk + kb, 1, kb);

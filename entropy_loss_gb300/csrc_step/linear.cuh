@@ -424,29 +424,24 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             uint32_t gk = 0;    // k-blocks consumed so far
             uint32_t uses = 0;  // bit h: parity of the uses of accumulator h so far
             bool ok = true;
-            auto issue = [&](uint32_t g, int acc, int half, bool first) {
-                const int s = static_cast<int>(g % STAGES_W);
-                const uint32_t a = smem_addr(sm.base + slot_a(true, s));
-                const uint32_t b = smem_addr(sm.base + slot_b(true, s)) + half * B_STAGE_BYTES;
+            // a tile of one half, into accumulator acc
+            auto single = [&](int acc, int KB) {
+                if (!mbar_wait(&sm.tempty[acc], (uses >> acc & 1u) ^ 1u, limit, abort_flag)) return false;
+                tc_fence_after();
+                for (int kb = 0; kb < KB; ++kb, ++gk) {
+                    const int s = static_cast<int>(gk % STAGES_W);
+                    if (!mbar_wait(&sm.full[s], (gk / STAGES_W) & 1u, limit, abort_flag)) return false;
+                    tc_fence_after();
+                    const uint32_t a = smem_addr(sm.base + slot_a(true, s)), b = smem_addr(sm.base + slot_b(true, s));
 #pragma unroll
-                for (int k = 0; k < BK / UMMA_K; ++k)
-                    umma_bf16_pair(tmem_base + static_cast<uint32_t>(acc * BN), operand_desc<0>(a, k),
-                                   operand_desc<B_MN>(b, k), idesc, (!first || k > 0) ? 1u : 0u);
-            };
-            auto wait_full = [&](uint32_t g) {
-                if (!mbar_wait(&sm.full[g % STAGES_W], (g / STAGES_W) & 1u, limit, abort_flag)) return false;
-                tc_fence_after();
+                    for (int k = 0; k < BK / UMMA_K; ++k)
+                        umma_bf16_pair(tmem_base + static_cast<uint32_t>(acc * BN), operand_desc<0>(a, k), operand_desc<B_MN>(b, k),
+                                       idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    umma_commit_pair_mc(&sm.empty[s], PAIR_MASK);
+                }
+                umma_commit_pair_mc(&sm.tfull[acc], PAIR_MASK);
+                uses ^= 1u << acc;
                 return true;
-            };
-            auto release = [&](uint32_t g) { umma_commit_pair_mc(&sm.empty[g % STAGES_W], PAIR_MASK); };
-            auto wait_tempty = [&](int h) {
-                if (!mbar_wait(&sm.tempty[h], ((uses >> h) & 1u) ^ 1u, limit, abort_flag)) return false;
-                tc_fence_after();
-                return true;
-            };
-            auto publish = [&](int h) {
-                umma_commit_pair_mc(&sm.tfull[h], PAIR_MASK);
-                uses ^= 1u << h;
             };
             int it = 0;
             for (int u = pair; u < p.units && ok; u += npairs, ++it) {
@@ -454,55 +449,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 const int KB = t.kb1 - t.kb0;
                 if (t.halves == 0) continue;
                 if (t.halves == 1) {
-                    const int acc = lin_single(it);
-                    ok = wait_tempty(acc);
-                    for (int kb = 0; kb < KB && ok; ++kb) {
-                        ok = wait_full(gk + kb);
-                        if (!ok) break;
-                        issue(gk + kb, acc, 0, kb == 0);
-                        release(gk + kb);
-                    }
-                    if (ok) publish(acc);
+                    ok = single(lin_single(it), KB);
                 } else {
-                    ok = wait_tempty(0);
-                    if (!ok) break;
-                    // halves staggered at both ends of the tile: half 0 completes (and is
-                    // drained) under the last half-1 MMAs, and fills while the previous
-                    // tile's half 1 is still drained
-                    const int head = min(WIDE_EDGE, KB);
-                    const int tail0 = max(head, KB - WIDE_EDGE);
-                    for (int kb = 0; kb < head && ok; ++kb) {
-                        ok = wait_full(gk + kb);
-                        if (ok) issue(gk + kb, 0, 0, kb == 0);
-                    }
-                    if (!ok) break;
-                    if (head == KB) publish(0);
-                    ok = wait_tempty(1);
-                    if (!ok) break;
-                    for (int kb = 0; kb < head; ++kb) {
-                        issue(gk + kb, 1, 1, kb == 0);
-                        release(gk + kb);
-                    }
-                    for (int kb = head; kb < tail0 && ok; ++kb) {
-                        ok = wait_full(gk + kb);
-                        if (!ok) break;
-                        issue(gk + kb, 0, 0, false);
-                        issue(gk + kb, 1, 1, false);
-                        release(gk + kb);
-                    }
-                    for (int kb = tail0; kb < KB && ok; ++kb) {
-                        ok = wait_full(gk + kb);
-                        if (ok) issue(gk + kb, 0, 0, false);
-                    }
-                    if (!ok) break;
-                    if (head < KB) publish(0);
-                    for (int kb = tail0; kb < KB; ++kb) {
-                        issue(gk + kb, 1, 1, false);
-                        release(gk + kb);
-                    }
-                    publish(1);
+                    ok = wide_tile_mma<B_MN>(sm, tmem_base, gk, uses & 1u, uses >> 1, KB, limit, abort_flag);
+                    uses ^= 3u;
                 }
-                gk += static_cast<uint32_t>(KB);
             }
             if (!ok) lin_raise(sm, p.err);
             umma_commit_pair_mc(sm.drain, 0x1);  // every MMA issued so far has completed
