@@ -1238,12 +1238,13 @@ class FusedExpertGather(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, order):
-        ctx.order = order
+        ctx.save_for_backward(*order)  # so that an order written over since is noticed
         return expert_gather(x, order)
 
     @staticmethod
     def backward(ctx, dxs):
-        return _once(lambda: expert_combine(dxs.contiguous(), ctx.order), dxs), None
+        order = ExpertOrder(*ctx.saved_tensors)
+        return _once(lambda: expert_combine(dxs.contiguous(), order), dxs), None
 
 
 def fused_expert_gather(x, order: ExpertOrder):
@@ -1256,15 +1257,14 @@ class FusedExpertCombine(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, ys, weights, order):
-        ctx.order = order
-        ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights)
+        ctx.save_for_backward(ys if ctx.needs_input_grad[1] else None, weights, *order)
         return expert_combine(ys, order, weights)
 
     @staticmethod
     def backward(ctx, dy):
-        ys, weights = ctx.saved_tensors
-        want = ctx.needs_input_grad[1]
-        dys, dw = _once(lambda: expert_combine_backward(dy.contiguous(), ys, ctx.order, weights, want_dweights=want),
+        ys, weights, *order = ctx.saved_tensors
+        order, want = ExpertOrder(*order), ctx.needs_input_grad[1]
+        dys, dw = _once(lambda: expert_combine_backward(dy.contiguous(), ys, order, weights, want_dweights=want),
                         dy, ys, weights)
         return dys, dw.to(weights.dtype) if want else None, None
 
