@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) flp_expert_gather_kernel(const M
 }
 
 // Vectors a lane, and rows under way at a time (loose bf16 rows, 20000 x 2 x 1001: four rows
-// 54 us, two 37; aligned ones, 65536 x 8 x 64: 56 and 64).
+// 54 us, two 38; aligned ones, 8192 x 8 x 2048: 58 and 63, 32768 x 4 x 5120: 251 and 263).
 constexpr int COMBINE_NV = 2;
 template <typename T, bool LOOSE>
 __global__ void __launch_bounds__(MOVE_THREADS) flp_expert_combine_kernel(const MoveParams p) {

@@ -20,11 +20,13 @@
 // one number or two in all.
 //
 // Bound by the tensor cores at many rows: 8192 x 4096 -> 16384 (582 us at the measured
-// matrix rate) takes 568 us plain, 611 with a bias and gelu_tanh, 724 with v kept as well
-// in a loop that meets the power cap (75 % of the tensor pipe busy; the rest is what the
-// epilogue, 65536 outputs a CTA and tile, does not hide: a tile's two accumulators are all
-// of TMEM).  Bound by reading W at few rows: 4096 -> 16384 (20 us) 29 us for one row,
-// 37 for 16; in between by latency (777 x 1000 -> 2047 with everything: 25 us).
+// matrix rate) takes 562 us plain, 606 with a bias and gelu_tanh, 720 to 740 with v kept as
+// well in a loop that meets the power cap (75 % of the tensor pipe busy; the rest is what
+// the epilogue, 65536 outputs a CTA and tile, does not hide: a tile's two accumulators are
+// all of TMEM).  Bound by reading W at few rows: 4096 -> 16384 (20 us) 26 us for one row,
+// 34 for 16.  In between, up to some 2048 rows, by operands through the L2 and by the joins:
+// 512 x 4096 -> 4096 (9 us) 26, where a library product takes 14; 777 x 1000 -> 2047 with
+// everything (2 us) 20.  (A graph replay's time, less the 5 us of an empty one.)
 #pragma once
 #include <type_traits>
 #include "../csrc/pair.cuh"

@@ -615,9 +615,10 @@ flp_status flp_token_logprob_backward(const void* logits, int64_t ld, int dtype,
  * in fp32 up to one rounding (contractions above 131072 as fp32 sums of shorter runs;
  * those of more than 2^22 runs of 256 x 256 outputs are refused).  bias: [N], bf16 or
  * fp32 (bias_dtype), or NULL; residual: [M, N] bf16, or NULL (Y may be the residual
- * itself); pre: v rounded to bf16, for the backward pass, or NULL.  Activations: relu,
- * gelu (v Phi(v)), gelu_tanh (v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))), silu
- * (v sigmoid(v)).  At v = -inf they are 0, 0 (the limit), NaN and NaN (the products).
+ * itself; the outputs overlap nothing else); pre: v rounded to bf16, for the backward
+ * pass, or NULL.  Activations: relu, gelu (v Phi(v)),
+ * gelu_tanh (v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3)))), silu (v sigmoid(v)).
+ * At v = -inf they are 0, 0 (the limit), NaN and NaN (the products).
  * The workspace query takes X and W for their alignment only and may say 0.  A
  * kernel's bounded wait that runs out leaves NaN in every tile of the outputs that
  * was not finished.
@@ -642,7 +643,7 @@ flp_status flp_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, co
  * An infinite d makes its row of dX and of dW infinite as in the formulas; an infinite X
  * or W meets both numbers, and may leave NaN where the formula has an infinity.
  * Each output may be NULL: it is not computed, and X (for dW) or W (for dX) is not
- * read.  The residual's gradient is dY.  M == 0 writes zeros to dW and dbias.  The
+ * read.  No output overlaps an input.  The residual's gradient is dY.  M == 0 writes zeros to dW and dbias.  The
  * workspace's first word is the error word of flp_get_error (FLP_ERR_TIMEOUT);
  * after a timeout what was not finished is NaN.
  */
