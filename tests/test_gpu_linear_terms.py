@@ -18,7 +18,9 @@ def inputs(M, N, K, pads=(0, 0, 0, 0), offsets=(0, 0, 0, 0)):
 
 
 SHAPES = [(1, 72, 64), (64, 264, 136), (65, 264, 136), (130, 1000, 2047), (300, 2048, 520), (700, 19456, 192), (2050, 1000, 4104),
-          (4100, 1000, 4608), (2050, 2048, 4608), (1030, 513, 8199), (2100, 264, 136)]
+          (4100, 1000, 4608), (2050, 2048, 4608), (1030, 513, 8199), (2100, 264, 136),
+          (40, 300000, 64), (40, 600000, 64),   # runs of a long contraction; more of them than a cluster holds
+          (70000, 72, 64)]                      # more than 131072 rows with both numbers
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
